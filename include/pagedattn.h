@@ -325,6 +325,220 @@ PA_API pa_status pa_gather_kv_head(const pa_kv_cache *cache, int32_t kv_head, co
                                    int32_t *compact_tables, int32_t *compact_offsets, pa_stream_t stream);
 
 /*
+ * Metadata of one serving step, built on the device: new pages from a free
+ * list, block tables, slots and positions of the new tokens, lengths and
+ * query starts -- the inputs of pa_reshape_and_cache and pa_paged_attention.
+ * The paper (the source pages) has no counterpart to this entry point.
+ * Request b has c_b = context_lens[b] cached tokens and brings
+ * n_b = query_lens[b] new ones.  With have_b = ceil(c_b/16), need_b =
+ * ceil((c_b+n_b)/16) - have_b, first_b = need_0 + .. + need_{b-1} and
+ * start_b = n_0 + .. + n_{b-1}:
+ *   block_tables[b][have_b + j]  = free_pages[cursor + first_b + j], j < need_b
+ *   seq_lens[b]                  = c_b + n_b
+ *   query_start_loc[b]           = start_b (and [num_seqs] = their sum)
+ *   positions[start_b + i]       = c_b + i,                          i < n_b
+ *   slot_mapping[start_b + i]    = block_tables[b][pos/16]*16 + pos%16
+ *   positions[t] = slot_mapping[t] = -1 for the padding tokens t from the
+ *                                  sum of the n_b up to num_tokens
+ *   *cursor_out                  = *cursor_in + the sum of the need_b
+ *   context_lens, query_lens : [num_seqs] int32.
+ *   block_tables   : [num_seqs, max_blocks_per_seq] int32; columns below
+ *                    have_b are read, the need_b new ones written, the rest
+ *                    left as they are.
+ *   free_pages     : [num_free_pages] int32; pages from index *cursor_in on
+ *                    are free.  cursor_in NULL means 0.  num_blocks: pages of
+ *                    the pool.
+ *   slot_mapping   : [num_tokens] int64.  positions: [num_tokens] int32.
+ *   seq_lens       : [num_seqs] int32.  query_start_loc: [num_seqs+1] int32.
+ *   cursor_out     : [1] int32.
+ *   seq_lens may be context_lens and cursor_out may be cursor_in (all inputs
+ *   are read before anything is written), so a captured graph of a decode
+ *   step advances its own state.  No other output may share bytes with an
+ *   input or another output (PA_ERR_INVALID_ARG).
+ * Errors latched on the device:
+ *   - c_b or n_b negative, or c_b + n_b > max_blocks_per_seq*16: the request
+ *     brings no tokens, its seq_lens entry is c_b (0 if c_b itself is out of
+ *     range); PA_ERR_BAD_METADATA, index = the request;
+ *   - a page id outside [0, num_blocks): the slots in it are -1 (a new one
+ *     still enters the table); PA_ERR_BAD_METADATA, index = the request;
+ *   - more new pages than free ones (PA_ERR_WORKSPACE, index = the pages
+ *     needed), more new tokens than num_tokens, or a cursor outside
+ *     [0, num_free_pages] (PA_ERR_BAD_METADATA, index = num_seqs): the step
+ *     is empty -- every seq_lens entry is c_b as above, every query start 0,
+ *     every token padding, tables and cursor unchanged.
+ * num_seqs in [0, 8192] (PA_ERR_UNSUPPORTED above); num_seqs == 0 launches
+ * nothing.  num_tokens == 0 is allowed (slot_mapping, positions unused).
+ */
+PA_API pa_status pa_build_step_metadata(const int32_t *context_lens, const int32_t *query_lens, int32_t num_seqs,
+                                        int32_t *block_tables, int32_t max_blocks_per_seq,
+                                        const int32_t *free_pages, int32_t num_free_pages,
+                                        const int32_t *cursor_in, int32_t *cursor_out, int64_t num_blocks,
+                                        int64_t *slot_mapping, int32_t *positions, int64_t num_tokens,
+                                        int32_t *seq_lens, int32_t *query_start_loc, pa_stream_t stream);
+
+/*
+ * Norm of every query and key head and the rotation by position, in one pass
+ * over the new tokens (the step between a layer's projections and its cache
+ * write).  The paper (the source pages) has no counterpart to this entry
+ * point.  For every token t with p = positions[t] >= 0 and every head row x
+ * of q and k:
+ *   y = x / sqrt(mean(x_i^2) + eps) * (weight + weight_offset)   (norm), then
+ *   (y_a, y_b) -> (y_a cos - y_b sin, y_b cos + y_a sin)       (rotation)
+ * for the rot_dim/2 pairs (a, b) = (i, i + rot_dim/2), or (2i, 2i+1) with
+ * interleaved != 0; cos = cos_sin[p][i], sin = cos_sin[p][rot_dim/2 + i].
+ * Elements from rot_dim on are not rotated.  Sums and products are fp32; the
+ * result is rounded to BF16 once.  Rows of a token with p < 0 (padding) are
+ * left untouched.  A token with p >= max_positions gets NaN rows and latches
+ * PA_ERR_BAD_METADATA (index = the token).
+ *   q [T, Hq, Dh], k [T, Hkv, Dh] : BF16, token strides in elements (>= the
+ *                   row, multiple of 8), heads contiguous, 16-byte aligned
+ *                   (slices of a fused projection are fine).
+ *   q_out, k_out  : the same shapes, their own token strides.  q_out may be q
+ *                   and k_out may be k (same pointer and stride: in place).
+ *   q_weight, k_weight : [Dh] BF16, or NULL for no norm of q or k.
+ *   weight_offset : added to the weights (1 for weights stored less one).
+ *   positions     : [T] int32.  cos_sin: [max_positions, rot_dim] fp32,
+ *                   contiguous, 16-byte aligned.
+ *   eps           : finite, >= 0.  rot_dim: a multiple of 16 in [16, Dh].
+ *                   head_dim 128, 256 or 512 (PA_ERR_UNSUPPORTED otherwise).
+ * Outputs may not share bytes with anything else (PA_ERR_INVALID_ARG), but
+ * rows of tensors with one token stride may interleave.  T == 0 launches
+ * nothing.
+ */
+PA_API pa_status pa_qk_norm_rope(const void *q, int64_t q_tok_stride, int32_t num_q_heads, const void *k,
+                                 int64_t k_tok_stride, int32_t num_kv_heads, int32_t head_dim, int64_t num_tokens,
+                                 const int32_t *positions, const float *cos_sin, int64_t max_positions,
+                                 int32_t rot_dim, int32_t interleaved, const void *q_weight, const void *k_weight,
+                                 float weight_offset, float eps, void *q_out, int64_t q_out_tok_stride, void *k_out,
+                                 int64_t k_out_tok_stride, pa_stream_t stream);
+
+/*
+ * pa_qk_norm_rope with the cache write of pa_reshape_and_cache in the same
+ * pass: the rotated keys and the values go into the pool at slot_mapping, and
+ * no k_out is written.  A negative slot skips the token's cache write; a slot
+ * past the pool latches PA_ERR_BAD_METADATA (index = the token) and is
+ * skipped, as is the cache write of a token with a bad or negative position.
+ * Results are bitwise those of pa_qk_norm_rope followed by
+ * pa_reshape_and_cache.  The pool may not share bytes with the other
+ * arguments (PA_ERR_INVALID_ARG).
+ */
+PA_API pa_status pa_qk_norm_rope_and_cache(
+    const void *q, int64_t q_tok_stride, int32_t num_q_heads, const void *k, int64_t k_tok_stride, const void *value,
+    int64_t value_tok_stride, int64_t num_tokens, const int32_t *positions, const float *cos_sin,
+    int64_t max_positions, int32_t rot_dim, int32_t interleaved, const void *q_weight, const void *k_weight,
+    float weight_offset, float eps, void *q_out, int64_t q_out_tok_stride, const pa_kv_cache *cache,
+    const int64_t *slot_mapping, pa_stream_t stream);
+
+/*
+ * A paged KV cache held in 4 bits.  The paper (the source pages) has no
+ * counterpart to it.  Sixteen neighbouring head-dim elements of a token share
+ * one scale: an element's value is
+ *   code (e2m1: 0, .5, 1, 1.5, 2, 3, 4, 6, with a sign) * scale (e4m3) *
+ *   k_scale or v_scale.
+ * That value is exact in BF16 (two significant bits times four, times a power
+ * of two).  For one page and KV head, K and V each have a contiguous RECORD of
+ * 9*head_dim bytes:
+ *   K : codes [16 tokens][Dh/2 bytes], then scales [16 tokens][Dh/16];
+ *   V : codes [Dh/2][16 tokens],       then scales [Dh/16][16 tokens].
+ * A code byte holds elements 2i (low half) and 2i+1 of a token.  The record
+ * of (block, head) starts at k + block*block_stride + head*head_stride, in
+ * BYTES (v likewise).  Pools map onto it as two [num_blocks, Hkv, 9*Dh] byte
+ * tensors or one [num_blocks, 2, Hkv, 9*Dh] one.
+ * Requirements: block_size == 16; head_dim in {128, 256, 512}; k and v
+ * 16-byte aligned; strides positive multiples of 16, head_stride >= 9*Dh;
+ * k_scale and v_scale powers of two in [2^-32, 2^32]; reserved == 0.
+ */
+typedef struct {
+    void *k;
+    void *v;
+    int64_t num_blocks;
+    int32_t block_size;
+    int32_t num_kv_heads;
+    int32_t head_dim;
+    int32_t reserved;
+    int64_t block_stride;
+    int64_t head_stride;
+    float k_scale;
+    float v_scale;
+} pa_quant_cache;
+
+/*
+ * pa_reshape_and_cache into a 4-bit pool.  For the 16 elements x of a block,
+ * with x' = x / k_scale (or v_scale):
+ *   scale = e4m3(max|x'| / 6), saturating at 448; code = e2m1(x' / scale),
+ * both to nearest, ties to even, saturating; a zero scale gives zero codes,
+ * and a block that holds a NaN or an infinity reads back as NaN.  Arguments,
+ * padding (negative slots) and errors as for pa_reshape_and_cache; key and
+ * value may not share bytes with the pool (PA_ERR_INVALID_ARG).
+ */
+PA_API pa_status pa_reshape_and_cache_quant(const void *key, int64_t key_tok_stride, const void *value,
+                                            int64_t value_tok_stride, int64_t num_tokens,
+                                            const pa_quant_cache *cache, const int64_t *slot_mapping,
+                                            pa_stream_t stream);
+
+/*
+ * Reads the pages that the block tables select back as a BF16 pool: the
+ * counterpart of pa_gather_kv_head for a 4-bit cache, for every KV head.
+ * Request b selects the n_b = ceil(L_b/16) pages block_tables[b][0..n_b-1];
+ * with off_b = n_0 + .. + n_{b-1},
+ *   k_out[off_b + p][t][h][:] = the values of K[block_tables[b][p]], token t,
+ *                               head h (exact), v_out likewise;
+ *   compact_tables[b][p] = off_b + p for p < n_b, -1 beyond;
+ *   compact_offsets[b] = off_b, compact_offsets[num_seqs] = the total.
+ * k_out and v_out ([capacity_pages, 16, Hkv, Dh] BF16, contiguous) are a pool
+ * that the library's BF16 calls take.  Whole pages are converted.
+ *   compact_tables : [num_seqs, max_blocks_per_seq] int32.
+ * Errors on the device as for pa_gather_kv_head: a bad length selects no
+ * pages, a bad block id gives a NaN page, a total above capacity_pages writes
+ * only compact_offsets (PA_ERR_WORKSPACE, index = total).  Outputs may not
+ * share bytes with the pool, the metadata or each other.  num_seqs <= 8192.
+ */
+PA_API pa_status pa_dequantize_kv(const pa_quant_cache *cache, const int32_t *block_tables,
+                                  int32_t max_blocks_per_seq, const int32_t *seq_lens, int32_t num_seqs, void *k_out,
+                                  void *v_out, int64_t capacity_pages, int32_t *compact_tables,
+                                  int32_t *compact_offsets, pa_stream_t stream);
+
+/*
+ * Bytes of scratch that pa_paged_attention_quant needs for these bounds.
+ * max_pages: an upper bound of the pages of all requests together, or 0 for
+ * num_seqs * ceil(max_seq_len / 16).  Returns 0 for invalid arguments.
+ */
+PA_API size_t pa_paged_attention_quant_workspace_size(int32_t num_seqs, int32_t num_q_heads, int32_t num_kv_heads,
+                                                      int32_t head_dim, int32_t max_query_len, int32_t max_seq_len,
+                                                      int64_t max_pages);
+
+/*
+ * pa_paged_attention over a 4-bit pool: the softmax attention of q over the
+ * values that the pool stands for.  Arguments, ownership and errors as for
+ * pa_paged_attention; max_pages as in the workspace size.
+ *   - Few rows (max_query_len * Hq/Hkv up to 64 at head dim 128, 32 at 256
+ *     and 512: decode steps, drafted tokens): one kernel reads the codes
+ *     directly.  It has a fixed schedule of its own: a row's results are
+ *     bitwise the same whatever the batch, the other requests and the bounds
+ *     (within that limit).
+ *   - More rows: the selected pages are read back into the workspace (as by
+ *     pa_dequantize_kv), and pa_paged_attention's kernel runs over them:
+ *     bitwise its results on the read-back pool.  More than max_pages
+ *     selected pages: PA_ERR_WORKSPACE is latched (index = the pages) and all
+ *     rows are NaN.
+ *   The two round differently.
+ *   - A bad block id makes all rows of its request NaN.  Keys past a
+ *     request's length never matter, whatever their bytes.
+ *   - workspace: as for pa_paged_attention, sized by
+ *     pa_paged_attention_quant_workspace_size for the call's bounds; one
+ *     workspace may serve calls with different bounds (one after the other)
+ *     if it is large enough for each.
+ * num_seqs <= 8192; num_seqs * Hkv <= 65536.
+ */
+PA_API pa_status pa_paged_attention_quant(const void *q, int64_t num_q_tokens, int64_t q_tok_stride,
+                                          int32_t num_q_heads, const pa_quant_cache *cache,
+                                          const int32_t *block_tables, int32_t max_blocks_per_seq,
+                                          const int32_t *seq_lens, const int32_t *query_start_loc, int32_t num_seqs,
+                                          int32_t max_query_len, int32_t max_seq_len, int64_t max_pages, float scale,
+                                          void *out, float *lse, void *workspace, size_t workspace_bytes,
+                                          pa_stream_t stream);
+
+/*
  * Synchronises `stream`, then reads and clears the current device's error
  * flag.  Returns PA_OK, PA_ERR_BAD_METADATA or PA_ERR_TIMEOUT (or
  * PA_ERR_CUDA if the synchronisation failed).  *first_bad_index (may be

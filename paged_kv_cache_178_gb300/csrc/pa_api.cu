@@ -22,13 +22,14 @@ constexpr int kMaxDevices = 64;
 static std::mutex g_mu;
 static ErrState *g_err_ptr[kMaxDevices];
 static bool g_attr_done[kMaxDevices];
+static int g_num_sms[kMaxDevices];
 static thread_local char g_last_info[256] = "none";
 
 static pa_status cuda_status(cudaError_t e) { return e == cudaSuccess ? PA_OK : PA_ERR_CUDA; }
 
 // Per-device one-time set-up: resolve the error latch address and set kernel
 // attributes.  Must run with the device current.
-static pa_status device_setup(ErrState **err_out)
+static pa_status device_setup(ErrState **err_out, int *num_sms = nullptr)
 {
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices)
@@ -38,13 +39,18 @@ static pa_status device_setup(ErrState **err_out)
         void *ptr = nullptr;
         if (cudaGetSymbolAddress(&ptr, g_err_state) != cudaSuccess)
             return PA_ERR_CUDA;
-        if (init_attention_attributes() != cudaSuccess)
+        if (init_attention_attributes() != cudaSuccess || init_step_attributes() != cudaSuccess ||
+            init_quant_attributes() != cudaSuccess || init_quant_attention_attributes() != cudaSuccess)
+            return PA_ERR_CUDA;
+        if (cudaDeviceGetAttribute(&g_num_sms[dev], cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
             return PA_ERR_CUDA;
         g_err_ptr[dev] = static_cast<ErrState *>(ptr);
         g_attr_done[dev] = true;
     }
     if (err_out)
         *err_out = g_err_ptr[dev];
+    if (num_sms)
+        *num_sms = g_num_sms[dev];
     return PA_OK;
 }
 
@@ -687,6 +693,504 @@ pa_status pa_gather_kv_head(const pa_kv_cache *cache, int32_t kv_head, const int
     snprintf(g_last_info, sizeof g_last_info, "gather_kv_head head=%d seqs=%d capacity_pages=%lld", kv_head,
              num_seqs, (long long)capacity_pages);
     return cuda_status(e);
+}
+
+// ------------------------------------------------------ step metadata ----
+static bool aligned4(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+static bool aligned8(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 7u) == 0; }
+
+pa_status pa_build_step_metadata(const int32_t *context_lens, const int32_t *query_lens, int32_t num_seqs,
+                                 int32_t *block_tables, int32_t max_blocks_per_seq, const int32_t *free_pages,
+                                 int32_t num_free_pages, const int32_t *cursor_in, int32_t *cursor_out,
+                                 int64_t num_blocks, int64_t *slot_mapping, int32_t *positions, int64_t num_tokens,
+                                 int32_t *seq_lens, int32_t *query_start_loc, pa_stream_t stream)
+{
+    if (num_seqs < 0 || max_blocks_per_seq <= 0 || num_free_pages < 0 || num_blocks <= 0 ||
+        num_blocks > (int64_t)1 << 31 || num_tokens < 0 || num_tokens > INT32_MAX)
+        return PA_ERR_INVALID_ARG;
+    // positions and lengths are 32-bit
+    if (num_seqs > kScanMaxSeqsHost || max_blocks_per_seq > INT32_MAX / 16)
+        return PA_ERR_UNSUPPORTED;
+    if (num_seqs == 0) {
+        snprintf(g_last_info, sizeof g_last_info, "build_step_metadata: empty batch (nothing launched)");
+        return PA_OK;
+    }
+    if (!context_lens || !query_lens || !block_tables || !cursor_out || !seq_lens || !query_start_loc ||
+        (num_free_pages > 0 && !free_pages) || (num_tokens > 0 && (!slot_mapping || !positions)))
+        return PA_ERR_INVALID_ARG;
+    if (!aligned4(context_lens) || !aligned4(query_lens) || !aligned4(block_tables) || !aligned4(free_pages) ||
+        !aligned4(cursor_in) || !aligned4(cursor_out) || !aligned4(seq_lens) || !aligned4(query_start_loc) ||
+        !aligned4(positions) || !aligned8(slot_mapping))
+        return PA_ERR_INVALID_ARG;
+    {
+        const int64_t n4 = (int64_t)num_seqs * 4;
+        const Span reads[4] = {span(context_lens, n4), span(query_lens, n4),
+                               span(free_pages, (int64_t)num_free_pages * 4), span(cursor_in, cursor_in ? 4 : 0)};
+        const Span writes[6] = {span(block_tables, n4 * max_blocks_per_seq), span(seq_lens, n4),
+                                span(query_start_loc, n4 + 4), span(slot_mapping, num_tokens * 8),
+                                span(positions, num_tokens * 4), span(cursor_out, 4)};
+        for (int i = 0; i < 6; ++i) {
+            for (int j = 0; j < 4; ++j) {
+                // lengths and cursor may advance in place
+                if ((i == 1 && j == 0 && seq_lens == context_lens) || (i == 5 && j == 3 && cursor_out == cursor_in))
+                    continue;
+                if (overlaps(writes[i], reads[j]))
+                    return PA_ERR_INVALID_ARG;
+            }
+            for (int j = i + 1; j < 6; ++j)
+                if (overlaps(writes[i], writes[j]))
+                    return PA_ERR_INVALID_ARG;
+        }
+    }
+    ErrState *err = nullptr;
+    pa_status st = device_setup(&err);
+    if (st != PA_OK)
+        return st;
+    const StepMetaArgs a{context_lens, query_lens, num_seqs,   block_tables, max_blocks_per_seq,
+                         free_pages,   num_free_pages, cursor_in, cursor_out,   num_blocks,
+                         slot_mapping, positions,  num_tokens, seq_lens,     query_start_loc};
+    int grid = 0;
+    const cudaError_t e = launch_step_metadata(a, err, reinterpret_cast<cudaStream_t>(stream), &grid);
+    snprintf(g_last_info, sizeof g_last_info, "build_step_metadata seqs=%d tokens=%lld grid=%d", num_seqs,
+             (long long)num_tokens, grid);
+    return cuda_status(e);
+}
+
+// ---------------------------------------------- norm, rotation (and write) --
+// num_tokens rows of `row` elements, `stride` elements apart.
+struct Rows {
+    const void *p;
+    int64_t stride, row;
+};
+
+static Span rows_span(const Rows &r, int64_t n) { return span(r.p, ((n - 1) * r.stride + r.row) * 2); }
+
+// Whether two row sets share bytes.  Rows of one stride that interleave
+// without touching (slices of a fused projection) do not.
+static bool rows_overlap(const Rows &a, const Rows &b, int64_t n)
+{
+    if (!overlaps(rows_span(a, n), rows_span(b, n)))
+        return false;
+    if (a.stride != b.stride || n <= 1)
+        return true;
+    const int64_t period = a.stride * 2;
+    int64_t d = (int64_t)(reinterpret_cast<uintptr_t>(b.p) - reinterpret_cast<uintptr_t>(a.p)) % period;
+    if (d < 0)
+        d += period;
+    return d < a.row * 2 || d + b.row * 2 > period;
+}
+
+static bool bad_rows(const Rows &r) { return !r.p || !aligned16(r.p) || r.stride < r.row || (r.stride & 7); }
+
+static pa_status rope_call(const Rows &q, int32_t hq, const Rows &k, int32_t hkv, const Rows *value, int32_t head_dim,
+                           int64_t num_tokens, const int32_t *positions, const float *cos_sin, int64_t max_positions,
+                           int32_t rot_dim, int32_t interleaved, const void *q_weight, const void *k_weight,
+                           float weight_offset, float eps, const Rows &q_out, const Rows *k_out,
+                           const pa_kv_cache *cache, const int64_t *slot_mapping, pa_stream_t stream, const char *name)
+{
+    if (num_tokens < 0 || num_tokens > INT32_MAX || max_positions <= 0)
+        return PA_ERR_INVALID_ARG;
+    if (rot_dim < 16 || rot_dim > head_dim || rot_dim % 16)
+        return PA_ERR_UNSUPPORTED;
+    if (!(eps >= 0.f) || eps == INFINITY || !std::isfinite(weight_offset))
+        return PA_ERR_INVALID_ARG;
+    if (num_tokens == 0) {
+        snprintf(g_last_info, sizeof g_last_info, "%s tokens=0 (nothing launched)", name);
+        return PA_OK;
+    }
+    if (bad_rows(q) || bad_rows(k) || bad_rows(q_out) || (value && bad_rows(*value)) || (k_out && bad_rows(*k_out)))
+        return PA_ERR_INVALID_ARG;
+    if (!positions || !aligned4(positions) || !cos_sin || !aligned16(cos_sin) || !aligned16(q_weight) ||
+        !aligned16(k_weight) || (cache && (!slot_mapping || !aligned8(slot_mapping))))
+        return PA_ERR_INVALID_ARG;
+    {
+        const int64_t n = num_tokens;
+        // in place: the very rows that are read
+        const bool q_same = q_out.p == q.p && q_out.stride == q.stride;
+        const bool k_same = k_out && k_out->p == k.p && k_out->stride == k.stride;
+        if ((!q_same && rows_overlap(q_out, q, n)) || rows_overlap(q_out, k, n) ||
+            (value && rows_overlap(q_out, *value, n)))
+            return PA_ERR_INVALID_ARG;
+        if (k_out && ((!k_same && rows_overlap(*k_out, k, n)) || rows_overlap(*k_out, q, n) ||
+                      rows_overlap(*k_out, q_out, n)))
+            return PA_ERR_INVALID_ARG;
+        const Span small[5] = {span(positions, n * 4), span(cos_sin, max_positions * rot_dim * 4),
+                               span(q_weight, q_weight ? head_dim * 2 : 0), span(k_weight, k_weight ? head_dim * 2 : 0),
+                               span(slot_mapping, cache ? n * 8 : 0)};
+        const Span pool[2] = {cache ? span(cache->k, pool_view_bytes(cache)) : Span{0, 0},
+                              cache ? span(cache->v, pool_view_bytes(cache)) : Span{0, 0}};
+        for (const Span &x : small)
+            if (overlaps(x, rows_span(q_out, n)) || (k_out && overlaps(x, rows_span(*k_out, n))) || overlaps(x, pool[0]) ||
+                overlaps(x, pool[1]))
+                return PA_ERR_INVALID_ARG;
+        for (const Span &x : pool)
+            if (overlaps(x, rows_span(q, n)) || overlaps(x, rows_span(k, n)) || overlaps(x, rows_span(q_out, n)) ||
+                (value && overlaps(x, rows_span(*value, n))))
+                return PA_ERR_INVALID_ARG;
+    }
+    ErrState *err = nullptr;
+    int nsm = 0;
+    const pa_status st = device_setup(&err, &nsm);
+    if (st != PA_OK)
+        return st;
+    RopeArgs a{};
+    a.q = static_cast<const uint4 *>(q.p);
+    a.k = static_cast<const uint4 *>(k.p);
+    a.q_stride = q.stride / 8;
+    a.k_stride = k.stride / 8;
+    if (value) {
+        a.v = static_cast<const uint4 *>(value->p);
+        a.v_stride = value->stride / 8;
+    }
+    a.num_q_heads = hq;
+    a.num_kv_heads = hkv;
+    a.head_dim = head_dim;
+    a.num_tokens = num_tokens;
+    a.positions = positions;
+    a.cos_sin = cos_sin;
+    a.max_positions = max_positions;
+    a.rot_dim = rot_dim;
+    a.interleaved = interleaved != 0;
+    a.q_weight = static_cast<const uint4 *>(q_weight);
+    a.k_weight = static_cast<const uint4 *>(k_weight);
+    a.weight_offset = weight_offset;
+    a.eps = eps;
+    a.q_out = static_cast<uint4 *>(const_cast<void *>(q_out.p));
+    a.q_out_stride = q_out.stride / 8;
+    if (k_out) {
+        a.k_out = static_cast<uint4 *>(const_cast<void *>(k_out->p));
+        a.k_out_stride = k_out->stride / 8;
+    }
+    if (cache) {
+        a.k_cache = static_cast<uint4 *>(cache->k);
+        a.v_cache = static_cast<uint4 *>(cache->v);
+        a.num_slots = cache->num_blocks * 16;
+        a.block_stride = cache->block_stride / 8;
+        a.token_stride = cache->token_stride / 8;
+        a.head_stride = cache->head_stride / 8;
+        a.slot_mapping = slot_mapping;
+    }
+    int64_t grid = 0;
+    const cudaError_t e = launch_qk_norm_rope(a, err, reinterpret_cast<cudaStream_t>(stream), nsm, &grid);
+    snprintf(g_last_info, sizeof g_last_info, "%s tokens=%lld grid=%lld", name, (long long)num_tokens, (long long)grid);
+    return cuda_status(e);
+}
+
+pa_status pa_qk_norm_rope(const void *q, int64_t q_tok_stride, int32_t num_q_heads, const void *k,
+                          int64_t k_tok_stride, int32_t num_kv_heads, int32_t head_dim, int64_t num_tokens,
+                          const int32_t *positions, const float *cos_sin, int64_t max_positions, int32_t rot_dim,
+                          int32_t interleaved, const void *q_weight, const void *k_weight, float weight_offset,
+                          float eps, void *q_out, int64_t q_out_tok_stride, void *k_out, int64_t k_out_tok_stride,
+                          pa_stream_t stream)
+{
+    if (num_q_heads <= 0 || num_kv_heads <= 0)
+        return PA_ERR_INVALID_ARG;
+    if (head_dim != 128 && head_dim != 256 && head_dim != 512)
+        return PA_ERR_UNSUPPORTED;
+    const int64_t qr = (int64_t)num_q_heads * head_dim, kr = (int64_t)num_kv_heads * head_dim;
+    const Rows ko{k_out, k_out_tok_stride, kr};
+    return rope_call(Rows{q, q_tok_stride, qr}, num_q_heads, Rows{k, k_tok_stride, kr}, num_kv_heads, nullptr, head_dim,
+                     num_tokens, positions, cos_sin, max_positions, rot_dim, interleaved, q_weight, k_weight,
+                     weight_offset, eps, Rows{q_out, q_out_tok_stride, qr}, &ko, nullptr, nullptr, stream,
+                     "qk_norm_rope");
+}
+
+pa_status pa_qk_norm_rope_and_cache(const void *q, int64_t q_tok_stride, int32_t num_q_heads, const void *k,
+                                    int64_t k_tok_stride, const void *value, int64_t value_tok_stride,
+                                    int64_t num_tokens, const int32_t *positions, const float *cos_sin,
+                                    int64_t max_positions, int32_t rot_dim, int32_t interleaved, const void *q_weight,
+                                    const void *k_weight, float weight_offset, float eps, void *q_out,
+                                    int64_t q_out_tok_stride, const pa_kv_cache *cache, const int64_t *slot_mapping,
+                                    pa_stream_t stream)
+{
+    const pa_status st = check_cache(cache);
+    if (st != PA_OK)
+        return st;
+    if (num_q_heads <= 0)
+        return PA_ERR_INVALID_ARG;
+    const int32_t hkv = cache->num_kv_heads, dh = cache->head_dim;
+    const int64_t qr = (int64_t)num_q_heads * dh, kr = (int64_t)hkv * dh;
+    const Rows v{value, value_tok_stride, kr};
+    return rope_call(Rows{q, q_tok_stride, qr}, num_q_heads, Rows{k, k_tok_stride, kr}, hkv, &v, dh, num_tokens,
+                     positions, cos_sin, max_positions, rot_dim, interleaved, q_weight, k_weight, weight_offset, eps,
+                     Rows{q_out, q_out_tok_stride, qr}, nullptr, cache, slot_mapping, stream,
+                     "qk_norm_rope_and_cache");
+}
+
+// --------------------------------------------------------- 4-bit cache ----
+// A power of two in [2^-32, 2^32].
+static bool tensor_scale_ok(float s)
+{
+    int e = 0;
+    return s > 0.f && std::isfinite(s) && std::frexp(s, &e) == 0.5f && e - 1 >= -32 && e - 1 <= 32;
+}
+
+static pa_status check_quant_cache(const pa_quant_cache *c)
+{
+    if (!c || !c->k || !c->v || !aligned16(c->k) || !aligned16(c->v))
+        return PA_ERR_INVALID_ARG;
+    if (c->num_blocks <= 0 || c->num_blocks > (int64_t)1 << 31 || c->num_kv_heads <= 0 || c->head_dim <= 0 ||
+        c->reserved != 0)
+        return PA_ERR_INVALID_ARG;
+    if (c->block_size != 16 || (c->head_dim != 128 && c->head_dim != 256 && c->head_dim != 512))
+        return PA_ERR_UNSUPPORTED;
+    if (c->block_stride <= 0 || c->head_stride < (int64_t)9 * c->head_dim || ((c->block_stride | c->head_stride) & 15))
+        return PA_ERR_INVALID_ARG;
+    return tensor_scale_ok(c->k_scale) && tensor_scale_ok(c->v_scale) ? PA_OK : PA_ERR_INVALID_ARG;
+}
+
+static QuantPool quant_pool(const pa_quant_cache *c)
+{
+    return QuantPool{static_cast<uint8_t *>(c->k), static_cast<uint8_t *>(c->v), c->num_blocks, c->block_stride,
+                     c->head_stride,               c->num_kv_heads,              c->head_dim,   c->k_scale,
+                     c->v_scale};
+}
+
+static int64_t quant_view_bytes(const pa_quant_cache *c)
+{
+    return (c->num_blocks - 1) * c->block_stride + (int64_t)(c->num_kv_heads - 1) * c->head_stride + 9 * c->head_dim;
+}
+
+pa_status pa_reshape_and_cache_quant(const void *key, int64_t key_tok_stride, const void *value,
+                                     int64_t value_tok_stride, int64_t num_tokens, const pa_quant_cache *cache,
+                                     const int64_t *slot_mapping, pa_stream_t stream)
+{
+    pa_status st = check_quant_cache(cache);
+    if (st != PA_OK)
+        return st;
+    if (num_tokens < 0)
+        return PA_ERR_INVALID_ARG;
+    if (num_tokens == 0) {
+        snprintf(g_last_info, sizeof g_last_info, "reshape_and_cache_quant tokens=0 (nothing launched)");
+        return PA_OK;
+    }
+    const int64_t row = (int64_t)cache->num_kv_heads * cache->head_dim;
+    const Rows k{key, key_tok_stride, row}, v{value, value_tok_stride, row};
+    if (bad_rows(k) || bad_rows(v) || !slot_mapping || !aligned8(slot_mapping))
+        return PA_ERR_INVALID_ARG;
+    const Span pool[2] = {span(cache->k, quant_view_bytes(cache)), span(cache->v, quant_view_bytes(cache))};
+    for (const Span &x : pool)
+        if (overlaps(x, rows_span(k, num_tokens)) || overlaps(x, rows_span(v, num_tokens)) ||
+            overlaps(x, span(slot_mapping, num_tokens * 8)))
+            return PA_ERR_INVALID_ARG;
+    ErrState *err = nullptr;
+    int nsm = 0;
+    if ((st = device_setup(&err, &nsm)) != PA_OK)
+        return st;
+    int64_t grid = 0;
+    const cudaError_t e = launch_quant_write(key, key_tok_stride, value, value_tok_stride, num_tokens,
+                                             quant_pool(cache), slot_mapping, err,
+                                             reinterpret_cast<cudaStream_t>(stream), nsm, &grid);
+    snprintf(g_last_info, sizeof g_last_info, "reshape_and_cache_quant tokens=%lld grid=%lld", (long long)num_tokens,
+             (long long)grid);
+    return cuda_status(e);
+}
+
+pa_status pa_dequantize_kv(const pa_quant_cache *cache, const int32_t *block_tables, int32_t max_blocks_per_seq,
+                           const int32_t *seq_lens, int32_t num_seqs, void *k_out, void *v_out,
+                           int64_t capacity_pages, int32_t *compact_tables, int32_t *compact_offsets,
+                           pa_stream_t stream)
+{
+    pa_status st = check_quant_cache(cache);
+    if (st != PA_OK)
+        return st;
+    if (num_seqs < 0 || max_blocks_per_seq <= 0 || capacity_pages < 0)
+        return PA_ERR_INVALID_ARG;
+    if (num_seqs > kScanMaxSeqsHost || (int64_t)num_seqs * max_blocks_per_seq > INT32_MAX)
+        return PA_ERR_UNSUPPORTED;
+    if (num_seqs == 0) {
+        snprintf(g_last_info, sizeof g_last_info, "dequantize_kv: empty batch (nothing launched)");
+        return PA_OK;
+    }
+    if (!block_tables || !seq_lens || !compact_tables || !compact_offsets || !aligned4(block_tables) ||
+        !aligned4(seq_lens) || !aligned4(compact_tables) || !aligned4(compact_offsets))
+        return PA_ERR_INVALID_ARG;
+    if (capacity_pages > 0 && (!k_out || !v_out || !aligned16(k_out) || !aligned16(v_out)))
+        return PA_ERR_INVALID_ARG;
+    {
+        const int64_t out_bytes = capacity_pages * 16 * cache->num_kv_heads * cache->head_dim * 2;
+        const int64_t table_bytes = (int64_t)num_seqs * max_blocks_per_seq * 4;
+        const Span reads[4] = {span(cache->k, quant_view_bytes(cache)), span(cache->v, quant_view_bytes(cache)),
+                               span(block_tables, table_bytes), span(seq_lens, (int64_t)num_seqs * 4)};
+        const Span writes[4] = {span(k_out, out_bytes), span(v_out, out_bytes), span(compact_tables, table_bytes),
+                                span(compact_offsets, ((int64_t)num_seqs + 1) * 4)};
+        for (int i = 0; i < 4; ++i) {
+            for (const Span &r : reads)
+                if (overlaps(writes[i], r))
+                    return PA_ERR_INVALID_ARG;
+            for (int j = i + 1; j < 4; ++j)
+                if (overlaps(writes[i], writes[j]))
+                    return PA_ERR_INVALID_ARG;
+        }
+    }
+    ErrState *err = nullptr;
+    int nsm = 0;
+    if ((st = device_setup(&err, &nsm)) != PA_OK)
+        return st;
+    int64_t grid = 0;
+    const cudaError_t e = launch_dequantize_kv(quant_pool(cache), block_tables, max_blocks_per_seq, seq_lens, num_seqs,
+                                               k_out, v_out, capacity_pages, compact_tables, max_blocks_per_seq,
+                                               compact_offsets, false, nullptr, 0, err,
+                                               reinterpret_cast<cudaStream_t>(stream), nsm, &grid);
+    snprintf(g_last_info, sizeof g_last_info, "dequantize_kv seqs=%d capacity_pages=%lld grid=%lld", num_seqs,
+             (long long)capacity_pages, (long long)grid);
+    return cuda_status(e);
+}
+
+// The workspace of an attention call over a 4-bit cache.  The arrival
+// counters of the direct kernel have a region of their own at its head, the
+// same for all bounds, so whatever another call leaves behind it they stay
+// zero between calls; the counters of the BF16 attention over read-back pages
+// are cleared by the read-back itself.
+constexpr int64_t kQuantMaxGroups = 65536;
+struct QuantPlan {
+    bool direct;
+    size_t records;                     // direct: chunk records
+    int64_t pages;                      // otherwise: read-back pages,
+    int32_t cols;                       // compact table columns,
+    size_t k, v, tables, inner, bytes;  // and offsets
+    AttnPlan attn;
+};
+
+static size_t round256(size_t n) { return (n + 255) / 256 * 256; }
+
+static pa_status plan_quant(int32_t num_seqs, int32_t hq, int32_t hkv, int32_t dh, int32_t max_query_len,
+                            int32_t max_seq_len, int64_t max_pages, QuantPlan *pl)
+{
+    *pl = QuantPlan{};
+    if (max_pages < 0)
+        return PA_ERR_INVALID_ARG;
+    if (!plan_attention(num_seqs, hq, hkv, dh, max_query_len, max_seq_len, &pl->attn))
+        return PA_ERR_UNSUPPORTED;
+    if (num_seqs > kScanMaxSeqsHost || (int64_t)num_seqs * hkv > kQuantMaxGroups ||
+        (int64_t)num_seqs * (((int64_t)max_seq_len + 15) / 16) > INT32_MAX)
+        return PA_ERR_UNSUPPORTED;
+    const int64_t rows = (int64_t)max_query_len * (hq / hkv);
+    pl->direct = rows <= quant_attn_max_rows(dh);
+    const size_t counters = (size_t)kQuantMaxGroups * 4;
+    if (pl->direct) {
+        pl->records = counters;
+        pl->bytes = counters + quant_attn_record_bytes(num_seqs, hkv, dh, (int)rows, max_seq_len);
+        return PA_OK;
+    }
+    pl->cols = (int32_t)(((int64_t)max_seq_len + 15) / 16);
+    if (pl->cols < 1)
+        pl->cols = 1;
+    pl->pages = (int64_t)num_seqs * pl->cols;
+    if (max_pages > 0 && max_pages < pl->pages)
+        pl->pages = max_pages;
+    const size_t view = (size_t)pl->pages * 16 * hkv * dh * 2;
+    pl->k = counters;
+    pl->v = pl->k + round256(view);
+    pl->tables = pl->v + round256(view);
+    pl->inner = pl->tables + round256((size_t)num_seqs * pl->cols * 4);
+    pl->bytes = pl->inner + pl->attn.ws_bytes;
+    return PA_OK;
+}
+
+size_t pa_paged_attention_quant_workspace_size(int32_t num_seqs, int32_t num_q_heads, int32_t num_kv_heads,
+                                               int32_t head_dim, int32_t max_query_len, int32_t max_seq_len,
+                                               int64_t max_pages)
+{
+    QuantPlan pl;
+    return plan_quant(num_seqs, num_q_heads, num_kv_heads, head_dim, max_query_len, max_seq_len, max_pages, &pl) == PA_OK
+               ? pl.bytes
+               : 0;
+}
+
+pa_status pa_paged_attention_quant(const void *q, int64_t num_q_tokens, int64_t q_tok_stride, int32_t num_q_heads,
+                                   const pa_quant_cache *cache, const int32_t *block_tables,
+                                   int32_t max_blocks_per_seq, const int32_t *seq_lens, const int32_t *query_start_loc,
+                                   int32_t num_seqs, int32_t max_query_len, int32_t max_seq_len, int64_t max_pages,
+                                   float scale, void *out, float *lse, void *workspace, size_t workspace_bytes,
+                                   pa_stream_t stream)
+{
+    pa_status st = check_quant_cache(cache);
+    if (st != PA_OK)
+        return st;
+    if (num_q_heads <= 0 || num_seqs < 0 || max_query_len < 0 || max_seq_len < 0 || num_q_tokens < 0 ||
+        max_blocks_per_seq < 0 || max_pages < 0 || num_q_tokens > INT32_MAX)
+        return PA_ERR_INVALID_ARG;
+    const int32_t hkv = cache->num_kv_heads, dh = cache->head_dim;
+    if (num_q_heads % hkv != 0 || num_q_heads / hkv > 128)
+        return PA_ERR_UNSUPPORTED;
+    if (!(scale > 0.f) || scale == INFINITY)
+        return PA_ERR_INVALID_ARG;
+    if (num_seqs == 0 || num_q_tokens == 0 || max_query_len == 0) {
+        snprintf(g_last_info, sizeof g_last_info, "quant attention: empty batch (nothing launched)");
+        return PA_OK;
+    }
+    const int64_t row = (int64_t)num_q_heads * dh;
+    if (!q || !out || !block_tables || !seq_lens || !query_start_loc || !aligned16(q) || !aligned16(out) ||
+        !aligned4(lse) || !aligned4(block_tables) || !aligned4(seq_lens) || !aligned4(query_start_loc))
+        return PA_ERR_INVALID_ARG;
+    if (q_tok_stride < row || (q_tok_stride & 7) || max_blocks_per_seq == 0)
+        return PA_ERR_INVALID_ARG;
+    QuantPlan pl;
+    if ((st = plan_quant(num_seqs, num_q_heads, hkv, dh, max_query_len, max_seq_len, max_pages, &pl)) != PA_OK)
+        return st;
+    if (!workspace || workspace_bytes < pl.bytes)
+        return PA_ERR_WORKSPACE;
+    if (reinterpret_cast<uintptr_t>(workspace) & 255u)
+        return PA_ERR_INVALID_ARG;
+    ErrState *err = nullptr;
+    int nsm = 0;
+    if ((st = device_setup(&err, &nsm)) != PA_OK)
+        return st;
+    uint8_t *ws = static_cast<uint8_t *>(workspace);
+    const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    if (pl.direct) {
+        QuantAttnArgs a{};
+        a.q = q;
+        a.num_q_tokens = num_q_tokens;
+        a.q_tok_stride = q_tok_stride;
+        a.num_q_heads = num_q_heads;
+        a.pool = quant_pool(cache);
+        a.block_tables = block_tables;
+        a.max_blocks = max_blocks_per_seq;
+        a.seq_lens = seq_lens;
+        a.query_start_loc = query_start_loc;
+        a.num_seqs = num_seqs;
+        a.max_query_len = max_query_len;
+        a.max_seq_len = max_seq_len;
+        a.scale = scale;
+        a.out = out;
+        a.lse = lse;
+        a.counters = reinterpret_cast<uint32_t *>(ws);
+        a.records = reinterpret_cast<float *>(ws + pl.records);
+        return cuda_status(launch_quant_attention(a, err, s, nsm, g_last_info, sizeof g_last_info));
+    }
+    // read the selected pages back, then the BF16 attention over them
+    const int32_t cols = pl.cols < max_blocks_per_seq ? pl.cols : max_blocks_per_seq;
+    int32_t *tables = reinterpret_cast<int32_t *>(ws + pl.tables);
+    int64_t grid = 0;
+    cudaError_t e = launch_dequantize_kv(quant_pool(cache), block_tables, max_blocks_per_seq, seq_lens, num_seqs,
+                                         ws + pl.k, ws + pl.v, pl.pages, tables, cols, nullptr, true, ws + pl.inner,
+                                         pl.attn.ws_counter_bytes, err, s, nsm, &grid);
+    if (e != cudaSuccess)
+        return cuda_status(e);
+    pa_kv_cache pool{};
+    pool.k = ws + pl.k;
+    pool.v = ws + pl.v;
+    pool.num_blocks = pl.pages;
+    pool.block_size = 16;
+    pool.num_kv_heads = hkv;
+    pool.head_dim = dh;
+    pool.block_stride = (int64_t)16 * hkv * dh;
+    pool.token_stride = (int64_t)hkv * dh;
+    pool.head_stride = dh;
+    AttnArgs a;
+    AttnPlan ap{};
+    bool empty = false;
+    st = attention_check(q, num_q_tokens, q_tok_stride, num_q_heads, &pool, tables, cols, seq_lens, query_start_loc,
+                         num_seqs, max_query_len, max_seq_len, scale, out, lse, ws + pl.inner,
+                         workspace_bytes - pl.inner, &a, &ap, &empty);
+    if (st != PA_OK)
+        return st;
+    char info[192];
+    st = attention_launch(a, ap, err, s, info, sizeof info);
+    snprintf(g_last_info, sizeof g_last_info, "quant attention read-back grid=%lld; %.180s", (long long)grid, info);
+    return st;
 }
 
 }  // extern "C"

@@ -98,6 +98,92 @@ cudaError_t launch_gather_kv_head(const void *k, const void *v, int64_t num_bloc
                                   cudaStream_t stream, int num_sms);
 constexpr int kGatherMaxSeqsHost = 512;
 
+// Step metadata (pa_step.cu); the fields are pa_build_step_metadata's arguments.
+struct StepMetaArgs {
+    const int32_t *context_lens, *query_lens;
+    int32_t num_seqs;
+    int32_t *block_tables;
+    int32_t max_blocks;
+    const int32_t *free_pages;
+    int32_t num_free;
+    const int32_t *cursor_in;
+    int32_t *cursor_out;
+    int64_t num_blocks;
+    int64_t *slot_mapping;
+    int32_t *positions;
+    int64_t num_tokens;
+    int32_t *seq_lens, *query_start_loc;
+};
+cudaError_t launch_step_metadata(const StepMetaArgs &a, ErrState *err, cudaStream_t stream, int *grid);
+constexpr int kScanMaxSeqsHost = 8192;  // kScanMaxSeqs of pa_scan.cuh
+
+// Norm and rotation of q and k (pa_step.cu).  Tensor strides in 16-byte units.
+struct RopeArgs {
+    const uint4 *q, *k, *v;
+    int64_t q_stride, k_stride, v_stride;
+    int32_t num_q_heads, num_kv_heads, head_dim;
+    int64_t num_tokens;
+    const int32_t *positions;
+    const float *cos_sin;
+    int64_t max_positions;
+    int32_t rot_dim, interleaved;
+    const uint4 *q_weight, *k_weight;
+    float weight_offset, eps;
+    uint4 *q_out, *k_out;
+    int64_t q_out_stride, k_out_stride;
+    // with the cache write: the pool (k_cache not null), no k_out
+    uint4 *k_cache, *v_cache;
+    int64_t num_slots, block_stride, token_stride, head_stride;
+    const int64_t *slot_mapping;
+};
+cudaError_t launch_qk_norm_rope(const RopeArgs &a, ErrState *err, cudaStream_t stream, int num_sms, int64_t *grid);
+cudaError_t init_step_attributes();
+
+// 4-bit cache: write and read-back (pa_quant.cu).  Pool strides in bytes.
+struct QuantPool {
+    uint8_t *k, *v;
+    int64_t num_blocks, block_stride, head_stride;
+    int32_t num_kv_heads, head_dim;
+    float k_scale, v_scale;
+};
+cudaError_t launch_quant_write(const void *key, int64_t key_stride, const void *value, int64_t value_stride,
+                               int64_t num_tokens, const QuantPool &pool, const int64_t *slot_mapping, ErrState *err,
+                               cudaStream_t stream, int num_sms, int64_t *grid);
+// compact_tables has out_cols columns (columns past them are not written).
+// With poison_tables a total above the capacity fills compact_tables with -1.
+// zero_bytes bytes at `zero` (16-byte aligned, may be 0) are cleared.
+cudaError_t launch_dequantize_kv(const QuantPool &pool, const int32_t *block_tables, int32_t max_blocks,
+                                 const int32_t *seq_lens, int32_t num_seqs, void *k_out, void *v_out,
+                                 int64_t capacity_pages, int32_t *compact_tables, int32_t out_cols,
+                                 int32_t *compact_offsets, bool poison_tables, void *zero, size_t zero_bytes,
+                                 ErrState *err, cudaStream_t stream, int num_sms, int64_t *grid);
+cudaError_t init_quant_attributes();
+
+// Attention of few rows over a 4-bit pool (pa_attn_quant.cu).
+struct QuantAttnArgs {
+    const void *q;
+    int64_t num_q_tokens, q_tok_stride;
+    int32_t num_q_heads;
+    QuantPool pool;
+    const int32_t *block_tables;
+    int32_t max_blocks;
+    const int32_t *seq_lens, *query_start_loc;
+    int32_t num_seqs, max_query_len, max_seq_len;
+    float scale;
+    void *out;
+    float *lse;
+    uint32_t *counters;  // one per (request, KV head) group, zero between calls
+    float *records;
+};
+// Rows (query tokens x group) the kernel takes at a head dim.
+constexpr int quant_attn_max_rows(int head_dim) { return head_dim == 128 ? 64 : 32; }
+// Bytes of chunk records for these bounds.
+size_t quant_attn_record_bytes(int32_t num_seqs, int32_t num_kv_heads, int32_t head_dim, int rows,
+                               int32_t max_seq_len);
+cudaError_t launch_quant_attention(const QuantAttnArgs &a, ErrState *err, cudaStream_t stream, int num_sms,
+                                   char *info, size_t info_len);
+cudaError_t init_quant_attention_attributes();
+
 // Encodes a tiled tensor map (driver entry point fetched at run time).
 CUresult encode_tiled(CUtensorMap *map, CUtensorMapDataType dtype, cuuint32_t rank, void *base,
                       const cuuint64_t *dims, const cuuint64_t *strides_bytes,

@@ -1,0 +1,355 @@
+// 4-bit cache: the slot-mapped write and the read-back of the pages that the
+// block tables select.  Layout and conversions: pa_quant_common.cuh.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include "pa_internal.h"
+#include "pa_ptx.cuh"
+#include "pa_quant_common.cuh"
+#include "pa_scan.cuh"
+
+namespace pa {
+
+constexpr int kQuantThreads = 256;
+
+// ---------------------------------------------------------------- write ----
+// One thread per block of 16 elements: scale = e4m3(max / 6), codes =
+// e2m1(x / scale).  The quotient is computed as x times the rounded
+// reciprocal r of the scale plus one correction by its exact residual,
+//   q0 = x*r,  q = q0 + (x - q0*scale)*r,
+// which gives the exact value whenever x/scale is a tie of the code (x has
+// 8 significant bits and the scale 4, so quotients that are not ties stay
+// 2^-12 away from one, and a tie is representable).
+struct Quantised {
+    uint32_t scale;    // e4m3 byte
+    uint32_t code[2];  // 16 codes, element i in bits 4i
+};
+
+__device__ __forceinline__ Quantised quantise16(const uint4 &lo, const uint4 &hi, float inv_tensor_scale)
+{
+    const uint32_t w[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+    // largest magnitude as BF16 bits (an infinity or NaN is at least 0x7F80)
+    uint32_t top = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        top = max(top, max(w[i] & 0x7fffu, (w[i] >> 16) & 0x7fffu));
+    Quantised o;
+    if (top >= 0x7F80u) {
+        o.scale = 0x7F;  // NaN: the whole block reads back as NaN
+        o.code[0] = o.code[1] = 0u;
+        return o;
+    }
+    const float amax = __uint_as_float(top << 16) * inv_tensor_scale;
+    uint16_t sc;
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(sc) : "f"(0.f), "f"(amax * (1.f / 6.f)));
+    o.scale = sc & 0xffu;
+    if (o.scale == 0) {
+        // codes of zero, the signs kept
+        o.code[0] = o.code[1] = 0u;
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            o.code[i / 4] |= (((w[i] >> 15) & 1u) << 3 | ((w[i] >> 31) & 1u) << 7) << (8 * (i % 4));
+        return o;
+    }
+    const uint32_t sp = e4m3x2_to_f16x2(o.scale);
+    const float s = __half2float(__ushort_as_half((unsigned short)(sp & 0xffffu)));
+    const float r = __frcp_rn(s);
+    const float cap = 65536.f * s;  // far above the largest code: saturates, and keeps q0 finite
+    float q[16];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+        float x = __uint_as_float(i % 2 ? (w[i / 2] & 0xffff0000u) : (w[i / 2] << 16)) * inv_tensor_scale;
+        x = fminf(fmaxf(x, -cap), cap);
+        const float q0 = x * r;
+        q[i] = __fmaf_rn(__fmaf_rn(-q0, s, x), r, q0);
+    }
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+        asm("{\n\t.reg .b8 a, b, c, d;\n\t"
+            "cvt.rn.satfinite.e2m1x2.f32 a, %2, %1;\n\t"
+            "cvt.rn.satfinite.e2m1x2.f32 b, %4, %3;\n\t"
+            "cvt.rn.satfinite.e2m1x2.f32 c, %6, %5;\n\t"
+            "cvt.rn.satfinite.e2m1x2.f32 d, %8, %7;\n\t"
+            "mov.b32 %0, {a, b, c, d};\n\t}"
+            : "=r"(o.code[k])
+            : "f"(q[8 * k]), "f"(q[8 * k + 1]), "f"(q[8 * k + 2]), "f"(q[8 * k + 3]), "f"(q[8 * k + 4]),
+              "f"(q[8 * k + 5]), "f"(q[8 * k + 6]), "f"(q[8 * k + 7]));
+    }
+    return o;
+}
+
+// K items run with the 16-element block fastest (a token's codes are
+// contiguous), V items with the token fastest in groups of 16 (the codes of
+// neighbouring tokens are): neighbouring lanes then store neighbouring bytes
+// when the slots are consecutive, as in a prompt.
+template <int DH>
+__global__ void __launch_bounds__(kQuantThreads) quant_write_kernel(
+    const uint4 *__restrict__ key, int64_t key_stride, const uint4 *__restrict__ value, int64_t value_stride,
+    int64_t num_tokens, QuantPool pool, const int64_t *__restrict__ slot_mapping, ErrState *err)
+{
+    griddep_wait();
+    griddep_launch_dependents();
+    constexpr int NB = DH / 16;  // blocks of a row
+    const int hk = pool.num_kv_heads;
+    const int64_t num_slots = pool.num_blocks * 16;
+    const int64_t groups = (num_tokens + 15) / 16;
+    const int64_t per_kind = groups * 16 * hk * NB;  // V counts whole groups of 16 tokens, K the same for symmetry
+    for (int64_t i = (int64_t)blockIdx.x * kQuantThreads + threadIdx.x; i < 2 * per_kind;
+         i += (int64_t)gridDim.x * kQuantThreads) {
+        const bool is_v = i >= per_kind;
+        int64_t x = is_v ? i - per_kind : i;
+        int64_t t;
+        int blk, h;
+        if (is_v) {
+            const int lo = (int)(x % 16);
+            x /= 16;
+            blk = (int)(x % NB);
+            x /= NB;
+            h = (int)(x % hk);
+            t = x / hk * 16 + lo;
+        } else {
+            blk = (int)(x % NB);
+            x /= NB;
+            h = (int)(x % hk);
+            t = x / hk;
+        }
+        if (t >= num_tokens)
+            continue;
+        const uint4 *src = (is_v ? value + t * value_stride : key + t * key_stride) + (int64_t)h * (DH / 8) + 2 * blk;
+        const uint4 a = __ldg(src), b = __ldg(src + 1);
+        const int64_t slot = __ldg(slot_mapping + t);
+        if (slot < 0)
+            continue;
+        if (slot >= num_slots) {
+            if (!is_v && blk == 0 && h == 0)
+                record_error(err, kErrBadMetadata, t);
+            continue;
+        }
+        const Quantised q = quantise16(a, b, 1.f / (is_v ? pool.v_scale : pool.k_scale));
+        const int tok = (int)(slot & 15);
+        uint8_t *rec = (is_v ? pool.v : pool.k) + (slot >> 4) * pool.block_stride + h * pool.head_stride;
+        if (is_v) {
+            uint8_t *p = rec + blk * 128 + tok;
+#pragma unroll
+            for (int c = 0; c < 8; ++c)
+                p[c * 16] = (uint8_t)(q.code[c / 4] >> (8 * (c % 4)));
+            rec[quant_code_bytes(DH) + blk * 16 + tok] = (uint8_t)q.scale;
+        } else {
+            *reinterpret_cast<uint2 *>(rec + tok * (DH / 2) + blk * 8) = make_uint2(q.code[0], q.code[1]);
+            rec[quant_code_bytes(DH) + tok * NB + blk] = (uint8_t)q.scale;
+        }
+    }
+}
+
+cudaError_t launch_quant_write(const void *key, int64_t key_stride, const void *value, int64_t value_stride,
+                               int64_t num_tokens, const QuantPool &pool, const int64_t *slot_mapping, ErrState *err,
+                               cudaStream_t stream, int num_sms, int64_t *grid)
+{
+    const int64_t items = (num_tokens + 15) / 16 * 16 * pool.num_kv_heads * (pool.head_dim / 16) * 2;
+    int64_t blocks = (items + kQuantThreads - 1) / kQuantThreads;
+    if (blocks > (int64_t)num_sms * 32)
+        blocks = (int64_t)num_sms * 32;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)blocks);
+    cfg.blockDim = dim3(kQuantThreads);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    *grid = blocks;
+    void (*kern)(const uint4 *, int64_t, const uint4 *, int64_t, int64_t, QuantPool, const int64_t *, ErrState *) =
+        pool.head_dim == 128 ? quant_write_kernel<128>
+                             : (pool.head_dim == 256 ? quant_write_kernel<256> : quant_write_kernel<512>);
+    return cudaLaunchKernelEx(&cfg, kern, static_cast<const uint4 *>(key), key_stride / 8,
+                              static_cast<const uint4 *>(value), value_stride / 8, num_tokens, pool, slot_mapping,
+                              err);
+}
+
+// ------------------------------------------------------------- read-back ----
+// Bound by the BF16 bytes it writes (16 of every 20.5 bytes moved).  Eight
+// codes (one 32-bit word) become one 16-byte store.  K: neighbouring lanes
+// take neighbouring words of a token.  V: a lane takes eight head-dim elements
+// of all 16 tokens (four 16-byte loads, the bytes regrouped by token with
+// permutes), neighbouring lanes neighbouring elements; every store
+// instruction then covers whole rows.
+__device__ __forceinline__ uint4 values8(uint32_t codes, uint32_t scale_pair, float tensor_scale)
+{
+    uint32_t p[4];
+    e2m1x8_to_f16x2(codes, p);
+    uint32_t o[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const uint32_t v = mul_f16x2(p[i], scale_pair);  // exact
+        const __half2 hv = *reinterpret_cast<const __half2 *>(&v);
+        const float2 f = __half22float2(hv);
+        const __nv_bfloat162 b = __floats2bfloat162_rn(f.x * tensor_scale, f.y * tensor_scale);  // exact
+        o[i] = *reinterpret_cast<const uint32_t *>(&b);
+    }
+    return make_uint4(o[0], o[1], o[2], o[3]);
+}
+
+template <int DH>
+__global__ void __launch_bounds__(kQuantThreads) dequantize_kv_kernel(
+    QuantPool pool, const int32_t *__restrict__ block_tables, int32_t max_blocks,
+    const int32_t *__restrict__ seq_lens, int32_t num_seqs, uint4 *__restrict__ k_out, uint4 *__restrict__ v_out,
+    int64_t capacity_pages, int32_t *__restrict__ compact_tables, int32_t out_cols,
+    int32_t *__restrict__ compact_offsets, bool poison_tables, uint4 *__restrict__ zero, int64_t zero16, ErrState *err)
+{
+    griddep_wait();
+    griddep_launch_dependents();
+    extern __shared__ int32_t s_off[];  // [num_seqs + 1]
+    __shared__ long long s_sums[kQuantThreads / 32];
+    const int tid = threadIdx.x;
+    const int64_t gtid = (int64_t)blockIdx.x * kQuantThreads + tid, gsize = (int64_t)gridDim.x * kQuantThreads;
+    for (int64_t i = gtid; i < zero16; i += gsize)
+        zero[i] = make_uint4(0u, 0u, 0u, 0u);
+    const long long total = block_exclusive_sums<kQuantThreads>(num_seqs, s_off, s_sums, [&](int b) {
+        const int L = __ldg(seq_lens + b);
+        if (L < 0 || (int64_t)L > (int64_t)out_cols * 16) {
+            if (blockIdx.x == 0)
+                record_error(err, kErrBadMetadata, b);
+            return 0;
+        }
+        return (L + 15) / 16;
+    });
+    if (compact_offsets && blockIdx.x == 0)
+        for (int b = tid; b <= num_seqs; b += kQuantThreads)
+            compact_offsets[b] = s_off[b];
+    const bool over = total > capacity_pages;
+    if (over && gtid == 0)
+        record_error(err, kErrBudget, total);
+    if (over && !poison_tables)
+        return;
+    const int64_t n_tab = (int64_t)num_seqs * out_cols;
+    for (int64_t e = gtid; e < n_tab; e += gsize) {
+        const int b = (int)(e / out_cols), p = (int)(e % out_cols);
+        compact_tables[e] = !over && p < s_off[b + 1] - s_off[b] ? s_off[b] + p : -1;
+    }
+    if (over)
+        return;
+    constexpr int VEC = DH / 8;  // 16-byte vectors of an output row
+    const int hk = pool.num_kv_heads;
+    const uint4 qnan = make_uint4(0x7FC07FC0u, 0x7FC07FC0u, 0x7FC07FC0u, 0x7FC07FC0u);
+    // one (page, head) after another, half of the CTA for K and half for V
+    constexpr int HALF = kQuantThreads / 2;
+    const bool is_v = tid >= HALF;
+    const int ht = tid % HALF;
+    const int64_t units = (int64_t)total * hk;
+    // a pass covers PASS (page, head) units so that every thread has V work
+    constexpr int PASS = HALF / VEC;
+    for (int64_t u0 = (int64_t)blockIdx.x * PASS; u0 < units; u0 += (int64_t)gridDim.x * PASS) {
+        if (is_v) {
+            const int64_t u = u0 + ht / VEC;
+            if (u < units) {
+                const int i = ht % VEC;
+                const int c = (int)(u / hk), h = (int)(u % hk);
+                const int b = owner_of(s_off, num_seqs, c);
+                const int id = __ldg(block_tables + (int64_t)b * max_blocks + (c - s_off[b]));
+                uint4 *dst = v_out + ((int64_t)c * 16 * hk + h) * VEC + i;
+                if (id < 0 || (int64_t)id >= pool.num_blocks) {
+                    if (i == 0 && h == 0)
+                        record_error(err, kErrBadMetadata, b);
+                    for (int t = 0; t < 16; ++t)
+                        dst[(int64_t)t * hk * VEC] = qnan;
+                } else {
+                    const uint8_t *rec = pool.v + (int64_t)id * pool.block_stride + h * pool.head_stride;
+                    uint4 col[4];  // element pairs 4i .. 4i+3, sixteen tokens each
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        col[j] = __ldg(reinterpret_cast<const uint4 *>(rec) + 4 * i + j);
+                    const uint4 sc = __ldg(reinterpret_cast<const uint4 *>(rec + quant_code_bytes(DH)) + i / 2);
+#pragma unroll
+                    for (int t4 = 0; t4 < 4; ++t4) {
+                        auto part = [&](const uint4 &v) { return t4 == 0 ? v.x : t4 == 1 ? v.y : t4 == 2 ? v.z : v.w; };
+                        const uint32_t w0 = part(col[0]), w1 = part(col[1]), w2 = part(col[2]), w3 = part(col[3]);
+                        // 4x4 byte transpose: tokens 4*t4 .. +3
+                        const uint32_t a = __byte_perm(w0, w1, 0x5140), bb = __byte_perm(w0, w1, 0x7362);
+                        const uint32_t e = __byte_perm(w2, w3, 0x5140), f = __byte_perm(w2, w3, 0x7362);
+                        const uint32_t tw[4] = {__byte_perm(a, e, 0x5410), __byte_perm(a, e, 0x7632),
+                                                __byte_perm(bb, f, 0x5410), __byte_perm(bb, f, 0x7632)};
+                        const uint32_t s4 = part(sc);
+                        const uint32_t s01 = e4m3x2_to_f16x2(s4), s23 = e4m3x2_to_f16x2(s4 >> 16);
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            const uint32_t sp = __byte_perm(k < 2 ? s01 : s23, 0u, k % 2 ? 0x3232 : 0x1010);
+                            dst[(int64_t)(4 * t4 + k) * hk * VEC] = values8(tw[k], sp, pool.v_scale);
+                        }
+                    }
+                }
+            }
+        } else {
+            for (int x = ht; x < PASS * 16 * VEC; x += HALF) {
+                const int64_t u = u0 + x / (16 * VEC);
+                if (u >= units)
+                    break;
+                const int r = x % (16 * VEC), t = r / VEC, i = r % VEC;
+                const int c = (int)(u / hk), h = (int)(u % hk);
+                const int b = owner_of(s_off, num_seqs, c);
+                const int id = __ldg(block_tables + (int64_t)b * max_blocks + (c - s_off[b]));
+                uint4 v = qnan;
+                if (id >= 0 && (int64_t)id < pool.num_blocks) {
+                    const uint8_t *rec = pool.k + (int64_t)id * pool.block_stride + h * pool.head_stride;
+                    const uint32_t w = __ldg(reinterpret_cast<const uint32_t *>(rec) + t * VEC + i);
+                    const uint32_t s = e4m3x2_to_f16x2(__ldg(rec + quant_code_bytes(DH) + t * (DH / 16) + i / 2));
+                    v = values8(w, __byte_perm(s, 0u, 0x1010), pool.k_scale);
+                }
+                k_out[(((int64_t)c * 16 + t) * hk + h) * VEC + i] = v;
+            }
+        }
+    }
+}
+
+cudaError_t launch_dequantize_kv(const QuantPool &pool, const int32_t *block_tables, int32_t max_blocks,
+                                 const int32_t *seq_lens, int32_t num_seqs, void *k_out, void *v_out,
+                                 int64_t capacity_pages, int32_t *compact_tables, int32_t out_cols,
+                                 int32_t *compact_offsets, bool poison_tables, void *zero, size_t zero_bytes,
+                                 ErrState *err, cudaStream_t stream, int num_sms, int64_t *grid)
+{
+    const int pass = kQuantThreads / 2 / (pool.head_dim / 8);
+    int64_t pages = (int64_t)num_seqs * out_cols;
+    if (pages > capacity_pages)
+        pages = capacity_pages;
+    int64_t blocks = (pages * pool.num_kv_heads + pass - 1) / pass;
+    const int64_t tab = ((int64_t)num_seqs * out_cols + kQuantThreads - 1) / kQuantThreads;
+    if (blocks < tab)
+        blocks = tab;
+    if (blocks > (int64_t)num_sms * 8)
+        blocks = (int64_t)num_sms * 8;
+    if (blocks < 1)
+        blocks = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)blocks);
+    cfg.blockDim = dim3(kQuantThreads);
+    cfg.dynamicSmemBytes = (size_t)(num_seqs + 1) * 4;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    *grid = blocks;
+    void (*kern)(QuantPool, const int32_t *, int32_t, const int32_t *, int32_t, uint4 *, uint4 *, int64_t, int32_t *,
+                 int32_t, int32_t *, bool, uint4 *, int64_t, ErrState *) =
+        pool.head_dim == 128 ? dequantize_kv_kernel<128>
+                             : (pool.head_dim == 256 ? dequantize_kv_kernel<256> : dequantize_kv_kernel<512>);
+    return cudaLaunchKernelEx(&cfg, kern, pool, block_tables, max_blocks, seq_lens, num_seqs,
+                              static_cast<uint4 *>(k_out), static_cast<uint4 *>(v_out), capacity_pages, compact_tables,
+                              out_cols, compact_offsets, poison_tables, static_cast<uint4 *>(zero),
+                              (int64_t)(zero_bytes / 16), err);
+}
+
+cudaError_t init_quant_attributes()
+{
+    const int bytes = (kScanMaxSeqs + 1) * 4;
+    cudaError_t e;
+    if ((e = cudaFuncSetAttribute(dequantize_kv_kernel<128>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes)) !=
+            cudaSuccess ||
+        (e = cudaFuncSetAttribute(dequantize_kv_kernel<256>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes)) !=
+            cudaSuccess)
+        return e;
+    return cudaFuncSetAttribute(dequantize_kv_kernel<512>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+}
+
+}  // namespace pa

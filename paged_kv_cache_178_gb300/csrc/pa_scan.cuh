@@ -1,0 +1,67 @@
+// Block-wide exclusive sums over the requests of a batch, shared by the
+// kernels that turn per-request lengths into offsets.
+#pragma once
+#include <cstdint>
+
+namespace pa {
+
+// Largest batch those kernels take: their offsets sit in shared memory.
+constexpr int kScanMaxSeqs = 8192;
+
+// Exclusive prefix sums of count(b), b in [0, n), into off[0..n] (off[n] =
+// the total) by all NTH threads of the CTA.  The returned total is exact in
+// 64 bits; off[] holds the low 32 bits, so callers check the total against
+// their own (32-bit) limit before they use it.  `warp_sums` is scratch for
+// NTH/32 values.  Ends with a CTA barrier.
+template <int NTH, typename Count>
+__device__ __forceinline__ long long block_exclusive_sums(int n, int32_t *off, long long *warp_sums, Count count)
+{
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    long long base = 0;
+    for (int b0 = 0; b0 < n; b0 += NTH) {
+        const int b = b0 + tid;
+        const long long c = b < n ? (long long)count(b) : 0;
+        long long incl = c;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const long long x = __shfl_up_sync(0xffffffffu, incl, o);
+            if (lane >= o)
+                incl += x;
+        }
+        if (lane == 31)
+            warp_sums[warp] = incl;
+        __syncthreads();
+        long long before = base, total = base;
+#pragma unroll
+        for (int w = 0; w < NTH / 32; ++w) {
+            const long long s = warp_sums[w];
+            before += w < warp ? s : 0;
+            total += s;
+        }
+        if (b < n)
+            off[b] = (int32_t)(before + incl - c);
+        base = total;
+        __syncthreads();  // warp_sums is reused by the next pass
+    }
+    if (tid == 0)
+        off[n] = (int32_t)base;
+    __syncthreads();
+    return base;
+}
+
+// The last b in [0, n) with off[b] <= x: the request that owns item x (off[]
+// as above, x below the total; requests without items are passed over).
+__device__ __forceinline__ int owner_of(const int32_t *off, int n, int x)
+{
+    int lo = 0, hi = n - 1;
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (off[mid] <= x)
+            lo = mid;
+        else
+            hi = mid - 1;
+    }
+    return lo;
+}
+
+}  // namespace pa

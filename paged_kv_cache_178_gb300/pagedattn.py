@@ -10,6 +10,12 @@ fails, an exception is raised.
                     query_start_loc, scale, max_query_len, max_seq_len)
     prepare_reshape_and_cache(...) / prepare_paged_attention(...)
         the same calls validated once, re-issued by calling the result
+    build_step_metadata(...), qk_norm_rope(...), qk_norm_rope_and_cache(...)
+        what a step needs before them: tables, slots and positions from the
+        request lengths; the norm and rotation of queries and keys
+    QuantCache, reshape_and_cache_quant(...), dequantize_kv(...),
+    paged_attention_quant(...)
+        the cache in 4 bits: its write, read-back and attention
 
 k_cache / v_cache are [num_blocks, 16, Hkv, Dh] BF16 views (they may be
 slices of one interleaved [num_blocks, 2, 16, Hkv, Dh] pool) with identical
@@ -38,7 +44,9 @@ PA_ERR_CUDA = 6
 EXPORTED = ("pa_init", "pa_reshape_and_cache", "pa_paged_attention_workspace_size",
             "pa_paged_attention", "pa_paged_attention_noalloc", "pa_reshape_and_paged_attention",
             "pa_gather_kv_head", "pa_check_errors", "pa_set_fold_wait_limit_ns",
-            "pa_copy_to_device", "pa_status_string", "pa_last_launch_info")
+            "pa_copy_to_device", "pa_status_string", "pa_last_launch_info", "pa_build_step_metadata",
+            "pa_qk_norm_rope", "pa_qk_norm_rope_and_cache", "pa_reshape_and_cache_quant", "pa_dequantize_kv",
+            "pa_paged_attention_quant_workspace_size", "pa_paged_attention_quant")
 NOALLOC_SCRATCH_BYTES = 8 << 20
 
 
@@ -48,6 +56,14 @@ class PaKvCache(ctypes.Structure):
                 ("head_dim", ctypes.c_int32), ("kv_tile", ctypes.c_int32),
                 ("block_stride", ctypes.c_int64), ("token_stride", ctypes.c_int64),
                 ("head_stride", ctypes.c_int64)]
+
+
+class PaQuantCache(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("num_blocks", ctypes.c_int64),
+                ("block_size", ctypes.c_int32), ("num_kv_heads", ctypes.c_int32),
+                ("head_dim", ctypes.c_int32), ("reserved", ctypes.c_int32),
+                ("block_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64),
+                ("k_scale", ctypes.c_float), ("v_scale", ctypes.c_float)]
 
 
 class PagedAttnError(RuntimeError):
@@ -96,6 +112,24 @@ def load(path: str = LIB_PATH):
         lib.pa_set_fold_wait_limit_ns.argtypes = [ctypes.c_uint64]
         lib.pa_copy_to_device.restype = i32
         lib.pa_copy_to_device.argtypes = [vp, vp, sz, i32, vp]
+        f32, qc = ctypes.c_float, ctypes.POINTER(PaQuantCache)
+        lib.pa_build_step_metadata.restype = i32
+        lib.pa_build_step_metadata.argtypes = [vp, vp, i32, vp, i32, vp, i32, vp, vp, i64, vp, vp, i64, vp, vp, vp]
+        lib.pa_qk_norm_rope.restype = i32
+        lib.pa_qk_norm_rope.argtypes = [vp, i64, i32, vp, i64, i32, i32, i64, vp, vp, i64, i32, i32, vp, vp, f32, f32,
+                                        vp, i64, vp, i64, vp]
+        lib.pa_qk_norm_rope_and_cache.restype = i32
+        lib.pa_qk_norm_rope_and_cache.argtypes = [vp, i64, i32, vp, i64, vp, i64, i64, vp, vp, i64, i32, i32, vp, vp,
+                                                  f32, f32, vp, i64, ctypes.POINTER(PaKvCache), vp, vp]
+        lib.pa_reshape_and_cache_quant.restype = i32
+        lib.pa_reshape_and_cache_quant.argtypes = [vp, i64, vp, i64, i64, qc, vp, vp]
+        lib.pa_dequantize_kv.restype = i32
+        lib.pa_dequantize_kv.argtypes = [qc, vp, i32, vp, i32, vp, vp, i64, vp, vp, vp]
+        lib.pa_paged_attention_quant_workspace_size.restype = sz
+        lib.pa_paged_attention_quant_workspace_size.argtypes = [i32, i32, i32, i32, i32, i32, i64]
+        lib.pa_paged_attention_quant.restype = i32
+        lib.pa_paged_attention_quant.argtypes = [vp, i64, i64, i32, qc, vp, i32, vp, vp, i32, i32, i32, i64, f32, vp,
+                                                 vp, vp, sz, vp]
         lib.pa_status_string.restype = ctypes.c_char_p
         lib.pa_status_string.argtypes = [i32]
         lib.pa_last_launch_info.restype = None
@@ -480,6 +514,330 @@ def prepare_gather_kv_head(k_cache: torch.Tensor, v_cache: torch.Tensor, kv_head
             seq_lens.numel(), packed_k.data_ptr(), packed_v.data_ptr(), cap, compact_tables.data_ptr(),
             compact_offsets.data_ptr(), _stream_handle(stream))
     return PreparedCall(load().pa_gather_kv_head, args, "pa_gather_kv_head", keep)
+
+
+def _require_i32(**tensors: torch.Tensor) -> None:
+    for name, t in tensors.items():
+        if t.dtype != torch.int32 or not t.is_cuda or not t.is_contiguous():
+            raise ValueError(f"{name} must be a contiguous int32 CUDA tensor")
+
+
+def _require_same_device(*tensors: Optional[torch.Tensor]) -> None:
+    """The library launches on the current device: every tensor must be there."""
+    here = torch.cuda.current_device()
+    for t in tensors:
+        if t is not None and t.is_cuda and t.device.index != here:
+            raise ValueError(f"tensors must be on the current CUDA device (cuda:{here}), got {t.device}")
+
+
+def prepare_build_step_metadata(context_lens: torch.Tensor, query_lens: torch.Tensor, block_tables: torch.Tensor,
+                                free_pages: torch.Tensor, num_blocks: int, slot_mapping: torch.Tensor,
+                                positions: torch.Tensor, seq_lens: torch.Tensor, query_start_loc: torch.Tensor,
+                                cursor_out: torch.Tensor, cursor_in: Optional[torch.Tensor] = None,
+                                stream: Optional[torch.cuda.Stream] = None) -> PreparedCall:
+    """build_step_metadata, validated now and issued by each call of the result."""
+    _require_i32(context_lens=context_lens, query_lens=query_lens, block_tables=block_tables, free_pages=free_pages,
+                 positions=positions, seq_lens=seq_lens, query_start_loc=query_start_loc, cursor_out=cursor_out)
+    if cursor_in is not None:
+        _require_i32(cursor_in=cursor_in)
+    if slot_mapping.dtype != torch.int64 or not slot_mapping.is_cuda or not slot_mapping.is_contiguous():
+        raise ValueError("slot_mapping must be a contiguous int64 CUDA tensor")
+    _require_same_device(context_lens, query_lens, block_tables, free_pages, slot_mapping, positions, seq_lens,
+                         query_start_loc, cursor_out, cursor_in)
+    n = context_lens.numel()
+    if query_lens.numel() != n or seq_lens.numel() != n or query_start_loc.numel() != n + 1 \
+            or block_tables.dim() != 2 or block_tables.shape[0] != n or positions.numel() != slot_mapping.numel() \
+            or cursor_out.numel() != 1 or (cursor_in is not None and cursor_in.numel() != 1):
+        raise ValueError("metadata shapes disagree")
+    args = (context_lens.data_ptr(), query_lens.data_ptr(), n, block_tables.data_ptr(), block_tables.shape[1],
+            free_pages.data_ptr(), free_pages.numel(), cursor_in.data_ptr() if cursor_in is not None else 0,
+            cursor_out.data_ptr(), int(num_blocks), slot_mapping.data_ptr(), positions.data_ptr(),
+            slot_mapping.numel(), seq_lens.data_ptr(), query_start_loc.data_ptr(), _stream_handle(stream))
+    return PreparedCall(load().pa_build_step_metadata, args, "pa_build_step_metadata",
+                        (context_lens, query_lens, block_tables, free_pages, slot_mapping, positions, seq_lens,
+                         query_start_loc, cursor_out, cursor_in))
+
+
+def build_step_metadata(context_lens: torch.Tensor, query_lens: torch.Tensor, block_tables: torch.Tensor,
+                        free_pages: torch.Tensor, num_blocks: int, slot_mapping: torch.Tensor,
+                        positions: torch.Tensor, seq_lens: torch.Tensor, query_start_loc: torch.Tensor,
+                        cursor_out: torch.Tensor, cursor_in: Optional[torch.Tensor] = None,
+                        stream: Optional[torch.cuda.Stream] = None) -> None:
+    """One step's metadata from context_lens and query_lens [B] (int32): pages
+    from free_pages (from index cursor_in on) enter block_tables [B, max_blocks];
+    slot_mapping (int64) and positions [N] of the new tokens (-1 past them),
+    seq_lens [B], query_start_loc [B + 1] and cursor_out [1] are written.
+    seq_lens may be context_lens, cursor_out may be cursor_in."""
+    prepare_build_step_metadata(context_lens, query_lens, block_tables, free_pages, num_blocks, slot_mapping,
+                                positions, seq_lens, query_start_loc, cursor_out, cursor_in, stream)()
+
+
+def rope_table(max_positions: int, rot_dim: int, theta: float = 10000.0, device=None) -> torch.Tensor:
+    """The [max_positions, rot_dim] fp32 cos/sin table of qk_norm_rope for the
+    angles p * theta**(-2i/rot_dim), computed in 64 bits and rounded once."""
+    i = torch.arange(0, rot_dim, 2, dtype=torch.float64, device=device)
+    angle = torch.arange(max_positions, dtype=torch.float64, device=device)[:, None] * float(theta) ** (-i / rot_dim)
+    return torch.cat([angle.cos(), angle.sin()], dim=1).float().contiguous()
+
+
+def _head_rows(name: str, t: torch.Tensor) -> None:
+    if t.dtype != torch.bfloat16 or not t.is_cuda or t.dim() != 3 or t.stride(2) != 1 \
+            or (t.shape[1] > 1 and t.stride(1) != t.shape[2]):
+        raise ValueError(f"{name} must be a [T, heads, Dh] BF16 CUDA tensor with contiguous heads")
+
+
+def _tok_stride(t: torch.Tensor) -> int:
+    """Token stride; that of one token does not matter (torch may report any)."""
+    return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), t.shape[1] * t.shape[2])
+
+
+def _rope_args(q, k, positions, cos_sin, q_out, q_weight, k_weight):
+    for name, t in (("q", q), ("k", k), ("q_out", q_out)):
+        _head_rows(name, t)
+    _require_i32(positions=positions)
+    n, dh = q.shape[0], q.shape[2]
+    if k.shape[0] != n or k.shape[2] != dh or q_out.shape != q.shape or positions.numel() != n:
+        raise ValueError("q, k, q_out and positions disagree")
+    if cos_sin.dtype != torch.float32 or not cos_sin.is_cuda or not cos_sin.is_contiguous() or cos_sin.dim() != 2:
+        raise ValueError("cos_sin must be a contiguous [max_positions, rot_dim] fp32 CUDA tensor")
+    for name, w in (("q_weight", q_weight), ("k_weight", k_weight)):
+        if w is not None and (w.dtype != torch.bfloat16 or not w.is_cuda or not w.is_contiguous() or w.numel() != dh):
+            raise ValueError(f"{name} must be a contiguous [Dh] BF16 CUDA tensor")
+    return n, dh
+
+
+def _ptr(t: Optional[torch.Tensor]) -> int:
+    return t.data_ptr() if t is not None else 0
+
+
+def prepare_qk_norm_rope(q: torch.Tensor, k: torch.Tensor, positions: torch.Tensor, cos_sin: torch.Tensor,
+                         q_out: torch.Tensor, k_out: torch.Tensor, q_weight: Optional[torch.Tensor] = None,
+                         k_weight: Optional[torch.Tensor] = None, eps: float = 1e-6, interleaved: bool = False,
+                         weight_offset: float = 0.0, stream: Optional[torch.cuda.Stream] = None) -> PreparedCall:
+    """qk_norm_rope, validated now and issued by each call of the result."""
+    n, dh = _rope_args(q, k, positions, cos_sin, q_out, q_weight, k_weight)
+    _head_rows("k_out", k_out)
+    if k_out.shape != k.shape:
+        raise ValueError("k_out must have k's shape")
+    _require_same_device(q, k, positions, cos_sin, q_out, k_out, q_weight, k_weight)
+    args = (q.data_ptr(), _tok_stride(q), q.shape[1], k.data_ptr(), _tok_stride(k), k.shape[1], dh, n,
+            positions.data_ptr(), cos_sin.data_ptr(), cos_sin.shape[0], cos_sin.shape[1], 1 if interleaved else 0,
+            _ptr(q_weight), _ptr(k_weight), ctypes.c_float(weight_offset), ctypes.c_float(eps), q_out.data_ptr(),
+            _tok_stride(q_out), k_out.data_ptr(), _tok_stride(k_out), _stream_handle(stream))
+    return PreparedCall(load().pa_qk_norm_rope, args, "pa_qk_norm_rope",
+                        (q, k, positions, cos_sin, q_out, k_out, q_weight, k_weight))
+
+
+def qk_norm_rope(q: torch.Tensor, k: torch.Tensor, positions: torch.Tensor, cos_sin: torch.Tensor,
+                 q_out: Optional[torch.Tensor] = None, k_out: Optional[torch.Tensor] = None,
+                 q_weight: Optional[torch.Tensor] = None, k_weight: Optional[torch.Tensor] = None, eps: float = 1e-6,
+                 interleaved: bool = False, weight_offset: float = 0.0,
+                 stream: Optional[torch.cuda.Stream] = None) -> Tuple[torch.Tensor, torch.Tensor]:
+    """RMS norm of every head row of q [T, Hq, Dh] and k [T, Hkv, Dh] (where a
+    weight is given), then the rotation by positions [T] (int32, -1: padding, the
+    row is left untouched) with cos_sin (see rope_table).  q_out / k_out may be
+    q / k.  Returns (q_out, k_out)."""
+    q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device) if q_out is None else q_out
+    k_out = torch.empty(k.shape, dtype=k.dtype, device=k.device) if k_out is None else k_out
+    prepare_qk_norm_rope(q, k, positions, cos_sin, q_out, k_out, q_weight, k_weight, eps, interleaved, weight_offset,
+                         stream)()
+    return q_out, k_out
+
+
+def prepare_qk_norm_rope_and_cache(q: torch.Tensor, k: torch.Tensor, value: torch.Tensor, positions: torch.Tensor,
+                                   cos_sin: torch.Tensor, q_out: torch.Tensor, k_cache: torch.Tensor,
+                                   v_cache: torch.Tensor, slot_mapping: torch.Tensor,
+                                   q_weight: Optional[torch.Tensor] = None, k_weight: Optional[torch.Tensor] = None,
+                                   eps: float = 1e-6, interleaved: bool = False, weight_offset: float = 0.0,
+                                   stream: Optional[torch.cuda.Stream] = None) -> PreparedCall:
+    """qk_norm_rope_and_cache, validated now and issued by each call of the result."""
+    c = cache_struct(k_cache, v_cache)
+    n, dh = _rope_args(q, k, positions, cos_sin, q_out, q_weight, k_weight)
+    _head_rows("value", value)
+    if value.shape != k.shape or k.shape[1] != c.num_kv_heads or dh != c.head_dim:
+        raise ValueError("k and value must be [T, Hkv, Dh] of the cache")
+    if slot_mapping.dtype != torch.int64 or not slot_mapping.is_cuda or not slot_mapping.is_contiguous() \
+            or slot_mapping.numel() != n:
+        raise ValueError("slot_mapping must be a contiguous int64 CUDA tensor of one slot per token")
+    _require_same_device(q, k, value, positions, cos_sin, q_out, k_cache, v_cache, slot_mapping, q_weight, k_weight)
+    args = (q.data_ptr(), _tok_stride(q), q.shape[1], k.data_ptr(), _tok_stride(k), value.data_ptr(),
+            _tok_stride(value), n, positions.data_ptr(), cos_sin.data_ptr(), cos_sin.shape[0], cos_sin.shape[1],
+            1 if interleaved else 0, _ptr(q_weight), _ptr(k_weight), ctypes.c_float(weight_offset),
+            ctypes.c_float(eps), q_out.data_ptr(), _tok_stride(q_out), ctypes.byref(c), slot_mapping.data_ptr(),
+            _stream_handle(stream))
+    return PreparedCall(load().pa_qk_norm_rope_and_cache, args, "pa_qk_norm_rope_and_cache",
+                        (q, k, value, positions, cos_sin, q_out, k_cache, v_cache, slot_mapping, q_weight, k_weight, c))
+
+
+def qk_norm_rope_and_cache(q: torch.Tensor, k: torch.Tensor, value: torch.Tensor, positions: torch.Tensor,
+                           cos_sin: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
+                           slot_mapping: torch.Tensor, q_out: Optional[torch.Tensor] = None,
+                           q_weight: Optional[torch.Tensor] = None, k_weight: Optional[torch.Tensor] = None,
+                           eps: float = 1e-6, interleaved: bool = False, weight_offset: float = 0.0,
+                           stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
+    """qk_norm_rope and the cache write in one pass: the rotated keys and the
+    values go to slot_mapping of the BF16 pool.  Returns q_out."""
+    q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device) if q_out is None else q_out
+    prepare_qk_norm_rope_and_cache(q, k, value, positions, cos_sin, q_out, k_cache, v_cache, slot_mapping, q_weight,
+                                   k_weight, eps, interleaved, weight_offset, stream)()
+    return q_out
+
+
+def quant_record_bytes(head_dim: int) -> int:
+    """Bytes of one page's K (or V) of one head in a 4-bit pool."""
+    return 9 * int(head_dim)
+
+
+class QuantCache:
+    """A paged KV cache in 4 bits: byte pools k_pool, v_pool [num_blocks, Hkv,
+    9*Dh] (two tensors, or the slices [:, 0] and [:, 1] of one [num_blocks, 2,
+    Hkv, 9*Dh] tensor) with identical strides, and the power-of-two factors
+    k_scale, v_scale of all their values."""
+
+    def __init__(self, k_pool: torch.Tensor, v_pool: torch.Tensor, head_dim: int, k_scale: float = 1.0,
+                 v_scale: float = 1.0):
+        for t in (k_pool, v_pool):
+            if t.dtype != torch.uint8 or not t.is_cuda or t.dim() != 3 or t.stride(2) != 1 \
+                    or t.shape[2] != quant_record_bytes(head_dim):
+                raise ValueError("4-bit pools must be [num_blocks, Hkv, 9*Dh] uint8 CUDA tensors with contiguous records")
+        if k_pool.shape != v_pool.shape or k_pool.stride() != v_pool.stride():
+            raise ValueError("K and V pools must have the same shape and strides")
+        self.k_pool, self.v_pool = k_pool, v_pool
+        self.head_dim, self.num_kv_heads, self.num_blocks = int(head_dim), k_pool.shape[1], k_pool.shape[0]
+        self.struct = PaQuantCache(k_pool.data_ptr(), v_pool.data_ptr(), k_pool.shape[0], 16, k_pool.shape[1],
+                                   int(head_dim), 0, k_pool.stride(0), k_pool.stride(1), float(k_scale),
+                                   float(v_scale))
+
+
+def new_quant_cache(num_blocks: int, num_kv_heads: int, head_dim: int, k_scale: float = 1.0, v_scale: float = 1.0,
+                    device=None) -> QuantCache:
+    """A zero-filled interleaved 4-bit cache (every value reads as 0)."""
+    pool = torch.zeros((num_blocks, 2, num_kv_heads, quant_record_bytes(head_dim)), dtype=torch.uint8,
+                       device=device if device is not None else "cuda")
+    return QuantCache(pool[:, 0], pool[:, 1], head_dim, k_scale, v_scale)
+
+
+def prepare_reshape_and_cache_quant(key: torch.Tensor, value: torch.Tensor, cache: QuantCache,
+                                    slot_mapping: torch.Tensor,
+                                    stream: Optional[torch.cuda.Stream] = None) -> PreparedCall:
+    """reshape_and_cache_quant, validated now and issued by each call of the result."""
+    n = key.shape[0]
+    for name, t in (("key", key), ("value", value)):
+        _head_rows(name, t)
+        if tuple(t.shape) != (n, cache.num_kv_heads, cache.head_dim):
+            raise ValueError(f"{name} must be [N, Hkv, Dh] of the cache")
+    if slot_mapping.dtype != torch.int64 or not slot_mapping.is_cuda or not slot_mapping.is_contiguous() \
+            or slot_mapping.numel() != n:
+        raise ValueError("slot_mapping must be a contiguous int64 CUDA tensor of one slot per token")
+    _require_same_device(key, value, cache.k_pool, slot_mapping)
+    args = (key.data_ptr(), _tok_stride(key), value.data_ptr(), _tok_stride(value), n, ctypes.byref(cache.struct),
+            slot_mapping.data_ptr(), _stream_handle(stream))
+    return PreparedCall(load().pa_reshape_and_cache_quant, args, "pa_reshape_and_cache_quant",
+                        (key, value, cache, slot_mapping))
+
+
+def reshape_and_cache_quant(key: torch.Tensor, value: torch.Tensor, cache: QuantCache, slot_mapping: torch.Tensor,
+                            stream: Optional[torch.cuda.Stream] = None) -> None:
+    """Quantise key/value [N, Hkv, Dh] into the 4-bit cache at slot_mapping [N]
+    (int64); negative slots are skipped."""
+    prepare_reshape_and_cache_quant(key, value, cache, slot_mapping, stream)()
+
+
+def prepare_dequantize_kv(cache: QuantCache, block_tables: torch.Tensor, seq_lens: torch.Tensor, k_out: torch.Tensor,
+                          v_out: torch.Tensor, compact_tables: torch.Tensor, compact_offsets: torch.Tensor,
+                          stream: Optional[torch.cuda.Stream] = None) -> PreparedCall:
+    """dequantize_kv, validated now and issued by each call of the result."""
+    _require_i32(block_tables=block_tables, seq_lens=seq_lens, compact_tables=compact_tables,
+                 compact_offsets=compact_offsets)
+    num_seqs = seq_lens.numel()
+    if block_tables.dim() != 2 or block_tables.shape[0] != num_seqs or compact_tables.shape != block_tables.shape \
+            or compact_offsets.numel() != num_seqs + 1:
+        raise ValueError("metadata shapes disagree")
+    for t in (k_out, v_out):
+        if t.dtype != torch.bfloat16 or not t.is_cuda or not t.is_contiguous() or t.dim() != 4 \
+                or tuple(t.shape[1:]) != (16, cache.num_kv_heads, cache.head_dim):
+            raise ValueError("k_out/v_out must be contiguous BF16 CUDA tensors [capacity_pages, 16, Hkv, Dh]")
+    if k_out.shape != v_out.shape:
+        raise ValueError("k_out and v_out must have the same capacity")
+    _require_same_device(cache.k_pool, block_tables, seq_lens, k_out, v_out, compact_tables, compact_offsets)
+    args = (ctypes.byref(cache.struct), block_tables.data_ptr(), block_tables.shape[1], seq_lens.data_ptr(), num_seqs,
+            k_out.data_ptr(), v_out.data_ptr(), k_out.shape[0], compact_tables.data_ptr(), compact_offsets.data_ptr(),
+            _stream_handle(stream))
+    return PreparedCall(load().pa_dequantize_kv, args, "pa_dequantize_kv",
+                        (cache, block_tables, seq_lens, k_out, v_out, compact_tables, compact_offsets))
+
+
+def dequantize_kv(cache: QuantCache, block_tables: torch.Tensor, seq_lens: torch.Tensor, k_out: torch.Tensor,
+                  v_out: torch.Tensor, compact_tables: torch.Tensor, compact_offsets: torch.Tensor,
+                  stream: Optional[torch.cuda.Stream] = None) -> None:
+    """Read the pages that block_tables/seq_lens select back into k_out/v_out
+    [capacity_pages, 16, Hkv, Dh] (a BF16 pool of their own), writing the compact
+    table [B, max_blocks] and page offsets [B + 1]."""
+    prepare_dequantize_kv(cache, block_tables, seq_lens, k_out, v_out, compact_tables, compact_offsets, stream)()
+
+
+def quant_workspace_size(num_seqs: int, num_q_heads: int, num_kv_heads: int, head_dim: int, max_query_len: int,
+                         max_seq_len: int, max_pages: int = 0) -> int:
+    return int(load().pa_paged_attention_quant_workspace_size(num_seqs, num_q_heads, num_kv_heads, head_dim,
+                                                              max_query_len, max_seq_len, max_pages))
+
+
+def new_quant_workspace(num_seqs: int, num_q_heads: int, num_kv_heads: int, head_dim: int, max_query_len: int,
+                        max_seq_len: int, max_pages: int = 0, device=None) -> torch.Tensor:
+    """Zero-filled scratch for paged_attention_quant (reusable across calls)."""
+    n = quant_workspace_size(num_seqs, num_q_heads, num_kv_heads, head_dim, max_query_len, max_seq_len, max_pages)
+    return torch.zeros(max(n, 256), dtype=torch.uint8, device=device if device is not None else "cuda")
+
+
+def prepare_paged_attention_quant(q: torch.Tensor, cache: QuantCache, block_tables: torch.Tensor,
+                                  seq_lens: torch.Tensor, query_start_loc: torch.Tensor, scale: float,
+                                  max_query_len: int, max_seq_len: int, out: torch.Tensor,
+                                  lse: Optional[torch.Tensor], workspace: torch.Tensor, max_pages: int = 0,
+                                  stream: Optional[torch.cuda.Stream] = None) -> PreparedCall:
+    """paged_attention_quant into given out / lse / workspace, validated now
+    and issued by each call of the result."""
+    tq, hq, dh, num_seqs = _validate_attention(q, block_tables, seq_lens, query_start_loc)
+    if dh != cache.head_dim:
+        raise ValueError("q and the cache disagree on the head dim")
+    if out.shape != (tq, hq, dh) or out.dtype != torch.bfloat16 or not out.is_contiguous():
+        raise ValueError("out must be a contiguous [Tq, Hq, Dh] BF16 tensor")
+    if lse is not None and (lse.shape != (tq, hq) or lse.dtype != torch.float32 or not lse.is_contiguous()):
+        raise ValueError("lse must be a contiguous [Tq, Hq] fp32 tensor")
+    _check_result_tensor("out", out)
+    if lse is not None:
+        _check_result_tensor("lse", lse)
+    _require_same_device(q, cache.k_pool, block_tables, seq_lens, query_start_loc, out, lse, workspace)
+    need = quant_workspace_size(num_seqs, hq, cache.num_kv_heads, dh, max_query_len, max_seq_len, max_pages)
+    ws_len = workspace.numel() * workspace.element_size() if workspace is not None else 0
+    if ws_len < need:
+        raise ValueError(f"workspace needs {need} bytes")
+    args = (q.data_ptr(), tq, _tok_stride(q), hq, ctypes.byref(cache.struct), block_tables.data_ptr(),
+            block_tables.shape[1], seq_lens.data_ptr(), query_start_loc.data_ptr(), num_seqs, int(max_query_len),
+            int(max_seq_len), int(max_pages), ctypes.c_float(float(scale)), out.data_ptr(), _ptr(lse),
+            _ptr(workspace), ws_len, _stream_handle(stream))
+    return PreparedCall(load().pa_paged_attention_quant, args, "pa_paged_attention_quant",
+                        (q, cache, block_tables, seq_lens, query_start_loc, out, lse, workspace))
+
+
+def paged_attention_quant(q: torch.Tensor, cache: QuantCache, block_tables: torch.Tensor, seq_lens: torch.Tensor,
+                          query_start_loc: torch.Tensor, scale: float, max_query_len: int, max_seq_len: int,
+                          out: Optional[torch.Tensor] = None, lse: Optional[torch.Tensor] = None,
+                          want_lse: bool = True, workspace: Optional[torch.Tensor] = None, max_pages: int = 0,
+                          stream: Optional[torch.cuda.Stream] = None
+                          ) -> Tuple[torch.Tensor, Optional[torch.Tensor]]:
+    """Causal GQA attention of q [Tq, Hq, Dh] over the 4-bit cache.  Returns
+    (out [Tq, Hq, Dh] BF16, lse [Tq, Hq] fp32 or None)."""
+    tq, hq, dh = q.shape
+    if out is None:
+        out = torch.empty((tq, hq, dh), dtype=torch.bfloat16, device=q.device)
+    if lse is None and want_lse:
+        lse = torch.empty((tq, hq), dtype=torch.float32, device=q.device)
+    if workspace is None:
+        workspace = new_quant_workspace(seq_lens.numel(), hq, cache.num_kv_heads, dh, max_query_len, max_seq_len,
+                                        max_pages, q.device)
+    prepare_paged_attention_quant(q, cache, block_tables, seq_lens, query_start_loc, scale, max_query_len,
+                                  max_seq_len, out, lse, workspace, max_pages, stream)()
+    return out, lse
 
 
 def check_errors(stream: Optional[torch.cuda.Stream] = None) -> Tuple[int, int]:
