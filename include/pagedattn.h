@@ -511,8 +511,8 @@ PA_API size_t pa_paged_attention_quant_workspace_size(int32_t num_seqs, int32_t 
  * pa_paged_attention over a 4-bit pool: the softmax attention of q over the
  * values that the pool stands for.  Arguments, ownership and errors as for
  * pa_paged_attention; max_pages as in the workspace size.
- *   - Few rows (max_query_len * Hq/Hkv up to 64 at head dim 128, 32 at 256
- *     and 512: decode steps, drafted tokens): one kernel reads the codes
+ *   - Few rows (max_query_len * Hq/Hkv up to 32, at head dim 512 up to
+ *     16: decode steps, drafted tokens): one kernel reads the codes
  *     directly.  It has a fixed schedule of its own: a row's results are
  *     bitwise the same whatever the batch, the other requests and the bounds
  *     (within that limit).
@@ -528,7 +528,8 @@ PA_API size_t pa_paged_attention_quant_workspace_size(int32_t num_seqs, int32_t 
  *     pa_paged_attention_quant_workspace_size for the call's bounds; one
  *     workspace may serve calls with different bounds (one after the other)
  *     if it is large enough for each.
- * num_seqs <= 8192; num_seqs * Hkv <= 65536.
+ * num_seqs <= 8192; with few rows also num_seqs * Hkv * (1 + the number of
+ * 8192-key spans (4096 at head dim 512) of max_seq_len) <= 262144.
  */
 PA_API pa_status pa_paged_attention_quant(const void *q, int64_t num_q_tokens, int64_t q_tok_stride,
                                           int32_t num_q_heads, const pa_quant_cache *cache,

@@ -1042,7 +1042,7 @@ pa_status pa_dequantize_kv(const pa_quant_cache *cache, const int32_t *block_tab
 // same for all bounds, so whatever another call leaves behind it they stay
 // zero between calls; the counters of the BF16 attention over read-back pages
 // are cleared by the read-back itself.
-constexpr int64_t kQuantMaxGroups = 65536;
+constexpr int64_t kQuantMaxCounters = 262144;
 struct QuantPlan {
     bool direct;
     size_t records;                     // direct: chunk records
@@ -1062,15 +1062,17 @@ static pa_status plan_quant(int32_t num_seqs, int32_t hq, int32_t hkv, int32_t d
         return PA_ERR_INVALID_ARG;
     if (!plan_attention(num_seqs, hq, hkv, dh, max_query_len, max_seq_len, &pl->attn))
         return PA_ERR_UNSUPPORTED;
-    if (num_seqs > kScanMaxSeqsHost || (int64_t)num_seqs * hkv > kQuantMaxGroups ||
-        (int64_t)num_seqs * (((int64_t)max_seq_len + 15) / 16) > INT32_MAX)
+    if (num_seqs > kScanMaxSeqsHost || (int64_t)num_seqs * (((int64_t)max_seq_len + 15) / 16) > INT32_MAX)
         return PA_ERR_UNSUPPORTED;
     const int64_t rows = (int64_t)max_query_len * (hq / hkv);
     pl->direct = rows <= quant_attn_max_rows(dh);
-    const size_t counters = (size_t)kQuantMaxGroups * 4;
+    const size_t counters = (size_t)kQuantMaxCounters * 4;
     if (pl->direct) {
+        const QuantAttnSpace sp = quant_attn_space(num_seqs, hkv, dh, (int)rows, max_seq_len);
+        if (sp.counters > kQuantMaxCounters)
+            return PA_ERR_UNSUPPORTED;
         pl->records = counters;
-        pl->bytes = counters + quant_attn_record_bytes(num_seqs, hkv, dh, (int)rows, max_seq_len);
+        pl->bytes = counters + sp.chunk_bytes + sp.span_bytes;
         return PA_OK;
     }
     pl->cols = (int32_t)(((int64_t)max_seq_len + 15) / 16);
@@ -1158,7 +1160,7 @@ pa_status pa_paged_attention_quant(const void *q, int64_t num_q_tokens, int64_t 
         a.lse = lse;
         a.counters = reinterpret_cast<uint32_t *>(ws);
         a.records = reinterpret_cast<float *>(ws + pl.records);
-        return cuda_status(launch_quant_attention(a, err, s, nsm, g_last_info, sizeof g_last_info));
+        return cuda_status(launch_quant_attention(a, err, s, g_last_info, sizeof g_last_info));
     }
     // read the selected pages back, then the BF16 attention over them
     const int32_t cols = pl.cols < max_blocks_per_seq ? pl.cols : max_blocks_per_seq;

@@ -5,36 +5,46 @@
 // What bounds it: a 16-token page of one KV head at head dim 128 is 2304
 // bytes (K and V), 98 clocks of an SM's share of the memory bandwidth.  Its
 // 4096 elements need 2048 conversions (two elements each) and as many scale
-// products; both issue at two warp instructions per clock and SM, about 64
-// clocks together with the regrouping of V.  Passing dequantised tiles
-// through shared memory (as operands of tcgen05) would add 16 KB of writes and
-// 16 KB of operand reads per page, 256 clocks at 128 bytes per clock; so the
-// fragments of mma.sync are built in registers, straight from the codes, and
-// nothing dequantised is ever stored.
+// products, which issue at two warp instructions per clock and SM: 64 clocks.
+// So the instruction count decides.  Passing dequantised tiles through shared
+// memory (as operands of tcgen05) would add 16 KB of writes and 16 KB of operand
+// reads per page, 256 clocks at 128 bytes per clock; the fragments of mma.sync
+// are built in registers, straight from the codes, and nothing dequantised is
+// ever stored.
 //
-// The keys (then the head-dim elements) are the M = 16 dimension of
-// mma.m16n8k16 and the query rows its N = 8: one page is one M tile, and up to
-// eight rows cost one instruction.  Everything is f16 with fp32 accumulation:
-// codes times scales are exact there; q is scaled per row by a power of two
-// to [1, 2) at its largest element (elements below 2^-14 of it lose bits, at
-// most 2^-25 of the largest); p is scaled by 2^15 (11 bits down to
-// 2^-29 of the row's largest probability).
+// The products are mma.m16n8k16, f16 with fp32 accumulation.  Codes times
+// scales are exact in f16; q is scaled per row by a power of two to [1, 2) at
+// its largest element (what is below 2^-14 of it loses bits, at most 2^-25 of
+// the largest); p is scaled by 2^15 (11 bits down to 2^-29 of the row's largest
+// probability).
+//   S^T = K.Q^T: M = the 16 tokens of a page, N = 8 query rows, K = head dim.
+//   O^T = V^T.P^T: a V byte holds two neighbouring elements (d, d+1) of one
+//     token, so a converted register is a pair of different M rows.  Up to
+//     eight rows (PAR) the pair is taken as one row with two K indices
+//     (token, parity), and P^T has two columns per query row: (p, 0) gives
+//     element d, (0, p) element d+1.  The wasted half of the product is free
+//     (four rows fill N = 8; eight take two instructions), and no permutes are
+//     needed.  From 16 rows on, permutes that regroup the pairs by element cost
+//     less than doubling the instructions.
 //
 // Fixed arithmetic (a row's results do not depend on the batch or the grid):
-//   tiles of 128 keys from key 0, one page per warp; the running maximum is
-//   exact per tile; chunks of 256 keys start fresh; a chunk's row sum is, per
-//   warp, a butterfly over the keys, then the eight warps' sums pairwise;
-//   chunk states fold left to right (fold_coef, fold_elem).
+//   chunks of 256 keys (128 at head dim 512) from key 0, each with its own exact maximum; a chunk's
+//   row sum is, per warp, a butterfly over its keys, then the eight warps'
+//   sums pairwise; chunk states fold left to right (State::fold) within spans
+//   of 32 chunks, and the span states left to right.
 //
-// A CTA (8 warps): per tile, warp w scores page w, the warps exchange row
-// maxima (barrier), write P to shared memory in fragment order (barrier), and
-// warp w multiplies P by head-dim elements 16w..16w+15 (of each 128) of all
-// pages: O needs no exchange between warps.  Each warp's lane 0 copies page w
-// of the tiles ahead (cp.async.bulk, one mbarrier per tile).  The chunks of
-// all (request, KV head) groups are dealt out as equal contiguous ranges; a
-// group inside one range is folded in registers, the chunks of a group cut by
-// a range end become records, folded by the last CTA to arrive.
+// A CTA (8 warps) per chunk: warp w scores its one or two pages and spreads their
+// V scales (one f16 pair per scale); row maxima are exchanged (barrier); P goes
+// to shared memory in fragment order (barrier); each warp multiplies P by 32
+// head-dim elements of the pages (at head dim 128 of half of the pages, the
+// halves are added through shared memory, with the row sums; barrier).  Each
+// warp copies its pages of the chunk after next (cp.async.bulk, one mbarrier
+// per chunk).  The chunks of all (request, KV head) groups are dealt out as
+// equal contiguous ranges.  A span inside one range is folded in registers; the
+// chunks of a span cut by a range end become records, folded by the last CTA
+// to arrive; so do the spans of a cut group.  No CTA waits for another.
 #include <cstdio>
+#include <type_traits>
 
 #include "pa_attn_common.cuh"
 #include "pa_quant_common.cuh"
@@ -45,40 +55,48 @@ namespace pa {
 
 namespace qa {
 
-constexpr int kThreads = 256;
 constexpr int kWarps = 8;
-constexpr int kTile = 128;   // keys per tile: one page per warp
-constexpr int kChunk = 256;  // keys per chunk
-constexpr int kTilesPerChunk = kChunk / kTile;
-constexpr int kPagesPerChunk = kChunk / 16;
-constexpr float kShift = 15.f;  // p is scaled by 2^kShift (largest f16: 2^16)
+constexpr int kThreads = 32 * kWarps;
+// pages per warp of a chunk: two stages of a chunk fit shared memory
+__host__ __device__ constexpr int pages_per_warp(int dh) { return dh == 512 ? 1 : 2; }
+__host__ __device__ constexpr int chunk_pages(int dh) { return kWarps * pages_per_warp(dh); }
+__host__ __device__ constexpr int chunk_keys(int dh) { return 16 * chunk_pages(dh); }
+constexpr int kSpan = 32;           // chunks per span
+constexpr int kStages = 2;          // chunks in shared memory
+constexpr float kShift = 15.f;      // p is scaled by 2^kShift (largest f16: 2^16)
+constexpr int kGridSms = 152;       // SMs the grid is sized for
 
 template <int DH>
-constexpr int stages() { return DH == 512 ? 2 : 3; }
-template <int DH>
-constexpr int stage_bytes() { return 2 * kWarps * quant_record_bytes(DH); }
-// CTAs per SM that registers (256 threads) and shared memory are sized for
-template <int DH, int NT>
-constexpr int ctas_per_sm()
-{
-    return DH == 128 ? (NT == 1 ? 3 : NT <= 4 ? 2 : 1) : (DH == 256 && NT <= 2 ? 2 : 1);
-}
+constexpr int stage_bytes() { return 2 * chunk_pages(DH) * quant_record_bytes(DH); }
+// CTAs per SM that registers and shared memory are sized for
+template <int DH, int RN>
+constexpr int ctas_per_sm() { return DH == 128 && RN <= 16 ? 2 : 1; }
+// up to eight rows: element parity as a K index (see above)
+template <int RN>
+constexpr bool par_mode() { return RN <= 8; }
 
-// Shared-memory layout in bytes.
-template <int DH, int NT>
+// Shared-memory layout in bytes.  RN: query rows (4, 8, 16 or 32).
+template <int DH, int RN>
 struct Layout {
-    static constexpr int R = 8 * NT;
-    static constexpr int q = stages<DH>() * stage_bytes<DH>();
-    static constexpr int p = q + NT * DH * 16;
-    static constexpr int max = p + kWarps * NT * 256;
-    static constexpr int sum = max + R * kWarps * 4;
-    static constexpr int cq = sum + R * kWarps * 4;
-    static constexpr int bars = cq + R * 4;
-    static constexpr int bad = bars + 8 * 4;
-    static constexpr int flags = bad + 8 * 4;
+    static constexpr int kPages = chunk_pages(DH);
+    static constexpr int NQ = RN < 8 ? 1 : RN / 8;                  // N tiles of the first product
+    static constexpr int PV4 = RN == 4 ? 4 : (RN == 8 ? 8 : 2 * NQ);  // 32-bit registers of a page's P fragments
+    static constexpr int NCF = DH == 128 ? RN / 2 : 0;              // floats a thread hands to the other half
+    static constexpr int q = kStages * stage_bytes<DH>();
+    static constexpr int p = q + NQ * DH * 16;
+    static constexpr int spread = p + kPages * PV4 * 128;           // V scales as f16 pairs
+    static constexpr int half = spread + kPages * DH * 4;
+    static constexpr int max = half + kThreads * NCF * 4;
+    static constexpr int sum = max + NQ * 8 * kWarps * 4;
+    static constexpr int cq = sum + NQ * 8 * kWarps * 4;
+    static constexpr int lim = cq + NQ * 8 * 4;
+    static constexpr int nan = lim + NQ * 8 * 4;
+    static constexpr int bars = nan + 2 * (DH / 16) * 4;
+    static constexpr int bad = bars + kStages * 8;
+    static constexpr int flags = bad + 16;
     static constexpr int sums = flags + 16;
     static constexpr int pre = sums + kWarps * 8;  // [num_seqs + 1] int32
-    static_assert(stages<DH>() <= 4 && q % 16 == 0 && bars % 8 == 0 && sums % 8 == 0, "layout");
+    static_assert(q % 16 == 0 && spread % 16 == 0 && max % 16 == 0 && bars % 16 == 0 && bad % 16 == 0 && sums % 8 == 0, "layout");
     static_assert(pre + (kScanMaxSeqs + 1) * 4 <= (int)kMaxSmemPerBlock, "shared memory");
     static size_t bytes(int num_seqs) { return (size_t)pre + 4 * ((size_t)num_seqs + 1); }
 };
@@ -90,14 +108,17 @@ struct Params {
     int64_t q_tok_stride, num_q_tokens;
     const int32_t *block_tables, *seq_lens, *qsl;
     int32_t max_blocks, num_seqs, hq, hkv, group, max_query_len, max_seq_len;
-    int32_t rows;     // rows of a record
-    int64_t nch;      // records of a group
+    int32_t rows;       // rows of a record
+    int32_t slots;      // chunk records of a cut span at most
+    int32_t spans;      // spans of a group at most
     float score_scale;  // scale * log2(e) * k_scale
     float v_scale;
     __nv_bfloat16 *out;
     float *lse;
-    uint32_t *counters;
-    float *records;
+    uint32_t *span_counters;   // [group][spans]
+    uint32_t *group_counters;  // [group]
+    float *chunk_records;      // [CTA][slots]: of the span that starts in the CTA's range and does not end there
+    float *span_records;       // [group][spans]
     ErrState *err;
 };
 
@@ -133,6 +154,14 @@ __device__ __forceinline__ void bulk_copy(uint32_t dst, const void *src, uint32_
                  : "memory");
 }
 
+// floor(a / b), 0 <= a, 0 < b: one 32-bit division when both fit
+__device__ __forceinline__ int64_t div_floor(int64_t a, int64_t b)
+{
+    if (((uint64_t)a | (uint64_t)b) >> 32 == 0)
+        return (int64_t)((uint32_t)a / (uint32_t)b);
+    return a / b;
+}
+
 struct Meta {
     int qs, qn, L;
     bool sane, ok;  // as ReqMeta
@@ -152,6 +181,7 @@ __device__ __forceinline__ Meta meta_of(const Params &p, int b)
 }
 
 // A chunk of the dealt sequence: chunk lc of group (b, kvh), request-major.
+template <int DH>
 struct Chunk {
     int b, kvh, lc, nch;
     int qs, qn, L;
@@ -166,11 +196,11 @@ struct Chunk {
     }
     __device__ __forceinline__ void at(const Params &p, const int32_t *pre, int64_t x)
     {
-        b = owner_of(pre, p.num_seqs, (int)(x / p.hkv));
+        b = owner_of(pre, p.num_seqs, (int)div_floor(x, p.hkv));
         load(p, pre);
         const int r = (int)(x - (int64_t)p.hkv * pre[b]);
-        kvh = r / nch;
-        lc = r % nch;
+        kvh = (int)((uint32_t)r / (uint32_t)nch);
+        lc = r - kvh * nch;
     }
     // the chunk after this one (there is one)
     __device__ __forceinline__ void next(const Params &p, const int32_t *pre)
@@ -186,92 +216,98 @@ struct Chunk {
         while (pre[b + 1] == pre[b]);
         load(p, pre);
     }
-    __device__ __forceinline__ int tiles() const
-    {
-        return min(kTilesPerChunk, (L - lc * kChunk + kTile - 1) / kTile);
-    }
     // block id of the chunk's page `lane` (lanes 0..15; 0 where there is none)
     __device__ __forceinline__ int id(const Params &p, int lane) const
     {
-        const int pg = lc * kPagesPerChunk + lane;
-        return lane < kPagesPerChunk && pg < (L + 15) / 16 ? __ldg(p.block_tables + (int64_t)b * p.max_blocks + pg) : 0;
+        const int pg = lc * chunk_pages(DH) + lane;
+        return lane < chunk_pages(DH) && pg < (L + 15) / 16 ? __ldg(p.block_tables + (int64_t)b * p.max_blocks + pg) : 0;
     }
 };
 
-// Left-to-right fold of a group's records by the whole CTA, and its output.
-template <int DH>
-__device__ __forceinline__ void merge_group(const Params &p, const float *rec0, int nch, int rv, int64_t tok, int kvh)
-{
-    const int64_t hdr = part_header_floats(p.rows), stride = part_record_floats(p.rows, DH);
-    for (int e = threadIdx.x; e < rv * (DH / 4); e += kThreads) {
-        const int n = e / (DH / 4), d = e % (DH / 4) * 4;
-        const float *base = rec0 + n;
-        float m = -INFINITY, l = 0.f;
-        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-        for (int c0 = 0; c0 < nch; c0 += 4) {
-            float mc[4], lc[4];
-            float4 oc[4];
+// A thread's share of a softmax state (of a chunk, a span or a group): NR
+// query rows, for each of them NP pairs of neighbouring head-dim elements.
+template <int NR, int NP>
+struct State {
+    float m[NR], l[NR];
+    float2 o[NP][NR];
+
+    __device__ __forceinline__ void clear()
+    {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int c = min(c0 + i, nch - 1);
-                mc[i] = __ldcg(base + c * stride);
-                lc[i] = __ldcg(base + c * stride + p.rows);
-                oc[i] = __ldcg(reinterpret_cast<const float4 *>(rec0 + c * stride + hdr + (int64_t)n * DH + d));
-            }
+        for (int r = 0; r < NR; ++r) {
+            m[r] = -INFINITY;
+            l[r] = 0.f;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                if (c0 + i < nch) {
-                    const Fold f = fold_coef(m, l, mc[i], lc[i]);
-                    m = f.m;
-                    l = f.l;
-                    o.x = fold_elem(o.x, oc[i].x, f);
-                    o.y = fold_elem(o.y, oc[i].y, f);
-                    o.z = fold_elem(o.z, oc[i].z, f);
-                    o.w = fold_elem(o.w, oc[i].w, f);
-                }
+            for (int i = 0; i < NP; ++i)
+                o[i][r] = make_float2(0.f, 0.f);
+        }
+    }
+    // This state, then x.  An empty state (m = -inf, l = 0, o = 0) changes
+    // nothing: its factor is 0 and the other's exactly 1.
+    __device__ __forceinline__ void fold(const State &x)
+    {
+#pragma unroll
+        for (int r = 0; r < NR; ++r) {
+            const float mn = fmaxf(m[r], x.m[r]), ref = mn == -INFINITY ? 0.f : mn;
+            const float fa = ex2(m[r] - ref), fx = ex2(x.m[r] - ref);
+            m[r] = mn;
+            l[r] = __fmaf_rn(x.l[r], fx, l[r] * fa);
+#pragma unroll
+            for (int i = 0; i < NP; ++i) {
+                o[i][r].x = __fmaf_rn(x.o[i][r].x, fx, o[i][r].x * fa);
+                o[i][r].y = __fmaf_rn(x.o[i][r].y, fx, o[i][r].y * fa);
             }
         }
-        const int64_t row = (tok + n / p.group) * p.hq + kvh * p.group + n % p.group;
-        const float r = __frcp_rn(l) * p.v_scale;
-        *reinterpret_cast<uint2 *>(p.out + row * DH + d) =
-            make_uint2(pack_bf16x2(o.x * r, o.y * r), pack_bf16x2(o.z * r, o.w * r));
-        if (d == 0 && p.lse)
-            p.lse[row] = lse_of(m, l * 0x1p-15f);
     }
-}
+};
 
-template <int DH, int NT>
-__global__ void __launch_bounds__(kThreads, ctas_per_sm<DH, NT>()) quant_attn_kernel(const Params p)
+template <int DH, int RN>
+__global__ void __launch_bounds__(kThreads, ctas_per_sm<DH, RN>()) quant_attn_kernel(const Params p)
 {
-    using Lay = Layout<DH, NT>;
-    constexpr int R = 8 * NT;            // query rows
-    constexpr int NB = DH / 128;         // 128-element blocks of the head dim
-    constexpr int NST = stages<DH>();
+    using Lay = Layout<DH, RN>;
+    constexpr bool PAR = par_mode<RN>();
+    constexpr int NQ = Lay::NQ;
+    constexpr int PV4 = Lay::PV4;
+    constexpr int PPW = pages_per_warp(DH), kPages = chunk_pages(DH), kChunk = chunk_keys(DH);
+    constexpr int NB = DH / 128;            // 128-element blocks of the head dim
+    constexpr int NE = DH <= 256 ? 1 : 2;   // 32-element blocks of a warp
+    constexpr bool HALVES = DH == 128;      // warps 4-7 take the other half of the pages
+    constexpr int NR = RN == 4 ? 1 : RN / 4;  // rows of a thread's state
+    constexpr int NP = HALVES ? 1 : 2 * NE;   // element pairs of a thread's state
     constexpr int REC = quant_record_bytes(DH), CODES = quant_code_bytes(DH);
-    constexpr bool kQRegs = NT * DH <= 256;  // Q fragments in registers (else read from shared memory)
+    constexpr bool kQRegs = NQ * DH <= 256;  // Q fragments in registers (else read from shared memory)
+    constexpr int OT = PAR ? RN / 4 : 2 * NQ;  // accumulator tiles of a 32-element block
+    using St = State<NR, NP>;
     griddep_wait();
     griddep_launch_dependents();
     extern __shared__ __align__(128) uint8_t smem[];
-    uint8_t *const s_stage = smem;
-    uint2 *const s_q = reinterpret_cast<uint2 *>(smem + Lay::q);   // [NT][DH/16][32]
-    uint2 *const s_p = reinterpret_cast<uint2 *>(smem + Lay::p);   // [8 pages][NT][32]
-    float *const s_max = reinterpret_cast<float *>(smem + Lay::max);  // [R][8 warps]
-    float *const s_sum = reinterpret_cast<float *>(smem + Lay::sum);  // [R][8 warps]
-    float *const s_cq = reinterpret_cast<float *>(smem + Lay::cq);    // [R] raw score -> log2 units
+    uint2 *const s_q = reinterpret_cast<uint2 *>(smem + Lay::q);        // [NQ][DH/16][32]
+    uint32_t *const s_p = reinterpret_cast<uint32_t *>(smem + Lay::p);  // [16 pages][PV4/2 or /4][32 lanes][2 or 4]
+    uint4 *const s_spread = reinterpret_cast<uint4 *>(smem + Lay::spread);  // [16 pages][DH/16][4] x 4 tokens
+    float *const s_half = reinterpret_cast<float *>(smem + Lay::half);
+    float *const s_max = reinterpret_cast<float *>(smem + Lay::max);  // [rows][8 warps]
+    float *const s_sum = reinterpret_cast<float *>(smem + Lay::sum);  // [rows][8 warps]
+    float *const s_cq = reinterpret_cast<float *>(smem + Lay::cq);    // raw score -> log2 units
+    int *const s_lim = reinterpret_cast<int *>(smem + Lay::lim);      // last key of a row
+    int *const s_nan = reinterpret_cast<int *>(smem + Lay::nan);      // [chunk parity][DH/16] first NaN key of an element block
     uint64_t *const s_bars = reinterpret_cast<uint64_t *>(smem + Lay::bars);
-    uint8_t *const s_bad = smem + Lay::bad;                           // [stage][8 warps]
-    volatile int *const s_flags = reinterpret_cast<int *>(smem + Lay::flags);  // [0] abort [1] fold
+    volatile int *const s_bad = reinterpret_cast<int *>(smem + Lay::bad);  // [stage] 1 + the last chunk there with a bad block id
+    volatile int *const s_flags = reinterpret_cast<int *>(smem + Lay::flags);  // [0] abort [1] last to arrive
     int32_t *const s_pre = reinterpret_cast<int32_t *>(smem + Lay::pre);
     const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32, g = lane / 4, t = lane % 4;
     const int G = p.group, hkv = p.hkv;
 
     // the work: chunks of the valid requests
     if (tid == 0) {
-        for (int i = 0; i < NST; ++i)
-            mbar_init(smem_addr(s_bars + i), kWarps);
+        for (int i = 0; i < kStages; ++i)
+            mbar_init(smem_addr(s_bars + i), 2 * kPages);
         s_flags[0] = 0;
         fence_barrier_init();
     }
+    if (tid < 2 * (DH / 16))
+        s_nan[tid] = 0x7fffffff;
+    if (tid < kStages)
+        s_bad[tid] = 0;
     const long long tot = block_exclusive_sums<kThreads>(
         p.num_seqs, s_pre, reinterpret_cast<long long *>(smem + Lay::sums), [&](int b) {
             const Meta m = meta_of(p, b);
@@ -296,77 +332,501 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm<DH, NT>()) quant_attn_ke
     const int64_t ctas = T < (int64_t)gridDim.x ? T : (int64_t)gridDim.x;
     if ((int64_t)blockIdx.x >= ctas)
         return;
-    const int64_t lo = blockIdx.x * T / ctas, hi = (blockIdx.x + 1) * T / ctas;
-    auto cta_of = [&](int64_t x) { return (int)(((x + 1) * ctas + T - 1) / T - 1); };
+    auto range_start = [&](int64_t cta) { return div_floor(cta * T, ctas); };
+    auto cta_of = [&](int64_t x) { return div_floor((x + 1) * ctas + T - 1, T) - 1; };
+    const int64_t lo = range_start(blockIdx.x), hi = range_start((int64_t)blockIdx.x + 1);
 
-    // producer state: every warp copies its page of each tile
+    // Copies: every warp its pages of a chunk, K and V, one by each of its
+    // first lanes; the block ids are loaded one chunk ahead.  (One warp issuing
+    // all copies of a chunk held the others up by 4 us in 37; a ninth warp for
+    // them leaves 96 registers a thread.)
     const uint64_t policy = l2_policy_evict_first();
-    Chunk pc;
+    const int chunks = (int)(hi - lo);
+    const int cpage = PPW * warp + lane % PPW;
+    const bool is_v = (lane / PPW) % 2 != 0;
+    const uint8_t *const cpool = is_v ? p.v : p.k;
+    const uint32_t cdst = smem_addr(smem + ((is_v ? kPages : 0) + cpage) * REC);
+    Chunk<DH> pc;
     pc.at(p, s_pre, lo);
-    int64_t px = lo;      // the chunk being issued
-    int ptile = 0;        // its next tile
-    int issued = 0;       // tiles issued so far
-    int ids = pc.id(p, lane);
-    auto issue = [&]() {
-        if (px >= hi)
+    int copied = 0;  // chunks copied so far
+    int id = pc.id(p, cpage);
+    auto copy_next = [&]() {
+        if (copied >= chunks)
             return;
-        const int in_chunk = ptile * kWarps + warp;
-        const int id = __shfl_sync(0xffffffffu, ids, in_chunk);
-        const bool exists = pc.lc * kPagesPerChunk + in_chunk < (pc.L + 15) / 16;
-        const int st = issued % NST;
-        if (lane == 0) {
+        if (lane < 2 * PPW) {
+            const int st = copied % kStages;
             const uint32_t bar = smem_addr(s_bars + st);
-            const bool bad = exists && (id < 0 || (int64_t)id >= p.num_blocks);
-            s_bad[st * 8 + warp] = bad;
-            if (bad)
-                record_error(p.err, kErrBadMetadata, pc.b);
-            if (exists && !bad) {
-                const int64_t off = (int64_t)id * p.block_stride + pc.kvh * p.head_stride;
-                const uint32_t dst = smem_addr(s_stage + st * stage_bytes<DH>() + warp * REC);
-                mbar_arrive_expect_tx(bar, 2 * REC);
-                bulk_copy(dst, p.k + off, REC, bar, policy);
-                bulk_copy(dst + kWarps * REC, p.v + off, REC, bar, policy);
+            const bool exists = pc.lc * kPages + cpage < (pc.L + 15) / 16;
+            if (exists && (uint64_t)(int64_t)id < (uint64_t)p.num_blocks) {
+                mbar_arrive_expect_tx(bar, REC);
+                bulk_copy(cdst + st * stage_bytes<DH>(), cpool + (int64_t)id * p.block_stride + pc.kvh * p.head_stride,
+                          REC, bar, policy);
             } else {
+                if (exists) {
+                    s_bad[st] = copied + 1;
+                    record_error(p.err, kErrBadMetadata, pc.b);
+                }
                 mbar_arrive(bar);
             }
         }
-        ++issued;
-        if (++ptile >= pc.tiles()) {
-            ptile = 0;
-            if (++px < hi) {
-                pc.next(p, s_pre);
-                ids = pc.id(p, lane);
-            }
+        if (++copied < chunks) {
+            pc.next(p, s_pre);
+            id = pc.id(p, cpage);
         }
     };
-    for (int i = 0; i < NST; ++i)
-        issue();
+    for (int i = 0; i < kStages; ++i)
+        copy_next();
 
-    Chunk c;
+    // this thread's place in the second product: element pairs c0 = 16*wd + g
+    // and c0 + 8 of each 32-element block
+    const int wd = HALVES ? warp % 4 : warp;
+    const int token0 = 4 * (g >> 1) + (g & 1);  // token of fragment row g; row g + 8 is token0 + 2
+    // rows of a thread's scores (columns of S^T) and of its state
+    auto score_row = [&](int n, int i) { return RN == 4 ? (2 * t + i) & 3 : 8 * n + 2 * t + i; };
+    auto state_row = [&](int r) { return RN == 4 ? 2 * (t & 1) + (t >> 1) : 8 * (r / 2) + 2 * t + r % 2; };
+    // state pair i: its index among the DH/2 pairs
+    auto state_pair = [&](int i) { return HALVES ? 16 * wd + 8 * (warp / 4) + g : 16 * (NE * wd + i / 2) + 8 * (i % 2) + g; };
+
+    uint2 qf[kQRegs ? NQ * (DH / 16) : 1];
+    Chunk<DH> c;
     c.at(p, s_pre, lo);
-    int tile_no = 0;
-    uint2 qf[kQRegs ? NT * (DH / 16) : 1];
-    float cq[2 * NT];
-    int lim[2 * NT];  // last key of the row
-    // rows 8nt + 2t, +1 of this thread: folded state of a whole group
-    float acc_m[2 * NT], acc_l[2 * NT], acc_o[NB][NT][4];
-    bool whole = false;
-    int64_t seg_first = 0;
-    for (int64_t x = lo; x < hi; ++x) {
-        if (x > lo)
+    St span, group;
+    const int64_t rec_hdr = part_header_floats(p.rows), rec_size = part_record_floats(p.rows, DH);
+
+    // ------------------------------------------------ one chunk's state --
+    auto chunk_state = [&](auto masked_tag, const uint8_t *stage, int parity, St &st) -> bool {
+        constexpr bool MASKED = decltype(masked_tag)::value;  // some row does not see some key of the chunk
+        const int key0 = c.lc * kChunk;
+        const int npages = MASKED ? min(kPages, (c.L - key0 + 15) / 16) : kPages;
+        // two accumulators per tile, for the even and the odd steps: one
+        // chain of dependent products is latency bound
+        float s[PPW][NQ][4];
+#pragma unroll
+        for (int j = 0; j < PPW; ++j) {
+            float acc[2][NQ][4];
+#pragma unroll
+            for (int n = 0; n < NQ; ++n)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    s[j][n][i] = 0.f;
+#pragma unroll
+                    for (int k = 0; k < 2; ++k)
+                        acc[k][n][i] = 0.f;
+                }
+            const int page = PPW * warp + j;
+            if (MASKED && page >= npages)
+                continue;
+            // S^T = K . Q^T: thread t takes elements 32t..32t+31 of each 128
+            const uint8_t *kr = stage + page * REC + token0 * (DH / 2) + 16 * t;
+            const uint8_t *ks = stage + page * REC + CODES + token0 * (DH / 16) + 2 * t;
+#pragma unroll
+            for (int b = 0; b < NB; ++b) {
+                const uint4 ka = *reinterpret_cast<const uint4 *>(kr + 64 * b);
+                const uint4 kb = *reinterpret_cast<const uint4 *>(kr + DH + 64 * b);
+                const uint32_t sa = e4m3x2_to_f16x2(*reinterpret_cast<const uint16_t *>(ks + 8 * b));
+                const uint32_t sb = e4m3x2_to_f16x2(*reinterpret_cast<const uint16_t *>(ks + DH / 8 + 8 * b));
+                const uint32_t wa[4] = {ka.x, ka.y, ka.z, ka.w}, wb[4] = {kb.x, kb.y, kb.z, kb.w};
+                const uint32_t fa[2] = {__byte_perm(sa, 0u, 0x1010), __byte_perm(sa, 0u, 0x3232)};
+                const uint32_t fb[2] = {__byte_perm(sb, 0u, 0x1010), __byte_perm(sb, 0u, 0x3232)};
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    uint32_t x[4], y[4];
+                    e2m1x8_to_f16x2(wa[i], x);
+                    e2m1x8_to_f16x2(wb[i], y);
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        x[k] = mul_f16x2(x[k], fa[i / 2]);
+                        y[k] = mul_f16x2(y[k], fb[i / 2]);
+                    }
+#pragma unroll
+                    for (int n = 0; n < NQ; ++n)
+#pragma unroll
+                        for (int k = 0; k < 2; ++k) {
+                            const int step = n * (DH / 16) + 8 * b + 2 * i + k;
+                            const uint2 q = kQRegs ? qf[kQRegs ? step : 0] : s_q[step * 32 + lane];
+                            mma_f16(acc[k][n], x[2 * k], y[2 * k], x[2 * k + 1], y[2 * k + 1], q.x, q.y);
+                        }
+                }
+            }
+#pragma unroll
+            for (int n = 0; n < NQ; ++n)
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    s[j][n][i] = acc[0][n][i] + acc[1][n][i];
+            if (MASKED) {
+                const int key = key0 + 16 * page + token0;
+#pragma unroll
+                for (int n = 0; n < NQ; ++n)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        if (key + (i < 2 ? 0 : 2) > s_lim[score_row(n, i % 2)])
+                            s[j][n][i] = -INFINITY;
+            }
+            // the page's V scales: lane = (element block lane/4 + 8b, tokens 4*(lane%4)..+3)
+#pragma unroll
+            for (int b = 0; b < NB; ++b) {
+                const uint32_t w = reinterpret_cast<const uint32_t *>(stage + (kPages + page) * REC + CODES)[32 * b + lane];
+                const uint32_t s01 = e4m3x2_to_f16x2(w), s23 = e4m3x2_to_f16x2(w >> 16);
+                uint32_t f[4] = {__byte_perm(s01, 0u, 0x1010), __byte_perm(s01, 0u, 0x3232), __byte_perm(s23, 0u, 0x1010),
+                                 __byte_perm(s23, 0u, 0x3232)};
+                if (MASKED) {
+                    // tokens no row sees count as zero whatever their bytes; a
+                    // NaN that only some rows see is given to those rows below
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const int key = key0 + 16 * page + 4 * t + i;
+                        const bool gone = key >= c.L, nan = ((w >> (8 * i)) & 0x7fu) == 0x7fu;
+                        if (gone || (nan && key > c.L - c.qn)) {
+                            f[i] = 0u;
+                            if (!gone)
+                                atomicMin(s_nan + parity * (DH / 16) + 8 * b + g, key);
+                        }
+                    }
+                }
+                s_spread[(page * (DH / 16) + 8 * b + g) * 4 + t] = make_uint4(f[0], f[1], f[2], f[3]);
+            }
+        }
+        if (MASKED) {
+            // pages that do not exist: no key
+#pragma unroll
+            for (int j = 0; j < PPW; ++j)
+                if (PPW * warp + j >= npages)
+#pragma unroll
+                    for (int n = 0; n < NQ; ++n)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            s[j][n][i] = -INFINITY;
+        }
+        // largest raw score of each row, over the warp's keys
+#pragma unroll
+        for (int n = 0; n < NQ; ++n)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                float x = fmaxf(s[0][n][i], s[0][n][2 + i]);
+                if constexpr (PPW == 2)
+                    x = max3f(x, s[PPW - 1][n][i], s[PPW - 1][n][2 + i]);
+#pragma unroll
+                for (int w = 4; w < 32; w <<= 1)
+                    x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, w));
+                if (g == 0 && (RN > 4 || t < 2))
+                    s_max[score_row(n, i) * kWarps + warp] = x;
+            }
+        __syncthreads();  // A: maxima and scales written; the previous chunk is consumed
+        const bool aborted = s_flags[0] != 0;  // before B, so that every thread reads the same
+        if (tid < DH / 16)
+            s_nan[(parity ^ 1) * (DH / 16) + tid] = 0x7fffffff;  // for the next chunk
+        float l[NQ][2], mrow[NQ][2];
+#pragma unroll
+        for (int n = 0; n < NQ; ++n) {
+            float pr[PPW][4];
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const int r = score_row(n, i);
+                const float4 u = *reinterpret_cast<const float4 *>(s_max + r * kWarps);
+                const float4 v = *reinterpret_cast<const float4 *>(s_max + r * kWarps + 4);
+                const float cq = s_cq[r];
+                const float m = fmaxf(max3f(u.x, u.y, max3f(u.z, u.w, v.x)), max3f(v.y, v.z, v.w)) * cq;
+                mrow[n][i] = m;
+                const float add = kShift - (m == -INFINITY ? 0.f : m);
+#pragma unroll
+                for (int j = 0; j < PPW; ++j) {
+                    pr[j][i] = ex2(__fmaf_rn(s[j][n][i], cq, add));  // 0 for keys left out
+                    pr[j][2 + i] = ex2(__fmaf_rn(s[j][n][2 + i], cq, add));
+                }
+                l[n][i] = pr[0][i] + pr[0][2 + i];
+                if constexpr (PPW == 2)
+                    l[n][i] += pr[PPW - 1][i] + pr[PPW - 1][2 + i];
+            }
+            // P^T fragments: after the transpose thread (g, t) holds column
+            // g's keys in pairs, tokens 4t, 4t+1 (x) and 4t+2, 4t+3 (y)
+#pragma unroll
+            for (int j = 0; j < PPW; ++j) {
+                const int page = PPW * warp + j;
+                const uint32_t x = movmatrix(pack_f16x2(pr[j][0], pr[j][1])), y = movmatrix(pack_f16x2(pr[j][2], pr[j][3]));
+                if constexpr (RN == 4) {
+                    // columns 0-3 give the even elements, 4-7 (the same rows) the odd ones
+                    const uint32_t a = g < 4 ? 0x4410u : 0x1044u, b = g < 4 ? 0x4432u : 0x3244u;
+                    reinterpret_cast<uint4 *>(s_p)[page * 32 + lane] =
+                        make_uint4(__byte_perm(x, 0u, a), __byte_perm(x, 0u, b), __byte_perm(y, 0u, a), __byte_perm(y, 0u, b));
+                } else if constexpr (RN == 8) {
+                    reinterpret_cast<uint4 *>(s_p)[(2 * page) * 32 + lane] =
+                        make_uint4(x & 0xffffu, x >> 16, y & 0xffffu, y >> 16);
+                    reinterpret_cast<uint4 *>(s_p)[(2 * page + 1) * 32 + lane] =
+                        make_uint4(x << 16, x & 0xffff0000u, y << 16, y & 0xffff0000u);
+                } else {
+                    reinterpret_cast<uint2 *>(s_p)[(page * NQ + n) * 32 + lane] = make_uint2(x, y);
+                }
+            }
+        }
+        __syncthreads();  // B: P written
+        float o[NE][OT][4], acc[2][NE][OT][4];  // for the even and the odd pages, as above
+#pragma unroll
+        for (int e = 0; e < NE; ++e)
+#pragma unroll
+            for (int n = 0; n < OT; ++n)
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+#pragma unroll
+                    for (int k = 0; k < 2; ++k)
+                        acc[k][e][n][i] = 0.f;
+        const int first = HALVES ? warp / 4 * (kPages / 2) : 0;
+        const int last = HALVES ? min(npages, first + kPages / 2) : npages;
+        auto page_product = [&](int page, auto parity_tag) {
+            constexpr int h = decltype(parity_tag)::value;
+            const uint8_t *vr = stage + (kPages + page) * REC + (16 * NE * wd + g) * 16 + 4 * t;
+            uint32_t pf[PV4];
+            if constexpr (PAR) {
+#pragma unroll
+                for (int i = 0; i < PV4 / 4; ++i) {
+                    const uint4 v = reinterpret_cast<const uint4 *>(s_p)[(page * (PV4 / 4) + i) * 32 + lane];
+                    pf[4 * i] = v.x;
+                    pf[4 * i + 1] = v.y;
+                    pf[4 * i + 2] = v.z;
+                    pf[4 * i + 3] = v.w;
+                }
+            } else {
+#pragma unroll
+                for (int n = 0; n < NQ; ++n) {
+                    const uint2 v = reinterpret_cast<const uint2 *>(s_p)[(page * NQ + n) * 32 + lane];
+                    pf[2 * n] = v.x;
+                    pf[2 * n + 1] = v.y;
+                }
+            }
+#pragma unroll
+            for (int e = 0; e < NE; ++e) {
+                // pairs c0 (block 2*(NE*wd + e)) and c0 + 8 (the next block), tokens 4t..4t+3
+                const uint32_t w0 = *reinterpret_cast<const uint32_t *>(vr + e * 256);
+                const uint32_t w1 = *reinterpret_cast<const uint32_t *>(vr + e * 256 + 128);
+                const uint4 f0 = s_spread[(page * (DH / 16) + 2 * (NE * wd + e)) * 4 + t];
+                const uint4 f1 = s_spread[(page * (DH / 16) + 2 * (NE * wd + e) + 1) * 4 + t];
+                uint32_t x[4], y[4];
+                e2m1x8_to_f16x2(w0, x);
+                e2m1x8_to_f16x2(w1, y);
+                x[0] = mul_f16x2(x[0], f0.x);
+                x[1] = mul_f16x2(x[1], f0.y);
+                x[2] = mul_f16x2(x[2], f0.z);
+                x[3] = mul_f16x2(x[3], f0.w);
+                y[0] = mul_f16x2(y[0], f1.x);
+                y[1] = mul_f16x2(y[1], f1.y);
+                y[2] = mul_f16x2(y[2], f1.z);
+                y[3] = mul_f16x2(y[3], f1.w);
+                if constexpr (PAR) {
+                    // rows c0, c0 + 8; K: tokens 4t, 4t+1, then 4t+2, 4t+3, each (even, odd)
+#pragma unroll
+                    for (int n = 0; n < OT; ++n) {
+                        mma_f16(acc[h][e][n], x[0], y[0], x[1], y[1], pf[4 * n], pf[4 * n + 1]);
+                        mma_f16(acc[h][e][n], x[2], y[2], x[3], y[3], pf[4 * n + 2], pf[4 * n + 3]);
+                    }
+                } else {
+                    // tile 2n: rows are the even, then the odd elements of the pairs c0, tile 2n+1: of c0 + 8
+                    const uint32_t x0 = __byte_perm(x[0], x[1], 0x5410), x1 = __byte_perm(x[0], x[1], 0x7632);
+                    const uint32_t x2 = __byte_perm(x[2], x[3], 0x5410), x3 = __byte_perm(x[2], x[3], 0x7632);
+                    const uint32_t y0 = __byte_perm(y[0], y[1], 0x5410), y1 = __byte_perm(y[0], y[1], 0x7632);
+                    const uint32_t y2 = __byte_perm(y[2], y[3], 0x5410), y3 = __byte_perm(y[2], y[3], 0x7632);
+#pragma unroll
+                    for (int n = 0; n < NQ; ++n) {
+                        mma_f16(acc[h][e][2 * n], x0, x1, x2, x3, pf[2 * n], pf[2 * n + 1]);
+                        mma_f16(acc[h][e][2 * n + 1], y0, y1, y2, y3, pf[2 * n], pf[2 * n + 1]);
+                    }
+                }
+            }
+        };
+        if constexpr (MASKED) {
+#pragma unroll 1
+            for (int page = first; page < last; page += 2) {
+                page_product(page, std::integral_constant<int, 0>{});
+                if (page + 1 < last)
+                    page_product(page + 1, std::integral_constant<int, 1>{});
+            }
+        } else {
+#pragma unroll(RN <= 8 ? 2 : 1)
+            for (int i = 0; i < (HALVES ? kPages / 2 : kPages); i += 2) {
+                page_product(first + i, std::integral_constant<int, 0>{});
+                page_product(first + i + 1, std::integral_constant<int, 1>{});
+            }
+        }
+#pragma unroll
+        for (int e = 0; e < NE; ++e)
+#pragma unroll
+            for (int n = 0; n < OT; ++n)
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    o[e][n][i] = acc[0][e][n][i] + acc[1][e][n][i];
+        // accumulators by element pair: pr[i][k], i = 0 (c0) or 1 (c0 + 8) of
+        // each 32-element block, then for k the rows (and, at four rows, one
+        // parity: even for t < 2, odd for t >= 2)
+        constexpr int F = RN / 2;  // floats of a pair
+        float pr[2 * NE][F];
+#pragma unroll
+        for (int e = 0; e < NE; ++e)
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+#pragma unroll
+                for (int k = 0; k < F; ++k) {
+                    if constexpr (RN == 4)
+                        pr[2 * e + i][k] = o[e][0][2 * i + k];
+                    else if constexpr (RN == 8)  // k: parity, row
+                        pr[2 * e + i][k] = o[e][k / 2][2 * i + k % 2];
+                    else  // k: N tile, parity, row
+                        pr[2 * e + i][k] = o[e][2 * (k / 4) + i][k % 4];
+                }
+        // row sums over the warp's keys
+#pragma unroll
+        for (int n = 0; n < NQ; ++n)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+#pragma unroll
+                for (int w = 4; w < 32; w <<= 1)
+                    l[n][i] += __shfl_xor_sync(0xffffffffu, l[n][i], w);
+                if (g == 0 && (RN > 4 || t < 2))
+                    s_sum[score_row(n, i) * kWarps + warp] = l[n][i];
+            }
+        if constexpr (HALVES) {
+            // warps 0-3 keep the pairs c0, 4-7 the pairs c0 + 8; the others' go
+            // through shared memory
+            const int keep = warp / 4;
+#pragma unroll
+            for (int k = 0; k < F; ++k)
+                s_half[k * kThreads + (tid ^ 128)] = keep ? pr[0][k] : pr[1][k];
+        }
+        __syncthreads();  // C: sums and halves written
+        if constexpr (HALVES) {
+            const int keep = warp / 4;
+#pragma unroll
+            for (int k = 0; k < F; ++k) {
+                const float own = keep ? pr[1][k] : pr[0][k], other = s_half[k * kThreads + tid];
+                pr[0][k] = keep ? other + own : own + other;  // the first half of the pages first
+            }
+        }
+        // the thread's state: rows' maxima and sums, pairs of elements
+#pragma unroll
+        for (int r = 0; r < NR; ++r) {
+            st.m[r] = RN == 4 ? (t < 2 ? mrow[0][0] : mrow[0][1]) : mrow[RN == 4 ? 0 : r / 2][r % 2];
+            const float *ss = s_sum + state_row(r) * kWarps;
+            const float4 u = *reinterpret_cast<const float4 *>(ss), v = *reinterpret_cast<const float4 *>(ss + 4);
+            st.l[r] = ((u.x + u.y) + (u.z + u.w)) + ((v.x + v.y) + (v.z + v.w));
+#pragma unroll
+            for (int i = 0; i < NP; ++i) {
+                if constexpr (RN == 4) {
+                    // the other parity of the kept row from lane t ^ 2
+                    const float got = __shfl_xor_sync(0xffffffffu, t < 2 ? pr[i][1] : pr[i][0], 2);
+                    st.o[i][0] = t < 2 ? make_float2(pr[i][0], got) : make_float2(got, pr[i][1]);
+                } else if constexpr (RN == 8) {
+                    st.o[i][r] = make_float2(pr[i][r], pr[i][2 + r]);
+                } else {
+                    st.o[i][r] = make_float2(pr[i][4 * (r / 2) + r % 2], pr[i][4 * (r / 2) + 2 + r % 2]);
+                }
+            }
+        }
+        if constexpr (MASKED) {
+#pragma unroll
+            for (int i = 0; i < NP; ++i) {
+                const int k = s_nan[parity * (DH / 16) + state_pair(i) / 8];
+                if (k != 0x7fffffff)
+#pragma unroll
+                    for (int r = 0; r < NR; ++r)
+                        if (s_lim[state_row(r)] >= k)
+                            st.o[i][r] = make_float2(__int_as_float(0x7FC00000), __int_as_float(0x7FC00000));
+            }
+        }
+        return aborted;
+    };
+
+    // records: m, l and the element pairs of this thread's rows
+    const int pair_zero = state_pair(0) == 0;  // this thread also speaks for the row's m and l
+    auto write_record = [&](float *rec, const St &st, int rv) {
+#pragma unroll
+        for (int r = 0; r < NR; ++r) {
+            const int row = state_row(r);
+            if (row >= rv)
+                continue;
+            if (pair_zero) {
+                __stcg(rec + row, st.m[r]);
+                __stcg(rec + p.rows + row, st.l[r]);
+            }
+#pragma unroll
+            for (int i = 0; i < NP; ++i)
+                __stcg(reinterpret_cast<float2 *>(rec + rec_hdr + (int64_t)row * DH) + state_pair(i), st.o[i][r]);
+        }
+    };
+    // st = the fold of n records, one after another from `recs`
+    auto fold_records = [&](St &st, const float *recs, int n, int rv) {
+        st.clear();
+        constexpr int W = NR * (2 + 2 * NP);                              // registers of a state
+        constexpr int U = W <= 4 ? 8 : W <= 12 ? 4 : W <= 24 ? 2 : 1;  // records in flight
+        for (int k0 = 0; k0 < n; k0 += U) {
+            St x[U];
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const float *rec = recs + min(k0 + u, n - 1) * rec_size;
+#pragma unroll
+                for (int r = 0; r < NR; ++r) {
+                    const int row = min(state_row(r), rv - 1);
+                    x[u].m[r] = __ldcg(rec + row);
+                    x[u].l[r] = __ldcg(rec + p.rows + row);
+#pragma unroll
+                    for (int i = 0; i < NP; ++i)
+                        x[u].o[i][r] = __ldcg(reinterpret_cast<const float2 *>(rec + rec_hdr + (int64_t)row * DH) + state_pair(i));
+                }
+            }
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+                if (k0 + u < n)
+                    st.fold(x[u]);
+        }
+    };
+    // Arrival of this CTA, its records written; true in the last of `n` CTAs.
+    auto last_to_arrive = [&](uint32_t *counter, int n) {
+        __syncthreads();
+        if (tid == 0) {
+            // releases this CTA's records and, for the last arrival, acquires the others'
+            uint32_t old;
+            asm volatile("atom.acq_rel.gpu.global.add.u32 %0, [%1], 1;" : "=r"(old) : "l"(counter) : "memory");
+            const bool last = old == (uint32_t)(n - 1);
+            if (last)
+                *counter = 0u;  // ready for the next call
+            s_flags[1] = last;
+        }
+        __syncthreads();
+        return s_flags[1] != 0;
+    };
+    auto write_output = [&](const St &st, int rv) {
+#pragma unroll
+        for (int r = 0; r < NR; ++r) {
+            const int row = state_row(r);
+            if (row >= rv)
+                continue;
+            const int64_t at = (int64_t)(c.qs + row / G) * p.hq + c.kvh * G + row % G;
+            const float f = __frcp_rn(st.l[r]) * p.v_scale;
+#pragma unroll
+            for (int i = 0; i < NP; ++i)
+                reinterpret_cast<uint32_t *>(p.out + at * DH)[state_pair(i)] =
+                    pack_bf16x2(st.o[i][r].x * f, st.o[i][r].y * f);
+            if (pair_zero && p.lse)
+                p.lse[at] = lse_of(st.m[r], st.l[r] * 0x1p-15f);
+        }
+    };
+
+    bool span_whole = false, group_whole = false;
+    float *span_area = nullptr;      // the cut span's chunk records
+    int span_ctas = 0;               // and the CTAs that write them
+    for (int step = 0; step < chunks; ++step) {
+        const bool first_chunk = step == 0, last_chunk = step + 1 == chunks;
+        if (!first_chunk)
             c.next(p, s_pre);
-        const int64_t gs = x - c.lc;  // the group's first chunk
-        if (x == lo || c.lc == 0) {
+        if (first_chunk || c.lc == 0) {
             // a new group: its rows, scaled to [1, 2) by a power of two, in
             // fragment order (the previous group's readers are past a barrier)
-            seg_first = x;
-            whole = gs >= lo && gs + c.nch <= hi;
+            const int64_t gs = lo + step - c.lc;  // the group's first chunk
+            group_whole = gs >= lo && gs + c.nch <= hi;
+            group.clear();
 #pragma unroll
-            for (int k = 0; k < NT; ++k) {
-                const int r = 8 * k + warp;
+            for (int k = 0; k < NQ; ++k) {
+                const int slot = 8 * k + warp, r = RN == 4 ? slot & 3 : slot;
                 const bool valid = r < c.qn * G;
-                const uint2 *src = reinterpret_cast<const uint2 *>(p.q + (int64_t)(c.qs + (valid ? r / G : 0)) * p.q_tok_stride +
-                                                                   (int64_t)(c.kvh * G + (valid ? r % G : 0)) * DH);
+                const int tok = valid ? r / G : 0;
+                const uint2 *src = reinterpret_cast<const uint2 *>(p.q + (int64_t)(c.qs + tok) * p.q_tok_stride +
+                                                                   (int64_t)(c.kvh * G + (valid ? r - tok * G : 0)) * DH);
                 uint2 w[NB];
                 uint32_t top = 0;
 #pragma unroll
@@ -387,352 +847,145 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm<DH, NT>()) quant_attn_ke
                     s_q[(k * (DH / 16) + 8 * i + lane % 8) * 32 + warp * 4 + lane / 8] =
                         make_uint2(pack_f16x2(a0, a1), pack_f16x2(a2, a3));
                 }
-                if (lane == 0)
-                    s_cq[r] = p.score_scale * __int_as_float((127 + e) << 23);
+                if (lane == 0) {
+                    s_cq[slot] = fmaxf(1e-37f, fminf(p.score_scale * __int_as_float((127 + e) << 23), 3e38f));
+                    s_lim[slot] = c.L - c.qn + (valid ? tok : c.qn - 1);
+                }
             }
             __syncthreads();
             if constexpr (kQRegs) {
 #pragma unroll
-                for (int i = 0; i < NT * (DH / 16); ++i)
+                for (int i = 0; i < NQ * (DH / 16); ++i)
                     qf[i] = s_q[i * 32 + lane];
             }
-#pragma unroll
-            for (int i = 0; i < 2 * NT; ++i) {
-                const int r = 8 * (i / 2) + 2 * t + i % 2;
-                cq[i] = s_cq[r];
-                lim[i] = c.L - c.qn + min(r / G, c.qn - 1);
-                acc_m[i] = -INFINITY;
-                acc_l[i] = 0.f;
-            }
-#pragma unroll
-            for (int b = 0; b < NB; ++b)
-#pragma unroll
-                for (int n = 0; n < NT; ++n)
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        acc_o[b][n][i] = 0.f;
         }
-
-        // ------------------------------------------------------ one chunk --
-        float m[2 * NT], l[2 * NT], o[NB][NT][4];
-        bool bad = false;
-#pragma unroll
-        for (int i = 0; i < 2 * NT; ++i) {
-            m[i] = -INFINITY;
-            l[i] = 0.f;
-        }
-#pragma unroll
-        for (int b = 0; b < NB; ++b)
-#pragma unroll
-            for (int n = 0; n < NT; ++n)
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    o[b][n][i] = 0.f;
-        const int tiles = c.tiles();
-        for (int tile = 0; tile < tiles; ++tile, ++tile_no) {
-            const int st = tile_no % NST;
-            const int key0 = c.lc * kChunk + tile * kTile;
-            const int npages = min(kWarps, (c.L - key0 + 15) / 16);
-            const bool masked = key0 + kTile > c.L - c.qn + 1;  // some row does not see some key
-            wait_bar(smem_addr(s_bars + st), (tile_no / NST) & 1, s_flags, p.err, st);
-            const uint8_t *stage = s_stage + st * stage_bytes<DH>();
-
-            // S = K . Q^T of page `warp`: rows are keys, columns query rows
-            float s[NT][4];
-#pragma unroll
-            for (int n = 0; n < NT; ++n)
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    s[n][i] = 0.f;
-            const int r0 = 4 * (g >> 1) + (g & 1);  // token of fragment row g; row g + 8 is token r0 + 2
-            if (warp < npages) {
-                const uint8_t *kr = stage + warp * REC + r0 * (DH / 2) + 16 * t;
-                const uint8_t *ks = stage + warp * REC + CODES + r0 * (DH / 16) + 2 * t;
-#pragma unroll
-                for (int b = 0; b < NB; ++b) {
-                    const uint4 ka = *reinterpret_cast<const uint4 *>(kr + 64 * b);
-                    const uint4 kb = *reinterpret_cast<const uint4 *>(kr + DH + 64 * b);
-                    const uint32_t sa = e4m3x2_to_f16x2(*reinterpret_cast<const uint16_t *>(ks + 8 * b));
-                    const uint32_t sb = e4m3x2_to_f16x2(*reinterpret_cast<const uint16_t *>(ks + DH / 8 + 8 * b));
-                    const uint32_t wa[4] = {ka.x, ka.y, ka.z, ka.w}, wb[4] = {kb.x, kb.y, kb.z, kb.w};
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        // words 0, 1 are the thread's first 16 elements, 2, 3 the next
-                        const uint32_t fa = __byte_perm(sa, 0u, i < 2 ? 0x1010 : 0x3232);
-                        const uint32_t fb = __byte_perm(sb, 0u, i < 2 ? 0x1010 : 0x3232);
-                        uint32_t a[4], bb[4];
-                        e2m1x8_to_f16x2(wa[i], a);
-                        e2m1x8_to_f16x2(wb[i], bb);
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) {
-                            a[j] = mul_f16x2(a[j], fa);
-                            bb[j] = mul_f16x2(bb[j], fb);
-                        }
-#pragma unroll
-                        for (int n = 0; n < NT; ++n)
-#pragma unroll
-                            for (int j = 0; j < 2; ++j) {
-                                const int step = n * (DH / 16) + 8 * b + 2 * i + j;
-                                const uint2 q = kQRegs ? qf[kQRegs ? step : 0] : s_q[step * 32 + lane];
-                                mma_f16(s[n], a[2 * j], bb[2 * j], a[2 * j + 1], bb[2 * j + 1], q.x, q.y);
-                            }
-                    }
-                }
-            }
-            // raw scores to log2 units; keys a row does not see are left out
-            const int key = key0 + 16 * warp + r0;
-#pragma unroll
-            for (int n = 0; n < NT; ++n) {
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    s[n][i] = s[n][i] * cq[2 * n + i % 2];
-                if (masked) {
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        if (key + (i < 2 ? 0 : 2) > lim[2 * n + i % 2])
-                            s[n][i] = -INFINITY;
-                }
-                float x0 = fmaxf(s[n][0], s[n][2]), x1 = fmaxf(s[n][1], s[n][3]);
-#pragma unroll
-                for (int w = 4; w < 32; w <<= 1) {
-                    x0 = fmaxf(x0, __shfl_xor_sync(0xffffffffu, x0, w));
-                    x1 = fmaxf(x1, __shfl_xor_sync(0xffffffffu, x1, w));
-                }
-                if (g == 0) {
-                    s_max[(8 * n + 2 * t) * kWarps + warp] = x0;
-                    s_max[(8 * n + 2 * t + 1) * kWarps + warp] = x1;
-                }
-            }
-            __syncthreads();  // A: maxima written; the previous tile is consumed
-            if (s_flags[0]) {
-                // a wait ran out of time: let the copies in flight land, give up
-                for (int k = tile_no; k < issued; ++k)
-                    wait_bar_drain(smem_addr(s_bars + k % NST), (k / NST) & 1);
-                return;
-            }
-            if (tile_no > 0)
-                issue();
-            bad |= *reinterpret_cast<const uint64_t *>(s_bad + 8 * st) != 0;
-#pragma unroll
-            for (int n = 0; n < NT; ++n) {
-                float p4[4];
-#pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    const float4 u = *reinterpret_cast<const float4 *>(s_max + (8 * n + 2 * t + i) * kWarps);
-                    const float4 v = *reinterpret_cast<const float4 *>(s_max + (8 * n + 2 * t + i) * kWarps + 4);
-                    const float mx = fmaxf(fmaxf(fmaxf(u.x, u.y), fmaxf(u.z, u.w)), fmaxf(fmaxf(v.x, v.y), fmaxf(v.z, v.w)));
-                    const float mo = m[2 * n + i], mn = fmaxf(mo, mx);
-                    const float f = mo == mn ? 1.f : ex2(mo - mn);
-                    m[2 * n + i] = mn;
-                    l[2 * n + i] *= f;
-#pragma unroll
-                    for (int b = 0; b < NB; ++b) {
-                        o[b][n][i] *= f;
-                        o[b][n][2 + i] *= f;
-                    }
-                    const float ref = (mn == -INFINITY ? 0.f : mn) - kShift;
-                    p4[i] = ex2(s[n][i] - ref);  // 0 for keys left out
-                    p4[2 + i] = ex2(s[n][2 + i] - ref);
-                    l[2 * n + i] += p4[i] + p4[2 + i];
-                }
-                // P^T fragment of the second product: keys in pairs
-                s_p[(warp * NT + n) * 32 + lane] =
-                    make_uint2(movmatrix(pack_f16x2(p4[0], p4[1])), movmatrix(pack_f16x2(p4[2], p4[3])));
-            }
-            __syncthreads();  // B: P written
-
-            // O^T += V^T . P^T: rows are head-dim elements 16*(warp + 8b)..+15
-            int nan_key[NB];
-#pragma unroll
-            for (int b = 0; b < NB; ++b)
-                nan_key[b] = 0x7fffffff;
-            const uint8_t *vr = stage + kWarps * REC + (warp * 8 + g) * 16 + 4 * t;
-            const uint8_t *vs = stage + kWarps * REC + CODES + warp * 16 + 4 * t;
-#pragma unroll 2
-            for (int j = 0; j < npages; ++j) {
-                uint2 pf[NT];
-#pragma unroll
-                for (int n = 0; n < NT; ++n)
-                    pf[n] = s_p[(j * NT + n) * 32 + lane];
-#pragma unroll
-                for (int b = 0; b < NB; ++b) {
-                    const uint32_t w = *reinterpret_cast<const uint32_t *>(vr + j * REC + b * 1024);
-                    const uint32_t sw = *reinterpret_cast<const uint32_t *>(vs + j * REC + b * 128);
-                    uint32_t s01 = e4m3x2_to_f16x2(sw), s23 = e4m3x2_to_f16x2(sw >> 16);
-                    if (masked) {
-                        // tokens no row sees count as zero whatever their
-                        // bytes; a NaN that only some rows see is added to
-                        // those rows below
-                        const int k0 = key0 + 16 * j + 4 * t;
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            const bool gone = k0 + i >= c.L;
-                            const bool nan = ((sw >> (8 * i)) & 0x7fu) == 0x7fu;
-                            if (gone || (nan && k0 + i > c.L - c.qn)) {
-                                uint32_t &sp = i < 2 ? s01 : s23;
-                                sp &= i % 2 ? 0x0000ffffu : 0xffff0000u;
-                                if (!gone)
-                                    nan_key[b] = min(nan_key[b], k0 + i);
-                            }
-                        }
-                    }
-                    uint32_t e[4];
-                    e2m1x8_to_f16x2(w, e);  // token 4t + i: elements 2g (low), 2g + 1
-                    const uint32_t a0 = mul_f16x2(__byte_perm(e[0], e[1], 0x5410), s01);
-                    const uint32_t a1 = mul_f16x2(__byte_perm(e[0], e[1], 0x7632), s01);
-                    const uint32_t a2 = mul_f16x2(__byte_perm(e[2], e[3], 0x5410), s23);
-                    const uint32_t a3 = mul_f16x2(__byte_perm(e[2], e[3], 0x7632), s23);
-#pragma unroll
-                    for (int n = 0; n < NT; ++n)
-                        mma_f16(o[b][n], a0, a1, a2, a3, pf[n].x, pf[n].y);
-                }
-            }
-            if (masked) {
-#pragma unroll
-                for (int b = 0; b < NB; ++b) {
-                    const int k = __reduce_min_sync(0xffffffffu, nan_key[b]);
-                    if (k != 0x7fffffff) {
-#pragma unroll
-                        for (int n = 0; n < NT; ++n)
-#pragma unroll
-                            for (int i = 0; i < 4; ++i)
-                                if (lim[2 * n + i % 2] >= k)
-                                    o[b][n][i] = __int_as_float(0x7FC00000);
-                    }
-                }
+        if (first_chunk || c.lc % kSpan == 0) {
+            const int64_t sa = lo + step - c.lc % kSpan;  // the span's chunks: [sa, sb)
+            const int64_t sb = sa + min(kSpan, c.nch - (c.lc - c.lc % kSpan));
+            span_whole = sa >= lo && sb <= hi;
+            span.clear();
+            if (!span_whole) {
+                const int64_t first = sa >= lo ? (int64_t)blockIdx.x : cta_of(sa);
+                span_area = p.chunk_records + first * p.slots * rec_size;
+                span_ctas = (int)((sb <= hi ? (int64_t)blockIdx.x : cta_of(sb - 1)) - first) + 1;
             }
         }
 
-        // ------------------------------------------------ the chunk's state --
-#pragma unroll
-        for (int i = 0; i < 2 * NT; ++i) {
-#pragma unroll
-            for (int w = 4; w < 32; w <<= 1)
-                l[i] += __shfl_xor_sync(0xffffffffu, l[i], w);
-            if (g == 0)
-                s_sum[(8 * (i / 2) + 2 * t + i % 2) * kWarps + warp] = l[i];
+        const int stg = step % kStages;
+        wait_bar(smem_addr(s_bars + stg), (step / kStages) & 1, s_flags, p.err, stg);
+        const uint8_t *stage = smem + stg * stage_bytes<DH>();
+        const bool bad = s_bad[stg] == step + 1;
+        St st;
+        const bool masked = c.lc * kChunk + kChunk > c.L - c.qn + 1;
+        const bool aborted = masked ? chunk_state(std::true_type{}, stage, step & 1, st)
+                                    : chunk_state(std::false_type{}, stage, step & 1, st);
+        if (aborted) {
+            // a wait ran out of time: let the copies in flight land, give up
+            for (int k = step + 1; k < copied; ++k)
+                wait_bar_drain(smem_addr(s_bars + k % kStages), (k / kStages) & 1);
+            return;
         }
-        __syncthreads();  // C: sums written
+        copy_next();  // every warp is past barrier C: the stage is free
 #pragma unroll
-        for (int i = 0; i < 2 * NT; ++i) {
-            const float *ss = s_sum + (8 * (i / 2) + 2 * t + i % 2) * kWarps;
-            const float4 u = *reinterpret_cast<const float4 *>(ss), v = *reinterpret_cast<const float4 *>(ss + 4);
-            l[i] = ((u.x + u.y) + (u.z + u.w)) + ((v.x + v.y) + (v.z + v.w));
+        for (int r = 0; r < NR; ++r) {
             if (bad)
-                l[i] = __int_as_float(0x7FC00000);
-            if (l[i] != l[i] && m[i] == -INFINITY)
-                m[i] = 0.f;  // a NaN state must not pass for an empty one
+                st.l[r] = __int_as_float(0x7FC00000);
+            if (st.l[r] != st.l[r] && st.m[r] == -INFINITY)
+                st.m[r] = 0.f;  // a NaN state must not pass for an empty one
         }
+
         const int rv = c.qn * G;
-        const bool last = c.lc + 1 == c.nch;
-        const int64_t group = (int64_t)c.b * hkv + c.kvh;
-        if (whole) {
-#pragma unroll
-            for (int i = 0; i < 2 * NT; ++i) {
-                const Fold f = fold_coef(acc_m[i], acc_l[i], m[i], l[i]);
-                acc_m[i] = f.m;
-                acc_l[i] = f.l;
-#pragma unroll
-                for (int b = 0; b < NB; ++b)
-#pragma unroll
-                    for (int k = 0; k < 2; ++k)
-                        acc_o[b][i / 2][i % 2 + 2 * k] = fold_elem(acc_o[b][i / 2][i % 2 + 2 * k], o[b][i / 2][i % 2 + 2 * k], f);
-                const int r = 8 * (i / 2) + 2 * t + i % 2;
-                if (last && r < rv) {
-                    const int64_t row = (int64_t)(c.qs + r / G) * p.hq + c.kvh * G + r % G;
-                    const float rl = __frcp_rn(acc_l[i]) * p.v_scale;
-#pragma unroll
-                    for (int b = 0; b < NB; ++b)
-                        *reinterpret_cast<uint32_t *>(p.out + row * DH + 16 * (warp + 8 * b) + 2 * g) =
-                            pack_bf16x2(acc_o[b][i / 2][i % 2] * rl, acc_o[b][i / 2][i % 2 + 2] * rl);
-                    if (p.lse && warp == 0 && g == 0)
-                        p.lse[row] = lse_of(acc_m[i], acc_l[i] * 0x1p-15f);
-                }
-            }
+        if (span_whole)
+            span.fold(st);
+        else
+            write_record(span_area + (c.lc % kSpan) * rec_size, st, rv);
+        const bool span_end = c.lc + 1 == c.nch || (c.lc + 1) % kSpan == 0;
+        if (!span_end && !last_chunk)
+            continue;
+        const int sp = c.lc / kSpan;
+        const int64_t grp = (int64_t)c.b * hkv + c.kvh;
+        if (!span_whole) {
+            if (!last_to_arrive(p.span_counters + grp * p.spans + sp, span_ctas))
+                continue;
+            fold_records(span, span_area, min(kSpan, c.nch - sp * kSpan), rv);
+        }
+        // the span is folded, here
+        const int nsp = (c.nch + kSpan - 1) / kSpan;
+        if (nsp == 1) {
+            write_output(span, rv);
+        } else if (group_whole) {
+            group.fold(span);
+            if (sp + 1 == nsp)
+                write_output(group, rv);
         } else {
-            float *rec = p.records + (group * p.nch + c.lc) * part_record_floats(p.rows, DH);
-            float *ro = rec + part_header_floats(p.rows);
-#pragma unroll
-            for (int i = 0; i < 2 * NT; ++i) {
-                const int r = 8 * (i / 2) + 2 * t + i % 2;
-                if (r < rv) {
-                    if (warp == 0 && g == 0) {
-                        __stcg(rec + r, m[i]);
-                        __stcg(rec + p.rows + r, l[i]);
-                    }
-#pragma unroll
-                    for (int b = 0; b < NB; ++b)
-                        __stcg(reinterpret_cast<float2 *>(ro + (int64_t)r * DH + 16 * (warp + 8 * b) + 2 * g),
-                               make_float2(o[b][i / 2][i % 2], o[b][i / 2][i % 2 + 2]));
-                }
-            }
-            if (last || x + 1 == hi) {
-                // the group's chunks of this range are written: arrive; the
-                // last CTA folds them all
-                const int arrivals = cta_of(gs + c.nch - 1) - cta_of(gs) + 1;
-                __syncthreads();
-                if (tid == 0) {
-                    uint32_t old;
-                    asm volatile("atom.acq_rel.gpu.global.add.u32 %0, [%1], 1;"
-                                 : "=r"(old)
-                                 : "l"(p.counters + group)
-                                 : "memory");
-                    const bool fold = old == (uint32_t)(arrivals - 1);
-                    if (fold)
-                        p.counters[group] = 0u;  // ready for the next call
-                    s_flags[1] = fold;
-                }
-                __syncthreads();
-                if (s_flags[1])
-                    merge_group<DH>(p, p.records + group * p.nch * part_record_floats(p.rows, DH), c.nch, rv, c.qs,
-                                    c.kvh);
+            float *recs = p.span_records + grp * p.spans * rec_size;
+            write_record(recs + sp * rec_size, span, rv);
+            if (last_to_arrive(p.group_counters + grp, nsp)) {
+                fold_records(group, recs, nsp, rv);
+                write_output(group, rv);
             }
         }
     }
-    (void)seg_first;
 }
 
-template <int DH, int NT>
+template <int DH, int RN>
 cudaError_t set_attributes()
 {
-    return cudaFuncSetAttribute(quant_attn_kernel<DH, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                (int)Layout<DH, NT>::bytes(kScanMaxSeqs));
+    return cudaFuncSetAttribute(quant_attn_kernel<DH, RN>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                (int)Layout<DH, RN>::bytes(kScanMaxSeqs));
 }
 
-template <int DH, int NT>
-cudaError_t launch(const Params &p, cudaStream_t stream, int num_sms, int64_t max_chunks, int64_t *grid)
+static int rows_capacity(int rows) { return rows <= 4 ? 4 : rows <= 8 ? 8 : rows <= 16 ? 16 : 32; }
+
+// CTAs of the grid: one wave, fewer when there are fewer chunks.
+static int64_t grid_of(int dh, int rn, int64_t max_chunks)
 {
-    const size_t smem = Layout<DH, NT>::bytes(p.num_seqs);
-    // CTAs resident at once: registers allow ctas_per_sm, shared memory (228 KB
-    // per SM, 1 KB of it reserved per CTA) may allow fewer
-    int64_t per_sm = (int64_t)(228 * 1024 / (smem + 1024));
-    per_sm = per_sm < 1 ? 1 : (per_sm > ctas_per_sm<DH, NT>() ? ctas_per_sm<DH, NT>() : per_sm);
-    *grid = per_sm * num_sms < max_chunks ? per_sm * num_sms : max_chunks;
-    if (*grid < 1)
-        *grid = 1;
+    const int64_t wave = (int64_t)kGridSms * (dh == 128 && rn <= 16 ? 2 : 1);
+    return max_chunks < 1 ? 1 : (max_chunks < wave ? max_chunks : wave);
+}
+
+static int64_t chunks_of(int dh, int32_t len) { return ((int64_t)len + chunk_keys(dh) - 1) / chunk_keys(dh); }
+static int64_t spans_of(int dh, int32_t len) { return (chunks_of(dh, len) + kSpan - 1) / kSpan; }
+
+// Chunk records of a cut span at most.
+static int slots_of(int dh, int32_t len)
+{
+    const int64_t n = chunks_of(dh, len);
+    return (int)(n < kSpan ? n : kSpan);
+}
+
+template <int DH, int RN>
+cudaError_t launch(const Params &p, cudaStream_t stream, int64_t grid)
+{
+    static_assert(ctas_per_sm<DH, RN>() == (DH == 128 && RN <= 16 ? 2 : 1), "grid_of");
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)*grid);
+    cfg.gridDim = dim3((unsigned)grid);
     cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = smem;
+    cfg.dynamicSmemBytes = Layout<DH, RN>::bytes(p.num_seqs);
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, quant_attn_kernel<DH, NT>, p);
+    return cudaLaunchKernelEx(&cfg, quant_attn_kernel<DH, RN>, p);
 }
-
-static int64_t chunks_of(int32_t len) { return ((int64_t)len + kChunk - 1) / kChunk; }
 
 }  // namespace qa
 
-size_t quant_attn_record_bytes(int32_t num_seqs, int32_t num_kv_heads, int32_t head_dim, int rows, int32_t max_seq_len)
+QuantAttnSpace quant_attn_space(int32_t num_seqs, int32_t num_kv_heads, int32_t head_dim, int rows, int32_t max_seq_len)
 {
-    return (size_t)num_seqs * num_kv_heads * qa::chunks_of(max_seq_len) * (size_t)part_record_floats(rows, head_dim) * 4;
+    QuantAttnSpace s{};
+    const int64_t groups = (int64_t)num_seqs * num_kv_heads, max_chunks = groups * qa::chunks_of(head_dim, max_seq_len);
+    const int64_t grid = qa::grid_of(head_dim, qa::rows_capacity(rows), max_chunks);
+    const size_t rec = (size_t)part_record_floats(rows, head_dim) * 4;
+    s.counters = groups * (qa::spans_of(head_dim, max_seq_len) + 1);
+    s.chunk_bytes = (size_t)grid * qa::slots_of(head_dim, max_seq_len) * rec;
+    s.span_bytes = qa::spans_of(head_dim, max_seq_len) > 1 ? (size_t)groups * qa::spans_of(head_dim, max_seq_len) * rec : 0;
+    return s;
 }
 
-cudaError_t launch_quant_attention(const QuantAttnArgs &a, ErrState *err, cudaStream_t stream, int num_sms, char *info,
+cudaError_t launch_quant_attention(const QuantAttnArgs &a, ErrState *err, cudaStream_t stream, char *info,
                                    size_t info_len)
 {
     qa::Params p{};
@@ -755,45 +1008,53 @@ cudaError_t launch_quant_attention(const QuantAttnArgs &a, ErrState *err, cudaSt
     p.max_query_len = a.max_query_len;
     p.max_seq_len = a.max_seq_len;
     p.rows = a.max_query_len * p.group;
-    p.nch = qa::chunks_of(a.max_seq_len);
     p.score_scale = a.scale * 1.4426950408889634f * a.pool.k_scale;
     p.v_scale = a.pool.v_scale;
     p.out = static_cast<__nv_bfloat16 *>(a.out);
     p.lse = a.lse;
-    p.counters = a.counters;
-    p.records = a.records;
     p.err = err;
-    const int64_t max_chunks = (int64_t)p.num_seqs * p.hkv * p.nch;
-    const int nt = p.rows <= 8 ? 1 : p.rows <= 16 ? 2 : p.rows <= 32 ? 4 : 8;
-    int64_t grid = 0;
+    const int64_t groups = (int64_t)p.num_seqs * p.hkv, max_chunks = groups * qa::chunks_of(a.pool.head_dim, p.max_seq_len);
+    const int rn = qa::rows_capacity(p.rows);
+    const int64_t grid = qa::grid_of(a.pool.head_dim, rn, max_chunks);
+    const QuantAttnSpace s = quant_attn_space(p.num_seqs, p.hkv, a.pool.head_dim, p.rows, p.max_seq_len);
+    p.slots = qa::slots_of(a.pool.head_dim, p.max_seq_len);
+    p.spans = (int32_t)qa::spans_of(a.pool.head_dim, p.max_seq_len);
+    p.group_counters = a.counters;
+    p.span_counters = a.counters + groups;
+    p.chunk_records = a.records;
+    p.span_records = a.records + s.chunk_bytes / 4;
     cudaError_t e = cudaErrorNotSupported;
-    auto go = [&](auto fn) { e = fn(p, stream, num_sms, max_chunks, &grid); };
+    auto go = [&](auto fn) { e = fn(p, stream, grid); };
     switch (a.pool.head_dim) {
     case 128:
-        go(nt == 1 ? qa::launch<128, 1> : nt == 2 ? qa::launch<128, 2> : nt == 4 ? qa::launch<128, 4> : qa::launch<128, 8>);
+        go(rn == 4    ? qa::launch<128, 4>
+           : rn == 8  ? qa::launch<128, 8>
+           : rn == 16 ? qa::launch<128, 16>
+                      : qa::launch<128, 32>);
         break;
     case 256:
-        go(nt == 1 ? qa::launch<256, 1> : nt == 2 ? qa::launch<256, 2> : qa::launch<256, 4>);
+        go(rn == 4 ? qa::launch<256, 4> : rn == 8 ? qa::launch<256, 8> : rn == 16 ? qa::launch<256, 16> : qa::launch<256, 32>);
         break;
     case 512:
-        go(nt == 1 ? qa::launch<512, 1> : nt == 2 ? qa::launch<512, 2> : qa::launch<512, 4>);
+        go(rn == 4 ? qa::launch<512, 4> : rn == 8 ? qa::launch<512, 8> : qa::launch<512, 16>);
         break;
     }
-    snprintf(info, info_len, "quant attention direct dh=%d rows=%d grid=%lld chunks<=%lld", a.pool.head_dim, p.rows,
-             (long long)grid, (long long)max_chunks);
+    snprintf(info, info_len, "quant attention direct dh=%d rows=%d/%d grid=%lld chunks<=%lld", a.pool.head_dim, p.rows,
+             rn, (long long)grid, (long long)max_chunks);
     return e;
 }
 
 cudaError_t init_quant_attention_attributes()
 {
     cudaError_t e;
-    if ((e = qa::set_attributes<128, 1>()) != cudaSuccess || (e = qa::set_attributes<128, 2>()) != cudaSuccess ||
-        (e = qa::set_attributes<128, 4>()) != cudaSuccess || (e = qa::set_attributes<128, 8>()) != cudaSuccess ||
-        (e = qa::set_attributes<256, 1>()) != cudaSuccess || (e = qa::set_attributes<256, 2>()) != cudaSuccess ||
-        (e = qa::set_attributes<256, 4>()) != cudaSuccess || (e = qa::set_attributes<512, 1>()) != cudaSuccess ||
-        (e = qa::set_attributes<512, 2>()) != cudaSuccess)
+    if ((e = qa::set_attributes<128, 4>()) != cudaSuccess || (e = qa::set_attributes<128, 8>()) != cudaSuccess ||
+        (e = qa::set_attributes<128, 16>()) != cudaSuccess || (e = qa::set_attributes<128, 32>()) != cudaSuccess ||
+        (e = qa::set_attributes<256, 4>()) != cudaSuccess ||
+        (e = qa::set_attributes<256, 8>()) != cudaSuccess || (e = qa::set_attributes<256, 16>()) != cudaSuccess ||
+        (e = qa::set_attributes<256, 32>()) != cudaSuccess || (e = qa::set_attributes<512, 4>()) != cudaSuccess ||
+        (e = qa::set_attributes<512, 8>()) != cudaSuccess)
         return e;
-    return qa::set_attributes<512, 4>();
+    return qa::set_attributes<512, 16>();
 }
 
 }  // namespace pa

@@ -95,10 +95,10 @@ def _same(a, b):
 
 @pytest.mark.parametrize("lens,new,hq,hkv,dh", [
     ([1], 1, 1, 1, 128), ([16], 1, 8, 2, 128), ([17, 1, 128, 129, 255, 256, 257], 1, 8, 2, 128),
-    ([700, 513], 1, 7, 1, 128), ([300, 40], 1, 16, 2, 128), ([300, 5, 129], 5, 8, 2, 128), ([64, 600], 8, 8, 1, 128),
-    ([530, 31], 4, 32, 2, 128), ([1000], 1, 64, 1, 128), ([2, 3, 300], [2, 1, 3], 8, 2, 128),
+    ([700, 513], 1, 7, 1, 128), ([300, 40], 1, 16, 2, 128), ([300, 5, 129], 5, 8, 2, 128), ([64, 600], 4, 8, 1, 128),
+    ([530, 31], 2, 32, 2, 128), ([1000], 1, 32, 1, 128), ([2, 3, 300], [2, 1, 3], 8, 2, 128),
     ([90, 257, 1], 1, 8, 2, 256), ([300, 44], 5, 8, 2, 256), ([260], 8, 4, 1, 256), ([131], 3, 10, 2, 256),
-    ([200, 33], 1, 16, 2, 512), ([140], 2, 16, 2, 512), ([150], 4, 8, 1, 512),
+    ([200, 33], 1, 16, 2, 512), ([140], 2, 16, 2, 512), ([150], 4, 4, 1, 512), ([4097], 1, 4, 1, 512),
     ([5, 9, 40], [0, 1, 2], 4, 4, 128)])
 def test_direct_matches_formula(lens, new, hq, hkv, dh):
     c = Case(lens, new, hq, hkv, dh, seed=len(lens) + dh + hq, k_scale=0.5, v_scale=2.0)
