@@ -445,7 +445,8 @@ PA_API pa_status pa_qk_norm_rope_and_cache(
  * BYTES (v likewise).  Pools map onto it as two [num_blocks, Hkv, 9*Dh] byte
  * tensors or one [num_blocks, 2, Hkv, 9*Dh] one.
  * Requirements: block_size == 16; head_dim in {128, 256, 512}; k and v
- * 16-byte aligned; strides positive multiples of 16, head_stride >= 9*Dh;
+ * 16-byte aligned; strides positive multiples of 16 below 2^32, head_stride
+ * >= 9*Dh;
  * k_scale and v_scale powers of two in [2^-32, 2^32]; reserved == 0.
  */
 typedef struct {

@@ -936,6 +936,8 @@ static pa_status check_quant_cache(const pa_quant_cache *c)
         return PA_ERR_UNSUPPORTED;
     if (c->block_stride <= 0 || c->head_stride < (int64_t)9 * c->head_dim || ((c->block_stride | c->head_stride) & 15))
         return PA_ERR_INVALID_ARG;
+    if (c->block_stride > UINT32_MAX || c->head_stride > UINT32_MAX)
+        return PA_ERR_UNSUPPORTED;
     return tensor_scale_ok(c->k_scale) && tensor_scale_ok(c->v_scale) ? PA_OK : PA_ERR_INVALID_ARG;
 }
 

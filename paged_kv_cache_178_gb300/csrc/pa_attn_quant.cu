@@ -20,26 +20,25 @@
 //   S^T = K.Q^T: M = the 16 tokens of a page, N = 8 query rows, K = head dim.
 //   O^T = V^T.P^T: a V byte holds two neighbouring elements (d, d+1) of one
 //     token, so a converted register is a pair of different M rows.  Up to
-//     eight rows (PAR) the pair is taken as one row with two K indices
-//     (token, parity), and P^T has two columns per query row: (p, 0) gives
-//     element d, (0, p) element d+1.  The wasted half of the product is free
-//     (four rows fill N = 8; eight take two instructions), and no permutes are
-//     needed.  From 16 rows on, permutes that regroup the pairs by element cost
-//     less than doubling the instructions.
+//     four rows (PAR) the pair is taken as one row with two K indices (token,
+//     parity), and P^T has two columns per query row: (p, 0) gives element d,
+//     (0, p) element d+1.  That fills N = 8 and needs no permutes.  With more
+//     rows the pairs are regrouped by element with eight permutes per page,
+//     which costs less than twice the products.
 //
 // Fixed arithmetic (a row's results do not depend on the batch or the grid):
-//   chunks of 256 keys (128 at head dim 512) from key 0, each with its own exact maximum; a chunk's
+//   chunks of 512 keys (256 at head dim 256, 128 at 512) from key 0, each with its own exact maximum; a chunk's
 //   row sum is, per warp, a butterfly over its keys, then the eight warps'
 //   sums pairwise; chunk states fold left to right (State::fold) within spans
 //   of 32 chunks, and the span states left to right.
 //
-// A CTA (8 warps) per chunk: warp w scores its one or two pages and spreads their
-// V scales (one f16 pair per scale); row maxima are exchanged (barrier); P goes
-// to shared memory in fragment order (barrier); each warp multiplies P by 32
+// A CTA (8 warps) per chunk: each warp scores its pages; row maxima are
+// exchanged (barrier); P goes to shared memory in fragment order, the V scales
+// as one f16 pair each (barrier); each warp multiplies P by 32
 // head-dim elements of the pages (at head dim 128 of half of the pages, the
 // halves are added through shared memory, with the row sums; barrier).  Each
-// warp copies its pages of the chunk after next (cp.async.bulk, one mbarrier
-// per chunk).  The chunks of all (request, KV head) groups are dealt out as
+// warp copies its pages of the next chunk (cp.async): K during the second
+// product, V during the first one.  The chunks of all (request, KV head) groups are dealt out as
 // equal contiguous ranges.  A span inside one range is folded in registers; the
 // chunks of a span cut by a range end become records, folded by the last CTA
 // to arrive; so do the spans of a cut group.  No CTA waits for another.
@@ -57,32 +56,30 @@ namespace qa {
 
 constexpr int kWarps = 8;
 constexpr int kThreads = 32 * kWarps;
-// pages per warp of a chunk: two stages of a chunk fit shared memory
-__host__ __device__ constexpr int pages_per_warp(int dh) { return dh == 512 ? 1 : 2; }
+// pages per warp of a chunk: as many as shared memory holds (at head dim 128
+// for two CTAs), since a chunk's exchanges and bookkeeping cost the same
+__host__ __device__ constexpr int pages_per_warp(int dh) { return dh == 128 ? 4 : dh == 256 ? 2 : 1; }
 __host__ __device__ constexpr int chunk_pages(int dh) { return kWarps * pages_per_warp(dh); }
 __host__ __device__ constexpr int chunk_keys(int dh) { return 16 * chunk_pages(dh); }
 constexpr int kSpan = 32;           // chunks per span
-constexpr int kStages = 2;          // chunks in shared memory
 constexpr float kShift = 15.f;      // p is scaled by 2^kShift (largest f16: 2^16)
 constexpr int kGridSms = 152;       // SMs the grid is sized for
 
-template <int DH>
-constexpr int stage_bytes() { return 2 * chunk_pages(DH) * quant_record_bytes(DH); }
 // CTAs per SM that registers and shared memory are sized for
 template <int DH, int RN>
-constexpr int ctas_per_sm() { return DH == 128 && RN <= 16 ? 2 : 1; }
-// up to eight rows: element parity as a K index (see above)
+constexpr int ctas_per_sm() { return DH == 128 && RN <= 8 ? 2 : 1; }
+// up to four rows: element parity as a K index (see above)
 template <int RN>
-constexpr bool par_mode() { return RN <= 8; }
+constexpr bool par_mode() { return RN == 4; }
 
 // Shared-memory layout in bytes.  RN: query rows (4, 8, 16 or 32).
 template <int DH, int RN>
 struct Layout {
     static constexpr int kPages = chunk_pages(DH);
     static constexpr int NQ = RN < 8 ? 1 : RN / 8;                  // N tiles of the first product
-    static constexpr int PV4 = RN == 4 ? 4 : (RN == 8 ? 8 : 2 * NQ);  // 32-bit registers of a page's P fragments
+    static constexpr int PV4 = RN == 4 ? 4 : 2 * NQ;  // 32-bit registers of a page's P fragments
     static constexpr int NCF = DH == 128 ? RN / 2 : 0;              // floats a thread hands to the other half
-    static constexpr int q = kStages * stage_bytes<DH>();
+    static constexpr int q = 2 * kPages * quant_record_bytes(DH);  // after the K and the V records
     static constexpr int p = q + NQ * DH * 16;
     static constexpr int spread = p + kPages * PV4 * 128;           // V scales as f16 pairs
     static constexpr int half = spread + kPages * DH * 4;
@@ -91,19 +88,19 @@ struct Layout {
     static constexpr int cq = sum + NQ * 8 * kWarps * 4;
     static constexpr int lim = cq + NQ * 8 * 4;
     static constexpr int nan = lim + NQ * 8 * 4;
-    static constexpr int bars = nan + 2 * (DH / 16) * 4;
-    static constexpr int bad = bars + kStages * 8;
+    static constexpr int bad = nan + 2 * (DH / 16) * 4;
     static constexpr int flags = bad + 16;
     static constexpr int sums = flags + 16;
     static constexpr int pre = sums + kWarps * 8;  // [num_seqs + 1] int32
-    static_assert(q % 16 == 0 && spread % 16 == 0 && max % 16 == 0 && bars % 16 == 0 && bad % 16 == 0 && sums % 8 == 0, "layout");
+    static_assert(q % 16 == 0 && spread % 16 == 0 && max % 16 == 0 && bad % 8 == 0 && sums % 8 == 0, "layout");
     static_assert(pre + (kScanMaxSeqs + 1) * 4 <= (int)kMaxSmemPerBlock, "shared memory");
     static size_t bytes(int num_seqs) { return (size_t)pre + 4 * ((size_t)num_seqs + 1); }
 };
 
 struct Params {
     const uint8_t *k, *v;
-    int64_t block_stride, head_stride, num_blocks;
+    uint32_t block_stride, head_stride;  // bytes (the host refuses larger ones)
+    int64_t num_blocks;
     const __nv_bfloat16 *q;
     int64_t q_tok_stride, num_q_tokens;
     const int32_t *block_tables, *seq_lens, *qsl;
@@ -146,11 +143,9 @@ __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi)
     return r;
 }
 
-__device__ __forceinline__ void bulk_copy(uint32_t dst, const void *src, uint32_t bytes, uint32_t bar, uint64_t policy)
+__device__ __forceinline__ void copy16(uint32_t dst, const void *src, uint64_t policy)
 {
-    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint [%0], [%1], %2, [%3], "
-                 "%4;" ::"r"(dst),
-                 "l"(src), "r"(bytes), "r"(bar), "l"(policy)
+    asm volatile("cp.async.cg.shared.global.L2::cache_hint [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "l"(policy)
                  : "memory");
 }
 
@@ -185,6 +180,7 @@ template <int DH>
 struct Chunk {
     int b, kvh, lc, nch;
     int qs, qn, L;
+    const int32_t *row;  // the request's block table
 
     __device__ __forceinline__ void load(const Params &p, const int32_t *pre)
     {
@@ -193,6 +189,7 @@ struct Chunk {
         qn = m.qn;
         L = m.L;
         nch = pre[b + 1] - pre[b];
+        row = p.block_tables + (int64_t)b * p.max_blocks;
     }
     __device__ __forceinline__ void at(const Params &p, const int32_t *pre, int64_t x)
     {
@@ -216,12 +213,9 @@ struct Chunk {
         while (pre[b + 1] == pre[b]);
         load(p, pre);
     }
-    // block id of the chunk's page `lane` (lanes 0..15; 0 where there is none)
-    __device__ __forceinline__ int id(const Params &p, int lane) const
-    {
-        const int pg = lc * chunk_pages(DH) + lane;
-        return lane < chunk_pages(DH) && pg < (L + 15) / 16 ? __ldg(p.block_tables + (int64_t)b * p.max_blocks + pg) : 0;
-    }
+    __device__ __forceinline__ bool has_page(int i) const { return (lc * chunk_pages(DH) + i) * 16 < L; }
+    // block id of the chunk's page i (0 where there is none)
+    __device__ __forceinline__ int id(int i) const { return has_page(i) ? __ldg(row + lc * chunk_pages(DH) + i) : 0; }
 };
 
 // A thread's share of a softmax state (of a chunk, a span or a group): NR
@@ -276,7 +270,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm<DH, RN>()) quant_attn_ke
     constexpr int NP = HALVES ? 1 : 2 * NE;   // element pairs of a thread's state
     constexpr int REC = quant_record_bytes(DH), CODES = quant_code_bytes(DH);
     constexpr bool kQRegs = NQ * DH <= 256;  // Q fragments in registers (else read from shared memory)
-    constexpr int OT = PAR ? RN / 4 : 2 * NQ;  // accumulator tiles of a 32-element block
+    constexpr int OT = PAR ? 1 : 2 * NQ;  // accumulator tiles of a 32-element block
     using St = State<NR, NP>;
     griddep_wait();
     griddep_launch_dependents();
@@ -290,23 +284,16 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm<DH, RN>()) quant_attn_ke
     float *const s_cq = reinterpret_cast<float *>(smem + Lay::cq);    // raw score -> log2 units
     int *const s_lim = reinterpret_cast<int *>(smem + Lay::lim);      // last key of a row
     int *const s_nan = reinterpret_cast<int *>(smem + Lay::nan);      // [chunk parity][DH/16] first NaN key of an element block
-    uint64_t *const s_bars = reinterpret_cast<uint64_t *>(smem + Lay::bars);
-    volatile int *const s_bad = reinterpret_cast<int *>(smem + Lay::bad);  // [stage] 1 + the last chunk there with a bad block id
-    volatile int *const s_flags = reinterpret_cast<int *>(smem + Lay::flags);  // [0] abort [1] last to arrive
+    volatile int *const s_bad = reinterpret_cast<int *>(smem + Lay::bad);  // [chunk parity] 1 + the last chunk with a bad block id
+    volatile int *const s_flags = reinterpret_cast<int *>(smem + Lay::flags);  // [0] last to arrive
     int32_t *const s_pre = reinterpret_cast<int32_t *>(smem + Lay::pre);
     const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32, g = lane / 4, t = lane % 4;
     const int G = p.group, hkv = p.hkv;
 
     // the work: chunks of the valid requests
-    if (tid == 0) {
-        for (int i = 0; i < kStages; ++i)
-            mbar_init(smem_addr(s_bars + i), 2 * kPages);
-        s_flags[0] = 0;
-        fence_barrier_init();
-    }
     if (tid < 2 * (DH / 16))
         s_nan[tid] = 0x7fffffff;
-    if (tid < kStages)
+    if (tid < 2)
         s_bad[tid] = 0;
     const long long tot = block_exclusive_sums<kThreads>(
         p.num_seqs, s_pre, reinterpret_cast<long long *>(smem + Lay::sums), [&](int b) {
@@ -336,46 +323,69 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm<DH, RN>()) quant_attn_ke
     auto cta_of = [&](int64_t x) { return div_floor((x + 1) * ctas + T - 1, T) - 1; };
     const int64_t lo = range_start(blockIdx.x), hi = range_start((int64_t)blockIdx.x + 1);
 
-    // Copies: every warp its pages of a chunk, K and V, one by each of its
-    // first lanes; the block ids are loaded one chunk ahead.  (One warp issuing
-    // all copies of a chunk held the others up by 4 us in 37; a ninth warp for
-    // them leaves 96 registers a thread.)
+    // Copies: every warp its pages of a chunk, 16 bytes a lane and step, the K
+    // records while the chunk before is past its first product, the V records
+    // when that is past its second; the block ids are loaded a chunk ahead.
+    // A warp scores and spreads what it copied itself, and the other warps read
+    // its V codes after barrier B: waiting for the own copies is all the
+    // synchronisation they need.  (Bulk copies, four a warp, took 600 clocks of
+    // every chunk to issue.)
     const uint64_t policy = l2_policy_evict_first();
     const int chunks = (int)(hi - lo);
-    const int cpage = PPW * warp + lane % PPW;
-    const bool is_v = (lane / PPW) % 2 != 0;
-    const uint8_t *const cpool = is_v ? p.v : p.k;
-    const uint32_t cdst = smem_addr(smem + ((is_v ? kPages : 0) + cpage) * REC);
+    const int64_t v_delta = p.v - p.k;
+    const uint32_t nblocks = (uint32_t)min(p.num_blocks, (int64_t)0x7fffffff + 1);
     Chunk<DH> pc;
     pc.at(p, s_pre, lo);
-    int copied = 0;  // chunks copied so far
-    int id = pc.id(p, cpage);
-    auto copy_next = [&]() {
-        if (copied >= chunks)
-            return;
-        if (lane < 2 * PPW) {
-            const int st = copied % kStages;
-            const uint32_t bar = smem_addr(s_bars + st);
-            const bool exists = pc.lc * kPages + cpage < (pc.L + 15) / 16;
-            if (exists && (uint64_t)(int64_t)id < (uint64_t)p.num_blocks) {
-                mbar_arrive_expect_tx(bar, REC);
-                bulk_copy(cdst + st * stage_bytes<DH>(), cpool + (int64_t)id * p.block_stride + pc.kvh * p.head_stride,
-                          REC, bar, policy);
-            } else {
-                if (exists) {
-                    s_bad[st] = copied + 1;
+    int copied = 0;  // the chunk pc stands at
+    int id[PPW];
+    auto load_ids = [&]() {
+#pragma unroll
+        for (int j = 0; j < PPW; ++j)
+            id[j] = pc.id(PPW * warp + j);
+    };
+    load_ids();
+    auto copy = [&](auto is_v) {
+        constexpr int V = decltype(is_v)::value;
+        if (copied < chunks) {
+            constexpr int UN = REC / 16;  // 16-byte units of a record
+            const uint8_t *src[PPW];
+            bool go[PPW];
+            const uint8_t *const base = p.k + (V ? v_delta : 0) + ((uint64_t)(uint32_t)pc.kvh * p.head_stride + 16 * lane);
+#pragma unroll
+            for (int j = 0; j < PPW; ++j) {
+                const bool exists = pc.has_page(PPW * warp + j);
+                go[j] = exists && (uint32_t)id[j] < nblocks;
+                if (!V && exists && !go[j] && lane == 0) {
+                    s_bad[copied & 1] = copied + 1;
                     record_error(p.err, kErrBadMetadata, pc.b);
                 }
-                mbar_arrive(bar);
+                src[j] = base + (uint64_t)(uint32_t)id[j] * p.block_stride;
+            }
+            const uint32_t dst = smem_addr(smem + (V * kPages + PPW * warp) * REC) + 16 * lane;
+#pragma unroll
+            for (int i = 0; i < (PPW * UN + 31) / 32; ++i) {
+                // unit lane + 32i: of record r0, or past its end of r1
+                const int r0 = 32 * i / UN, r1 = (32 * i + 31) / UN;
+                const bool next = r1 != r0 && lane >= UN * r1 - 32 * i;
+                const bool end = next && r1 >= PPW;
+                const int rn = r1 >= PPW ? PPW - 1 : r1;
+                if ((next ? go[rn] : go[r0]) && !end)
+                    copy16(dst + 512 * i, (next ? src[rn] - rn * REC : src[r0] - r0 * REC) + 512 * i, policy);
             }
         }
-        if (++copied < chunks) {
+        asm volatile("cp.async.commit_group;" ::: "memory");
+        if (V && copied < chunks && ++copied < chunks) {
             pc.next(p, s_pre);
-            id = pc.id(p, cpage);
+            load_ids();
         }
     };
-    for (int i = 0; i < kStages; ++i)
-        copy_next();
+    // all own copies but the last group have landed
+    auto wait_copies = [&]() {
+        asm volatile("cp.async.wait_group 1;" ::: "memory");
+        __syncwarp();
+    };
+    copy(std::integral_constant<int, 0>{});
+    copy(std::integral_constant<int, 1>{});
 
     // this thread's place in the second product: element pairs c0 = 16*wd + g
     // and c0 + 8 of each 32-element block
@@ -391,10 +401,12 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm<DH, RN>()) quant_attn_ke
     Chunk<DH> c;
     c.at(p, s_pre, lo);
     St span, group;
-    const int64_t rec_hdr = part_header_floats(p.rows), rec_size = part_record_floats(p.rows, DH);
+    const uint32_t rec_hdr = (uint32_t)part_header_floats(p.rows), rec_size = (uint32_t)part_record_floats(p.rows, DH);
 
     // ------------------------------------------------ one chunk's state --
-    auto chunk_state = [&](auto masked_tag, const uint8_t *stage, int parity, St &st) -> bool {
+    auto chunk_state = [&](auto masked_tag, int step, St &st) -> bool {
+        const int parity = step & 1;
+        const uint8_t *const stage = smem;
         constexpr bool MASKED = decltype(masked_tag)::value;  // some row does not see some key of the chunk
         const int key0 = c.lc * kChunk;
         const int npages = MASKED ? min(kPages, (c.L - key0 + 15) / 16) : kPages;
@@ -462,6 +474,44 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm<DH, RN>()) quant_attn_ke
                         if (key + (i < 2 ? 0 : 2) > s_lim[score_row(n, i % 2)])
                             s[j][n][i] = -INFINITY;
             }
+        }
+        if (MASKED) {
+            // pages that do not exist: no key
+#pragma unroll
+            for (int j = 0; j < PPW; ++j)
+                if (PPW * warp + j >= npages)
+#pragma unroll
+                    for (int n = 0; n < NQ; ++n)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            s[j][n][i] = -INFINITY;
+        }
+        // largest raw score of each row, over the warp's keys
+#pragma unroll
+        for (int n = 0; n < NQ; ++n)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                float x = fmaxf(s[0][n][i], s[0][n][2 + i]);
+#pragma unroll
+                for (int j = 1; j < PPW; ++j)
+                    x = max3f(x, s[j][n][i], s[j][n][2 + i]);
+#pragma unroll
+                for (int w = 4; w < 32; w <<= 1)
+                    x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, w));
+                if (g == 0 && (RN > 4 || t < 2))
+                    s_max[score_row(n, i) * kWarps + warp] = x;
+            }
+        __syncthreads();  // A: maxima written; K is consumed
+        const bool bad = s_bad[parity] == step + 1;
+        if (tid < DH / 16)
+            s_nan[(parity ^ 1) * (DH / 16) + tid] = 0x7fffffff;  // for the next chunk
+        copy(std::integral_constant<int, 0>{});  // the next chunk's K
+        wait_copies();                           // this chunk's V
+#pragma unroll
+        for (int j = 0; j < PPW; ++j) {
+            const int page = PPW * warp + j;
+            if (MASKED && page >= npages)
+                break;
             // the page's V scales: lane = (element block lane/4 + 8b, tokens 4*(lane%4)..+3)
 #pragma unroll
             for (int b = 0; b < NB; ++b) {
@@ -486,35 +536,6 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm<DH, RN>()) quant_attn_ke
                 s_spread[(page * (DH / 16) + 8 * b + g) * 4 + t] = make_uint4(f[0], f[1], f[2], f[3]);
             }
         }
-        if (MASKED) {
-            // pages that do not exist: no key
-#pragma unroll
-            for (int j = 0; j < PPW; ++j)
-                if (PPW * warp + j >= npages)
-#pragma unroll
-                    for (int n = 0; n < NQ; ++n)
-#pragma unroll
-                        for (int i = 0; i < 4; ++i)
-                            s[j][n][i] = -INFINITY;
-        }
-        // largest raw score of each row, over the warp's keys
-#pragma unroll
-        for (int n = 0; n < NQ; ++n)
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                float x = fmaxf(s[0][n][i], s[0][n][2 + i]);
-                if constexpr (PPW == 2)
-                    x = max3f(x, s[PPW - 1][n][i], s[PPW - 1][n][2 + i]);
-#pragma unroll
-                for (int w = 4; w < 32; w <<= 1)
-                    x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, w));
-                if (g == 0 && (RN > 4 || t < 2))
-                    s_max[score_row(n, i) * kWarps + warp] = x;
-            }
-        __syncthreads();  // A: maxima and scales written; the previous chunk is consumed
-        const bool aborted = s_flags[0] != 0;  // before B, so that every thread reads the same
-        if (tid < DH / 16)
-            s_nan[(parity ^ 1) * (DH / 16) + tid] = 0x7fffffff;  // for the next chunk
         float l[NQ][2], mrow[NQ][2];
 #pragma unroll
         for (int n = 0; n < NQ; ++n) {
@@ -534,8 +555,9 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm<DH, RN>()) quant_attn_ke
                     pr[j][2 + i] = ex2(__fmaf_rn(s[j][n][2 + i], cq, add));
                 }
                 l[n][i] = pr[0][i] + pr[0][2 + i];
-                if constexpr (PPW == 2)
-                    l[n][i] += pr[PPW - 1][i] + pr[PPW - 1][2 + i];
+#pragma unroll
+                for (int j = 1; j < PPW; ++j)
+                    l[n][i] += pr[j][i] + pr[j][2 + i];
             }
             // P^T fragments: after the transpose thread (g, t) holds column
             // g's keys in pairs, tokens 4t, 4t+1 (x) and 4t+2, 4t+3 (y)
@@ -548,17 +570,12 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm<DH, RN>()) quant_attn_ke
                     const uint32_t a = g < 4 ? 0x4410u : 0x1044u, b = g < 4 ? 0x4432u : 0x3244u;
                     reinterpret_cast<uint4 *>(s_p)[page * 32 + lane] =
                         make_uint4(__byte_perm(x, 0u, a), __byte_perm(x, 0u, b), __byte_perm(y, 0u, a), __byte_perm(y, 0u, b));
-                } else if constexpr (RN == 8) {
-                    reinterpret_cast<uint4 *>(s_p)[(2 * page) * 32 + lane] =
-                        make_uint4(x & 0xffffu, x >> 16, y & 0xffffu, y >> 16);
-                    reinterpret_cast<uint4 *>(s_p)[(2 * page + 1) * 32 + lane] =
-                        make_uint4(x << 16, x & 0xffff0000u, y << 16, y & 0xffff0000u);
                 } else {
                     reinterpret_cast<uint2 *>(s_p)[(page * NQ + n) * 32 + lane] = make_uint2(x, y);
                 }
             }
         }
-        __syncthreads();  // B: P written
+        __syncthreads();  // B: P and scales written, V visible
         float o[NE][OT][4], acc[2][NE][OT][4];  // for the even and the odd pages, as above
 #pragma unroll
         for (int e = 0; e < NE; ++e)
@@ -665,8 +682,6 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm<DH, RN>()) quant_attn_ke
                 for (int k = 0; k < F; ++k) {
                     if constexpr (RN == 4)
                         pr[2 * e + i][k] = o[e][0][2 * i + k];
-                    else if constexpr (RN == 8)  // k: parity, row
-                        pr[2 * e + i][k] = o[e][k / 2][2 * i + k % 2];
                     else  // k: N tile, parity, row
                         pr[2 * e + i][k] = o[e][2 * (k / 4) + i][k % 4];
                 }
@@ -689,7 +704,8 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm<DH, RN>()) quant_attn_ke
             for (int k = 0; k < F; ++k)
                 s_half[k * kThreads + (tid ^ 128)] = keep ? pr[0][k] : pr[1][k];
         }
-        __syncthreads();  // C: sums and halves written
+        __syncthreads();  // C: sums and halves written; V is consumed
+        copy(std::integral_constant<int, 1>{});  // the next chunk's V
         if constexpr (HALVES) {
             const int keep = warp / 4;
 #pragma unroll
@@ -711,8 +727,6 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm<DH, RN>()) quant_attn_ke
                     // the other parity of the kept row from lane t ^ 2
                     const float got = __shfl_xor_sync(0xffffffffu, t < 2 ? pr[i][1] : pr[i][0], 2);
                     st.o[i][0] = t < 2 ? make_float2(pr[i][0], got) : make_float2(got, pr[i][1]);
-                } else if constexpr (RN == 8) {
-                    st.o[i][r] = make_float2(pr[i][r], pr[i][2 + r]);
                 } else {
                     st.o[i][r] = make_float2(pr[i][4 * (r / 2) + r % 2], pr[i][4 * (r / 2) + 2 + r % 2]);
                 }
@@ -729,7 +743,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm<DH, RN>()) quant_attn_ke
                             st.o[i][r] = make_float2(__int_as_float(0x7FC00000), __int_as_float(0x7FC00000));
             }
         }
-        return aborted;
+        return bad;
     };
 
     // records: m, l and the element pairs of this thread's rows
@@ -746,7 +760,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm<DH, RN>()) quant_attn_ke
             }
 #pragma unroll
             for (int i = 0; i < NP; ++i)
-                __stcg(reinterpret_cast<float2 *>(rec + rec_hdr + (int64_t)row * DH) + state_pair(i), st.o[i][r]);
+                __stcg(reinterpret_cast<float2 *>(rec + (rec_hdr + (uint32_t)(row * DH + 2 * state_pair(i)))), st.o[i][r]);
         }
     };
     // st = the fold of n records, one after another from `recs`
@@ -758,7 +772,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm<DH, RN>()) quant_attn_ke
             St x[U];
 #pragma unroll
             for (int u = 0; u < U; ++u) {
-                const float *rec = recs + min(k0 + u, n - 1) * rec_size;
+                const float *rec = recs + (uint32_t)min(k0 + u, n - 1) * rec_size;
 #pragma unroll
                 for (int r = 0; r < NR; ++r) {
                     const int row = min(state_row(r), rv - 1);
@@ -766,7 +780,8 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm<DH, RN>()) quant_attn_ke
                     x[u].l[r] = __ldcg(rec + p.rows + row);
 #pragma unroll
                     for (int i = 0; i < NP; ++i)
-                        x[u].o[i][r] = __ldcg(reinterpret_cast<const float2 *>(rec + rec_hdr + (int64_t)row * DH) + state_pair(i));
+                        x[u].o[i][r] =
+                            __ldcg(reinterpret_cast<const float2 *>(rec + (rec_hdr + (uint32_t)(row * DH + 2 * state_pair(i)))));
                 }
             }
 #pragma unroll
@@ -785,10 +800,10 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm<DH, RN>()) quant_attn_ke
             const bool last = old == (uint32_t)(n - 1);
             if (last)
                 *counter = 0u;  // ready for the next call
-            s_flags[1] = last;
+            s_flags[0] = last;
         }
         __syncthreads();
-        return s_flags[1] != 0;
+        return s_flags[0] != 0;
     };
     auto write_output = [&](const St &st, int rv) {
 #pragma unroll
@@ -866,26 +881,15 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm<DH, RN>()) quant_attn_ke
             span.clear();
             if (!span_whole) {
                 const int64_t first = sa >= lo ? (int64_t)blockIdx.x : cta_of(sa);
-                span_area = p.chunk_records + first * p.slots * rec_size;
+                span_area = p.chunk_records + first * p.slots * (int64_t)rec_size;
                 span_ctas = (int)((sb <= hi ? (int64_t)blockIdx.x : cta_of(sb - 1)) - first) + 1;
             }
         }
 
-        const int stg = step % kStages;
-        wait_bar(smem_addr(s_bars + stg), (step / kStages) & 1, s_flags, p.err, stg);
-        const uint8_t *stage = smem + stg * stage_bytes<DH>();
-        const bool bad = s_bad[stg] == step + 1;
+        wait_copies();  // this chunk's K
         St st;
         const bool masked = c.lc * kChunk + kChunk > c.L - c.qn + 1;
-        const bool aborted = masked ? chunk_state(std::true_type{}, stage, step & 1, st)
-                                    : chunk_state(std::false_type{}, stage, step & 1, st);
-        if (aborted) {
-            // a wait ran out of time: let the copies in flight land, give up
-            for (int k = step + 1; k < copied; ++k)
-                wait_bar_drain(smem_addr(s_bars + k % kStages), (k / kStages) & 1);
-            return;
-        }
-        copy_next();  // every warp is past barrier C: the stage is free
+        const bool bad = masked ? chunk_state(std::true_type{}, step, st) : chunk_state(std::false_type{}, step, st);
 #pragma unroll
         for (int r = 0; r < NR; ++r) {
             if (bad)
@@ -898,7 +902,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm<DH, RN>()) quant_attn_ke
         if (span_whole)
             span.fold(st);
         else
-            write_record(span_area + (c.lc % kSpan) * rec_size, st, rv);
+            write_record(span_area + (uint32_t)(c.lc % kSpan) * rec_size, st, rv);
         const bool span_end = c.lc + 1 == c.nch || (c.lc + 1) % kSpan == 0;
         if (!span_end && !last_chunk)
             continue;
@@ -918,8 +922,8 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm<DH, RN>()) quant_attn_ke
             if (sp + 1 == nsp)
                 write_output(group, rv);
         } else {
-            float *recs = p.span_records + grp * p.spans * rec_size;
-            write_record(recs + sp * rec_size, span, rv);
+            float *recs = p.span_records + grp * p.spans * (int64_t)rec_size;
+            write_record(recs + (int64_t)sp * rec_size, span, rv);
             if (last_to_arrive(p.group_counters + grp, nsp)) {
                 fold_records(group, recs, nsp, rv);
                 write_output(group, rv);
@@ -940,7 +944,7 @@ static int rows_capacity(int rows) { return rows <= 4 ? 4 : rows <= 8 ? 8 : rows
 // CTAs of the grid: one wave, fewer when there are fewer chunks.
 static int64_t grid_of(int dh, int rn, int64_t max_chunks)
 {
-    const int64_t wave = (int64_t)kGridSms * (dh == 128 && rn <= 16 ? 2 : 1);
+    const int64_t wave = (int64_t)kGridSms * (dh == 128 && rn <= 8 ? 2 : 1);
     return max_chunks < 1 ? 1 : (max_chunks < wave ? max_chunks : wave);
 }
 
@@ -957,7 +961,7 @@ static int slots_of(int dh, int32_t len)
 template <int DH, int RN>
 cudaError_t launch(const Params &p, cudaStream_t stream, int64_t grid)
 {
-    static_assert(ctas_per_sm<DH, RN>() == (DH == 128 && RN <= 16 ? 2 : 1), "grid_of");
+    static_assert(ctas_per_sm<DH, RN>() == (DH == 128 && RN <= 8 ? 2 : 1), "grid_of");
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)grid);
     cfg.blockDim = dim3(kThreads);
@@ -991,8 +995,8 @@ cudaError_t launch_quant_attention(const QuantAttnArgs &a, ErrState *err, cudaSt
     qa::Params p{};
     p.k = a.pool.k;
     p.v = a.pool.v;
-    p.block_stride = a.pool.block_stride;
-    p.head_stride = a.pool.head_stride;
+    p.block_stride = (uint32_t)a.pool.block_stride;
+    p.head_stride = (uint32_t)a.pool.head_stride;
     p.num_blocks = a.pool.num_blocks;
     p.q = static_cast<const __nv_bfloat16 *>(a.q);
     p.q_tok_stride = a.q_tok_stride;
