@@ -18,13 +18,12 @@
 // the largest); p is scaled by 2^15 (11 bits down to 2^-29 of the row's largest
 // probability).
 //   S^T = K.Q^T: M = the 16 tokens of a page, N = 8 query rows, K = head dim.
-//   O^T = V^T.P^T: a V byte holds two neighbouring elements (d, d+1) of one
-//     token, so a converted register is a pair of different M rows.  Up to
-//     four rows (PAR) the pair is taken as one row with two K indices (token,
-//     parity), and P^T has two columns per query row: (p, 0) gives element d,
-//     (0, p) element d+1.  That fills N = 8 and needs no permutes.  With more
-//     rows the pairs are regrouped by element with eight permutes per page,
-//     which costs less than twice the products.
+//   O^T = V^T.P^T: M = the head dim, N = 8 query rows, K = the 16 tokens.  A V
+//     byte holds two neighbouring elements of one token; permutes regroup the
+//     converted pairs by element, and the scales come as pairs of tokens.
+//     (Taking the pair as two K indices instead, with (p, 0) and (0, p) as
+//     columns of P, saves the permutes but needs each scale twice: 56 clocks of
+//     shared-memory reads per page against 32.)
 //
 // Fixed arithmetic (a row's results do not depend on the batch or the grid):
 //   chunks of 512 keys (256 at head dim 256, 128 at 512) from key 0, each with its own exact maximum; a chunk's
@@ -36,12 +35,12 @@
 // exchanged (barrier); P goes to shared memory in fragment order, the V scales
 // as one f16 pair each (barrier); each warp multiplies P by 32
 // head-dim elements of the pages (at head dim 128 of half of the pages, the
-// halves are added through shared memory, with the row sums; barrier).  Each
-// warp copies its pages of the next chunk (cp.async): K during the second
-// product, V during the first one.  The chunks of all (request, KV head) groups are dealt out as
+// halves are added through shared memory, with the row sums; barrier).  A
+// ninth warp copies the next chunk (cp.async.bulk): K during the second product,
+// V during the first one.  The chunks of all (request, KV head) groups are dealt out as
 // equal contiguous ranges.  A span inside one range is folded in registers; the
 // chunks of a span cut by a range end become records, folded by the last CTA
-// to arrive; so do the spans of a cut group.  No CTA waits for another.
+// to arrive, and so do the spans of a group of several.  No CTA waits for another.
 #include <cstdio>
 #include <type_traits>
 
@@ -54,8 +53,9 @@ namespace pa {
 
 namespace qa {
 
-constexpr int kWarps = 8;
-constexpr int kThreads = 32 * kWarps;
+constexpr int kWarps = 8;                   // computing warps
+constexpr int kThreads = 32 * kWarps;       // computing threads
+constexpr int kAllThreads = kThreads + 32;  // and the copying warp
 // pages per warp of a chunk: as many as shared memory holds (at head dim 128
 // for two CTAs), since a chunk's exchanges and bookkeeping cost the same
 __host__ __device__ constexpr int pages_per_warp(int dh) { return dh == 128 ? 4 : dh == 256 ? 2 : 1; }
@@ -68,21 +68,16 @@ constexpr int kGridSms = 152;       // SMs the grid is sized for
 // CTAs per SM that registers and shared memory are sized for
 template <int DH, int RN>
 constexpr int ctas_per_sm() { return DH == 128 && RN <= 8 ? 2 : 1; }
-// up to four rows: element parity as a K index (see above)
-template <int RN>
-constexpr bool par_mode() { return RN == 4; }
-
-// Shared-memory layout in bytes.  RN: query rows (4, 8, 16 or 32).
+// Shared-memory layout in bytes.  RN: query rows (8, 16 or 32).
 template <int DH, int RN>
 struct Layout {
     static constexpr int kPages = chunk_pages(DH);
-    static constexpr int NQ = RN < 8 ? 1 : RN / 8;                  // N tiles of the first product
-    static constexpr int PV4 = RN == 4 ? 4 : 2 * NQ;  // 32-bit registers of a page's P fragments
+    static constexpr int NQ = RN / 8;                               // N tiles
     static constexpr int NCF = DH == 128 ? RN / 2 : 0;              // floats a thread hands to the other half
     static constexpr int q = 2 * kPages * quant_record_bytes(DH);  // after the K and the V records
     static constexpr int p = q + NQ * DH * 16;
-    static constexpr int spread = p + kPages * PV4 * 128;           // V scales as f16 pairs
-    static constexpr int half = spread + kPages * DH * 4;
+    static constexpr int spread = p + kPages * NQ * 256;            // V scales as f16
+    static constexpr int half = spread + kPages * DH * 2;
     static constexpr int max = half + kThreads * NCF * 4;
     static constexpr int sum = max + NQ * 8 * kWarps * 4;
     static constexpr int cq = sum + NQ * 8 * kWarps * 4;
@@ -90,9 +85,10 @@ struct Layout {
     static constexpr int nan = lim + NQ * 8 * 4;
     static constexpr int bad = nan + 2 * (DH / 16) * 4;
     static constexpr int flags = bad + 16;
-    static constexpr int sums = flags + 16;
-    static constexpr int pre = sums + kWarps * 8;  // [num_seqs + 1] int32
-    static_assert(q % 16 == 0 && spread % 16 == 0 && max % 16 == 0 && bad % 8 == 0 && sums % 8 == 0, "layout");
+    static constexpr int bars = flags + 16;         // full and empty, of K and of V
+    static constexpr int sums = bars + 32;
+    static constexpr int pre = sums + (kWarps + 2) * 8;  // [num_seqs + 1] int32
+    static_assert(q % 16 == 0 && spread % 16 == 0 && max % 16 == 0 && bad % 8 == 0 && bars % 8 == 0, "layout");
     static_assert(pre + (kScanMaxSeqs + 1) * 4 <= (int)kMaxSmemPerBlock, "shared memory");
     static size_t bytes(int num_seqs) { return (size_t)pre + 4 * ((size_t)num_seqs + 1); }
 };
@@ -143,9 +139,11 @@ __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi)
     return r;
 }
 
-__device__ __forceinline__ void copy16(uint32_t dst, const void *src, uint64_t policy)
+__device__ __forceinline__ void bulk_copy(uint32_t dst, const void *src, uint32_t bytes, uint32_t bar, uint64_t policy)
 {
-    asm volatile("cp.async.cg.shared.global.L2::cache_hint [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "l"(policy)
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint [%0], [%1], %2, [%3], "
+                 "%4;" ::"r"(dst),
+                 "l"(src), "r"(bytes), "r"(bar), "l"(policy)
                  : "memory");
 }
 
@@ -256,28 +254,26 @@ struct State {
 };
 
 template <int DH, int RN>
-__global__ void __launch_bounds__(kThreads, ctas_per_sm<DH, RN>()) quant_attn_kernel(const Params p)
+__global__ void __launch_bounds__(kAllThreads, ctas_per_sm<DH, RN>()) quant_attn_kernel(const Params p)
 {
     using Lay = Layout<DH, RN>;
-    constexpr bool PAR = par_mode<RN>();
     constexpr int NQ = Lay::NQ;
-    constexpr int PV4 = Lay::PV4;
     constexpr int PPW = pages_per_warp(DH), kPages = chunk_pages(DH), kChunk = chunk_keys(DH);
     constexpr int NB = DH / 128;            // 128-element blocks of the head dim
     constexpr int NE = DH <= 256 ? 1 : 2;   // 32-element blocks of a warp
     constexpr bool HALVES = DH == 128;      // warps 4-7 take the other half of the pages
-    constexpr int NR = RN == 4 ? 1 : RN / 4;  // rows of a thread's state
+    constexpr int NR = RN / 4;  // rows of a thread's state
     constexpr int NP = HALVES ? 1 : 2 * NE;   // element pairs of a thread's state
     constexpr int REC = quant_record_bytes(DH), CODES = quant_code_bytes(DH);
     constexpr bool kQRegs = NQ * DH <= 256;  // Q fragments in registers (else read from shared memory)
-    constexpr int OT = PAR ? 1 : 2 * NQ;  // accumulator tiles of a 32-element block
+    constexpr int OT = 2 * NQ;              // accumulator tiles of a 32-element block
     using St = State<NR, NP>;
     griddep_wait();
     griddep_launch_dependents();
     extern __shared__ __align__(128) uint8_t smem[];
     uint2 *const s_q = reinterpret_cast<uint2 *>(smem + Lay::q);        // [NQ][DH/16][32]
-    uint32_t *const s_p = reinterpret_cast<uint32_t *>(smem + Lay::p);  // [16 pages][PV4/2 or /4][32 lanes][2 or 4]
-    uint4 *const s_spread = reinterpret_cast<uint4 *>(smem + Lay::spread);  // [16 pages][DH/16][4] x 4 tokens
+    uint2 *const s_p = reinterpret_cast<uint2 *>(smem + Lay::p);            // [pages][NQ][32]
+    uint2 *const s_spread = reinterpret_cast<uint2 *>(smem + Lay::spread);  // [pages][DH/16][4] x 4 tokens
     float *const s_half = reinterpret_cast<float *>(smem + Lay::half);
     float *const s_max = reinterpret_cast<float *>(smem + Lay::max);  // [rows][8 warps]
     float *const s_sum = reinterpret_cast<float *>(smem + Lay::sum);  // [rows][8 warps]
@@ -285,17 +281,25 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm<DH, RN>()) quant_attn_ke
     int *const s_lim = reinterpret_cast<int *>(smem + Lay::lim);      // last key of a row
     int *const s_nan = reinterpret_cast<int *>(smem + Lay::nan);      // [chunk parity][DH/16] first NaN key of an element block
     volatile int *const s_bad = reinterpret_cast<int *>(smem + Lay::bad);  // [chunk parity] 1 + the last chunk with a bad block id
-    volatile int *const s_flags = reinterpret_cast<int *>(smem + Lay::flags);  // [0] last to arrive
+    volatile int *const s_flags = reinterpret_cast<int *>(smem + Lay::flags);  // [0] abort [1] last to arrive
     int32_t *const s_pre = reinterpret_cast<int32_t *>(smem + Lay::pre);
     const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32, g = lane / 4, t = lane % 4;
     const int G = p.group, hkv = p.hkv;
+    enum { kFullK, kFullV, kEmptyK, kEmptyV };
+    auto bar = [&](int i) { return smem_addr(smem + Lay::bars + 8 * i); };
+    auto wait = [&](int i, int parity) { return wait_bar(bar(i), parity, s_flags, p.err, i); };
 
     // the work: chunks of the valid requests
     if (tid < 2 * (DH / 16))
         s_nan[tid] = 0x7fffffff;
-    if (tid < 2)
-        s_bad[tid] = 0;
-    const long long tot = block_exclusive_sums<kThreads>(
+    if (tid == 0) {
+        for (int i = 0; i < 4; ++i)
+            mbar_init(bar(i), 1);
+        s_flags[0] = 0;
+        s_bad[0] = s_bad[1] = 0;
+        fence_barrier_init();
+    }
+    const long long tot = block_exclusive_sums<kAllThreads>(
         p.num_seqs, s_pre, reinterpret_cast<long long *>(smem + Lay::sums), [&](int b) {
             const Meta m = meta_of(p, b);
             if (!m.ok && blockIdx.x == 0)
@@ -308,10 +312,10 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm<DH, RN>()) quant_attn_ke
         const Meta m = meta_of(p, b);
         if (m.sane && !m.ok) {  // bad lengths: NaN rows
             const int64_t first = (int64_t)m.qs * p.hq, n = (int64_t)m.qn * p.hq;
-            for (int64_t i = tid; i < n * DH; i += kThreads)
+            for (int64_t i = tid; i < n * DH; i += kAllThreads)
                 p.out[first * DH + i] = __ushort_as_bfloat16(0x7FC0);
             if (p.lse)
-                for (int64_t i = tid; i < n; i += kThreads)
+                for (int64_t i = tid; i < n; i += kAllThreads)
                     p.lse[first + i] = __int_as_float(0x7FC00000);
         }
     }
@@ -323,93 +327,93 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm<DH, RN>()) quant_attn_ke
     auto cta_of = [&](int64_t x) { return div_floor((x + 1) * ctas + T - 1, T) - 1; };
     const int64_t lo = range_start(blockIdx.x), hi = range_start((int64_t)blockIdx.x + 1);
 
-    // Copies: every warp its pages of a chunk, 16 bytes a lane and step, the K
-    // records while the chunk before is past its first product, the V records
-    // when that is past its second; the block ids are loaded a chunk ahead.
-    // A warp scores and spreads what it copied itself, and the other warps read
-    // its V codes after barrier B: waiting for the own copies is all the
-    // synchronisation they need.  (Bulk copies, four a warp, took 600 clocks of
-    // every chunk to issue.)
-    const uint64_t policy = l2_policy_evict_first();
     const int chunks = (int)(hi - lo);
-    const int64_t v_delta = p.v - p.k;
-    const uint32_t nblocks = (uint32_t)min(p.num_blocks, (int64_t)0x7fffffff + 1);
-    Chunk<DH> pc;
-    pc.at(p, s_pre, lo);
-    int copied = 0;  // the chunk pc stands at
-    int id[PPW];
-    auto load_ids = [&]() {
+    if (warp == kWarps) {
+        // The copying warp: a lane per page, the K records of a chunk when the
+        // one before is past its first product, the V records when it is past
+        // its second; the block ids are loaded a chunk ahead.  (Copies issued
+        // by the computing warps held them up: 600 clocks of every 256 keys as
+        // bulk copies, 1700 of every 512 as 16-byte cp.async.)
+        static_assert(kPages <= 32, "one lane per page");
+        const uint64_t policy = l2_policy_evict_first();
+        const uint32_t dst = smem_addr(smem) + lane * REC;
+        Chunk<DH> c;
+        c.at(p, s_pre, lo);
+        int id = lane < kPages ? c.id(lane) : 0;
+        bool ok = true;
+        for (int k = 0; k < chunks; ++k) {
+            const bool exists = lane < kPages && c.has_page(lane);
+            const bool go = exists && id >= 0 && (int64_t)id < p.num_blocks;
+            const int n = __popc(__ballot_sync(0xffffffffu, go));
+            const uint64_t off = (uint64_t)(uint32_t)id * p.block_stride + (uint64_t)(uint32_t)c.kvh * p.head_stride;
+            const int b = c.b;
+            const bool any_bad = __any_sync(0xffffffffu, exists && !go);
+            if (k + 1 < chunks) {
+                c.next(p, s_pre);
+                id = lane < kPages ? c.id(lane) : 0;
+            }
 #pragma unroll
-        for (int j = 0; j < PPW; ++j)
-            id[j] = pc.id(PPW * warp + j);
-    };
-    load_ids();
-    auto copy = [&](auto is_v) {
-        constexpr int V = decltype(is_v)::value;
-        if (copied < chunks) {
-            constexpr int UN = REC / 16;  // 16-byte units of a record
-            const uint8_t *src[PPW];
-            bool go[PPW];
-            const uint8_t *const base = p.k + (V ? v_delta : 0) + ((uint64_t)(uint32_t)pc.kvh * p.head_stride + 16 * lane);
-#pragma unroll
-            for (int j = 0; j < PPW; ++j) {
-                const bool exists = pc.has_page(PPW * warp + j);
-                go[j] = exists && (uint32_t)id[j] < nblocks;
-                if (!V && exists && !go[j] && lane == 0) {
-                    s_bad[copied & 1] = copied + 1;
-                    record_error(p.err, kErrBadMetadata, pc.b);
+            for (int v = 0; v < 2; ++v) {
+                if (k > 0 && ok)
+                    ok = wait(v ? kEmptyV : kEmptyK, (k - 1) & 1);
+                ok = __all_sync(0xffffffffu, ok);
+                if (!ok)
+                    break;
+                if (lane == 0) {
+                    if (v == 0 && any_bad) {
+                        s_bad[k & 1] = k + 1;
+                        record_error(p.err, kErrBadMetadata, b);
+                    }
+                    if (n)
+                        mbar_arrive_expect_tx(bar(v ? kFullV : kFullK), n * REC);
+                    else
+                        mbar_arrive(bar(v ? kFullV : kFullK));
                 }
-                src[j] = base + (uint64_t)(uint32_t)id[j] * p.block_stride;
+                __syncwarp();
+                if (go)
+                    bulk_copy(dst + v * kPages * REC, (v ? p.v : p.k) + off, REC, bar(v ? kFullV : kFullK), policy);
             }
-            const uint32_t dst = smem_addr(smem + (V * kPages + PPW * warp) * REC) + 16 * lane;
-#pragma unroll
-            for (int i = 0; i < (PPW * UN + 31) / 32; ++i) {
-                // unit lane + 32i: of record r0, or past its end of r1
-                const int r0 = 32 * i / UN, r1 = (32 * i + 31) / UN;
-                const bool next = r1 != r0 && lane >= UN * r1 - 32 * i;
-                const bool end = next && r1 >= PPW;
-                const int rn = r1 >= PPW ? PPW - 1 : r1;
-                if ((next ? go[rn] : go[r0]) && !end)
-                    copy16(dst + 512 * i, (next ? src[rn] - rn * REC : src[r0] - r0 * REC) + 512 * i, policy);
+            if (!ok) {
+                // gave up (here or elsewhere in the CTA): let the copies in flight land
+                wait_bar_drain(bar(kFullK), k > 0 ? (k - 1) & 1 : 1);
+                wait_bar_drain(bar(kFullK), k & 1);
+                wait_bar_drain(bar(kFullV), k > 0 ? (k - 1) & 1 : 1);
+                return;
             }
         }
-        asm volatile("cp.async.commit_group;" ::: "memory");
-        if (V && copied < chunks && ++copied < chunks) {
-            pc.next(p, s_pre);
-            load_ids();
-        }
-    };
-    // all own copies but the last group have landed
-    auto wait_copies = [&]() {
-        asm volatile("cp.async.wait_group 1;" ::: "memory");
-        __syncwarp();
-    };
-    copy(std::integral_constant<int, 0>{});
-    copy(std::integral_constant<int, 1>{});
+        return;
+    }
+    auto sync = [&]() { named_sync(1, kThreads); };  // the computing warps
 
     // this thread's place in the second product: element pairs c0 = 16*wd + g
     // and c0 + 8 of each 32-element block
     const int wd = HALVES ? warp % 4 : warp;
     const int token0 = 4 * (g >> 1) + (g & 1);  // token of fragment row g; row g + 8 is token0 + 2
     // rows of a thread's scores (columns of S^T) and of its state
-    auto score_row = [&](int n, int i) { return RN == 4 ? (2 * t + i) & 3 : 8 * n + 2 * t + i; };
-    auto state_row = [&](int r) { return RN == 4 ? 2 * (t & 1) + (t >> 1) : 8 * (r / 2) + 2 * t + r % 2; };
+    auto score_row = [&](int n, int i) { return 8 * n + 2 * t + i; };
+    auto state_row = [&](int r) { return 8 * (r / 2) + 2 * t + r % 2; };
     // state pair i: its index among the DH/2 pairs
     auto state_pair = [&](int i) { return HALVES ? 16 * wd + 8 * (warp / 4) + g : 16 * (NE * wd + i / 2) + 8 * (i % 2) + g; };
 
-    uint2 qf[kQRegs ? NQ * (DH / 16) : 1];
     Chunk<DH> c;
     c.at(p, s_pre, lo);
-    St span, group;
+    St span;  // the span so far
     const uint32_t rec_hdr = (uint32_t)part_header_floats(p.rows), rec_size = (uint32_t)part_record_floats(p.rows, DH);
 
     // ------------------------------------------------ one chunk's state --
-    auto chunk_state = [&](auto masked_tag, int step, St &st) -> bool {
+    auto chunk_state = [&](auto masked_tag, int step, St &st) -> int {
         const int parity = step & 1;
         const uint8_t *const stage = smem;
         constexpr bool MASKED = decltype(masked_tag)::value;  // some row does not see some key of the chunk
         const int key0 = c.lc * kChunk;
         const int npages = MASKED ? min(kPages, (c.L - key0 + 15) / 16) : kPages;
+        uint2 qf[kQRegs ? NQ * (DH / 16) : 1];
+        if constexpr (kQRegs) {
+#pragma unroll
+            for (int i = 0; i < NQ * (DH / 16); ++i)
+                qf[i] = s_q[i * 32 + lane];
+        }
+        wait(kFullK, parity);
         // two accumulators per tile, for the even and the odd steps: one
         // chain of dependent products is latency bound
         float s[PPW][NQ][4];
@@ -498,15 +502,17 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm<DH, RN>()) quant_attn_ke
 #pragma unroll
                 for (int w = 4; w < 32; w <<= 1)
                     x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, w));
-                if (g == 0 && (RN > 4 || t < 2))
+                if (g == 0)
                     s_max[score_row(n, i) * kWarps + warp] = x;
             }
-        __syncthreads();  // A: maxima written; K is consumed
-        const bool bad = s_bad[parity] == step + 1;
+        sync();  // A: maxima written; K is consumed
+        // read between A and B, so that every thread reads the same
+        const int bad = s_flags[0] ? -1 : s_bad[parity] == step + 1;
         if (tid < DH / 16)
             s_nan[(parity ^ 1) * (DH / 16) + tid] = 0x7fffffff;  // for the next chunk
-        copy(std::integral_constant<int, 0>{});  // the next chunk's K
-        wait_copies();                           // this chunk's V
+        if (tid == 0)
+            mbar_arrive(bar(kEmptyK));
+        wait(kFullV, parity);
 #pragma unroll
         for (int j = 0; j < PPW; ++j) {
             const int page = PPW * warp + j;
@@ -516,9 +522,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm<DH, RN>()) quant_attn_ke
 #pragma unroll
             for (int b = 0; b < NB; ++b) {
                 const uint32_t w = reinterpret_cast<const uint32_t *>(stage + (kPages + page) * REC + CODES)[32 * b + lane];
-                const uint32_t s01 = e4m3x2_to_f16x2(w), s23 = e4m3x2_to_f16x2(w >> 16);
-                uint32_t f[4] = {__byte_perm(s01, 0u, 0x1010), __byte_perm(s01, 0u, 0x3232), __byte_perm(s23, 0u, 0x1010),
-                                 __byte_perm(s23, 0u, 0x3232)};
+                uint32_t s01 = e4m3x2_to_f16x2(w), s23 = e4m3x2_to_f16x2(w >> 16);
                 if (MASKED) {
                     // tokens no row sees count as zero whatever their bytes; a
                     // NaN that only some rows see is given to those rows below
@@ -527,13 +531,13 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm<DH, RN>()) quant_attn_ke
                         const int key = key0 + 16 * page + 4 * t + i;
                         const bool gone = key >= c.L, nan = ((w >> (8 * i)) & 0x7fu) == 0x7fu;
                         if (gone || (nan && key > c.L - c.qn)) {
-                            f[i] = 0u;
+                            (i < 2 ? s01 : s23) &= i % 2 ? 0x0000ffffu : 0xffff0000u;
                             if (!gone)
                                 atomicMin(s_nan + parity * (DH / 16) + 8 * b + g, key);
                         }
                     }
                 }
-                s_spread[(page * (DH / 16) + 8 * b + g) * 4 + t] = make_uint4(f[0], f[1], f[2], f[3]);
+                s_spread[(page * (DH / 16) + 8 * b + g) * 4 + t] = make_uint2(s01, s23);
             }
         }
         float l[NQ][2], mrow[NQ][2];
@@ -565,113 +569,56 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm<DH, RN>()) quant_attn_ke
             for (int j = 0; j < PPW; ++j) {
                 const int page = PPW * warp + j;
                 const uint32_t x = movmatrix(pack_f16x2(pr[j][0], pr[j][1])), y = movmatrix(pack_f16x2(pr[j][2], pr[j][3]));
-                if constexpr (RN == 4) {
-                    // columns 0-3 give the even elements, 4-7 (the same rows) the odd ones
-                    const uint32_t a = g < 4 ? 0x4410u : 0x1044u, b = g < 4 ? 0x4432u : 0x3244u;
-                    reinterpret_cast<uint4 *>(s_p)[page * 32 + lane] =
-                        make_uint4(__byte_perm(x, 0u, a), __byte_perm(x, 0u, b), __byte_perm(y, 0u, a), __byte_perm(y, 0u, b));
-                } else {
-                    reinterpret_cast<uint2 *>(s_p)[(page * NQ + n) * 32 + lane] = make_uint2(x, y);
-                }
+                s_p[(page * NQ + n) * 32 + lane] = make_uint2(x, y);
             }
         }
-        __syncthreads();  // B: P and scales written, V visible
-        float o[NE][OT][4], acc[2][NE][OT][4];  // for the even and the odd pages, as above
+        sync();  // B: P and scales written, V visible
+        float o[NE][OT][4];
 #pragma unroll
         for (int e = 0; e < NE; ++e)
 #pragma unroll
             for (int n = 0; n < OT; ++n)
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
-#pragma unroll
-                    for (int k = 0; k < 2; ++k)
-                        acc[k][e][n][i] = 0.f;
+                    o[e][n][i] = 0.f;
         const int first = HALVES ? warp / 4 * (kPages / 2) : 0;
         const int last = HALVES ? min(npages, first + kPages / 2) : npages;
-        auto page_product = [&](int page, auto parity_tag) {
-            constexpr int h = decltype(parity_tag)::value;
+        auto page_product = [&](int page) {
             const uint8_t *vr = stage + (kPages + page) * REC + (16 * NE * wd + g) * 16 + 4 * t;
-            uint32_t pf[PV4];
-            if constexpr (PAR) {
+            uint2 pf[NQ];
 #pragma unroll
-                for (int i = 0; i < PV4 / 4; ++i) {
-                    const uint4 v = reinterpret_cast<const uint4 *>(s_p)[(page * (PV4 / 4) + i) * 32 + lane];
-                    pf[4 * i] = v.x;
-                    pf[4 * i + 1] = v.y;
-                    pf[4 * i + 2] = v.z;
-                    pf[4 * i + 3] = v.w;
-                }
-            } else {
-#pragma unroll
-                for (int n = 0; n < NQ; ++n) {
-                    const uint2 v = reinterpret_cast<const uint2 *>(s_p)[(page * NQ + n) * 32 + lane];
-                    pf[2 * n] = v.x;
-                    pf[2 * n + 1] = v.y;
-                }
-            }
+            for (int n = 0; n < NQ; ++n)
+                pf[n] = s_p[(page * NQ + n) * 32 + lane];
 #pragma unroll
             for (int e = 0; e < NE; ++e) {
-                // pairs c0 (block 2*(NE*wd + e)) and c0 + 8 (the next block), tokens 4t..4t+3
-                const uint32_t w0 = *reinterpret_cast<const uint32_t *>(vr + e * 256);
-                const uint32_t w1 = *reinterpret_cast<const uint32_t *>(vr + e * 256 + 128);
-                const uint4 f0 = s_spread[(page * (DH / 16) + 2 * (NE * wd + e)) * 4 + t];
-                const uint4 f1 = s_spread[(page * (DH / 16) + 2 * (NE * wd + e) + 1) * 4 + t];
-                uint32_t x[4], y[4];
-                e2m1x8_to_f16x2(w0, x);
-                e2m1x8_to_f16x2(w1, y);
-                x[0] = mul_f16x2(x[0], f0.x);
-                x[1] = mul_f16x2(x[1], f0.y);
-                x[2] = mul_f16x2(x[2], f0.z);
-                x[3] = mul_f16x2(x[3], f0.w);
-                y[0] = mul_f16x2(y[0], f1.x);
-                y[1] = mul_f16x2(y[1], f1.y);
-                y[2] = mul_f16x2(y[2], f1.z);
-                y[3] = mul_f16x2(y[3], f1.w);
-                if constexpr (PAR) {
-                    // rows c0, c0 + 8; K: tokens 4t, 4t+1, then 4t+2, 4t+3, each (even, odd)
+                // pairs c0 (element block 2*(NE*wd + e)) and c0 + 8 (the next block), tokens 4t..4t+3
 #pragma unroll
-                    for (int n = 0; n < OT; ++n) {
-                        mma_f16(acc[h][e][n], x[0], y[0], x[1], y[1], pf[4 * n], pf[4 * n + 1]);
-                        mma_f16(acc[h][e][n], x[2], y[2], x[3], y[3], pf[4 * n + 2], pf[4 * n + 3]);
-                    }
-                } else {
-                    // tile 2n: rows are the even, then the odd elements of the pairs c0, tile 2n+1: of c0 + 8
-                    const uint32_t x0 = __byte_perm(x[0], x[1], 0x5410), x1 = __byte_perm(x[0], x[1], 0x7632);
-                    const uint32_t x2 = __byte_perm(x[2], x[3], 0x5410), x3 = __byte_perm(x[2], x[3], 0x7632);
-                    const uint32_t y0 = __byte_perm(y[0], y[1], 0x5410), y1 = __byte_perm(y[0], y[1], 0x7632);
-                    const uint32_t y2 = __byte_perm(y[2], y[3], 0x5410), y3 = __byte_perm(y[2], y[3], 0x7632);
+                for (int h = 0; h < 2; ++h) {
+                    const uint32_t w = *reinterpret_cast<const uint32_t *>(vr + e * 256 + h * 128);
+                    const uint2 f = s_spread[(page * (DH / 16) + 2 * (NE * wd + e) + h) * 4 + t];
+                    uint32_t x[4];
+                    e2m1x8_to_f16x2(w, x);  // token 4t + i: (even, odd) element
+                    const uint32_t a0 = mul_f16x2(__byte_perm(x[0], x[1], 0x5410), f.x);  // even, tokens 4t, 4t+1
+                    const uint32_t a1 = mul_f16x2(__byte_perm(x[0], x[1], 0x7632), f.x);  // odd
+                    const uint32_t a2 = mul_f16x2(__byte_perm(x[2], x[3], 0x5410), f.y);  // even, tokens 4t+2, 4t+3
+                    const uint32_t a3 = mul_f16x2(__byte_perm(x[2], x[3], 0x7632), f.y);
 #pragma unroll
-                    for (int n = 0; n < NQ; ++n) {
-                        mma_f16(acc[h][e][2 * n], x0, x1, x2, x3, pf[2 * n], pf[2 * n + 1]);
-                        mma_f16(acc[h][e][2 * n + 1], y0, y1, y2, y3, pf[2 * n], pf[2 * n + 1]);
-                    }
+                    for (int n = 0; n < NQ; ++n)
+                        mma_f16(o[e][2 * n + h], a0, a1, a2, a3, pf[n].x, pf[n].y);
                 }
             }
         };
         if constexpr (MASKED) {
 #pragma unroll 1
-            for (int page = first; page < last; page += 2) {
-                page_product(page, std::integral_constant<int, 0>{});
-                if (page + 1 < last)
-                    page_product(page + 1, std::integral_constant<int, 1>{});
-            }
+            for (int page = first; page < last; ++page)
+                page_product(page);
         } else {
-#pragma unroll(RN <= 8 ? 2 : 1)
-            for (int i = 0; i < (HALVES ? kPages / 2 : kPages); i += 2) {
-                page_product(first + i, std::integral_constant<int, 0>{});
-                page_product(first + i + 1, std::integral_constant<int, 1>{});
-            }
+#pragma unroll(NQ * NE == 1 ? 4 : 2)
+            for (int i = 0; i < (HALVES ? kPages / 2 : kPages); ++i)
+                page_product(first + i);
         }
-#pragma unroll
-        for (int e = 0; e < NE; ++e)
-#pragma unroll
-            for (int n = 0; n < OT; ++n)
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    o[e][n][i] = acc[0][e][n][i] + acc[1][e][n][i];
         // accumulators by element pair: pr[i][k], i = 0 (c0) or 1 (c0 + 8) of
-        // each 32-element block, then for k the rows (and, at four rows, one
-        // parity: even for t < 2, odd for t >= 2)
+        // each 32-element block; k: N tile, parity, row
         constexpr int F = RN / 2;  // floats of a pair
         float pr[2 * NE][F];
 #pragma unroll
@@ -679,12 +626,8 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm<DH, RN>()) quant_attn_ke
 #pragma unroll
             for (int i = 0; i < 2; ++i)
 #pragma unroll
-                for (int k = 0; k < F; ++k) {
-                    if constexpr (RN == 4)
-                        pr[2 * e + i][k] = o[e][0][2 * i + k];
-                    else  // k: N tile, parity, row
-                        pr[2 * e + i][k] = o[e][2 * (k / 4) + i][k % 4];
-                }
+                for (int k = 0; k < F; ++k)
+                    pr[2 * e + i][k] = o[e][2 * (k / 4) + i][k % 4];
         // row sums over the warp's keys
 #pragma unroll
         for (int n = 0; n < NQ; ++n)
@@ -693,7 +636,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm<DH, RN>()) quant_attn_ke
 #pragma unroll
                 for (int w = 4; w < 32; w <<= 1)
                     l[n][i] += __shfl_xor_sync(0xffffffffu, l[n][i], w);
-                if (g == 0 && (RN > 4 || t < 2))
+                if (g == 0)
                     s_sum[score_row(n, i) * kWarps + warp] = l[n][i];
             }
         if constexpr (HALVES) {
@@ -704,8 +647,9 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm<DH, RN>()) quant_attn_ke
             for (int k = 0; k < F; ++k)
                 s_half[k * kThreads + (tid ^ 128)] = keep ? pr[0][k] : pr[1][k];
         }
-        __syncthreads();  // C: sums and halves written; V is consumed
-        copy(std::integral_constant<int, 1>{});  // the next chunk's V
+        sync();  // C: sums and halves written; V is consumed
+        if (tid == 0)
+            mbar_arrive(bar(kEmptyV));
         if constexpr (HALVES) {
             const int keep = warp / 4;
 #pragma unroll
@@ -717,20 +661,13 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm<DH, RN>()) quant_attn_ke
         // the thread's state: rows' maxima and sums, pairs of elements
 #pragma unroll
         for (int r = 0; r < NR; ++r) {
-            st.m[r] = RN == 4 ? (t < 2 ? mrow[0][0] : mrow[0][1]) : mrow[RN == 4 ? 0 : r / 2][r % 2];
+            st.m[r] = mrow[r / 2][r % 2];
             const float *ss = s_sum + state_row(r) * kWarps;
             const float4 u = *reinterpret_cast<const float4 *>(ss), v = *reinterpret_cast<const float4 *>(ss + 4);
             st.l[r] = ((u.x + u.y) + (u.z + u.w)) + ((v.x + v.y) + (v.z + v.w));
 #pragma unroll
-            for (int i = 0; i < NP; ++i) {
-                if constexpr (RN == 4) {
-                    // the other parity of the kept row from lane t ^ 2
-                    const float got = __shfl_xor_sync(0xffffffffu, t < 2 ? pr[i][1] : pr[i][0], 2);
-                    st.o[i][0] = t < 2 ? make_float2(pr[i][0], got) : make_float2(got, pr[i][1]);
-                } else {
-                    st.o[i][r] = make_float2(pr[i][4 * (r / 2) + r % 2], pr[i][4 * (r / 2) + 2 + r % 2]);
-                }
-            }
+            for (int i = 0; i < NP; ++i)
+                st.o[i][r] = make_float2(pr[i][4 * (r / 2) + r % 2], pr[i][4 * (r / 2) + 2 + r % 2]);
         }
         if constexpr (MASKED) {
 #pragma unroll
@@ -763,36 +700,35 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm<DH, RN>()) quant_attn_ke
                 __stcg(reinterpret_cast<float2 *>(rec + (rec_hdr + (uint32_t)(row * DH + 2 * state_pair(i)))), st.o[i][r]);
         }
     };
-    // st = the fold of n records, one after another from `recs`
-    auto fold_records = [&](St &st, const float *recs, int n, int rv) {
-        st.clear();
-        constexpr int W = NR * (2 + 2 * NP);                              // registers of a state
-        constexpr int U = W <= 4 ? 8 : W <= 12 ? 4 : W <= 24 ? 2 : 1;  // records in flight
-        for (int k0 = 0; k0 < n; k0 += U) {
-            St x[U];
+    // The fold of n records, one after another from `recs`, by all computing
+    // threads, one element pair of a valid row at a time: emit(row, pair, state).
+    auto fold_records = [&](const float *recs, int n, int rv, auto emit) {
+        for (int e = tid; e < rv * (DH / 2); e += kThreads) {
+            const int row = e / (DH / 2), pair = e % (DH / 2);
+            const float *const rm = recs + row, *const ro = recs + (rec_hdr + (uint32_t)(row * DH + 2 * pair));
+            State<1, 1> acc;
+            acc.clear();
+            constexpr int U = 8;  // records in flight
+            for (int k0 = 0; k0 < n; k0 += U) {
+                State<1, 1> x[U];
 #pragma unroll
-            for (int u = 0; u < U; ++u) {
-                const float *rec = recs + (uint32_t)min(k0 + u, n - 1) * rec_size;
-#pragma unroll
-                for (int r = 0; r < NR; ++r) {
-                    const int row = min(state_row(r), rv - 1);
-                    x[u].m[r] = __ldcg(rec + row);
-                    x[u].l[r] = __ldcg(rec + p.rows + row);
-#pragma unroll
-                    for (int i = 0; i < NP; ++i)
-                        x[u].o[i][r] =
-                            __ldcg(reinterpret_cast<const float2 *>(rec + (rec_hdr + (uint32_t)(row * DH + 2 * state_pair(i)))));
+                for (int u = 0; u < U; ++u) {
+                    const uint32_t at = (uint32_t)min(k0 + u, n - 1) * rec_size;
+                    x[u].m[0] = __ldcg(rm + at);
+                    x[u].l[0] = __ldcg(rm + at + p.rows);
+                    x[u].o[0][0] = __ldcg(reinterpret_cast<const float2 *>(ro + at));
                 }
-            }
 #pragma unroll
-            for (int u = 0; u < U; ++u)
-                if (k0 + u < n)
-                    st.fold(x[u]);
+                for (int u = 0; u < U; ++u)
+                    if (k0 + u < n)
+                        acc.fold(x[u]);
+            }
+            emit(row, pair, acc);
         }
     };
     // Arrival of this CTA, its records written; true in the last of `n` CTAs.
     auto last_to_arrive = [&](uint32_t *counter, int n) {
-        __syncthreads();
+        sync();
         if (tid == 0) {
             // releases this CTA's records and, for the last arrival, acquires the others'
             uint32_t old;
@@ -800,29 +736,23 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm<DH, RN>()) quant_attn_ke
             const bool last = old == (uint32_t)(n - 1);
             if (last)
                 *counter = 0u;  // ready for the next call
-            s_flags[0] = last;
+            s_flags[1] = last;
         }
-        __syncthreads();
-        return s_flags[0] != 0;
+        sync();
+        return s_flags[1] != 0;
     };
-    auto write_output = [&](const St &st, int rv) {
-#pragma unroll
-        for (int r = 0; r < NR; ++r) {
-            const int row = state_row(r);
-            if (row >= rv)
-                continue;
-            const int64_t at = (int64_t)(c.qs + row / G) * p.hq + c.kvh * G + row % G;
-            const float f = __frcp_rn(st.l[r]) * p.v_scale;
-#pragma unroll
-            for (int i = 0; i < NP; ++i)
-                reinterpret_cast<uint32_t *>(p.out + at * DH)[state_pair(i)] =
-                    pack_bf16x2(st.o[i][r].x * f, st.o[i][r].y * f);
-            if (pair_zero && p.lse)
-                p.lse[at] = lse_of(st.m[r], st.l[r] * 0x1p-15f);
-        }
+    auto output_pair = [&](int row, int pair, float2 o, float m, float l) {
+        const int64_t at = (int64_t)(c.qs + row / G) * p.hq + c.kvh * G + row % G;
+        const float f = __frcp_rn(l) * p.v_scale;
+        reinterpret_cast<uint32_t *>(p.out + at * DH)[pair] = pack_bf16x2(o.x * f, o.y * f);
+        if (pair == 0 && p.lse)
+            p.lse[at] = lse_of(m, l * 0x1p-15f);
+    };
+    auto output_folded = [&](int row, int pair, const State<1, 1> &x) {
+        output_pair(row, pair, x.o[0][0], x.m[0], x.l[0]);
     };
 
-    bool span_whole = false, group_whole = false;
+    bool span_whole = false;
     float *span_area = nullptr;      // the cut span's chunk records
     int span_ctas = 0;               // and the CTAs that write them
     for (int step = 0; step < chunks; ++step) {
@@ -832,12 +762,9 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm<DH, RN>()) quant_attn_ke
         if (first_chunk || c.lc == 0) {
             // a new group: its rows, scaled to [1, 2) by a power of two, in
             // fragment order (the previous group's readers are past a barrier)
-            const int64_t gs = lo + step - c.lc;  // the group's first chunk
-            group_whole = gs >= lo && gs + c.nch <= hi;
-            group.clear();
 #pragma unroll
             for (int k = 0; k < NQ; ++k) {
-                const int slot = 8 * k + warp, r = RN == 4 ? slot & 3 : slot;
+                const int slot = 8 * k + warp, r = slot;
                 const bool valid = r < c.qn * G;
                 const int tok = valid ? r / G : 0;
                 const uint2 *src = reinterpret_cast<const uint2 *>(p.q + (int64_t)(c.qs + tok) * p.q_tok_stride +
@@ -867,12 +794,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm<DH, RN>()) quant_attn_ke
                     s_lim[slot] = c.L - c.qn + (valid ? tok : c.qn - 1);
                 }
             }
-            __syncthreads();
-            if constexpr (kQRegs) {
-#pragma unroll
-                for (int i = 0; i < NQ * (DH / 16); ++i)
-                    qf[i] = s_q[i * 32 + lane];
-            }
+            sync();
         }
         if (first_chunk || c.lc % kSpan == 0) {
             const int64_t sa = lo + step - c.lc % kSpan;  // the span's chunks: [sa, sb)
@@ -886,13 +808,14 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm<DH, RN>()) quant_attn_ke
             }
         }
 
-        wait_copies();  // this chunk's K
         St st;
         const bool masked = c.lc * kChunk + kChunk > c.L - c.qn + 1;
-        const bool bad = masked ? chunk_state(std::true_type{}, step, st) : chunk_state(std::false_type{}, step, st);
+        const int bad = masked ? chunk_state(std::true_type{}, step, st) : chunk_state(std::false_type{}, step, st);
+        if (bad < 0)
+            return;  // a wait ran out of time (the copying warp lets its copies land)
 #pragma unroll
         for (int r = 0; r < NR; ++r) {
-            if (bad)
+            if (bad > 0)
                 st.l[r] = __int_as_float(0x7FC00000);
             if (st.l[r] != st.l[r] && st.m[r] == -INFINITY)
                 st.m[r] = 0.f;  // a NaN state must not pass for an empty one
@@ -906,29 +829,39 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm<DH, RN>()) quant_attn_ke
         const bool span_end = c.lc + 1 == c.nch || (c.lc + 1) % kSpan == 0;
         if (!span_end && !last_chunk)
             continue;
-        const int sp = c.lc / kSpan;
+        const int sp = c.lc / kSpan, nsp = (c.nch + kSpan - 1) / kSpan;
         const int64_t grp = (int64_t)c.b * hkv + c.kvh;
-        if (!span_whole) {
+        float *const span_recs = p.span_records + grp * p.spans * (int64_t)rec_size, *const span_rec = span_recs + (int64_t)sp * rec_size;
+        if (span_whole) {
+            if (nsp == 1) {
+#pragma unroll
+                for (int r = 0; r < NR; ++r)
+                    if (state_row(r) < rv)
+#pragma unroll
+                        for (int i = 0; i < NP; ++i)
+                            output_pair(state_row(r), state_pair(i), span.o[i][r], span.m[r], span.l[r]);
+                continue;
+            }
+            write_record(span_rec, span, rv);
+        } else {
             if (!last_to_arrive(p.span_counters + grp * p.spans + sp, span_ctas))
                 continue;
-            fold_records(span, span_area, min(kSpan, c.nch - sp * kSpan), rv);
-        }
-        // the span is folded, here
-        const int nsp = (c.nch + kSpan - 1) / kSpan;
-        if (nsp == 1) {
-            write_output(span, rv);
-        } else if (group_whole) {
-            group.fold(span);
-            if (sp + 1 == nsp)
-                write_output(group, rv);
-        } else {
-            float *recs = p.span_records + grp * p.spans * (int64_t)rec_size;
-            write_record(recs + (int64_t)sp * rec_size, span, rv);
-            if (last_to_arrive(p.group_counters + grp, nsp)) {
-                fold_records(group, recs, nsp, rv);
-                write_output(group, rv);
+            const int n = min(kSpan, c.nch - sp * kSpan);
+            if (nsp == 1) {
+                fold_records(span_area, n, rv, output_folded);
+                continue;
             }
+            fold_records(span_area, n, rv, [&](int row, int pair, const State<1, 1> &x) {
+                if (pair == 0) {
+                    __stcg(span_rec + row, x.m[0]);
+                    __stcg(span_rec + p.rows + row, x.l[0]);
+                }
+                __stcg(reinterpret_cast<float2 *>(span_rec + (rec_hdr + (uint32_t)(row * DH + 2 * pair))), x.o[0][0]);
+            });
         }
+        // one of several spans is folded and written: the last one folds them
+        if (last_to_arrive(p.group_counters + grp, nsp))
+            fold_records(span_recs, nsp, rv, output_folded);
     }
 }
 
@@ -939,7 +872,7 @@ cudaError_t set_attributes()
                                 (int)Layout<DH, RN>::bytes(kScanMaxSeqs));
 }
 
-static int rows_capacity(int rows) { return rows <= 4 ? 4 : rows <= 8 ? 8 : rows <= 16 ? 16 : 32; }
+static int rows_capacity(int rows) { return rows <= 8 ? 8 : rows <= 16 ? 16 : 32; }
 
 // CTAs of the grid: one wave, fewer when there are fewer chunks.
 static int64_t grid_of(int dh, int rn, int64_t max_chunks)
@@ -964,7 +897,7 @@ cudaError_t launch(const Params &p, cudaStream_t stream, int64_t grid)
     static_assert(ctas_per_sm<DH, RN>() == (DH == 128 && RN <= 8 ? 2 : 1), "grid_of");
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)grid);
-    cfg.blockDim = dim3(kThreads);
+    cfg.blockDim = dim3(kAllThreads);
     cfg.dynamicSmemBytes = Layout<DH, RN>::bytes(p.num_seqs);
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
@@ -1031,16 +964,15 @@ cudaError_t launch_quant_attention(const QuantAttnArgs &a, ErrState *err, cudaSt
     auto go = [&](auto fn) { e = fn(p, stream, grid); };
     switch (a.pool.head_dim) {
     case 128:
-        go(rn == 4    ? qa::launch<128, 4>
-           : rn == 8  ? qa::launch<128, 8>
+        go(rn == 8    ? qa::launch<128, 8>
            : rn == 16 ? qa::launch<128, 16>
                       : qa::launch<128, 32>);
         break;
     case 256:
-        go(rn == 4 ? qa::launch<256, 4> : rn == 8 ? qa::launch<256, 8> : rn == 16 ? qa::launch<256, 16> : qa::launch<256, 32>);
+        go(rn == 8 ? qa::launch<256, 8> : rn == 16 ? qa::launch<256, 16> : qa::launch<256, 32>);
         break;
     case 512:
-        go(rn == 4 ? qa::launch<512, 4> : rn == 8 ? qa::launch<512, 8> : qa::launch<512, 16>);
+        go(rn == 8 ? qa::launch<512, 8> : qa::launch<512, 16>);
         break;
     }
     snprintf(info, info_len, "quant attention direct dh=%d rows=%d/%d grid=%lld chunks<=%lld", a.pool.head_dim, p.rows,
@@ -1051,11 +983,9 @@ cudaError_t launch_quant_attention(const QuantAttnArgs &a, ErrState *err, cudaSt
 cudaError_t init_quant_attention_attributes()
 {
     cudaError_t e;
-    if ((e = qa::set_attributes<128, 4>()) != cudaSuccess || (e = qa::set_attributes<128, 8>()) != cudaSuccess ||
-        (e = qa::set_attributes<128, 16>()) != cudaSuccess || (e = qa::set_attributes<128, 32>()) != cudaSuccess ||
-        (e = qa::set_attributes<256, 4>()) != cudaSuccess ||
-        (e = qa::set_attributes<256, 8>()) != cudaSuccess || (e = qa::set_attributes<256, 16>()) != cudaSuccess ||
-        (e = qa::set_attributes<256, 32>()) != cudaSuccess || (e = qa::set_attributes<512, 4>()) != cudaSuccess ||
+    if ((e = qa::set_attributes<128, 8>()) != cudaSuccess || (e = qa::set_attributes<128, 16>()) != cudaSuccess ||
+        (e = qa::set_attributes<128, 32>()) != cudaSuccess || (e = qa::set_attributes<256, 8>()) != cudaSuccess ||
+        (e = qa::set_attributes<256, 16>()) != cudaSuccess || (e = qa::set_attributes<256, 32>()) != cudaSuccess ||
         (e = qa::set_attributes<512, 8>()) != cudaSuccess)
         return e;
     return qa::set_attributes<512, 16>();
