@@ -743,14 +743,15 @@ pa_status pa_build_step_metadata(const int32_t *context_lens, const int32_t *que
         }
     }
     ErrState *err = nullptr;
-    pa_status st = device_setup(&err);
+    int nsm = 0;
+    pa_status st = device_setup(&err, &nsm);
     if (st != PA_OK)
         return st;
     const StepMetaArgs a{context_lens, query_lens, num_seqs,   block_tables, max_blocks_per_seq,
                          free_pages,   num_free_pages, cursor_in, cursor_out,   num_blocks,
                          slot_mapping, positions,  num_tokens, seq_lens,     query_start_loc};
     int grid = 0;
-    const cudaError_t e = launch_step_metadata(a, err, reinterpret_cast<cudaStream_t>(stream), &grid);
+    const cudaError_t e = launch_step_metadata(a, err, reinterpret_cast<cudaStream_t>(stream), nsm, &grid);
     snprintf(g_last_info, sizeof g_last_info, "build_step_metadata seqs=%d tokens=%lld grid=%d", num_seqs,
              (long long)num_tokens, grid);
     return cuda_status(e);
@@ -1077,6 +1078,14 @@ static pa_status plan_quant(int32_t num_seqs, int32_t hq, int32_t hkv, int32_t d
         pl->bytes = counters + sp.chunk_bytes + sp.span_bytes;
         return PA_OK;
     }
+    // The BF16 attention gives the same bits with the keys split over CTAs or
+    // not.  Split, it writes and folds a record per (tile, 256-key chunk), whose
+    // cost grows with the rows; measured, read-back included, 7168 keys, 8
+    // query and 2 KV heads, split against not: 4 tiles of 128 rows 64 us to 94,
+    // 8 tiles of 36 rows 68 to 118, of 68 rows 162 to 118, of 128 rows 547 to
+    // 95; 2048 keys, 8 tiles of 68 rows 29 to 44, 16 of 128 rows 42 to 37.
+    if (pl->attn.split && (int64_t)num_seqs * hkv * pl->attn.qtiles * pl->attn.nch * pl->attn.ws_rows > 96 * 152)
+        plan_attention(num_seqs, hq, hkv, dh, max_query_len, max_seq_len, &pl->attn, false);
     pl->cols = (int32_t)(((int64_t)max_seq_len + 15) / 16);
     if (pl->cols < 1)
         pl->cols = 1;
@@ -1173,26 +1182,33 @@ pa_status pa_paged_attention_quant(const void *q, int64_t num_q_tokens, int64_t 
                                          pl.attn.ws_counter_bytes, err, s, nsm, &grid);
     if (e != cudaSuccess)
         return cuda_status(e);
-    pa_kv_cache pool{};
-    pool.k = ws + pl.k;
-    pool.v = ws + pl.v;
-    pool.num_blocks = pl.pages;
-    pool.block_size = 16;
-    pool.num_kv_heads = hkv;
-    pool.head_dim = dh;
-    pool.block_stride = (int64_t)16 * hkv * dh;
-    pool.token_stride = (int64_t)hkv * dh;
-    pool.head_stride = dh;
-    AttnArgs a;
-    AttnPlan ap{};
-    bool empty = false;
-    st = attention_check(q, num_q_tokens, q_tok_stride, num_q_heads, &pool, tables, cols, seq_lens, query_start_loc,
-                         num_seqs, max_query_len, max_seq_len, scale, out, lse, ws + pl.inner,
-                         workspace_bytes - pl.inner, &a, &ap, &empty);
-    if (st != PA_OK)
-        return st;
+    AttnArgs a{};
+    a.q = q;
+    a.num_q_tokens = num_q_tokens;
+    a.q_tok_stride = q_tok_stride;
+    a.num_q_heads = num_q_heads;
+    a.k = ws + pl.k;
+    a.v = ws + pl.v;
+    a.num_blocks = pl.pages;
+    a.num_kv_heads = hkv;
+    a.head_dim = dh;
+    a.block_stride = (int64_t)16 * hkv * dh;
+    a.token_stride = (int64_t)hkv * dh;
+    a.head_stride = dh;
+    a.block_tables = tables;
+    a.max_blocks_per_seq = cols;
+    a.seq_lens = seq_lens;
+    a.query_start_loc = query_start_loc;
+    a.num_seqs = num_seqs;
+    a.max_query_len = max_query_len;
+    a.max_seq_len = max_seq_len;
+    a.scale = scale;
+    a.out = out;
+    a.lse = lse;
+    a.workspace = ws + pl.inner;
+    a.workspace_bytes = workspace_bytes - pl.inner;
     char info[192];
-    st = attention_launch(a, ap, err, s, info, sizeof info);
+    st = attention_launch(a, pl.attn, err, s, info, sizeof info);
     snprintf(g_last_info, sizeof g_last_info, "quant attention read-back grid=%lld; %.180s", (long long)grid, info);
     return st;
 }

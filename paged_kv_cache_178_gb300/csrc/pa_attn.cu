@@ -974,7 +974,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
 // ------------------------------------------------------------------ host --
 
 bool plan_attention(int32_t num_seqs, int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim,
-                    int32_t max_query_len, int32_t max_seq_len, AttnPlan *plan)
+                    int32_t max_query_len, int32_t max_seq_len, AttnPlan *plan, bool allow_split)
 {
     if (num_seqs < 0 || num_kv_heads <= 0 || num_q_heads <= 0 || num_q_heads % num_kv_heads ||
         max_query_len < 0 || max_seq_len < 0)
@@ -992,7 +992,7 @@ bool plan_attention(int32_t num_seqs, int32_t num_q_heads, int32_t num_kv_heads,
     pl.qtiles = max_query_len > 0 ? (max_query_len + pl.tokens_per_tile - 1) / pl.tokens_per_tile : 0;
     const int chunk = head_dim == 128 ? Cfg<128>::kChunk : 0;
     const long long full_ctas = (long long)num_seqs * num_kv_heads * pl.qtiles;
-    pl.split = chunk > 0 && max_seq_len > chunk && full_ctas < kSplitCtaThreshold;
+    pl.split = allow_split && chunk > 0 && max_seq_len > chunk && full_ctas < kSplitCtaThreshold;
     pl.nch = pl.split ? (max_seq_len + chunk - 1) / chunk : 1;
     // Split-KV: about four waves of CTAs at most.  Larger batches give each CTA
     // several consecutive chunks (still one record per chunk, so the fold and

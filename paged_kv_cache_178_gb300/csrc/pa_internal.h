@@ -71,7 +71,8 @@ struct AttnPlan {
 };
 
 bool plan_attention(int32_t num_seqs, int32_t num_q_heads, int32_t num_kv_heads,
-                    int32_t head_dim, int32_t max_query_len, int32_t max_seq_len, AttnPlan *plan);
+                    int32_t head_dim, int32_t max_query_len, int32_t max_seq_len, AttnPlan *plan,
+                    bool allow_split = true);
 
 // Launch the attention kernel for a validated call.  Returns a CUDA error
 // code; *unsupported is set when the shape has no kernel.
@@ -114,7 +115,7 @@ struct StepMetaArgs {
     int64_t num_tokens;
     int32_t *seq_lens, *query_start_loc;
 };
-cudaError_t launch_step_metadata(const StepMetaArgs &a, ErrState *err, cudaStream_t stream, int *grid);
+cudaError_t launch_step_metadata(const StepMetaArgs &a, ErrState *err, cudaStream_t stream, int num_sms, int *grid);
 constexpr int kScanMaxSeqsHost = 8192;  // kScanMaxSeqs of pa_scan.cuh
 
 // Norm and rotation of q and k (pa_step.cu).  Tensor strides in 16-byte units.
@@ -135,6 +136,7 @@ struct RopeArgs {
     uint4 *k_cache, *v_cache;
     int64_t num_slots, block_stride, token_stride, head_stride;
     const int64_t *slot_mapping;
+    int32_t rows_per_task;  // set by the launch
 };
 cudaError_t launch_qk_norm_rope(const RopeArgs &a, ErrState *err, cudaStream_t stream, int num_sms, int64_t *grid);
 cudaError_t init_step_attributes();

@@ -25,14 +25,19 @@ struct Quantised {
     uint32_t code[2];  // 16 codes, element i in bits 4i
 };
 
-__device__ __forceinline__ Quantised quantise16(const uint4 &lo, const uint4 &hi, float inv_tensor_scale)
+__device__ __forceinline__ Quantised quantise16(const uint4 &lo, const uint4 &hi, float tensor_scale,
+                                                float inv_tensor_scale)
 {
     const uint32_t w[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
-    // largest magnitude as BF16 bits (an infinity or NaN is at least 0x7F80)
-    uint32_t top = 0;
+    // largest magnitude as BF16 bits (an infinity or NaN is at least 0x7F80):
+    // of the high halves as they stand, of the low ones shifted up
+    uint32_t th = 0, tl = 0;
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-        top = max(top, max(w[i] & 0x7fffu, (w[i] >> 16) & 0x7fffu));
+    for (int i = 0; i < 8; ++i) {
+        th = max(th, w[i] & 0x7fffffffu);
+        tl = max(tl, (w[i] << 16) & 0x7fffffffu);
+    }
+    const uint32_t top = max(th, tl) >> 16;
     Quantised o;
     if (top >= 0x7F80u) {
         o.scale = 0x7F;  // NaN: the whole block reads back as NaN
@@ -52,16 +57,25 @@ __device__ __forceinline__ Quantised quantise16(const uint4 &lo, const uint4 &hi
         return o;
     }
     const uint32_t sp = e4m3x2_to_f16x2(o.scale);
-    const float s = __half2float(__ushort_as_half((unsigned short)(sp & 0xffffu)));
-    const float r = __frcp_rn(s);
-    const float cap = 65536.f * s;  // far above the largest code: saturates, and keeps q0 finite
+    const float s0 = __half2float(__ushort_as_half((unsigned short)(sp & 0xffffu)));
+    // the tensor scale is a power of two: its products are exact
+    const float s = s0 * tensor_scale, r = __frcp_rn(s0) * inv_tensor_scale;
     float q[16];
 #pragma unroll
+    for (int i = 0; i < 16; ++i)
+        q[i] = __uint_as_float(i % 2 ? (w[i / 2] & 0xffff0000u) : (w[i / 2] << 16));
+    if (o.scale == 0x7E) {
+        // a saturated scale: values far above the largest code, up to
+        // infinity after the product, would leave no finite residual
+        const float cap = 65536.f * s;
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+            q[i] = fminf(fmaxf(q[i], -cap), cap);
+    }
+#pragma unroll
     for (int i = 0; i < 16; ++i) {
-        float x = __uint_as_float(i % 2 ? (w[i / 2] & 0xffff0000u) : (w[i / 2] << 16)) * inv_tensor_scale;
-        x = fminf(fmaxf(x, -cap), cap);
-        const float q0 = x * r;
-        q[i] = __fmaf_rn(__fmaf_rn(-q0, s, x), r, q0);
+        const float q0 = q[i] * r;
+        q[i] = __fmaf_rn(__fmaf_rn(-q0, s, q[i]), r, q0);
     }
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
@@ -81,8 +95,9 @@ __device__ __forceinline__ Quantised quantise16(const uint4 &lo, const uint4 &hi
 // K items run with the 16-element block fastest (a token's codes are
 // contiguous), V items with the token fastest in groups of 16 (the codes of
 // neighbouring tokens are): neighbouring lanes then store neighbouring bytes
-// when the slots are consecutive, as in a prompt.
-template <int DH>
+// when the slots are consecutive, as in a prompt.  The index arithmetic is 32
+// bits wide while the items allow; in 64 bits it took as long as the rest.
+template <int DH, typename Index>
 __global__ void __launch_bounds__(kQuantThreads) quant_write_kernel(
     const uint4 *__restrict__ key, int64_t key_stride, const uint4 *__restrict__ value, int64_t value_stride,
     int64_t num_tokens, QuantPool pool, const int64_t *__restrict__ slot_mapping, ErrState *err)
@@ -90,44 +105,44 @@ __global__ void __launch_bounds__(kQuantThreads) quant_write_kernel(
     griddep_wait();
     griddep_launch_dependents();
     constexpr int NB = DH / 16;  // blocks of a row
-    const int hk = pool.num_kv_heads;
+    const Index hk = (Index)pool.num_kv_heads;
     const int64_t num_slots = pool.num_blocks * 16;
-    const int64_t groups = (num_tokens + 15) / 16;
-    const int64_t per_kind = groups * 16 * hk * NB;  // V counts whole groups of 16 tokens, K the same for symmetry
-    for (int64_t i = (int64_t)blockIdx.x * kQuantThreads + threadIdx.x; i < 2 * per_kind;
-         i += (int64_t)gridDim.x * kQuantThreads) {
-        const bool is_v = i >= per_kind;
-        int64_t x = is_v ? i - per_kind : i;
-        int64_t t;
-        int blk, h;
+    const Index groups = (Index)((num_tokens + 15) / 16);
+    const Index per_kind = groups * 16 * hk * NB;  // whole groups of 16 tokens
+    const bool is_v = blockIdx.y != 0;
+    const float scale = is_v ? pool.v_scale : pool.k_scale, inv = 1.f / scale;
+    const uint4 *const base = is_v ? value : key;
+    const int64_t stride = is_v ? value_stride : key_stride;
+    uint8_t *const out = is_v ? pool.v : pool.k;
+    for (Index i = (Index)blockIdx.x * kQuantThreads + threadIdx.x; i < per_kind; i += (Index)gridDim.x * kQuantThreads) {
+        Index t, h;
+        int blk;
         if (is_v) {
-            const int lo = (int)(x % 16);
-            x /= 16;
-            blk = (int)(x % NB);
-            x /= NB;
-            h = (int)(x % hk);
-            t = x / hk * 16 + lo;
+            const Index x = i / (16 * NB);
+            blk = (int)(i / 16 % NB);
+            h = x % hk;
+            t = x / hk * 16 + i % 16;
         } else {
-            blk = (int)(x % NB);
-            x /= NB;
-            h = (int)(x % hk);
+            const Index x = i / NB;
+            blk = (int)(i % NB);
+            h = x % hk;
             t = x / hk;
         }
-        if (t >= num_tokens)
+        if ((int64_t)t >= num_tokens)
             continue;
-        const uint4 *src = (is_v ? value + t * value_stride : key + t * key_stride) + (int64_t)h * (DH / 8) + 2 * blk;
+        const uint4 *src = base + (int64_t)t * stride + (int64_t)h * (DH / 8) + 2 * blk;
         const uint4 a = __ldg(src), b = __ldg(src + 1);
         const int64_t slot = __ldg(slot_mapping + t);
         if (slot < 0)
             continue;
         if (slot >= num_slots) {
             if (!is_v && blk == 0 && h == 0)
-                record_error(err, kErrBadMetadata, t);
+                record_error(err, kErrBadMetadata, (long long)t);
             continue;
         }
-        const Quantised q = quantise16(a, b, 1.f / (is_v ? pool.v_scale : pool.k_scale));
+        const Quantised q = quantise16(a, b, scale, inv);
         const int tok = (int)(slot & 15);
-        uint8_t *rec = (is_v ? pool.v : pool.k) + (slot >> 4) * pool.block_stride + h * pool.head_stride;
+        uint8_t *rec = out + (slot >> 4) * pool.block_stride + (int64_t)h * pool.head_stride;
         if (is_v) {
             uint8_t *p = rec + blk * 128 + tok;
 #pragma unroll
@@ -141,16 +156,23 @@ __global__ void __launch_bounds__(kQuantThreads) quant_write_kernel(
     }
 }
 
+template <typename Index>
+static auto quant_write_of(int head_dim)
+{
+    return head_dim == 128 ? quant_write_kernel<128, Index>
+                           : (head_dim == 256 ? quant_write_kernel<256, Index> : quant_write_kernel<512, Index>);
+}
+
 cudaError_t launch_quant_write(const void *key, int64_t key_stride, const void *value, int64_t value_stride,
                                int64_t num_tokens, const QuantPool &pool, const int64_t *slot_mapping, ErrState *err,
                                cudaStream_t stream, int num_sms, int64_t *grid)
 {
-    const int64_t items = (num_tokens + 15) / 16 * 16 * pool.num_kv_heads * (pool.head_dim / 16) * 2;
+    const int64_t items = (num_tokens + 15) / 16 * 16 * pool.num_kv_heads * (pool.head_dim / 16);
     int64_t blocks = (items + kQuantThreads - 1) / kQuantThreads;
     if (blocks > (int64_t)num_sms * 32)
         blocks = (int64_t)num_sms * 32;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)blocks);
+    cfg.gridDim = dim3((unsigned)blocks, 2);
     cfg.blockDim = dim3(kQuantThreads);
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
@@ -158,10 +180,10 @@ cudaError_t launch_quant_write(const void *key, int64_t key_stride, const void *
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    *grid = blocks;
-    void (*kern)(const uint4 *, int64_t, const uint4 *, int64_t, int64_t, QuantPool, const int64_t *, ErrState *) =
-        pool.head_dim == 128 ? quant_write_kernel<128>
-                             : (pool.head_dim == 256 ? quant_write_kernel<256> : quant_write_kernel<512>);
+    *grid = 2 * blocks;
+    // the loop's last step may pass the items by one grid
+    const bool narrow = items + blocks * kQuantThreads <= (int64_t)UINT32_MAX;
+    auto kern = narrow ? quant_write_of<uint32_t>(pool.head_dim) : quant_write_of<uint64_t>(pool.head_dim);
     return cudaLaunchKernelEx(&cfg, kern, static_cast<const uint4 *>(key), key_stride / 8,
                               static_cast<const uint4 *>(value), value_stride / 8, num_tokens, pool, slot_mapping,
                               err);
@@ -169,11 +191,12 @@ cudaError_t launch_quant_write(const void *key, int64_t key_stride, const void *
 
 // ------------------------------------------------------------- read-back ----
 // Bound by the BF16 bytes it writes (16 of every 20.5 bytes moved).  Eight
-// codes (one 32-bit word) become one 16-byte store.  K: neighbouring lanes
-// take neighbouring words of a token.  V: a lane takes eight head-dim elements
-// of all 16 tokens (four 16-byte loads, the bytes regrouped by token with
-// permutes), neighbouring lanes neighbouring elements; every store
-// instruction then covers whole rows.
+// codes (one 32-bit word) become one 16-byte store.  A warp takes a run of
+// units of 4096 elements of K and of V (two records at head dim 128, one at
+// 256, half of one at 512).  K: neighbouring lanes take neighbouring words of
+// a token.  V: a lane takes eight head-dim elements of all 16 tokens (four
+// 16-byte loads, the bytes regrouped by token with permutes), neighbouring
+// lanes neighbouring elements; every store instruction then covers whole rows.
 __device__ __forceinline__ uint4 values8(uint32_t codes, uint32_t scale_pair, float tensor_scale)
 {
     uint32_t p[4];
@@ -232,71 +255,114 @@ __global__ void __launch_bounds__(kQuantThreads) dequantize_kv_kernel(
     constexpr int VEC = DH / 8;  // 16-byte vectors of an output row
     const int hk = pool.num_kv_heads;
     const uint4 qnan = make_uint4(0x7FC07FC0u, 0x7FC07FC0u, 0x7FC07FC0u, 0x7FC07FC0u);
-    // one (page, head) after another, half of the CTA for K and half for V
-    constexpr int HALF = kQuantThreads / 2;
-    const bool is_v = tid >= HALF;
-    const int ht = tid % HALF;
-    const int64_t units = (int64_t)total * hk;
-    // a pass covers PASS (page, head) units so that every thread has V work
-    constexpr int PASS = HALF / VEC;
-    for (int64_t u0 = (int64_t)blockIdx.x * PASS; u0 < units; u0 += (int64_t)gridDim.x * PASS) {
-        if (is_v) {
-            const int64_t u = u0 + ht / VEC;
-            if (u < units) {
-                const int i = ht % VEC;
-                const int c = (int)(u / hk), h = (int)(u % hk);
-                const int b = owner_of(s_off, num_seqs, c);
-                const int id = __ldg(block_tables + (int64_t)b * max_blocks + (c - s_off[b]));
-                uint4 *dst = v_out + ((int64_t)c * 16 * hk + h) * VEC + i;
-                if (id < 0 || (int64_t)id >= pool.num_blocks) {
-                    if (i == 0 && h == 0)
-                        record_error(err, kErrBadMetadata, b);
-                    for (int t = 0; t < 16; ++t)
-                        dst[(int64_t)t * hk * VEC] = qnan;
-                } else {
-                    const uint8_t *rec = pool.v + (int64_t)id * pool.block_stride + h * pool.head_stride;
-                    uint4 col[4];  // element pairs 4i .. 4i+3, sixteen tokens each
+    // this warp's units, one after another: consecutive records, so the
+    // request and the block id follow with the page
+    const int lane = tid & 31;
+    const int64_t records = (int64_t)total * hk, units = (records * DH + 255) / 256;
+    const int64_t warps = gsize / 32, w = gtid / 32;
+    const int64_t u_lo = w * units / warps, u_hi = (w + 1) * units / warps;
+    // per lane: the page a record index stands in, followed as it grows
+    struct Where {
+        int64_t rec;  // record index (page * heads + head)
+        int c, h, b, id;
+    };
+    auto seek = [&](Where &x, int64_t rec) {
+        x.rec = rec;
+        if (rec >= records)
+            return;
+        x.c = (int)(rec / hk);
+        x.h = (int)(rec - (int64_t)x.c * hk);
+        x.b = owner_of(s_off, num_seqs, x.c);
+        x.id = __ldg(block_tables + (int64_t)x.b * max_blocks + (x.c - s_off[x.b]));
+    };
+    auto advance = [&](Where &x, int by) {
+        x.rec += by;
+        if (x.rec >= records)
+            return;
+        x.h += by;
+        bool moved = false;
+        while (x.h >= hk) {
+            x.h -= hk;
+            ++x.c;
+            moved = true;
+        }
+        if (moved) {
+            while (x.c >= s_off[x.b + 1])
+                ++x.b;
+            x.id = __ldg(block_tables + (int64_t)x.b * max_blocks + (x.c - s_off[x.b]));
+        }
+    };
+    auto good = [&](const Where &x) { return x.id >= 0 && (int64_t)x.id < pool.num_blocks; };
+    constexpr int RPU = DH == 128 ? 2 : 1;    // records of a unit
+    constexpr int HPR = DH == 512 ? 2 : 1;    // units of a record
+    Where kx[RPU], vx;
 #pragma unroll
-                    for (int j = 0; j < 4; ++j)
-                        col[j] = __ldg(reinterpret_cast<const uint4 *>(rec) + 4 * i + j);
-                    const uint4 sc = __ldg(reinterpret_cast<const uint4 *>(rec + quant_code_bytes(DH)) + i / 2);
+    for (int j = 0; j < RPU; ++j)
+        seek(kx[j], u_lo / HPR * RPU + j);
+    seek(vx, u_lo / HPR * RPU + (RPU == 2 ? lane / 16 : 0));
+    for (int64_t u = u_lo; u < u_hi; ++u) {
+        // --- K: 512 words, sixteen a lane
+        const int part = HPR == 2 ? (int)(u & 1) : 0;  // tokens 8*part.. of the record
 #pragma unroll
-                    for (int t4 = 0; t4 < 4; ++t4) {
-                        auto part = [&](const uint4 &v) { return t4 == 0 ? v.x : t4 == 1 ? v.y : t4 == 2 ? v.z : v.w; };
-                        const uint32_t w0 = part(col[0]), w1 = part(col[1]), w2 = part(col[2]), w3 = part(col[3]);
-                        // 4x4 byte transpose: tokens 4*t4 .. +3
-                        const uint32_t a = __byte_perm(w0, w1, 0x5140), bb = __byte_perm(w0, w1, 0x7362);
-                        const uint32_t e = __byte_perm(w2, w3, 0x5140), f = __byte_perm(w2, w3, 0x7362);
-                        const uint32_t tw[4] = {__byte_perm(a, e, 0x5410), __byte_perm(a, e, 0x7632),
-                                                __byte_perm(bb, f, 0x5410), __byte_perm(bb, f, 0x7632)};
-                        const uint32_t s4 = part(sc);
-                        const uint32_t s01 = e4m3x2_to_f16x2(s4), s23 = e4m3x2_to_f16x2(s4 >> 16);
+        for (int j = 0; j < RPU; ++j) {
+            constexpr int STEPS = 16 / RPU;
+            if (kx[j].rec < records) {
+                const bool ok = good(kx[j]);
+                const uint8_t *rec = pool.k + (int64_t)(ok ? kx[j].id : 0) * pool.block_stride + kx[j].h * pool.head_stride;
+                uint32_t word[STEPS];
+                uint8_t sb[STEPS];
 #pragma unroll
-                        for (int k = 0; k < 4; ++k) {
-                            const uint32_t sp = __byte_perm(k < 2 ? s01 : s23, 0u, k % 2 ? 0x3232 : 0x1010);
-                            dst[(int64_t)(4 * t4 + k) * hk * VEC] = values8(tw[k], sp, pool.v_scale);
-                        }
-                    }
+                for (int i = 0; i < STEPS; ++i) {
+                    const int x = 512 * part + 32 * i + lane;
+                    word[i] = __ldg(reinterpret_cast<const uint32_t *>(rec) + x);
+                    sb[i] = __ldg(rec + quant_code_bytes(DH) + x / 2);
+                }
+                uint4 *dst = k_out + ((int64_t)kx[j].c * 16 * hk + kx[j].h) * VEC;
+#pragma unroll
+                for (int i = 0; i < STEPS; ++i) {
+                    const int x = 512 * part + 32 * i + lane;
+                    const uint32_t s = e4m3x2_to_f16x2(sb[i]);
+                    dst[(int64_t)(x / VEC) * hk * VEC + x % VEC] =
+                        ok ? values8(word[i], __byte_perm(s, 0u, 0x1010), pool.k_scale) : qnan;
                 }
             }
-        } else {
-            for (int x = ht; x < PASS * 16 * VEC; x += HALF) {
-                const int64_t u = u0 + x / (16 * VEC);
-                if (u >= units)
-                    break;
-                const int r = x % (16 * VEC), t = r / VEC, i = r % VEC;
-                const int c = (int)(u / hk), h = (int)(u % hk);
-                const int b = owner_of(s_off, num_seqs, c);
-                const int id = __ldg(block_tables + (int64_t)b * max_blocks + (c - s_off[b]));
-                uint4 v = qnan;
-                if (id >= 0 && (int64_t)id < pool.num_blocks) {
-                    const uint8_t *rec = pool.k + (int64_t)id * pool.block_stride + h * pool.head_stride;
-                    const uint32_t w = __ldg(reinterpret_cast<const uint32_t *>(rec) + t * VEC + i);
-                    const uint32_t s = e4m3x2_to_f16x2(__ldg(rec + quant_code_bytes(DH) + t * (DH / 16) + i / 2));
-                    v = values8(w, __byte_perm(s, 0u, 0x1010), pool.k_scale);
+        }
+        // --- V: eight elements of all tokens a lane
+        if (vx.rec < records) {
+            const int i = (RPU == 2 ? lane % 16 : lane) + 32 * part;
+            const bool ok = good(vx);
+            if (!ok && i == 0 && vx.h == 0)
+                record_error(err, kErrBadMetadata, vx.b);
+            const uint8_t *rec = pool.v + (int64_t)(ok ? vx.id : 0) * pool.block_stride + vx.h * pool.head_stride;
+            uint4 *dst = v_out + ((int64_t)vx.c * 16 * hk + vx.h) * VEC + i;
+            uint4 col[4];  // element pairs 4i .. 4i+3, sixteen tokens each
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                col[j] = __ldg(reinterpret_cast<const uint4 *>(rec) + 4 * i + j);
+            const uint4 sc = __ldg(reinterpret_cast<const uint4 *>(rec + quant_code_bytes(DH)) + i / 2);
+#pragma unroll
+            for (int t4 = 0; t4 < 4; ++t4) {
+                auto part4 = [&](const uint4 &v) { return t4 == 0 ? v.x : t4 == 1 ? v.y : t4 == 2 ? v.z : v.w; };
+                const uint32_t w0 = part4(col[0]), w1 = part4(col[1]), w2 = part4(col[2]), w3 = part4(col[3]);
+                // 4x4 byte transpose: tokens 4*t4 .. +3
+                const uint32_t a = __byte_perm(w0, w1, 0x5140), bb = __byte_perm(w0, w1, 0x7362);
+                const uint32_t e = __byte_perm(w2, w3, 0x5140), f = __byte_perm(w2, w3, 0x7362);
+                const uint32_t tw[4] = {__byte_perm(a, e, 0x5410), __byte_perm(a, e, 0x7632),
+                                        __byte_perm(bb, f, 0x5410), __byte_perm(bb, f, 0x7632)};
+                const uint32_t s4 = part4(sc);
+                const uint32_t s01 = e4m3x2_to_f16x2(s4), s23 = e4m3x2_to_f16x2(s4 >> 16);
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const uint32_t sp = __byte_perm(k < 2 ? s01 : s23, 0u, k % 2 ? 0x3232 : 0x1010);
+                    dst[(int64_t)(4 * t4 + k) * hk * VEC] = ok ? values8(tw[k], sp, pool.v_scale) : qnan;
                 }
-                k_out[(((int64_t)c * 16 + t) * hk + h) * VEC + i] = v;
             }
+        }
+        if (HPR == 1 || (u & 1)) {
+#pragma unroll
+            for (int j = 0; j < RPU; ++j)
+                advance(kx[j], RPU);
+            advance(vx, RPU);
         }
     }
 }
@@ -307,16 +373,17 @@ cudaError_t launch_dequantize_kv(const QuantPool &pool, const int32_t *block_tab
                                  int32_t *compact_offsets, bool poison_tables, void *zero, size_t zero_bytes,
                                  ErrState *err, cudaStream_t stream, int num_sms, int64_t *grid)
 {
-    const int pass = kQuantThreads / 2 / (pool.head_dim / 8);
     int64_t pages = (int64_t)num_seqs * out_cols;
     if (pages > capacity_pages)
         pages = capacity_pages;
-    int64_t blocks = (pages * pool.num_kv_heads + pass - 1) / pass;
+    // one unit a warp, at most one wave
+    constexpr int kWarpsPerCta = kQuantThreads / 32;
+    int64_t blocks = (pages * pool.num_kv_heads * pool.head_dim / 256 + kWarpsPerCta - 1) / kWarpsPerCta;
     const int64_t tab = ((int64_t)num_seqs * out_cols + kQuantThreads - 1) / kQuantThreads;
     if (blocks < tab)
         blocks = tab;
-    if (blocks > (int64_t)num_sms * 8)
-        blocks = (int64_t)num_sms * 8;
+    if (blocks > (int64_t)num_sms * 3)
+        blocks = (int64_t)num_sms * 3;
     if (blocks < 1)
         blocks = 1;
     cudaLaunchConfig_t cfg = {};

@@ -12,54 +12,48 @@ namespace pa {
 // ------------------------------------------------------- step metadata ----
 // Two exclusive sums over the requests (new tokens, new pages), then one
 // binary search per token and per new page.  A few KB are read and 12 bytes
-// per token written: launch and latency bound, so one kernel does all of it.
-// Every CTA repeats the sums (from L2) rather than passing them on through
-// memory.  The inputs may be the outputs (lengths and cursor advance in
-// place), so nothing is written before every CTA has read them: the grid is
-// one cluster, and a cluster barrier stands between.
-constexpr int kMetaThreads = 1024;
+// per token written: launch and latency bound, so one kernel does all of it,
+// with the two sums in one pass and four tokens a thread in flight.  Every CTA
+// repeats the sums (from L2) rather than passing them on through memory.
+// Where lengths or cursor advance in place, nothing may be written before
+// every CTA has read them: the grid is then one cluster with a barrier of its
+// own in between (up to eight CTAs); otherwise it takes as many CTAs as there
+// is work.
+constexpr int kMetaThreads = 256;
 constexpr int kMetaClusterMax = 8;  // the portable cluster size
+constexpr int kMetaUnroll = 4;
 
-__global__ void __launch_bounds__(kMetaThreads, 1) step_metadata_kernel(StepMetaArgs a, ErrState *err)
+__global__ void __launch_bounds__(kMetaThreads) step_metadata_kernel(StepMetaArgs a, bool in_place, ErrState *err)
 {
     griddep_wait();
     griddep_launch_dependents();
     extern __shared__ int32_t s_meta[];
-    __shared__ long long s_sums[kMetaThreads / 32];
-    int32_t *s_tok = s_meta;                    // [n + 1] first token of a request
-    int32_t *s_page = s_tok + a.num_seqs + 1;   // [n + 1] first new page
-    int32_t *s_ctx = s_page + a.num_seqs + 1;   // [n] cached tokens (0: bad)
+    __shared__ longlong2 s_sums[kMetaThreads / 32];
+    int32_t *s_tok = s_meta;                   // [n + 1] first token of a request
+    int32_t *s_page = s_tok + a.num_seqs + 1;  // [n + 1] first new page
+    int32_t *s_ctx = s_page + a.num_seqs + 1;  // [n] cached tokens (0: bad)
     const int tid = threadIdx.x, n = a.num_seqs;
-    const int64_t gtid = (int64_t)blockIdx.x * kMetaThreads + tid, gsize = (int64_t)gridDim.x * kMetaThreads;
+    const int gtid = blockIdx.x * kMetaThreads + tid, gsize = gridDim.x * kMetaThreads;
     const int64_t limit = (int64_t)a.max_blocks * 16;
-    auto tokens_of = [&](int b, int &ctx) -> int {
+    const int cursor = a.cursor_in ? *a.cursor_in : 0;
+    longlong2 total;
+    block_exclusive_sums2<kMetaThreads>(n, s_tok, s_page, s_sums, total, [&](int b, int &tokens, int &pages) {
         const int c = a.context_lens[b], q = a.query_lens[b];
         const bool c_ok = c >= 0 && (int64_t)c <= limit;
-        ctx = c_ok ? c : 0;
-        if (c_ok && q >= 0 && (int64_t)c + q <= limit)
-            return q;
-        if (blockIdx.x == 0)
-            record_error(err, kErrBadMetadata, b);
-        return 0;
-    };
-    const int cursor = a.cursor_in ? *a.cursor_in : 0;
-    // s_ctx is filled by the first sum and read by the second from the same
-    // thread (both give request b to thread b % kMetaThreads)
-    const long long tokens = block_exclusive_sums<kMetaThreads>(n, s_tok, s_sums, [&](int b) {
-        int ctx;
-        const int q = tokens_of(b, ctx);
+        const int ctx = c_ok ? c : 0;
         s_ctx[b] = ctx;
-        s_page[b] = q;
-        return q;
+        if (c_ok && q >= 0 && (int64_t)c + q <= limit) {
+            tokens = q;
+            pages = (int)(((int64_t)ctx + q + 15) / 16) - (ctx + 15) / 16;  // limit is below 2^31
+        } else if (blockIdx.x == 0) {
+            record_error(err, kErrBadMetadata, b);
+        }
     });
-    const long long pages = block_exclusive_sums<kMetaThreads>(n, s_page, s_sums, [&](int b) {
-        const int64_t c = s_ctx[b], q = s_page[b];
-        return (c + q + 15) / 16 - (c + 15) / 16;
-    });
+    const long long tokens = total.x, pages = total.y;
     const bool bad_cursor = cursor < 0 || cursor > a.num_free;
     const bool short_pages = !bad_cursor && pages > (long long)a.num_free - cursor;
     const bool empty = bad_cursor || short_pages || tokens > a.num_tokens;
-    if (gridDim.x > 1)
+    if (in_place && gridDim.x > 1)
         cluster_sync_all();  // every CTA has read the inputs
     if (gtid == 0) {
         if (short_pages)
@@ -68,51 +62,65 @@ __global__ void __launch_bounds__(kMetaThreads, 1) step_metadata_kernel(StepMeta
             record_error(err, kErrBadMetadata, n);
         *a.cursor_out = empty ? cursor : cursor + (int)pages;
     }
-    for (int64_t b = gtid; b <= n; b += gsize) {
+    for (int b = gtid; b <= n; b += gsize) {
         a.query_start_loc[b] = empty ? 0 : s_tok[b];
         if (b < n)
             a.seq_lens[b] = s_ctx[b] + (empty ? 0 : s_tok[b + 1] - s_tok[b]);
     }
-    auto id_ok = [&](int id) { return id >= 0 && (int64_t)id < a.num_blocks; };
-    if (!empty) {
-        for (int64_t x = gtid; x < pages; x += gsize) {
-            const int b = owner_of(s_page, n, (int)x);
-            const int col = (s_ctx[b] + 15) / 16 + (int)x - s_page[b];
-            a.block_tables[(int64_t)b * a.max_blocks + col] = a.free_pages[cursor + x];
-        }
+    const int np = empty ? 0 : (int)pages, nt = empty ? 0 : (int)tokens;
+    for (int64_t x0 = gtid; x0 < np; x0 += gsize) {
+        const int x = (int)x0, b = owner_of(s_page, n, x);
+        const int col = (s_ctx[b] + 15) / 16 + x - s_page[b];
+        a.block_tables[(int64_t)b * a.max_blocks + col] = a.free_pages[cursor + x];
     }
-    for (int64_t t = gtid; t < a.num_tokens; t += gsize) {
-        int64_t slot = -1;
-        int pos = -1;
-        if (!empty && t < tokens) {
-            const int b = owner_of(s_tok, n, (int)t);
-            const int ctx = s_ctx[b], have = (ctx + 15) / 16;
-            pos = ctx + (int)t - s_tok[b];
-            // a new page's id comes from the free list: its table entry may
-            // be written by another thread just now
-            const int p = pos / 16;
-            const int id = p < have ? a.block_tables[(int64_t)b * a.max_blocks + p]
-                                    : a.free_pages[cursor + s_page[b] + p - have];
-            if (id_ok(id))
-                slot = (int64_t)id * 16 + pos % 16;
-            else
-                record_error(err, kErrBadMetadata, b);
+    for (int64_t t0 = gtid; t0 < a.num_tokens; t0 += (int64_t)kMetaUnroll * gsize) {
+        int pos[kMetaUnroll], id[kMetaUnroll], req[kMetaUnroll];
+#pragma unroll
+        for (int u = 0; u < kMetaUnroll; ++u) {
+            const int64_t t = t0 + (int64_t)u * gsize;
+            pos[u] = -1;
+            id[u] = req[u] = 0;
+            if (t < nt) {
+                const int b = owner_of(s_tok, n, (int)t), ctx = s_ctx[b], have = (ctx + 15) / 16;
+                req[u] = b;
+                pos[u] = ctx + (int)t - s_tok[b];
+                // a new page's id comes from the free list: its table entry
+                // may be written by another thread just now
+                const int p = pos[u] / 16;
+                id[u] = p < have ? a.block_tables[(int64_t)b * a.max_blocks + p]
+                                 : a.free_pages[cursor + s_page[b] + p - have];
+            }
         }
-        a.slot_mapping[t] = slot;
-        a.positions[t] = pos;
+#pragma unroll
+        for (int u = 0; u < kMetaUnroll; ++u) {
+            const int64_t t = t0 + (int64_t)u * gsize;
+            if (t >= a.num_tokens)
+                break;
+            int64_t slot = -1;
+            if (pos[u] >= 0) {
+                if (id[u] >= 0 && (int64_t)id[u] < a.num_blocks)
+                    slot = (int64_t)id[u] * 16 + pos[u] % 16;
+                else
+                    record_error(err, kErrBadMetadata, req[u]);
+            }
+            a.slot_mapping[t] = slot;
+            a.positions[t] = pos[u];
+        }
     }
 }
 
 static size_t meta_smem(int num_seqs) { return (size_t)(3 * num_seqs + 2) * 4; }
 
-cudaError_t launch_step_metadata(const StepMetaArgs &a, ErrState *err, cudaStream_t stream, int *grid)
+cudaError_t launch_step_metadata(const StepMetaArgs &a, ErrState *err, cudaStream_t stream, int num_sms, int *grid)
 {
-    // One CTA until a second one would have work (about one item per thread);
-    // eight of them write 12 bytes a token at about 8 x 64 bytes a clock.
+    const bool in_place = a.seq_lens == a.context_lens || a.cursor_out == a.cursor_in;
     const int64_t items = a.num_tokens + a.num_seqs;
-    int ctas = 1;
-    while (ctas < kMetaClusterMax && (int64_t)ctas * kMetaThreads < items)
-        ctas *= 2;
+    const int64_t want = (items + kMetaThreads * kMetaUnroll - 1) / (kMetaThreads * kMetaUnroll);
+    const int64_t most = in_place ? kMetaClusterMax : num_sms;
+    int ctas = (int)(want < 1 ? 1 : (want < most ? want : most));
+    if (in_place)
+        while (ctas & (ctas - 1))
+            ++ctas;  // a cluster size: a power of two
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)ctas);
     cfg.blockDim = dim3(kMetaThreads);
@@ -122,13 +130,13 @@ cudaError_t launch_step_metadata(const StepMetaArgs &a, ErrState *err, cudaStrea
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = (unsigned)ctas;
+    attr[1].val.clusterDim.x = in_place ? (unsigned)ctas : 1;
     attr[1].val.clusterDim.y = 1;
     attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
     *grid = ctas;
-    return cudaLaunchKernelEx(&cfg, step_metadata_kernel, a, err);
+    return cudaLaunchKernelEx(&cfg, step_metadata_kernel, a, in_place, err);
 }
 
 // ------------------------------------------- norm, rotation, cache write --
@@ -140,6 +148,7 @@ cudaError_t launch_step_metadata(const StepMetaArgs &a, ErrState *err, cudaStrea
 // (2i, 2i+1) any two vectors do.  So the rotation needs no exchange between
 // lanes, and the norm one butterfly over the group.
 constexpr int kRopeThreads = 256;
+constexpr int kRopeBatch = 4;  // rows in flight
 
 template <int DH>
 __device__ __forceinline__ float group_sum(float x)
@@ -183,138 +192,188 @@ __device__ __forceinline__ float sum_squares(const float (&a)[8], const float (&
     return s;
 }
 
+// A warp takes one token and a part of its rows, neighbouring groups
+// neighbouring rows, so that its loads and stores are contiguous; a group's
+// rows_per_task rows go one after another: the angles stay in registers, the
+// weights until the kind of row changes, and the loads of several rows are in
+// flight together.
 template <int DH, bool INTERLEAVED>
 __global__ void __launch_bounds__(kRopeThreads) qk_norm_rope_kernel(const RopeArgs a, ErrState *err)
 {
     griddep_wait();
     griddep_launch_dependents();
     constexpr int LANES = DH / 16;  // lanes of a row
+    constexpr int VEC = DH / 8;     // vectors of a row
     const int lane = threadIdx.x % LANES;
     const int hk = a.num_kv_heads, hq = a.num_q_heads;
     const int rows_tok = hq + hk * (a.k_cache ? 2 : 1);
-    const int64_t rows = a.num_tokens * rows_tok;
-    const int64_t step = (int64_t)gridDim.x * (kRopeThreads / LANES);
+    const int per = a.rows_per_task;
+    constexpr int GPW = 32 / LANES;  // groups of a warp
+    const uint32_t parts = (uint32_t)(rows_tok + GPW * per - 1) / (uint32_t)(GPW * per);
     // vectors of this lane, and the pairs of the first one
     const int rv = a.rot_dim / 16;  // vectors of half the rotated part
     const bool turned = lane < rv;
-    const int v0 = turned ? (INTERLEAVED ? 2 * lane : lane) : 2 * lane;
+    const int v0 = turned && !INTERLEAVED ? lane : 2 * lane;
     const int v1 = turned && !INTERLEAVED ? lane + rv : v0 + 1;
-    // Every lane of a warp runs the same number of passes (the butterflies
-    // name all 32); a group past the last row works on row 0 and stores
-    // nothing.
-    const int64_t first = (int64_t)blockIdx.x * (kRopeThreads / LANES) + threadIdx.x / LANES;
-    const int64_t warp_first = (int64_t)blockIdx.x * (kRopeThreads / LANES) + (threadIdx.x & ~31) / LANES;
-    for (int64_t r0 = warp_first, row = first; r0 < rows; r0 += step, row += step) {
-        const bool live = row < rows;
-        const int64_t t = !live ? 0 : rows <= 0xffffffffll ? (int64_t)((uint32_t)row / (uint32_t)rows_tok) : row / rows_tok;
-        const int h = live ? (int)(row - t * rows_tok) : 0;
-        const int kind = h < hq ? 0 : (h < hq + hk ? 1 : 2);  // q, k, v
-        const int head = kind == 0 ? h : (kind == 1 ? h - hq : h - hq - hk);
-        const uint4 *src = (kind == 0   ? a.q + t * a.q_stride
-                            : kind == 1 ? a.k + t * a.k_stride
-                                        : a.v + t * a.v_stride) +
-                           (int64_t)head * (DH / 8);
-        uint4 x0 = src[v0], x1 = src[v1];
+    // Every lane of a warp runs the same passes (the butterflies name all
+    // 32); a group without a row computes on zeros and stores nothing.
+    const int64_t tasks = a.num_tokens * parts, step = (int64_t)gridDim.x * (kRopeThreads / 32);
+    const int group = (threadIdx.x & 31) / LANES;
+    for (int64_t task = (int64_t)blockIdx.x * (kRopeThreads / 32) + threadIdx.x / 32; task < tasks; task += step) {
+        const int64_t t = tasks <= 0xffffffffll ? (int64_t)((uint32_t)task / parts) : task / parts;
+        // the group's rows: h0, h0 + GPW, ..
+        const int part0 = (int)(task - t * parts) * GPW * per, h0 = part0 + group;
+        const int nrows = h0 < rows_tok ? min(per, (rows_tok - h0 + GPW - 1) / GPW) : 0;
         const int pos = __ldg(a.positions + t);
-        int64_t slot = -1;
-        if (kind != 0 && a.k_cache)
-            slot = __ldg(a.slot_mapping + t);
         const bool bad_pos = (int64_t)pos >= a.max_positions;
-        const uint4 *wv = kind == 0 ? a.q_weight : (kind == 1 ? a.k_weight : nullptr);
-        float p[8], q[8];
-        unpack8(x0, p);
-        unpack8(x1, q);
-        // the whole warp takes part in the sums, whatever its rows are
-        float ss = group_sum<DH>(sum_squares(p, q));
-        float eps = a.eps;
-        const bool large = !(ss < 1e36f), tiny = ss < 1e-30f && eps < 1e-20f;
-        if (__any_sync(0xffffffffu, wv && (large || tiny))) {
-            // squares past fp32's range: the row times a power of two, eps
-            // times its square (the norm cancels it)
-            const float g = !wv ? 1.f : (large ? 0x1p-96f : (!tiny ? 1.f : (eps < 1e-38f ? 0x1p96f : 0x1p64f)));
+        const int64_t slot = a.k_cache ? __ldg(a.slot_mapping + t) : 0;
+        const bool store = nrows > 0 && pos >= 0;
+        const bool slot_bad = a.k_cache && slot >= a.num_slots;
+        const bool cached = slot >= 0 && !slot_bad && !bad_pos;
+        if (pos >= 0 && (threadIdx.x & 31) == 0 && part0 == 0 && (bad_pos || slot_bad))
+            record_error(err, kErrBadMetadata, t);
+        float co[8], si[8];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                p[i] *= g;
-                q[i] *= g;
-            }
-            ss = group_sum<DH>(sum_squares(p, q));
-            eps = eps * g * g;
+        for (int i = 0; i < 8; ++i) {
+            co[i] = 1.f;
+            si[i] = 0.f;
         }
-        if (kind != 2) {
-            if (wv) {
-                const float r = __frsqrt_rn(ss * (1.f / DH) + eps);
-                float w0[8], w1[8];
-                unpack8(__ldg(wv + v0), w0);
-                unpack8(__ldg(wv + v1), w1);
+        if (turned && store && !bad_pos) {
+            // the angles of this lane's eight pairs
+            const float4 *c = reinterpret_cast<const float4 *>(a.cos_sin + (int64_t)pos * a.rot_dim + 8 * lane);
+            const float4 *s = reinterpret_cast<const float4 *>(a.cos_sin + (int64_t)pos * a.rot_dim + a.rot_dim / 2 + 8 * lane);
+            const float4 ca = __ldg(c), cb = __ldg(c + 1), sa = __ldg(s), sb = __ldg(s + 1);
+            co[0] = ca.x, co[1] = ca.y, co[2] = ca.z, co[3] = ca.w, co[4] = cb.x, co[5] = cb.y, co[6] = cb.z, co[7] = cb.w;
+            si[0] = sa.x, si[1] = sa.y, si[2] = sa.z, si[3] = sa.w, si[4] = sb.x, si[5] = sb.y, si[6] = sb.z, si[7] = sb.w;
+        }
+        auto source = [&](int h) {
+            return h < hq        ? a.q + t * a.q_stride + (int64_t)h * VEC
+                   : h < hq + hk ? a.k + t * a.k_stride + (int64_t)(h - hq) * VEC
+                                 : a.v + t * a.v_stride + (int64_t)(h - hq - hk) * VEC;
+        };
+        const uint4 *w_now = nullptr;  // whose weights w0, w1 hold
+        float w0[8], w1[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            w0[i] = w1[i] = 1.f;
+        for (int r0 = 0; r0 < per; r0 += kRopeBatch) {
+        uint4 x0[kRopeBatch], x1[kRopeBatch];
+#pragma unroll
+        for (int u = 0; u < kRopeBatch; ++u) {
+            x0[u] = x1[u] = make_uint4(0u, 0u, 0u, 0u);
+            if (r0 + u < nrows) {
+                const uint4 *src = source(h0 + GPW * (r0 + u));
+                x0[u] = src[v0];
+                x1[u] = src[v1];
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < kRopeBatch; ++u) {
+            if (r0 + u >= per)
+                break;
+            const int h = h0 + GPW * (r0 + u);
+            const bool on = r0 + u < nrows;
+            float p[8], q[8];
+            unpack8(x0[u], p);
+            unpack8(x1[u], q);
+            uint4 y0 = x0[u], y1 = x1[u];
+            const uint4 *wv = !on || h >= hq + hk ? nullptr : (h < hq ? a.q_weight : a.k_weight);
+            // the whole warp takes part in the sums, whatever its rows are
+            float ss = group_sum<DH>(sum_squares(p, q));
+            float eps = a.eps;
+            const bool large = !(ss < 1e36f), tiny = ss < 1e-30f && eps < 1e-20f;
+            if (__any_sync(0xffffffffu, wv && (large || tiny))) {
+                // squares past fp32's range: the row times a power of two, eps
+                // times its square (the norm cancels it)
+                const float g = !wv ? 1.f : (large ? 0x1p-96f : (!tiny ? 1.f : (eps < 1e-38f ? 0x1p96f : 0x1p64f)));
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
-                    p[i] = p[i] * r * (w0[i] + a.weight_offset);
-                    q[i] = q[i] * r * (w1[i] + a.weight_offset);
+                    p[i] *= g;
+                    q[i] *= g;
                 }
+                ss = group_sum<DH>(sum_squares(p, q));
+                eps = eps * g * g;
             }
-            if (turned && pos >= 0 && !bad_pos) {
-                // the angles of this lane's eight pairs
-                const float4 *c = reinterpret_cast<const float4 *>(a.cos_sin + (int64_t)pos * a.rot_dim + 8 * lane);
-                const float4 *s = reinterpret_cast<const float4 *>(a.cos_sin + (int64_t)pos * a.rot_dim +
-                                                                   a.rot_dim / 2 + 8 * lane);
-                const float4 ca = __ldg(c), cb = __ldg(c + 1), sa = __ldg(s), sb = __ldg(s + 1);
-                const float co[8] = {ca.x, ca.y, ca.z, ca.w, cb.x, cb.y, cb.z, cb.w};
-                const float si[8] = {sa.x, sa.y, sa.z, sa.w, sb.x, sb.y, sb.z, sb.w};
-                if (INTERLEAVED) {
+            if (on && h < hq + hk) {
+                if (wv) {
+                    if (wv != w_now) {
+                        w_now = wv;
+                        unpack8(__ldg(wv + v0), w0);
+                        unpack8(__ldg(wv + v1), w1);
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const float u = p[2 * i], v = p[2 * i + 1], m = q[2 * i], o = q[2 * i + 1];
-                        p[2 * i] = __fmaf_rn(u, co[i], -(v * si[i]));
-                        p[2 * i + 1] = __fmaf_rn(v, co[i], u * si[i]);
-                        q[2 * i] = __fmaf_rn(m, co[4 + i], -(o * si[4 + i]));
-                        q[2 * i + 1] = __fmaf_rn(o, co[4 + i], m * si[4 + i]);
+                        for (int i = 0; i < 8; ++i) {
+                            w0[i] += a.weight_offset;
+                            w1[i] += a.weight_offset;
+                        }
                     }
-                } else {
+                    const float rs = __frsqrt_rn(ss * (1.f / DH) + eps);
 #pragma unroll
                     for (int i = 0; i < 8; ++i) {
-                        const float u = p[i], v = q[i];
-                        p[i] = __fmaf_rn(u, co[i], -(v * si[i]));
-                        q[i] = __fmaf_rn(v, co[i], u * si[i]);
+                        p[i] = p[i] * rs * w0[i];
+                        q[i] = q[i] * rs * w1[i];
                     }
                 }
+                if (turned) {
+                    if (INTERLEAVED) {
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const float u = p[2 * i], v = p[2 * i + 1], m = q[2 * i], o = q[2 * i + 1];
+                            p[2 * i] = __fmaf_rn(u, co[i], -(v * si[i]));
+                            p[2 * i + 1] = __fmaf_rn(v, co[i], u * si[i]);
+                            q[2 * i] = __fmaf_rn(m, co[4 + i], -(o * si[4 + i]));
+                            q[2 * i + 1] = __fmaf_rn(o, co[4 + i], m * si[4 + i]);
+                        }
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) {
+                            const float u = p[i], v = q[i];
+                            p[i] = __fmaf_rn(u, co[i], -(v * si[i]));
+                            q[i] = __fmaf_rn(v, co[i], u * si[i]);
+                        }
+                    }
+                }
+                y0 = pack8(p);
+                y1 = pack8(q);
+                if (bad_pos)
+                    y0 = y1 = make_uint4(0x7FC07FC0u, 0x7FC07FC0u, 0x7FC07FC0u, 0x7FC07FC0u);
             }
-            x0 = pack8(p);
-            x1 = pack8(q);
-            if (bad_pos) {
-                x0 = x1 = make_uint4(0x7FC07FC0u, 0x7FC07FC0u, 0x7FC07FC0u, 0x7FC07FC0u);
-                if (live && lane == 0)
-                    record_error(err, kErrBadMetadata, t);
+            if (!on || !store)
+                continue;
+            uint4 *dst = nullptr;
+            if (h < hq)
+                dst = a.q_out + t * a.q_out_stride + (int64_t)h * VEC;
+            else if (!a.k_cache)
+                dst = a.k_out + t * a.k_out_stride + (int64_t)(h - hq) * VEC;
+            else if (cached)
+                dst = (h < hq + hk ? a.k_cache : a.v_cache) + (slot >> 4) * a.block_stride + (slot & 15) * a.token_stride +
+                      (int64_t)(h < hq + hk ? h - hq : h - hq - hk) * a.head_stride;
+            if (dst) {
+                dst[v0] = y0;
+                dst[v1] = y1;
             }
         }
-        if (!live || pos < 0)
-            continue;
-        uint4 *dst = nullptr;
-        if (kind == 0) {
-            dst = a.q_out + t * a.q_out_stride + (int64_t)head * (DH / 8);
-        } else if (!a.k_cache) {
-            dst = a.k_out + t * a.k_out_stride + (int64_t)head * (DH / 8);
-        } else if (slot >= a.num_slots) {
-            if (lane == 0 && head == 0 && kind == 1)
-                record_error(err, kErrBadMetadata, t);
-        } else if (slot >= 0 && !bad_pos) {
-            dst = (kind == 1 ? a.k_cache : a.v_cache) + (slot >> 4) * a.block_stride + (slot & 15) * a.token_stride +
-                  (int64_t)head * a.head_stride;
-        }
-        if (dst) {
-            dst[v0] = x0;
-            dst[v1] = x1;
         }
     }
 }
 
-cudaError_t launch_qk_norm_rope(const RopeArgs &a, ErrState *err, cudaStream_t stream, int num_sms, int64_t *grid)
+cudaError_t launch_qk_norm_rope(const RopeArgs &args, ErrState *err, cudaStream_t stream, int num_sms, int64_t *grid)
 {
-    const int64_t rows = a.num_tokens * (a.num_q_heads + a.num_kv_heads * (a.k_cache ? 2 : 1));
-    const int per_cta = kRopeThreads / (a.head_dim / 16);
-    int64_t blocks = (rows + per_cta - 1) / per_cta;
-    // four waves of the eight CTAs that fit an SM
-    if (blocks > (int64_t)num_sms * 32)
-        blocks = (int64_t)num_sms * 32;
+    RopeArgs a = args;
+    const int rows_tok = a.num_q_heads + a.num_kv_heads * (a.k_cache ? 2 : 1);
+    const int gpw = 512 / a.head_dim;  // groups of a warp
+    // Rows of a group: one while that leaves warps idle, more (their shared
+    // loads then count once) as long as 24 warps per SM have some.
+    const int64_t steps = (rows_tok + gpw - 1) / gpw;  // rows of a group that had the whole token
+    int64_t per = a.num_tokens * steps / ((int64_t)num_sms * 24);
+    per = per < 1 ? 1 : (per > 16 ? 16 : per);
+    if (per > steps)
+        per = steps;
+    const int64_t parts = (steps + per - 1) / per;
+    a.rows_per_task = (int)((steps + parts - 1) / parts);  // parts of about one size
+    const int64_t tasks = a.num_tokens * ((steps + a.rows_per_task - 1) / a.rows_per_task);
+    int64_t blocks = (tasks + kRopeThreads / 32 - 1) / (kRopeThreads / 32);
+    if (blocks > (int64_t)num_sms * 64)
+        blocks = (int64_t)num_sms * 64;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)blocks);
     cfg.blockDim = dim3(kRopeThreads);
