@@ -136,7 +136,7 @@ struct RopeArgs {
     uint4 *k_cache, *v_cache;
     int64_t num_slots, block_stride, token_stride, head_stride;
     const int64_t *slot_mapping;
-    int32_t rows_per_task;  // set by the launch
+    int32_t steps_per_task;  // set by the launch
 };
 cudaError_t launch_qk_norm_rope(const RopeArgs &a, ErrState *err, cudaStream_t stream, int num_sms, int64_t *grid);
 cudaError_t init_step_attributes();

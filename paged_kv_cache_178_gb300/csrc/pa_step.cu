@@ -148,7 +148,8 @@ cudaError_t launch_step_metadata(const StepMetaArgs &a, ErrState *err, cudaStrea
 // (2i, 2i+1) any two vectors do.  So the rotation needs no exchange between
 // lanes, and the norm one butterfly over the group.
 constexpr int kRopeThreads = 256;
-constexpr int kRopeBatch = 4;  // rows in flight
+constexpr int kRopeCtas = 4;   // per SM
+constexpr int kRopeBatch = 2;  // steps loaded together
 
 template <int DH>
 __device__ __forceinline__ float group_sum(float x)
@@ -192,185 +193,207 @@ __device__ __forceinline__ float sum_squares(const float (&a)[8], const float (&
     return s;
 }
 
-// A warp takes one token and a part of its rows, neighbouring groups
-// neighbouring rows, so that its loads and stores are contiguous; a group's
-// rows_per_task rows go one after another: the angles stay in registers, the
-// weights until the kind of row changes, and the loads of several rows are in
-// flight together.
+// A warp takes one token and a part of its steps: a step is 32*16/DH
+// neighbouring rows of q, of k or of v, a row to a group, so that loads and
+// stores are contiguous.  The angles stay in registers, the weights (offset
+// added) in shared memory, the rows' addresses advance by one addition, and
+// kRopeBatch steps are loaded before the first is computed.  What bounds it
+// after the memory is the instruction count: a step of 1 KB takes about 130.
 template <int DH, bool INTERLEAVED>
-__global__ void __launch_bounds__(kRopeThreads) qk_norm_rope_kernel(const RopeArgs a, ErrState *err)
+__global__ void __launch_bounds__(kRopeThreads, kRopeCtas) qk_norm_rope_kernel(const RopeArgs a, ErrState *err)
 {
     griddep_wait();
     griddep_launch_dependents();
-    constexpr int LANES = DH / 16;  // lanes of a row
-    constexpr int VEC = DH / 8;     // vectors of a row
-    const int lane = threadIdx.x % LANES;
+    constexpr int LANES = DH / 16;   // lanes of a row
+    constexpr int VEC = DH / 8;      // vectors of a row
+    constexpr int GPW = 32 / LANES;  // groups of a warp: rows of a step
+    __shared__ __align__(16) float s_w[2 * DH];  // weights of q and k, offset added
+    const int wl = threadIdx.x & 31, lane = threadIdx.x % LANES, group = wl / LANES;
     const int hk = a.num_kv_heads, hq = a.num_q_heads;
-    const int rows_tok = hq + hk * (a.k_cache ? 2 : 1);
-    const int per = a.rows_per_task;
-    constexpr int GPW = 32 / LANES;  // groups of a warp
-    const uint32_t parts = (uint32_t)(rows_tok + GPW * per - 1) / (uint32_t)(GPW * per);
-    // vectors of this lane, and the pairs of the first one
+    // steps of a token: of q, of k, of v
+    const int jq = (hq + GPW - 1) / GPW, jk = (hk + GPW - 1) / GPW, jall = jq + jk + (a.k_cache ? jk : 0);
+    const int per = a.steps_per_task;
+    const uint32_t parts = (uint32_t)(jall + per - 1) / (uint32_t)per;
+    // Vectors of this lane: neighbouring lanes have neighbouring ones in both
+    // loads.  With pairs (i, i + rot/2) lanes below rv hold partners.
     const int rv = a.rot_dim / 16;  // vectors of half the rotated part
-    const bool turned = lane < rv;
-    const int v0 = turned && !INTERLEAVED ? lane : 2 * lane;
-    const int v1 = turned && !INTERLEAVED ? lane + rv : v0 + 1;
-    // Every lane of a warp runs the same passes (the butterflies name all
-    // 32); a group without a row computes on zeros and stores nothing.
-    const int64_t tasks = a.num_tokens * parts, step = (int64_t)gridDim.x * (kRopeThreads / 32);
-    const int group = (threadIdx.x & 31) / LANES;
-    for (int64_t task = (int64_t)blockIdx.x * (kRopeThreads / 32) + threadIdx.x / 32; task < tasks; task += step) {
-        const int64_t t = tasks <= 0xffffffffll ? (int64_t)((uint32_t)task / parts) : task / parts;
-        // the group's rows: h0, h0 + GPW, ..
-        const int part0 = (int)(task - t * parts) * GPW * per, h0 = part0 + group;
-        const int nrows = h0 < rows_tok ? min(per, (rows_tok - h0 + GPW - 1) / GPW) : 0;
-        const int pos = __ldg(a.positions + t);
+    const int v0 = INTERLEAVED || lane < rv ? lane : lane + rv;
+    const int v1 = INTERLEAVED || lane >= rv ? lane + LANES : lane + rv;
+    const bool turned = INTERLEAVED ? lane < 2 * rv : lane < rv;
+    for (int i = threadIdx.x; i < 2 * DH; i += kRopeThreads) {
+        const __nv_bfloat16 *w = reinterpret_cast<const __nv_bfloat16 *>(i < DH ? a.q_weight : a.k_weight);
+        s_w[i] = w ? __bfloat162float(w[i % DH]) + a.weight_offset : 1.f;
+    }
+    __syncthreads();
+    const int64_t tasks = a.num_tokens * parts;
+    auto token_of = [&](int64_t task) {
+        return tasks <= 0xffffffffll ? (int64_t)((uint32_t)task / parts) : task / parts;
+    };
+    // positions and slots are loaded a task ahead; a task's first rows before
+    // anything waits for its position
+    int64_t task = (int64_t)blockIdx.x * (kRopeThreads / 32) + threadIdx.x / 32;
+    const int64_t step = (int64_t)gridDim.x * (kRopeThreads / 32);
+    int64_t t_next = task < tasks ? token_of(task) : 0;
+    int pos_next = 0;
+    int64_t slot_next = 0;
+    auto load_next = [&]() {
+        pos_next = __ldg(a.positions + t_next);
+        slot_next = a.k_cache ? __ldg(a.slot_mapping + t_next) : 0;
+    };
+    if (task < tasks)
+        load_next();
+    for (; task < tasks; task += step) {
+        const int64_t t = t_next, slot = slot_next;
+        const int pos = pos_next, part = (int)(task - t * parts), j0 = part * per, j1 = min(j0 + per, jall);
+        if (task + step < tasks) {
+            t_next = token_of(task + step);
+            load_next();
+        }
         const bool bad_pos = (int64_t)pos >= a.max_positions;
-        const int64_t slot = a.k_cache ? __ldg(a.slot_mapping + t) : 0;
-        const bool store = nrows > 0 && pos >= 0;
         const bool slot_bad = a.k_cache && slot >= a.num_slots;
-        const bool cached = slot >= 0 && !slot_bad && !bad_pos;
-        if (pos >= 0 && (threadIdx.x & 31) == 0 && part0 == 0 && (bad_pos || slot_bad))
+        if (pos >= 0 && wl == 0 && part == 0 && (bad_pos || slot_bad))
             record_error(err, kErrBadMetadata, t);
         float co[8], si[8];
+        bool have_angles = false;
+        auto load_angles = [&]() {
+            if (have_angles)
+                return;
+            have_angles = true;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            co[i] = 1.f;
-            si[i] = 0.f;
-        }
-        if (turned && store && !bad_pos) {
-            // the angles of this lane's eight pairs
-            const float4 *c = reinterpret_cast<const float4 *>(a.cos_sin + (int64_t)pos * a.rot_dim + 8 * lane);
-            const float4 *s = reinterpret_cast<const float4 *>(a.cos_sin + (int64_t)pos * a.rot_dim + a.rot_dim / 2 + 8 * lane);
-            const float4 ca = __ldg(c), cb = __ldg(c + 1), sa = __ldg(s), sb = __ldg(s + 1);
-            co[0] = ca.x, co[1] = ca.y, co[2] = ca.z, co[3] = ca.w, co[4] = cb.x, co[5] = cb.y, co[6] = cb.z, co[7] = cb.w;
-            si[0] = sa.x, si[1] = sa.y, si[2] = sa.z, si[3] = sa.w, si[4] = sb.x, si[5] = sb.y, si[6] = sb.z, si[7] = sb.w;
-        }
-        auto source = [&](int h) {
-            return h < hq        ? a.q + t * a.q_stride + (int64_t)h * VEC
-                   : h < hq + hk ? a.k + t * a.k_stride + (int64_t)(h - hq) * VEC
-                                 : a.v + t * a.v_stride + (int64_t)(h - hq - hk) * VEC;
+            for (int i = 0; i < 8; ++i) {
+                co[i] = 1.f;  // elements past the rotated part stay as they are
+                si[i] = 0.f;
+            }
+            if (turned && pos >= 0 && !bad_pos) {
+                // the angles of this lane's eight pairs (interleaved: four of
+                // v0, and of v1 where that is rotated)
+                const float4 *c = reinterpret_cast<const float4 *>(a.cos_sin + (int64_t)pos * a.rot_dim);
+                const int i0 = INTERLEAVED ? v0 : 2 * lane, i1 = INTERLEAVED ? v1 : 2 * lane + 1, sin0 = 2 * rv;
+                const bool both = !INTERLEAVED || v1 < 2 * rv;
+                const float4 ca = __ldg(c + i0), sa = __ldg(c + sin0 + i0);
+                const float4 cb = both ? __ldg(c + i1) : make_float4(1.f, 1.f, 1.f, 1.f);
+                const float4 sb = both ? __ldg(c + sin0 + i1) : make_float4(0.f, 0.f, 0.f, 0.f);
+                co[0] = ca.x, co[1] = ca.y, co[2] = ca.z, co[3] = ca.w, co[4] = cb.x, co[5] = cb.y, co[6] = cb.z, co[7] = cb.w;
+                si[0] = sa.x, si[1] = sa.y, si[2] = sa.z, si[3] = sa.w, si[4] = sb.x, si[5] = sb.y, si[6] = sb.z, si[7] = sb.w;
+            }
         };
-        const uint4 *w_now = nullptr;  // whose weights w0, w1 hold
-        float w0[8], w1[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-            w0[i] = w1[i] = 1.f;
-        for (int r0 = 0; r0 < per; r0 += kRopeBatch) {
-        uint4 x0[kRopeBatch], x1[kRopeBatch];
-#pragma unroll
-        for (int u = 0; u < kRopeBatch; ++u) {
-            x0[u] = x1[u] = make_uint4(0u, 0u, 0u, 0u);
-            if (r0 + u < nrows) {
-                const uint4 *src = source(h0 + GPW * (r0 + u));
-                x0[u] = src[v0];
-                x1[u] = src[v1];
-            }
-        }
-#pragma unroll
-        for (int u = 0; u < kRopeBatch; ++u) {
-            if (r0 + u >= per)
-                break;
-            const int h = h0 + GPW * (r0 + u);
-            const bool on = r0 + u < nrows;
+        // One row: norm and rotation.  The whole warp takes part in the sums.
+        auto row = [&](uint4 &x0, uint4 &x1, bool norm, const float4 *w) {
             float p[8], q[8];
-            unpack8(x0[u], p);
-            unpack8(x1[u], q);
-            uint4 y0 = x0[u], y1 = x1[u];
-            const uint4 *wv = !on || h >= hq + hk ? nullptr : (h < hq ? a.q_weight : a.k_weight);
-            // the whole warp takes part in the sums, whatever its rows are
-            float ss = group_sum<DH>(sum_squares(p, q));
-            float eps = a.eps;
-            const bool large = !(ss < 1e36f), tiny = ss < 1e-30f && eps < 1e-20f;
-            if (__any_sync(0xffffffffu, wv && (large || tiny))) {
-                // squares past fp32's range: the row times a power of two, eps
-                // times its square (the norm cancels it)
-                const float g = !wv ? 1.f : (large ? 0x1p-96f : (!tiny ? 1.f : (eps < 1e-38f ? 0x1p96f : 0x1p64f)));
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    p[i] *= g;
-                    q[i] *= g;
-                }
-                ss = group_sum<DH>(sum_squares(p, q));
-                eps = eps * g * g;
-            }
-            if (on && h < hq + hk) {
-                if (wv) {
-                    if (wv != w_now) {
-                        w_now = wv;
-                        unpack8(__ldg(wv + v0), w0);
-                        unpack8(__ldg(wv + v1), w1);
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) {
-                            w0[i] += a.weight_offset;
-                            w1[i] += a.weight_offset;
-                        }
-                    }
-                    const float rs = __frsqrt_rn(ss * (1.f / DH) + eps);
+            unpack8(x0, p);
+            unpack8(x1, q);
+            if (norm) {
+                float ss = group_sum<DH>(sum_squares(p, q)), eps = a.eps;
+                const bool large = !(ss < 1e36f), tiny = ss < 1e-30f && eps < 1e-20f;
+                if (__any_sync(0xffffffffu, large || tiny)) {
+                    // squares past fp32's range: the row times a power of two,
+                    // eps times its square (the norm cancels it)
+                    const float g = large ? 0x1p-96f : (!tiny ? 1.f : (eps < 1e-38f ? 0x1p96f : 0x1p64f));
 #pragma unroll
                     for (int i = 0; i < 8; ++i) {
-                        p[i] = p[i] * rs * w0[i];
-                        q[i] = q[i] * rs * w1[i];
+                        p[i] *= g;
+                        q[i] *= g;
+                    }
+                    ss = group_sum<DH>(sum_squares(p, q));
+                    eps = eps * g * g;
+                }
+                const float rs = rsqrtf(ss * (1.f / DH) + eps);
+                const float4 wa = w[2 * v0], wb = w[2 * v0 + 1], wc = w[2 * v1], wd = w[2 * v1 + 1];
+                const float w0[8] = {wa.x, wa.y, wa.z, wa.w, wb.x, wb.y, wb.z, wb.w};
+                const float w1[8] = {wc.x, wc.y, wc.z, wc.w, wd.x, wd.y, wd.z, wd.w};
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    p[i] = p[i] * rs * w0[i];
+                    q[i] = q[i] * rs * w1[i];
+                }
+            }
+            if (turned) {
+                if (INTERLEAVED) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const float u = p[2 * i], v = p[2 * i + 1], m = q[2 * i], o = q[2 * i + 1];
+                        p[2 * i] = __fmaf_rn(u, co[i], -(v * si[i]));
+                        p[2 * i + 1] = __fmaf_rn(v, co[i], u * si[i]);
+                        q[2 * i] = __fmaf_rn(m, co[4 + i], -(o * si[4 + i]));
+                        q[2 * i + 1] = __fmaf_rn(o, co[4 + i], m * si[4 + i]);
+                    }
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const float u = p[i], v = q[i];
+                        p[i] = __fmaf_rn(u, co[i], -(v * si[i]));
+                        q[i] = __fmaf_rn(v, co[i], u * si[i]);
                     }
                 }
-                if (turned) {
-                    if (INTERLEAVED) {
+            }
+            x0 = pack8(p);
+            x1 = pack8(q);
+            if (bad_pos)
+                x0 = x1 = make_uint4(0x7FC07FC0u, 0x7FC07FC0u, 0x7FC07FC0u, 0x7FC07FC0u);
+        };
+        // steps [ja, jb) of one kind: src, dst of its first row; dst null: not stored
+        auto run = [&](int ja, int jb, int heads, const uint4 *src, uint4 *dst, int64_t dst_row, bool compute, bool norm,
+                       const float4 *w) {
+            int h = ja * GPW + group;
+            src += (int64_t)h * VEC;
+            dst += h * dst_row;
+            const int64_t dst_step = GPW * dst_row;
+            for (int j = ja; j < jb; j += kRopeBatch) {
+                uint4 x0[kRopeBatch], x1[kRopeBatch];
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            const float u = p[2 * i], v = p[2 * i + 1], m = q[2 * i], o = q[2 * i + 1];
-                            p[2 * i] = __fmaf_rn(u, co[i], -(v * si[i]));
-                            p[2 * i + 1] = __fmaf_rn(v, co[i], u * si[i]);
-                            q[2 * i] = __fmaf_rn(m, co[4 + i], -(o * si[4 + i]));
-                            q[2 * i + 1] = __fmaf_rn(o, co[4 + i], m * si[4 + i]);
-                        }
-                    } else {
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) {
-                            const float u = p[i], v = q[i];
-                            p[i] = __fmaf_rn(u, co[i], -(v * si[i]));
-                            q[i] = __fmaf_rn(v, co[i], u * si[i]);
-                        }
+                for (int u = 0; u < kRopeBatch; ++u) {
+                    x0[u] = x1[u] = make_uint4(0u, 0u, 0u, 0u);
+                    if (j + u < jb && h + u * GPW < heads) {
+                        x0[u] = src[u * GPW * VEC + v0];
+                        x1[u] = src[u * GPW * VEC + v1];
                     }
                 }
-                y0 = pack8(p);
-                y1 = pack8(q);
-                if (bad_pos)
-                    y0 = y1 = make_uint4(0x7FC07FC0u, 0x7FC07FC0u, 0x7FC07FC0u, 0x7FC07FC0u);
+                if (compute)
+                    load_angles();
+#pragma unroll
+                for (int u = 0; u < kRopeBatch; ++u) {
+                    if (j + u >= jb)
+                        break;
+                    if (compute)
+                        row(x0[u], x1[u], norm, w);
+                    if (h + u * GPW < heads && pos >= 0) {
+                        dst[v0] = x0[u];
+                        dst[v1] = x1[u];
+                    }
+                    dst += dst_step;
+                }
+                src += kRopeBatch * GPW * VEC;
+                h += kRopeBatch * GPW;
             }
-            if (!on || !store)
-                continue;
-            uint4 *dst = nullptr;
-            if (h < hq)
-                dst = a.q_out + t * a.q_out_stride + (int64_t)h * VEC;
-            else if (!a.k_cache)
-                dst = a.k_out + t * a.k_out_stride + (int64_t)(h - hq) * VEC;
-            else if (cached)
-                dst = (h < hq + hk ? a.k_cache : a.v_cache) + (slot >> 4) * a.block_stride + (slot & 15) * a.token_stride +
-                      (int64_t)(h < hq + hk ? h - hq : h - hq - hk) * a.head_stride;
-            if (dst) {
-                dst[v0] = y0;
-                dst[v1] = y1;
-            }
-        }
-        }
+        };
+        if (j0 < jq)
+            run(j0, min(j1, jq), hq, a.q + t * a.q_stride, a.q_out + t * a.q_out_stride, VEC, true, a.q_weight != nullptr,
+                reinterpret_cast<const float4 *>(s_w));
+        const int64_t at = a.k_cache ? (slot >> 4) * a.block_stride + (slot & 15) * a.token_stride : 0;
+        const bool cached = pos >= 0 && slot >= 0 && !slot_bad && !bad_pos;
+        if (j1 > jq && j0 < jq + jk && (cached || !a.k_cache))
+            run(max(j0 - jq, 0), min(j1 - jq, jk), hk, a.k + t * a.k_stride,
+                a.k_cache ? a.k_cache + at : a.k_out + t * a.k_out_stride, a.k_cache ? a.head_stride : VEC, true,
+                a.k_weight != nullptr, reinterpret_cast<const float4 *>(s_w + DH));
+        if (j1 > jq + jk && cached)
+            run(max(j0 - jq - jk, 0), j1 - jq - jk, hk, a.v + t * a.v_stride, a.v_cache + at, a.head_stride, false, false,
+                nullptr);
     }
 }
 
 cudaError_t launch_qk_norm_rope(const RopeArgs &args, ErrState *err, cudaStream_t stream, int num_sms, int64_t *grid)
 {
     RopeArgs a = args;
-    const int rows_tok = a.num_q_heads + a.num_kv_heads * (a.k_cache ? 2 : 1);
-    const int gpw = 512 / a.head_dim;  // groups of a warp
-    // Rows of a group: one while that leaves warps idle, more (their shared
-    // loads then count once) as long as 24 warps per SM have some.
-    const int64_t steps = (rows_tok + gpw - 1) / gpw;  // rows of a group that had the whole token
-    int64_t per = a.num_tokens * steps / ((int64_t)num_sms * 24);
-    per = per < 1 ? 1 : (per > 16 ? 16 : per);
-    if (per > steps)
-        per = steps;
+    const int gpw = 512 / a.head_dim;  // rows of a step
+    const int64_t jk = (a.num_kv_heads + gpw - 1) / gpw;
+    const int64_t steps = (a.num_q_heads + gpw - 1) / gpw + jk * (a.k_cache ? 2 : 1);
+    // Steps of a warp: one while that leaves warps idle, more (the token's
+    // angles and addresses then count once) as long as 16 warps per SM have some.
+    int64_t per = a.num_tokens * steps / ((int64_t)num_sms * 16);
+    per = per < 1 ? 1 : (per > steps ? steps : per);
     const int64_t parts = (steps + per - 1) / per;
-    a.rows_per_task = (int)((steps + parts - 1) / parts);  // parts of about one size
-    const int64_t tasks = a.num_tokens * ((steps + a.rows_per_task - 1) / a.rows_per_task);
+    a.steps_per_task = (int)((steps + parts - 1) / parts);  // parts of about one size
+    const int64_t tasks = a.num_tokens * ((steps + a.steps_per_task - 1) / a.steps_per_task);
     int64_t blocks = (tasks + kRopeThreads / 32 - 1) / (kRopeThreads / 32);
     if (blocks > (int64_t)num_sms * 64)
         blocks = (int64_t)num_sms * 64;
