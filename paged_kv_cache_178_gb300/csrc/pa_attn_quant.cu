@@ -68,7 +68,7 @@ constexpr int kGridSms = 152;       // SMs the grid is sized for
 // CTAs per SM that registers and shared memory are sized for
 template <int DH, int RN>
 constexpr int ctas_per_sm() { return DH == 128 && RN <= 8 ? 2 : 1; }
-// Shared-memory layout in bytes.  RN: query rows (8, 16 or 32).
+// Shared-memory layout in bytes.  RN: query rows (8, 16, 24 or 32).
 template <int DH, int RN>
 struct Layout {
     static constexpr int kPages = chunk_pages(DH);
@@ -701,29 +701,58 @@ __global__ void __launch_bounds__(kAllThreads, ctas_per_sm<DH, RN>()) quant_attn
         }
     };
     // The fold of n records, one after another from `recs`, by all computing
-    // threads, one element pair of a valid row at a time: emit(row, pair, state).
+    // threads, two element pairs of a valid row at a time: emit(row, pair,
+    // state).  Its time is round trips to L2: eight records of up to two such
+    // items are in flight.
     auto fold_records = [&](const float *recs, int n, int rv, auto emit) {
-        for (int e = tid; e < rv * (DH / 2); e += kThreads) {
-            const int row = e / (DH / 2), pair = e % (DH / 2);
-            const float *const rm = recs + row, *const ro = recs + (rec_hdr + (uint32_t)(row * DH + 2 * pair));
-            State<1, 1> acc;
-            acc.clear();
-            constexpr int U = 8;  // records in flight
-            for (int k0 = 0; k0 < n; k0 += U) {
-                State<1, 1> x[U];
+        constexpr int U = 8, I = 2;
+        const int items = rv * (DH / 4);
+        for (int e0 = tid; e0 < items; e0 += I * kThreads) {
+            State<1, 2> acc[I];
+            const float *rm[I], *ro[I];
+            int row[I], pair[I];
 #pragma unroll
-                for (int u = 0; u < U; ++u) {
-                    const uint32_t at = (uint32_t)min(k0 + u, n - 1) * rec_size;
-                    x[u].m[0] = __ldcg(rm + at);
-                    x[u].l[0] = __ldcg(rm + at + p.rows);
-                    x[u].o[0][0] = __ldcg(reinterpret_cast<const float2 *>(ro + at));
-                }
-#pragma unroll
-                for (int u = 0; u < U; ++u)
-                    if (k0 + u < n)
-                        acc.fold(x[u]);
+            for (int i = 0; i < I; ++i) {
+                const int e = min(e0 + i * kThreads, items - 1);
+                row[i] = e / (DH / 4);
+                pair[i] = e % (DH / 4) * 2;
+                rm[i] = recs + row[i];
+                ro[i] = recs + (rec_hdr + (uint32_t)(row[i] * DH + 2 * pair[i]));
+                acc[i].clear();
             }
-            emit(row, pair, acc);
+            const int count = e0 + kThreads < items ? I : 1;
+            for (int k0 = 0; k0 < n; k0 += U) {
+#pragma unroll
+                for (int i = 0; i < I; ++i) {
+                    if (i >= count)
+                        break;
+                    State<1, 2> x[U];
+#pragma unroll
+                    for (int u = 0; u < U; ++u) {
+                        const uint32_t at = (uint32_t)min(k0 + u, n - 1) * rec_size;
+                        x[u].m[0] = __ldcg(rm[i] + at);
+                        x[u].l[0] = __ldcg(rm[i] + at + p.rows);
+                        const float4 v = __ldcg(reinterpret_cast<const float4 *>(ro[i] + at));
+                        x[u].o[0][0] = make_float2(v.x, v.y);
+                        x[u].o[1][0] = make_float2(v.z, v.w);
+                    }
+#pragma unroll
+                    for (int u = 0; u < U; ++u)
+                        if (k0 + u < n)
+                            acc[i].fold(x[u]);
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < I; ++i)
+                if (i < count)
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) {
+                        State<1, 1> one;
+                        one.m[0] = acc[i].m[0];
+                        one.l[0] = acc[i].l[0];
+                        one.o[0][0] = acc[i].o[k][0];
+                        emit(row[i], pair[i] + k, one);
+                    }
         }
     };
     // Arrival of this CTA, its records written; true in the last of `n` CTAs.
@@ -872,7 +901,7 @@ cudaError_t set_attributes()
                                 (int)Layout<DH, RN>::bytes(kScanMaxSeqs));
 }
 
-static int rows_capacity(int rows) { return rows <= 8 ? 8 : rows <= 16 ? 16 : 32; }
+static int rows_capacity(int rows) { return rows <= 8 ? 8 : rows <= 16 ? 16 : rows <= 24 ? 24 : 32; }
 
 // CTAs of the grid: one wave, fewer when there are fewer chunks.
 static int64_t grid_of(int dh, int rn, int64_t max_chunks)
@@ -966,10 +995,11 @@ cudaError_t launch_quant_attention(const QuantAttnArgs &a, ErrState *err, cudaSt
     case 128:
         go(rn == 8    ? qa::launch<128, 8>
            : rn == 16 ? qa::launch<128, 16>
+           : rn == 24 ? qa::launch<128, 24>
                       : qa::launch<128, 32>);
         break;
     case 256:
-        go(rn == 8 ? qa::launch<256, 8> : rn == 16 ? qa::launch<256, 16> : qa::launch<256, 32>);
+        go(rn == 8 ? qa::launch<256, 8> : rn == 16 ? qa::launch<256, 16> : rn == 24 ? qa::launch<256, 24> : qa::launch<256, 32>);
         break;
     case 512:
         go(rn == 8 ? qa::launch<512, 8> : qa::launch<512, 16>);
@@ -986,7 +1016,8 @@ cudaError_t init_quant_attention_attributes()
     if ((e = qa::set_attributes<128, 8>()) != cudaSuccess || (e = qa::set_attributes<128, 16>()) != cudaSuccess ||
         (e = qa::set_attributes<128, 32>()) != cudaSuccess || (e = qa::set_attributes<256, 8>()) != cudaSuccess ||
         (e = qa::set_attributes<256, 16>()) != cudaSuccess || (e = qa::set_attributes<256, 32>()) != cudaSuccess ||
-        (e = qa::set_attributes<512, 8>()) != cudaSuccess)
+        (e = qa::set_attributes<512, 8>()) != cudaSuccess || (e = qa::set_attributes<128, 24>()) != cudaSuccess ||
+        (e = qa::set_attributes<256, 24>()) != cudaSuccess)
         return e;
     return qa::set_attributes<512, 16>();
 }
