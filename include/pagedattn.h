@@ -519,18 +519,16 @@ PA_API size_t pa_paged_attention_quant_workspace_size(int32_t num_seqs, int32_t 
  *     (within that limit).
  *   - More rows: the selected pages are read back into the workspace (as by
  *     pa_dequantize_kv), and pa_paged_attention's kernel runs over them:
- *     bitwise its results on the read-back pool.  More than max_pages
- *     selected pages: PA_ERR_WORKSPACE is latched (index = the pages) and all
- *     rows are NaN.
+ *     bitwise its results on the read-back pool.
  *   The two round differently.
+ *   - More than max_pages (> 0) selected pages: PA_ERR_WORKSPACE is latched
+ *     (index = the pages) and all rows are NaN.
  *   - A bad block id makes all rows of its request NaN.  Keys past a
  *     request's length never matter, whatever their bytes.
- *   - workspace: as for pa_paged_attention, sized by
- *     pa_paged_attention_quant_workspace_size for the call's bounds; one
- *     workspace may serve calls with different bounds (one after the other)
- *     if it is large enough for each.
- * num_seqs <= 8192; with few rows also num_seqs * Hkv * (1 + the number of
- * 8192-key spans (4096 at head dim 512) of max_seq_len) <= 262144.
+ *   - workspace: at least pa_paged_attention_quant_workspace_size(...) bytes
+ *     for the call's bounds, 256-byte aligned; it needs no particular contents,
+ *     and calls with different bounds may share it one after another.
+ * num_seqs <= 2048.
  */
 PA_API pa_status pa_paged_attention_quant(const void *q, int64_t num_q_tokens, int64_t q_tok_stride,
                                           int32_t num_q_heads, const pa_quant_cache *cache,

@@ -1040,18 +1040,14 @@ pa_status pa_dequantize_kv(const pa_quant_cache *cache, const int32_t *block_tab
     return cuda_status(e);
 }
 
-// The workspace of an attention call over a 4-bit cache.  The arrival
-// counters of the direct kernel have a region of their own at its head, the
-// same for all bounds, so whatever another call leaves behind it they stay
-// zero between calls; the counters of the BF16 attention over read-back pages
-// are cleared by the read-back itself.
-constexpr int64_t kQuantMaxCounters = 262144;
+// The workspace of an attention call over a 4-bit cache.  Nothing in it has to
+// outlast a call: the direct kernels write what they read, and the counters of
+// the BF16 attention over read-back pages are cleared by the read-back.
 struct QuantPlan {
     bool direct;
-    size_t records;                     // direct: chunk records
-    int64_t pages;                      // otherwise: read-back pages,
+    int64_t pages;                      // not direct: read-back pages,
     int32_t cols;                       // compact table columns,
-    size_t k, v, tables, inner, bytes;  // and offsets
+    size_t v, tables, inner, bytes;     // and offsets (K at 0)
     AttnPlan attn;
 };
 
@@ -1065,17 +1061,12 @@ static pa_status plan_quant(int32_t num_seqs, int32_t hq, int32_t hkv, int32_t d
         return PA_ERR_INVALID_ARG;
     if (!plan_attention(num_seqs, hq, hkv, dh, max_query_len, max_seq_len, &pl->attn))
         return PA_ERR_UNSUPPORTED;
-    if (num_seqs > kScanMaxSeqsHost || (int64_t)num_seqs * (((int64_t)max_seq_len + 15) / 16) > INT32_MAX)
+    if (num_seqs > kQuantMaxSeqsHost || (int64_t)num_seqs * (((int64_t)max_seq_len + 15) / 16) > INT32_MAX)
         return PA_ERR_UNSUPPORTED;
     const int64_t rows = (int64_t)max_query_len * (hq / hkv);
     pl->direct = rows <= quant_attn_max_rows(dh);
-    const size_t counters = (size_t)kQuantMaxCounters * 4;
     if (pl->direct) {
-        const QuantAttnSpace sp = quant_attn_space(num_seqs, hkv, dh, (int)rows, max_seq_len);
-        if (sp.counters > kQuantMaxCounters)
-            return PA_ERR_UNSUPPORTED;
-        pl->records = counters;
-        pl->bytes = counters + sp.chunk_bytes + sp.span_bytes;
+        pl->bytes = quant_attn_bytes(num_seqs, hkv, dh, (int)rows, max_seq_len, max_pages);
         return PA_OK;
     }
     // The BF16 attention gives the same bits with the keys split over CTAs or
@@ -1093,8 +1084,7 @@ static pa_status plan_quant(int32_t num_seqs, int32_t hq, int32_t hkv, int32_t d
     if (max_pages > 0 && max_pages < pl->pages)
         pl->pages = max_pages;
     const size_t view = (size_t)pl->pages * 16 * hkv * dh * 2;
-    pl->k = counters;
-    pl->v = pl->k + round256(view);
+    pl->v = round256(view);
     pl->tables = pl->v + round256(view);
     pl->inner = pl->tables + round256((size_t)num_seqs * pl->cols * 4);
     pl->bytes = pl->inner + pl->attn.ws_bytes;
@@ -1169,8 +1159,8 @@ pa_status pa_paged_attention_quant(const void *q, int64_t num_q_tokens, int64_t 
         a.scale = scale;
         a.out = out;
         a.lse = lse;
-        a.counters = reinterpret_cast<uint32_t *>(ws);
-        a.records = reinterpret_cast<float *>(ws + pl.records);
+        a.max_pages = max_pages;
+        a.workspace = ws;
         return cuda_status(launch_quant_attention(a, err, s, g_last_info, sizeof g_last_info));
     }
     // read the selected pages back, then the BF16 attention over them
@@ -1178,7 +1168,7 @@ pa_status pa_paged_attention_quant(const void *q, int64_t num_q_tokens, int64_t 
     int32_t *tables = reinterpret_cast<int32_t *>(ws + pl.tables);
     int64_t grid = 0;
     cudaError_t e = launch_dequantize_kv(quant_pool(cache), block_tables, max_blocks_per_seq, seq_lens, num_seqs,
-                                         ws + pl.k, ws + pl.v, pl.pages, tables, cols, nullptr, true, ws + pl.inner,
+                                         ws, ws + pl.v, pl.pages, tables, cols, nullptr, true, ws + pl.inner,
                                          pl.attn.ws_counter_bytes, err, s, nsm, &grid);
     if (e != cudaSuccess)
         return cuda_status(e);
@@ -1187,7 +1177,7 @@ pa_status pa_paged_attention_quant(const void *q, int64_t num_q_tokens, int64_t 
     a.num_q_tokens = num_q_tokens;
     a.q_tok_stride = q_tok_stride;
     a.num_q_heads = num_q_heads;
-    a.k = ws + pl.k;
+    a.k = ws;
     a.v = ws + pl.v;
     a.num_blocks = pl.pages;
     a.num_kv_heads = hkv;

@@ -26,21 +26,22 @@
 //     shared-memory reads per page against 32.)
 //
 // Fixed arithmetic (a row's results do not depend on the batch or the grid):
-//   chunks of 512 keys (256 at head dim 256, 128 at 512) from key 0, each with its own exact maximum; a chunk's
-//   row sum is, per warp, a butterfly over its keys, then the eight warps'
-//   sums pairwise; chunk states fold left to right (State::fold) within spans
-//   of 32 chunks, and the span states left to right.
+//   chunks of 512 keys (256 at head dim 256, 128 at 512) from key 0, each with
+//   its own exact maximum; a chunk's row sum is, per warp, a butterfly over its
+//   keys, then the eight warps' sums pairwise; chunk states fold left to right
+//   (State::fold) within spans of 16 chunks, and the span states left to right.
 //
 // A CTA (8 warps) per chunk: each warp scores its pages; row maxima are
 // exchanged (barrier); P goes to shared memory in fragment order, the V scales
-// as one f16 pair each (barrier); each warp multiplies P by 32
-// head-dim elements of the pages (at head dim 128 of half of the pages, the
-// halves are added through shared memory, with the row sums; barrier).  A
-// ninth warp copies the next chunk (cp.async.bulk): K during the second product,
-// V during the first one.  The chunks of all (request, KV head) groups are dealt out as
-// equal contiguous ranges.  A span inside one range is folded in registers; the
-// chunks of a span cut by a range end become records, folded by the last CTA
-// to arrive, and so do the spans of a group of several.  No CTA waits for another.
+// as one f16 pair each (barrier); each warp multiplies P by 32 head-dim
+// elements of the pages (at head dim 128 of half of the pages, the halves are
+// added through shared memory, with the row sums; barrier).  A ninth warp
+// copies the next chunk (cp.async.bulk): K during the second product, V during
+// the first one.  The chunks of all (request, KV head) groups are dealt out as
+// contiguous ranges of about equal weight; the state of a chunk becomes a
+// record, unless it is its group's only one, and a second kernel folds the
+// records.  (Folded by the last CTA to arrive instead, 32 records of eight rows
+// took that CTA 5 us, 17 of twenty rows at head dim 256 13 us.)
 #include <cstdio>
 #include <type_traits>
 
@@ -61,7 +62,11 @@ constexpr int kAllThreads = kThreads + 32;  // and the copying warp
 __host__ __device__ constexpr int pages_per_warp(int dh) { return dh == 128 ? 4 : dh == 256 ? 2 : 1; }
 __host__ __device__ constexpr int chunk_pages(int dh) { return kWarps * pages_per_warp(dh); }
 __host__ __device__ constexpr int chunk_keys(int dh) { return 16 * chunk_pages(dh); }
-constexpr int kSpan = 32;           // chunks per span
+constexpr int kSpan = 16;           // chunks per span of the fold
+// What a chunk costs without its pages, in pages, when the chunks are dealt out:
+// 64 requests 31.5 us at 8, 30.5 at 18, 32.4 at 32.
+constexpr int kChunkCost = 18;
+constexpr int kQuantMaxSeqs = 2048; // two offsets of each in shared memory
 constexpr float kShift = 15.f;      // p is scaled by 2^kShift (largest f16: 2^16)
 constexpr int kGridSms = 152;       // SMs the grid is sized for
 
@@ -86,11 +91,11 @@ struct Layout {
     static constexpr int bad = nan + 2 * (DH / 16) * 4;
     static constexpr int flags = bad + 16;
     static constexpr int bars = flags + 16;         // full and empty, of K and of V
-    static constexpr int sums = bars + 32;
-    static constexpr int pre = sums + (kWarps + 2) * 8;  // [num_seqs + 1] int32
-    static_assert(q % 16 == 0 && spread % 16 == 0 && max % 16 == 0 && bad % 8 == 0 && bars % 8 == 0, "layout");
-    static_assert(pre + (kScanMaxSeqs + 1) * 4 <= (int)kMaxSmemPerBlock, "shared memory");
-    static size_t bytes(int num_seqs) { return (size_t)pre + 4 * ((size_t)num_seqs + 1); }
+    static constexpr int sums = bars + 32;           // 16 bytes for each of nine warps
+    static constexpr int pre = sums + (kWarps + 2) * 16;  // two arrays [num_seqs + 1] int32
+    static_assert(q % 16 == 0 && spread % 16 == 0 && max % 16 == 0 && bad % 8 == 0 && bars % 16 == 0, "layout");
+    static_assert(pre + (kQuantMaxSeqs + 1) * 8 <= (int)kMaxSmemPerBlock, "shared memory");
+    static size_t bytes(int num_seqs) { return (size_t)pre + 8 * ((size_t)num_seqs + 1); }
 };
 
 struct Params {
@@ -102,16 +107,13 @@ struct Params {
     const int32_t *block_tables, *seq_lens, *qsl;
     int32_t max_blocks, num_seqs, hq, hkv, group, max_query_len, max_seq_len;
     int32_t rows;       // rows of a record
-    int32_t slots;      // chunk records of a cut span at most
-    int32_t spans;      // spans of a group at most
+    int64_t max_pages;  // pages of all requests together
     float score_scale;  // scale * log2(e) * k_scale
     float v_scale;
     __nv_bfloat16 *out;
     float *lse;
-    uint32_t *span_counters;   // [group][spans]
-    uint32_t *group_counters;  // [group]
-    float *chunk_records;      // [CTA][slots]: of the span that starts in the CTA's range and does not end there
-    float *span_records;       // [group][spans]
+    float *records;     // [chunk]: m, l, O
+    int32_t *offsets;   // [num_seqs + 1]: chunks of a KV head before each request
     ErrState *err;
 };
 
@@ -281,8 +283,9 @@ __global__ void __launch_bounds__(kAllThreads, ctas_per_sm<DH, RN>()) quant_attn
     int *const s_lim = reinterpret_cast<int *>(smem + Lay::lim);      // last key of a row
     int *const s_nan = reinterpret_cast<int *>(smem + Lay::nan);      // [chunk parity][DH/16] first NaN key of an element block
     volatile int *const s_bad = reinterpret_cast<int *>(smem + Lay::bad);  // [chunk parity] 1 + the last chunk with a bad block id
-    volatile int *const s_flags = reinterpret_cast<int *>(smem + Lay::flags);  // [0] abort [1] last to arrive
+    volatile int *const s_flags = reinterpret_cast<int *>(smem + Lay::flags);  // [0] abort
     int32_t *const s_pre = reinterpret_cast<int32_t *>(smem + Lay::pre);
+    int32_t *const s_weight = s_pre + p.num_seqs + 1;
     const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32, g = lane / 4, t = lane % 4;
     const int G = p.group, hkv = p.hkv;
     enum { kFullK, kFullV, kEmptyK, kEmptyV };
@@ -299,18 +302,28 @@ __global__ void __launch_bounds__(kAllThreads, ctas_per_sm<DH, RN>()) quant_attn
         s_bad[0] = s_bad[1] = 0;
         fence_barrier_init();
     }
-    const long long tot = block_exclusive_sums<kAllThreads>(
-        p.num_seqs, s_pre, reinterpret_cast<long long *>(smem + Lay::sums), [&](int b) {
+    // chunks of a KV head of each request, and their weights: pages, and what
+    // a chunk costs without any
+    longlong2 total;
+    block_exclusive_sums2<kAllThreads>(
+        p.num_seqs, s_pre, s_weight, reinterpret_cast<longlong2 *>(smem + Lay::sums), total,
+        [&](int b, int &chunks, int &weight) {
             const Meta m = meta_of(p, b);
             if (!m.ok && blockIdx.x == 0)
                 record_error(p.err, kErrBadMetadata, b);
-            return m.ok && m.qn > 0 ? (m.L + kChunk - 1) / kChunk : 0;
+            if (m.ok && m.qn > 0) {
+                chunks = (m.L + kChunk - 1) / kChunk;
+                weight = (m.L + 15) / 16 + kChunkCost * chunks;
+            }
         });
+    const bool over = total.y - kChunkCost * total.x > p.max_pages;
+    if (over && blockIdx.x == 0 && tid == 0)
+        record_error(p.err, kErrBudget, total.y - kChunkCost * total.x);
     for (int b = blockIdx.x; b < p.num_seqs; b += gridDim.x) {
-        if (s_pre[b + 1] != s_pre[b])
+        if (s_pre[b + 1] != s_pre[b] && !over)
             continue;
         const Meta m = meta_of(p, b);
-        if (m.sane && !m.ok) {  // bad lengths: NaN rows
+        if (m.sane && (!m.ok || over)) {  // bad lengths, or no room for the records: NaN rows
             const int64_t first = (int64_t)m.qs * p.hq, n = (int64_t)m.qn * p.hq;
             for (int64_t i = tid; i < n * DH; i += kAllThreads)
                 p.out[first * DH + i] = __ushort_as_bfloat16(0x7FC0);
@@ -319,13 +332,34 @@ __global__ void __launch_bounds__(kAllThreads, ctas_per_sm<DH, RN>()) quant_attn
                     p.lse[first + i] = __int_as_float(0x7FC00000);
         }
     }
-    const int64_t T = tot * hkv;
-    const int64_t ctas = T < (int64_t)gridDim.x ? T : (int64_t)gridDim.x;
-    if ((int64_t)blockIdx.x >= ctas)
+    if (blockIdx.x == 0)  // for the folding kernel
+        for (int b = tid; b <= p.num_seqs; b += kAllThreads)
+            p.offsets[b] = over ? 0 : s_pre[b];
+    if (over)
         return;
-    auto range_start = [&](int64_t cta) { return div_floor(cta * T, ctas); };
-    auto cta_of = [&](int64_t x) { return div_floor((x + 1) * ctas + T - 1, T) - 1; };
-    const int64_t lo = range_start(blockIdx.x), hi = range_start((int64_t)blockIdx.x + 1);
+    // The chunks in order, a group's one after another, are cut where their
+    // weights add up to equal shares: a CTA takes those that start in its share
+    // (one each when there are no more chunks than CTAs).
+    const int64_t T = total.x * hkv, W = total.y * hkv;
+    int64_t lo = blockIdx.x, hi = lo + 1;
+    if (T > (int64_t)gridDim.x) {
+        // lane 0 of each warp finds the start of this share, lane 1 of the next
+        constexpr int kFull = kPages + kChunkCost;  // weight of a whole chunk
+        const int64_t cta = (int64_t)blockIdx.x + (lane & 1);
+        int64_t start = T;
+        if (cta < gridDim.x) {
+            const int64_t at = div_floor(cta * W + gridDim.x - 1, gridDim.x);
+            const int b = owner_of(s_weight, p.num_seqs, (int)div_floor(at, hkv));
+            const int n = s_pre[b + 1] - s_pre[b], w = s_weight[b + 1] - s_weight[b];
+            const int64_t rem = at - (int64_t)hkv * s_weight[b];
+            const int h = (int)div_floor(rem, w), lc = ((int)(rem - (int64_t)h * w) + kFull - 1) / kFull;
+            start = (int64_t)hkv * s_pre[b] + (int64_t)h * n + min(lc, n);
+        }
+        lo = __shfl_sync(0xffffffffu, start, 0);
+        hi = __shfl_sync(0xffffffffu, start, 1);
+    }
+    if (lo >= hi || lo >= T)
+        return;
 
     const int chunks = (int)(hi - lo);
     if (warp == kWarps) {
@@ -397,7 +431,6 @@ __global__ void __launch_bounds__(kAllThreads, ctas_per_sm<DH, RN>()) quant_attn
 
     Chunk<DH> c;
     c.at(p, s_pre, lo);
-    St span;  // the span so far
     const uint32_t rec_hdr = (uint32_t)part_header_floats(p.rows), rec_size = (uint32_t)part_record_floats(p.rows, DH);
 
     // ------------------------------------------------ one chunk's state --
@@ -700,76 +733,6 @@ __global__ void __launch_bounds__(kAllThreads, ctas_per_sm<DH, RN>()) quant_attn
                 __stcg(reinterpret_cast<float2 *>(rec + (rec_hdr + (uint32_t)(row * DH + 2 * state_pair(i)))), st.o[i][r]);
         }
     };
-    // The fold of n records, one after another from `recs`, by all computing
-    // threads, two element pairs of a valid row at a time: emit(row, pair,
-    // state).  Its time is round trips to L2: eight records of up to two such
-    // items are in flight.
-    auto fold_records = [&](const float *recs, int n, int rv, auto emit) {
-        constexpr int U = 8, I = 2;
-        const int items = rv * (DH / 4);
-        for (int e0 = tid; e0 < items; e0 += I * kThreads) {
-            State<1, 2> acc[I];
-            const float *rm[I], *ro[I];
-            int row[I], pair[I];
-#pragma unroll
-            for (int i = 0; i < I; ++i) {
-                const int e = min(e0 + i * kThreads, items - 1);
-                row[i] = e / (DH / 4);
-                pair[i] = e % (DH / 4) * 2;
-                rm[i] = recs + row[i];
-                ro[i] = recs + (rec_hdr + (uint32_t)(row[i] * DH + 2 * pair[i]));
-                acc[i].clear();
-            }
-            const int count = e0 + kThreads < items ? I : 1;
-            for (int k0 = 0; k0 < n; k0 += U) {
-#pragma unroll
-                for (int i = 0; i < I; ++i) {
-                    if (i >= count)
-                        break;
-                    State<1, 2> x[U];
-#pragma unroll
-                    for (int u = 0; u < U; ++u) {
-                        const uint32_t at = (uint32_t)min(k0 + u, n - 1) * rec_size;
-                        x[u].m[0] = __ldcg(rm[i] + at);
-                        x[u].l[0] = __ldcg(rm[i] + at + p.rows);
-                        const float4 v = __ldcg(reinterpret_cast<const float4 *>(ro[i] + at));
-                        x[u].o[0][0] = make_float2(v.x, v.y);
-                        x[u].o[1][0] = make_float2(v.z, v.w);
-                    }
-#pragma unroll
-                    for (int u = 0; u < U; ++u)
-                        if (k0 + u < n)
-                            acc[i].fold(x[u]);
-                }
-            }
-#pragma unroll
-            for (int i = 0; i < I; ++i)
-                if (i < count)
-#pragma unroll
-                    for (int k = 0; k < 2; ++k) {
-                        State<1, 1> one;
-                        one.m[0] = acc[i].m[0];
-                        one.l[0] = acc[i].l[0];
-                        one.o[0][0] = acc[i].o[k][0];
-                        emit(row[i], pair[i] + k, one);
-                    }
-        }
-    };
-    // Arrival of this CTA, its records written; true in the last of `n` CTAs.
-    auto last_to_arrive = [&](uint32_t *counter, int n) {
-        sync();
-        if (tid == 0) {
-            // releases this CTA's records and, for the last arrival, acquires the others'
-            uint32_t old;
-            asm volatile("atom.acq_rel.gpu.global.add.u32 %0, [%1], 1;" : "=r"(old) : "l"(counter) : "memory");
-            const bool last = old == (uint32_t)(n - 1);
-            if (last)
-                *counter = 0u;  // ready for the next call
-            s_flags[1] = last;
-        }
-        sync();
-        return s_flags[1] != 0;
-    };
     auto output_pair = [&](int row, int pair, float2 o, float m, float l) {
         const int64_t at = (int64_t)(c.qs + row / G) * p.hq + c.kvh * G + row % G;
         const float f = __frcp_rn(l) * p.v_scale;
@@ -777,15 +740,8 @@ __global__ void __launch_bounds__(kAllThreads, ctas_per_sm<DH, RN>()) quant_attn
         if (pair == 0 && p.lse)
             p.lse[at] = lse_of(m, l * 0x1p-15f);
     };
-    auto output_folded = [&](int row, int pair, const State<1, 1> &x) {
-        output_pair(row, pair, x.o[0][0], x.m[0], x.l[0]);
-    };
-
-    bool span_whole = false;
-    float *span_area = nullptr;      // the cut span's chunk records
-    int span_ctas = 0;               // and the CTAs that write them
     for (int step = 0; step < chunks; ++step) {
-        const bool first_chunk = step == 0, last_chunk = step + 1 == chunks;
+        const bool first_chunk = step == 0;
         if (!first_chunk)
             c.next(p, s_pre);
         if (first_chunk || c.lc == 0) {
@@ -825,18 +781,6 @@ __global__ void __launch_bounds__(kAllThreads, ctas_per_sm<DH, RN>()) quant_attn
             }
             sync();
         }
-        if (first_chunk || c.lc % kSpan == 0) {
-            const int64_t sa = lo + step - c.lc % kSpan;  // the span's chunks: [sa, sb)
-            const int64_t sb = sa + min(kSpan, c.nch - (c.lc - c.lc % kSpan));
-            span_whole = sa >= lo && sb <= hi;
-            span.clear();
-            if (!span_whole) {
-                const int64_t first = sa >= lo ? (int64_t)blockIdx.x : cta_of(sa);
-                span_area = p.chunk_records + first * p.slots * (int64_t)rec_size;
-                span_ctas = (int)((sb <= hi ? (int64_t)blockIdx.x : cta_of(sb - 1)) - first) + 1;
-            }
-        }
-
         St st;
         const bool masked = c.lc * kChunk + kChunk > c.L - c.qn + 1;
         const int bad = masked ? chunk_state(std::true_type{}, step, st) : chunk_state(std::false_type{}, step, st);
@@ -851,54 +795,121 @@ __global__ void __launch_bounds__(kAllThreads, ctas_per_sm<DH, RN>()) quant_attn
         }
 
         const int rv = c.qn * G;
-        if (span_whole)
-            span.fold(st);
-        else
-            write_record(span_area + (uint32_t)(c.lc % kSpan) * rec_size, st, rv);
-        const bool span_end = c.lc + 1 == c.nch || (c.lc + 1) % kSpan == 0;
-        if (!span_end && !last_chunk)
-            continue;
-        const int sp = c.lc / kSpan, nsp = (c.nch + kSpan - 1) / kSpan;
-        const int64_t grp = (int64_t)c.b * hkv + c.kvh;
-        float *const span_recs = p.span_records + grp * p.spans * (int64_t)rec_size, *const span_rec = span_recs + (int64_t)sp * rec_size;
-        if (span_whole) {
-            if (nsp == 1) {
-#pragma unroll
-                for (int r = 0; r < NR; ++r)
-                    if (state_row(r) < rv)
-#pragma unroll
-                        for (int i = 0; i < NP; ++i)
-                            output_pair(state_row(r), state_pair(i), span.o[i][r], span.m[r], span.l[r]);
-                continue;
-            }
-            write_record(span_rec, span, rv);
+        if (c.nch > 1) {
+            write_record(p.records + (lo + step) * (int64_t)rec_size, st, rv);
         } else {
-            if (!last_to_arrive(p.span_counters + grp * p.spans + sp, span_ctas))
-                continue;
-            const int n = min(kSpan, c.nch - sp * kSpan);
-            if (nsp == 1) {
-                fold_records(span_area, n, rv, output_folded);
-                continue;
-            }
-            fold_records(span_area, n, rv, [&](int row, int pair, const State<1, 1> &x) {
-                if (pair == 0) {
-                    __stcg(span_rec + row, x.m[0]);
-                    __stcg(span_rec + p.rows + row, x.l[0]);
-                }
-                __stcg(reinterpret_cast<float2 *>(span_rec + (rec_hdr + (uint32_t)(row * DH + 2 * pair))), x.o[0][0]);
-            });
+#pragma unroll
+            for (int r = 0; r < NR; ++r)
+                if (state_row(r) < rv)
+#pragma unroll
+                    for (int i = 0; i < NP; ++i)
+                        output_pair(state_row(r), state_pair(i), st.o[i][r], st.m[r], st.l[r]);
         }
-        // one of several spans is folded and written: the last one folds them
-        if (last_to_arrive(p.group_counters + grp, nsp))
-            fold_records(span_recs, nsp, rv, output_folded);
     }
+}
+
+// Folds the chunk records of the groups with several chunks.  Bound by round
+// trips to L2: a warp folds a span of a row, all its records in flight (at head
+// dim 256 eight of them, at 512 four), all rows and all spans (16 / rows per
+// CTA at a time) side by side; then one warp folds the spans of a row.  131k
+// keys on 8 KV heads: 32.2 us with spans of 32 chunks, 31.6 of 8, 30.1 of 16.
+constexpr int kFoldThreads = 512;  // at most
+
+template <int DH>
+__global__ void __launch_bounds__(kFoldThreads) quant_fold_kernel(const Params p, int SW)
+{
+    constexpr int V = DH / 128;  // float4 of a lane
+    __shared__ __align__(16) float s_state[kFoldThreads / 32][DH + 4];
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    const int row = blockIdx.y * (blockDim.x / 32 / SW) + warp / SW, slot = warp % SW;
+    const int b = blockIdx.x / p.hkv, kvh = blockIdx.x - b * p.hkv;
+    griddep_wait();
+    griddep_launch_dependents();
+    const int c0 = __ldcg(p.offsets + b), nch = __ldcg(p.offsets + b + 1) - c0;
+    const int qs = __ldg(p.qsl + b), qn = __ldg(p.qsl + b + 1) - qs;
+    if (nch <= 1)  // none, or written already
+        return;
+    const bool live = row < qn * p.group;
+    const uint32_t hdr = (uint32_t)part_header_floats(p.rows), size = (uint32_t)part_record_floats(p.rows, DH);
+    const float *rec = p.records + ((int64_t)p.hkv * c0 + (int64_t)kvh * nch) * size + (live ? row : 0);
+    const float *ro = rec - (live ? row : 0) + (hdr + (uint32_t)((live ? row : 0) * DH + 4 * lane));
+    State<1, 2 * V> acc;
+    acc.clear();
+    const int spans = (nch + kSpan - 1) / kSpan;
+    for (int s0 = 0; s0 < spans; s0 += SW) {
+        State<1, 2 * V> st;
+        st.clear();
+        const int first = (s0 + slot) * kSpan, n = live ? min(kSpan, nch - first) : 0;
+        constexpr int U = V == 1 ? 16 : 8 / (V / 2);  // records in flight
+        for (int k0 = 0; k0 < n; k0 += U) {
+            State<1, 2 * V> x[U];
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                if (k0 + u >= n)
+                    break;
+                const int64_t at = (int64_t)(first + k0 + u) * size;
+                x[u].m[0] = __ldcg(rec + at);
+                x[u].l[0] = __ldcg(rec + at + p.rows);
+#pragma unroll
+                for (int i = 0; i < V; ++i) {
+                    const float4 v = __ldcg(reinterpret_cast<const float4 *>(ro + at + 128 * i));
+                    x[u].o[2 * i][0] = make_float2(v.x, v.y);
+                    x[u].o[2 * i + 1][0] = make_float2(v.z, v.w);
+                }
+            }
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+                if (k0 + u < n)
+                    st.fold(x[u]);
+        }
+        if (SW == 1) {
+            acc.fold(st);
+            continue;
+        }
+        // the spans of this pass, in order, by the row's first warp
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+            *reinterpret_cast<float4 *>(&s_state[warp][4 * lane + 128 * i]) =
+                make_float4(st.o[2 * i][0].x, st.o[2 * i][0].y, st.o[2 * i + 1][0].x, st.o[2 * i + 1][0].y);
+        if (lane == 0) {
+            s_state[warp][DH] = st.m[0];
+            s_state[warp][DH + 1] = st.l[0];
+        }
+        __syncthreads();
+        if (slot == 0)
+            for (int k = 0; k < SW && s0 + k < spans; ++k) {
+                const float *t = s_state[warp + k];
+                State<1, 2 * V> x;
+                x.m[0] = t[DH];
+                x.l[0] = t[DH + 1];
+#pragma unroll
+                for (int i = 0; i < V; ++i) {
+                    const float4 v = *reinterpret_cast<const float4 *>(t + 4 * lane + 128 * i);
+                    x.o[2 * i][0] = make_float2(v.x, v.y);
+                    x.o[2 * i + 1][0] = make_float2(v.z, v.w);
+                }
+                acc.fold(x);
+            }
+        __syncthreads();
+    }
+    if (!live || slot != 0)
+        return;
+    const int64_t at = (int64_t)(qs + row / p.group) * p.hq + kvh * p.group + row % p.group;
+    const float f = __frcp_rn(acc.l[0]) * p.v_scale;
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+        *reinterpret_cast<uint2 *>(p.out + at * DH + 4 * lane + 128 * i) =
+            make_uint2(pack_bf16x2(acc.o[2 * i][0].x * f, acc.o[2 * i][0].y * f),
+                       pack_bf16x2(acc.o[2 * i + 1][0].x * f, acc.o[2 * i + 1][0].y * f));
+    if (lane == 0 && p.lse)
+        p.lse[at] = lse_of(acc.m[0], acc.l[0] * 0x1p-15f);
 }
 
 template <int DH, int RN>
 cudaError_t set_attributes()
 {
     return cudaFuncSetAttribute(quant_attn_kernel<DH, RN>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                (int)Layout<DH, RN>::bytes(kScanMaxSeqs));
+                                (int)Layout<DH, RN>::bytes(kQuantMaxSeqs));
 }
 
 static int rows_capacity(int rows) { return rows <= 8 ? 8 : rows <= 16 ? 16 : rows <= 24 ? 24 : 32; }
@@ -911,13 +922,13 @@ static int64_t grid_of(int dh, int rn, int64_t max_chunks)
 }
 
 static int64_t chunks_of(int dh, int32_t len) { return ((int64_t)len + chunk_keys(dh) - 1) / chunk_keys(dh); }
-static int64_t spans_of(int dh, int32_t len) { return (chunks_of(dh, len) + kSpan - 1) / kSpan; }
-
-// Chunk records of a cut span at most.
-static int slots_of(int dh, int32_t len)
+// Chunks of all groups at most.
+static int64_t max_chunks_of(int32_t num_seqs, int32_t hkv, int dh, int32_t max_seq_len, int64_t max_pages)
 {
-    const int64_t n = chunks_of(dh, len);
-    return (int)(n < kSpan ? n : kSpan);
+    int64_t per_head = (int64_t)num_seqs * chunks_of(dh, max_seq_len);
+    if (max_pages > 0 && max_pages / chunk_pages(dh) + num_seqs < per_head)
+        per_head = max_pages / chunk_pages(dh) + num_seqs;  // whole ones, and one in part a request
+    return per_head * hkv;
 }
 
 template <int DH, int RN>
@@ -934,21 +945,28 @@ cudaError_t launch(const Params &p, cudaStream_t stream, int64_t grid)
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, quant_attn_kernel<DH, RN>, p);
+    cudaError_t e = cudaLaunchKernelEx(&cfg, quant_attn_kernel<DH, RN>, p);
+    const int64_t chunks = chunks_of(DH, p.max_seq_len);
+    if (e != cudaSuccess || chunks <= 1)
+        return e;
+    int sw = 1;  // spans of a row side by side
+    while (sw < kFoldThreads / 32 && sw * kSpan < chunks)
+        sw *= 2;
+    const int most = kFoldThreads / 32 / sw, rows = p.rows < most ? p.rows : most;
+    cfg.gridDim = dim3((unsigned)(p.num_seqs * p.hkv), (unsigned)((p.rows + rows - 1) / rows));
+    cfg.blockDim = dim3(32 * sw * rows);
+    cfg.dynamicSmemBytes = 0;
+    return cudaLaunchKernelEx(&cfg, quant_fold_kernel<DH>, p, sw);
 }
 
 }  // namespace qa
 
-QuantAttnSpace quant_attn_space(int32_t num_seqs, int32_t num_kv_heads, int32_t head_dim, int rows, int32_t max_seq_len)
+size_t quant_attn_bytes(int32_t num_seqs, int32_t num_kv_heads, int32_t head_dim, int rows, int32_t max_seq_len,
+                        int64_t max_pages)
 {
-    QuantAttnSpace s{};
-    const int64_t groups = (int64_t)num_seqs * num_kv_heads, max_chunks = groups * qa::chunks_of(head_dim, max_seq_len);
-    const int64_t grid = qa::grid_of(head_dim, qa::rows_capacity(rows), max_chunks);
-    const size_t rec = (size_t)part_record_floats(rows, head_dim) * 4;
-    s.counters = groups * (qa::spans_of(head_dim, max_seq_len) + 1);
-    s.chunk_bytes = (size_t)grid * qa::slots_of(head_dim, max_seq_len) * rec;
-    s.span_bytes = qa::spans_of(head_dim, max_seq_len) > 1 ? (size_t)groups * qa::spans_of(head_dim, max_seq_len) * rec : 0;
-    return s;
+    const size_t offsets = ((size_t)num_seqs + 1) * 4, rec = (size_t)part_record_floats(rows, head_dim) * 4;
+    return (offsets + 255) / 256 * 256 +
+           (size_t)qa::max_chunks_of(num_seqs, num_kv_heads, head_dim, max_seq_len, max_pages) * rec;
 }
 
 cudaError_t launch_quant_attention(const QuantAttnArgs &a, ErrState *err, cudaStream_t stream, char *info,
@@ -979,16 +997,12 @@ cudaError_t launch_quant_attention(const QuantAttnArgs &a, ErrState *err, cudaSt
     p.out = static_cast<__nv_bfloat16 *>(a.out);
     p.lse = a.lse;
     p.err = err;
-    const int64_t groups = (int64_t)p.num_seqs * p.hkv, max_chunks = groups * qa::chunks_of(a.pool.head_dim, p.max_seq_len);
+    p.max_pages = a.max_pages > 0 ? a.max_pages : INT64_MAX;
+    const int64_t max_chunks = qa::max_chunks_of(p.num_seqs, p.hkv, a.pool.head_dim, p.max_seq_len, a.max_pages);
     const int rn = qa::rows_capacity(p.rows);
     const int64_t grid = qa::grid_of(a.pool.head_dim, rn, max_chunks);
-    const QuantAttnSpace s = quant_attn_space(p.num_seqs, p.hkv, a.pool.head_dim, p.rows, p.max_seq_len);
-    p.slots = qa::slots_of(a.pool.head_dim, p.max_seq_len);
-    p.spans = (int32_t)qa::spans_of(a.pool.head_dim, p.max_seq_len);
-    p.group_counters = a.counters;
-    p.span_counters = a.counters + groups;
-    p.chunk_records = a.records;
-    p.span_records = a.records + s.chunk_bytes / 4;
+    p.offsets = static_cast<int32_t *>(a.workspace);
+    p.records = reinterpret_cast<float *>(static_cast<uint8_t *>(a.workspace) + (((size_t)p.num_seqs + 1) * 4 + 255) / 256 * 256);
     cudaError_t e = cudaErrorNotSupported;
     auto go = [&](auto fn) { e = fn(p, stream, grid); };
     switch (a.pool.head_dim) {

@@ -174,17 +174,14 @@ struct QuantAttnArgs {
     float scale;
     void *out;
     float *lse;
-    uint32_t *counters;  // QuantAttnSpace::counters of them, zero between calls
-    float *records;      // chunk_bytes, then span_bytes
+    int64_t max_pages;  // 0: what the bounds allow
+    void *workspace;    // quant_attn_bytes
 };
+constexpr int kQuantMaxSeqsHost = 2048;  // kQuantMaxSeqs of pa_attn_quant.cu
 // Rows (query tokens x group) the kernel takes at a head dim.
 constexpr int quant_attn_max_rows(int head_dim) { return head_dim == 512 ? 16 : 32; }
-struct QuantAttnSpace {
-    int64_t counters;
-    size_t chunk_bytes, span_bytes;
-};
-QuantAttnSpace quant_attn_space(int32_t num_seqs, int32_t num_kv_heads, int32_t head_dim, int rows,
-                                int32_t max_seq_len);
+size_t quant_attn_bytes(int32_t num_seqs, int32_t num_kv_heads, int32_t head_dim, int rows, int32_t max_seq_len,
+                        int64_t max_pages);
 cudaError_t launch_quant_attention(const QuantAttnArgs &a, ErrState *err, cudaStream_t stream, char *info,
                                    size_t info_len);
 cudaError_t init_quant_attention_attributes();

@@ -141,13 +141,14 @@ def test_rows_do_not_depend_on_batch_bounds_or_splits():
     assert pa.check_errors() == (pa.PA_OK, -1)
 
 
-def test_drafted_tokens_equal_single_steps_in_bits():
-    """Token i of a five-token request equals the single-token call at its length."""
-    c = Case([530, 258], 5, 8, 2, 128, seed=7)
+@pytest.mark.parametrize("new,hq,hkv,dh", [(5, 8, 2, 128), (8, 2, 2, 128), (2, 16, 1, 128), (5, 8, 2, 256), (4, 8, 2, 512)])
+def test_drafted_tokens_equal_single_steps_in_bits(new, hq, hkv, dh):
+    """Token i of a request's `new` tokens equals the single-token call at its length."""
+    c = Case([1030, 258], new, hq, hkv, dh, seed=7)
     out, lse = c.run()
-    for i in range(5):
-        rows = torch.tensor([i, 5 + i], device="cuda")
-        o, l = c.run(q=c.q[rows], seq_lens=c.sl - (4 - i), max_q=1,
+    for i in range(new):
+        rows = torch.tensor([i, new + i], device="cuda")
+        o, l = c.run(q=c.q[rows], seq_lens=c.sl - (new - 1 - i), max_q=1,
                      query_start_loc=torch.tensor([0, 1, 2], dtype=torch.int32, device="cuda"))
         assert _same(o, out[rows]) and _same(l, lse[rows]), i
 
@@ -237,6 +238,24 @@ def test_one_workspace_serves_calls_of_different_bounds():
             o, l = c.run(workspace=ws)
             assert _same(o, r[0]) and _same(l, r[1])
     assert pa.check_errors() == (pa.PA_OK, -1)
+
+
+@pytest.mark.parametrize("new", [1, 20])
+def test_a_page_bound_sizes_the_workspace_and_is_enforced(new):
+    c = Case([1500, 20, 700, 513], new, 8, 2, 128, seed=15)
+    out, lse = c.run()
+    pages = sum(-(-n // 16) for n in c.lens)
+    n = pa.quant_workspace_size(4, 8, 2, 128, new, 1500, pages)
+    assert n < pa.quant_workspace_size(4, 8, 2, 128, new, 1500)
+    ws = torch.full((n,), 0xA5, dtype=torch.uint8, device="cuda")
+    o, l = c.run(workspace=ws, max_pages=pages)
+    assert _same(o, out) and _same(l, lse)
+    assert pa.check_errors() == (pa.PA_OK, -1)
+    o, l = c.run(workspace=ws, max_pages=pages - 1)
+    assert bool(o.isnan().all()) and bool(l.isnan().all())
+    assert pa.check_errors() == (pa.PA_ERR_WORKSPACE, pages)
+    o, l = c.run(workspace=ws, max_pages=pages)
+    assert _same(o, out) and _same(l, lse)
 
 
 def test_two_graphs_share_a_workspace_and_replay():
