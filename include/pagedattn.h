@@ -512,12 +512,13 @@ PA_API size_t pa_paged_attention_quant_workspace_size(int32_t num_seqs, int32_t 
  * pa_paged_attention over a 4-bit pool: the softmax attention of q over the
  * values that the pool stands for.  Arguments, ownership and errors as for
  * pa_paged_attention; max_pages as in the workspace size.
- *   - Few rows (max_query_len * Hq/Hkv up to 32, at head dim 512 up to
- *     16: decode steps, drafted tokens): one kernel reads the codes
- *     directly.  It has a fixed schedule of its own: a row's results are
- *     bitwise the same whatever the batch, the other requests and the bounds
- *     (within that limit).
- *   - More rows: the selected pages are read back into the workspace (as by
+ *   - Few tokens (max_query_len at most 2 * floor(32 / (Hq/Hkv)), at head dim
+ *     512 at most 2 * floor(16 / (Hq/Hkv)): decode steps, drafted tokens; above
+ *     1024 requests half of that): kernels that read the codes directly.  They
+ *     have a fixed schedule of their own: a row's results are bitwise the same
+ *     whatever the batch, the other requests and the bounds (within that
+ *     limit).
+ *   - More tokens: the selected pages are read back into the workspace (as by
  *     pa_dequantize_kv), and pa_paged_attention's kernel runs over them:
  *     bitwise its results on the read-back pool.
  *   The two round differently.
@@ -528,7 +529,7 @@ PA_API size_t pa_paged_attention_quant_workspace_size(int32_t num_seqs, int32_t 
  *   - workspace: at least pa_paged_attention_quant_workspace_size(...) bytes
  *     for the call's bounds, 256-byte aligned; it needs no particular contents,
  *     and calls with different bounds may share it one after another.
- * num_seqs <= 2048.
+ * num_seqs <= 2048, and num_seqs times the pages of max_seq_len at most 2^28.
  */
 PA_API pa_status pa_paged_attention_quant(const void *q, int64_t num_q_tokens, int64_t q_tok_stride,
                                           int32_t num_q_heads, const pa_quant_cache *cache,

@@ -1051,6 +1051,8 @@ struct QuantPlan {
     AttnPlan attn;
 };
 
+constexpr int kQuantMaxSeqs = 2048;
+constexpr int64_t kQuantMaxPages = int64_t(1) << 28;  // sums of the chunks' weights stay below 2^31
 static size_t round256(size_t n) { return (n + 255) / 256 * 256; }
 
 static pa_status plan_quant(int32_t num_seqs, int32_t hq, int32_t hkv, int32_t dh, int32_t max_query_len,
@@ -1061,12 +1063,17 @@ static pa_status plan_quant(int32_t num_seqs, int32_t hq, int32_t hkv, int32_t d
         return PA_ERR_INVALID_ARG;
     if (!plan_attention(num_seqs, hq, hkv, dh, max_query_len, max_seq_len, &pl->attn))
         return PA_ERR_UNSUPPORTED;
-    if (num_seqs > kQuantMaxSeqsHost || (int64_t)num_seqs * (((int64_t)max_seq_len + 15) / 16) > INT32_MAX)
+    if (num_seqs > kQuantMaxSeqs || (int64_t)num_seqs * (((int64_t)max_seq_len + 15) / 16) > kQuantMaxPages)
         return PA_ERR_UNSUPPORTED;
-    const int64_t rows = (int64_t)max_query_len * (hq / hkv);
-    pl->direct = rows <= quant_attn_max_rows(dh);
+    // The direct kernel takes up to two tiles of a request's tokens.  Measured
+    // against the read-back path: 8 requests of 3345 keys, 40 rows 12 us to 30;
+    // 16 of up to 7168 keys with 2 KV heads, 64 rows 46 to 137; 64 of them with
+    // 8 KV heads, 64 rows 567 to 613, so twice the rows would lose there.
+    const int tiles = quant_attn_tiles(num_seqs, dh, hq / hkv, max_query_len);
+    pl->direct = tiles > 0;
     if (pl->direct) {
-        pl->bytes = quant_attn_bytes(num_seqs, hkv, dh, (int)rows, max_seq_len, max_pages);
+        const int rows = (max_query_len + tiles - 1) / tiles * (hq / hkv);
+        pl->bytes = quant_attn_bytes(num_seqs, tiles, hkv, dh, rows, max_seq_len, max_pages);
         return PA_OK;
     }
     // The BF16 attention gives the same bits with the keys split over CTAs or

@@ -37,7 +37,7 @@
 // elements of the pages (at head dim 128 of half of the pages, the halves are
 // added through shared memory, with the row sums; barrier).  A ninth warp
 // copies the next chunk (cp.async.bulk): K during the second product, V during
-// the first one.  The chunks of all (request, KV head) groups are dealt out as
+// the first one.  The chunks of all (token tile, KV head) groups are dealt out as
 // contiguous ranges of about equal weight; the state of a chunk becomes a
 // record, unless it is its group's only one, and a second kernel folds the
 // records.  (Folded by the last CTA to arrive instead, 32 records of eight rows
@@ -66,7 +66,9 @@ constexpr int kSpan = 16;           // chunks per span of the fold
 // What a chunk costs without its pages, in pages, when the chunks are dealt out:
 // 64 requests 31.5 us at 8, 30.5 at 18, 32.4 at 32.
 constexpr int kChunkCost = 18;
-constexpr int kQuantMaxSeqs = 2048; // two offsets of each in shared memory
+// A tile's weight is at most 1 + kChunkCost / 8 times its pages, and kChunkCost:
+// sums stay below 2^31 for two tiles of requests of 2^28 pages.
+static_assert(2.0 * (1 << 28) * (1 + kChunkCost / 8.0) + kQuantMaxTiles * kChunkCost < 2147483648.0, "weights");
 constexpr float kShift = 15.f;      // p is scaled by 2^kShift (largest f16: 2^16)
 constexpr int kGridSms = 152;       // SMs the grid is sized for
 
@@ -92,10 +94,10 @@ struct Layout {
     static constexpr int flags = bad + 16;
     static constexpr int bars = flags + 16;         // full and empty, of K and of V
     static constexpr int sums = bars + 32;           // 16 bytes for each of nine warps
-    static constexpr int pre = sums + (kWarps + 2) * 16;  // two arrays [num_seqs + 1] int32
+    static constexpr int pre = sums + (kWarps + 2) * 16;  // two arrays [num_tiles + 1] int32
     static_assert(q % 16 == 0 && spread % 16 == 0 && max % 16 == 0 && bad % 8 == 0 && bars % 16 == 0, "layout");
-    static_assert(pre + (kQuantMaxSeqs + 1) * 8 <= (int)kMaxSmemPerBlock, "shared memory");
-    static size_t bytes(int num_seqs) { return (size_t)pre + 8 * ((size_t)num_seqs + 1); }
+    static_assert(pre + (kQuantMaxTiles + 1) * 8 <= (int)kMaxSmemPerBlock, "shared memory");
+    static size_t bytes(int num_tiles) { return (size_t)pre + 8 * ((size_t)num_tiles + 1); }
 };
 
 struct Params {
@@ -105,15 +107,17 @@ struct Params {
     const __nv_bfloat16 *q;
     int64_t q_tok_stride, num_q_tokens;
     const int32_t *block_tables, *seq_lens, *qsl;
-    int32_t max_blocks, num_seqs, hq, hkv, group, max_query_len, max_seq_len;
-    int32_t rows;       // rows of a record
+    int32_t max_blocks, hq, hkv, group, max_query_len, max_seq_len;
+    int32_t tile_shift, tile_tokens;  // a request's tokens form 1 << tile_shift tiles of tile_tokens
+    int32_t num_tiles;  // of all requests
+    int32_t rows;       // rows of a record (of a tile)
     int64_t max_pages;  // pages of all requests together
     float score_scale;  // scale * log2(e) * k_scale
     float v_scale;
     __nv_bfloat16 *out;
     float *lse;
     float *records;     // [chunk]: m, l, O
-    int32_t *offsets;   // [num_seqs + 1]: chunks of a KV head before each request
+    int32_t *offsets;   // [num_tiles + 1]: chunks of a KV head before each tile
     ErrState *err;
 };
 
@@ -157,45 +161,54 @@ __device__ __forceinline__ int64_t div_floor(int64_t a, int64_t b)
     return a / b;
 }
 
+// A tile of a request's tokens: the rows one CTA holds at a time.
 struct Meta {
-    int qs, qn, L;
+    int qs, qn;     // first token and tokens of the tile
+    int L;          // keys of the request
+    int seen;       // last key that the tile's first token sees
     bool sane, ok;  // as ReqMeta
 };
 
-__device__ __forceinline__ Meta meta_of(const Params &p, int b)
+__device__ __forceinline__ Meta meta_of(const Params &p, int tile)
 {
     Meta m;
+    const int b = tile >> p.tile_shift, first = (tile - (b << p.tile_shift)) * p.tile_tokens;
     const int qs = __ldg(p.qsl + b), qe = __ldg(p.qsl + b + 1);
     m.L = __ldg(p.seq_lens + b);
-    m.qs = qs;
     m.sane = qs >= 0 && qe >= qs && (int64_t)qe <= p.num_q_tokens;
-    m.qn = m.sane ? qe - qs : 0;
-    m.ok = m.sane && m.L >= m.qn && (int64_t)m.L <= (int64_t)p.max_blocks * 16 && m.qn <= p.max_query_len &&
+    const int qn = m.sane ? qe - qs : 0;
+    m.ok = m.sane && m.L >= qn && (int64_t)m.L <= (int64_t)p.max_blocks * 16 && qn <= p.max_query_len &&
            m.L <= p.max_seq_len;
+    m.qs = qs + first;
+    m.qn = max(0, qn - first);
+    if (m.ok || (tile + 1) >> p.tile_shift == b)  // (too many tokens: the last tile has the rest)
+        m.qn = min(m.qn, p.tile_tokens);
+    m.seen = m.L - qn + first;
     return m;
 }
 
-// A chunk of the dealt sequence: chunk lc of group (b, kvh), request-major.
+// A chunk of the dealt sequence: chunk lc of group (tile, kvh), tile-major.
 template <int DH>
 struct Chunk {
-    int b, kvh, lc, nch;
-    int qs, qn, L;
+    int tile, kvh, lc, nch;
+    int qs, qn, L, seen;
     const int32_t *row;  // the request's block table
 
     __device__ __forceinline__ void load(const Params &p, const int32_t *pre)
     {
-        const Meta m = meta_of(p, b);
+        const Meta m = meta_of(p, tile);
         qs = m.qs;
         qn = m.qn;
         L = m.L;
-        nch = pre[b + 1] - pre[b];
-        row = p.block_tables + (int64_t)b * p.max_blocks;
+        seen = m.seen;
+        nch = pre[tile + 1] - pre[tile];
+        row = p.block_tables + (int64_t)(tile >> p.tile_shift) * p.max_blocks;
     }
     __device__ __forceinline__ void at(const Params &p, const int32_t *pre, int64_t x)
     {
-        b = owner_of(pre, p.num_seqs, (int)div_floor(x, p.hkv));
+        tile = owner_of(pre, p.num_tiles, (int)div_floor(x, p.hkv));
         load(p, pre);
-        const int r = (int)(x - (int64_t)p.hkv * pre[b]);
+        const int r = (int)(x - (int64_t)p.hkv * pre[tile]);
         kvh = (int)((uint32_t)r / (uint32_t)nch);
         lc = r - kvh * nch;
     }
@@ -209,8 +222,8 @@ struct Chunk {
             return;
         kvh = 0;
         do
-            ++b;
-        while (pre[b + 1] == pre[b]);
+            ++tile;
+        while (pre[tile + 1] == pre[tile]);
         load(p, pre);
     }
     __device__ __forceinline__ bool has_page(int i) const { return (lc * chunk_pages(DH) + i) * 16 < L; }
@@ -285,7 +298,7 @@ __global__ void __launch_bounds__(kAllThreads, ctas_per_sm<DH, RN>()) quant_attn
     volatile int *const s_bad = reinterpret_cast<int *>(smem + Lay::bad);  // [chunk parity] 1 + the last chunk with a bad block id
     volatile int *const s_flags = reinterpret_cast<int *>(smem + Lay::flags);  // [0] abort
     int32_t *const s_pre = reinterpret_cast<int32_t *>(smem + Lay::pre);
-    int32_t *const s_weight = s_pre + p.num_seqs + 1;
+    int32_t *const s_weight = s_pre + p.num_tiles + 1;
     const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32, g = lane / 4, t = lane % 4;
     const int G = p.group, hkv = p.hkv;
     enum { kFullK, kFullV, kEmptyK, kEmptyV };
@@ -302,39 +315,51 @@ __global__ void __launch_bounds__(kAllThreads, ctas_per_sm<DH, RN>()) quant_attn
         s_bad[0] = s_bad[1] = 0;
         fence_barrier_init();
     }
-    // chunks of a KV head of each request, and their weights: pages, and what
-    // a chunk costs without any
+    // chunks of a KV head of each tile, and their weights: pages, and what a
+    // chunk costs without any
     longlong2 total;
     block_exclusive_sums2<kAllThreads>(
-        p.num_seqs, s_pre, s_weight, reinterpret_cast<longlong2 *>(smem + Lay::sums), total,
-        [&](int b, int &chunks, int &weight) {
-            const Meta m = meta_of(p, b);
+        p.num_tiles, s_pre, s_weight, reinterpret_cast<longlong2 *>(smem + Lay::sums), total,
+        [&](int tile, int &chunks, int &weight) {
+            const Meta m = meta_of(p, tile);
             if (!m.ok && blockIdx.x == 0)
-                record_error(p.err, kErrBadMetadata, b);
+                record_error(p.err, kErrBadMetadata, tile >> p.tile_shift);
             if (m.ok && m.qn > 0) {
                 chunks = (m.L + kChunk - 1) / kChunk;
                 weight = (m.L + 15) / 16 + kChunkCost * chunks;
             }
         });
-    const bool over = total.y - kChunkCost * total.x > p.max_pages;
-    if (over && blockIdx.x == 0 && tid == 0)
-        record_error(p.err, kErrBudget, total.y - kChunkCost * total.x);
-    for (int b = blockIdx.x; b < p.num_seqs; b += gridDim.x) {
-        if (s_pre[b + 1] != s_pre[b] && !over)
+    bool over = false;
+    if (p.max_pages != INT64_MAX) {
+        // pages of the requests: of their first tiles
+        long long pages = 0;
+        for (int b = lane; b < p.num_tiles >> p.tile_shift; b += 32) {
+            const int i = b << p.tile_shift;
+            pages += s_weight[i + 1] - s_weight[i] - kChunkCost * (s_pre[i + 1] - s_pre[i]);
+        }
+#pragma unroll
+        for (int w = 16; w; w >>= 1)
+            pages += __shfl_xor_sync(0xffffffffu, pages, w);
+        over = pages > p.max_pages;
+        if (over && blockIdx.x == 0 && tid == 0)
+            record_error(p.err, kErrBudget, pages);
+    }
+    for (int i = blockIdx.x; i < p.num_tiles; i += gridDim.x) {
+        if (s_pre[i + 1] != s_pre[i] && !over)
             continue;
-        const Meta m = meta_of(p, b);
+        const Meta m = meta_of(p, i);
         if (m.sane && (!m.ok || over)) {  // bad lengths, or no room for the records: NaN rows
             const int64_t first = (int64_t)m.qs * p.hq, n = (int64_t)m.qn * p.hq;
-            for (int64_t i = tid; i < n * DH; i += kAllThreads)
-                p.out[first * DH + i] = __ushort_as_bfloat16(0x7FC0);
+            for (int64_t k = tid; k < n * DH; k += kAllThreads)
+                p.out[first * DH + k] = __ushort_as_bfloat16(0x7FC0);
             if (p.lse)
-                for (int64_t i = tid; i < n; i += kAllThreads)
-                    p.lse[first + i] = __int_as_float(0x7FC00000);
+                for (int64_t k = tid; k < n; k += kAllThreads)
+                    p.lse[first + k] = __int_as_float(0x7FC00000);
         }
     }
     if (blockIdx.x == 0)  // for the folding kernel
-        for (int b = tid; b <= p.num_seqs; b += kAllThreads)
-            p.offsets[b] = over ? 0 : s_pre[b];
+        for (int i = tid; i <= p.num_tiles; i += kAllThreads)
+            p.offsets[i] = over ? 0 : s_pre[i];
     if (over)
         return;
     // The chunks in order, a group's one after another, are cut where their
@@ -349,11 +374,11 @@ __global__ void __launch_bounds__(kAllThreads, ctas_per_sm<DH, RN>()) quant_attn
         int64_t start = T;
         if (cta < gridDim.x) {
             const int64_t at = div_floor(cta * W + gridDim.x - 1, gridDim.x);
-            const int b = owner_of(s_weight, p.num_seqs, (int)div_floor(at, hkv));
-            const int n = s_pre[b + 1] - s_pre[b], w = s_weight[b + 1] - s_weight[b];
-            const int64_t rem = at - (int64_t)hkv * s_weight[b];
+            const int i = owner_of(s_weight, p.num_tiles, (int)div_floor(at, hkv));
+            const int n = s_pre[i + 1] - s_pre[i], w = s_weight[i + 1] - s_weight[i];
+            const int64_t rem = at - (int64_t)hkv * s_weight[i];
             const int h = (int)div_floor(rem, w), lc = ((int)(rem - (int64_t)h * w) + kFull - 1) / kFull;
-            start = (int64_t)hkv * s_pre[b] + (int64_t)h * n + min(lc, n);
+            start = (int64_t)hkv * s_pre[i] + (int64_t)h * n + min(lc, n);
         }
         lo = __shfl_sync(0xffffffffu, start, 0);
         hi = __shfl_sync(0xffffffffu, start, 1);
@@ -380,7 +405,7 @@ __global__ void __launch_bounds__(kAllThreads, ctas_per_sm<DH, RN>()) quant_attn
             const bool go = exists && id >= 0 && (int64_t)id < p.num_blocks;
             const int n = __popc(__ballot_sync(0xffffffffu, go));
             const uint64_t off = (uint64_t)(uint32_t)id * p.block_stride + (uint64_t)(uint32_t)c.kvh * p.head_stride;
-            const int b = c.b;
+            const int b = c.tile >> p.tile_shift;
             const bool any_bad = __any_sync(0xffffffffu, exists && !go);
             if (k + 1 < chunks) {
                 c.next(p, s_pre);
@@ -563,7 +588,7 @@ __global__ void __launch_bounds__(kAllThreads, ctas_per_sm<DH, RN>()) quant_attn
                     for (int i = 0; i < 4; ++i) {
                         const int key = key0 + 16 * page + 4 * t + i;
                         const bool gone = key >= c.L, nan = ((w >> (8 * i)) & 0x7fu) == 0x7fu;
-                        if (gone || (nan && key > c.L - c.qn)) {
+                        if (gone || (nan && key > c.seen)) {
                             (i < 2 ? s01 : s23) &= i % 2 ? 0x0000ffffu : 0xffff0000u;
                             if (!gone)
                                 atomicMin(s_nan + parity * (DH / 16) + 8 * b + g, key);
@@ -776,13 +801,13 @@ __global__ void __launch_bounds__(kAllThreads, ctas_per_sm<DH, RN>()) quant_attn
                 }
                 if (lane == 0) {
                     s_cq[slot] = fmaxf(1e-37f, fminf(p.score_scale * __int_as_float((127 + e) << 23), 3e38f));
-                    s_lim[slot] = c.L - c.qn + (valid ? tok : c.qn - 1);
+                    s_lim[slot] = c.seen + (valid ? tok : c.qn - 1);
                 }
             }
             sync();
         }
         St st;
-        const bool masked = c.lc * kChunk + kChunk > c.L - c.qn + 1;
+        const bool masked = c.lc * kChunk + kChunk > c.seen + 1;
         const int bad = masked ? chunk_state(std::true_type{}, step, st) : chunk_state(std::false_type{}, step, st);
         if (bad < 0)
             return;  // a wait ran out of time (the copying warp lets its copies land)
@@ -822,14 +847,14 @@ __global__ void __launch_bounds__(kFoldThreads) quant_fold_kernel(const Params p
     __shared__ __align__(16) float s_state[kFoldThreads / 32][DH + 4];
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     const int row = blockIdx.y * (blockDim.x / 32 / SW) + warp / SW, slot = warp % SW;
-    const int b = blockIdx.x / p.hkv, kvh = blockIdx.x - b * p.hkv;
+    const int tile = blockIdx.x / p.hkv, kvh = blockIdx.x - tile * p.hkv;
     griddep_wait();
     griddep_launch_dependents();
-    const int c0 = __ldcg(p.offsets + b), nch = __ldcg(p.offsets + b + 1) - c0;
-    const int qs = __ldg(p.qsl + b), qn = __ldg(p.qsl + b + 1) - qs;
+    const int c0 = __ldcg(p.offsets + tile), nch = __ldcg(p.offsets + tile + 1) - c0;
+    const Meta m = meta_of(p, tile);
     if (nch <= 1)  // none, or written already
         return;
-    const bool live = row < qn * p.group;
+    const bool live = row < m.qn * p.group;
     const uint32_t hdr = (uint32_t)part_header_floats(p.rows), size = (uint32_t)part_record_floats(p.rows, DH);
     const float *rec = p.records + ((int64_t)p.hkv * c0 + (int64_t)kvh * nch) * size + (live ? row : 0);
     const float *ro = rec - (live ? row : 0) + (hdr + (uint32_t)((live ? row : 0) * DH + 4 * lane));
@@ -894,7 +919,7 @@ __global__ void __launch_bounds__(kFoldThreads) quant_fold_kernel(const Params p
     }
     if (!live || slot != 0)
         return;
-    const int64_t at = (int64_t)(qs + row / p.group) * p.hq + kvh * p.group + row % p.group;
+    const int64_t at = (int64_t)(m.qs + row / p.group) * p.hq + kvh * p.group + row % p.group;
     const float f = __frcp_rn(acc.l[0]) * p.v_scale;
 #pragma unroll
     for (int i = 0; i < V; ++i)
@@ -909,7 +934,7 @@ template <int DH, int RN>
 cudaError_t set_attributes()
 {
     return cudaFuncSetAttribute(quant_attn_kernel<DH, RN>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                (int)Layout<DH, RN>::bytes(kQuantMaxSeqs));
+                                (int)Layout<DH, RN>::bytes(kQuantMaxTiles));
 }
 
 static int rows_capacity(int rows) { return rows <= 8 ? 8 : rows <= 16 ? 16 : rows <= 24 ? 24 : 32; }
@@ -923,12 +948,13 @@ static int64_t grid_of(int dh, int rn, int64_t max_chunks)
 
 static int64_t chunks_of(int dh, int32_t len) { return ((int64_t)len + chunk_keys(dh) - 1) / chunk_keys(dh); }
 // Chunks of all groups at most.
-static int64_t max_chunks_of(int32_t num_seqs, int32_t hkv, int dh, int32_t max_seq_len, int64_t max_pages)
+static int64_t max_chunks_of(int32_t num_seqs, int32_t tiles, int32_t hkv, int dh, int32_t max_seq_len,
+                             int64_t max_pages)
 {
     int64_t per_head = (int64_t)num_seqs * chunks_of(dh, max_seq_len);
     if (max_pages > 0 && max_pages / chunk_pages(dh) + num_seqs < per_head)
         per_head = max_pages / chunk_pages(dh) + num_seqs;  // whole ones, and one in part a request
-    return per_head * hkv;
+    return per_head * tiles * hkv;
 }
 
 template <int DH, int RN>
@@ -938,7 +964,7 @@ cudaError_t launch(const Params &p, cudaStream_t stream, int64_t grid)
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)grid);
     cfg.blockDim = dim3(kAllThreads);
-    cfg.dynamicSmemBytes = Layout<DH, RN>::bytes(p.num_seqs);
+    cfg.dynamicSmemBytes = Layout<DH, RN>::bytes(p.num_tiles);
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -953,7 +979,7 @@ cudaError_t launch(const Params &p, cudaStream_t stream, int64_t grid)
     while (sw < kFoldThreads / 32 && sw * kSpan < chunks)
         sw *= 2;
     const int most = kFoldThreads / 32 / sw, rows = p.rows < most ? p.rows : most;
-    cfg.gridDim = dim3((unsigned)(p.num_seqs * p.hkv), (unsigned)((p.rows + rows - 1) / rows));
+    cfg.gridDim = dim3((unsigned)(p.num_tiles * p.hkv), (unsigned)((p.rows + rows - 1) / rows));
     cfg.blockDim = dim3(32 * sw * rows);
     cfg.dynamicSmemBytes = 0;
     return cudaLaunchKernelEx(&cfg, quant_fold_kernel<DH>, p, sw);
@@ -961,12 +987,15 @@ cudaError_t launch(const Params &p, cudaStream_t stream, int64_t grid)
 
 }  // namespace qa
 
-size_t quant_attn_bytes(int32_t num_seqs, int32_t num_kv_heads, int32_t head_dim, int rows, int32_t max_seq_len,
-                        int64_t max_pages)
+// The tiles' offsets, then the records.
+static size_t offset_bytes(int32_t num_tiles) { return (((size_t)num_tiles + 1) * 4 + 255) / 256 * 256; }
+
+size_t quant_attn_bytes(int32_t num_seqs, int tiles, int32_t num_kv_heads, int32_t head_dim, int rows,
+                        int32_t max_seq_len, int64_t max_pages)
 {
-    const size_t offsets = ((size_t)num_seqs + 1) * 4, rec = (size_t)part_record_floats(rows, head_dim) * 4;
-    return (offsets + 255) / 256 * 256 +
-           (size_t)qa::max_chunks_of(num_seqs, num_kv_heads, head_dim, max_seq_len, max_pages) * rec;
+    return offset_bytes(num_seqs * tiles) +
+           (size_t)qa::max_chunks_of(num_seqs, tiles, num_kv_heads, head_dim, max_seq_len, max_pages) *
+               (size_t)part_record_floats(rows, head_dim) * 4;
 }
 
 cudaError_t launch_quant_attention(const QuantAttnArgs &a, ErrState *err, cudaStream_t stream, char *info,
@@ -985,24 +1014,28 @@ cudaError_t launch_quant_attention(const QuantAttnArgs &a, ErrState *err, cudaSt
     p.seq_lens = a.seq_lens;
     p.qsl = a.query_start_loc;
     p.max_blocks = a.max_blocks;
-    p.num_seqs = a.num_seqs;
     p.hq = a.num_q_heads;
     p.hkv = a.pool.num_kv_heads;
     p.group = p.hq / p.hkv;
     p.max_query_len = a.max_query_len;
     p.max_seq_len = a.max_seq_len;
-    p.rows = a.max_query_len * p.group;
+    const int tiles = quant_attn_tiles(a.num_seqs, a.pool.head_dim, p.group, a.max_query_len);
+    p.tile_shift = tiles - 1;  // one or two
+    p.tile_tokens = (a.max_query_len + tiles - 1) / tiles;
+    p.num_tiles = a.num_seqs * tiles;
+    p.rows = p.tile_tokens * p.group;
     p.score_scale = a.scale * 1.4426950408889634f * a.pool.k_scale;
     p.v_scale = a.pool.v_scale;
     p.out = static_cast<__nv_bfloat16 *>(a.out);
     p.lse = a.lse;
     p.err = err;
     p.max_pages = a.max_pages > 0 ? a.max_pages : INT64_MAX;
-    const int64_t max_chunks = qa::max_chunks_of(p.num_seqs, p.hkv, a.pool.head_dim, p.max_seq_len, a.max_pages);
+    const int64_t max_chunks =
+        qa::max_chunks_of(a.num_seqs, tiles, p.hkv, a.pool.head_dim, p.max_seq_len, a.max_pages);
     const int rn = qa::rows_capacity(p.rows);
     const int64_t grid = qa::grid_of(a.pool.head_dim, rn, max_chunks);
     p.offsets = static_cast<int32_t *>(a.workspace);
-    p.records = reinterpret_cast<float *>(static_cast<uint8_t *>(a.workspace) + (((size_t)p.num_seqs + 1) * 4 + 255) / 256 * 256);
+    p.records = reinterpret_cast<float *>(static_cast<uint8_t *>(a.workspace) + offset_bytes(p.num_tiles));
     cudaError_t e = cudaErrorNotSupported;
     auto go = [&](auto fn) { e = fn(p, stream, grid); };
     switch (a.pool.head_dim) {
@@ -1019,8 +1052,8 @@ cudaError_t launch_quant_attention(const QuantAttnArgs &a, ErrState *err, cudaSt
         go(rn == 8 ? qa::launch<512, 8> : qa::launch<512, 16>);
         break;
     }
-    snprintf(info, info_len, "quant attention direct dh=%d rows=%d/%d grid=%lld chunks<=%lld", a.pool.head_dim, p.rows,
-             rn, (long long)grid, (long long)max_chunks);
+    snprintf(info, info_len, "quant attention direct dh=%d tiles=%d rows=%d/%d grid=%lld chunks<=%lld", a.pool.head_dim,
+             tiles, p.rows, rn, (long long)grid, (long long)max_chunks);
     return e;
 }
 

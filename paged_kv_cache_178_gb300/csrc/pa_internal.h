@@ -177,11 +177,19 @@ struct QuantAttnArgs {
     int64_t max_pages;  // 0: what the bounds allow
     void *workspace;    // quant_attn_bytes
 };
-constexpr int kQuantMaxSeqsHost = 2048;  // kQuantMaxSeqs of pa_attn_quant.cu
-// Rows (query tokens x group) the kernel takes at a head dim.
-constexpr int quant_attn_max_rows(int head_dim) { return head_dim == 512 ? 16 : 32; }
-size_t quant_attn_bytes(int32_t num_seqs, int32_t num_kv_heads, int32_t head_dim, int rows, int32_t max_seq_len,
-                        int64_t max_pages);
+// Tiles that a request's tokens form there, at most 32 rows each (16 at head
+// dim 512): one or two, or 0 when the call is not one for these kernels.
+constexpr int kQuantMaxTiles = 2048;
+constexpr int quant_attn_tiles(int32_t num_seqs, int head_dim, int group, int max_query_len)
+{
+    const int tokens = (head_dim == 512 ? 16 : 32) / group;
+    if (tokens && max_query_len <= tokens && num_seqs <= kQuantMaxTiles)
+        return 1;
+    return tokens && max_query_len <= 2 * tokens && num_seqs <= kQuantMaxTiles / 2 ? 2 : 0;
+}
+// rows: of a tile
+size_t quant_attn_bytes(int32_t num_seqs, int tiles, int32_t num_kv_heads, int32_t head_dim, int rows,
+                        int32_t max_seq_len, int64_t max_pages);
 cudaError_t launch_quant_attention(const QuantAttnArgs &a, ErrState *err, cudaStream_t stream, char *info,
                                    size_t info_len);
 cudaError_t init_quant_attention_attributes();

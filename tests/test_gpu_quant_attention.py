@@ -99,7 +99,10 @@ def _same(a, b):
     ([530, 31], 2, 32, 2, 128), ([1000], 1, 32, 1, 128), ([2, 3, 300], [2, 1, 3], 8, 2, 128),
     ([90, 257, 1], 1, 8, 2, 256), ([300, 44], 5, 8, 2, 256), ([260], 8, 4, 1, 256), ([131], 3, 10, 2, 256),
     ([200, 33], 1, 16, 2, 512), ([140], 2, 16, 2, 512), ([150], 4, 4, 1, 512), ([4097], 1, 4, 1, 512),
-    ([5, 9, 40], [0, 1, 2], 4, 4, 128)])
+    ([5, 9, 40], [0, 1, 2], 4, 4, 128),
+    # two tiles of tokens
+    ([300, 77, 9, 1040], [8, 5, 1, 3], 8, 1, 128), ([700, 40], 8, 28, 4, 128), ([530, 31], [16, 9], 8, 2, 128),
+    ([64, 600], 2, 32, 1, 128), ([300, 44], [9, 16], 8, 2, 256), ([140, 33], [6, 8], 8, 2, 512), ([9], 9, 4, 1, 128)])
 def test_direct_matches_formula(lens, new, hq, hkv, dh):
     c = Case(lens, new, hq, hkv, dh, seed=len(lens) + dh + hq, k_scale=0.5, v_scale=2.0)
     out, lse = c.run()
@@ -141,7 +144,8 @@ def test_rows_do_not_depend_on_batch_bounds_or_splits():
     assert pa.check_errors() == (pa.PA_OK, -1)
 
 
-@pytest.mark.parametrize("new,hq,hkv,dh", [(5, 8, 2, 128), (8, 2, 2, 128), (2, 16, 1, 128), (5, 8, 2, 256), (4, 8, 2, 512)])
+@pytest.mark.parametrize("new,hq,hkv,dh", [(5, 8, 2, 128), (8, 2, 2, 128), (2, 16, 1, 128), (5, 8, 2, 256), (4, 8, 2, 512),
+                                              (12, 8, 2, 128), (8, 7, 1, 128), (11, 8, 2, 256), (6, 8, 2, 512)])
 def test_drafted_tokens_equal_single_steps_in_bits(new, hq, hkv, dh):
     """Token i of a request's `new` tokens equals the single-token call at its length."""
     c = Case([1030, 258], new, hq, hkv, dh, seed=7)
@@ -179,7 +183,7 @@ def test_bytes_past_the_length_and_unseen_nans_do_not_matter():
     assert pa.check_errors() == (pa.PA_OK, -1)
 
 
-@pytest.mark.parametrize("new", [1, 40])
+@pytest.mark.parametrize("new", [1, 10, 40])
 def test_bad_metadata_gives_nan_rows_and_leaves_the_rest(new):
     c = Case([300, 200, 150], new, 8, 2, 128, seed=9)
     out, lse = c.run()
@@ -227,6 +231,32 @@ def test_more_rows_equal_bf16_attention_on_the_read_back_pool(lens, new, hq, hkv
         assert bool(o.isnan().all()) and bool(l.isnan().all())
 
 
+def test_errors_and_nans_seen_by_the_second_tile_only():
+    """Ten tokens of four query heads to a KV head: tiles of five tokens."""
+    c = Case([1037, 200], 10, 8, 2, 128, seed=16)
+    out, lse = c.run()
+    assert "tiles=2" in pa.last_launch_info()
+    # the last page's id: every row of the request
+    bt = c.bt.clone()
+    bt[0, 1036 // 16] = -1
+    o, l = c.run(block_tables=bt)
+    assert pa.check_errors() == (pa.PA_ERR_BAD_METADATA, 0)
+    assert bool(o[:10].isnan().all()) and bool(l[:10].isnan().all()) and _same(o[10:], out[10:])
+    # more tokens than the bound allows: every row, and no other
+    o, l = c.run(query_start_loc=torch.tensor([0, 13, 20], dtype=torch.int32, device="cuda"), max_q=10)
+    assert pa.check_errors() == (pa.PA_ERR_BAD_METADATA, 0)
+    assert bool(o[:13].isnan().all()) and bool(l[:13].isnan().all()) and not bool(o[13:].isnan().any())
+    # a NaN scale of V at a key that only the last two tokens see
+    page, tok = int(c.tables[0, 1035 // 16]), 1035 % 16
+    c.cache.v_pool[page, 0, 8 * 128 + 3 * 16 + tok] = 0x7F
+    o, l = c.run()
+    want = torch.zeros_like(o, dtype=torch.bool)
+    want[8:10, :4, 48:64] = True
+    assert torch.equal(o.isnan(), want) and _same(l, lse)
+    assert _same(o[~want], out[~want])
+    assert pa.check_errors() == (pa.PA_OK, -1)
+
+
 def test_one_workspace_serves_calls_of_different_bounds():
     a = Case([7168, 513], 1, 8, 2, 128, seed=11)
     b = Case([400, 90], 60, 8, 2, 128, seed=12)
@@ -240,7 +270,7 @@ def test_one_workspace_serves_calls_of_different_bounds():
     assert pa.check_errors() == (pa.PA_OK, -1)
 
 
-@pytest.mark.parametrize("new", [1, 20])
+@pytest.mark.parametrize("new", [1, 10, 20])
 def test_a_page_bound_sizes_the_workspace_and_is_enforced(new):
     c = Case([1500, 20, 700, 513], new, 8, 2, 128, seed=15)
     out, lse = c.run()
