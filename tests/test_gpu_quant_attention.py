@@ -288,6 +288,24 @@ def test_a_page_bound_sizes_the_workspace_and_is_enforced(new):
     assert _same(o, out) and _same(l, lse)
 
 
+@pytest.mark.parametrize("new", [1, 40])
+def test_calls_on_another_stream_keep_their_own_memory(new):
+    """Results, statistics and scratch that the call allocates belong to its
+    stream: what the current stream does meanwhile cannot meet them."""
+    c = Case([3000, 513, 90], new, 8, 2, 128, seed=17)
+    out, lse = c.run()
+    n = pa.quant_workspace_size(3, 8, 2, 128, new, 3000)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    for _ in range(20):
+        o, l = c.run(stream=side)
+        junk = [torch.full((n,), 0xFF, dtype=torch.uint8, device="cuda"), torch.full_like(o, 3.0)]
+        side.synchronize()
+        assert _same(o, out) and _same(l, lse)
+        del o, l, junk
+    assert pa.check_errors() == (pa.PA_OK, -1)
+
+
 def test_two_graphs_share_a_workspace_and_replay():
     a = Case([3000, 513, 90], 1, 8, 2, 128, seed=13)
     b = Case([400, 90], 60, 8, 2, 128, seed=14)
