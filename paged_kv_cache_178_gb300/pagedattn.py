@@ -305,7 +305,13 @@ class PreparedCall:
     keeps references to them)."""
 
     def __init__(self, fn, args, what: str, keep):
-        self._fn, self._args, self._what, self._keep = fn, args, what, keep
+        # The arguments are converted here, and the call goes through a function
+        # object without argument types, which would convert them each time
+        # (22 arguments: 2.1 us a call, 1.1 so).
+        self._args = tuple(t(a) if isinstance(a, (int, float)) or a is None else a for t, a in zip(fn.argtypes, args))
+        self._fn = load()[fn.__name__]
+        self._fn.restype = fn.restype
+        self._what, self._keep = what, keep
 
     def __call__(self) -> None:
         st = self._fn(*self._args)
