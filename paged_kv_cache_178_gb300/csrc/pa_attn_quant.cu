@@ -839,6 +839,10 @@ __global__ void __launch_bounds__(kAllThreads, ctas_per_sm<DH, RN>()) quant_attn
 // CTA at a time) side by side; then one warp folds the spans of a row.  131k
 // keys on 8 KV heads: 32.2 us with spans of 32 chunks, 31.6 of 8, 30.1 of 16.
 constexpr int kFoldThreads = 512;  // at most
+// Up to this many tiles a CTA sums the chunks before its own while it waits for
+// the attention kernel; above, it reads the sums that one has left (a round trip
+// more, but 2048 tiles cost every CTA as many loads).
+constexpr int kFoldSums = 256;
 
 template <int DH>
 __global__ void __launch_bounds__(kFoldThreads) quant_fold_kernel(const Params p, int SW)
@@ -848,12 +852,33 @@ __global__ void __launch_bounds__(kFoldThreads) quant_fold_kernel(const Params p
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     const int row = blockIdx.y * (blockDim.x / 32 / SW) + warp / SW, slot = warp % SW;
     const int tile = blockIdx.x / p.hkv, kvh = blockIdx.x - tile * p.hkv;
+    // The metadata's writers are done (the attention kernel waited for them
+    // before it let this one start), so it is read while that one still runs.
+    const Meta m = meta_of(p, tile);
+    const int nch = m.ok && m.qn > 0 ? (m.L + chunk_keys(DH) - 1) / chunk_keys(DH) : 0;
+    int c0 = 0;
+    if (nch > 1 && p.num_tiles <= kFoldSums) {
+        __shared__ int s_sum[kFoldThreads / 32];
+        for (int i = threadIdx.x; i < tile; i += blockDim.x) {
+            const Meta x = meta_of(p, i);
+            c0 += x.ok && x.qn > 0 ? (x.L + chunk_keys(DH) - 1) / chunk_keys(DH) : 0;
+        }
+        c0 = __reduce_add_sync(0xffffffffu, c0);
+        if (lane == 0)
+            s_sum[warp] = c0;
+        __syncthreads();
+        c0 = 0;
+        for (int w = 0; w < blockDim.x / 32; ++w)
+            c0 += s_sum[w];
+    }
     griddep_wait();
     griddep_launch_dependents();
-    const int c0 = __ldcg(p.offsets + tile), nch = __ldcg(p.offsets + tile + 1) - c0;
-    const Meta m = meta_of(p, tile);
     if (nch <= 1)  // none, or written already
         return;
+    if (p.num_tiles > kFoldSums)
+        c0 = __ldcg(p.offsets + tile);
+    if (p.max_pages != INT64_MAX && __ldcg(p.offsets + p.num_tiles) == 0)
+        return;  // no room for the records
     const bool live = row < m.qn * p.group;
     const uint32_t hdr = (uint32_t)part_header_floats(p.rows), size = (uint32_t)part_record_floats(p.rows, DH);
     const float *rec = p.records + ((int64_t)p.hkv * c0 + (int64_t)kvh * nch) * size + (live ? row : 0);
