@@ -153,14 +153,6 @@ __device__ __forceinline__ void bulk_copy(uint32_t dst, const void *src, uint32_
                  : "memory");
 }
 
-// floor(a / b), 0 <= a, 0 < b: one 32-bit division when both fit
-__device__ __forceinline__ int64_t div_floor(int64_t a, int64_t b)
-{
-    if (((uint64_t)a | (uint64_t)b) >> 32 == 0)
-        return (int64_t)((uint32_t)a / (uint32_t)b);
-    return a / b;
-}
-
 // A tile of a request's tokens: the rows one CTA holds at a time.
 struct Meta {
     int qs, qn;     // first token and tokens of the tile

@@ -301,7 +301,7 @@ __global__ void __launch_bounds__(kQuantThreads) dequantize_kv_kernel(
         return;
     const int64_t n_tab = (int64_t)num_seqs * out_cols;
     for (int64_t e = gtid; e < n_tab; e += gsize) {
-        const int b = (int)(e / out_cols), p = (int)(e % out_cols);
+        const int b = (int)div_floor(e, out_cols), p = (int)(e - (int64_t)b * out_cols);
         compact_tables[e] = !over && p < s_off[b + 1] - s_off[b] ? s_off[b] + p : -1;
     }
     if (over)
@@ -310,11 +310,12 @@ __global__ void __launch_bounds__(kQuantThreads) dequantize_kv_kernel(
     const int hk = pool.num_kv_heads;
     const uint4 qnan = make_uint4(0x7FC07FC0u, 0x7FC07FC0u, 0x7FC07FC0u, 0x7FC07FC0u);
     // this warp's units, one after another: consecutive records, so the
-    // request and the block id follow with the page
+    // request and the block id follow with the page (dealt in turn to the
+    // warps of a CTA instead, so that they write next to one another, no faster)
     const int lane = tid & 31;
     const int64_t records = (int64_t)total * hk, units = (records * DH + 255) / 256;
     const int64_t warps = gsize / 32, w = gtid / 32;
-    const int64_t u_lo = w * units / warps, u_hi = (w + 1) * units / warps;
+    const int64_t u_lo = div_floor(w * units, warps), u_hi = div_floor((w + 1) * units, warps);
     // per lane: the page a record index stands in, followed as it grows
     struct Where {
         int64_t rec;  // record index (page * heads + head)
@@ -324,7 +325,7 @@ __global__ void __launch_bounds__(kQuantThreads) dequantize_kv_kernel(
         x.rec = rec;
         if (rec >= records)
             return;
-        x.c = (int)(rec / hk);
+        x.c = (int)div_floor(rec, hk);
         x.h = (int)(rec - (int64_t)x.c * hk);
         x.b = owner_of(s_off, num_seqs, x.c);
         x.id = __ldg(block_tables + (int64_t)x.b * max_blocks + (x.c - s_off[x.b]));

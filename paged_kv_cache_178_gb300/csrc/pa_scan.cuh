@@ -5,6 +5,14 @@
 
 namespace pa {
 
+// floor(a / b), 0 <= a, 0 < b: one 32-bit division when both fit
+__device__ __forceinline__ int64_t div_floor(int64_t a, int64_t b)
+{
+    if (((uint64_t)a | (uint64_t)b) >> 32 == 0)
+        return (int64_t)((uint32_t)a / (uint32_t)b);
+    return a / b;
+}
+
 // Largest batch those kernels take: their offsets sit in shared memory.
 constexpr int kScanMaxSeqs = 8192;
 
