@@ -419,8 +419,8 @@ PA_API pa_status pa_qk_norm_rope(const void *q, int64_t q_tok_stride, int32_t nu
  * past the pool latches PA_ERR_BAD_METADATA (index = the token) and is
  * skipped, as is the cache write of a token with a bad or negative position.
  * Results are bitwise those of pa_qk_norm_rope followed by
- * pa_reshape_and_cache.  The pool may not share bytes with the other
- * arguments (PA_ERR_INVALID_ARG).
+ * pa_reshape_and_cache (the slots of a call have to differ).  The pool may not
+ * share bytes with the other arguments (PA_ERR_INVALID_ARG).
  */
 PA_API pa_status pa_qk_norm_rope_and_cache(
     const void *q, int64_t q_tok_stride, int32_t num_q_heads, const void *k, int64_t k_tok_stride, const void *value,
@@ -470,7 +470,8 @@ typedef struct {
  * both to nearest, ties to even, saturating; a zero scale gives zero codes,
  * and a block that holds a NaN or an infinity reads back as NaN.  Arguments,
  * padding (negative slots) and errors as for pa_reshape_and_cache; key and
- * value may not share bytes with the pool (PA_ERR_INVALID_ARG).
+ * value may not share bytes with the pool (PA_ERR_INVALID_ARG).  The slots of
+ * a call have to differ: what two tokens leave in one slot is a mixture.
  */
 PA_API pa_status pa_reshape_and_cache_quant(const void *key, int64_t key_tok_stride, const void *value,
                                             int64_t value_tok_stride, int64_t num_tokens,

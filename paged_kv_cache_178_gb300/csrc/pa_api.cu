@@ -1063,7 +1063,8 @@ static pa_status plan_quant(int32_t num_seqs, int32_t hq, int32_t hkv, int32_t d
         return PA_ERR_INVALID_ARG;
     if (!plan_attention(num_seqs, hq, hkv, dh, max_query_len, max_seq_len, &pl->attn))
         return PA_ERR_UNSUPPORTED;
-    if (num_seqs > kQuantMaxSeqs || (int64_t)num_seqs * (((int64_t)max_seq_len + 15) / 16) > kQuantMaxPages)
+    if (num_seqs > kQuantMaxSeqs || (int64_t)num_seqs * (((int64_t)max_seq_len + 15) / 16) > kQuantMaxPages ||
+        (int64_t)num_seqs * 2 * hkv > INT32_MAX)
         return PA_ERR_UNSUPPORTED;
     // The direct kernel takes up to two tiles of a request's tokens.  Measured
     // against the read-back path: 8 requests of 3345 keys, 40 rows 12 us to 30;

@@ -278,6 +278,7 @@ __global__ void __launch_bounds__(kAllThreads, ctas_per_sm<DH, RN>()) quant_attn
     constexpr bool HALVES = DH == 128;      // warps 4-7 take the other half of the pages
     constexpr int NR = RN / 4;  // rows of a thread's state
     constexpr int NP = HALVES ? 1 : 2 * NE;   // element pairs of a thread's state
+    static_assert(NP * NR <= 32, "a bit each");
     constexpr int REC = quant_record_bytes(DH), CODES = quant_code_bytes(DH);
     constexpr bool kQRegs = NQ * DH <= 256;  // Q fragments in registers (else read from shared memory)
     constexpr int OT = 2 * NQ;              // accumulator tiles of a 32-element block
@@ -295,7 +296,7 @@ __global__ void __launch_bounds__(kAllThreads, ctas_per_sm<DH, RN>()) quant_attn
     int *const s_lim = reinterpret_cast<int *>(smem + Lay::lim);      // last key of a row
     int *const s_nan = reinterpret_cast<int *>(smem + Lay::nan);      // [chunk parity][DH/16] first NaN key of an element block
     volatile int *const s_bad = reinterpret_cast<int *>(smem + Lay::bad);  // [chunk parity] 1 + the last chunk with a bad block id
-    volatile int *const s_flags = reinterpret_cast<int *>(smem + Lay::flags);  // [0] abort
+    volatile int *const s_flags = reinterpret_cast<int *>(smem + Lay::flags);  // [0] gave up [1] a copy for all to see
     int32_t *const s_pre = reinterpret_cast<int32_t *>(smem + Lay::pre);
     int32_t *const s_weight = s_pre + p.num_tiles + 1;
     const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32, g = lane / 4, t = lane % 4;
@@ -310,7 +311,7 @@ __global__ void __launch_bounds__(kAllThreads, ctas_per_sm<DH, RN>()) quant_attn
     if (tid == 0) {
         for (int i = 0; i < 4; ++i)
             mbar_init(bar(i), 1);
-        s_flags[0] = 0;
+        s_flags[0] = s_flags[1] = 0;
         s_bad[0] = s_bad[1] = 0;
         fence_barrier_init();
     }
@@ -562,9 +563,11 @@ __global__ void __launch_bounds__(kAllThreads, ctas_per_sm<DH, RN>()) quant_attn
                 if (g == 0)
                     s_max[score_row(n, i) * kWarps + warp] = x;
             }
+        if (tid == 0)
+            s_flags[1] = s_flags[0];  // any thread may set [0] at any time
         sync();  // A: maxima written; K is consumed
         // read between A and B, so that every thread reads the same
-        const int bad = s_flags[0] ? -1 : s_bad[parity] == step + 1;
+        const int bad = s_flags[1] ? -1 : s_bad[parity] == step + 1;
         if (tid < DH / 16)
             s_nan[(parity ^ 1) * (DH / 16) + tid] = 0x7fffffff;  // for the next chunk
         if (tid == 0)
@@ -704,6 +707,18 @@ __global__ void __launch_bounds__(kAllThreads, ctas_per_sm<DH, RN>()) quant_attn
             for (int k = 0; k < F; ++k)
                 s_half[k * kThreads + (tid ^ 128)] = keep ? pr[0][k] : pr[1][k];
         }
+        // (before C: after it a new group's limits may be written)
+        uint32_t nan_rows = 0;  // bit i * NR + r
+        if constexpr (MASKED) {
+#pragma unroll
+            for (int i = 0; i < NP; ++i) {
+                const int k = s_nan[parity * (DH / 16) + state_pair(i) / 8];
+                if (k != 0x7fffffff)
+#pragma unroll
+                    for (int r = 0; r < NR; ++r)
+                        nan_rows |= (uint32_t)(s_lim[state_row(r)] >= k) << (i * NR + r);
+            }
+        }
         sync();  // C: sums and halves written; V is consumed
         if (tid == 0)
             mbar_arrive(bar(kEmptyV));
@@ -726,16 +741,13 @@ __global__ void __launch_bounds__(kAllThreads, ctas_per_sm<DH, RN>()) quant_attn
             for (int i = 0; i < NP; ++i)
                 st.o[i][r] = make_float2(pr[i][4 * (r / 2) + r % 2], pr[i][4 * (r / 2) + 2 + r % 2]);
         }
-        if constexpr (MASKED) {
+        if (MASKED && nan_rows) {
 #pragma unroll
-            for (int i = 0; i < NP; ++i) {
-                const int k = s_nan[parity * (DH / 16) + state_pair(i) / 8];
-                if (k != 0x7fffffff)
+            for (int i = 0; i < NP; ++i)
 #pragma unroll
-                    for (int r = 0; r < NR; ++r)
-                        if (s_lim[state_row(r)] >= k)
-                            st.o[i][r] = make_float2(__int_as_float(0x7FC00000), __int_as_float(0x7FC00000));
-            }
+                for (int r = 0; r < NR; ++r)
+                    if (nan_rows >> (i * NR + r) & 1)
+                        st.o[i][r] = make_float2(__int_as_float(0x7FC00000), __int_as_float(0x7FC00000));
         }
         return bad;
     };

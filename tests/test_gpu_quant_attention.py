@@ -257,6 +257,24 @@ def test_errors_and_nans_seen_by_the_second_tile_only():
     assert pa.check_errors() == (pa.PA_OK, -1)
 
 
+def test_unseen_nans_where_groups_follow_one_another_in_a_cta():
+    """Far more groups than CTAs, of lengths in turn short and long: a NaN that
+    only a request's last token sees reaches that row alone."""
+    n = 300
+    c = Case([40, 500] * (n // 2), 2, 8, 2, 128, seed=18)
+    out, lse = c.run()
+    for b, length in enumerate(c.lens):
+        page, tok = int(c.tables[b, (length - 1) // 16]), (length - 1) % 16
+        c.cache.v_pool[page, 1, 8 * 128 + 5 * 16 + tok] = 0x7F
+    want = torch.zeros_like(out, dtype=torch.bool)
+    want[1::2, 4:, 80:96] = True
+    for _ in range(5):
+        o, l = c.run()
+        assert torch.equal(o.isnan(), want) and _same(l, lse)
+        assert _same(o[~want], out[~want])
+    assert pa.check_errors() == (pa.PA_OK, -1)
+
+
 def test_one_workspace_serves_calls_of_different_bounds():
     a = Case([7168, 513], 1, 8, 2, 128, seed=11)
     b = Case([400, 90], 60, 8, 2, 128, seed=12)
