@@ -61,7 +61,10 @@ namespace pa {
 
 namespace qa {
 
-constexpr int kWarps = 8;                   // computing warps
+// Computing warps.  (Sixteen of them at head dim 256, a page each, took 43 us
+// for five new tokens instead of 24.6: each reads all of Q and all maxima and
+// sums from shared memory, which is then busy.)
+constexpr int kWarps = 8;
 constexpr int kThreads = 32 * kWarps;       // computing threads
 constexpr int kAllThreads = kThreads + 32;  // and the copying warp
 // pages per warp of a chunk: as many as shared memory holds (at head dim 128
@@ -79,9 +82,13 @@ static_assert(2.0 * (1 << 28) * (1 + kChunkCost / 8.0) + kQuantMaxTiles * kChunk
 constexpr float kShift = 15.f;      // p is scaled by 2^kShift (largest f16: 2^16)
 constexpr int kGridSms = 152;       // SMs the grid is sized for
 
-// CTAs per SM that registers and shared memory are sized for
-template <int DH, int RN>
-constexpr int ctas_per_sm() { return DH == 128 && RN <= 8 ? 2 : 1; }
+// CTAs per SM that registers and shared memory are sized for: two where a
+// thread's share of the state fits in half of the registers (64 requests at head
+// dim 256 54 us with one, 48 with two; at head dim 512 59 and 53, with 12 rows
+// 157 and 149; but 12 rows at head dim 256 79 and 85).
+__host__ __device__ constexpr int ctas_per_sm(int dh, int rn) { return rn <= 8 || dh == 512 ? 2 : 1; }
+// Shared memory that keeps a second CTA off an SM.
+constexpr int kSmemAlone = 118 * 1024;
 // Shared-memory layout in bytes.  RN: query rows (8, 16, 24 or 32).
 template <int DH, int RN>
 struct Layout {
@@ -268,7 +275,7 @@ struct State {
 };
 
 template <int DH, int RN>
-__global__ void __launch_bounds__(kAllThreads, ctas_per_sm<DH, RN>()) quant_attn_kernel(const Params p)
+__global__ void __launch_bounds__(kAllThreads, ctas_per_sm(DH, RN)) quant_attn_kernel(const Params p)
 {
     using Lay = Layout<DH, RN>;
     constexpr int NQ = Lay::NQ;
@@ -969,8 +976,9 @@ __global__ void __launch_bounds__(kFoldThreads) quant_fold_kernel(const Params p
 template <int DH, int RN>
 cudaError_t set_attributes()
 {
+    const int bytes = (int)Layout<DH, RN>::bytes(kQuantMaxTiles);
     return cudaFuncSetAttribute(quant_attn_kernel<DH, RN>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                (int)Layout<DH, RN>::bytes(kQuantMaxTiles));
+                                bytes > kSmemAlone ? bytes : kSmemAlone);
 }
 
 static int rows_capacity(int rows) { return rows <= 8 ? 8 : rows <= 16 ? 16 : rows <= 24 ? 24 : 32; }
@@ -978,7 +986,7 @@ static int rows_capacity(int rows) { return rows <= 8 ? 8 : rows <= 16 ? 16 : ro
 // CTAs of the grid: one wave, fewer when there are fewer chunks.
 static int64_t grid_of(int dh, int rn, int64_t max_chunks)
 {
-    const int64_t wave = (int64_t)kGridSms * (dh == 128 && rn <= 8 ? 2 : 1);
+    const int64_t wave = (int64_t)kGridSms * ctas_per_sm(dh, rn);
     return max_chunks < 1 ? 1 : (max_chunks < wave ? max_chunks : wave);
 }
 
@@ -996,11 +1004,14 @@ static int64_t max_chunks_of(int32_t num_seqs, int32_t tiles, int32_t hkv, int d
 template <int DH, int RN>
 cudaError_t launch(const Params &p, cudaStream_t stream, int64_t grid)
 {
-    static_assert(ctas_per_sm<DH, RN>() == (DH == 128 && RN <= 8 ? 2 : 1), "grid_of");
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)grid);
     cfg.blockDim = dim3(kAllThreads);
     cfg.dynamicSmemBytes = Layout<DH, RN>::bytes(p.num_tiles);
+    // no more CTAs than SMs: one to each (4 requests at head dim 256 10.6 us,
+    // where some share an SM 12.1)
+    if (grid <= kGridSms && cfg.dynamicSmemBytes < kSmemAlone)
+        cfg.dynamicSmemBytes = kSmemAlone;
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
