@@ -519,10 +519,13 @@ PA_API size_t pa_paged_attention_quant_workspace_size(int32_t num_seqs, int32_t 
  *     have a fixed schedule of their own: a row's results are bitwise the same
  *     whatever the batch, the other requests and the bounds (within that
  *     limit).
- *   - More tokens: the selected pages are read back into the workspace (as by
+ *   - More tokens where that is faster, by the bounds alone (num_seqs, the
+ *     heads, max_query_len, max_seq_len; pa_last_launch_info tells): the same
+ *     kernels, and the same bits.
+ *   - More tokens otherwise: the selected pages are read back into the workspace (as by
  *     pa_dequantize_kv), and pa_paged_attention's kernel runs over them:
  *     bitwise its results on the read-back pool.
- *   The two round differently.
+ *   The two ways round differently.
  *   - More than max_pages (> 0) selected pages: PA_ERR_WORKSPACE is latched
  *     (index = the pages) and all rows are NaN.
  *   - A bad block id makes all rows of its request NaN.  Keys past a

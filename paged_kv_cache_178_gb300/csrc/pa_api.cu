@@ -1066,11 +1066,12 @@ static pa_status plan_quant(int32_t num_seqs, int32_t hq, int32_t hkv, int32_t d
     if (num_seqs > kQuantMaxSeqs || (int64_t)num_seqs * (((int64_t)max_seq_len + 15) / 16) > kQuantMaxPages ||
         (int64_t)num_seqs * 2 * hkv > INT32_MAX)
         return PA_ERR_UNSUPPORTED;
-    // The direct kernel takes up to two tiles of a request's tokens.  Measured
-    // against the read-back path: 8 requests of 3345 keys, 40 rows 12 us to 30;
-    // 16 of up to 7168 keys with 2 KV heads, 64 rows 46 to 137; 64 of them with
-    // 8 KV heads, 64 rows 567 to 613, so twice the rows would lose there.
-    const int tiles = quant_attn_tiles(num_seqs, dh, hq / hkv, max_query_len);
+    // The direct kernels take up to two tiles of a request's tokens whatever
+    // the batch.  Measured against the read-back path: 8 requests of 3345 keys,
+    // 40 rows 12 us to 30; 16 of up to 7168 keys with 2 KV heads, 64 rows 46 to
+    // 137; 64 of them with 8 KV heads, 64 rows 567 to 613, so twice the rows
+    // would lose there: they take more only in small calls.
+    const int tiles = quant_attn_tiles(num_seqs, hkv, dh, hq / hkv, max_query_len, max_seq_len);
     pl->direct = tiles > 0;
     if (pl->direct) {
         const int rows = (max_query_len + tiles - 1) / tiles * (hq / hkv);

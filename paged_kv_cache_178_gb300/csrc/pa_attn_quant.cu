@@ -1037,10 +1037,48 @@ cudaError_t launch(const Params &p, cudaStream_t stream, int64_t grid)
 // The tiles' offsets, then the records.
 static size_t offset_bytes(int32_t num_tiles) { return (((size_t)num_tiles + 1) * 4 + 255) / 256 * 256; }
 
+// log2 of the tiles that a request's share of the numbering has room for.
+static int tile_shift_of(int tiles)
+{
+    int shift = 0;
+    while (1 << shift < tiles)
+        ++shift;
+    return shift;
+}
+
+int quant_attn_tiles(int32_t num_seqs, int32_t num_kv_heads, int head_dim, int group, int32_t max_query_len,
+                     int32_t max_seq_len)
+{
+    const int tokens = (head_dim == 512 ? 16 : 32) / group;
+    if (tokens == 0)
+        return 0;
+    const int64_t tiles = max_query_len <= tokens ? 1 : ((int64_t)max_query_len + tokens - 1) / tokens;
+    if (tiles > kQuantMaxTiles || ((int64_t)num_seqs << tile_shift_of((int)tiles)) > kQuantMaxTiles)
+        return 0;
+    if (tiles > 2) {
+        // Estimates in ns: a wave of chunks here, against a start and the keys
+        // that one CTA of the BF16 attention takes one after another (with one
+        // tile of 128 rows to an SM or less; where it has more, or splits the
+        // keys, or the read-back is long, it takes longer).  Measured, direct
+        // against read-back, 8 query and 2 KV heads unless said: 128 tokens of
+        // 4096 keys 23 us to 59, 128 of 512 keys in 4 requests 13 to 66, 64 of
+        // 1024 in 8 requests 25 to 26, 40 of 120 in 32 requests 28 to 18; 64 of
+        // 1024 with 32 and 8 heads in 4 requests 45 to 27, of 4096 in one 36 to
+        // 59; head dim 256, 157 of 4521 with 2 and 1 heads 23 to 81; head dim
+        // 512, 27 of 4764 with 8 and 1 heads 31 to 139.
+        const int64_t per_key = head_dim == 128 ? 12 : (head_dim == 256 ? 16 : 27);
+        const int64_t wave = (int64_t)qa::kGridSms * qa::ctas_per_sm(head_dim, head_dim == 512 ? 16 : 32);
+        const int64_t chunks = num_seqs * num_kv_heads * tiles * qa::chunks_of(head_dim, max_seq_len);
+        if (9000 * ((chunks + wave - 1) / wave) > 12000 + per_key * max_seq_len)
+            return 0;
+    }
+    return (int)tiles;
+}
+
 size_t quant_attn_bytes(int32_t num_seqs, int tiles, int32_t num_kv_heads, int32_t head_dim, int rows,
                         int32_t max_seq_len, int64_t max_pages)
 {
-    return offset_bytes(num_seqs * tiles) +
+    return offset_bytes(num_seqs << tile_shift_of(tiles)) +
            (size_t)qa::max_chunks_of(num_seqs, tiles, num_kv_heads, head_dim, max_seq_len, max_pages) *
                (size_t)part_record_floats(rows, head_dim) * 4;
 }
@@ -1066,10 +1104,10 @@ cudaError_t launch_quant_attention(const QuantAttnArgs &a, ErrState *err, cudaSt
     p.group = p.hq / p.hkv;
     p.max_query_len = a.max_query_len;
     p.max_seq_len = a.max_seq_len;
-    const int tiles = quant_attn_tiles(a.num_seqs, a.pool.head_dim, p.group, a.max_query_len);
-    p.tile_shift = tiles - 1;  // one or two
+    const int tiles = quant_attn_tiles(a.num_seqs, p.hkv, a.pool.head_dim, p.group, a.max_query_len, a.max_seq_len);
+    p.tile_shift = tile_shift_of(tiles);
     p.tile_tokens = (a.max_query_len + tiles - 1) / tiles;
-    p.num_tiles = a.num_seqs * tiles;
+    p.num_tiles = a.num_seqs << p.tile_shift;
     p.rows = p.tile_tokens * p.group;
     p.score_scale = a.scale * 1.4426950408889634f * a.pool.k_scale;
     p.v_scale = a.pool.v_scale;

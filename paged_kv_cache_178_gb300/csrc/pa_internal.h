@@ -178,15 +178,11 @@ struct QuantAttnArgs {
     void *workspace;    // quant_attn_bytes
 };
 // Tiles that a request's tokens form there, at most 32 rows each (16 at head
-// dim 512): one or two, or 0 when the call is not one for these kernels.
+// dim 512), or 0 when the call is not one for these kernels: more than two
+// tiles a request only where that is faster than reading the pages back.
 constexpr int kQuantMaxTiles = 2048;
-constexpr int quant_attn_tiles(int32_t num_seqs, int head_dim, int group, int max_query_len)
-{
-    const int tokens = (head_dim == 512 ? 16 : 32) / group;
-    if (tokens && max_query_len <= tokens && num_seqs <= kQuantMaxTiles)
-        return 1;
-    return tokens && max_query_len <= 2 * tokens && num_seqs <= kQuantMaxTiles / 2 ? 2 : 0;
-}
+int quant_attn_tiles(int32_t num_seqs, int32_t num_kv_heads, int head_dim, int group, int32_t max_query_len,
+                     int32_t max_seq_len);
 // rows: of a tile
 size_t quant_attn_bytes(int32_t num_seqs, int tiles, int32_t num_kv_heads, int32_t head_dim, int rows,
                         int32_t max_seq_len, int64_t max_pages);

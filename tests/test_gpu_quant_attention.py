@@ -13,7 +13,8 @@ values that the pool stands for.  Tolerances, per element:
     p is off by at most half a step, 2^-25 * 2^-15 of the row's largest (1, and
     the sum of p is at least that);
   lse: d + 2^-18 + 2^-22 |lse|.
-More rows: bit for bit pa_paged_attention over the read-back pool."""
+More rows in larger calls: bit for bit pa_paged_attention over the read-back
+pool."""
 import numpy as np
 import pytest
 import torch
@@ -102,7 +103,10 @@ def _same(a, b):
     ([5, 9, 40], [0, 1, 2], 4, 4, 128),
     # two tiles of tokens
     ([300, 77, 9, 1040], [8, 5, 1, 3], 8, 1, 128), ([700, 40], 8, 28, 4, 128), ([530, 31], [16, 9], 8, 2, 128),
-    ([64, 600], 2, 32, 1, 128), ([300, 44], [9, 16], 8, 2, 256), ([140, 33], [6, 8], 8, 2, 512), ([9], 9, 4, 1, 128)])
+    ([64, 600], 2, 32, 1, 128), ([300, 44], [9, 16], 8, 2, 256), ([140, 33], [6, 8], 8, 2, 512), ([9], 9, 4, 1, 128),
+    # more tiles, in small calls
+    ([300, 77], 77, 8, 2, 128), ([513, 40, 1030], [17, 40, 33], 8, 2, 128), ([200], 20, 16, 2, 256),
+    ([150, 64], 50, 16, 2, 512), ([100, 1, 30, 600], [70, 1, 0, 5], 4, 4, 128), ([700], 10, 7, 1, 256)])
 def test_direct_matches_formula(lens, new, hq, hkv, dh):
     c = Case(lens, new, hq, hkv, dh, seed=len(lens) + dh + hq, k_scale=0.5, v_scale=2.0)
     out, lse = c.run()
@@ -145,7 +149,8 @@ def test_rows_do_not_depend_on_batch_bounds_or_splits():
 
 
 @pytest.mark.parametrize("new,hq,hkv,dh", [(5, 8, 2, 128), (8, 2, 2, 128), (2, 16, 1, 128), (5, 8, 2, 256), (4, 8, 2, 512),
-                                              (12, 8, 2, 128), (8, 7, 1, 128), (11, 8, 2, 256), (6, 8, 2, 512)])
+                                              (12, 8, 2, 128), (8, 7, 1, 128), (11, 8, 2, 256), (6, 8, 2, 512),
+                                              (33, 8, 2, 128), (20, 16, 2, 256), (9, 8, 1, 512)])
 def test_drafted_tokens_equal_single_steps_in_bits(new, hq, hkv, dh):
     """Token i of a request's `new` tokens equals the single-token call at its length."""
     c = Case([1030, 258], new, hq, hkv, dh, seed=7)
@@ -183,10 +188,12 @@ def test_bytes_past_the_length_and_unseen_nans_do_not_matter():
     assert pa.check_errors() == (pa.PA_OK, -1)
 
 
-@pytest.mark.parametrize("new", [1, 10, 40])
-def test_bad_metadata_gives_nan_rows_and_leaves_the_rest(new):
-    c = Case([300, 200, 150], new, 8, 2, 128, seed=9)
+@pytest.mark.parametrize("new,hq,hkv,kind", [(1, 8, 2, "direct"), (10, 8, 2, "direct"), (40, 8, 2, "direct"),
+                                             (40, 64, 16, "read-back")])
+def test_bad_metadata_gives_nan_rows_and_leaves_the_rest(new, hq, hkv, kind):
+    c = Case([300, 200, 150], new, hq, hkv, 128, seed=9)
     out, lse = c.run()
+    assert kind in pa.last_launch_info()
     bt = c.bt.clone()
     bt[1, 3] = 10**6
     fill = torch.full_like(out, 7.0)
@@ -202,15 +209,16 @@ def test_bad_metadata_gives_nan_rows_and_leaves_the_rest(new):
     assert pa.check_errors() == (pa.PA_ERR_BAD_METADATA, 0)
     assert bool(o[:new].isnan().all()) and _same(o[new:], out[new:])
     # rows that no request owns stay as they are
-    tail = torch.full((3 * new + 2, 8, 128), 7.0, dtype=torch.bfloat16, device="cuda")
+    tail = torch.full((3 * new + 2, hq, 128), 7.0, dtype=torch.bfloat16, device="cuda")
     q = torch.cat([c.q, c.q[:2]])
     o, _ = c.run(q=q, out=tail)
     assert pa.check_errors() == (pa.PA_OK, -1)
     assert _same(o[:3 * new], out) and bool((o[3 * new:] == 7).all())
 
 
-@pytest.mark.parametrize("lens,new,hq,hkv,dh", [([300, 77], 77, 8, 2, 128), ([513, 40, 1030], [17, 40, 33], 8, 2, 128),
-                                                ([200], 20, 16, 2, 256), ([150, 64], 50, 16, 2, 512),
+@pytest.mark.parametrize("lens,new,hq,hkv,dh", [([300, 77] * 4, 77, 8, 2, 128),
+                                                ([513, 40, 1030] * 6, [17, 40, 33] * 6, 8, 2, 128),
+                                                ([200] * 16, 20, 16, 2, 256), ([150, 64] * 2, 50, 16, 2, 512),
                                                 ([40, 3], 1, 128, 1, 128)])
 def test_more_rows_equal_bf16_attention_on_the_read_back_pool(lens, new, hq, hkv, dh):
     c = Case(lens, new, hq, hkv, dh, seed=dh, k_scale=2.0, v_scale=0.25)
@@ -277,9 +285,10 @@ def test_unseen_nans_where_groups_follow_one_another_in_a_cta():
 
 def test_one_workspace_serves_calls_of_different_bounds():
     a = Case([7168, 513], 1, 8, 2, 128, seed=11)
-    b = Case([400, 90], 60, 8, 2, 128, seed=12)
+    b = Case([400, 90] * 6, 60, 8, 2, 128, seed=12)
     ra, rb = a.run(), b.run()
-    n = max(pa.quant_workspace_size(2, 8, 2, 128, 1, 7168), pa.quant_workspace_size(2, 8, 2, 128, 60, 400))
+    assert "read-back" in pa.last_launch_info()
+    n = max(pa.quant_workspace_size(2, 8, 2, 128, 1, 7168), pa.quant_workspace_size(12, 8, 2, 128, 60, 400))
     ws = torch.zeros(n, dtype=torch.uint8, device="cuda")
     for _ in range(3):
         for c, r in ((a, ra), (b, rb)):
@@ -288,13 +297,15 @@ def test_one_workspace_serves_calls_of_different_bounds():
     assert pa.check_errors() == (pa.PA_OK, -1)
 
 
-@pytest.mark.parametrize("new", [1, 10, 20])
-def test_a_page_bound_sizes_the_workspace_and_is_enforced(new):
-    c = Case([1500, 20, 700, 513], new, 8, 2, 128, seed=15)
+@pytest.mark.parametrize("new,hq,hkv,kind", [(1, 8, 2, "direct"), (10, 8, 2, "direct"), (20, 8, 2, "direct"),
+                                             (20, 64, 16, "read-back")])
+def test_a_page_bound_sizes_the_workspace_and_is_enforced(new, hq, hkv, kind):
+    c = Case([1500, 20, 700, 513], new, hq, hkv, 128, seed=15)
     out, lse = c.run()
+    assert kind in pa.last_launch_info()
     pages = sum(-(-n // 16) for n in c.lens)
-    n = pa.quant_workspace_size(4, 8, 2, 128, new, 1500, pages)
-    assert n < pa.quant_workspace_size(4, 8, 2, 128, new, 1500)
+    n = pa.quant_workspace_size(4, hq, hkv, 128, new, 1500, pages)
+    assert n < pa.quant_workspace_size(4, hq, hkv, 128, new, 1500)
     ws = torch.full((n,), 0xA5, dtype=torch.uint8, device="cuda")
     o, l = c.run(workspace=ws, max_pages=pages)
     assert _same(o, out) and _same(l, lse)
@@ -306,13 +317,14 @@ def test_a_page_bound_sizes_the_workspace_and_is_enforced(new):
     assert _same(o, out) and _same(l, lse)
 
 
-@pytest.mark.parametrize("new", [1, 40])
-def test_calls_on_another_stream_keep_their_own_memory(new):
+@pytest.mark.parametrize("new,hq,hkv,kind", [(1, 8, 2, "direct"), (40, 64, 16, "read-back")])
+def test_calls_on_another_stream_keep_their_own_memory(new, hq, hkv, kind):
     """Results, statistics and scratch that the call allocates belong to its
     stream: what the current stream does meanwhile cannot meet them."""
-    c = Case([3000, 513, 90], new, 8, 2, 128, seed=17)
+    c = Case([3000, 513, 90], new, hq, hkv, 128, seed=17)
     out, lse = c.run()
-    n = pa.quant_workspace_size(3, 8, 2, 128, new, 3000)
+    assert kind in pa.last_launch_info()
+    n = pa.quant_workspace_size(3, hq, hkv, 128, new, 3000)
     side = torch.cuda.Stream()
     side.wait_stream(torch.cuda.current_stream())
     for _ in range(20):
@@ -326,9 +338,9 @@ def test_calls_on_another_stream_keep_their_own_memory(new):
 
 def test_two_graphs_share_a_workspace_and_replay():
     a = Case([3000, 513, 90], 1, 8, 2, 128, seed=13)
-    b = Case([400, 90], 60, 8, 2, 128, seed=14)
+    b = Case([400, 90] * 6, 60, 8, 2, 128, seed=14)
     want = [x for c in (a, b) for x in c.run()]
-    n = max(pa.quant_workspace_size(3, 8, 2, 128, 1, 3000), pa.quant_workspace_size(2, 8, 2, 128, 60, 400))
+    n = max(pa.quant_workspace_size(3, 8, 2, 128, 1, 3000), pa.quant_workspace_size(12, 8, 2, 128, 60, 400))
     ws = torch.zeros(n, dtype=torch.uint8, device="cuda")
     pa.init()
     s = torch.cuda.Stream()
