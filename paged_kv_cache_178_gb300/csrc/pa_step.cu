@@ -202,8 +202,10 @@ __device__ __forceinline__ float sum_squares(const float (&a)[8], const float (&
 // kRopeBatch steps are loaded before the first is computed.  What bounds it
 // after the memory is the instruction count: a step of 1 KB takes about 130.
 // 16384 tokens of 32 query and 8 KV heads at head dim 128, with the cache
-// write (411 MB): 70 us, 5.8 TB/s; 4099 tokens of 16 and 2 heads of 256
-// elements, 64 of them rotated (77 MB): 17 us, 4.4 TB/s; 64 tokens 2.4 us.  The
+// write (411 MB): 69 us, 6.0 TB/s; 4099 tokens of 16 and 2 heads of 256
+// elements, 64 of them rotated (77 MB): 16.4 us, 4.7 TB/s; 64 tokens 2.5 us.
+// Loads and stores are marked as streaming (neither: 70.5 and 17.4 us; the
+// loads alone 71.8 and 17.6): every row passes once.  The
 // first case took 88 us with 16-byte vectors that were not neighbours in a
 // load, 81 to 90 with the rows staged through shared memory, 106 with a token to
 // each group of lanes.
@@ -352,8 +354,8 @@ __global__ void __launch_bounds__(kRopeThreads, kRopeCtas) qk_norm_rope_kernel(c
                 for (int u = 0; u < kRopeBatch; ++u) {
                     x0[u] = x1[u] = make_uint4(0u, 0u, 0u, 0u);
                     if (j + u < jb && h + u * GPW < heads) {
-                        x0[u] = src[u * GPW * VEC + v0];
-                        x1[u] = src[u * GPW * VEC + v1];
+                        x0[u] = __ldcs(src + u * GPW * VEC + v0);
+                        x1[u] = __ldcs(src + u * GPW * VEC + v1);
                     }
                 }
                 if (compute)
@@ -365,8 +367,8 @@ __global__ void __launch_bounds__(kRopeThreads, kRopeCtas) qk_norm_rope_kernel(c
                     if (compute)
                         row(x0[u], x1[u], norm, w);
                     if (h + u * GPW < heads && pos >= 0) {
-                        dst[v0] = x0[u];
-                        dst[v1] = x1[u];
+                        __stcs(dst + v0, x0[u]);
+                        __stcs(dst + v1, x1[u]);
                     }
                     dst += dst_step;
                 }
