@@ -504,6 +504,8 @@ PA_API pa_status pa_dequantize_kv(const pa_quant_cache *cache, const int32_t *bl
  * Bytes of scratch that pa_paged_attention_quant needs for these bounds.
  * max_pages: an upper bound of the pages of all requests together, or 0 for
  * num_seqs * ceil(max_seq_len / 16).  Returns 0 for invalid arguments.
+ * Smaller bounds may need more (their calls take another way, see below): a
+ * workspace for several calls is as large as the largest of their sizes.
  */
 PA_API size_t pa_paged_attention_quant_workspace_size(int32_t num_seqs, int32_t num_q_heads, int32_t num_kv_heads,
                                                       int32_t head_dim, int32_t max_query_len, int32_t max_seq_len,
@@ -522,9 +524,9 @@ PA_API size_t pa_paged_attention_quant_workspace_size(int32_t num_seqs, int32_t 
  *   - More tokens where that is faster, by the bounds alone (num_seqs, the
  *     heads, max_query_len, max_seq_len; pa_last_launch_info tells): the same
  *     kernels, and the same bits.
- *   - More tokens otherwise: the selected pages are read back into the workspace (as by
- *     pa_dequantize_kv), and pa_paged_attention's kernel runs over them:
- *     bitwise its results on the read-back pool.
+ *   - More tokens otherwise: the selected pages are read back into the
+ *     workspace (as by pa_dequantize_kv), and pa_paged_attention's kernel runs
+ *     over them: bitwise its results on the read-back pool.
  *   The two ways round differently.
  *   - More than max_pages (> 0) selected pages: PA_ERR_WORKSPACE is latched
  *     (index = the pages) and all rows are NaN.
