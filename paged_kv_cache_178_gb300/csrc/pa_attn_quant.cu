@@ -28,8 +28,9 @@
 // Fixed arithmetic (a row's results do not depend on the batch or the grid):
 //   chunks of 512 keys (256 at head dim 256, 128 at 512) from key 0, each with
 //   its own exact maximum; a chunk's row sum is, per warp, a butterfly over its
-//   keys, then the eight warps' sums pairwise; chunk states fold left to right
-//   (State::fold) within spans of 16 chunks, and the span states left to right.
+//   keys, then the eight warps' sums pairwise; the states of a span of 16 chunks
+//   are added with their exact maximum (the outputs in order, the sums as a
+//   tree of fixed shape), and the spans fold left to right (State::fold).
 //
 // A CTA (8 warps) per chunk: each warp scores its pages; row maxima are
 // exchanged (barrier); P goes to shared memory in fragment order, the V scales
@@ -908,27 +909,51 @@ __global__ void __launch_bounds__(kFoldThreads) quant_fold_kernel(const Params p
         State<1, 2 * V> st;
         st.clear();
         const int first = (s0 + slot) * kSpan, n = live ? min(kSpan, nch - first) : 0;
-        constexpr int U = V == 1 ? 16 : 8 / (V / 2);  // records in flight
+        // lane k has record k's maximum and sum; the factors are known at once
+        const int64_t span_at = (int64_t)first * size;
+        float mk = -INFINITY, lk = 0.f;
+        if (lane < n) {
+            mk = __ldcg(rec + span_at + (int64_t)lane * size);
+            lk = __ldcg(rec + span_at + (int64_t)lane * size + p.rows);
+        }
+        constexpr int U = 16 / V;  // records in flight
+        float f = 0.f;
         for (int k0 = 0; k0 < n; k0 += U) {
-            State<1, 2 * V> x[U];
+            float4 x[U][V];
 #pragma unroll
             for (int u = 0; u < U; ++u) {
                 if (k0 + u >= n)
                     break;
-                const int64_t at = (int64_t)(first + k0 + u) * size;
-                x[u].m[0] = __ldcg(rec + at);
-                x[u].l[0] = __ldcg(rec + at + p.rows);
 #pragma unroll
-                for (int i = 0; i < V; ++i) {
-                    const float4 v = __ldcg(reinterpret_cast<const float4 *>(ro + at + 128 * i));
-                    x[u].o[2 * i][0] = make_float2(v.x, v.y);
-                    x[u].o[2 * i + 1][0] = make_float2(v.z, v.w);
-                }
+                for (int i = 0; i < V; ++i)
+                    x[u][i] = __ldcg(reinterpret_cast<const float4 *>(ro + span_at + (int64_t)(k0 + u) * size + 128 * i));
+            }
+            if (k0 == 0) {
+                float m = mk;
+#pragma unroll
+                for (int w = 1; w < kSpan; w <<= 1)
+                    m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, w));
+                m = __shfl_sync(0xffffffffu, m, 0);
+                f = ex2(mk - (m == -INFINITY ? 0.f : m));  // 0 for an empty chunk
+                float l = lk * f;
+#pragma unroll
+                for (int w = 1; w < kSpan; w <<= 1)
+                    l += __shfl_xor_sync(0xffffffffu, l, w);
+                st.m[0] = m;
+                st.l[0] = __shfl_sync(0xffffffffu, l, 0);
             }
 #pragma unroll
-            for (int u = 0; u < U; ++u)
-                if (k0 + u < n)
-                    st.fold(x[u]);
+            for (int u = 0; u < U; ++u) {
+                if (k0 + u >= n)
+                    break;
+                const float fu = __shfl_sync(0xffffffffu, f, k0 + u);
+#pragma unroll
+                for (int i = 0; i < V; ++i) {
+                    float2 &a = st.o[2 * i][0], &b = st.o[2 * i + 1][0];
+                    a = make_float2(__fmaf_rn(x[u][i].x, fu, a.x), __fmaf_rn(x[u][i].y, fu, a.y));
+                    b = make_float2(__fmaf_rn(x[u][i].z, fu, b.x), __fmaf_rn(x[u][i].w, fu, b.y));
+                }
+            }
         }
         if (SW == 1) {
             acc.fold(st);
