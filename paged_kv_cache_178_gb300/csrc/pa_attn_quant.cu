@@ -853,9 +853,11 @@ __global__ void __launch_bounds__(kAllThreads, ctas_per_sm(DH, RN)) quant_attn_k
 }
 
 // Folds the chunk records of the groups with several chunks.  Bound by round
-// trips to L2: a warp folds a span of a row, all its records in flight (at head
-// dim 256 eight of them, at 512 four), all rows and all spans (16 / rows per
-// CTA at a time) side by side; then one warp folds the spans of a row.  131k
+// trips to L2: a warp folds 128 * V elements of a row over a span, 16 / V
+// records in flight; all parts, rows and spans (up to 16 warps to a CTA) side by
+// side; then one warp folds the spans of a part.  V is 1 while an SM is there
+// for every CTA, else the whole row (head dim 512, 4 requests 12.0 us against
+// 14.0, but 64 of them 58.6 against 51.5).  131k
 // keys on 8 KV heads: 32.2 us with spans of 32 chunks, 31.6 of 8, 30.1 of 16.
 constexpr int kFoldThreads = 512;  // at most
 // Up to this many tiles a CTA sums the chunks before its own while it waits for
@@ -863,13 +865,14 @@ constexpr int kFoldThreads = 512;  // at most
 // more, but 2048 tiles cost every CTA as many loads).
 constexpr int kFoldSums = 256;
 
-template <int DH>
+template <int DH, int V>  // V: float4 of a lane
 __global__ void __launch_bounds__(kFoldThreads) quant_fold_kernel(const Params p, int SW)
 {
-    constexpr int V = DH / 128;  // float4 of a lane
-    __shared__ __align__(16) float s_state[kFoldThreads / 32][DH + 4];
+    constexpr int PARTS = DH / (128 * V);
+    __shared__ __align__(16) float s_state[kFoldThreads / 32][128 * V + 4];
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-    const int row = blockIdx.y * (blockDim.x / 32 / SW) + warp / SW, slot = warp % SW;
+    const int item = blockIdx.y * (blockDim.x / 32 / SW) + warp / SW, slot = warp % SW;
+    const int row = item / PARTS, col = item % PARTS * 128 * V + 4 * lane;
     const int tile = blockIdx.x / p.hkv, kvh = blockIdx.x - tile * p.hkv;
     // The metadata's writers are done (the attention kernel waited for them
     // before it let this one start), so it is read while that one still runs.
@@ -901,7 +904,7 @@ __global__ void __launch_bounds__(kFoldThreads) quant_fold_kernel(const Params p
     const bool live = row < m.qn * p.group;
     const uint32_t hdr = (uint32_t)part_header_floats(p.rows), size = (uint32_t)part_record_floats(p.rows, DH);
     const float *rec = p.records + ((int64_t)p.hkv * c0 + (int64_t)kvh * nch) * size + (live ? row : 0);
-    const float *ro = rec - (live ? row : 0) + (hdr + (uint32_t)((live ? row : 0) * DH + 4 * lane));
+    const float *ro = rec - (live ? row : 0) + (hdr + (uint32_t)((live ? row : 0) * DH + col));
     State<1, 2 * V> acc;
     acc.clear();
     const int spans = (nch + kSpan - 1) / kSpan;
@@ -959,22 +962,22 @@ __global__ void __launch_bounds__(kFoldThreads) quant_fold_kernel(const Params p
             acc.fold(st);
             continue;
         }
-        // the spans of this pass, in order, by the row's first warp
+        // the spans of this pass, in order, by the part's first warp
 #pragma unroll
         for (int i = 0; i < V; ++i)
             *reinterpret_cast<float4 *>(&s_state[warp][4 * lane + 128 * i]) =
                 make_float4(st.o[2 * i][0].x, st.o[2 * i][0].y, st.o[2 * i + 1][0].x, st.o[2 * i + 1][0].y);
         if (lane == 0) {
-            s_state[warp][DH] = st.m[0];
-            s_state[warp][DH + 1] = st.l[0];
+            s_state[warp][128 * V] = st.m[0];
+            s_state[warp][128 * V + 1] = st.l[0];
         }
         __syncthreads();
         if (slot == 0)
             for (int k = 0; k < SW && s0 + k < spans; ++k) {
                 const float *t = s_state[warp + k];
                 State<1, 2 * V> x;
-                x.m[0] = t[DH];
-                x.l[0] = t[DH + 1];
+                x.m[0] = t[128 * V];
+                x.l[0] = t[128 * V + 1];
 #pragma unroll
                 for (int i = 0; i < V; ++i) {
                     const float4 v = *reinterpret_cast<const float4 *>(t + 4 * lane + 128 * i);
@@ -991,10 +994,10 @@ __global__ void __launch_bounds__(kFoldThreads) quant_fold_kernel(const Params p
     const float f = __frcp_rn(acc.l[0]) * p.v_scale;
 #pragma unroll
     for (int i = 0; i < V; ++i)
-        *reinterpret_cast<uint2 *>(p.out + at * DH + 4 * lane + 128 * i) =
+        *reinterpret_cast<uint2 *>(p.out + at * DH + col + 128 * i) =
             make_uint2(pack_bf16x2(acc.o[2 * i][0].x * f, acc.o[2 * i][0].y * f),
                        pack_bf16x2(acc.o[2 * i + 1][0].x * f, acc.o[2 * i + 1][0].y * f));
-    if (lane == 0 && p.lse)
+    if (col == 0 && p.lse)
         p.lse[at] = lse_of(acc.m[0], acc.l[0] * 0x1p-15f);
 }
 
@@ -1047,14 +1050,16 @@ cudaError_t launch(const Params &p, cudaStream_t stream, int64_t grid)
     const int64_t chunks = chunks_of(DH, p.max_seq_len);
     if (e != cudaSuccess || chunks <= 1)
         return e;
-    int sw = 1;  // spans of a row side by side
+    int sw = 1;  // spans of a part side by side
     while (sw < kFoldThreads / 32 && sw * kSpan < chunks)
         sw *= 2;
-    const int most = kFoldThreads / 32 / sw, rows = p.rows < most ? p.rows : most;
-    cfg.gridDim = dim3((unsigned)(p.num_tiles * p.hkv), (unsigned)((p.rows + rows - 1) / rows));
-    cfg.blockDim = dim3(32 * sw * rows);
+    const int most = kFoldThreads / 32 / sw, parts = p.rows * (DH / 128);
+    const bool split = (int64_t)p.num_tiles * p.hkv * ((parts + most - 1) / most) <= kGridSms;
+    const int items = split ? parts : p.rows, some = items < most ? items : most;
+    cfg.gridDim = dim3((unsigned)(p.num_tiles * p.hkv), (unsigned)((items + some - 1) / some));
+    cfg.blockDim = dim3(32 * sw * some);
     cfg.dynamicSmemBytes = 0;
-    return cudaLaunchKernelEx(&cfg, quant_fold_kernel<DH>, p, sw);
+    return cudaLaunchKernelEx(&cfg, split ? quant_fold_kernel<DH, 1> : quant_fold_kernel<DH, DH / 128>, p, sw);
 }
 
 }  // namespace qa

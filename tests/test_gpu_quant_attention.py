@@ -162,6 +162,21 @@ def test_drafted_tokens_equal_single_steps_in_bits(new, hq, hkv, dh):
         assert _same(o, out[rows]) and _same(l, lse[rows]), i
 
 
+@pytest.mark.parametrize("dh,hq,hkv,new", [(128, 8, 2, 1), (256, 8, 2, 3), (512, 8, 2, 2)])
+def test_rows_of_a_large_batch_equal_those_of_small_calls(dh, hq, hkv, new):
+    """The folding kernel splits rows between warps only in small calls, and
+    the deal of the chunks depends on the batch: no bit may."""
+    lens = [700, 33, 5000, 300] * 40
+    c = Case(lens, new, hq, hkv, dh, seed=dh + 1)
+    out, lse = c.run()
+    for b in (0, 2, 7, 158):
+        rows = torch.arange(b * new, (b + 1) * new, device="cuda")
+        o, l = c.run(q=c.q[rows], block_tables=c.bt[b:b + 1].contiguous(), seq_lens=c.sl[b:b + 1].contiguous(),
+                     query_start_loc=torch.tensor([0, new], dtype=torch.int32, device="cuda"), max_s=lens[b])
+        assert _same(o, out[rows]) and _same(l, lse[rows]), b
+    assert pa.check_errors() == (pa.PA_OK, -1)
+
+
 def test_bytes_past_the_length_and_unseen_nans_do_not_matter():
     c = Case([37, 130, 20], [3, 2, 1], 8, 2, 128, seed=8)
     out, lse = c.run()
