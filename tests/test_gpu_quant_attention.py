@@ -166,10 +166,10 @@ def test_drafted_tokens_equal_single_steps_in_bits(new, hq, hkv, dh):
 def test_rows_of_a_large_batch_equal_those_of_small_calls(dh, hq, hkv, new):
     """The folding kernel splits rows between warps only in small calls, and
     the deal of the chunks depends on the batch: no bit may."""
-    lens = [700, 33, 5000, 300] * 40
+    lens = [700, 33, 5000, 300] * 12
     c = Case(lens, new, hq, hkv, dh, seed=dh + 1)
     out, lse = c.run()
-    for b in (0, 2, 7, 158):
+    for b in (0, 2, 7, 46):
         rows = torch.arange(b * new, (b + 1) * new, device="cuda")
         o, l = c.run(q=c.q[rows], block_tables=c.bt[b:b + 1].contiguous(), seq_lens=c.sl[b:b + 1].contiguous(),
                      query_start_loc=torch.tensor([0, new], dtype=torch.int32, device="cuda"), max_s=lens[b])
