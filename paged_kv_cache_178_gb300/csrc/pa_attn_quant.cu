@@ -325,9 +325,9 @@ __global__ void __launch_bounds__(kAllThreads, ctas_per_sm(DH, RN)) quant_attn_k
     }
     // chunks of a KV head of each tile, and their weights: pages, and what a
     // chunk costs without any
-    longlong2 total;
+    int2 total;  // (the host's limits keep the sums below 2^31)
     block_exclusive_sums2<kAllThreads>(
-        p.num_tiles, s_pre, s_weight, reinterpret_cast<longlong2 *>(smem + Lay::sums), total,
+        p.num_tiles, s_pre, s_weight, reinterpret_cast<int2 *>(smem + Lay::sums), total,
         [&](int tile, int &chunks, int &weight) {
             const Meta m = meta_of(p, tile);
             if (!m.ok && blockIdx.x == 0)
@@ -373,7 +373,7 @@ __global__ void __launch_bounds__(kAllThreads, ctas_per_sm(DH, RN)) quant_attn_k
     // The chunks in order, a group's one after another, are cut where their
     // weights add up to equal shares: a CTA takes those that start in its share
     // (one each when there are no more chunks than CTAs).
-    const int64_t T = total.x * hkv, W = total.y * hkv;
+    const int64_t T = (int64_t)total.x * hkv, W = (int64_t)total.y * hkv;
     int64_t lo = blockIdx.x, hi = lo + 1;
     if (T > (int64_t)gridDim.x) {
         // lane 0 of each warp finds the start of this share, lane 1 of the next

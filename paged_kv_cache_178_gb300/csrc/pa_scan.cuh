@@ -57,34 +57,36 @@ __device__ __forceinline__ long long block_exclusive_sums(int n, int32_t *off, l
     return base;
 }
 
-// The same for two counts at once: count(b, first, second).
-template <int NTH, typename Count>
-__device__ __forceinline__ void block_exclusive_sums2(int n, int32_t *off0, int32_t *off1, longlong2 *warp_sums,
-                                                      longlong2 &total, Count count)
+// The same for two counts at once: count(b, first, second).  Pair is longlong2,
+// or int2 where the sums are known to fit.
+template <int NTH, typename Pair, typename Count>
+__device__ __forceinline__ void block_exclusive_sums2(int n, int32_t *off0, int32_t *off1, Pair *warp_sums, Pair &total,
+                                                      Count count)
 {
+    using Sum = decltype(Pair::x);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    longlong2 base = make_longlong2(0, 0);
+    Pair base{0, 0};
     for (int b0 = 0; b0 < n; b0 += NTH) {
         const int b = b0 + tid;
         int c0 = 0, c1 = 0;
         if (b < n)
             count(b, c0, c1);
-        long long i0 = c0, i1 = c1;
+        Sum i0 = c0, i1 = c1;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
-            const long long x0 = __shfl_up_sync(0xffffffffu, i0, o), x1 = __shfl_up_sync(0xffffffffu, i1, o);
+            const Sum x0 = __shfl_up_sync(0xffffffffu, i0, o), x1 = __shfl_up_sync(0xffffffffu, i1, o);
             if (lane >= o) {
                 i0 += x0;
                 i1 += x1;
             }
         }
         if (lane == 31)
-            warp_sums[warp] = make_longlong2(i0, i1);
+            warp_sums[warp] = Pair{i0, i1};
         __syncthreads();
-        longlong2 before = base;
+        Pair before = base;
 #pragma unroll
         for (int w = 0; w < NTH / 32; ++w) {
-            const longlong2 s = warp_sums[w];
+            const Pair s = warp_sums[w];
             before.x += w < warp ? s.x : 0;
             before.y += w < warp ? s.y : 0;
             base.x += s.x;
