@@ -47,7 +47,7 @@
 // Measured, head dim 128 unless said: 64 requests of 7168, 7168, 4171 and 513
 // keys with 8 query and 2 KV heads (88 MB) 29.5 us, of which the metadata and
 // the shares take 2, the first chunk 7, three more 4.2 each (5.3 TB/s, two CTAs
-// per SM), uneven ends 4 and the fold 3; four of them 9.0 us; 131072 keys and 32
+// per SM), uneven ends 4 and the fold 3; four of them 8.8 us; 131072 keys and 32
 // query and 4 KV heads 29.9 us; 16 requests of up to 5000 keys with five new
 // tokens at head dim 256 24.1 us, 4.8 a chunk of 256 keys.
 #include <cstdio>
