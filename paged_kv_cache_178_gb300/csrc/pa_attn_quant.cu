@@ -47,8 +47,8 @@
 // Measured, head dim 128 unless said: 64 requests of 7168, 7168, 4171 and 513
 // keys with 8 query and 2 KV heads (88 MB) 29.5 us, of which the metadata and
 // the shares take 2, the first chunk 7, three more 4.2 each (5.3 TB/s, two CTAs
-// per SM), uneven ends 4 and the fold 3; four of them 8.8 us; 131072 keys and 32
-// query and 4 KV heads 29.9 us; 16 requests of up to 5000 keys with five new
+// per SM), uneven ends 4 and the fold 3; four of them 8.2 us; 131072 keys and 32
+// query and 4 KV heads 29.6 us; 16 requests of up to 5000 keys with five new
 // tokens at head dim 256 24.1 us, 4.8 a chunk of 256 keys.
 #include <cstdio>
 #include <type_traits>
@@ -125,6 +125,7 @@ struct Params {
     int32_t max_blocks, hq, hkv, group, max_query_len, max_seq_len;
     int32_t tile_shift, tile_tokens;  // a request's tokens form 1 << tile_shift tiles of tile_tokens
     int32_t num_tiles;  // of all requests
+    int32_t per_group;  // a CTA for each of so many chunks of every group (0: the chunks are dealt out)
     int32_t rows;       // rows of a record (of a tile)
     int64_t max_pages;  // pages of all requests together
     float score_scale;  // scale * log2(e) * k_scale
@@ -201,23 +202,36 @@ struct Chunk {
     int qs, qn, L, seen;
     const int32_t *row;  // the request's block table
 
-    __device__ __forceinline__ void load(const Params &p, const int32_t *pre)
+    __device__ __forceinline__ void load(const Params &p)
     {
         const Meta m = meta_of(p, tile);
         qs = m.qs;
         qn = m.qn;
         L = m.L;
         seen = m.seen;
-        nch = pre[tile + 1] - pre[tile];
+        nch = (L + chunk_keys(DH) - 1) / chunk_keys(DH);
         row = p.block_tables + (int64_t)(tile >> p.tile_shift) * p.max_blocks;
     }
     __device__ __forceinline__ void at(const Params &p, const int32_t *pre, int64_t x)
     {
         tile = owner_of(pre, p.num_tiles, (int)div_floor(x, p.hkv));
-        load(p, pre);
+        load(p);
         const int r = (int)(x - (int64_t)p.hkv * pre[tile]);
         kvh = (int)((uint32_t)r / (uint32_t)nch);
         lc = r - kvh * nch;
+    }
+    // the first chunk of a CTA
+    __device__ __forceinline__ void start(const Params &p, const int32_t *pre, int64_t x)
+    {
+        if (p.per_group == 0) {
+            at(p, pre, x);
+            return;
+        }
+        const uint32_t group = (uint32_t)x / (uint32_t)p.per_group;
+        tile = (int)(group / (uint32_t)p.hkv);
+        kvh = (int)(group - (uint32_t)tile * p.hkv);
+        lc = (int)((uint32_t)x - group * p.per_group);
+        load(p);
     }
     // the chunk after this one (there is one)
     __device__ __forceinline__ void next(const Params &p, const int32_t *pre)
@@ -231,7 +245,7 @@ struct Chunk {
         do
             ++tile;
         while (pre[tile + 1] == pre[tile]);
-        load(p, pre);
+        load(p);
     }
     __device__ __forceinline__ bool has_page(int i) const { return (lc * chunk_pages(DH) + i) * 16 < L; }
     // block id of the chunk's page i (0 where there is none)
@@ -323,77 +337,97 @@ __global__ void __launch_bounds__(kAllThreads, ctas_per_sm(DH, RN)) quant_attn_k
         s_bad[0] = s_bad[1] = 0;
         fence_barrier_init();
     }
-    // chunks of a KV head of each tile, and their weights: pages, and what a
-    // chunk costs without any
-    int2 total;  // (the host's limits keep the sums below 2^31)
-    block_exclusive_sums2<kAllThreads>(
-        p.num_tiles, s_pre, s_weight, reinterpret_cast<int2 *>(smem + Lay::sums), total,
-        [&](int tile, int &chunks, int &weight) {
-            const Meta m = meta_of(p, tile);
-            if (!m.ok && blockIdx.x == 0)
-                record_error(p.err, kErrBadMetadata, tile >> p.tile_shift);
-            if (m.ok && m.qn > 0) {
-                chunks = (m.L + kChunk - 1) / kChunk;
-                weight = (m.L + 15) / 16 + kChunkCost * chunks;
+    // rows of a tile with bad lengths, or in a call without room for its records
+    auto nan_rows = [&](const Meta &m, bool over) {
+        if (!m.sane || (m.ok && !over))
+            return;
+        const int64_t first = (int64_t)m.qs * p.hq, n = (int64_t)m.qn * p.hq;
+        for (int64_t k = tid; k < n * DH; k += kAllThreads)
+            p.out[first * DH + k] = __ushort_as_bfloat16(0x7FC0);
+        if (p.lse)
+            for (int64_t k = tid; k < n; k += kAllThreads)
+                p.lse[first + k] = __int_as_float(0x7FC00000);
+    };
+    int64_t lo, hi;  // chunks of this CTA
+    if (p.per_group) {
+        // Few: a CTA for each that the bounds allow, found without the others
+        // (4 requests 8.2 us, dealt out 8.8).
+        Chunk<DH> c;
+        c.start(p, s_pre, blockIdx.x);
+        const Meta m = meta_of(p, c.tile);
+        if (c.kvh == 0 && c.lc == 0) {
+            if (!m.ok && tid == 0)
+                record_error(p.err, kErrBadMetadata, c.tile >> p.tile_shift);
+            nan_rows(m, false);
+        }
+        lo = blockIdx.x;
+        hi = lo + (m.ok && m.qn > 0 && c.lc < c.nch);
+        if (hi == lo)
+            return;
+        __syncthreads();  // the barriers are set up
+    } else {
+        // chunks of a KV head of each tile, and their weights: pages, and what a
+        // chunk costs without any
+        int2 total;  // (the host's limits keep the sums below 2^31)
+        block_exclusive_sums2<kAllThreads>(
+            p.num_tiles, s_pre, s_weight, reinterpret_cast<int2 *>(smem + Lay::sums), total,
+            [&](int tile, int &chunks, int &weight) {
+                const Meta m = meta_of(p, tile);
+                if (!m.ok && blockIdx.x == 0)
+                    record_error(p.err, kErrBadMetadata, tile >> p.tile_shift);
+                if (m.ok && m.qn > 0) {
+                    chunks = (m.L + kChunk - 1) / kChunk;
+                    weight = (m.L + 15) / 16 + kChunkCost * chunks;
+                }
+            });
+        bool over = false;
+        if (p.max_pages != INT64_MAX) {
+            // pages of the requests: of their first tiles
+            long long pages = 0;
+            for (int b = lane; b < p.num_tiles >> p.tile_shift; b += 32) {
+                const int i = b << p.tile_shift;
+                pages += s_weight[i + 1] - s_weight[i] - kChunkCost * (s_pre[i + 1] - s_pre[i]);
             }
-        });
-    bool over = false;
-    if (p.max_pages != INT64_MAX) {
-        // pages of the requests: of their first tiles
-        long long pages = 0;
-        for (int b = lane; b < p.num_tiles >> p.tile_shift; b += 32) {
-            const int i = b << p.tile_shift;
-            pages += s_weight[i + 1] - s_weight[i] - kChunkCost * (s_pre[i + 1] - s_pre[i]);
-        }
 #pragma unroll
-        for (int w = 16; w; w >>= 1)
-            pages += __shfl_xor_sync(0xffffffffu, pages, w);
-        over = pages > p.max_pages;
-        if (over && blockIdx.x == 0 && tid == 0)
-            record_error(p.err, kErrBudget, pages);
-    }
-    for (int i = blockIdx.x; i < p.num_tiles; i += gridDim.x) {
-        if (s_pre[i + 1] != s_pre[i] && !over)
-            continue;
-        const Meta m = meta_of(p, i);
-        if (m.sane && (!m.ok || over)) {  // bad lengths, or no room for the records: NaN rows
-            const int64_t first = (int64_t)m.qs * p.hq, n = (int64_t)m.qn * p.hq;
-            for (int64_t k = tid; k < n * DH; k += kAllThreads)
-                p.out[first * DH + k] = __ushort_as_bfloat16(0x7FC0);
-            if (p.lse)
-                for (int64_t k = tid; k < n; k += kAllThreads)
-                    p.lse[first + k] = __int_as_float(0x7FC00000);
+            for (int w = 16; w; w >>= 1)
+                pages += __shfl_xor_sync(0xffffffffu, pages, w);
+            over = pages > p.max_pages;
+            if (over && blockIdx.x == 0 && tid == 0)
+                record_error(p.err, kErrBudget, pages);
         }
-    }
-    if (blockIdx.x == 0)  // for the folding kernel
-        for (int i = tid; i <= p.num_tiles; i += kAllThreads)
-            p.offsets[i] = over ? 0 : s_pre[i];
-    if (over)
-        return;
-    // The chunks in order, a group's one after another, are cut where their
-    // weights add up to equal shares: a CTA takes those that start in its share
-    // (one each when there are no more chunks than CTAs).
-    const int64_t T = (int64_t)total.x * hkv, W = (int64_t)total.y * hkv;
-    int64_t lo = blockIdx.x, hi = lo + 1;
-    if (T > (int64_t)gridDim.x) {
-        // lane 0 of each warp finds the start of this share, lane 1 of the next
-        constexpr int kFull = kPages + kChunkCost;  // weight of a whole chunk
-        const int64_t cta = (int64_t)blockIdx.x + (lane & 1);
-        int64_t start = T;
-        if (cta < gridDim.x) {
-            const int64_t at = div_floor(cta * W + gridDim.x - 1, gridDim.x);
-            const int i = owner_of(s_weight, p.num_tiles, (int)div_floor(at, hkv));
-            const int n = s_pre[i + 1] - s_pre[i], w = s_weight[i + 1] - s_weight[i];
-            const int64_t rem = at - (int64_t)hkv * s_weight[i];
-            const int h = (int)div_floor(rem, w), lc = ((int)(rem - (int64_t)h * w) + kFull - 1) / kFull;
-            start = (int64_t)hkv * s_pre[i] + (int64_t)h * n + min(lc, n);
+        for (int i = blockIdx.x; i < p.num_tiles; i += gridDim.x)
+            if (s_pre[i + 1] == s_pre[i] || over)
+                nan_rows(meta_of(p, i), over);
+        if (blockIdx.x == 0)  // for the folding kernel
+            for (int i = tid; i <= p.num_tiles; i += kAllThreads)
+                p.offsets[i] = over ? 0 : s_pre[i];
+        if (over)
+            return;
+        // The chunks in order, a group's one after another, are cut where their
+        // weights add up to equal shares: a CTA takes those that start in its share
+        // (one each when there are no more chunks than CTAs).
+        const int64_t T = (int64_t)total.x * hkv, W = (int64_t)total.y * hkv;
+        lo = blockIdx.x, hi = lo + 1;
+        if (T > (int64_t)gridDim.x) {
+            // lane 0 of each warp finds the start of this share, lane 1 of the next
+            constexpr int kFull = kPages + kChunkCost;  // weight of a whole chunk
+            const int64_t cta = (int64_t)blockIdx.x + (lane & 1);
+            int64_t start = T;
+            if (cta < gridDim.x) {
+                const int64_t at = div_floor(cta * W + gridDim.x - 1, gridDim.x);
+                const int i = owner_of(s_weight, p.num_tiles, (int)div_floor(at, hkv));
+                const int n = s_pre[i + 1] - s_pre[i], w = s_weight[i + 1] - s_weight[i];
+                const int64_t rem = at - (int64_t)hkv * s_weight[i];
+                const int h = (int)div_floor(rem, w), lc = ((int)(rem - (int64_t)h * w) + kFull - 1) / kFull;
+                start = (int64_t)hkv * s_pre[i] + (int64_t)h * n + min(lc, n);
+            }
+            lo = __shfl_sync(0xffffffffu, start, 0);
+            hi = __shfl_sync(0xffffffffu, start, 1);
         }
-        lo = __shfl_sync(0xffffffffu, start, 0);
-        hi = __shfl_sync(0xffffffffu, start, 1);
-    }
-    if (lo >= hi || lo >= T)
-        return;
+        if (lo >= hi || lo >= T)
+            return;
 
+    }
     const int chunks = (int)(hi - lo);
     if (warp == kWarps) {
         // The copying warp: a lane per page, the K records of a chunk when the
@@ -405,7 +439,7 @@ __global__ void __launch_bounds__(kAllThreads, ctas_per_sm(DH, RN)) quant_attn_k
         const uint64_t policy = l2_policy_evict_first();
         const uint32_t dst = smem_addr(smem) + lane * REC;
         Chunk<DH> c;
-        c.at(p, s_pre, lo);
+        c.start(p, s_pre, lo);
         int id = lane < kPages ? c.id(lane) : 0;
         bool ok = true;
         for (int k = 0; k < chunks; ++k) {
@@ -463,7 +497,7 @@ __global__ void __launch_bounds__(kAllThreads, ctas_per_sm(DH, RN)) quant_attn_k
     auto state_pair = [&](int i) { return HALVES ? 16 * wd + 8 * (warp / 4) + g : 16 * (NE * wd + i / 2) + 8 * (i % 2) + g; };
 
     Chunk<DH> c;
-    c.at(p, s_pre, lo);
+    c.start(p, s_pre, lo);
     const uint32_t rec_hdr = (uint32_t)part_header_floats(p.rows), rec_size = (uint32_t)part_record_floats(p.rows, DH);
 
     // ------------------------------------------------ one chunk's state --
@@ -879,7 +913,7 @@ __global__ void __launch_bounds__(kFoldThreads) quant_fold_kernel(const Params p
     const Meta m = meta_of(p, tile);
     const int nch = m.ok && m.qn > 0 ? (m.L + chunk_keys(DH) - 1) / chunk_keys(DH) : 0;
     int c0 = 0;
-    if (nch > 1 && p.num_tiles <= kFoldSums) {
+    if (nch > 1 && p.per_group == 0 && p.num_tiles <= kFoldSums) {
         __shared__ int s_sum[kFoldThreads / 32];
         for (int i = threadIdx.x; i < tile; i += blockDim.x) {
             const Meta x = meta_of(p, i);
@@ -897,13 +931,15 @@ __global__ void __launch_bounds__(kFoldThreads) quant_fold_kernel(const Params p
     griddep_launch_dependents();
     if (nch <= 1)  // none, or written already
         return;
-    if (p.num_tiles > kFoldSums)
+    if (p.per_group == 0 && p.num_tiles > kFoldSums)
         c0 = __ldcg(p.offsets + tile);
     if (p.max_pages != INT64_MAX && __ldcg(p.offsets + p.num_tiles) == 0)
         return;  // no room for the records
     const bool live = row < m.qn * p.group;
     const uint32_t hdr = (uint32_t)part_header_floats(p.rows), size = (uint32_t)part_record_floats(p.rows, DH);
-    const float *rec = p.records + ((int64_t)p.hkv * c0 + (int64_t)kvh * nch) * size + (live ? row : 0);
+    const int64_t first_record =
+        p.per_group ? (int64_t)blockIdx.x * p.per_group : (int64_t)p.hkv * c0 + (int64_t)kvh * nch;
+    const float *rec = p.records + first_record * size + (live ? row : 0);
     const float *ro = rec - (live ? row : 0) + (hdr + (uint32_t)((live ? row : 0) * DH + col));
     State<1, 2 * V> acc;
     acc.clear();
@@ -1019,14 +1055,24 @@ static int64_t grid_of(int dh, int rn, int64_t max_chunks)
 }
 
 static int64_t chunks_of(int dh, int32_t len) { return ((int64_t)len + chunk_keys(dh) - 1) / chunk_keys(dh); }
-// Chunks of all groups at most.
+// log2 of the tiles that a request's share of the numbering has room for.
+static int tile_shift_of(int tiles)
+{
+    int shift = 0;
+    while (1 << shift < tiles)
+        ++shift;
+    return shift;
+}
+
+// Chunks of all groups at most, of tiles without tokens among them (a CTA for
+// each chunk that the bounds allow numbers its records that way).
 static int64_t max_chunks_of(int32_t num_seqs, int32_t tiles, int32_t hkv, int dh, int32_t max_seq_len,
                              int64_t max_pages)
 {
     int64_t per_head = (int64_t)num_seqs * chunks_of(dh, max_seq_len);
     if (max_pages > 0 && max_pages / chunk_pages(dh) + num_seqs < per_head)
         per_head = max_pages / chunk_pages(dh) + num_seqs;  // whole ones, and one in part a request
-    return per_head * tiles * hkv;
+    return (per_head << tile_shift_of(tiles)) * hkv;
 }
 
 template <int DH, int RN>
@@ -1067,15 +1113,6 @@ cudaError_t launch(const Params &p, cudaStream_t stream, int64_t grid)
 // The tiles' offsets, then the records.
 static size_t offset_bytes(int32_t num_tiles) { return (((size_t)num_tiles + 1) * 4 + 255) / 256 * 256; }
 
-// log2 of the tiles that a request's share of the numbering has room for.
-static int tile_shift_of(int tiles)
-{
-    int shift = 0;
-    while (1 << shift < tiles)
-        ++shift;
-    return shift;
-}
-
 int quant_attn_tiles(int32_t num_seqs, int32_t num_kv_heads, int head_dim, int group, int32_t max_query_len,
                      int32_t max_seq_len)
 {
@@ -1083,7 +1120,7 @@ int quant_attn_tiles(int32_t num_seqs, int32_t num_kv_heads, int head_dim, int g
     if (tokens == 0)
         return 0;
     const int64_t tiles = max_query_len <= tokens ? 1 : ((int64_t)max_query_len + tokens - 1) / tokens;
-    if (tiles > kQuantMaxTiles || ((int64_t)num_seqs << tile_shift_of((int)tiles)) > kQuantMaxTiles)
+    if (tiles > kQuantMaxTiles || ((int64_t)num_seqs << qa::tile_shift_of((int)tiles)) > kQuantMaxTiles)
         return 0;
     if (tiles > 2) {
         // Estimates in ns: a wave of chunks here, against a start and the keys
@@ -1108,7 +1145,7 @@ int quant_attn_tiles(int32_t num_seqs, int32_t num_kv_heads, int head_dim, int g
 size_t quant_attn_bytes(int32_t num_seqs, int tiles, int32_t num_kv_heads, int32_t head_dim, int rows,
                         int32_t max_seq_len, int64_t max_pages)
 {
-    return offset_bytes(num_seqs << tile_shift_of(tiles)) +
+    return offset_bytes(num_seqs << qa::tile_shift_of(tiles)) +
            (size_t)qa::max_chunks_of(num_seqs, tiles, num_kv_heads, head_dim, max_seq_len, max_pages) *
                (size_t)part_record_floats(rows, head_dim) * 4;
 }
@@ -1135,7 +1172,7 @@ cudaError_t launch_quant_attention(const QuantAttnArgs &a, ErrState *err, cudaSt
     p.max_query_len = a.max_query_len;
     p.max_seq_len = a.max_seq_len;
     const int tiles = quant_attn_tiles(a.num_seqs, p.hkv, a.pool.head_dim, p.group, a.max_query_len, a.max_seq_len);
-    p.tile_shift = tile_shift_of(tiles);
+    p.tile_shift = qa::tile_shift_of(tiles);
     p.tile_tokens = (a.max_query_len + tiles - 1) / tiles;
     p.num_tiles = a.num_seqs << p.tile_shift;
     p.rows = p.tile_tokens * p.group;
@@ -1148,7 +1185,15 @@ cudaError_t launch_quant_attention(const QuantAttnArgs &a, ErrState *err, cudaSt
     const int64_t max_chunks =
         qa::max_chunks_of(a.num_seqs, tiles, p.hkv, a.pool.head_dim, p.max_seq_len, a.max_pages);
     const int rn = qa::rows_capacity(p.rows);
-    const int64_t grid = qa::grid_of(a.pool.head_dim, rn, max_chunks);
+    int64_t grid = qa::grid_of(a.pool.head_dim, rn, max_chunks);
+    const int64_t per_group = qa::chunks_of(a.pool.head_dim, p.max_seq_len);
+    const bool limited = a.max_pages > 0 && a.max_pages < a.num_seqs * (((int64_t)p.max_seq_len + 15) / 16);
+    if (!limited && per_group > 0 &&
+        (int64_t)p.num_tiles * p.hkv * per_group <= (int64_t)qa::kGridSms * qa::ctas_per_sm(a.pool.head_dim, rn)) {
+        p.per_group = (int32_t)per_group;
+        grid = (int64_t)p.num_tiles * p.hkv * per_group;
+        p.max_pages = INT64_MAX;
+    }
     p.offsets = static_cast<int32_t *>(a.workspace);
     p.records = reinterpret_cast<float *>(static_cast<uint8_t *>(a.workspace) + offset_bytes(p.num_tiles));
     cudaError_t e = cudaErrorNotSupported;
