@@ -250,8 +250,10 @@ cudaError_t launch_quant_write(const void *key, int64_t key_stride, const void *
 // 16-byte loads, the bytes regrouped by token with permutes), neighbouring
 // lanes neighbouring elements; every store instruction then covers whole rows.
 // 66 thousand tokens of 8 KV heads at head dim 128 (76 MB read, 268 written)
-// take 57 us alone, 6.0 TB/s, with three CTAs per SM.  Loads and stores are
-// marked as streaming: in a row of launches 67 us (neither: 71, one of them 69).
+// take 57 us alone, 6.0 TB/s, with three CTAs per SM.  (Marked as streaming,
+// loads and stores took 67 us instead of 71 in a row of launches, but write and
+// read-back of 19 thousand tokens of 2 KV heads 11.0 instead of 9.9: what is
+// read back is read again soon.)
 __device__ __forceinline__ uint4 values8(uint32_t codes, uint32_t scale_pair, float tensor_scale)
 {
     uint32_t p[4];
@@ -370,7 +372,7 @@ __global__ void __launch_bounds__(kQuantThreads) dequantize_kv_kernel(
 #pragma unroll
                 for (int i = 0; i < STEPS; ++i) {
                     const int x = 512 * part + 32 * i + lane;
-                    word[i] = __ldcs(reinterpret_cast<const uint32_t *>(rec) + x);
+                    word[i] = __ldg(reinterpret_cast<const uint32_t *>(rec) + x);
                     sb[i] = __ldg(rec + quant_code_bytes(DH) + x / 2);
                 }
                 uint4 *dst = k_out + ((int64_t)kx[j].c * 16 * hk + kx[j].h) * VEC;
@@ -378,8 +380,8 @@ __global__ void __launch_bounds__(kQuantThreads) dequantize_kv_kernel(
                 for (int i = 0; i < STEPS; ++i) {
                     const int x = 512 * part + 32 * i + lane;
                     const uint32_t s = e4m3x2_to_f16x2(sb[i]);
-                    __stcs(&dst[(int64_t)(x / VEC) * hk * VEC + x % VEC],
-                        ok ? values8(word[i], __byte_perm(s, 0u, 0x1010), pool.k_scale) : qnan);
+                    dst[(int64_t)(x / VEC) * hk * VEC + x % VEC] =
+                        ok ? values8(word[i], __byte_perm(s, 0u, 0x1010), pool.k_scale) : qnan;
                 }
             }
         }
@@ -394,7 +396,7 @@ __global__ void __launch_bounds__(kQuantThreads) dequantize_kv_kernel(
             uint4 col[4];  // element pairs 4i .. 4i+3, sixteen tokens each
 #pragma unroll
             for (int j = 0; j < 4; ++j)
-                col[j] = __ldcs(reinterpret_cast<const uint4 *>(rec) + 4 * i + j);
+                col[j] = __ldg(reinterpret_cast<const uint4 *>(rec) + 4 * i + j);
             const uint4 sc = __ldg(reinterpret_cast<const uint4 *>(rec + quant_code_bytes(DH)) + i / 2);
 #pragma unroll
             for (int t4 = 0; t4 < 4; ++t4) {
@@ -410,7 +412,7 @@ __global__ void __launch_bounds__(kQuantThreads) dequantize_kv_kernel(
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
                     const uint32_t sp = __byte_perm(k < 2 ? s01 : s23, 0u, k % 2 ? 0x3232 : 0x1010);
-                    __stcs(&dst[(int64_t)(4 * t4 + k) * hk * VEC], ok ? values8(tw[k], sp, pool.v_scale) : qnan);
+                    dst[(int64_t)(4 * t4 + k) * hk * VEC] = ok ? values8(tw[k], sp, pool.v_scale) : qnan;
                 }
             }
         }
