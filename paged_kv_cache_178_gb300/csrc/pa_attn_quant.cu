@@ -652,13 +652,17 @@ __global__ void __launch_bounds__(kAllThreads, ctas_per_sm(DH, RN)) quant_attn_k
                 const float4 u = *reinterpret_cast<const float4 *>(s_max + r * kWarps);
                 const float4 v = *reinterpret_cast<const float4 *>(s_max + r * kWarps + 4);
                 const float cq = s_cq[r];
-                const float m = fmaxf(max3f(u.x, u.y, max3f(u.z, u.w, v.x)), max3f(v.y, v.z, v.w)) * cq;
-                mrow[n][i] = m;
-                const float add = kShift - (m == -INFINITY ? 0.f : m);
+                const float top = fmaxf(max3f(u.x, u.y, max3f(u.z, u.w, v.x)), max3f(v.y, v.z, v.w));
+                mrow[n][i] = top * cq;
+                // The maximum is taken off the raw score: p is then 2^kShift at
+                // the largest key and never above.  (Off the score in log2
+                // units, the two roundings of a product of 2^24 and more are
+                // whole units, and p leaves f16's range.)
+                const float ref = top == -INFINITY ? 0.f : top;
 #pragma unroll
                 for (int j = 0; j < PPW; ++j) {
-                    pr[j][i] = ex2(__fmaf_rn(s[j][n][i], cq, add));  // 0 for keys left out
-                    pr[j][2 + i] = ex2(__fmaf_rn(s[j][n][2 + i], cq, add));
+                    pr[j][i] = ex2(__fmaf_rn(s[j][n][i] - ref, cq, kShift));  // 0 for keys left out
+                    pr[j][2 + i] = ex2(__fmaf_rn(s[j][n][2 + i] - ref, cq, kShift));
                 }
                 l[n][i] = pr[0][i] + pr[0][2 + i];
 #pragma unroll
