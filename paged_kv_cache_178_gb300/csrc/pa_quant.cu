@@ -80,12 +80,15 @@ __device__ __forceinline__ Quantised quantise16(const uint4 &lo, const uint4 &hi
         for (int i = 0; i < 16; ++i)
             q[i] = fminf(fmaxf(q[i], -cap), cap);
     }
-    const uint64_t rr = pack_f32x2(r, r), ss = pack_f32x2(-s, -s), zz = pack_f32x2(-0.f, -0.f);
+    // Everything with the sign turned, -q: a residual of zero is +0 for x of
+    // either sign, its product with -r is then -0, which changes no summand,
+    // the zeros of x = +0 and -0 included (with +r a -0 would be lost in the sum).
+    const uint64_t nr = pack_f32x2(-r, -r), ss = pack_f32x2(s, s), nz = pack_f32x2(-0.f, -0.f);
 #pragma unroll
     for (int i = 0; i < 16; i += 2) {
         const uint64_t x = pack_f32x2(q[i], q[i + 1]);
-        const uint64_t q0 = fma_f32x2(x, rr, zz);  // x*r, zeros with their sign
-        unpack_f32x2(fma_f32x2(fma_f32x2(q0, ss, x), rr, q0), q[i], q[i + 1]);
+        const uint64_t n0 = fma_f32x2(x, nr, nz);  // -q0
+        unpack_f32x2(fma_f32x2(fma_f32x2(n0, ss, x), nr, n0), q[i], q[i + 1]);
     }
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
@@ -98,6 +101,7 @@ __device__ __forceinline__ Quantised quantise16(const uint4 &lo, const uint4 &hi
             : "=r"(o.code[k])
             : "f"(q[8 * k]), "f"(q[8 * k + 1]), "f"(q[8 * k + 2]), "f"(q[8 * k + 3]), "f"(q[8 * k + 4]),
               "f"(q[8 * k + 5]), "f"(q[8 * k + 6]), "f"(q[8 * k + 7]));
+        o.code[k] ^= 0x88888888u;  // the sign turned back
     }
     return o;
 }
