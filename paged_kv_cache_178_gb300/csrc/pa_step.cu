@@ -271,7 +271,7 @@ __global__ void __launch_bounds__(kRopeThreads, kRopeCtas) qk_norm_rope_kernel(c
             have_angles = true;
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-                co[i] = 1.f;  // elements past the rotated part stay as they are
+                co[i] = 1.f;  // (for rows without an angle: not stored, or NaN)
                 si[i] = 0.f;
             }
             if (turned && pos >= 0 && !bad_pos) {
@@ -321,12 +321,19 @@ __global__ void __launch_bounds__(kRopeThreads, kRopeCtas) qk_norm_rope_kernel(c
                 if (INTERLEAVED) {
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
-                        const float u = p[2 * i], v = p[2 * i + 1], m = q[2 * i], o = q[2 * i + 1];
+                        const float u = p[2 * i], v = p[2 * i + 1];
                         p[2 * i] = __fmaf_rn(u, co[i], -(v * si[i]));
                         p[2 * i + 1] = __fmaf_rn(v, co[i], u * si[i]);
-                        q[2 * i] = __fmaf_rn(m, co[4 + i], -(o * si[4 + i]));
-                        q[2 * i + 1] = __fmaf_rn(o, co[4 + i], m * si[4 + i]);
                     }
+                    // (cos 1 and sin 0 would not do: infinities, NaN and -0
+                    // of unrotated elements would change their neighbours)
+                    if (v1 < 2 * rv)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const float m = q[2 * i], o = q[2 * i + 1];
+                            q[2 * i] = __fmaf_rn(m, co[4 + i], -(o * si[4 + i]));
+                            q[2 * i + 1] = __fmaf_rn(o, co[4 + i], m * si[4 + i]);
+                        }
                 } else {
 #pragma unroll
                     for (int i = 0; i < 8; ++i) {
