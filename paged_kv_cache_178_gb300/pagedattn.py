@@ -307,8 +307,9 @@ class PreparedCall:
     def __init__(self, fn, args, what: str, keep):
         # The arguments are converted here, and the call goes through a function
         # object without argument types, which would convert them each time
-        # (22 arguments: 2.1 us a call, 1.1 so).
-        self._args = tuple(t(a) if isinstance(a, (int, float)) or a is None else a for t, a in zip(fn.argtypes, args))
+        # (22 arguments: 2.1 us a call, 1.1 so).  from_param is the prototypes'
+        # own conversion: what they take (numpy and torch integers too) or refuse.
+        self._args = tuple(t.from_param(a) for t, a in zip(fn.argtypes, args))
         self._fn = load()[fn.__name__]
         self._fn.restype = fn.restype
         self._what, self._keep = what, keep
