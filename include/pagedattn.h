@@ -559,16 +559,20 @@ PA_API pa_status pa_check_errors(pa_stream_t stream, int64_t *first_bad_index);
 /*
  * Sets the time limit of the one wait in the split-KV fold that depends on
  * other CTAs (the folders of a (request, KV head) group waiting until every
- * CTA of the group has published its chunk state) and returns the previous
+ * CTA of the group has published its chunk state), and of the waits for copied
+ * pages in pa_paged_attention_quant's direct kernels, and returns the previous
  * limit.  The default is 2 s.  It exists to exercise the timeout path ("ROCm:
  * harden compact peer-local KV prefill for Gemma-4", Required hardening:
  * bounded waits, fatal after submit, no retry): with 0 the waiting CTAs give
  * up at once, latch PA_ERR_TIMEOUT and leave their share of the rows
  * unwritten; the kernel still ends normally.  While nothing is copied or
- * computed at that point, no other wait is affected.  The value is read at
+ * computed at that point, no other wait is affected.  In the direct kernels
+ * every wait then gives up at once, and a CTA ends when the copies that it
+ * asked for have landed (2 s at most).  The value is read at
  * each launch (a captured CUDA graph keeps the value of its capture) and is
  * process-wide.  After a call that reported PA_ERR_TIMEOUT, zero-fill the
- * workspace before reusing it.
+ * workspace before reusing it (that of pa_paged_attention_quant needs no
+ * particular contents).
  */
 PA_API uint64_t pa_set_fold_wait_limit_ns(uint64_t limit_ns);
 

@@ -147,10 +147,10 @@ __device__ __forceinline__ float lse_of(float m, float l)
 
 // Bounded mbarrier wait (inline: no call, so no register spills around it).
 // Gives up when another thread of the CTA already gave up (abort flag) or
-// after kWaitLimitNs, latching PA_ERR_TIMEOUT.
+// after limit_ns, latching PA_ERR_TIMEOUT.
 // The first timeout records (block index << 8) | barrier slot as its index.
 __device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity, volatile int *abort_flag,
-                                         ErrState *err, int where)
+                                         ErrState *err, int where, uint64_t limit_ns = kWaitLimitNs)
 {
     if (mbar_try_wait(bar, parity))
         return true;
@@ -158,7 +158,7 @@ __device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity, volatile
     while (!mbar_try_wait(bar, parity)) {
         if (*abort_flag)
             return false;
-        if (global_timer_ns() - t0 > kWaitLimitNs) {
+        if (global_timer_ns() - t0 > limit_ns) {
             *abort_flag = 1;
             record_error(err, kErrTimeout, ((long long)blockIdx.x << 8) | where);
             return false;

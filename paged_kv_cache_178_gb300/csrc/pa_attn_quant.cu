@@ -134,6 +134,7 @@ struct Params {
     float *lse;
     float *records;     // [chunk]: m, l, O
     int32_t *offsets;   // [num_tiles + 1]: chunks of a KV head before each tile
+    uint64_t wait_ns;   // limit of a wait
     ErrState *err;
 };
 
@@ -325,7 +326,7 @@ __global__ void __launch_bounds__(kAllThreads, ctas_per_sm(DH, RN)) quant_attn_k
     const int G = p.group, hkv = p.hkv;
     enum { kFullK, kFullV, kEmptyK, kEmptyV };
     auto bar = [&](int i) { return smem_addr(smem + Lay::bars + 8 * i); };
-    auto wait = [&](int i, int parity) { return wait_bar(bar(i), parity, s_flags, p.err, i); };
+    auto wait = [&](int i, int parity) { return wait_bar(bar(i), parity, s_flags, p.err, i, p.wait_ns); };
 
     // the work: chunks of the valid requests
     if (tid < 2 * (DH / 16))
@@ -333,7 +334,8 @@ __global__ void __launch_bounds__(kAllThreads, ctas_per_sm(DH, RN)) quant_attn_k
     if (tid == 0) {
         for (int i = 0; i < 4; ++i)
             mbar_init(bar(i), 1);
-        s_flags[0] = s_flags[1] = 0;
+        s_flags[0] = p.wait_ns == 0;  // no time at all: given up from the start
+        s_flags[1] = 0;
         s_bad[0] = s_bad[1] = 0;
         fence_barrier_init();
     }
@@ -442,7 +444,8 @@ __global__ void __launch_bounds__(kAllThreads, ctas_per_sm(DH, RN)) quant_attn_k
         c.start(p, s_pre, lo);
         int id = lane < kPages ? c.id(lane) : 0;
         bool ok = true;
-        for (int k = 0; k < chunks; ++k) {
+        int landing[2] = {0, 0};  // chunks whose K, and V, were asked for
+        for (int k = 0; k < chunks && ok; ++k) {
             const bool exists = lane < kPages && c.has_page(lane);
             const bool go = exists && id >= 0 && (int64_t)id < p.num_blocks;
             const int n = __popc(__ballot_sync(0xffffffffu, go));
@@ -473,15 +476,15 @@ __global__ void __launch_bounds__(kAllThreads, ctas_per_sm(DH, RN)) quant_attn_k
                 __syncwarp();
                 if (go)
                     bulk_copy(dst + v * kPages * REC, (v ? p.v : p.k) + off, REC, bar(v ? kFullV : kFullK), policy);
-            }
-            if (!ok) {
-                // gave up (here or elsewhere in the CTA): let the copies in flight land
-                wait_bar_drain(bar(kFullK), k > 0 ? (k - 1) & 1 : 1);
-                wait_bar_drain(bar(kFullK), k & 1);
-                wait_bar_drain(bar(kFullV), k > 0 ? (k - 1) & 1 : 1);
-                return;
+                landing[v] = k + 1;
             }
         }
+        // Shared memory is given up when the last warp ends, and the computing
+        // warps do not wait for copies once one of them has given up: this warp
+        // stays until the last copies of both kinds have landed (each was asked
+        // for when the one before it had been consumed).
+        wait_bar_drain(bar(kFullK), (landing[0] - 1) & 1);
+        wait_bar_drain(bar(kFullV), (landing[1] - 1) & 1);
         return;
     }
     auto sync = [&]() { named_sync(1, kThreads); };  // the computing warps
@@ -605,16 +608,19 @@ __global__ void __launch_bounds__(kAllThreads, ctas_per_sm(DH, RN)) quant_attn_k
                 if (g == 0)
                     s_max[score_row(n, i) * kWarps + warp] = x;
             }
+        int gave_up = 0;  // of thread 0
         if (tid == 0)
-            s_flags[1] = s_flags[0];  // any thread may set [0] at any time
+            s_flags[1] = gave_up = s_flags[0];  // any thread may set [0] at any time
         sync();  // A: maxima written; K is consumed
         // read between A and B, so that every thread reads the same
         const int bad = s_flags[1] ? -1 : s_bad[parity] == step + 1;
         if (tid < DH / 16)
             s_nan[(parity ^ 1) * (DH / 16) + tid] = 0x7fffffff;  // for the next chunk
-        if (tid == 0)
+        // (after a wait that gave up the copies may not have landed: nothing may
+        // be asked for in their place)
+        if (tid == 0 && !gave_up)
             mbar_arrive(bar(kEmptyK));
-        wait(kFullV, parity);
+        const bool have_v = wait(kFullV, parity);
 #pragma unroll
         for (int j = 0; j < PPW; ++j) {
             const int page = PPW * warp + j;
@@ -766,7 +772,7 @@ __global__ void __launch_bounds__(kAllThreads, ctas_per_sm(DH, RN)) quant_attn_k
             }
         }
         sync();  // C: sums and halves written; V is consumed
-        if (tid == 0)
+        if (tid == 0 && have_v)
             mbar_arrive(bar(kEmptyV));
         if constexpr (HALVES) {
             const int keep = warp / 4;
@@ -866,8 +872,12 @@ __global__ void __launch_bounds__(kAllThreads, ctas_per_sm(DH, RN)) quant_attn_k
         St st;
         const bool masked = c.lc * kChunk + kChunk > c.seen + 1;
         const int bad = masked ? chunk_state(std::true_type{}, step, st) : chunk_state(std::false_type{}, step, st);
-        if (bad < 0)
-            return;  // a wait ran out of time (the copying warp lets its copies land)
+        if (bad < 0) {
+            // a wait ran out of time (the copying warp lets its copies land)
+            if (tid == 0)
+                record_error(p.err, kErrTimeout, ((long long)blockIdx.x << 8) | 0xFF);
+            return;
+        }
 #pragma unroll
         for (int r = 0; r < NR; ++r) {
             if (bad > 0)
@@ -1185,6 +1195,7 @@ cudaError_t launch_quant_attention(const QuantAttnArgs &a, ErrState *err, cudaSt
     p.out = static_cast<__nv_bfloat16 *>(a.out);
     p.lse = a.lse;
     p.err = err;
+    p.wait_ns = fold_wait_limit_ns();
     p.max_pages = a.max_pages > 0 ? a.max_pages : INT64_MAX;
     const int64_t max_chunks =
         qa::max_chunks_of(a.num_seqs, tiles, p.hkv, a.pool.head_dim, p.max_seq_len, a.max_pages);

@@ -157,9 +157,9 @@ def init() -> None:
 
 
 def set_fold_wait_limit_ns(limit_ns: int) -> int:
-    """Time limit of the split-KV fold's cross-CTA wait (default 2 s); returns
-    the previous limit.  0 makes the waiting CTAs give up at once (a test of
-    the timeout path)."""
+    """Time limit of the split-KV fold's cross-CTA wait and of the direct 4-bit
+    attention's waits for pages (default 2 s); returns the previous limit.  0
+    makes the waiting CTAs give up at once (a test of the timeout path)."""
     return int(load().pa_set_fold_wait_limit_ns(int(limit_ns)))
 
 
