@@ -537,6 +537,9 @@ PA_API size_t pa_paged_attention_quant_workspace_size(int32_t num_seqs, int32_t 
  *     and calls with different bounds may share it one after another.
  *   - out, lse and the workspace may not share bytes with an input or with one
  *     another (PA_ERR_INVALID_ARG).
+ *   - When the direct kernels latch PA_ERR_TIMEOUT, the rows of the requests
+ *     that a wait ran out for are NaN or, where one step takes all of a
+ *     request's keys, may be left as they were.
  * num_seqs <= 2048, and num_seqs times the pages of max_seq_len at most 2^28.
  */
 PA_API pa_status pa_paged_attention_quant(const void *q, int64_t num_q_tokens, int64_t q_tok_stride,

@@ -147,6 +147,12 @@ __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1,
                  : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
+// Arrives at a named barrier without waiting.
+__device__ __forceinline__ void bar_arrive(int id, int nthreads)
+{
+    asm volatile("bar.arrive %0, %1;" ::"r"(id), "r"(nthreads) : "memory");
+}
+
 // 8x8 transpose of 16-bit elements across the warp.
 __device__ __forceinline__ uint32_t movmatrix(uint32_t x)
 {
@@ -485,6 +491,22 @@ __global__ void __launch_bounds__(kAllThreads, ctas_per_sm(DH, RN)) quant_attn_k
         // for when the one before it had been consumed).
         wait_bar_drain(bar(kFullK), (landing[0] - 1) & 1);
         wait_bar_drain(bar(kFullV), (landing[1] - 1) & 1);
+        // When the computing warps are done: if a wait ran out of time, the sums
+        // of this CTA's records are NaN, which makes their rows NaN.  (Groups of
+        // one chunk have none; those not begun stay unwritten.)
+        named_sync(2, kAllThreads);
+        if (!s_flags[0])
+            return;
+        if (lane == 0)
+            record_error(p.err, kErrTimeout, ((long long)blockIdx.x << 8) | 0xFF);
+        static_assert(RN <= 32, "a lane per row");
+#pragma unroll 1
+        for (int k = 0; k < chunks; ++k)
+            if (lane < p.rows) {
+                float *const rec = p.records + (lo + k) * (int64_t)part_record_floats(p.rows, DH) + lane;
+                __stcg(rec, 0.f);
+                __stcg(rec + p.rows, __int_as_float(0x7FC00000));
+            }
         return;
     }
     auto sync = [&]() { named_sync(1, kThreads); };  // the computing warps
@@ -872,15 +894,9 @@ __global__ void __launch_bounds__(kAllThreads, ctas_per_sm(DH, RN)) quant_attn_k
         St st;
         const bool masked = c.lc * kChunk + kChunk > c.seen + 1;
         const int bad = masked ? chunk_state(std::true_type{}, step, st) : chunk_state(std::false_type{}, step, st);
-        if (bad < 0) {
-            // a wait ran out of time (the copying warp lets its copies land)
-            if (tid == 0)
-                record_error(p.err, kErrTimeout, ((long long)blockIdx.x << 8) | 0xFF);
-            return;
-        }
 #pragma unroll
         for (int r = 0; r < NR; ++r) {
-            if (bad > 0)
+            if (bad != 0)
                 st.l[r] = __int_as_float(0x7FC00000);
             if (st.l[r] != st.l[r] && st.m[r] == -INFINITY)
                 st.m[r] = 0.f;  // a NaN state must not pass for an empty one
@@ -890,14 +906,20 @@ __global__ void __launch_bounds__(kAllThreads, ctas_per_sm(DH, RN)) quant_attn_k
         if (c.nch > 1) {
             write_record(p.records + (lo + step) * (int64_t)rec_size, st, rv);
         } else {
+            // (any thread that gave up on this chunk did before its last barrier)
+            const bool gone = s_flags[0];
 #pragma unroll
             for (int r = 0; r < NR; ++r)
                 if (state_row(r) < rv)
 #pragma unroll
                     for (int i = 0; i < NP; ++i)
-                        output_pair(state_row(r), state_pair(i), st.o[i][r], st.m[r], st.l[r]);
+                        output_pair(state_row(r), state_pair(i), st.o[i][r], st.m[r],
+                                    gone ? __int_as_float(0x7FC00000) : st.l[r]);
         }
+        if (bad < 0)
+            break;  // a wait ran out of time
     }
+    bar_arrive(2, kAllThreads);
 }
 
 // Folds the chunk records of the groups with several chunks.  Bound by round

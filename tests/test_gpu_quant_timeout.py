@@ -41,3 +41,25 @@ def test_waits_that_run_out_are_reported_and_the_next_call_is_right(lens, new, h
         o, l = c.run(workspace=ws)
         assert pa.check_errors() == (pa.PA_OK, -1)
         assert _same(o, out) and _same(l, lse)
+
+
+@pytest.mark.parametrize("lens,new,hq,hkv,dh", CASES)
+def test_no_row_of_waits_that_ran_out_passes_for_a_result(lens, new, hq, hkv, dh):
+    """Requests of several chunks: NaN.  Of one chunk: NaN or not written.  Rows
+    that no request owns stay as they are."""
+    c = Case(lens, new, hq, hkv, dh, seed=dh + len(lens))
+    rows = c.q.shape[0]
+    q = torch.cat([c.q, c.q[:1]])
+    o = torch.full(q.shape, 7.0, dtype=torch.bfloat16, device="cuda")
+    l = torch.full((rows + 1, hq), 7.0, device="cuda")
+    # records left by an earlier call, which would pass for results
+    ws = torch.zeros(pa.quant_workspace_size(len(lens), hq, hkv, dh, new, max(lens)), dtype=torch.uint8, device="cuda")
+    c.run(workspace=ws)
+    _timed_out(c, q=q, out=o, lse=l, workspace=ws)
+    chunk = {128: 512, 256: 256, 512: 128}[dh]
+    for x in (o, l):
+        assert bool((x[:rows].isnan() | (x[:rows] == 7)).all()) and bool((x[rows:] == 7).all())
+        assert len(lens) == 1 or bool(x[:rows].isnan().any())
+        for b, n in enumerate(lens):
+            if n > chunk:
+                assert bool(x[b * new:(b + 1) * new].isnan().all()), (b, n)
