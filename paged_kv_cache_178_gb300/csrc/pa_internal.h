@@ -152,7 +152,8 @@ cudaError_t launch_quant_write(const void *key, int64_t key_stride, const void *
                                int64_t num_tokens, const QuantPool &pool, const int64_t *slot_mapping, ErrState *err,
                                cudaStream_t stream, int num_sms, int64_t *grid);
 // compact_tables has out_cols columns (columns past them are not written).
-// With poison_tables a total above the capacity fills compact_tables with -1.
+// With poison_tables a total above the capacity fills compact_tables with -1,
+// and the first entry of a request with a bad block id is -1.
 // zero_bytes bytes at `zero` (16-byte aligned, may be 0) are cleared.
 cudaError_t launch_dequantize_kv(const QuantPool &pool, const int32_t *block_tables, int32_t max_blocks,
                                  const int32_t *seq_lens, int32_t num_seqs, void *k_out, void *v_out,

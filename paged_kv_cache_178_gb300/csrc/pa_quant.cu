@@ -309,10 +309,26 @@ __global__ void __launch_bounds__(kQuantThreads) dequantize_kv_kernel(
     const int64_t n_tab = (int64_t)num_seqs * out_cols;
     for (int64_t e = gtid; e < n_tab; e += gsize) {
         const int b = (int)div_floor(e, out_cols), p = (int)(e - (int64_t)b * out_cols);
-        compact_tables[e] = !over && p < s_off[b + 1] - s_off[b] ? s_off[b] + p : -1;
+        if (!poison_tables || over || p > 0)
+            compact_tables[e] = !over && p < s_off[b + 1] - s_off[b] ? s_off[b] + p : -1;
     }
     if (over)
         return;
+    if (poison_tables)
+        // The first entry of each request: -1 if any of its block ids is bad.
+        // Every row sees that page, so all of the request's rows become NaN,
+        // whether they see the bad one or not.
+        for (int b = blockIdx.x; b < num_seqs; b += gridDim.x) {
+            const int n = s_off[b + 1] - s_off[b];
+            bool bad = n == 0;
+            for (int p = tid; p < n; p += kQuantThreads) {
+                const int id = __ldg(block_tables + (int64_t)b * max_blocks + p);
+                bad |= id < 0 || (int64_t)id >= pool.num_blocks;
+            }
+            bad = __syncthreads_or(bad);
+            if (tid == 0)
+                compact_tables[(int64_t)b * out_cols] = bad ? -1 : s_off[b];
+        }
     constexpr int VEC = DH / 8;  // 16-byte vectors of an output row
     const int hk = pool.num_kv_heads;
     const uint4 qnan = make_uint4(0x7FC07FC0u, 0x7FC07FC0u, 0x7FC07FC0u, 0x7FC07FC0u);
