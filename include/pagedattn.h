@@ -527,7 +527,13 @@ PA_API size_t pa_paged_attention_quant_workspace_size(int32_t num_seqs, int32_t 
  *   - More tokens otherwise: the selected pages are read back into the
  *     workspace (as by pa_dequantize_kv), and pa_paged_attention's kernel runs
  *     over them: bitwise its results on the read-back pool.
- *   The two ways round differently.
+ *   The two ways round differently: the direct kernels take q (times a power
+ *   of two per row) and the probabilities in f16, the BF16 attention takes the
+ *   probabilities in BF16.  Sums, maxima and lse are fp32 in both.  The direct
+ *   kernels hold for scores (scale * q.k) up to fp32's range, the BF16 attention
+ *   for scores below 2^30.
+ *   - Hq/Hkv above 32 (16 at head dim 512): no row tile holds a token's heads,
+ *     so every call, decode steps too, goes by way of the read-back.
  *   - More than max_pages (> 0) selected pages: PA_ERR_WORKSPACE is latched
  *     (index = the pages) and all rows are NaN.
  *   - A bad block id makes all rows of its request NaN.  Keys past a

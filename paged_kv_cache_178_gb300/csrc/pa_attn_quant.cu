@@ -16,7 +16,8 @@
 // scales are exact in f16; q is scaled per row by a power of two to [1, 2) at
 // its largest element (what is below 2^-14 of it loses bits, at most 2^-25 of
 // the largest); p is scaled by 2^15 (11 bits down to 2^-29 of the row's largest
-// probability).
+// probability).  Both are the matrix instruction's operand type; p's rounding
+// adds less than 1% to the error that the rounding of the result leaves.
 //   S^T = K.Q^T: M = the 16 tokens of a page, N = 8 query rows, K = head dim.
 //   O^T = V^T.P^T: M = the head dim, N = 8 query rows, K = the 16 tokens.  A V
 //     byte holds two neighbouring elements of one token; permutes regroup the
@@ -44,12 +45,15 @@
 // records.  (Folded by the last CTA to arrive instead, 32 records of eight rows
 // took that CTA 5 us, 17 of twenty rows at head dim 256 13 us.)
 //
-// Measured, head dim 128 unless said: 64 requests of 7168, 7168, 4171 and 513
-// keys with 8 query and 2 KV heads (88 MB) 29.5 us, of which the metadata and
-// the shares take 2, the first chunk 7, three more 4.2 each (5.3 TB/s, two CTAs
-// per SM), uneven ends 4 and the fold 3; four of them 8.2 us; 131072 keys and 32
-// query and 4 KV heads 29.6 us; 16 requests of up to 5000 keys with five new
-// tokens at head dim 256 24.1 us, 4.8 a chunk of 256 keys.
+// Measured in a CUDA graph (as all times in this file; issued one by one they
+// are 0.4 to 0.9 us longer), head dim 128 unless said: 64 requests of 7168,
+// 7168, 4171 and 513 keys with 8 query and 2 KV heads (88 MB) 29.8 us, of which
+// the metadata and the shares take 2, the first chunk 7, three more 4.2 each
+// (5.3 TB/s, two CTAs per SM), uneven ends 4 and the fold 3; four of them 8.6
+// us; 131072 keys and 32 query and 4 KV heads 29.9 us; 16 requests of up to 5000
+// keys with five new tokens at head dim 256 24.3 us, 4.8 a chunk of 256 keys,
+// bound by latency: one CTA per SM goes from product to exchange to product (a
+// quarter of the issue slots, 18% of the tensor pipe, 13% of the DRAM's rate).
 #include <cstdio>
 #include <type_traits>
 
@@ -78,7 +82,10 @@ constexpr int kSpan = 16;           // chunks per span of the fold
 // 64 requests 31.5 us at 8, 30.5 at 18, 32.4 at 32.
 constexpr int kChunkCost = 18;
 // A tile's weight is at most 1 + kChunkCost / 8 times its pages, and kChunkCost:
-// sums stay below 2^31 for two tiles of requests of 2^28 pages.
+// sums stay below 2^31 for two tiles of requests of 2^28 pages.  (More tiles to
+// a request: each chunk of a tile has a record of nine rows or more, so the
+// sums pass 2^31 only where the records pass the memory of a GPU, or the pages
+// max_pages, and then differences alone are used.)
 static_assert(2.0 * (1 << 28) * (1 + kChunkCost / 8.0) + kQuantMaxTiles * kChunkCost < 2147483648.0, "weights");
 constexpr float kShift = 15.f;      // p is scaled by 2^kShift (largest f16: 2^16)
 constexpr int kGridSms = 152;       // SMs the grid is sized for

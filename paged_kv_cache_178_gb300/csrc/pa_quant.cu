@@ -115,9 +115,11 @@ __device__ __forceinline__ Quantised quantise16(const uint4 &lo, const uint4 &hi
 // loads its next item before it works on one.  The index arithmetic is 32 bits
 // wide while the items allow; in 64 bits it took as long as the rest.
 //
-// Bound by instruction issue (62% of the slots, 240 instructions per 16
-// elements of K or V): 16384 tokens of 8 KV heads take 25 us at head dim 128,
-// where moving their 86 MB takes 13.
+// 16384 tokens of 8 KV heads take 24 us at head dim 128, alone and with cold
+// caches, where moving their 86 MB takes 13.  62% of the issue slots are taken
+// (240 instructions per 16 elements of K or V) by 56% of the warps that an SM
+// holds: neither alone bounds it, the instructions and what little is in flight
+// (one item ahead) do together.
 template <int DH, typename Index>
 __global__ void __launch_bounds__(kQuantThreads) quant_write_kernel(
     const uint4 *__restrict__ key, int64_t key_stride, const uint4 *__restrict__ value, int64_t value_stride,

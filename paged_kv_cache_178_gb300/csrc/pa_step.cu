@@ -18,9 +18,10 @@ namespace pa {
 // Where lengths or cursor advance in place, nothing may be written before
 // every CTA has read them: the grid is then one cluster with a barrier of its
 // own in between (up to eight CTAs); otherwise it takes as many CTAs as there
-// is work.  64 decoding requests take 2.5 us, 240 requests with 62 thousand
-// tokens 4.1 us (with the sums one after the other and a token a thread, 5.2
-// and 12).
+// is work.  In a CUDA graph 64 decoding requests take 2.6 us, 240 requests with
+// 62 thousand tokens 4.2 us (with the sums one after the other and a token a
+// thread, 5.2 and 12); issued one by one 2.8 and 4.4, of which the host's part
+// is most.
 constexpr int kMetaThreads = 256;
 constexpr int kMetaClusterMax = 8;  // the portable cluster size
 constexpr int kMetaUnroll = 4;
@@ -199,11 +200,14 @@ __device__ __forceinline__ float sum_squares(const float (&a)[8], const float (&
 // neighbouring rows of q, of k or of v, a row to a group, so that loads and
 // stores are contiguous.  The angles stay in registers, the weights (offset
 // added) in shared memory, the rows' addresses advance by one addition, and
-// kRopeBatch steps are loaded before the first is computed.  What bounds it
-// after the memory is the instruction count: a step of 1 KB takes about 130.
-// 16384 tokens of 32 query and 8 KV heads at head dim 128, with the cache
-// write (411 MB): 69 us, 6.0 TB/s; 4099 tokens of 16 and 2 heads of 256
-// elements, 64 of them rotated (77 MB): 16.4 us, 4.7 TB/s; 64 tokens 2.5 us.
+// kRopeBatch steps are loaded before the first is computed.  A step of 1 KB
+// takes about 130 instructions.  Times in a CUDA graph: 16384 tokens of 32
+// query and 8 KV heads at head dim 128, with the cache write (411 MB): 69 us,
+// 6.0 TB/s, bound by the memory; 4099 tokens of 16 and 2 heads of 256 elements,
+// 64 of them rotated (77 MB): 16.4 us, 4.7 TB/s, bound by latency (half of the
+// issue slots and 28% of the DRAM's rate: less than one wave of CTAs, two steps
+// in flight, the position and then its angles before the first store); 64 tokens
+// 2.6 us.
 // Loads and stores are marked as streaming (neither: 70.5 and 17.4 us; the
 // loads alone 71.8 and 17.6): every row passes once.  The
 // first case took 88 us with 16-byte vectors that were not neighbours in a

@@ -67,3 +67,23 @@ def test_many_keys_give_the_best_one(lens, new, hq, hkv, dh, std, k_scale):
     best, sure = _winners(c)
     assert sure.any() and np.array_equal(_f64(out)[sure], best[sure])
     c.check(out, lse)
+
+
+@pytest.mark.parametrize("std,k_scale", [(1e7, 1.0), (1e8, 1.0)])
+@pytest.mark.parametrize("lens,new,hq,hkv,dh", [([300, 77] * 4, 77, 8, 2, 128), ([200] * 16, 20, 16, 2, 256),
+                                                ([150, 64] * 2, 50, 16, 2, 512), ([1, 40, 3], 1, 128, 1, 128)])
+def test_the_read_back_gives_the_best_key_too(lens, new, hq, hkv, dh, std, k_scale):
+    """P and the result are rounded to BF16 there, half a step (2^-8) each; the
+    sums have 2^-14 to spare.  For scores below 2^30: the exponent of the largest
+    p is off by half a unit in the last place of the score in log2 units, up to
+    64 below 2^31 and 128, where p leaves fp32, from there on."""
+    c = Case(lens, new, hq, hkv, dh, seed=dh + new, std=std, k_scale=k_scale)
+    out, lse = c.run()
+    assert "read-back" in pa.last_launch_info()
+    assert pa.check_errors() == (pa.PA_OK, -1)
+    assert bool(out.isfinite().all()) and bool(lse.isfinite().all())
+    assert float(lse.abs().max()) < 2.0 ** 30
+    best, sure = _winners(c)
+    assert sure.any()
+    err = np.abs(_f64(out) - best)[sure]
+    assert (err <= (2.0 ** -7 + 2.0 ** -14) * np.abs(best[sure])).all(), float(err.max())
