@@ -557,6 +557,145 @@ PA_API pa_status pa_paged_attention_quant(const void *q, int64_t num_q_tokens, i
                                           pa_stream_t stream);
 
 /*
+ * Pages between requests.  The paper (the source pages) has no counterpart to
+ * the calls from here to pa_compact_pages.  They keep the owners of pages in
+ * an array shares [num_blocks] int32: shares[p] counts the owners of page p
+ * beyond its first, so that it is 0 for a free page and for a page of one
+ * request, and pa_build_step_metadata needs to know nothing of it.
+ * free_pages is a stack whose entries from the cursor on are free: that call
+ * and forks take from the cursor upwards, releases put back below it.
+ *   In place: seq_lens may be context_lens, shares_out shares_in, cursor_out
+ * cursor_in and tables_out block_tables (the same pointer: all inputs are read
+ * before anything is written, or by the thread that writes), so a captured
+ * graph advances its own state.  No other output may share bytes with an input
+ * or another output (PA_ERR_INVALID_ARG).  With shares_out != shares_in all of
+ * shares_out is written.
+ *   num_seqs <= 8192, num_forks <= 8192, num_seqs * max_blocks_per_seq <=
+ * INT32_MAX (PA_ERR_UNSUPPORTED above).
+ */
+
+/*
+ * Copies pages within the pools of num_caches layers: for every pair i with
+ * src_pages[i] >= 0, page dst_pages[i] of K and of V of each cache becomes
+ * page src_pages[i] (all 16 tokens, all heads).  Pairs with a negative source,
+ * or with the source as destination, are skipped: lists may be padded.
+ *   caches      : host array; sizes and strides of all caches are the same
+ *                 (PA_ERR_INVALID_ARG otherwise).  num_caches <= 128.
+ *   src_pages, dst_pages : [num_pairs] int32 on the device, outside the pools.
+ * A page outside [0, num_blocks) copies nothing and latches
+ * PA_ERR_BAD_METADATA (index = the pair).  The pairs of a call are copied in no
+ * order: its destinations have to differ from one another and from its sources.
+ * num_pairs == 0 or num_caches == 0 launches nothing.
+ */
+PA_API pa_status pa_copy_pages(const pa_kv_cache *caches, int32_t num_caches, const int32_t *src_pages,
+                               const int32_t *dst_pages, int64_t num_pairs, pa_stream_t stream);
+
+/* pa_copy_pages within 4-bit pools: whole records, codes and scales.  (The
+ * caches' k_scale and v_scale may differ: each page stays in its pool.) */
+PA_API pa_status pa_copy_pages_quant(const pa_quant_cache *caches, int32_t num_caches, const int32_t *src_pages,
+                                     const int32_t *dst_pages, int64_t num_pairs, pa_stream_t stream);
+
+/*
+ * Forks requests: fork i gives the empty request c = children[i] the first
+ * l = fork_lens[i] tokens of request p = parents[i] (all of them where
+ * fork_lens is NULL).
+ *   block_tables[c][j] = block_tables[p][j] and one owner more for that page,
+ *                        for the l/16 whole pages;
+ *   where l % 16 != 0, block_tables[c][l/16] = the next free page, and
+ *   copy_src[i], copy_dst[i] = the parent's page and the new one: a list for
+ *                        pa_copy_pages, once for every pool.  Otherwise both -1.
+ *   seq_lens[c] = l; seq_lens[b] = context_lens[b] for all others.
+ *   *cursor_out = *cursor_in + the new pages, which go to the forks in order.
+ * So a page that tokens are yet to be written to has one owner.
+ *   parents, children, fork_lens, copy_src, copy_dst : [num_forks] int32.
+ *   context_lens, seq_lens : [num_seqs] int32.  block_tables: [num_seqs,
+ *                        max_blocks_per_seq]; other entries are left alone.
+ * Errors latched on the device:
+ *   - a parent or child outside [0, num_seqs), a child that is not empty or
+ *     that an earlier fork of the call names too, l outside [0,
+ *     context_lens[p]], a context past its table row: the fork does nothing;
+ *     PA_ERR_BAD_METADATA, index = the fork;
+ *   - a page outside [0, num_blocks): its entry is copied (or the free page
+ *     taken) all the same, but no owner is counted and no copy listed;
+ *     PA_ERR_BAD_METADATA, index = the fork;
+ *   - more new pages than free ones (PA_ERR_WORKSPACE, index = the pages
+ *     needed), a cursor outside [0, num_free_pages] or more than INT32_MAX
+ *     pages (PA_ERR_BAD_METADATA, index = num_forks): no fork does anything.
+ * num_seqs == 0 launches nothing.
+ */
+PA_API pa_status pa_fork_requests(const int32_t *parents, const int32_t *children, const int32_t *fork_lens,
+                                  int32_t num_forks, const int32_t *context_lens, int32_t num_seqs,
+                                  int32_t *block_tables, int32_t max_blocks_per_seq, const int32_t *shares_in,
+                                  int32_t *shares_out, int64_t num_blocks, const int32_t *free_pages,
+                                  int32_t num_free_pages, const int32_t *cursor_in, int32_t *cursor_out,
+                                  int32_t *seq_lens, int32_t *copy_src, int32_t *copy_dst, pa_stream_t stream);
+
+/*
+ * Releases pages: request b keeps its first keep_lens[b] tokens (0: it has
+ * ended; negative: it stays as it is) and gives up the pages past them, in
+ * columns ceil(keep/16) .. ceil(context/16)-1 of its table row.  Each loses an
+ * owner; one that has none left goes onto the free stack:
+ *   free_pages[*cursor_in - n + k] = the k-th of the n freed pages, in the
+ *     order (request, column) of the reference that was its last;
+ *   *cursor_out = *cursor_in - n;  seq_lens[b] = keep_lens[b] (or
+ *     context_lens[b]).
+ * The table is left as it is.  Several requests of a call may own a page.
+ * Errors latched on the device:
+ *   - context_lens[b] outside [0, max_blocks_per_seq*16], or keep_lens[b] >
+ *     context_lens[b]: the request stays as it is; PA_ERR_BAD_METADATA, index
+ *     = the request;
+ *   - tokens that stay end inside a page which other requests own too (at the
+ *     call's start): the next token would be written into it; the same (fork
+ *     the request instead);
+ *   - a page outside [0, num_blocks) is passed over, a page given up more often
+ *     than it had owners is freed once; the same;
+ *   - more freed pages than *cursor_in (PA_ERR_WORKSPACE, index = the pages), a
+ *     cursor outside [0, num_free_pages] or more than 2^30 given up pages
+ *     (PA_ERR_BAD_METADATA, index = num_seqs): nothing is released.
+ * num_seqs == 0 launches nothing.
+ */
+PA_API pa_status pa_release_pages(const int32_t *context_lens, const int32_t *keep_lens, int32_t num_seqs,
+                                  const int32_t *block_tables, int32_t max_blocks_per_seq, const int32_t *shares_in,
+                                  int32_t *shares_out, int64_t num_blocks, int32_t *free_pages,
+                                  int32_t num_free_pages, const int32_t *cursor_in, int32_t *cursor_out,
+                                  int32_t *seq_lens, pa_stream_t stream);
+
+/* Bytes of scratch for pa_compact_pages (any contents); 0 for invalid sizes. */
+PA_API size_t pa_compact_pages_workspace_size(int64_t num_blocks);
+
+/*
+ * Plans the compaction of a pool: with n pages in use by the requests' tables
+ * (context_lens[b] tokens each), the k-th page in use from page n on moves to
+ * the k-th unused page below n, so that pages 0 .. n-1 are in use afterwards.
+ *   copy_src[k], copy_dst[k] = the k-th move, ascending; -1 from the number of
+ *                   moves up to max_moves: a list for pa_copy_pages;
+ *   tables_out[b][j] = the new place of block_tables[b][j], for the columns in
+ *                   use (others are left alone);
+ *   shares_out      = shares_in moved along, 0 from page n on;
+ *   free_pages[num_free_pages - num_blocks + p] = p for n <= p < num_blocks,
+ *   *cursor_out     = num_free_pages - num_blocks + n;
+ *   counts[0], counts[1] = n and the number of moves.
+ * Pages that only the free list holds are unused; a page held elsewhere has to
+ * be in some table.  num_free_pages >= num_blocks (PA_ERR_INVALID_ARG);
+ * num_blocks <= 2^20 (PA_ERR_UNSUPPORTED).
+ *   workspace : pa_compact_pages_workspace_size(num_blocks) bytes, 256-byte
+ *               aligned, any contents.
+ * Errors latched on the device:
+ *   - context_lens[b] outside [0, max_blocks_per_seq*16]: none of the row's
+ *     pages count, its entries are not written; a page outside [0, num_blocks)
+ *     keeps its entry; PA_ERR_BAD_METADATA, index = the request;
+ *   - more than max_moves moves: nothing moves (tables_out and shares_out are
+ *     the inputs, *cursor_out is *cursor_in, free_pages stays, the lists are
+ *     -1); PA_ERR_WORKSPACE, index = the moves.
+ */
+PA_API pa_status pa_compact_pages(const int32_t *context_lens, int32_t num_seqs, const int32_t *block_tables,
+                                  int32_t *tables_out, int32_t max_blocks_per_seq, const int32_t *shares_in,
+                                  int32_t *shares_out, int64_t num_blocks, int32_t *free_pages,
+                                  int32_t num_free_pages, const int32_t *cursor_in, int32_t *cursor_out,
+                                  int32_t *copy_src, int32_t *copy_dst, int32_t max_moves, int32_t *counts,
+                                  void *workspace, size_t workspace_bytes, pa_stream_t stream);
+
+/*
  * Synchronises `stream`, then reads and clears the current device's error
  * flag.  Returns PA_OK, PA_ERR_BAD_METADATA or PA_ERR_TIMEOUT (or
  * PA_ERR_CUDA if the synchronisation failed).  *first_bad_index (may be

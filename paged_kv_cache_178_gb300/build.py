@@ -17,7 +17,7 @@ CSRC = os.path.join(HERE, "csrc")
 BUILD_DIR = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libpagedattn.so")
 SOURCES = ["pa_api.cu", "pa_attn.cu", "pa_attn512.cu", "pa_decode.cu", "pa_gather.cu",
-           "pa_step.cu", "pa_quant.cu", "pa_attn_quant.cu"]
+           "pa_step.cu", "pa_quant.cu", "pa_attn_quant.cu", "pa_pages.cu"]
 HEADERS = ["pa_internal.h", "pa_ptx.cuh", "pa_attn_common.cuh", "pa_split.cuh", "pa_scan.cuh",
            "pa_quant_common.cuh", os.path.join("..", "..", "include", "pagedattn.h")]
 

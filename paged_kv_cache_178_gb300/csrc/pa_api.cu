@@ -40,7 +40,8 @@ static pa_status device_setup(ErrState **err_out, int *num_sms = nullptr)
         if (cudaGetSymbolAddress(&ptr, g_err_state) != cudaSuccess)
             return PA_ERR_CUDA;
         if (init_attention_attributes() != cudaSuccess || init_step_attributes() != cudaSuccess ||
-            init_quant_attributes() != cudaSuccess || init_quant_attention_attributes() != cudaSuccess)
+            init_quant_attributes() != cudaSuccess || init_quant_attention_attributes() != cudaSuccess ||
+            init_page_attributes() != cudaSuccess)
             return PA_ERR_CUDA;
         if (cudaDeviceGetAttribute(&g_num_sms[dev], cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
             return PA_ERR_CUDA;
@@ -1229,6 +1230,298 @@ pa_status pa_paged_attention_quant(const void *q, int64_t num_q_tokens, int64_t 
     st = attention_launch(a, pl.attn, err, s, info, sizeof info);
     snprintf(g_last_info, sizeof g_last_info, "quant attention read-back grid=%lld; %.180s", (long long)grid, info);
     return st;
+}
+
+// ------------------------------------------------------------ page copies --
+// pa_copy_pages and pa_copy_pages_quant after the checks of the caches:
+// geometry of a view's page in 16-byte units, first cache's strides for all.
+static pa_status copy_call(CopyArgs &a, const int32_t *src_pages, const int32_t *dst_pages, int64_t num_pairs,
+                           const Span *views, const char *name, pa_stream_t stream)
+{
+    if (num_pairs < 0 || num_pairs > INT32_MAX)
+        return PA_ERR_INVALID_ARG;
+    if (num_pairs == 0 || a.num_caches == 0) {
+        snprintf(g_last_info, sizeof g_last_info, "%s pairs=0 (nothing launched)", name);
+        return PA_OK;
+    }
+    if (!src_pages || !dst_pages || !aligned4(src_pages) || !aligned4(dst_pages))
+        return PA_ERR_INVALID_ARG;
+    for (int i = 0; i < 2 * a.num_caches; ++i)
+        if (overlaps(views[i], span(src_pages, num_pairs * 4)) || overlaps(views[i], span(dst_pages, num_pairs * 4)))
+            return PA_ERR_INVALID_ARG;
+    a.num_pairs = (int32_t)num_pairs;
+    a.src = src_pages;
+    a.dst = dst_pages;
+    ErrState *err = nullptr;
+    int nsm = 0;
+    const pa_status st = device_setup(&err, &nsm);
+    if (st != PA_OK)
+        return st;
+    int64_t grid = 0;
+    const cudaError_t e = launch_copy_pages(a, err, reinterpret_cast<cudaStream_t>(stream), nsm, &grid);
+    snprintf(g_last_info, sizeof g_last_info, "%s caches=%d pairs=%lld grid=%lld", name, a.num_caches,
+             (long long)num_pairs, (long long)grid);
+    return cuda_status(e);
+}
+
+pa_status pa_copy_pages(const pa_kv_cache *caches, int32_t num_caches, const int32_t *src_pages,
+                        const int32_t *dst_pages, int64_t num_pairs, pa_stream_t stream)
+{
+    if (num_caches < 0 || (num_caches > 0 && !caches))
+        return PA_ERR_INVALID_ARG;
+    if (num_caches > kCopyMaxCachesHost)
+        return PA_ERR_UNSUPPORTED;
+    CopyArgs a{};
+    a.num_caches = num_caches;
+    Span views[2 * kCopyMaxCachesHost];
+    for (int i = 0; i < num_caches; ++i) {
+        const pa_kv_cache &c = caches[i], &f = caches[0];
+        const pa_status st = check_cache(&c);
+        if (st != PA_OK)
+            return st;
+        if (c.num_blocks != f.num_blocks || c.num_kv_heads != f.num_kv_heads || c.head_dim != f.head_dim ||
+            c.block_stride != f.block_stride || c.token_stride != f.token_stride || c.head_stride != f.head_stride)
+            return PA_ERR_INVALID_ARG;
+        a.k[i] = static_cast<uint4 *>(c.k);
+        a.v[i] = static_cast<uint4 *>(c.v);
+        views[2 * i] = span(c.k, pool_view_bytes(&c));
+        views[2 * i + 1] = span(c.v, pool_view_bytes(&c));
+    }
+    if (num_caches > 0) {
+        const pa_kv_cache &f = caches[0];
+        const int64_t dh = f.head_dim, hkv = f.num_kv_heads;
+        if (2 * hkv * dh > INT32_MAX / 4)
+            return PA_ERR_UNSUPPORTED;
+        a.num_blocks = f.num_blocks;
+        a.block_stride = f.block_stride / 8;
+        a.page_vecs = (int32_t)(2 * hkv * dh);
+        // the longest runs of neighbouring bytes; one head has no head stride
+        if (hkv == 1 ? f.token_stride == dh : f.head_stride == dh && f.token_stride == hkv * dh) {
+            a.run_vecs = a.page_vecs;
+        } else if (f.token_stride == dh) {
+            a.run_vecs = f.head_stride == 16 * dh ? a.page_vecs : (int32_t)(2 * dh);
+            a.c1 = (int32_t)hkv;
+            a.s1 = f.head_stride / 8;
+        } else if (hkv == 1 || f.head_stride == dh) {
+            a.run_vecs = (int32_t)(hkv * dh / 8);
+            a.c1 = 16;
+            a.s1 = f.token_stride / 8;
+        } else {
+            a.run_vecs = (int32_t)(dh / 8);
+            a.c1 = (int32_t)hkv;
+            a.s1 = f.head_stride / 8;
+            a.s0 = f.token_stride / 8;
+        }
+    }
+    return copy_call(a, src_pages, dst_pages, num_pairs, views, "copy_pages", stream);
+}
+
+pa_status pa_copy_pages_quant(const pa_quant_cache *caches, int32_t num_caches, const int32_t *src_pages,
+                              const int32_t *dst_pages, int64_t num_pairs, pa_stream_t stream)
+{
+    if (num_caches < 0 || (num_caches > 0 && !caches))
+        return PA_ERR_INVALID_ARG;
+    if (num_caches > kCopyMaxCachesHost)
+        return PA_ERR_UNSUPPORTED;
+    CopyArgs a{};
+    a.num_caches = num_caches;
+    Span views[2 * kCopyMaxCachesHost];
+    for (int i = 0; i < num_caches; ++i) {
+        const pa_quant_cache &c = caches[i], &f = caches[0];
+        const pa_status st = check_quant_cache(&c);
+        if (st != PA_OK)
+            return st;
+        if (c.num_blocks != f.num_blocks || c.num_kv_heads != f.num_kv_heads || c.head_dim != f.head_dim ||
+            c.block_stride != f.block_stride || c.head_stride != f.head_stride)
+            return PA_ERR_INVALID_ARG;
+        a.k[i] = static_cast<uint4 *>(c.k);
+        a.v[i] = static_cast<uint4 *>(c.v);
+        views[2 * i] = span(c.k, quant_view_bytes(&c));
+        views[2 * i + 1] = span(c.v, quant_view_bytes(&c));
+    }
+    if (num_caches > 0) {
+        const pa_quant_cache &f = caches[0];
+        const int64_t record = 9 * (int64_t)f.head_dim / 16, hkv = f.num_kv_heads;
+        if (record * hkv > INT32_MAX / 4)
+            return PA_ERR_UNSUPPORTED;
+        a.num_blocks = f.num_blocks;
+        a.block_stride = f.block_stride / 16;
+        a.page_vecs = (int32_t)(record * hkv);
+        a.run_vecs = hkv == 1 || f.head_stride == record * 16 ? a.page_vecs : (int32_t)record;
+        a.c1 = (int32_t)hkv;
+        a.s1 = f.head_stride / 16;
+    }
+    return copy_call(a, src_pages, dst_pages, num_pairs, views, "copy_pages_quant", stream);
+}
+
+// ------------------------------------------------- fork, release, compact --
+// Whether a write shares bytes with a read or another write.  same[i] >= 0:
+// write i may be read same[i] itself (in place), bytes 0 on.
+static bool any_overlap(const Span *writes, const int *same, int nw, const Span *reads, int nr)
+{
+    for (int i = 0; i < nw; ++i) {
+        for (int j = 0; j < nr; ++j)
+            if (!(same[i] == j && writes[i].lo == reads[j].lo) && overlaps(writes[i], reads[j]))
+                return true;
+        for (int j = i + 1; j < nw; ++j)
+            if (overlaps(writes[i], writes[j]))
+                return true;
+    }
+    return false;
+}
+
+static bool bad_i32(const void *p) { return !p || !aligned4(p); }
+
+static pa_status page_limits(int32_t num_seqs, int32_t max_blocks_per_seq, int64_t num_blocks, int32_t num_free_pages)
+{
+    if (num_seqs < 0 || max_blocks_per_seq <= 0 || num_blocks <= 0 || num_blocks > (int64_t)1 << 31 ||
+        num_free_pages < 0)
+        return PA_ERR_INVALID_ARG;
+    // lengths are 32-bit, and so is the number of a table entry
+    if (num_seqs > kPageMaxSeqsHost || max_blocks_per_seq > INT32_MAX / 16 ||
+        (int64_t)num_seqs * max_blocks_per_seq > INT32_MAX)
+        return PA_ERR_UNSUPPORTED;
+    return PA_OK;
+}
+
+pa_status pa_fork_requests(const int32_t *parents, const int32_t *children, const int32_t *fork_lens,
+                           int32_t num_forks, const int32_t *context_lens, int32_t num_seqs, int32_t *block_tables,
+                           int32_t max_blocks_per_seq, const int32_t *shares_in, int32_t *shares_out,
+                           int64_t num_blocks, const int32_t *free_pages, int32_t num_free_pages,
+                           const int32_t *cursor_in, int32_t *cursor_out, int32_t *seq_lens, int32_t *copy_src,
+                           int32_t *copy_dst, pa_stream_t stream)
+{
+    pa_status st = page_limits(num_seqs, max_blocks_per_seq, num_blocks, num_free_pages);
+    if (st != PA_OK)
+        return st;
+    if (num_forks < 0)
+        return PA_ERR_INVALID_ARG;
+    if (num_forks > kPageMaxSeqsHost)
+        return PA_ERR_UNSUPPORTED;
+    if (num_seqs == 0) {
+        snprintf(g_last_info, sizeof g_last_info, "fork_requests: empty batch (nothing launched)");
+        return num_forks == 0 ? PA_OK : PA_ERR_INVALID_ARG;
+    }
+    if ((num_forks > 0 && (bad_i32(parents) || bad_i32(children) || bad_i32(copy_src) || bad_i32(copy_dst))) ||
+        !aligned4(fork_lens) || bad_i32(context_lens) || bad_i32(block_tables) || bad_i32(shares_in) ||
+        bad_i32(shares_out) || (num_free_pages > 0 && bad_i32(free_pages)) || bad_i32(cursor_in) ||
+        bad_i32(cursor_out) || bad_i32(seq_lens))
+        return PA_ERR_INVALID_ARG;
+    const int64_t f4 = (int64_t)num_forks * 4, n4 = (int64_t)num_seqs * 4;
+    const Span reads[7] = {span(context_lens, n4), span(shares_in, num_blocks * 4), span(cursor_in, 4),
+                           span(parents, f4),      span(children, f4),              span(fork_lens, fork_lens ? f4 : 0),
+                           span(free_pages, (int64_t)num_free_pages * 4)};
+    const Span writes[6] = {span(seq_lens, n4), span(shares_out, num_blocks * 4), span(cursor_out, 4),
+                            span(block_tables, n4 * max_blocks_per_seq), span(copy_src, f4), span(copy_dst, f4)};
+    const int same[6] = {0, 1, 2, -1, -1, -1};
+    if (any_overlap(writes, same, 6, reads, 7))
+        return PA_ERR_INVALID_ARG;
+    ErrState *err = nullptr;
+    if ((st = device_setup(&err)) != PA_OK)
+        return st;
+    PageArgs a{};
+    a.parents = parents, a.children = children, a.fork_lens = fork_lens, a.num_forks = num_forks;
+    a.context_lens = context_lens, a.num_seqs = num_seqs, a.block_tables = block_tables, a.max_blocks = max_blocks_per_seq;
+    a.shares_in = shares_in, a.shares_out = shares_out, a.num_blocks = num_blocks;
+    a.free_pages = const_cast<int32_t *>(free_pages), a.num_free = num_free_pages;
+    a.cursor_in = cursor_in, a.cursor_out = cursor_out, a.seq_lens = seq_lens, a.copy_src = copy_src, a.copy_dst = copy_dst;
+    int grid = 0;
+    const cudaError_t e = launch_fork_requests(a, err, reinterpret_cast<cudaStream_t>(stream), &grid);
+    snprintf(g_last_info, sizeof g_last_info, "fork_requests forks=%d seqs=%d grid=%d", num_forks, num_seqs, grid);
+    return cuda_status(e);
+}
+
+pa_status pa_release_pages(const int32_t *context_lens, const int32_t *keep_lens, int32_t num_seqs,
+                           const int32_t *block_tables, int32_t max_blocks_per_seq, const int32_t *shares_in,
+                           int32_t *shares_out, int64_t num_blocks, int32_t *free_pages, int32_t num_free_pages,
+                           const int32_t *cursor_in, int32_t *cursor_out, int32_t *seq_lens, pa_stream_t stream)
+{
+    pa_status st = page_limits(num_seqs, max_blocks_per_seq, num_blocks, num_free_pages);
+    if (st != PA_OK)
+        return st;
+    if (num_seqs == 0) {
+        snprintf(g_last_info, sizeof g_last_info, "release_pages: empty batch (nothing launched)");
+        return PA_OK;
+    }
+    if (bad_i32(context_lens) || bad_i32(keep_lens) || bad_i32(block_tables) || bad_i32(shares_in) ||
+        bad_i32(shares_out) || (num_free_pages > 0 && bad_i32(free_pages)) || bad_i32(cursor_in) ||
+        bad_i32(cursor_out) || bad_i32(seq_lens))
+        return PA_ERR_INVALID_ARG;
+    const int64_t n4 = (int64_t)num_seqs * 4;
+    const Span reads[5] = {span(context_lens, n4), span(shares_in, num_blocks * 4), span(cursor_in, 4),
+                           span(keep_lens, n4), span(block_tables, n4 * max_blocks_per_seq)};
+    const Span writes[4] = {span(seq_lens, n4), span(shares_out, num_blocks * 4), span(cursor_out, 4),
+                            span(free_pages, (int64_t)num_free_pages * 4)};
+    const int same[4] = {0, 1, 2, -1};
+    if (any_overlap(writes, same, 4, reads, 5))
+        return PA_ERR_INVALID_ARG;
+    ErrState *err = nullptr;
+    if ((st = device_setup(&err)) != PA_OK)
+        return st;
+    PageArgs a{};
+    a.context_lens = context_lens, a.keep_lens = keep_lens, a.num_seqs = num_seqs;
+    a.block_tables = const_cast<int32_t *>(block_tables), a.max_blocks = max_blocks_per_seq;
+    a.shares_in = shares_in, a.shares_out = shares_out, a.num_blocks = num_blocks;
+    a.free_pages = free_pages, a.num_free = num_free_pages, a.cursor_in = cursor_in, a.cursor_out = cursor_out;
+    a.seq_lens = seq_lens;
+    int grid = 0;
+    const cudaError_t e = launch_release_pages(a, err, reinterpret_cast<cudaStream_t>(stream), &grid);
+    snprintf(g_last_info, sizeof g_last_info, "release_pages seqs=%d grid=%d", num_seqs, grid);
+    return cuda_status(e);
+}
+
+size_t pa_compact_pages_workspace_size(int64_t num_blocks)
+{
+    return num_blocks <= 0 || num_blocks > kPageMaxBlocksHost ? 0 : round256(((size_t)num_blocks + 31) / 32 * 4);
+}
+
+pa_status pa_compact_pages(const int32_t *context_lens, int32_t num_seqs, const int32_t *block_tables,
+                           int32_t *tables_out, int32_t max_blocks_per_seq, const int32_t *shares_in,
+                           int32_t *shares_out, int64_t num_blocks, int32_t *free_pages, int32_t num_free_pages,
+                           const int32_t *cursor_in, int32_t *cursor_out, int32_t *copy_src, int32_t *copy_dst,
+                           int32_t max_moves, int32_t *counts, void *workspace, size_t workspace_bytes,
+                           pa_stream_t stream)
+{
+    pa_status st = page_limits(num_seqs, max_blocks_per_seq, num_blocks, num_free_pages);
+    if (st != PA_OK)
+        return st;
+    if (max_moves < 0 || (int64_t)num_free_pages < num_blocks)
+        return PA_ERR_INVALID_ARG;
+    if (num_blocks > kPageMaxBlocksHost)
+        return PA_ERR_UNSUPPORTED;
+    if ((num_seqs > 0 && (bad_i32(context_lens) || bad_i32(block_tables) || bad_i32(tables_out))) || bad_i32(shares_in) ||
+        bad_i32(shares_out) || bad_i32(free_pages) || bad_i32(cursor_in) || bad_i32(cursor_out) ||
+        (max_moves > 0 && (bad_i32(copy_src) || bad_i32(copy_dst))) || bad_i32(counts))
+        return PA_ERR_INVALID_ARG;
+    const size_t need = pa_compact_pages_workspace_size(num_blocks);
+    if (!workspace || workspace_bytes < need)
+        return PA_ERR_WORKSPACE;
+    if (reinterpret_cast<uintptr_t>(workspace) & 255u)
+        return PA_ERR_INVALID_ARG;
+    const int64_t n4 = (int64_t)num_seqs * 4, m4 = (int64_t)max_moves * 4, t4 = n4 * max_blocks_per_seq;
+    const Span reads[4] = {span(block_tables, t4), span(shares_in, num_blocks * 4), span(cursor_in, 4),
+                           span(context_lens, n4)};
+    const Span writes[8] = {span(tables_out, t4), span(shares_out, num_blocks * 4), span(cursor_out, 4),
+                            span(free_pages, (int64_t)num_free_pages * 4), span(copy_src, m4), span(copy_dst, m4),
+                            span(counts, 8), span(workspace, (int64_t)need)};
+    const int same[8] = {0, 1, 2, -1, -1, -1, -1, -1};
+    if (any_overlap(writes, same, 8, reads, 4))
+        return PA_ERR_INVALID_ARG;
+    ErrState *err = nullptr;
+    if ((st = device_setup(&err)) != PA_OK)
+        return st;
+    PageArgs a{};
+    a.context_lens = context_lens, a.num_seqs = num_seqs, a.block_tables = const_cast<int32_t *>(block_tables);
+    a.tables_out = tables_out, a.max_blocks = max_blocks_per_seq;
+    a.shares_in = shares_in, a.shares_out = shares_out, a.num_blocks = num_blocks;
+    a.free_pages = free_pages, a.num_free = num_free_pages, a.cursor_in = cursor_in, a.cursor_out = cursor_out;
+    a.copy_src = copy_src, a.copy_dst = copy_dst, a.max_moves = max_moves, a.counts = counts;
+    a.bitmap = static_cast<uint32_t *>(workspace);
+    int grid = 0;
+    const cudaError_t e = launch_compact_pages(a, err, reinterpret_cast<cudaStream_t>(stream), &grid);
+    snprintf(g_last_info, sizeof g_last_info, "compact_pages seqs=%d blocks=%lld grid=%d", num_seqs, (long long)num_blocks,
+             grid);
+    return cuda_status(e);
 }
 
 }  // extern "C"

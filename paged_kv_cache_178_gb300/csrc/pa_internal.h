@@ -191,6 +191,49 @@ cudaError_t launch_quant_attention(const QuantAttnArgs &a, ErrState *err, cudaSt
                                    size_t info_len);
 cudaError_t init_quant_attention_attributes();
 
+// Page copies (pa_pages.cu).  Strides and sizes in 16-byte units; a view's
+// page is c0 runs (s0 apart) of c1 runs (s1 apart) of run_vecs vectors, or one
+// run (run_vecs == page_vecs).
+constexpr int kCopyMaxCachesHost = 128;
+struct CopyArgs {
+    uint4 *k[kCopyMaxCachesHost], *v[kCopyMaxCachesHost];
+    int32_t num_caches;
+    int32_t num_pairs;
+    const int32_t *src, *dst;
+    int64_t num_blocks, block_stride, s0, s1;
+    int32_t page_vecs, run_vecs, c1;
+};
+cudaError_t launch_copy_pages(const CopyArgs &a, ErrState *err, cudaStream_t stream, int num_sms, int64_t *grid);
+
+// Fork, release and compaction (pa_pages.cu): the calls' arguments, those that
+// a call does not have left out.
+constexpr int kPageMaxSeqsHost = 8192;
+constexpr int64_t kPageMaxBlocksHost = int64_t(1) << 20;  // of a compaction
+struct PageArgs {
+    const int32_t *parents, *children, *fork_lens;
+    int32_t num_forks;
+    const int32_t *context_lens, *keep_lens;
+    int32_t num_seqs;
+    int32_t *block_tables, *tables_out;
+    int32_t max_blocks;
+    const int32_t *shares_in;
+    int32_t *shares_out;
+    int64_t num_blocks;
+    int32_t *free_pages;
+    int32_t num_free;
+    const int32_t *cursor_in;
+    int32_t *cursor_out;
+    int32_t *seq_lens;
+    int32_t *copy_src, *copy_dst;
+    int32_t max_moves;
+    int32_t *counts;
+    uint32_t *bitmap;
+};
+cudaError_t launch_fork_requests(const PageArgs &a, ErrState *err, cudaStream_t stream, int *grid);
+cudaError_t launch_release_pages(const PageArgs &a, ErrState *err, cudaStream_t stream, int *grid);
+cudaError_t launch_compact_pages(const PageArgs &a, ErrState *err, cudaStream_t stream, int *grid);
+cudaError_t init_page_attributes();
+
 // Encodes a tiled tensor map (driver entry point fetched at run time).
 CUresult encode_tiled(CUtensorMap *map, CUtensorMapDataType dtype, cuuint32_t rank, void *base,
                       const cuuint64_t *dims, const cuuint64_t *strides_bytes,

@@ -16,6 +16,9 @@ fails, an exception is raised.
     QuantCache, reshape_and_cache_quant(...), dequantize_kv(...),
     paged_attention_quant(...)
         the cache in 4 bits: its write, read-back and attention
+    copy_pages(...), copy_pages_quant(...), fork_requests(...),
+    release_pages(...), compact_pages(...)
+        pages between requests: shared by forks, released, moved together
 
 k_cache / v_cache are [num_blocks, 16, Hkv, Dh] BF16 views (they may be
 slices of one interleaved [num_blocks, 2, 16, Hkv, Dh] pool) with identical
@@ -26,7 +29,7 @@ from __future__ import annotations
 import ctypes
 import os
 import threading
-from typing import Optional, Tuple
+from typing import Optional, Sequence, Tuple
 
 import torch
 
@@ -46,7 +49,9 @@ EXPORTED = ("pa_init", "pa_reshape_and_cache", "pa_paged_attention_workspace_siz
             "pa_gather_kv_head", "pa_check_errors", "pa_set_fold_wait_limit_ns",
             "pa_copy_to_device", "pa_status_string", "pa_last_launch_info", "pa_build_step_metadata",
             "pa_qk_norm_rope", "pa_qk_norm_rope_and_cache", "pa_reshape_and_cache_quant", "pa_dequantize_kv",
-            "pa_paged_attention_quant_workspace_size", "pa_paged_attention_quant")
+            "pa_paged_attention_quant_workspace_size", "pa_paged_attention_quant", "pa_copy_pages",
+            "pa_copy_pages_quant", "pa_fork_requests", "pa_release_pages", "pa_compact_pages_workspace_size",
+            "pa_compact_pages")
 NOALLOC_SCRATCH_BYTES = 8 << 20
 
 
@@ -130,6 +135,18 @@ def load(path: str = LIB_PATH):
         lib.pa_paged_attention_quant.restype = i32
         lib.pa_paged_attention_quant.argtypes = [vp, i64, i64, i32, qc, vp, i32, vp, vp, i32, i32, i32, i64, f32, vp,
                                                  vp, vp, sz, vp]
+        lib.pa_copy_pages.restype = i32
+        lib.pa_copy_pages.argtypes = [ctypes.POINTER(PaKvCache), i32, vp, vp, i64, vp]
+        lib.pa_copy_pages_quant.restype = i32
+        lib.pa_copy_pages_quant.argtypes = [qc, i32, vp, vp, i64, vp]
+        lib.pa_fork_requests.restype = i32
+        lib.pa_fork_requests.argtypes = [vp, vp, vp, i32, vp, i32, vp, i32, vp, vp, i64, vp, i32, vp, vp, vp, vp, vp, vp]
+        lib.pa_release_pages.restype = i32
+        lib.pa_release_pages.argtypes = [vp, vp, i32, vp, i32, vp, vp, i64, vp, i32, vp, vp, vp, vp]
+        lib.pa_compact_pages_workspace_size.restype = sz
+        lib.pa_compact_pages_workspace_size.argtypes = [i64]
+        lib.pa_compact_pages.restype = i32
+        lib.pa_compact_pages.argtypes = [vp, i32, vp, vp, i32, vp, vp, i64, vp, i32, vp, vp, vp, vp, i32, vp, vp, sz, vp]
         lib.pa_status_string.restype = ctypes.c_char_p
         lib.pa_status_string.argtypes = [i32]
         lib.pa_last_launch_info.restype = None
@@ -854,6 +871,170 @@ def paged_attention_quant(q: torch.Tensor, cache: QuantCache, block_tables: torc
     prepare_paged_attention_quant(q, cache, block_tables, seq_lens, query_start_loc, scale, max_query_len,
                                   max_seq_len, out, lse, workspace, max_pages, stream)()
     return out, lse
+
+
+# ------------------------------------------------- pages between requests ----
+
+def _copy_lists(src_pages: torch.Tensor, dst_pages: torch.Tensor) -> int:
+    _require_i32(src_pages=src_pages, dst_pages=dst_pages)
+    if src_pages.dim() != 1 or src_pages.shape != dst_pages.shape:
+        raise ValueError("src_pages and dst_pages must be lists of one length")
+    return src_pages.numel()
+
+
+def prepare_copy_pages(caches: Sequence[Tuple[torch.Tensor, torch.Tensor]], src_pages: torch.Tensor,
+                       dst_pages: torch.Tensor, stream: Optional[torch.cuda.Stream] = None) -> PreparedCall:
+    """copy_pages, validated now and issued by each call of the result."""
+    n = _copy_lists(src_pages, dst_pages)
+    caches = [tuple(c) for c in caches]
+    structs = (PaKvCache * len(caches))(*[cache_struct(k, v) for k, v in caches])
+    _require_same_device(src_pages, dst_pages, *[t for c in caches for t in c])
+    args = (structs, len(caches), src_pages.data_ptr(), dst_pages.data_ptr(), n, _stream_handle(stream))
+    return PreparedCall(load().pa_copy_pages, args, "pa_copy_pages", (caches, src_pages, dst_pages, structs))
+
+
+def copy_pages(caches: Sequence[Tuple[torch.Tensor, torch.Tensor]], src_pages: torch.Tensor, dst_pages: torch.Tensor,
+               stream: Optional[torch.cuda.Stream] = None) -> None:
+    """Copy page src_pages[i] to page dst_pages[i] (int32; a negative source
+    skips) in every (k_cache, v_cache) of caches: the pools of a model's layers."""
+    prepare_copy_pages(caches, src_pages, dst_pages, stream)()
+
+
+def prepare_copy_pages_quant(caches: Sequence[QuantCache], src_pages: torch.Tensor, dst_pages: torch.Tensor,
+                             stream: Optional[torch.cuda.Stream] = None) -> PreparedCall:
+    """copy_pages_quant, validated now and issued by each call of the result."""
+    n = _copy_lists(src_pages, dst_pages)
+    caches = list(caches)
+    structs = (PaQuantCache * len(caches))(*[c.struct for c in caches])
+    _require_same_device(src_pages, dst_pages, *[c.k_pool for c in caches])
+    args = (structs, len(caches), src_pages.data_ptr(), dst_pages.data_ptr(), n, _stream_handle(stream))
+    return PreparedCall(load().pa_copy_pages_quant, args, "pa_copy_pages_quant", (caches, src_pages, dst_pages, structs))
+
+
+def copy_pages_quant(caches: Sequence[QuantCache], src_pages: torch.Tensor, dst_pages: torch.Tensor,
+                     stream: Optional[torch.cuda.Stream] = None) -> None:
+    """copy_pages within 4-bit caches."""
+    prepare_copy_pages_quant(caches, src_pages, dst_pages, stream)()
+
+
+def _page_state(context_lens, block_tables, shares_in, shares_out, free_pages, cursor_in, cursor_out, **more) -> int:
+    """Checks what fork, release and compaction share; returns the batch size."""
+    _require_i32(context_lens=context_lens, block_tables=block_tables, shares_in=shares_in, shares_out=shares_out,
+                 free_pages=free_pages, cursor_in=cursor_in, cursor_out=cursor_out, **more)
+    _require_same_device(context_lens, block_tables, shares_in, shares_out, free_pages, cursor_in, cursor_out, *more.values())
+    n = context_lens.numel()
+    if block_tables.dim() != 2 or block_tables.shape[0] != n or shares_in.shape != shares_out.shape \
+            or cursor_in.numel() != 1 or cursor_out.numel() != 1:
+        raise ValueError("metadata shapes disagree")
+    return n
+
+
+def prepare_fork_requests(parents: torch.Tensor, children: torch.Tensor, fork_lens: Optional[torch.Tensor],
+                          context_lens: torch.Tensor, block_tables: torch.Tensor, shares_in: torch.Tensor,
+                          shares_out: torch.Tensor, free_pages: torch.Tensor, cursor_in: torch.Tensor,
+                          cursor_out: torch.Tensor, seq_lens: torch.Tensor, copy_src: torch.Tensor,
+                          copy_dst: torch.Tensor, stream: Optional[torch.cuda.Stream] = None) -> PreparedCall:
+    """fork_requests, validated now and issued by each call of the result."""
+    lists = dict(parents=parents, children=children, copy_src=copy_src, copy_dst=copy_dst)
+    if fork_lens is not None:
+        lists["fork_lens"] = fork_lens
+    n = _page_state(context_lens, block_tables, shares_in, shares_out, free_pages, cursor_in, cursor_out,
+                    seq_lens=seq_lens, **lists)
+    if seq_lens.numel() != n or any(t.numel() != parents.numel() for t in lists.values()):
+        raise ValueError("metadata shapes disagree")
+    args = (parents.data_ptr(), children.data_ptr(), _ptr(fork_lens), parents.numel(), context_lens.data_ptr(), n,
+            block_tables.data_ptr(), block_tables.shape[1], shares_in.data_ptr(), shares_out.data_ptr(), shares_in.numel(),
+            free_pages.data_ptr(), free_pages.numel(), cursor_in.data_ptr(), cursor_out.data_ptr(), seq_lens.data_ptr(),
+            copy_src.data_ptr(), copy_dst.data_ptr(), _stream_handle(stream))
+    return PreparedCall(load().pa_fork_requests, args, "pa_fork_requests",
+                        (parents, children, fork_lens, context_lens, block_tables, shares_in, shares_out, free_pages,
+                         cursor_in, cursor_out, seq_lens, copy_src, copy_dst))
+
+
+def fork_requests(parents: torch.Tensor, children: torch.Tensor, fork_lens: Optional[torch.Tensor],
+                  context_lens: torch.Tensor, block_tables: torch.Tensor, shares_in: torch.Tensor,
+                  shares_out: torch.Tensor, free_pages: torch.Tensor, cursor_in: torch.Tensor, cursor_out: torch.Tensor,
+                  seq_lens: torch.Tensor, copy_src: torch.Tensor, copy_dst: torch.Tensor,
+                  stream: Optional[torch.cuda.Stream] = None) -> None:
+    """Give the empty requests children [F] the first fork_lens [F] tokens (None:
+    all) of the requests parents [F]: whole pages are shared (shares [num_blocks]
+    counts the owners beyond a page's first), a partial last page gets a free one
+    and an entry of copy_src / copy_dst [F] (-1 otherwise) for copy_pages.  All
+    int32; seq_lens, shares_out and cursor_out may be context_lens, shares_in and
+    cursor_in."""
+    prepare_fork_requests(parents, children, fork_lens, context_lens, block_tables, shares_in, shares_out, free_pages,
+                          cursor_in, cursor_out, seq_lens, copy_src, copy_dst, stream)()
+
+
+def prepare_release_pages(context_lens: torch.Tensor, keep_lens: torch.Tensor, block_tables: torch.Tensor,
+                          shares_in: torch.Tensor, shares_out: torch.Tensor, free_pages: torch.Tensor,
+                          cursor_in: torch.Tensor, cursor_out: torch.Tensor, seq_lens: torch.Tensor,
+                          stream: Optional[torch.cuda.Stream] = None) -> PreparedCall:
+    """release_pages, validated now and issued by each call of the result."""
+    n = _page_state(context_lens, block_tables, shares_in, shares_out, free_pages, cursor_in, cursor_out,
+                    keep_lens=keep_lens, seq_lens=seq_lens)
+    if keep_lens.numel() != n or seq_lens.numel() != n:
+        raise ValueError("metadata shapes disagree")
+    args = (context_lens.data_ptr(), keep_lens.data_ptr(), n, block_tables.data_ptr(), block_tables.shape[1],
+            shares_in.data_ptr(), shares_out.data_ptr(), shares_in.numel(), free_pages.data_ptr(), free_pages.numel(),
+            cursor_in.data_ptr(), cursor_out.data_ptr(), seq_lens.data_ptr(), _stream_handle(stream))
+    return PreparedCall(load().pa_release_pages, args, "pa_release_pages",
+                        (context_lens, keep_lens, block_tables, shares_in, shares_out, free_pages, cursor_in, cursor_out,
+                         seq_lens))
+
+
+def release_pages(context_lens: torch.Tensor, keep_lens: torch.Tensor, block_tables: torch.Tensor,
+                  shares_in: torch.Tensor, shares_out: torch.Tensor, free_pages: torch.Tensor, cursor_in: torch.Tensor,
+                  cursor_out: torch.Tensor, seq_lens: torch.Tensor, stream: Optional[torch.cuda.Stream] = None) -> None:
+    """Cut requests to their first keep_lens [B] tokens (0: ended, negative:
+    unchanged).  The pages past them lose an owner; those without one go onto the
+    stack free_pages, below the cursor.  seq_lens, shares_out and cursor_out may be
+    context_lens, shares_in and cursor_in."""
+    prepare_release_pages(context_lens, keep_lens, block_tables, shares_in, shares_out, free_pages, cursor_in, cursor_out,
+                          seq_lens, stream)()
+
+
+def new_compact_workspace(num_blocks: int, device=None) -> torch.Tensor:
+    """Scratch for compact_pages (reusable across calls, one after another)."""
+    n = int(load().pa_compact_pages_workspace_size(int(num_blocks)))
+    return torch.empty(max(n, 256), dtype=torch.uint8, device=device if device is not None else "cuda")
+
+
+def prepare_compact_pages(context_lens: torch.Tensor, block_tables: torch.Tensor, tables_out: torch.Tensor,
+                          shares_in: torch.Tensor, shares_out: torch.Tensor, free_pages: torch.Tensor,
+                          cursor_in: torch.Tensor, cursor_out: torch.Tensor, copy_src: torch.Tensor,
+                          copy_dst: torch.Tensor, counts: torch.Tensor, workspace: torch.Tensor,
+                          stream: Optional[torch.cuda.Stream] = None) -> PreparedCall:
+    """compact_pages, validated now and issued by each call of the result."""
+    n = _page_state(context_lens, block_tables, shares_in, shares_out, free_pages, cursor_in, cursor_out,
+                    tables_out=tables_out, copy_src=copy_src, copy_dst=copy_dst, counts=counts)
+    if tables_out.shape != block_tables.shape or copy_src.numel() != copy_dst.numel() or counts.numel() != 2:
+        raise ValueError("metadata shapes disagree")
+    _require_same_device(workspace)
+    if not workspace.is_cuda or not workspace.is_contiguous():
+        raise ValueError("workspace must be a contiguous CUDA tensor")
+    args = (context_lens.data_ptr(), n, block_tables.data_ptr(), tables_out.data_ptr(), block_tables.shape[1],
+            shares_in.data_ptr(), shares_out.data_ptr(), shares_in.numel(), free_pages.data_ptr(), free_pages.numel(),
+            cursor_in.data_ptr(), cursor_out.data_ptr(), copy_src.data_ptr(), copy_dst.data_ptr(), copy_src.numel(),
+            counts.data_ptr(), workspace.data_ptr(), workspace.numel() * workspace.element_size(), _stream_handle(stream))
+    return PreparedCall(load().pa_compact_pages, args, "pa_compact_pages",
+                        (context_lens, block_tables, tables_out, shares_in, shares_out, free_pages, cursor_in, cursor_out,
+                         copy_src, copy_dst, counts, workspace))
+
+
+def compact_pages(context_lens: torch.Tensor, block_tables: torch.Tensor, tables_out: torch.Tensor,
+                  shares_in: torch.Tensor, shares_out: torch.Tensor, free_pages: torch.Tensor, cursor_in: torch.Tensor,
+                  cursor_out: torch.Tensor, copy_src: torch.Tensor, copy_dst: torch.Tensor, counts: torch.Tensor,
+                  workspace: Optional[torch.Tensor] = None, stream: Optional[torch.cuda.Stream] = None) -> None:
+    """Plan the moves that leave the n pages in use at 0 .. n-1: copy_src /
+    copy_dst [max_moves] (-1 past them) for copy_pages, the tables, shares and free
+    stack after them, and counts [2] = (n, moves).  tables_out, shares_out and
+    cursor_out may be block_tables, shares_in and cursor_in."""
+    if workspace is None:
+        n = int(load().pa_compact_pages_workspace_size(shares_in.numel()))
+        workspace = _empty((max(n, 256),), torch.uint8, context_lens.device, stream)
+    prepare_compact_pages(context_lens, block_tables, tables_out, shares_in, shares_out, free_pages, cursor_in, cursor_out,
+                          copy_src, copy_dst, counts, workspace, stream)()
 
 
 def check_errors(stream: Optional[torch.cuda.Stream] = None) -> Tuple[int, int]:
