@@ -696,6 +696,68 @@ PA_API pa_status pa_compact_pages(const int32_t *context_lens, int32_t num_seqs,
                                   void *workspace, size_t workspace_bytes, pa_stream_t stream);
 
 /*
+ * What changes the scores of pa_paged_attention_scored.  All fields 0 (or no
+ * struct): plain causal attention.
+ */
+typedef struct {
+    float soft_cap;             /* scores z become soft_cap * tanh(z / soft_cap); 0: no cap,
+                                   else within [2^-20, 2^20] */
+    int32_t window;             /* a token sees the `window` keys that end at its position; 0: all */
+    const float *slopes;        /* [Hq]: slopes[h] * |p - j| is taken off the score of key j for a
+                                   token at position p, after the cap; NULL: no bias */
+    const int32_t *prefix_lens; /* [num_seqs]: every token of request b sees keys 0 .. prefix_lens[b]-1,
+                                   whatever the other rules (at most its length); NULL: no prefix */
+    const int32_t *first_keys;  /* [num_q_tokens]: token t sees no key before first_keys[t] (but the
+                                   prefix): the start of its document; NULL: 0 */
+} pa_score_rules;
+
+/*
+ * Bytes of scratch that pa_paged_attention_scored needs for these bounds.
+ * Returns 0 for invalid arguments and where none is needed.  Smaller bounds may
+ * need more: a workspace for several calls is as large as the largest of their
+ * sizes.
+ */
+PA_API size_t pa_paged_attention_scored_workspace_size(int32_t num_seqs, int32_t num_q_heads, int32_t num_kv_heads,
+                                                       int32_t head_dim, int32_t max_query_len, int32_t max_seq_len);
+
+/*
+ * pa_paged_attention with rules for the scores: a cap by tanh, a bias by
+ * distance, a sliding window, a prefix that all tokens see (first tokens kept
+ * beside a window; a prompt read in both directions), documents packed into one
+ * context.  The paper (the source pages) has no counterpart to it.  A token of
+ * request b at position p, with L = seq_lens[b], sees key j where
+ *   j < L and ((first_keys[t] <= j <= p and p - j < window) or j < prefix_lens[b]).
+ *   z_j = scale * q.K_j;  z_j = soft_cap * tanh(z_j / soft_cap);
+ *   z_j = z_j - slopes[h] * |p - j|
+ *   out = sum_j exp(z_j) V_j / sum_j exp(z_j),  lse = ln(sum_j exp(z_j))
+ * over the keys that it sees; a token that sees none gets zeros and lse -inf.
+ * Arguments, ownership and errors as for pa_paged_attention; kv_tile is
+ * ignored.  Differences:
+ *   - Keys that a token does not see never matter to it, whatever their bytes
+ *     (NaN included); a page that no token of the request sees a key of is
+ *     never read, and its table entry may be anything (pages that a window has
+ *     left behind may be released).  A bad id of another page makes the rows that
+ *     see a key of it NaN and latches PA_ERR_BAD_METADATA (index = the request).
+ *   - Sums, maxima and lse are fp32, the probabilities BF16.  A call's results
+ *     are bitwise reproducible; other bounds, or the token in another call, may
+ *     round differently (the fixed schedule of pa_paged_attention is not kept).
+ *   - workspace: pa_paged_attention_scored_workspace_size(...) bytes, 256-byte
+ *     aligned, any contents; calls with different bounds may share it one after
+ *     another.
+ *   - out, lse and the workspace may not share bytes with an input or with one
+ *     another (PA_ERR_INVALID_ARG).
+ * num_seqs <= 8192; num_seqs * max_query_len * Hkv <= INT32_MAX; max_seq_len <=
+ * INT32_MAX - 4096 (PA_ERR_UNSUPPORTED).
+ */
+PA_API pa_status pa_paged_attention_scored(const void *q, int64_t num_q_tokens, int64_t q_tok_stride,
+                                           int32_t num_q_heads, const pa_kv_cache *cache,
+                                           const int32_t *block_tables, int32_t max_blocks_per_seq,
+                                           const int32_t *seq_lens, const int32_t *query_start_loc, int32_t num_seqs,
+                                           int32_t max_query_len, int32_t max_seq_len, float scale,
+                                           const pa_score_rules *rules, void *out, float *lse, void *workspace,
+                                           size_t workspace_bytes, pa_stream_t stream);
+
+/*
  * Synchronises `stream`, then reads and clears the current device's error
  * flag.  Returns PA_OK, PA_ERR_BAD_METADATA or PA_ERR_TIMEOUT (or
  * PA_ERR_CUDA if the synchronisation failed).  *first_bad_index (may be

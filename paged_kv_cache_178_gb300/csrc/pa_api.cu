@@ -41,7 +41,7 @@ static pa_status device_setup(ErrState **err_out, int *num_sms = nullptr)
             return PA_ERR_CUDA;
         if (init_attention_attributes() != cudaSuccess || init_step_attributes() != cudaSuccess ||
             init_quant_attributes() != cudaSuccess || init_quant_attention_attributes() != cudaSuccess ||
-            init_page_attributes() != cudaSuccess)
+            init_page_attributes() != cudaSuccess || init_scored_attributes() != cudaSuccess)
             return PA_ERR_CUDA;
         if (cudaDeviceGetAttribute(&g_num_sms[dev], cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
             return PA_ERR_CUDA;
@@ -1522,6 +1522,117 @@ pa_status pa_compact_pages(const int32_t *context_lens, int32_t num_seqs, const 
     snprintf(g_last_info, sizeof g_last_info, "compact_pages seqs=%d blocks=%lld grid=%d", num_seqs, (long long)num_blocks,
              grid);
     return cuda_status(e);
+}
+
+// -------------------------------------------------------- scored attention --
+constexpr int kScoredMaxSeqs = 8192;
+
+static bool scored_sizes_ok(int32_t num_seqs, int32_t hq, int32_t hkv, int32_t dh, int32_t max_query_len,
+                            int32_t max_seq_len)
+{
+    return num_seqs > 0 && num_seqs <= kScoredMaxSeqs && hkv > 0 && hq > 0 && hq % hkv == 0 && hq / hkv <= 128 &&
+           (dh == 128 || dh == 256 || dh == 512) && max_query_len > 0 && max_seq_len >= 0 &&
+           max_seq_len <= INT32_MAX - 4096 && (int64_t)num_seqs * max_query_len * hkv <= INT32_MAX;
+}
+
+size_t pa_paged_attention_scored_workspace_size(int32_t num_seqs, int32_t num_q_heads, int32_t num_kv_heads,
+                                                int32_t head_dim, int32_t max_query_len, int32_t max_seq_len)
+{
+    if (!scored_sizes_ok(num_seqs, num_q_heads, num_kv_heads, head_dim, max_query_len, max_seq_len))
+        return 0;
+    return scored_workspace_bytes(num_seqs, num_q_heads, num_kv_heads, head_dim, max_query_len, max_seq_len);
+}
+
+pa_status pa_paged_attention_scored(const void *q, int64_t num_q_tokens, int64_t q_tok_stride, int32_t num_q_heads,
+                                    const pa_kv_cache *cache, const int32_t *block_tables, int32_t max_blocks_per_seq,
+                                    const int32_t *seq_lens, const int32_t *query_start_loc, int32_t num_seqs,
+                                    int32_t max_query_len, int32_t max_seq_len, float scale,
+                                    const pa_score_rules *rules, void *out, float *lse, void *workspace,
+                                    size_t workspace_bytes, pa_stream_t stream)
+{
+    pa_status st = check_cache(cache);
+    if (st != PA_OK)
+        return st;
+    if (num_q_heads <= 0 || num_seqs < 0 || max_query_len < 0 || max_seq_len < 0 || num_q_tokens < 0 ||
+        max_blocks_per_seq < 0 || num_q_tokens > INT32_MAX)
+        return PA_ERR_INVALID_ARG;
+    const int32_t hkv = cache->num_kv_heads, dh = cache->head_dim;
+    if (num_q_heads % hkv != 0 || num_q_heads / hkv > 128)
+        return PA_ERR_UNSUPPORTED;
+    if (!(scale > 0.f) || scale == INFINITY)
+        return PA_ERR_INVALID_ARG;
+    const pa_score_rules none{};
+    const pa_score_rules &r = rules ? *rules : none;
+    if (!(r.soft_cap == 0.f || (r.soft_cap >= 0x1p-20f && r.soft_cap <= 0x1p20f)) || r.window < 0 ||
+        !aligned4(r.slopes) || !aligned4(r.prefix_lens) || !aligned4(r.first_keys))
+        return PA_ERR_INVALID_ARG;
+    if (!std::isfinite(scale * 4.f) || (r.soft_cap > 0.f && !std::isfinite(4.f * scale / r.soft_cap)))
+        return PA_ERR_INVALID_ARG;
+    if (num_seqs == 0 || num_q_tokens == 0 || max_query_len == 0) {
+        snprintf(g_last_info, sizeof g_last_info, "scored attention: empty batch (nothing launched)");
+        return PA_OK;
+    }
+    const int64_t row = (int64_t)num_q_heads * dh;
+    if (!q || !out || !aligned16(q) || !aligned16(out) || !aligned4(lse) || bad_i32(block_tables) || bad_i32(seq_lens) ||
+        bad_i32(query_start_loc))
+        return PA_ERR_INVALID_ARG;
+    if (q_tok_stride < row || (q_tok_stride & 7) || max_blocks_per_seq == 0)
+        return PA_ERR_INVALID_ARG;
+    if (!scored_sizes_ok(num_seqs, num_q_heads, hkv, dh, max_query_len, max_seq_len))
+        return PA_ERR_UNSUPPORTED;
+    const size_t need = scored_workspace_bytes(num_seqs, num_q_heads, hkv, dh, max_query_len, max_seq_len);
+    if (need > 0) {
+        if (!workspace || workspace_bytes < need)
+            return PA_ERR_WORKSPACE;
+        if (reinterpret_cast<uintptr_t>(workspace) & 255u)
+            return PA_ERR_INVALID_ARG;
+    }
+    const int64_t n4 = (int64_t)num_seqs * 4;
+    const Span reads[9] = {rows_span(Rows{q, q_tok_stride, row}, num_q_tokens),
+                           span(cache->k, pool_view_bytes(cache)),
+                           span(cache->v, pool_view_bytes(cache)),
+                           span(block_tables, n4 * max_blocks_per_seq),
+                           span(seq_lens, n4),
+                           span(query_start_loc, n4 + 4),
+                           span(r.slopes, r.slopes ? (int64_t)num_q_heads * 4 : 0),
+                           span(r.prefix_lens, r.prefix_lens ? n4 : 0),
+                           span(r.first_keys, r.first_keys ? num_q_tokens * 4 : 0)};
+    const Span writes[3] = {span(out, num_q_tokens * row * 2), span(lse, lse ? num_q_tokens * num_q_heads * 4 : 0),
+                            span(workspace, (int64_t)need)};
+    const int same[3] = {-1, -1, -1};
+    if (any_overlap(writes, same, 3, reads, 9))
+        return PA_ERR_INVALID_ARG;
+    ErrState *err = nullptr;
+    if ((st = device_setup(&err)) != PA_OK)
+        return st;
+    AttnArgs a{};
+    a.q = q;
+    a.num_q_tokens = num_q_tokens;
+    a.q_tok_stride = q_tok_stride;
+    a.num_q_heads = num_q_heads;
+    a.k = cache->k;
+    a.v = cache->v;
+    a.num_blocks = cache->num_blocks;
+    a.num_kv_heads = hkv;
+    a.head_dim = dh;
+    a.block_stride = cache->block_stride;
+    a.token_stride = cache->token_stride;
+    a.head_stride = cache->head_stride;
+    a.block_tables = block_tables;
+    a.max_blocks_per_seq = max_blocks_per_seq;
+    a.seq_lens = seq_lens;
+    a.query_start_loc = query_start_loc;
+    a.num_seqs = num_seqs;
+    a.max_query_len = max_query_len;
+    a.max_seq_len = max_seq_len;
+    a.scale = scale;
+    a.out = out;
+    a.lse = lse;
+    a.workspace = workspace;
+    a.workspace_bytes = workspace_bytes;
+    const ScoreRules sr{r.soft_cap, r.window, r.slopes, r.prefix_lens, r.first_keys};
+    return cuda_status(launch_scored_attention(a, sr, err, reinterpret_cast<cudaStream_t>(stream), g_last_info,
+                                               sizeof g_last_info));
 }
 
 }  // extern "C"

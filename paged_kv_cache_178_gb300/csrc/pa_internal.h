@@ -234,6 +234,19 @@ cudaError_t launch_release_pages(const PageArgs &a, ErrState *err, cudaStream_t 
 cudaError_t launch_compact_pages(const PageArgs &a, ErrState *err, cudaStream_t stream, int *grid);
 cudaError_t init_page_attributes();
 
+// Attention with capped, biased or masked scores (pa_scored.cu).
+struct ScoreRules {
+    float soft_cap;   // 0: none
+    int32_t window;   // 0: none
+    const float *slopes;
+    const int32_t *prefix_lens, *first_keys;
+};
+size_t scored_workspace_bytes(int32_t num_seqs, int32_t hq, int32_t hkv, int32_t head_dim, int32_t max_query_len,
+                              int32_t max_seq_len);
+cudaError_t launch_scored_attention(const AttnArgs &a, const ScoreRules &r, ErrState *err, cudaStream_t stream,
+                                    char *info, size_t info_len);
+cudaError_t init_scored_attributes();
+
 // Encodes a tiled tensor map (driver entry point fetched at run time).
 CUresult encode_tiled(CUtensorMap *map, CUtensorMapDataType dtype, cuuint32_t rank, void *base,
                       const cuuint64_t *dims, const cuuint64_t *strides_bytes,

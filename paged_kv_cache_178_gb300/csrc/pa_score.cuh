@@ -1,0 +1,151 @@
+// What the kernels of pa_paged_attention_scored share: the call's parameters,
+// which keys a row sees, its scores, and one row computed plainly.
+#pragma once
+#include <cuda_bf16.h>
+
+#include "pa_attn_common.cuh"
+
+namespace pa {
+
+constexpr float kLog2e = 1.4426950408889634f;
+
+struct ScoreParams {
+    const __nv_bfloat16 *q;
+    int64_t q_tok_stride;
+    const __nv_bfloat16 *k, *v;
+    int64_t num_blocks, block_stride, token_stride, head_stride;  // elements
+    const int32_t *block_tables, *seq_lens, *qsl;
+    const float *slopes;
+    const int32_t *prefix_lens, *first_keys;
+    __nv_bfloat16 *out;
+    float *lse;
+    ErrState *err;
+    int64_t num_q_tokens;
+    int32_t max_blocks, num_seqs, hq, hkv, group, max_query_len, max_seq_len;
+    int32_t window;    // INT32_MAX: none
+    float scale_log2;  // without a cap: scale * log2 e; with one: 2 * scale * log2 e / cap
+    float cap_log2;    // cap * log2 e (0: no cap)
+};
+
+__device__ __forceinline__ ReqMeta score_meta(const ScoreParams &p, int b)
+{
+    ReqMeta m;
+    const int qs = __ldg(p.qsl + b), qe = __ldg(p.qsl + b + 1), L = __ldg(p.seq_lens + b);
+    m.qs = qs;
+    m.qn = qe - qs;
+    m.L = L;
+    m.sane = qs >= 0 && qe >= qs && (int64_t)qe <= p.num_q_tokens;
+    m.ok = m.sane && L >= m.qn && (int64_t)L <= (int64_t)p.max_blocks * 16 && m.qn <= p.max_query_len &&
+           L <= p.max_seq_len;
+    return m;
+}
+
+// Tokens of the prefix that request b's rows all see.
+__device__ __forceinline__ int score_prefix(const ScoreParams &p, int b, int L)
+{
+    const int x = p.prefix_lens ? __ldg(p.prefix_lens + b) : 0;
+    return x < 0 ? 0 : (x < L ? x : L);
+}
+
+// First key of the range that ends at position pos (pos + 1: the range is
+// empty) for query token t (its index among all tokens).
+__device__ __forceinline__ int score_low(const ScoreParams &p, int64_t t, int pos)
+{
+    const int first = p.first_keys ? __ldg(p.first_keys + t) : 0;
+    int lo = first > 0 ? first : 0;
+    if (pos - p.window >= lo)  // (no overflow: both are at least 0 ... INT32_MAX)
+        lo = pos - p.window + 1;
+    return lo <= pos ? lo : pos + 1;
+}
+
+// Distance from pos to the nearest key that a row sees.  Biases are taken
+// relative to it: what is common to a row's keys would cost bits far away.
+__device__ __forceinline__ int score_nearest(int lo, int pos, int prefix)
+{
+    return lo <= pos || prefix == 0 || pos < prefix ? 0 : pos - prefix + 1;
+}
+
+__device__ __forceinline__ float rcp_approx(float x)
+{
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// cap * tanh(s / cap) in log2 units from the raw product q.k, as
+// cap (1 - 2 / (1 + exp(2 s / cap))): exact limits at both ends, an absolute
+// error of about 2^-22 cap (a share of it around 0, where the result is small,
+// but exp takes differences of scores, so the absolute error is what counts).
+__device__ __forceinline__ float capped(float raw, float scale_log2, float cap_log2)
+{
+    const float e = ex2(raw * scale_log2);
+    return __fmaf_rn(-2.f * cap_log2, rcp_approx(1.f + e), cap_log2);
+}
+
+// One (token, head) row by one warp, key by key, over exactly the keys that it
+// sees: what no row sees is not read, so nothing there (NaN, infinities, a
+// page of another request) can matter.
+template <int DH>
+__device__ __noinline__ void scored_row(const ScoreParams &p, int b, const ReqMeta &m, int i, int h)
+{
+    constexpr int E = DH / 32;  // elements of a lane
+    const int lane = threadIdx.x % 32, kvh = h / p.group;
+    const int64_t t = (int64_t)m.qs + i;
+    const int pos = m.L - m.qn + i, prefix = score_prefix(p, b, m.L), lo = score_low(p, t, pos);
+    const int near = score_nearest(lo, pos, prefix);
+    const float slope = p.slopes ? __ldg(p.slopes + h) : 0.f, slope2 = slope * kLog2e;
+    const __nv_bfloat16 *qr = p.q + t * p.q_tok_stride + (int64_t)h * DH;
+    float q[E], o[E];
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+        q[e] = __bfloat162float(qr[e * 32 + lane]);
+        o[e] = 0.f;
+    }
+    float mx = -INFINITY, l = 0.f;
+    bool bad = false;
+    const int32_t *bt = p.block_tables + (int64_t)b * p.max_blocks;
+    // the prefix first, then what the range adds to it
+    const int from[2] = {0, lo > prefix ? lo : prefix}, to[2] = {prefix, pos + 1};
+    for (int part = 0; part < 2; ++part) {
+        int id = -1;
+        for (int j = from[part]; j < to[part]; ++j) {
+            if (j == from[part] || j % 16 == 0)
+                id = __ldg(bt + j / 16);
+            if (id < 0 || (int64_t)id >= p.num_blocks) {
+                bad = true;
+                break;
+            }
+            const int64_t at = id * p.block_stride + (j % 16) * p.token_stride + kvh * p.head_stride;
+            float s = 0.f;
+#pragma unroll
+            for (int e = 0; e < E; ++e)
+                s = __fmaf_rn(q[e], __bfloat162float(p.k[at + e * 32 + lane]), s);
+#pragma unroll
+            for (int o2 = 16; o2 >= 1; o2 >>= 1)
+                s += __shfl_xor_sync(0xffffffffu, s, o2);
+            float z = p.cap_log2 > 0.f ? capped(s, p.scale_log2, p.cap_log2) : s * p.scale_log2;
+            if (p.slopes)
+                z -= slope2 * (float)((pos > j ? pos - j : j - pos) - near);
+            const float m_new = fmaxf(mx, z);
+            const float keep = mx == m_new ? 1.f : ex2(mx - m_new);
+            const float w = z == -INFINITY ? 0.f : ex2(z - m_new);
+            l = l * keep + w;
+#pragma unroll
+            for (int e = 0; e < E; ++e)
+                o[e] = o[e] * keep + w * __bfloat162float(p.v[at + e * 32 + lane]);
+            mx = m_new;
+        }
+    }
+    const float inv = bad ? __int_as_float(0x7FC00000) : (l > 0.f || l != l ? 1.f / l : 0.f);
+    __nv_bfloat16 *dst = p.out + (t * p.hq + h) * DH;
+#pragma unroll
+    for (int e = 0; e < E; ++e)
+        dst[e * 32 + lane] = __float2bfloat16_rn(o[e] * inv);
+    if (lane == 0 && p.lse)
+        p.lse[t * p.hq + h] = bad ? __int_as_float(0x7FC00000)
+                                  : (l == 0.f ? -INFINITY : (mx + __log2f(l)) * kLn2 - slope * (float)near);
+    if (bad && lane == 0)
+        record_error(p.err, kErrBadMetadata, b);
+}
+
+}  // namespace pa

@@ -19,6 +19,9 @@ fails, an exception is raised.
     copy_pages(...), copy_pages_quant(...), fork_requests(...),
     release_pages(...), compact_pages(...)
         pages between requests: shared by forks, released, moved together
+    paged_attention_scored(...)
+        attention with capped scores, a bias by distance, a window, a prefix
+        that all tokens see, documents packed into one context
 
 k_cache / v_cache are [num_blocks, 16, Hkv, Dh] BF16 views (they may be
 slices of one interleaved [num_blocks, 2, 16, Hkv, Dh] pool) with identical
@@ -51,7 +54,7 @@ EXPORTED = ("pa_init", "pa_reshape_and_cache", "pa_paged_attention_workspace_siz
             "pa_qk_norm_rope", "pa_qk_norm_rope_and_cache", "pa_reshape_and_cache_quant", "pa_dequantize_kv",
             "pa_paged_attention_quant_workspace_size", "pa_paged_attention_quant", "pa_copy_pages",
             "pa_copy_pages_quant", "pa_fork_requests", "pa_release_pages", "pa_compact_pages_workspace_size",
-            "pa_compact_pages")
+            "pa_compact_pages", "pa_paged_attention_scored_workspace_size", "pa_paged_attention_scored")
 NOALLOC_SCRATCH_BYTES = 8 << 20
 
 
@@ -69,6 +72,11 @@ class PaQuantCache(ctypes.Structure):
                 ("head_dim", ctypes.c_int32), ("reserved", ctypes.c_int32),
                 ("block_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64),
                 ("k_scale", ctypes.c_float), ("v_scale", ctypes.c_float)]
+
+
+class PaScoreRules(ctypes.Structure):
+    _fields_ = [("soft_cap", ctypes.c_float), ("window", ctypes.c_int32), ("slopes", ctypes.c_void_p),
+                ("prefix_lens", ctypes.c_void_p), ("first_keys", ctypes.c_void_p)]
 
 
 class PagedAttnError(RuntimeError):
@@ -147,6 +155,11 @@ def load(path: str = LIB_PATH):
         lib.pa_compact_pages_workspace_size.argtypes = [i64]
         lib.pa_compact_pages.restype = i32
         lib.pa_compact_pages.argtypes = [vp, i32, vp, vp, i32, vp, vp, i64, vp, i32, vp, vp, vp, vp, i32, vp, vp, sz, vp]
+        lib.pa_paged_attention_scored_workspace_size.restype = sz
+        lib.pa_paged_attention_scored_workspace_size.argtypes = [i32, i32, i32, i32, i32, i32]
+        lib.pa_paged_attention_scored.restype = i32
+        lib.pa_paged_attention_scored.argtypes = [vp, i64, i64, i32, ctypes.POINTER(PaKvCache), vp, i32, vp, vp, i32, i32,
+                                                  i32, f32, ctypes.POINTER(PaScoreRules), vp, vp, vp, sz, vp]
         lib.pa_status_string.restype = ctypes.c_char_p
         lib.pa_status_string.argtypes = [i32]
         lib.pa_last_launch_info.restype = None
@@ -870,6 +883,95 @@ def paged_attention_quant(q: torch.Tensor, cache: QuantCache, block_tables: torc
         workspace = _empty((max(n, 256),), torch.uint8, q.device, stream)
     prepare_paged_attention_quant(q, cache, block_tables, seq_lens, query_start_loc, scale, max_query_len,
                                   max_seq_len, out, lse, workspace, max_pages, stream)()
+    return out, lse
+
+
+# --------------------------------------------------- attention with rules ----
+
+def scored_workspace_size(num_seqs: int, num_q_heads: int, num_kv_heads: int, head_dim: int, max_query_len: int,
+                          max_seq_len: int) -> int:
+    return int(load().pa_paged_attention_scored_workspace_size(num_seqs, num_q_heads, num_kv_heads, head_dim,
+                                                               max_query_len, max_seq_len))
+
+
+def new_scored_workspace(num_seqs: int, num_q_heads: int, num_kv_heads: int, head_dim: int, max_query_len: int,
+                         max_seq_len: int, device=None) -> torch.Tensor:
+    """Scratch for paged_attention_scored (reusable across calls, one after another)."""
+    n = scored_workspace_size(num_seqs, num_q_heads, num_kv_heads, head_dim, max_query_len, max_seq_len)
+    return torch.empty(max(n, 256), dtype=torch.uint8, device=device if device is not None else "cuda")
+
+
+def prepare_paged_attention_scored(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
+                                   block_tables: torch.Tensor, seq_lens: torch.Tensor, query_start_loc: torch.Tensor,
+                                   scale: float, max_query_len: int, max_seq_len: int, out: torch.Tensor,
+                                   lse: Optional[torch.Tensor], workspace: torch.Tensor, soft_cap: float = 0.0,
+                                   slopes: Optional[torch.Tensor] = None, window: int = 0,
+                                   prefix_lens: Optional[torch.Tensor] = None,
+                                   first_keys: Optional[torch.Tensor] = None,
+                                   stream: Optional[torch.cuda.Stream] = None) -> PreparedCall:
+    """paged_attention_scored into given out / lse / workspace, validated now
+    and issued by each call of the result."""
+    c = cache_struct(k_cache, v_cache)
+    tq, hq, dh, num_seqs = _validate_attention(q, block_tables, seq_lens, query_start_loc)
+    if dh != c.head_dim:
+        raise ValueError("q and the cache disagree on the head dim")
+    if out.shape != (tq, hq, dh) or out.dtype != torch.bfloat16 or not out.is_contiguous():
+        raise ValueError("out must be a contiguous [Tq, Hq, Dh] BF16 tensor")
+    if lse is not None and (lse.shape != (tq, hq) or lse.dtype != torch.float32 or not lse.is_contiguous()):
+        raise ValueError("lse must be a contiguous [Tq, Hq] fp32 tensor")
+    _check_result_tensor("out", out)
+    if lse is not None:
+        _check_result_tensor("lse", lse)
+    if slopes is not None and (slopes.dtype != torch.float32 or not slopes.is_cuda or not slopes.is_contiguous()
+                               or slopes.numel() != hq):
+        raise ValueError("slopes must be a contiguous [Hq] fp32 CUDA tensor")
+    for name, t, n in (("prefix_lens", prefix_lens, num_seqs), ("first_keys", first_keys, tq)):
+        if t is not None:
+            _require_i32(**{name: t})
+            if t.numel() != n:
+                raise ValueError(f"{name} must have {n} entries")
+    _require_same_device(q, k_cache, v_cache, block_tables, seq_lens, query_start_loc, out, lse, workspace, slopes,
+                         prefix_lens, first_keys)
+    if workspace is not None and (not workspace.is_cuda or not workspace.is_contiguous()):
+        raise ValueError("workspace must be a contiguous CUDA tensor")
+    need = scored_workspace_size(num_seqs, hq, c.num_kv_heads, dh, max_query_len, max_seq_len)
+    ws_len = workspace.numel() * workspace.element_size() if workspace is not None else 0
+    if ws_len < need:
+        raise ValueError(f"workspace needs {need} bytes")
+    rules = PaScoreRules(float(soft_cap), int(window), _ptr(slopes), _ptr(prefix_lens), _ptr(first_keys))
+    args = (q.data_ptr(), tq, _tok_stride(q), hq, ctypes.byref(c), block_tables.data_ptr(), block_tables.shape[1],
+            seq_lens.data_ptr(), query_start_loc.data_ptr(), num_seqs, int(max_query_len), int(max_seq_len),
+            ctypes.c_float(float(scale)), ctypes.byref(rules), out.data_ptr(), _ptr(lse), _ptr(workspace), ws_len,
+            _stream_handle(stream))
+    return PreparedCall(load().pa_paged_attention_scored, args, "pa_paged_attention_scored",
+                        (q, k_cache, v_cache, block_tables, seq_lens, query_start_loc, out, lse, workspace, slopes,
+                         prefix_lens, first_keys, c, rules))
+
+
+def paged_attention_scored(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, block_tables: torch.Tensor,
+                           seq_lens: torch.Tensor, query_start_loc: torch.Tensor, scale: float, max_query_len: int,
+                           max_seq_len: int, soft_cap: float = 0.0, slopes: Optional[torch.Tensor] = None,
+                           window: int = 0, prefix_lens: Optional[torch.Tensor] = None,
+                           first_keys: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None,
+                           lse: Optional[torch.Tensor] = None, want_lse: bool = True,
+                           workspace: Optional[torch.Tensor] = None, stream: Optional[torch.cuda.Stream] = None
+                           ) -> Tuple[torch.Tensor, Optional[torch.Tensor]]:
+    """paged_attention with rules for the scores: soft_cap * tanh(z / soft_cap);
+    less slopes[h] * distance (slopes [Hq] fp32); a window of keys that ends at the
+    token; keys below prefix_lens [B] seen by every token of a request; none before
+    first_keys [Tq] otherwise (int32; documents packed into one context).  Returns
+    (out [Tq, Hq, Dh] BF16, lse [Tq, Hq] fp32 or None)."""
+    tq, hq, dh = q.shape
+    if out is None:
+        out = _empty((tq, hq, dh), torch.bfloat16, q.device, stream)
+    if lse is None and want_lse:
+        lse = _empty((tq, hq), torch.float32, q.device, stream)
+    if workspace is None:
+        n = scored_workspace_size(seq_lens.numel(), hq, k_cache.shape[2], dh, max_query_len, max_seq_len)
+        workspace = _empty((max(n, 256),), torch.uint8, q.device, stream)
+    prepare_paged_attention_scored(q, k_cache, v_cache, block_tables, seq_lens, query_start_loc, scale, max_query_len,
+                                   max_seq_len, out, lse, workspace, soft_cap, slopes, window, prefix_lens, first_keys,
+                                   stream)()
     return out, lse
 
 
