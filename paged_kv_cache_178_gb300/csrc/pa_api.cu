@@ -1532,7 +1532,8 @@ static bool scored_sizes_ok(int32_t num_seqs, int32_t hq, int32_t hkv, int32_t d
 {
     return num_seqs > 0 && num_seqs <= kScoredMaxSeqs && hkv > 0 && hq > 0 && hq % hkv == 0 && hq / hkv <= 128 &&
            (dh == 128 || dh == 256 || dh == 512) && max_query_len > 0 && max_seq_len >= 0 &&
-           max_seq_len <= INT32_MAX - 4096 && (int64_t)num_seqs * max_query_len * hkv <= INT32_MAX;
+           max_seq_len <= INT32_MAX - 4096 && (int64_t)num_seqs * max_query_len * hq <= INT32_MAX &&
+           scored_supported(num_seqs, hq, hkv, dh, max_query_len, max_seq_len);
 }
 
 size_t pa_paged_attention_scored_workspace_size(int32_t num_seqs, int32_t num_q_heads, int32_t num_kv_heads,

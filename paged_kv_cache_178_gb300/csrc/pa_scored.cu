@@ -1,39 +1,33 @@
 // pa_paged_attention_scored: attention over the BF16 pool whose scores are
 // capped, biased by distance or masked.
-#include <cstdio>
-
-#include "pa_score.cuh"
+#include "pa_scored.h"
 
 namespace pa {
 
-constexpr int kRowThreads = 256;
-
-// A warp per (token, head) row.
-template <int DH>
-__global__ void __launch_bounds__(kRowThreads) scored_rows_kernel(const ScoreParams p)
+bool scored_pool_maps(const ScoreParams &p, int32_t head_dim, CUtensorMap (&tm)[2])
 {
-    griddep_wait();
-    griddep_launch_dependents();
-    const int b = blockIdx.y, warp = blockIdx.x * (kRowThreads / 32) + threadIdx.x / 32, lane = threadIdx.x % 32;
-    const ReqMeta m = score_meta(p, b);
-    if (!m.ok && blockIdx.x == 0 && threadIdx.x == 0)
-        record_error(p.err, kErrBadMetadata, b);
-    if (!m.sane)
-        return;
-    for (int64_t r = warp; r < (int64_t)m.qn * p.hq; r += (int64_t)gridDim.x * (kRowThreads / 32)) {
-        if (m.ok) {
-            scored_row<DH>(p, b, m, (int)(r / p.hq), (int)(r % p.hq));
-            continue;
-        }
-        const int64_t at = (int64_t)m.qs * p.hq + r;
-        for (int d = lane; d < DH; d += 32)
-            p.out[at * DH + d] = __ushort_as_bfloat16(0x7FC0);
-        if (lane == 0 && p.lse)
-            p.lse[at] = __int_as_float(0x7FC00000);
-    }
+    const cuuint64_t dims[4] = {(cuuint64_t)head_dim, (cuuint64_t)p.hkv, 16, (cuuint64_t)p.num_blocks};
+    const cuuint64_t strides[3] = {(cuuint64_t)p.head_stride * 2, (cuuint64_t)p.token_stride * 2,
+                                   (cuuint64_t)p.block_stride * 2};
+    const cuuint32_t box[4] = {64, 1, 16, 1};
+    for (int i = 0; i < 2; ++i)
+        if (encode_tiled(&tm[i], CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<__nv_bfloat16 *>(i ? p.v : p.k), dims,
+                         strides, box, CU_TENSOR_MAP_SWIZZLE_128B) != CUDA_SUCCESS)
+            return false;
+    return true;
 }
 
-size_t scored_workspace_bytes(int32_t, int32_t, int32_t, int32_t, int32_t, int32_t) { return 0; }
+bool scored_supported(int32_t num_seqs, int32_t hq, int32_t hkv, int32_t head_dim, int32_t max_query_len,
+                      int32_t max_seq_len)
+{
+    return scored_rows_fits(num_seqs, hkv, hq / hkv, head_dim, max_query_len, max_seq_len);
+}
+
+size_t scored_workspace_bytes(int32_t num_seqs, int32_t hq, int32_t hkv, int32_t head_dim, int32_t max_query_len,
+                              int32_t max_seq_len)
+{
+    return scored_rows_bytes(num_seqs, hkv, hq / hkv, head_dim, max_query_len, max_seq_len);
+}
 
 static ScoreParams score_params(const AttnArgs &a, const ScoreRules &r, ErrState *err)
 {
@@ -73,26 +67,9 @@ cudaError_t launch_scored_attention(const AttnArgs &a, const ScoreRules &r, ErrS
                                     char *info, size_t info_len)
 {
     const ScoreParams p = score_params(a, r, err);
-    const int64_t rows = (int64_t)a.max_query_len * a.num_q_heads;
-    int64_t blocks = (rows + kRowThreads / 32 - 1) / (kRowThreads / 32);
-    if (blocks > 4096)
-        blocks = 4096;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)blocks, (unsigned)a.num_seqs);
-    cfg.blockDim = dim3(kRowThreads);
-    cfg.stream = stream;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    snprintf(info, info_len, "scored attention dh=%d rows grid=%lldx%d", a.head_dim, (long long)blocks, a.num_seqs);
-    return cudaLaunchKernelEx(&cfg, a.head_dim == 128   ? scored_rows_kernel<128>
-                                    : a.head_dim == 256 ? scored_rows_kernel<256>
-                                                        : scored_rows_kernel<512>,
-                              p);
+    return launch_scored_rows(p, a.head_dim, a.workspace, stream, info, info_len);
 }
 
-cudaError_t init_scored_attributes() { return cudaSuccess; }
+cudaError_t init_scored_attributes() { return init_scored_rows_attributes(); }
 
 }  // namespace pa
