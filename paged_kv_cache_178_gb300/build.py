@@ -18,9 +18,11 @@ BUILD_DIR = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libpagedattn.so")
 SOURCES = ["pa_api.cu", "pa_attn.cu", "pa_attn512.cu", "pa_decode.cu", "pa_gather.cu",
            "pa_step.cu", "pa_quant.cu", "pa_attn_quant.cu", "pa_pages.cu", "pa_scored.cu",
-           "pa_scored_rows.cu"]
+           "pa_scored_rows.cu", "pa_scored_tiles.cu", "pa_scored_tiles128.cu", "pa_scored_tiles256.cu",
+           "pa_scored_tiles512.cu"]
 HEADERS = ["pa_internal.h", "pa_ptx.cuh", "pa_attn_common.cuh", "pa_split.cuh", "pa_scan.cuh",
-           "pa_quant_common.cuh", "pa_score.cuh", "pa_scored.h", os.path.join("..", "..", "include", "pagedattn.h")]
+           "pa_quant_common.cuh", "pa_score.cuh", "pa_scored.h",
+           "pa_scored_tiles.cuh", os.path.join("..", "..", "include", "pagedattn.h")]
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 # -fmad=false: no implicit FMA contraction, so the softmax/rescale order is

@@ -1528,18 +1528,18 @@ pa_status pa_compact_pages(const int32_t *context_lens, int32_t num_seqs, const 
 constexpr int kScoredMaxSeqs = 8192;
 
 static bool scored_sizes_ok(int32_t num_seqs, int32_t hq, int32_t hkv, int32_t dh, int32_t max_query_len,
-                            int32_t max_seq_len)
+                            int32_t max_seq_len, int64_t num_q_tokens)
 {
     return num_seqs > 0 && num_seqs <= kScoredMaxSeqs && hkv > 0 && hq > 0 && hq % hkv == 0 && hq / hkv <= 128 &&
            (dh == 128 || dh == 256 || dh == 512) && max_query_len > 0 && max_seq_len >= 0 &&
            max_seq_len <= INT32_MAX - 4096 && (int64_t)num_seqs * max_query_len * hq <= INT32_MAX &&
-           scored_supported(num_seqs, hq, hkv, dh, max_query_len, max_seq_len);
+           scored_supported(num_seqs, hq, hkv, dh, max_query_len, max_seq_len, num_q_tokens);
 }
 
 size_t pa_paged_attention_scored_workspace_size(int32_t num_seqs, int32_t num_q_heads, int32_t num_kv_heads,
                                                 int32_t head_dim, int32_t max_query_len, int32_t max_seq_len)
 {
-    if (!scored_sizes_ok(num_seqs, num_q_heads, num_kv_heads, head_dim, max_query_len, max_seq_len))
+    if (!scored_sizes_ok(num_seqs, num_q_heads, num_kv_heads, head_dim, max_query_len, max_seq_len, -1))
         return 0;
     return scored_workspace_bytes(num_seqs, num_q_heads, num_kv_heads, head_dim, max_query_len, max_seq_len);
 }
@@ -1579,7 +1579,7 @@ pa_status pa_paged_attention_scored(const void *q, int64_t num_q_tokens, int64_t
         return PA_ERR_INVALID_ARG;
     if (q_tok_stride < row || (q_tok_stride & 7) || max_blocks_per_seq == 0)
         return PA_ERR_INVALID_ARG;
-    if (!scored_sizes_ok(num_seqs, num_q_heads, hkv, dh, max_query_len, max_seq_len))
+    if (!scored_sizes_ok(num_seqs, num_q_heads, hkv, dh, max_query_len, max_seq_len, num_q_tokens))
         return PA_ERR_UNSUPPORTED;
     const size_t need = scored_workspace_bytes(num_seqs, num_q_heads, hkv, dh, max_query_len, max_seq_len);
     if (need > 0) {

@@ -241,8 +241,9 @@ struct ScoreRules {
     const float *slopes;
     const int32_t *prefix_lens, *first_keys;
 };
+// num_q_tokens < 0: not known
 bool scored_supported(int32_t num_seqs, int32_t hq, int32_t hkv, int32_t head_dim, int32_t max_query_len,
-                      int32_t max_seq_len);
+                      int32_t max_seq_len, int64_t num_q_tokens);
 size_t scored_workspace_bytes(int32_t num_seqs, int32_t hq, int32_t hkv, int32_t head_dim, int32_t max_query_len,
                               int32_t max_seq_len);
 cudaError_t launch_scored_attention(const AttnArgs &a, const ScoreRules &r, ErrState *err, cudaStream_t stream,

@@ -17,16 +17,29 @@ bool scored_pool_maps(const ScoreParams &p, int32_t head_dim, CUtensorMap (&tm)[
     return true;
 }
 
-bool scored_supported(int32_t num_seqs, int32_t hq, int32_t hkv, int32_t head_dim, int32_t max_query_len,
-                      int32_t max_seq_len)
+// Few rows a request go to the kernel whose work follows the bytes, others to
+// the one that fills tensor-memory tiles.
+static bool few_rows(int32_t num_seqs, int32_t hkv, int group, int32_t head_dim, int32_t max_query_len, int32_t max_seq_len)
 {
-    return scored_rows_fits(num_seqs, hkv, hq / hkv, head_dim, max_query_len, max_seq_len);
+    return (int64_t)max_query_len * group <= 32 &&
+           scored_rows_fits(num_seqs, hkv, group, head_dim, max_query_len, max_seq_len);
+}
+
+bool scored_supported(int32_t num_seqs, int32_t hq, int32_t hkv, int32_t head_dim, int32_t max_query_len,
+                      int32_t max_seq_len, int64_t num_q_tokens)
+{
+    const int group = hq / hkv;
+    return few_rows(num_seqs, hkv, group, head_dim, max_query_len, max_seq_len) ||
+           scored_tiles_fits(num_seqs, hkv, group, head_dim, max_query_len, max_seq_len, num_q_tokens);
 }
 
 size_t scored_workspace_bytes(int32_t num_seqs, int32_t hq, int32_t hkv, int32_t head_dim, int32_t max_query_len,
                               int32_t max_seq_len)
 {
-    return scored_rows_bytes(num_seqs, hkv, hq / hkv, head_dim, max_query_len, max_seq_len);
+    const int group = hq / hkv;
+    return few_rows(num_seqs, hkv, group, head_dim, max_query_len, max_seq_len)
+               ? scored_rows_bytes(num_seqs, hkv, group, head_dim, max_query_len, max_seq_len)
+               : scored_tiles_bytes(num_seqs, hkv, group, head_dim, max_query_len);
 }
 
 static ScoreParams score_params(const AttnArgs &a, const ScoreRules &r, ErrState *err)
@@ -67,9 +80,15 @@ cudaError_t launch_scored_attention(const AttnArgs &a, const ScoreRules &r, ErrS
                                     char *info, size_t info_len)
 {
     const ScoreParams p = score_params(a, r, err);
-    return launch_scored_rows(p, a.head_dim, a.workspace, stream, info, info_len);
+    return few_rows(p.num_seqs, p.hkv, p.group, a.head_dim, p.max_query_len, p.max_seq_len)
+               ? launch_scored_rows(p, a.head_dim, a.workspace, stream, info, info_len)
+               : launch_scored_tiles(p, a.head_dim, a.workspace, stream, info, info_len);
 }
 
-cudaError_t init_scored_attributes() { return init_scored_rows_attributes(); }
+cudaError_t init_scored_attributes()
+{
+    const cudaError_t e = init_scored_rows_attributes();
+    return e == cudaSuccess ? init_scored_tiles_attributes() : e;
+}
 
 }  // namespace pa

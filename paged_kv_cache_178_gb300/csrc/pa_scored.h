@@ -1,5 +1,5 @@
 // Between the parts of pa_paged_attention_scored: the choice of a kernel
-// (pa_scored.cu), few rows (pa_scored_rows.cu).
+// (pa_scored.cu), few rows (pa_scored_rows.cu), many rows (pa_scored_tiles*.cu).
 #pragma once
 #include "pa_score.cuh"
 
@@ -11,6 +11,61 @@ constexpr int kScoredMaxTilesHost = 8192;    // requests times tiles of rows tha
 // Tensor maps of K and V: boxes of 64 columns by the 16 tokens of one page and head.
 bool scored_pool_maps(const ScoreParams &p, int32_t head_dim, CUtensorMap (&tm)[2]);
 
+// Keys that a tile of rows sees: a prefix and one range (a hull: keys inside
+// it may be hidden from every row).
+struct TileView {
+    int prefix, lo, hi;  // [0, prefix) and [lo, hi); hi <= lo: no range
+};
+
+// rows [r0, r1) of a request (row = token * group + head)
+__device__ __forceinline__ TileView tile_view(const ScoreParams &p, int b, const ReqMeta &m, int r0, int r1)
+{
+    TileView v{0, 0, 0};
+    if (r0 >= r1)
+        return v;
+    v.prefix = score_prefix(p, b, m.L);
+    const int t0 = r0 / p.group, t1 = (r1 - 1) / p.group;
+    const int base = m.L - m.qn;
+    v.lo = INT32_MAX;
+    v.hi = 0;
+    if (!p.first_keys) {
+        v.lo = score_low(p, 0, base + t0);  // later tokens' ranges start no earlier
+        v.hi = base + t1 + 1;
+    } else {
+        for (int t = t0; t <= t1; ++t) {
+            const int pos = base + t, lo = score_low(p, (int64_t)m.qs + t, pos);
+            if (lo <= pos) {
+                v.lo = min(v.lo, lo);
+                v.hi = pos + 1;
+            }
+        }
+    }
+    return v;
+}
+
+// Blocks of `keys` keys that hold what a tile sees: the prefix's np first ones,
+// then those from b0 on; `count` in all.
+struct TileBlocks {
+    int np, b0, count;
+};
+
+__device__ __forceinline__ TileBlocks tile_blocks(const TileView &v, int keys)
+{
+    TileBlocks t;
+    t.np = (v.prefix + keys - 1) / keys;
+    t.b0 = t.np;
+    int n = 0;
+    if (v.hi > v.lo) {
+        t.b0 = max(v.lo / keys, t.np);
+        n = max((v.hi + keys - 1) / keys - t.b0, 0);
+    }
+    t.count = t.np + n;
+    return t;
+}
+
+// First item of CTA c's range.
+__device__ __forceinline__ int64_t range_lo(int64_t total, int c, int ctas) { return total * c / ctas; }
+
 bool scored_rows_fits(int32_t num_seqs, int32_t hkv, int group, int32_t head_dim, int32_t max_query_len,
                       int32_t max_seq_len);
 size_t scored_rows_bytes(int32_t num_seqs, int32_t hkv, int group, int32_t head_dim, int32_t max_query_len,
@@ -18,5 +73,16 @@ size_t scored_rows_bytes(int32_t num_seqs, int32_t hkv, int group, int32_t head_
 cudaError_t launch_scored_rows(const ScoreParams &p, int32_t head_dim, void *workspace, cudaStream_t stream, char *info,
                                size_t info_len);
 cudaError_t init_scored_rows_attributes();
+
+// Row tiles that the batch can form (num_q_tokens < 0: by the other bounds
+// alone), and whether the kernels take that many.
+constexpr int kScoredMaxEntriesHost = 24000;  // requests and row tiles that a CTA sums over
+int64_t scored_tiles_bound(int32_t num_seqs, int group, int32_t head_dim, int32_t max_query_len, int64_t num_q_tokens);
+bool scored_tiles_fits(int32_t num_seqs, int32_t hkv, int group, int32_t head_dim, int32_t max_query_len,
+                       int32_t max_seq_len, int64_t num_q_tokens);
+size_t scored_tiles_bytes(int32_t num_seqs, int32_t hkv, int group, int32_t head_dim, int32_t max_query_len);
+cudaError_t launch_scored_tiles(const ScoreParams &p, int32_t head_dim, void *workspace, cudaStream_t stream, char *info,
+                                size_t info_len);
+cudaError_t init_scored_tiles_attributes();
 
 }  // namespace pa

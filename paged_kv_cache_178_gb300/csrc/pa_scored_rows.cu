@@ -71,61 +71,6 @@ __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], 
                  : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-// Keys that a tile of rows sees: a prefix and one range (a hull: keys inside
-// it may be hidden from every row).
-struct TileView {
-    int prefix, lo, hi;  // [0, prefix) and [lo, hi); hi <= lo: no range
-};
-
-// rows [r0, r1) of a request (row = token * group + head)
-__device__ __forceinline__ TileView tile_view(const ScoreParams &p, int b, const ReqMeta &m, int r0, int r1)
-{
-    TileView v{0, 0, 0};
-    if (r0 >= r1)
-        return v;
-    v.prefix = score_prefix(p, b, m.L);
-    const int t0 = r0 / p.group, t1 = (r1 - 1) / p.group;
-    const int base = m.L - m.qn;
-    v.lo = INT32_MAX;
-    v.hi = 0;
-    if (!p.first_keys) {
-        v.lo = score_low(p, 0, base + t0);  // later tokens' ranges start no earlier
-        v.hi = base + t1 + 1;
-    } else {
-        for (int t = t0; t <= t1; ++t) {
-            const int pos = base + t, lo = score_low(p, (int64_t)m.qs + t, pos);
-            if (lo <= pos) {
-                v.lo = min(v.lo, lo);
-                v.hi = pos + 1;
-            }
-        }
-    }
-    return v;
-}
-
-// Blocks of `keys` keys that hold what a tile sees: the prefix's np first ones,
-// then those from b0 on; `count` in all.
-struct TileBlocks {
-    int np, b0, count;
-};
-
-__device__ __forceinline__ TileBlocks tile_blocks(const TileView &v, int keys)
-{
-    TileBlocks t;
-    t.np = (v.prefix + keys - 1) / keys;
-    t.b0 = t.np;
-    int n = 0;
-    if (v.hi > v.lo) {
-        t.b0 = max(v.lo / keys, t.np);
-        n = max((v.hi + keys - 1) / keys - t.b0, 0);
-    }
-    t.count = t.np + n;
-    return t;
-}
-
-// First item of CTA c's range.
-__device__ __forceinline__ int64_t range_lo(int64_t total, int c, int ctas) { return total * c / ctas; }
-
 // Workspace: the items before each group and its own, then the records.
 struct RowsWork {
     int2 *groups;      // [num_groups] (first item, items)

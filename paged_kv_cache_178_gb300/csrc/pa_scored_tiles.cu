@@ -1,0 +1,116 @@
+// pa_paged_attention_scored for many rows: the host's part.
+#include <cstdio>
+
+#include "pa_scored_tiles.cuh"
+
+namespace pa {
+
+extern template cudaError_t launch_tiles<128, 2>(const ScoreParams &, const CUtensorMap (&)[2], const TileWork &, int, cudaStream_t);
+extern template cudaError_t launch_tiles<128, 1>(const ScoreParams &, const CUtensorMap (&)[2], const TileWork &, int, cudaStream_t);
+extern template cudaError_t launch_tiles<256, 1>(const ScoreParams &, const CUtensorMap (&)[2], const TileWork &, int, cudaStream_t);
+extern template cudaError_t launch_tiles<512, 1>(const ScoreParams &, const CUtensorMap (&)[2], const TileWork &, int, cudaStream_t);
+extern template cudaError_t tiles_attributes<128, 2>();
+extern template cudaError_t tiles_attributes<128, 1>();
+extern template cudaError_t tiles_attributes<256, 1>();
+extern template cudaError_t tiles_attributes<512, 1>();
+
+// Two row tiles of 128 share their keys where a request can fill them (head
+// dim 128: tensor memory has room for both outputs).
+static int row_tiles(int group, int32_t head_dim, int32_t max_query_len)
+{
+    return head_dim == 128 && (int64_t)max_query_len * group > 128 ? 2 : 1;
+}
+
+int64_t scored_tiles_bound(int32_t num_seqs, int group, int32_t head_dim, int32_t max_query_len, int64_t num_q_tokens)
+{
+    const int rows = 128 * row_tiles(group, head_dim, max_query_len);
+    const int64_t by_len = num_seqs * (((int64_t)max_query_len * group + rows - 1) / rows);
+    if (num_q_tokens < 0)
+        return by_len;
+    const int64_t by_tokens = num_q_tokens * group / rows + num_seqs;
+    return by_len < by_tokens ? by_len : by_tokens;
+}
+
+bool scored_tiles_fits(int32_t num_seqs, int32_t hkv, int group, int32_t head_dim, int32_t max_query_len,
+                       int32_t max_seq_len, int64_t num_q_tokens)
+{
+    if (num_q_tokens < 0)
+        return true;  // (a workspace's size: the call itself is refused)
+    const int64_t tiles = scored_tiles_bound(num_seqs, group, head_dim, max_query_len, num_q_tokens);
+    return num_seqs + tiles + 2 <= kScoredMaxEntriesHost &&
+           tiles * hkv * 2 * (((int64_t)max_seq_len + kTileKeys - 1) / kTileKeys + 1) <= INT32_MAX;
+}
+
+static size_t align256(size_t n) { return (n + 255) / 256 * 256; }
+
+struct TileSizes {
+    int nt, parts;
+    int64_t tiles, record_floats;
+    size_t groups, entries, records, bytes;  // offsets, and the whole
+};
+
+static TileSizes tile_sizes(int64_t tiles, int32_t hkv, int group, int32_t head_dim, int32_t max_query_len)
+{
+    TileSizes s{};
+    s.nt = row_tiles(group, head_dim, max_query_len);
+    s.parts = head_dim == 512 ? 2 : 1;
+    s.tiles = tiles;
+    s.record_floats = s.nt * tile_record(head_dim / s.parts);
+    s.groups = 256;
+    s.entries = s.groups + align256((size_t)tiles * hkv * s.parts * 8);
+    s.records = s.entries + align256((size_t)tiles * 8);
+    s.bytes = s.records + (size_t)2 * kScoredSms * s.record_floats * 4;
+    return s;
+}
+
+size_t scored_tiles_bytes(int32_t num_seqs, int32_t hkv, int group, int32_t head_dim, int32_t max_query_len)
+{
+    int64_t tiles = scored_tiles_bound(num_seqs, group, head_dim, max_query_len, -1);
+    if (tiles > kScoredMaxEntriesHost)
+        tiles = kScoredMaxEntriesHost;
+    return tile_sizes(tiles, hkv, group, head_dim, max_query_len).bytes;
+}
+
+cudaError_t launch_scored_tiles(const ScoreParams &p, int32_t head_dim, void *workspace, cudaStream_t stream, char *info,
+                                size_t info_len)
+{
+    CUtensorMap tm[2];
+    if (!scored_pool_maps(p, head_dim, tm))
+        return cudaErrorInvalidValue;
+    const TileSizes s = tile_sizes(scored_tiles_bound(p.num_seqs, p.group, head_dim, p.max_query_len, p.num_q_tokens), p.hkv,
+                                   p.group, head_dim, p.max_query_len);
+    TileWork w{};
+    uint8_t *ws = static_cast<uint8_t *>(workspace);
+    w.header = reinterpret_cast<int64_t *>(ws);
+    w.groups = reinterpret_cast<int2 *>(ws + s.groups);
+    w.entries = reinterpret_cast<int2 *>(ws + s.entries);
+    w.records = reinterpret_cast<float *>(ws + s.records);
+    w.record_floats = s.record_floats;
+    const int64_t items = s.tiles * p.hkv * s.parts * (((int64_t)p.max_seq_len + kTileKeys - 1) / kTileKeys + 1);
+    w.ctas = (int32_t)(items < kScoredSms ? items : kScoredSms);
+    w.max_tiles = (int32_t)s.tiles;
+    // Without a maximum the exponents stay within the cap: 2^80 times any number
+    // of keys and values up to 2^20 is far from overflow (and a row that overflows
+    // all the same is computed again key by key).
+    const int mode = p.slopes                              ? kModeAny
+                     : p.cap_log2 > 0.f                    ? (p.cap_log2 <= 80.f ? kModeCapped : kModeAny)
+                                                           : kModePlain;
+    snprintf(info, info_len, "scored attention dh=%d kernel=tiles-m%d mode=%d grid=%d tiles=%lld", head_dim, 128 * s.nt, mode,
+             w.ctas, (long long)s.tiles);
+    switch (head_dim) {
+    case 128: return s.nt == 2 ? launch_tiles<128, 2>(p, tm, w, mode, stream) : launch_tiles<128, 1>(p, tm, w, mode, stream);
+    case 256: return launch_tiles<256, 1>(p, tm, w, mode, stream);
+    default: return launch_tiles<512, 1>(p, tm, w, mode, stream);
+    }
+}
+
+cudaError_t init_scored_tiles_attributes()
+{
+    cudaError_t e;
+    if ((e = tiles_attributes<128, 2>()) != cudaSuccess || (e = tiles_attributes<128, 1>()) != cudaSuccess ||
+        (e = tiles_attributes<256, 1>()) != cudaSuccess)
+        return e;
+    return tiles_attributes<512, 1>();
+}
+
+}  // namespace pa

@@ -1,0 +1,903 @@
+// pa_paged_attention_scored for many rows: prompts and chunks of them, on tcgen05.
+//
+// A group is one (request, KV head, NT tiles of 128 rows); row r of a group is
+// query head r % G of query token r / G, so the heads that share a KV head share
+// its tiles.  The items of a group are the tiles of 128 keys that some row sees;
+// the items of all groups are dealt out as one wave of equal contiguous ranges, a
+// CTA to an SM.  (A causal prompt's groups differ by a factor of its tiles:
+// 4096 tokens of 8 and 2 heads are 128 groups of 1 to 32 items, 16.5 on
+// average, and a group to a CTA would leave the time at the longest one's.)  A
+// group that lies wholly in a range goes straight to the output; a part of one
+// becomes a record (maximum, sum, unnormalised output), folded by a second kernel.
+//
+// Two score buffers in tensor memory keep the tensor pipe busy: with two row
+// tiles (head dim 128) each has its own, and the softmax of one runs beside the
+// products of the other; with one (head dims 256 and 512, or few rows) the key
+// tiles take them in turn.  The order on the pipe is QK(0), QK(1), then PV(i),
+// QK(i+2): probabilities overwrite their scores in tensor memory, and products
+// issued by one thread run in order.
+//   warp 0      copies units of 128 keys by 128 columns (32 KB, a TMA box for each
+//               page and 64 columns) into a ring, in the order of their use
+//   warp 1      issues the products (one thread)
+//   warps 4-7, 8-11   softmax of one score buffer each, a row to a thread; Q
+//               into shared memory at a group's start, the output at its end
+// Head dim 512: the output's halves are two groups, each with all of the scores
+// (tensor memory holds 256 columns of output beside the scores): three halves of
+// the products of a whole one instead of two, and no exchange.
+#pragma once
+#include "pa_scan.cuh"
+#include "pa_scored.h"
+
+namespace pa {
+
+constexpr int kTileThreads = 384;
+constexpr int kTileKeys = 128;
+constexpr int kUnitBytes = kTileKeys * 256;  // 128 keys by 128 columns
+
+// How a score becomes an exponent.
+enum ScoreMode : int {
+    kModePlain = 0,   // scaled
+    kModeCapped = 1,  // capped, and the cap small enough to need no running maximum
+    kModeAny = 2,     // capped or not, with a bias
+};
+
+template <int DH, int NT>
+struct TileCfg {
+    static constexpr int kSplit = DH == 512 ? 2 : 1;  // groups that share a row tile's columns
+    static constexpr int kUnitsK = DH / 128, kUnitsV = DH / 128 / kSplit;
+    static constexpr int kCols = DH / kSplit;         // output columns of a group
+    static constexpr int kQBytes = NT * 128 * DH * 2;
+    static constexpr int kStages = (224 * 1024 - kQBytes) / kUnitBytes;
+    static constexpr int kOCol = 256;                 // tensor-memory column of the output
+    static_assert(NT * kCols <= 256 && kStages >= 3, "tensor and shared memory");
+};
+
+struct TileWork {
+    int64_t *header;   // items of all groups; row tiles of all requests
+    int2 *groups;      // [row tiles * heads * parts] (first item, items)
+    int2 *entries;     // [row tiles] (request, row tile of it)
+    float *records;    // [2 * ctas] of record_floats
+    int64_t record_floats;
+    int32_t ctas, max_tiles;
+};
+
+// Floats of one row tile's record: m[128], l[128], then the output as [columns / 4][128 rows][4].
+constexpr int64_t tile_record(int cols) { return 256 + (int64_t)cols * 128; }
+
+constexpr int kTileSmall = 2048;  // barriers, flags, row exchange
+
+template <int DH, int NT>
+constexpr size_t tiles_smem()
+{
+    using C = TileCfg<DH, NT>;
+    return 1024 + (size_t)C::kQBytes + (size_t)C::kStages * kUnitBytes + kTileSmall;
+}
+
+__device__ __forceinline__ uint64_t mul_f32x2(uint64_t a, uint64_t b)
+{
+    uint64_t d;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+
+// Row tiles of NT * 128 rows that a request's tokens form.
+__device__ __forceinline__ int group_tiles(const ScoreParams &p, const ReqMeta &m, int rows)
+{
+    return m.ok ? (int)(((int64_t)m.qn * p.group + rows - 1) / rows) : 0;
+}
+
+// tile_view of rows [r0, r1) by a whole warp.
+__device__ __forceinline__ TileView warp_tile_view(const ScoreParams &p, int b, const ReqMeta &m, int r0, int r1)
+{
+    TileView v{0, 0, 0};
+    if (r0 >= r1)
+        return v;
+    v.prefix = score_prefix(p, b, m.L);
+    const int t0 = r0 / p.group, t1 = (r1 - 1) / p.group, base = m.L - m.qn;
+    if (!p.first_keys) {
+        v.lo = score_low(p, 0, base + t0);
+        v.hi = base + t1 + 1;
+        return v;
+    }
+    int lo = INT32_MAX, hi = 0;
+    for (int t = t0 + (int)(threadIdx.x % 32); t <= t1; t += 32) {
+        const int pos = base + t, l = score_low(p, (int64_t)m.qs + t, pos);
+        if (l <= pos) {
+            lo = min(lo, l);
+            hi = pos + 1;
+        }
+    }
+    v.lo = __reduce_min_sync(0xffffffffu, lo);
+    v.hi = __reduce_max_sync(0xffffffffu, hi);
+    return v;
+}
+
+// One group's part in a CTA's range, as every role walks through it.
+struct TileGroup {
+    int b, tile, hv;    // request, row tile, (KV head, part of the columns)
+    int64_t g0;         // first item
+    int n;              // items
+    ReqMeta m;
+    TileView v;
+    TileBlocks t;
+};
+
+template <int DH, int NT>
+__device__ __forceinline__ void load_group(const ScoreParams &p, TileGroup &x)
+{
+    constexpr int RT = NT * 128;
+    x.m = score_meta(p, x.b);
+    const int rows = x.m.qn * p.group;
+    x.v = warp_tile_view(p, x.b, x.m, min(x.tile * RT, rows), min(x.tile * RT + RT, rows));
+    x.t = tile_blocks(x.v, kTileKeys);
+    x.n = x.t.count;
+}
+
+// The next group with items (there is one: the range goes on).
+template <int DH, int NT>
+__device__ __forceinline__ void next_group(const ScoreParams &p, TileGroup &x, int heads)
+{
+    x.g0 += x.n;
+    if (++x.hv < heads)
+        return;
+    x.hv = 0;
+    do {
+        ++x.tile;
+        while (x.b < p.num_seqs && x.tile >= group_tiles(p, x.m, NT * 128)) {
+            x.tile = 0;
+            if (++x.b < p.num_seqs)
+                x.m = score_meta(p, x.b);
+        }
+        if (x.b >= p.num_seqs)
+            return;
+        load_group<DH, NT>(p, x);
+    } while (x.n == 0);
+}
+
+// Whether a tile of 16 keys at k0 holds one that the group sees.
+__device__ __forceinline__ bool page_seen(const TileView &v, int k0)
+{
+    return k0 < v.prefix || (k0 < v.hi && k0 + 16 > v.lo);
+}
+
+__device__ __forceinline__ int tile_key(const TileBlocks &t, int i)
+{
+    return (i < t.np ? i : t.b0 + i - t.np) * kTileKeys;
+}
+
+// First V row of the tile at k0 that holds no token of the request (128: none
+// that is loaded): rows past the length may hold anything.
+__device__ __forceinline__ int stale_row(const TileGroup &x, int k0)
+{
+    const int page = x.m.L / 16 * 16;  // the request's partial page
+    return x.m.L % 16 && page >= k0 && page < k0 + kTileKeys && page_seen(x.v, page) ? x.m.L - k0 : kTileKeys;
+}
+
+template <int DH, int NT, int MODE>
+__global__ void __launch_bounds__(kTileThreads, 1)
+    scored_tiles_kernel(const __grid_constant__ ScoreParams p, const __grid_constant__ CUtensorMap tm_k,
+                        const __grid_constant__ CUtensorMap tm_v, const TileWork w)
+{
+    using C = TileCfg<DH, NT>;
+    constexpr int RT = NT * 128, NS = C::kStages, UK = C::kUnitsK, UV = C::kUnitsV;
+    constexpr int COLS_W = NT == 2 ? 128 : C::kCols / 2;  // output columns that a softmax group reads
+    constexpr uint32_t ID_QK = idesc_bf16_f32(128, kTileKeys, false), ID_PV = idesc_bf16_f32(128, 128, true);
+    enum { B_FULL = 0, B_EMPTY = NS, B_S = 2 * NS, B_P = B_S + 2, B_M = B_P + 2, B_PV = B_M + 2, B_Q, B_O, B_DONE, B_Z, NBARS = B_Z + NS };
+    static_assert(NBARS * 8 <= 256, "barriers");
+    static_assert(tiles_smem<DH, NT>() <= kMaxSmemPerBlock, "shared-memory layout");
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
+    uint8_t *s_q = smem;                       // [NT][DH/64][128 rows][128 bytes]
+    uint8_t *s_ring = s_q + C::kQBytes;        // [NS][2][128 keys][128 bytes]
+    uint8_t *small = s_ring + NS * kUnitBytes;
+    uint64_t *bars = reinterpret_cast<uint64_t *>(small);
+    volatile int *s_flags = reinterpret_cast<volatile int *>(small + 256);  // [0] abort [1] tmem [2] bad [4..8) start
+    float *s_m = reinterpret_cast<float *>(small + 512);                    // [128] the shared running maximum
+    float *s_l = s_m + 128;                                                 // [2][128] the two halves' sums
+    volatile int *abort_flag = s_flags;
+    const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
+    auto bar = [&](int i) { return smem_addr(&bars[i]); };
+    auto wait = [&](int i, uint32_t parity) { return wait_bar(bar(i), parity & 1u, abort_flag, p.err, i); };
+    if (tid == 0) {
+        for (int i = 0; i < 2 * NS; ++i)
+            mbar_init(bar(i), 1);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(bar(B_S + i), 1);
+            mbar_init(bar(B_P + i), 4);
+            mbar_init(bar(B_M + i), 4);
+        }
+        mbar_init(bar(B_PV), 1);
+        mbar_init(bar(B_Q), 8);
+        mbar_init(bar(B_O), 2);
+        mbar_init(bar(B_DONE), 1);
+        for (int i = 0; i < NS; ++i)
+            mbar_init(bar(B_Z + i), 1);
+        s_flags[0] = s_flags[2] = 0;
+        fence_barrier_init();
+    }
+    griddep_wait();
+    griddep_launch_dependents();
+
+    // --------------------------------------- items before each row tile ----
+    // (in the ring, which is not in use yet; the roles then walk on from the
+    // range's first group by themselves)
+    const int heads = p.hkv * C::kSplit, ctas = w.ctas, c = blockIdx.x;
+    int32_t *s_first = reinterpret_cast<int32_t *>(s_ring);  // [num_seqs + 1] first row tile of a request
+    int32_t *s_off = s_first + p.num_seqs + 1;               // [row tiles + 1] first item of a row tile (of one head)
+    long long *scratch = reinterpret_cast<long long *>(small + 512);
+    const long long tiles = block_exclusive_sums<kTileThreads>(p.num_seqs, s_first, scratch, [&](int b) {
+        const ReqMeta m = score_meta(p, b);
+        if (!m.ok && c == 0)
+            record_error(p.err, kErrBadMetadata, b);
+        return group_tiles(p, m, RT);
+    });
+    // (the host's bound holds for requests that do not overlap; a query_start_loc
+    // that decreases may give more: those rows are left out, its request is named)
+    const int ntiles = (int)(tiles < w.max_tiles ? tiles : w.max_tiles);
+    const long long per_head = block_exclusive_sums<kTileThreads>(ntiles, s_off, scratch, [&](int e) {
+        const int b = owner_of(s_first, p.num_seqs, e), tile = e - s_first[b];
+        const ReqMeta m = score_meta(p, b);
+        const int rows = m.qn * p.group;
+        return tile_blocks(tile_view(p, b, m, min(tile * RT, rows), min(tile * RT + RT, rows)), kTileKeys).count;
+    });
+    const int64_t total = per_head * heads;
+    for (int g = c * kTileThreads + tid; g < ntiles * heads; g += ctas * kTileThreads) {
+        const int e = g / heads, n = s_off[e + 1] - s_off[e];
+        w.groups[g] = make_int2(s_off[e] * heads + (g - e * heads) * n, n);
+    }
+    for (int e = c * kTileThreads + tid; e < ntiles; e += ctas * kTileThreads) {
+        const int b = owner_of(s_first, p.num_seqs, e);
+        w.entries[e] = make_int2(b, e - s_first[b]);
+    }
+    if (c == 0 && tid == 0) {
+        w.header[0] = total;
+        w.header[1] = ntiles;
+    }
+    for (int b = c; b < p.num_seqs; b += ctas) {
+        const ReqMeta m = score_meta(p, b);
+        if (!m.ok && m.sane) {
+            const int64_t first = (int64_t)m.qs * p.hq, n = (int64_t)m.qn * p.hq;
+            for (int64_t i = tid; i < n * DH; i += kTileThreads)
+                p.out[first * DH + i] = __ushort_as_bfloat16(0x7FC0);
+            if (p.lse)
+                for (int64_t i = tid; i < n; i += kTileThreads)
+                    p.lse[first + i] = __int_as_float(0x7FC00000);
+        }
+    }
+    const int64_t lo = range_lo(total, c, ctas), hi = range_lo(total, c + 1, ctas);
+    if (lo >= hi)
+        return;
+    if (tid == 0) {
+        const int e = owner_of(s_off, ntiles, (int)div_floor(lo, heads));
+        const int b = owner_of(s_first, p.num_seqs, e);
+        s_flags[4] = b;
+        s_flags[5] = e - s_first[b];
+        s_flags[6] = s_off[e];
+    }
+    if (warp == 1) {
+        tmem_alloc(smem_addr(const_cast<int *>(&s_flags[1])), 512);
+        tmem_relinquish();
+    }
+    fence_proxy_async_smem();  // the sums have been read: copies may land on them
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = (uint32_t)s_flags[1];
+    TileGroup x;
+    x.b = s_flags[4];
+    x.tile = s_flags[5];
+    load_group<DH, NT>(p, x);
+    {
+        const int64_t first = (int64_t)s_flags[6] * heads;
+        x.hv = (int)((lo - first) / x.n);
+        x.g0 = first + (int64_t)x.hv * x.n;
+    }
+    // position in the ring, within a segment of n tiles, of K or V of tile j
+    auto pos_k = [&](int j) { return NT == 2 ? j * (UK + UV) : (j == 0 ? 0 : UK + (j - 1) * (UK + UV)); };
+    auto pos_v = [&](int j, int n) {
+        return NT == 2 ? j * (UK + UV) + UK : UK + j * (UK + UV) + (j + 1 < n ? UK : 0);
+    };
+    bool ok = true;
+    uint32_t seg = 0;  // segments so far
+    if (warp == 0) {
+        // -------------------------------------------------------- producer --
+        uint32_t pos = 0;  // units so far
+        const int pg = lane % 8, cb = (lane / 8) % 2;
+        auto ids_of = [&](int j) {
+            const int k0 = tile_key(x.t, j) + pg * 16;
+            return page_seen(x.v, k0) ? __ldg(p.block_tables + (int64_t)x.b * p.max_blocks + k0 / 16) : -1;
+        };
+        auto load = [&](const CUtensorMap *map, int units, int col0, int id) {
+            for (int u = 0; ok && u < units; ++u, ++pos) {
+                const int stage = pos % NS;
+                if (pos >= NS)
+                    ok = __all_sync(0xffffffffu, wait(B_EMPTY + stage, pos / NS - 1));
+                if (!ok)
+                    return;
+                if (lane == 0)
+                    mbar_arrive_expect_tx(bar(B_FULL + stage), kUnitBytes);
+                __syncwarp();
+                // (block -1 lies outside the pool: zeros, no bytes read)
+                if (lane < 16)
+                    tma_load_4d(smem_addr(s_ring + stage * kUnitBytes + cb * 16384 + pg * 2048), map, bar(B_FULL + stage),
+                                col0 + u * 128 + cb * 64, x.hv / C::kSplit, 0, id);
+            }
+        };
+        for (int64_t item = lo; ok && item < hi; item < hi ? next_group<DH, NT>(p, x, heads) : (void)0) {
+            const int j0 = (int)(item - x.g0), n = (int)(min(hi, x.g0 + x.n) - item);
+            item += n;
+            const int v_col = x.hv % C::kSplit * C::kCols;
+            auto check = [&](int raw, int j) {
+                const bool bad = page_seen(x.v, tile_key(x.t, j) + pg * 16) && (raw < 0 || (int64_t)raw >= p.num_blocks);
+                if (__any_sync(0xffffffffu, bad)) {
+                    if (lane == 0) {
+                        record_error(p.err, kErrBadMetadata, x.b);
+                        s_flags[2] = 1;  // every row is then computed key by key
+                    }
+                    __syncwarp();
+                }
+                return bad ? -1 : raw;
+            };
+            int cur = check(ids_of(j0), j0), ahead = n > 1 ? ids_of(j0 + 1) : -1;
+            load(&tm_k, UK, 0, cur);
+            for (int j = 0; ok && j < n; ++j) {
+                const int id = cur;
+                if (j + 1 < n) {
+                    cur = check(ahead, j0 + j + 1);
+                    ahead = j + 2 < n ? ids_of(j0 + j + 2) : -1;
+                }
+                if (NT == 2)
+                    load(&tm_v, UV, v_col, id);
+                if (j + 1 < n)
+                    load(&tm_k, UK, 0, cur);
+                if (NT == 1)
+                    load(&tm_v, UV, v_col, id);
+            }
+            // V rows past the request's length (in its last tile) become zeros
+            const int k_last = tile_key(x.t, j0 + n - 1), row0 = stale_row(x, k_last);
+            if (ok && row0 < kTileKeys) {
+                for (int u = 0; ok && u < UV; ++u) {
+                    const uint32_t at = pos - UV + u;
+                    ok = __all_sync(0xffffffffu, wait(B_FULL + at % NS, at / NS));
+                    if (!ok)
+                        break;
+                    uint8_t *v = s_ring + at % NS * kUnitBytes;
+                    for (int i = lane; i < (16 - x.m.L % 16) * 16; i += 32)
+                        *reinterpret_cast<uint4 *>(v + (i % 16 / 8) * 16384 + (row0 + i / 16) * 128 + (i % 8) * 16) =
+                            make_uint4(0u, 0u, 0u, 0u);
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0)
+                        mbar_arrive(bar(B_Z + at % NS));
+                }
+            }
+        }
+        // after a timeout: no copy may land in memory that the CTA has left
+        if (!ok && lane == 0)
+            for (uint32_t i = pos > NS ? pos - NS : 0; i < pos; ++i)
+                wait_bar_drain(bar(B_FULL + i % NS), (i / NS) & 1u);
+    } else if (warp == 1) {
+        // -------------------------------------------------------- products --
+        uint32_t base = 0;               // units before the segment
+        uint32_t p_seen[2] = {0, 0};     // probabilities consumed of each buffer
+        uint32_t zeroed = 0;             // a bit per stage: the phase of its B_Z
+        for (int64_t item = lo; ok && item < hi; item < hi ? next_group<DH, NT>(p, x, heads) : (void)0, ++seg) {
+            const int j0 = (int)(item - x.g0), n = (int)(min(hi, x.g0 + x.n) - item), ni = n * NT;
+            item += n;
+            const bool zero = stale_row(x, tile_key(x.t, j0 + n - 1)) < kTileKeys;
+            auto qk = [&](int i) {
+                const int t = NT == 2 ? i % 2 : 0, j = i / NT;
+                for (int u = 0; ok && u < UK; ++u) {
+                    const uint32_t at = base + pos_k(j) + u, stage = at % NS;
+                    ok = wait(B_FULL + stage, at / NS);
+                    if (!ok)
+                        return;
+                    const uint64_t qd = sdesc_sw128(smem_addr(s_q + t * 128 * DH * 2 + u * 32768), 16, 1024);
+                    const uint64_t kd = sdesc_sw128(smem_addr(s_ring + stage * kUnitBytes), 16, 1024);
+                    uint64_t a[8], b[8];
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) {
+                        const uint64_t step = (uint64_t)(((k / 4) * 16384 + (k % 4) * 32) >> 4);
+                        a[k] = qd + step;
+                        b[k] = kd + step;
+                    }
+                    tc_fence_after();
+                    mma8_ss<1>(tmem + (uint32_t)(i % 2) * 128u, a, b, ID_QK, u > 0);
+                    if (t == NT - 1)
+                        mma_commit(bar(B_EMPTY + stage));
+                }
+                mma_commit(bar(B_S + i % 2));
+            };
+            auto pv = [&](int i) {
+                const int t = NT == 2 ? i % 2 : 0, j = i / NT;
+                ok = wait(B_P + i % 2, p_seen[i % 2]);
+                ++p_seen[i % 2];
+                for (int u = 0; ok && u < UV; ++u) {
+                    const uint32_t at = base + pos_v(j, n) + u, stage = at % NS;
+                    ok = wait(B_FULL + stage, at / NS);
+                    if (ok && zero && j == n - 1 && t == 0) {
+                        ok = wait(B_Z + stage, zeroed >> stage);
+                        zeroed ^= 1u << stage;
+                    }
+                    if (!ok)
+                        return;
+                    const uint64_t vd = sdesc_sw128(smem_addr(s_ring + stage * kUnitBytes), 16384, 1024);
+                    uint32_t a[8];
+                    uint64_t b[8];
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) {
+                        a[k] = tmem + (uint32_t)(i % 2) * 128u + (uint32_t)k * 8u;
+                        b[k] = vd + (uint64_t)((k * 2048) >> 4);
+                    }
+                    tc_fence_after();
+                    mma8_ts<1>(tmem + (uint32_t)(C::kOCol + (t + u) * 128), a, b, ID_PV, j > 0);
+                    if (t == NT - 1)
+                        mma_commit(bar(B_EMPTY + stage));
+                }
+                if (NT == 1 && MODE != kModeCapped)
+                    mma_commit(bar(B_PV));
+            };
+            if (lane == 0) {
+                ok = wait(B_Q, seg);
+                for (int i = 0; ok && i < min(2, ni); ++i)
+                    qk(i);
+                for (int i = 0; ok && i < ni; ++i) {
+                    pv(i);
+                    if (ok && i + 2 < ni)
+                        qk(i + 2);
+                }
+                if (ok) {
+                    mma_commit(bar(B_O));
+                    mbar_arrive(bar(B_O));  // (and what this thread has seen of the producer's flag)
+                }
+            }
+            ok = __shfl_sync(0xffffffffu, ok, 0);
+            base += (uint32_t)n * (UK + UV);
+        }
+        if (lane == 0) {
+            mma_commit(bar(B_DONE));
+            wait_bar_drain(bar(B_DONE), 0);
+        }
+        __syncwarp();
+    } else if (warp >= 4) {
+        // --------------------------------------------------------- softmax --
+        const int wg = (warp - 4) / 4, r = (warp % 4) * 32 + lane;
+        const uint32_t lane_off = (uint32_t)(32 * (warp % 4)) << 16;
+        const uint32_t scol = tmem + lane_off + (uint32_t)wg * 128u;
+        const uint32_t ocol = tmem + lane_off + C::kOCol + (NT == 2 ? (uint32_t)wg * 128u : 0u);
+        uint32_t s_seen = 0, m_base[2] = {0, 0}, pv_base = 0;
+        const float c1 = p.scale_log2, cap = p.cap_log2;
+        // tanh(y) / y as a polynomial in y^2 for |y| <= 1/2 (least squares with
+        // weights moved to the largest errors; off by 1.5e-7 at most), times cap
+        const float y1 = c1 * (0.5f * kLn2);  // raw score to y: c1 = 2 scale log2 e / soft_cap
+        const float limit = 0.5f / y1;
+        const uint64_t t0 = pack_f32x2(cap * 0.9999976754188538f, cap * 0.9999976754188538f);
+        const uint64_t t1 = pack_f32x2(cap * -0.33320656418800354f, cap * -0.33320656418800354f);
+        const uint64_t t2 = pack_f32x2(cap * 0.13145145773887634f, cap * 0.13145145773887634f);
+        const uint64_t t3 = pack_f32x2(cap * -0.04337248206138611f, cap * -0.04337248206138611f);
+        const uint64_t yy1 = pack_f32x2(y1, y1);
+        for (int64_t item = lo; item < hi; item < hi ? next_group<DH, NT>(p, x, heads) : (void)0, ++seg) {
+            const int j0 = (int)(item - x.g0), n = (int)(min(hi, x.g0 + x.n) - item);
+            const bool whole = n == x.n;
+            const int kvh = x.hv / C::kSplit, part = x.hv % C::kSplit;
+            const int rows = min(RT, x.m.qn * p.group - x.tile * RT);
+            // Q: a softmax group its own row tile, or half of the one
+            {
+                constexpr int CH = DH / 8;  // 16-byte vectors of a row
+                const int count = NT == 2 ? 128 * CH : 64 * CH, first = wg * count;
+                for (int i = first + tid % 128; i < first + count; i += 128) {
+                    const int qr = i / CH, ch = i % CH;
+                    uint4 v = make_uint4(0u, 0u, 0u, 0u);
+                    if (qr < rows) {
+                        const int row = x.tile * RT + qr, tok = row / p.group, h = kvh * p.group + row - tok * p.group;
+                        v = __ldg(reinterpret_cast<const uint4 *>(p.q + ((int64_t)x.m.qs + tok) * p.q_tok_stride +
+                                                                  (int64_t)h * DH) + ch);
+                    }
+                    const int tr = qr % 128;
+                    *reinterpret_cast<uint4 *>(s_q + (qr / 128) * 128 * DH * 2 + (ch / 8) * 16384 + tr * 128 +
+                                               (((ch % 8) ^ (tr & 7)) << 4)) = v;
+                }
+                fence_proxy_async_smem();
+                tc_fence_before();  // (the output before has been read: products may overwrite it)
+                __syncwarp();
+                if (lane == 0)
+                    mbar_arrive(bar(B_Q));
+            }
+            // what this thread's row sees
+            const int gr = (NT == 2 ? wg * 128 : 0) + r, row = x.tile * RT + gr;
+            const bool valid = gr < rows;
+            const int tok = valid ? row / p.group : 0, head = kvh * p.group + (valid ? row - tok * p.group : 0);
+            const int pos = x.m.L - x.m.qn + tok;
+            const int prefix = valid ? x.v.prefix : 0;
+            const int r_lo = valid ? score_low(p, (int64_t)x.m.qs + tok, pos) : 1;
+            const int r_len = valid ? pos - r_lo + 1 : 0;
+            const int near = valid ? score_nearest(r_lo, pos, prefix) : 0;
+            const float slope = valid && p.slopes ? __ldg(p.slopes + head) : 0.f, slope2 = slope * kLog2e;
+            const int lo_max = __reduce_max_sync(0xffffffffu, valid ? r_lo : 0);
+            const int pos_min = __reduce_min_sync(0xffffffffu, valid ? pos : INT32_MAX);
+            const int pre_min = __reduce_min_sync(0xffffffffu, valid ? prefix : INT32_MAX);
+            float m = MODE == kModeCapped ? 0.f : -INFINITY, l = 0.f;
+            for (int i = NT == 2 ? 0 : wg; i < n; i += NT == 2 ? 1 : 2) {
+                const int k0 = tile_key(x.t, j0 + i);
+                if (ok)
+                    ok = wait(B_S + wg, s_seen);
+                ok = __all_sync(0xffffffffu, ok);
+                ++s_seen;
+                tc_fence_after();
+                // every row of the warp sees every key of the tile
+                const bool past = k0 >= lo_max && k0 + kTileKeys - 1 <= pos_min;  // (and none lies after its position)
+                const bool all = past || k0 + kTileKeys <= pre_min;
+                const int rel_lo = r_lo - k0, rel_pre = prefix - k0;
+                auto seen = [&](int col) { return col < rel_pre || (uint32_t)(col - rel_lo) < (uint32_t)r_len; };
+                uint64_t sum0 = 0, sum1 = 0;
+                if (ok && MODE == kModeCapped) {
+                    // no maximum: |z| <= cap, and 2^cap times any number of keys is far from overflow
+#pragma unroll
+                    for (int ch = 0; ch < 4; ++ch) {
+                        uint32_t v[32], o[16];
+                        tmem_ld32(scol + ch * 32, v);
+                        tmem_wait_ld();
+                        float top = 0.f;
+#pragma unroll
+                        for (int k = 0; k < 32; k += 2)
+                            top = max3f(top, fabsf(__uint_as_float(v[k])), fabsf(__uint_as_float(v[k + 1])));
+                        // (a NaN passes the test unseen and stays one in both ways)
+                        if (__all_sync(0xffffffffu, top <= limit)) {
+#pragma unroll
+                            for (int k = 0; k < 32; k += 2) {
+                                const uint64_t y = mul_f32x2(pack_f32x2(__uint_as_float(v[k]), __uint_as_float(v[k + 1])), yy1);
+                                const uint64_t u = mul_f32x2(y, y);
+                                const uint64_t z = mul_f32x2(y, fma_f32x2(fma_f32x2(fma_f32x2(t3, u, t2), u, t1), u, t0));
+                                float a, b;
+                                unpack_f32x2(z, a, b);
+                                v[k] = __float_as_uint(ex2(a));
+                                v[k + 1] = __float_as_uint(ex2(b));
+                            }
+                        } else {
+#pragma unroll
+                            for (int k = 0; k < 32; ++k)
+                                v[k] = __float_as_uint(ex2(capped(__uint_as_float(v[k]), c1, cap)));
+                        }
+                        if (!all)
+#pragma unroll
+                            for (int k = 0; k < 32; ++k)
+                                v[k] = seen(ch * 32 + k) ? v[k] : 0u;
+#pragma unroll
+                        for (int k = 0; k < 32; k += 4) {
+                            sum0 = add_f32x2(sum0, pack_f32x2(__uint_as_float(v[k]), __uint_as_float(v[k + 1])));
+                            sum1 = add_f32x2(sum1, pack_f32x2(__uint_as_float(v[k + 2]), __uint_as_float(v[k + 3])));
+                        }
+#pragma unroll
+                        for (int k = 0; k < 16; ++k)
+                            o[k] = pack_bf16x2(__uint_as_float(v[2 * k]), __uint_as_float(v[2 * k + 1]));
+                        tmem_st16(scol + ch * 16, o);
+                    }
+                } else if (MODE != kModeCapped) {
+                    uint32_t v[4][32];
+                    float mx = -INFINITY;
+                    if (ok) {
+#pragma unroll
+                        for (int ch = 0; ch < 4; ++ch)
+                            tmem_ld32(scol + ch * 32, v[ch]);
+                        tmem_wait_ld();
+                        if (MODE == kModeAny) {
+                            // capped, biased: exponents in log2 units
+                            const float b0 = -slope2 * (float)(pos - near - k0);
+#pragma unroll
+                            for (int ch = 0; ch < 4; ++ch)
+#pragma unroll
+                                for (int k = 0; k < 32; ++k) {
+                                    const float s = __uint_as_float(v[ch][k]);
+                                    const int col = ch * 32 + k;
+                                    float z = cap > 0.f ? capped(s, c1, cap) : s * c1;
+                                    if (past)
+                                        z += __fmaf_rn(slope2, (float)col, b0);
+                                    else
+                                        z -= slope2 * (float)(abs(pos - k0 - col) - near);
+                                    v[ch][k] = __float_as_uint(z);
+                                }
+                        }
+                        if (!all)
+#pragma unroll
+                            for (int ch = 0; ch < 4; ++ch)
+#pragma unroll
+                                for (int k = 0; k < 32; ++k)
+                                    v[ch][k] = seen(ch * 32 + k) ? v[ch][k] : 0xff800000u;
+                        float mx1 = -INFINITY;
+#pragma unroll
+                        for (int ch = 0; ch < 4; ++ch)
+#pragma unroll
+                            for (int k = 0; k < 32; k += 4) {
+                                mx = max3f(mx, __uint_as_float(v[ch][k]), __uint_as_float(v[ch][k + 1]));
+                                mx1 = max3f(mx1, __uint_as_float(v[ch][k + 2]), __uint_as_float(v[ch][k + 3]));
+                            }
+                        mx = fmaxf(mx, mx1);
+                        if (MODE == kModePlain)
+                            mx *= c1;
+                    }
+                    if (NT == 1 && i > 0) {
+                        // the maximum after the tile before, which the other group holds
+                        if (ok)
+                            ok = wait(B_M + (wg ^ 1), m_base[wg ^ 1] + (uint32_t)(wg ? (i - 1) / 2 : i / 2 - 1));
+                        ok = __all_sync(0xffffffffu, ok);
+                        const float other = s_m[r];
+                        if (other != m) {
+                            l = l == 0.f ? 0.f : l * ex2(m - other);
+                            m = other;
+                        }
+                    }
+                    // the maximum moves when a tile's is more than 8 (2^8) above it
+                    const bool move = mx > m + kTau || m == -INFINITY;
+                    const float m_old = m;
+                    if (move)
+                        m = mx;
+                    const float alpha = move && m_old != -INFINITY ? ex2(m_old - m) : 1.f;
+                    if (NT == 1) {
+                        s_m[r] = m;
+                        __syncwarp();
+                        if (lane == 0)
+                            mbar_arrive(bar(B_M + wg));
+                    }
+                    l *= alpha;
+                    if (__any_sync(0xffffffffu, alpha != 1.f) && i > 0 && ok) {
+                        // (two row tiles: QK of this tile was issued behind PV of the one before)
+                        if (NT == 1) {
+                            ok = wait(B_PV, pv_base + (uint32_t)i - 1);
+                            ok = __all_sync(0xffffffffu, ok);
+                            tc_fence_after();
+                        }
+                        constexpr int OC = NT == 2 ? 128 : C::kCols;
+                        if (ok)
+#pragma unroll 1
+                            for (int ch = 0; ch < OC; ch += 16) {
+                                uint32_t o[16];
+                                tmem_ld16(ocol + ch, o);
+                                tmem_wait_ld();
+#pragma unroll
+                                for (int k = 0; k < 16; ++k)
+                                    o[k] = __float_as_uint(__uint_as_float(o[k]) * alpha);
+                                tmem_st16(ocol + ch, o);
+                            }
+                    }
+                    const float base = m == -INFINITY ? 0.f : m;
+                    const uint64_t nb = pack_f32x2(-base, -base);
+                    const uint64_t cc = MODE == kModePlain ? pack_f32x2(c1, c1) : pack_f32x2(1.f, 1.f);
+                    if (ok)
+#pragma unroll
+                        for (int ch = 0; ch < 4; ++ch) {
+                            uint32_t o[16];
+#pragma unroll
+                            for (int k = 0; k < 32; k += 2) {
+                                const uint64_t s = pack_f32x2(__uint_as_float(v[ch][k]), __uint_as_float(v[ch][k + 1]));
+                                const uint64_t z = MODE == kModePlain ? fma_f32x2(s, cc, nb) : add_f32x2(s, nb);
+                                float a, b;
+                                unpack_f32x2(z, a, b);
+                                a = ex2(a), b = ex2(b);
+                                if (k % 4 == 0)
+                                    sum0 = add_f32x2(sum0, pack_f32x2(a, b));
+                                else
+                                    sum1 = add_f32x2(sum1, pack_f32x2(a, b));
+                                o[k / 2] = pack_bf16x2(a, b);
+                            }
+                            tmem_st16(scol + ch * 16, o);
+                        }
+                }
+                {
+                    float a, b, d, e;
+                    unpack_f32x2(sum0, a, b);
+                    unpack_f32x2(sum1, d, e);
+                    l += (a + b) + (d + e);
+                }
+                tmem_wait_st();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0)
+                    mbar_arrive(bar(B_P + wg));
+            }
+            // ------------------------------------------------ the output --
+            if (ok)
+                ok = wait(B_O, seg);
+            ok = __all_sync(0xffffffffu, ok);
+            tc_fence_after();
+            if (NT == 1) {
+                // both groups' sums, relative to the maximum after the last tile
+                if (MODE != kModeCapped) {
+                    named_sync(1, 256);
+                    const float m_end = s_m[r];
+                    l = l == 0.f ? 0.f : l * ex2(m - m_end);
+                    m = m_end;
+                }
+                s_l[wg * 128 + r] = l;
+                named_sync(1, 256);
+                l = s_l[r] + s_l[128 + r];
+            }
+            const bool lost = !ok || s_flags[2];
+            const int col0 = NT == 2 ? 0 : wg * COLS_W;  // of the group's columns
+            const float inv = l == 0.f ? 0.f : 1.f / l;
+            bool odd = lost || !(fabsf(l) < INFINITY);
+            float *rec = w.records + (2 * (int64_t)c + (x.g0 <= lo ? 0 : 1)) * w.record_floats +
+                         (NT == 2 ? wg : 0) * tile_record(C::kCols);
+            const int64_t at = ((int64_t)x.m.qs + tok) * p.hq + head;
+            if (ok)
+#pragma unroll 1
+                for (int ch = 0; ch < COLS_W; ch += 32) {
+                    uint32_t o[32];
+                    tmem_ld32(ocol + col0 + ch, o);
+                    tmem_wait_ld();
+                    if (whole) {
+#pragma unroll
+                        for (int k = 0; k < 32; ++k) {
+                            const float f = __uint_as_float(o[k]) * inv;
+                            odd |= !(fabsf(f) < INFINITY);
+                            o[k] = __float_as_uint(f);
+                        }
+                        if (valid)
+                            store_out32(p.out + at * DH + part * C::kCols + col0 + ch, o);
+                    } else {
+                        float4 *dst = reinterpret_cast<float4 *>(rec + 256) + (int64_t)(col0 + ch) / 4 * 128 + r;
+#pragma unroll
+                        for (int k = 0; k < 8; ++k)
+                            dst[k * 128] = make_float4(__uint_as_float(o[4 * k]), __uint_as_float(o[4 * k + 1]),
+                                                       __uint_as_float(o[4 * k + 2]), __uint_as_float(o[4 * k + 3]));
+                    }
+                }
+            if (NT == 2 || wg == 0) {
+                if (!whole) {
+                    rec[r] = m;
+                    rec[128 + r] = lost ? __int_as_float(0x7FC00000) : l;
+                } else if (valid && part == 0 && p.lse) {
+                    p.lse[at] = l == 0.f ? -INFINITY : (m + __log2f(l)) * kLn2 - slope * (float)near;
+                }
+            }
+            if (whole) {
+                __syncwarp();
+                for (uint32_t todo = __ballot_sync(0xffffffffu, odd && valid); todo; todo &= todo - 1) {
+                    const int from = __ffs(todo) - 1;
+                    scored_row<DH>(p, x.b, x.m, __shfl_sync(0xffffffffu, tok, from), __shfl_sync(0xffffffffu, head, from));
+                }
+            }
+            item += n;
+            m_base[0] += (uint32_t)(n + 1) / 2;
+            m_base[1] += (uint32_t)n / 2;
+            pv_base += (uint32_t)n;
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 1)
+        tmem_dealloc(tmem, 512);
+}
+
+// Folds the records of the groups that several CTAs have a part of: a thread per
+// row, 32 columns of the output a CTA.
+template <int DH, int NT>
+__global__ void __launch_bounds__(128) scored_tile_fold_kernel(const ScoreParams p, const TileWork w)
+{
+    using C = TileCfg<DH, NT>;
+    griddep_wait();
+    griddep_launch_dependents();
+    constexpr int CB = C::kCols / 32;
+    const int heads = p.hkv * C::kSplit;
+    const int unit = blockIdx.x / CB, cb = blockIdx.x % CB, g = unit / NT, t = unit % NT;
+    if (g >= w.header[1] * heads)
+        return;
+    const int64_t total = w.header[0];
+    const int2 gr = w.groups[g], en = w.entries[g / heads];
+    const int64_t g0 = gr.x, g1 = g0 + gr.y;
+    int c0 = 0, n = 0;
+    if (gr.y > 0) {
+        auto owner = [&](int64_t item) {
+            int c = (int)(item * w.ctas / total);
+            while (range_lo(total, c + 1, w.ctas) <= item)
+                ++c;
+            while (range_lo(total, c, w.ctas) > item)
+                --c;
+            return c;
+        };
+        c0 = owner(g0);
+        n = owner(g1 - 1) - c0 + 1;
+        if (n == 1)
+            return;  // written by the CTA that had all of it
+    }
+    const int b = en.x, hv = g % heads, kvh = hv / C::kSplit, part = hv % C::kSplit;
+    const ReqMeta m = score_meta(p, b);
+    const int r = threadIdx.x, row = en.y * (NT * 128) + t * 128 + r;
+    const bool valid = row < m.qn * p.group;
+    const int tok = valid ? row / p.group : 0, head = kvh * p.group + (valid ? row - tok * p.group : 0);
+    auto record = [&](int c) {
+        return w.records + (2 * (int64_t)c + (g0 <= range_lo(total, c, w.ctas) ? 0 : 1)) * w.record_floats +
+               t * tile_record(C::kCols);
+    };
+    // (where there are more CTAs than items, some have none)
+    auto has_part = [&](int c) { return range_lo(total, c, w.ctas) < range_lo(total, c + 1, w.ctas); };
+    float top = -INFINITY;
+    for (int i = 0; i < n; ++i)
+        if (has_part(c0 + i))
+            top = fmaxf(top, __ldcg(record(c0 + i) + r));
+    float sum = 0.f, o[32];
+#pragma unroll
+    for (int k = 0; k < 32; ++k)
+        o[k] = 0.f;
+#pragma unroll 2
+    for (int i = 0; i < n; ++i) {
+        if (!has_part(c0 + i))
+            continue;
+        const float *rec = record(c0 + i);
+        const float mi = __ldcg(rec + r), f = mi == top ? 1.f : ex2(mi - top);
+        sum += __ldcg(rec + 128 + r) * f;
+        const float4 *src = reinterpret_cast<const float4 *>(rec + 256) + (int64_t)cb * 8 * 128 + r;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            const float4 v = __ldcg(src + k * 128);
+            o[4 * k] += v.x * f;
+            o[4 * k + 1] += v.y * f;
+            o[4 * k + 2] += v.z * f;
+            o[4 * k + 3] += v.w * f;
+        }
+    }
+    const float inv = sum == 0.f ? 0.f : 1.f / sum;
+    bool odd = !(fabsf(sum) < INFINITY);
+    uint32_t q[32];
+#pragma unroll
+    for (int k = 0; k < 32; ++k) {
+        const float f = o[k] * inv;
+        odd |= !(fabsf(f) < INFINITY);
+        q[k] = __float_as_uint(f);
+    }
+    const int64_t at = ((int64_t)m.qs + tok) * p.hq + head;
+    if (valid) {
+        store_out32(p.out + at * DH + part * C::kCols + cb * 32, q);
+        if (p.lse && part == 0 && cb == 0) {
+            const int pos = m.L - m.qn + tok;
+            const int near = score_nearest(score_low(p, (int64_t)m.qs + tok, pos), pos, score_prefix(p, b, m.L));
+            const float slope = p.slopes ? __ldg(p.slopes + head) : 0.f;
+            p.lse[at] = sum == 0.f ? -INFINITY : (top + __log2f(sum)) * kLn2 - slope * (float)near;
+        }
+    }
+    __syncwarp();
+    for (uint32_t todo = __ballot_sync(0xffffffffu, odd && valid); todo; todo &= todo - 1) {
+        const int from = __ffs(todo) - 1;
+        scored_row<DH>(p, b, m, __shfl_sync(0xffffffffu, tok, from), __shfl_sync(0xffffffffu, head, from));
+    }
+}
+
+// --------------------------------------------------------------------- host --
+template <int DH, int NT>
+cudaError_t launch_tiles(const ScoreParams &p, const CUtensorMap (&tm)[2], const TileWork &w, int mode, cudaStream_t stream)
+{
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)w.ctas);
+    cfg.blockDim = dim3(kTileThreads);
+    cfg.dynamicSmemBytes = tiles_smem<DH, NT>();
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    auto kern = mode == kModePlain    ? scored_tiles_kernel<DH, NT, kModePlain>
+                : mode == kModeCapped ? scored_tiles_kernel<DH, NT, kModeCapped>
+                                      : scored_tiles_kernel<DH, NT, kModeAny>;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, p, tm[0], tm[1], w);
+    if (e != cudaSuccess)
+        return e;
+    using C = TileCfg<DH, NT>;
+    cfg.gridDim = dim3((unsigned)((int64_t)w.max_tiles * p.hkv * C::kSplit * NT * (C::kCols / 32)));
+    cfg.blockDim = dim3(128);
+    cfg.dynamicSmemBytes = 0;
+    return cudaLaunchKernelEx(&cfg, scored_tile_fold_kernel<DH, NT>, p, w);
+}
+
+template <int DH, int NT>
+cudaError_t tiles_attributes()
+{
+    constexpr auto attr = cudaFuncAttributeMaxDynamicSharedMemorySize;
+    cudaError_t e = cudaFuncSetAttribute(scored_tiles_kernel<DH, NT, kModePlain>, attr, (int)tiles_smem<DH, NT>());
+    if (e == cudaSuccess)
+        e = cudaFuncSetAttribute(scored_tiles_kernel<DH, NT, kModeCapped>, attr, (int)tiles_smem<DH, NT>());
+    if (e == cudaSuccess)
+        e = cudaFuncSetAttribute(scored_tiles_kernel<DH, NT, kModeAny>, attr, (int)tiles_smem<DH, NT>());
+    return e;
+}
+
+}  // namespace pa

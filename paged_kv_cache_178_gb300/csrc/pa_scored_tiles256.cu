@@ -1,0 +1,9 @@
+// pa_paged_attention_scored for many rows: head dim 256.
+#include "pa_scored_tiles.cuh"
+
+namespace pa {
+
+template cudaError_t launch_tiles<256, 1>(const ScoreParams &, const CUtensorMap (&)[2], const TileWork &, int, cudaStream_t);
+template cudaError_t tiles_attributes<256, 1>();
+
+}  // namespace pa
