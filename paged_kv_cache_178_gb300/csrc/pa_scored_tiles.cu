@@ -38,7 +38,7 @@ bool scored_tiles_fits(int32_t num_seqs, int32_t hkv, int group, int32_t head_di
         return true;  // (a workspace's size: the call itself is refused)
     const int64_t tiles = scored_tiles_bound(num_seqs, group, head_dim, max_query_len, num_q_tokens);
     return num_seqs + tiles + 2 <= kScoredMaxEntriesHost &&
-           tiles * hkv * 2 * (((int64_t)max_seq_len + kTileKeys - 1) / kTileKeys + 1) <= INT32_MAX;
+           tiles * hkv * 2 * (((int64_t)max_seq_len + kTileKeys - 1) / kTileKeys + 1 + kGroupSetup) <= INT32_MAX;
 }
 
 static size_t align256(size_t n) { return (n + 255) / 256 * 256; }
@@ -86,7 +86,7 @@ cudaError_t launch_scored_tiles(const ScoreParams &p, int32_t head_dim, void *wo
     w.entries = reinterpret_cast<int2 *>(ws + s.entries);
     w.records = reinterpret_cast<float *>(ws + s.records);
     w.record_floats = s.record_floats;
-    const int64_t items = s.tiles * p.hkv * s.parts * (((int64_t)p.max_seq_len + kTileKeys - 1) / kTileKeys + 1);
+    const int64_t items = s.tiles * p.hkv * s.parts * (((int64_t)p.max_seq_len + kTileKeys - 1) / kTileKeys + 1 + kGroupSetup);
     w.ctas = (int32_t)(items < kScoredSms ? items : kScoredSms);
     w.max_tiles = (int32_t)s.tiles;
     // Without a maximum the exponents stay within the cap: 2^80 times any number

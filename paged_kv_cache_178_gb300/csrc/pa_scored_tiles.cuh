@@ -19,8 +19,9 @@
 //   warp 0      copies units of 128 keys by 128 columns (32 KB, a TMA box for each
 //               page and 64 columns) into a ring, in the order of their use
 //   warp 1      issues the products (one thread)
-//   warps 4-7, 8-11   softmax of one score buffer each, a row to a thread; Q
-//               into shared memory at a group's start, the output at its end
+//   warps 2, 3  Q of a group, once the products of the group before have read theirs
+//   warps 4-7, 8-11   softmax of one score buffer each, a row to a thread, and
+//               the output at a group's end
 // Head dim 512: the output's halves are two groups, each with all of the scores
 // (tensor memory holds 256 columns of output beside the scores): three halves of
 // the products of a whole one instead of two, and no exchange.
@@ -33,6 +34,9 @@ namespace pa {
 constexpr int kTileThreads = 384;
 constexpr int kTileKeys = 128;
 constexpr int kUnitBytes = kTileKeys * 256;  // 128 keys by 128 columns
+// What a group costs beside its items, in items: it is dealt out with them, at
+// the group's start.
+constexpr int kGroupSetup = 2;
 
 // How a score becomes an exponent.
 enum ScoreMode : int {
@@ -47,7 +51,11 @@ struct TileCfg {
     static constexpr int kUnitsK = DH / 128, kUnitsV = DH / 128 / kSplit;
     static constexpr int kCols = DH / kSplit;         // output columns of a group
     static constexpr int kQBytes = NT * 128 * DH * 2;
-    static constexpr int kStages = (224 * 1024 - kQBytes) / kUnitBytes;
+    // The output passes through shared memory, 64 columns of a warp's rows at a
+    // time (a row to a thread stores 16 bytes to 32 lines at once); at head dim
+    // 512 there is no room for that.
+    static constexpr int kOutBytes = DH == 512 ? 0 : 32 * 1024;
+    static constexpr int kStages = (224 * 1024 - kQBytes - kOutBytes) / kUnitBytes;
     static constexpr int kOCol = 256;                 // tensor-memory column of the output
     static_assert(NT * kCols <= 256 && kStages >= 3, "tensor and shared memory");
 };
@@ -70,7 +78,7 @@ template <int DH, int NT>
 constexpr size_t tiles_smem()
 {
     using C = TileCfg<DH, NT>;
-    return 1024 + (size_t)C::kQBytes + (size_t)C::kStages * kUnitBytes + kTileSmall;
+    return 1024 + (size_t)C::kQBytes + (size_t)C::kStages * kUnitBytes + C::kOutBytes + kTileSmall;
 }
 
 __device__ __forceinline__ uint64_t mul_f32x2(uint64_t a, uint64_t b)
@@ -116,28 +124,29 @@ __device__ __forceinline__ TileView warp_tile_view(const ScoreParams &p, int b, 
 struct TileGroup {
     int b, tile, hv;    // request, row tile, (KV head, part of the columns)
     int64_t g0;         // first item
-    int n;              // items
+    int n, w;           // key tiles, items (kGroupSetup more, or none)
     ReqMeta m;
     TileView v;
     TileBlocks t;
 };
 
+// (x.m is request x.b's)
 template <int DH, int NT>
 __device__ __forceinline__ void load_group(const ScoreParams &p, TileGroup &x)
 {
     constexpr int RT = NT * 128;
-    x.m = score_meta(p, x.b);
     const int rows = x.m.qn * p.group;
     x.v = warp_tile_view(p, x.b, x.m, min(x.tile * RT, rows), min(x.tile * RT + RT, rows));
     x.t = tile_blocks(x.v, kTileKeys);
     x.n = x.t.count;
+    x.w = x.n ? x.n + kGroupSetup : 0;
 }
 
 // The next group with items (there is one: the range goes on).
 template <int DH, int NT>
 __device__ __forceinline__ void next_group(const ScoreParams &p, TileGroup &x, int heads)
 {
-    x.g0 += x.n;
+    x.g0 += x.w;
     if (++x.hv < heads)
         return;
     x.hv = 0;
@@ -173,6 +182,31 @@ __device__ __forceinline__ int stale_row(const TileGroup &x, int k0)
     return x.m.L % 16 && page >= k0 && page < k0 + kTileKeys && page_seen(x.v, page) ? x.m.L - k0 : kTileKeys;
 }
 
+// f(values of 32 columns, chunk) for the four chunks of a score tile, the next
+// chunk's load in flight meanwhile.  (Two copies of f, not four: a CTA lives for
+// some 15 tiles, so what the instruction cache has to fetch shows.)
+template <typename F>
+__device__ __forceinline__ void for_chunks(uint32_t scol, F f)
+{
+    uint32_t a[32], b[32];
+    tmem_ld32(scol, a);
+    tmem_wait_ld();
+#pragma unroll 1
+    for (int h = 0; h < 2; ++h) {
+        tmem_ld32(scol + h * 64 + 32, b);
+        f(a, 2 * h);
+        tmem_wait_ld();
+        if (h == 0)
+            tmem_ld32(scol + 64, a);
+        f(b, 2 * h + 1);
+        if (h == 0)
+            tmem_wait_ld();
+    }
+}
+
+// Bits below n.
+__device__ __forceinline__ uint32_t bits_below(int n) { return n <= 0 ? 0u : (n >= 32 ? ~0u : (1u << n) - 1u); }
+
 template <int DH, int NT, int MODE>
 __global__ void __launch_bounds__(kTileThreads, 1)
     scored_tiles_kernel(const __grid_constant__ ScoreParams p, const __grid_constant__ CUtensorMap tm_k,
@@ -182,14 +216,15 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     constexpr int RT = NT * 128, NS = C::kStages, UK = C::kUnitsK, UV = C::kUnitsV;
     constexpr int COLS_W = NT == 2 ? 128 : C::kCols / 2;  // output columns that a softmax group reads
     constexpr uint32_t ID_QK = idesc_bf16_f32(128, kTileKeys, false), ID_PV = idesc_bf16_f32(128, 128, true);
-    enum { B_FULL = 0, B_EMPTY = NS, B_S = 2 * NS, B_P = B_S + 2, B_M = B_P + 2, B_PV = B_M + 2, B_Q, B_O, B_DONE, B_Z, NBARS = B_Z + NS };
+    enum { B_FULL = 0, B_EMPTY = NS, B_S = 2 * NS, B_P = B_S + 2, B_M = B_P + 2, B_PV = B_M + 2, B_Q, B_QE, B_O, B_DONE, B_Z, NBARS = B_Z + NS };
     static_assert(NBARS * 8 <= 256, "barriers");
     static_assert(tiles_smem<DH, NT>() <= kMaxSmemPerBlock, "shared-memory layout");
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
     uint8_t *s_q = smem;                       // [NT][DH/64][128 rows][128 bytes]
     uint8_t *s_ring = s_q + C::kQBytes;        // [NS][2][128 keys][128 bytes]
-    uint8_t *small = s_ring + NS * kUnitBytes;
+    uint8_t *s_out = s_ring + NS * kUnitBytes; // [8 warps][32 rows][128 bytes]
+    uint8_t *small = s_out + C::kOutBytes;
     uint64_t *bars = reinterpret_cast<uint64_t *>(small);
     volatile int *s_flags = reinterpret_cast<volatile int *>(small + 256);  // [0] abort [1] tmem [2] bad [4..8) start
     float *s_m = reinterpret_cast<float *>(small + 512);                    // [128] the shared running maximum
@@ -207,7 +242,8 @@ __global__ void __launch_bounds__(kTileThreads, 1)
             mbar_init(bar(B_M + i), 4);
         }
         mbar_init(bar(B_PV), 1);
-        mbar_init(bar(B_Q), 8);
+        mbar_init(bar(B_Q), 2);
+        mbar_init(bar(B_QE), 1);
         mbar_init(bar(B_O), 2);
         mbar_init(bar(B_DONE), 1);
         for (int i = 0; i < NS; ++i)
@@ -238,7 +274,8 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         const int b = owner_of(s_first, p.num_seqs, e), tile = e - s_first[b];
         const ReqMeta m = score_meta(p, b);
         const int rows = m.qn * p.group;
-        return tile_blocks(tile_view(p, b, m, min(tile * RT, rows), min(tile * RT + RT, rows)), kTileKeys).count;
+        const int n = tile_blocks(tile_view(p, b, m, min(tile * RT, rows), min(tile * RT + RT, rows)), kTileKeys).count;
+        return n ? n + kGroupSetup : 0;
     });
     const int64_t total = per_head * heads;
     for (int g = c * kTileThreads + tid; g < ntiles * heads; g += ctas * kTileThreads) {
@@ -286,12 +323,25 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     TileGroup x;
     x.b = s_flags[4];
     x.tile = s_flags[5];
+    x.m = score_meta(p, x.b);
     load_group<DH, NT>(p, x);
     {
         const int64_t first = (int64_t)s_flags[6] * heads;
-        x.hv = (int)((lo - first) / x.n);
-        x.g0 = first + (int64_t)x.hv * x.n;
+        x.hv = (int)((lo - first) / x.w);
+        x.g0 = first + (int64_t)x.hv * x.w;
     }
+    // this CTA's key tiles [j0, j0 + n) of the group, and the items after them
+    struct Part {
+        int j0, n;
+        int64_t next;
+    };
+    auto part_of = [&](int64_t item) {
+        Part s;
+        s.next = min(hi, x.g0 + x.w);
+        s.j0 = max((int)(item - x.g0) - kGroupSetup, 0);
+        s.n = max((int)(s.next - x.g0) - kGroupSetup, 0) - s.j0;
+        return s;
+    };
     // position in the ring, within a segment of n tiles, of K or V of tile j
     auto pos_k = [&](int j) { return NT == 2 ? j * (UK + UV) : (j == 0 ? 0 : UK + (j - 1) * (UK + UV)); };
     auto pos_v = [&](int j, int n) {
@@ -324,8 +374,11 @@ __global__ void __launch_bounds__(kTileThreads, 1)
             }
         };
         for (int64_t item = lo; ok && item < hi; item < hi ? next_group<DH, NT>(p, x, heads) : (void)0) {
-            const int j0 = (int)(item - x.g0), n = (int)(min(hi, x.g0 + x.n) - item);
-            item += n;
+            const Part s = part_of(item);
+            const int j0 = s.j0, n = s.n;
+            item = s.next;
+            if (n == 0)
+                continue;
             const int v_col = x.hv % C::kSplit * C::kCols;
             auto check = [&](int raw, int j) {
                 const bool bad = page_seen(x.v, tile_key(x.t, j) + pg * 16) && (raw < 0 || (int64_t)raw >= p.num_blocks);
@@ -381,9 +434,12 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         uint32_t base = 0;               // units before the segment
         uint32_t p_seen[2] = {0, 0};     // probabilities consumed of each buffer
         uint32_t zeroed = 0;             // a bit per stage: the phase of its B_Z
-        for (int64_t item = lo; ok && item < hi; item < hi ? next_group<DH, NT>(p, x, heads) : (void)0, ++seg) {
-            const int j0 = (int)(item - x.g0), n = (int)(min(hi, x.g0 + x.n) - item), ni = n * NT;
-            item += n;
+        for (int64_t item = lo; ok && item < hi; item < hi ? next_group<DH, NT>(p, x, heads) : (void)0) {
+            const Part s = part_of(item);
+            const int j0 = s.j0, n = s.n, ni = n * NT;
+            item = s.next;
+            if (n == 0)
+                continue;
             const bool zero = stale_row(x, tile_key(x.t, j0 + n - 1)) < kTileKeys;
             auto qk = [&](int i) {
                 const int t = NT == 2 ? i % 2 : 0, j = i / NT;
@@ -407,6 +463,8 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                         mma_commit(bar(B_EMPTY + stage));
                 }
                 mma_commit(bar(B_S + i % 2));
+                if (i == ni - 1)
+                    mma_commit(bar(B_QE));  // Q may be replaced
             };
             auto pv = [&](int i) {
                 const int t = NT == 2 ? i % 2 : 0, j = i / NT;
@@ -453,13 +511,57 @@ __global__ void __launch_bounds__(kTileThreads, 1)
             }
             ok = __shfl_sync(0xffffffffu, ok, 0);
             base += (uint32_t)n * (UK + UV);
+            ++seg;
         }
         if (lane == 0) {
             mma_commit(bar(B_DONE));
             wait_bar_drain(bar(B_DONE), 0);
         }
         __syncwarp();
-    } else if (warp >= 4) {
+    } else if (warp < 4) {
+        // -------------------------------------------------------------- Q --
+        // A group's rows as soon as the products of the group before have read
+        // theirs: a thread keeps its column, so that all copies are in flight.
+        constexpr int CH = DH / 8, STEP = 64 / CH;  // 16-byte vectors of a row; rows apart
+        const int qt = tid - 64, ch = qt % CH;
+        const int step_tok = STEP / p.group, step_head = STEP - step_tok * p.group;
+        for (int64_t item = lo; ok && item < hi; item < hi ? next_group<DH, NT>(p, x, heads) : (void)0) {
+            const Part s = part_of(item);
+            item = s.next;
+            if (s.n == 0)
+                continue;
+            if (seg > 0)
+                ok = __all_sync(0xffffffffu, wait(B_QE, seg - 1));
+            ++seg;
+            if (!ok)
+                break;
+            const int kvh = x.hv / C::kSplit, rows = min(RT, x.m.qn * p.group - x.tile * RT);
+            const int first = x.tile * RT + qt / CH;
+            int tok = first / p.group, head = first - tok * p.group;
+            const __nv_bfloat16 *src = p.q + (int64_t)x.m.qs * p.q_tok_stride + (int64_t)kvh * p.group * DH + ch * 8;
+            const uint32_t dst = smem_addr(s_q) + (ch / 8) * 16384;
+#pragma unroll 4
+            for (int qr = qt / CH; qr < RT; qr += STEP) {
+                const bool have = qr < rows;
+                // (zeros for rows that are not there)
+                asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(
+                                 dst + (qr / 128) * 128 * DH * 2 + (qr % 128) * 128 + (((ch % 8) ^ (qr & 7)) << 4)),
+                             "l"(have ? src + tok * p.q_tok_stride + head * DH : p.q), "r"(have ? 16 : 0)
+                             : "memory");
+                tok += step_tok;
+                head += step_head;
+                if (head >= p.group) {
+                    head -= p.group;
+                    ++tok;
+                }
+            }
+            asm volatile("cp.async.wait_all;" ::: "memory");
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0)
+                mbar_arrive(bar(B_Q));
+        }
+    } else {
         // --------------------------------------------------------- softmax --
         const int wg = (warp - 4) / 4, r = (warp % 4) * 32 + lane;
         const uint32_t lane_off = (uint32_t)(32 * (warp % 4)) << 16;
@@ -476,33 +578,15 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         const uint64_t t2 = pack_f32x2(cap * 0.13145145773887634f, cap * 0.13145145773887634f);
         const uint64_t t3 = pack_f32x2(cap * -0.04337248206138611f, cap * -0.04337248206138611f);
         const uint64_t yy1 = pack_f32x2(y1, y1);
-        for (int64_t item = lo; item < hi; item < hi ? next_group<DH, NT>(p, x, heads) : (void)0, ++seg) {
-            const int j0 = (int)(item - x.g0), n = (int)(min(hi, x.g0 + x.n) - item);
+        for (int64_t item = lo; item < hi; item < hi ? next_group<DH, NT>(p, x, heads) : (void)0) {
+            const Part s = part_of(item);
+            const int j0 = s.j0, n = s.n;
+            item = s.next;
+            if (n == 0)
+                continue;
             const bool whole = n == x.n;
             const int kvh = x.hv / C::kSplit, part = x.hv % C::kSplit;
             const int rows = min(RT, x.m.qn * p.group - x.tile * RT);
-            // Q: a softmax group its own row tile, or half of the one
-            {
-                constexpr int CH = DH / 8;  // 16-byte vectors of a row
-                const int count = NT == 2 ? 128 * CH : 64 * CH, first = wg * count;
-                for (int i = first + tid % 128; i < first + count; i += 128) {
-                    const int qr = i / CH, ch = i % CH;
-                    uint4 v = make_uint4(0u, 0u, 0u, 0u);
-                    if (qr < rows) {
-                        const int row = x.tile * RT + qr, tok = row / p.group, h = kvh * p.group + row - tok * p.group;
-                        v = __ldg(reinterpret_cast<const uint4 *>(p.q + ((int64_t)x.m.qs + tok) * p.q_tok_stride +
-                                                                  (int64_t)h * DH) + ch);
-                    }
-                    const int tr = qr % 128;
-                    *reinterpret_cast<uint4 *>(s_q + (qr / 128) * 128 * DH * 2 + (ch / 8) * 16384 + tr * 128 +
-                                               (((ch % 8) ^ (tr & 7)) << 4)) = v;
-                }
-                fence_proxy_async_smem();
-                tc_fence_before();  // (the output before has been read: products may overwrite it)
-                __syncwarp();
-                if (lane == 0)
-                    mbar_arrive(bar(B_Q));
-            }
             // what this thread's row sees
             const int gr = (NT == 2 ? wg * 128 : 0) + r, row = x.tile * RT + gr;
             const bool valid = gr < rows;
@@ -528,21 +612,33 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                 const bool past = k0 >= lo_max && k0 + kTileKeys - 1 <= pos_min;  // (and none lies after its position)
                 const bool all = past || k0 + kTileKeys <= pre_min;
                 const int rel_lo = r_lo - k0, rel_pre = prefix - k0;
-                auto seen = [&](int col) { return col < rel_pre || (uint32_t)(col - rel_lo) < (uint32_t)r_len; };
+                // bit k: column ch * 32 + k is seen
+                auto seen = [&](int ch) {
+                    const int a = rel_lo - ch * 32;
+                    return (bits_below(a + r_len) & ~bits_below(a)) | bits_below(rel_pre - ch * 32);
+                };
                 uint64_t sum0 = 0, sum1 = 0;
                 if (ok && MODE == kModeCapped) {
                     // no maximum: |z| <= cap, and 2^cap times any number of keys is far from overflow
+                    for_chunks(scol, [&](uint32_t(&v)[32], int ch) {
+                        // (chunks that are seen whole, or by no row, are common in a tile that is neither)
+                        const uint32_t keep = all ? ~0u : seen(ch);
+                        if (!all && !__any_sync(0xffffffffu, keep != 0u)) {
+                            uint32_t o[16];
 #pragma unroll
-                    for (int ch = 0; ch < 4; ++ch) {
-                        uint32_t v[32], o[16];
-                        tmem_ld32(scol + ch * 32, v);
-                        tmem_wait_ld();
-                        float top = 0.f;
+                            for (int k = 0; k < 16; ++k)
+                                o[k] = 0u;
+                            tmem_st16(scol + ch * 16, o);
+                            return;
+                        }
+                        float top = 0.f, top1 = 0.f;
 #pragma unroll
-                        for (int k = 0; k < 32; k += 2)
+                        for (int k = 0; k < 32; k += 4) {
                             top = max3f(top, fabsf(__uint_as_float(v[k])), fabsf(__uint_as_float(v[k + 1])));
+                            top1 = max3f(top1, fabsf(__uint_as_float(v[k + 2])), fabsf(__uint_as_float(v[k + 3])));
+                        }
                         // (a NaN passes the test unseen and stays one in both ways)
-                        if (__all_sync(0xffffffffu, top <= limit)) {
+                        if (__all_sync(0xffffffffu, fmaxf(top, top1) <= limit)) {
 #pragma unroll
                             for (int k = 0; k < 32; k += 2) {
                                 const uint64_t y = mul_f32x2(pack_f32x2(__uint_as_float(v[k]), __uint_as_float(v[k + 1])), yy1);
@@ -558,59 +654,66 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                             for (int k = 0; k < 32; ++k)
                                 v[k] = __float_as_uint(ex2(capped(__uint_as_float(v[k]), c1, cap)));
                         }
-                        if (!all)
+                        if (!all && __any_sync(0xffffffffu, ~keep != 0u)) {
 #pragma unroll
                             for (int k = 0; k < 32; ++k)
-                                v[k] = seen(ch * 32 + k) ? v[k] : 0u;
+                                v[k] = keep & (1u << k) ? v[k] : 0u;
+                        }
+                        uint32_t o[16];
 #pragma unroll
                         for (int k = 0; k < 32; k += 4) {
                             sum0 = add_f32x2(sum0, pack_f32x2(__uint_as_float(v[k]), __uint_as_float(v[k + 1])));
                             sum1 = add_f32x2(sum1, pack_f32x2(__uint_as_float(v[k + 2]), __uint_as_float(v[k + 3])));
+                            o[k / 2] = pack_bf16x2(__uint_as_float(v[k]), __uint_as_float(v[k + 1]));
+                            o[k / 2 + 1] = pack_bf16x2(__uint_as_float(v[k + 2]), __uint_as_float(v[k + 3]));
                         }
-#pragma unroll
-                        for (int k = 0; k < 16; ++k)
-                            o[k] = pack_bf16x2(__uint_as_float(v[2 * k]), __uint_as_float(v[2 * k + 1]));
                         tmem_st16(scol + ch * 16, o);
-                    }
+                    });
                 } else if (MODE != kModeCapped) {
-                    uint32_t v[4][32];
+                    // two passes over the scores in tensor memory: the maximum (and
+                    // what the rules make of the scores, written back), the exponents
                     float mx = -INFINITY;
                     if (ok) {
+                        float mx1 = -INFINITY;
+                        const float b0 = -slope2 * (float)(pos - near - k0);
+                        for_chunks(scol, [&](uint32_t(&v)[32], int ch) {
+                            const uint32_t keep = all ? ~0u : seen(ch);
+                            const bool some = all || __any_sync(0xffffffffu, keep != 0u);
+                            if (MODE == kModeAny && some) {
+                                if (cap > 0.f)
 #pragma unroll
-                        for (int ch = 0; ch < 4; ++ch)
-                            tmem_ld32(scol + ch * 32, v[ch]);
-                        tmem_wait_ld();
-                        if (MODE == kModeAny) {
-                            // capped, biased: exponents in log2 units
-                            const float b0 = -slope2 * (float)(pos - near - k0);
+                                    for (int k = 0; k < 32; ++k)
+                                        v[k] = __float_as_uint(capped(__uint_as_float(v[k]), c1, cap));
+                                else
 #pragma unroll
-                            for (int ch = 0; ch < 4; ++ch)
+                                    for (int k = 0; k < 32; ++k)
+                                        v[k] = __float_as_uint(__uint_as_float(v[k]) * c1);
+                                if (past) {
+                                    const float bc = __fmaf_rn(slope2, (float)(ch * 32), b0);
 #pragma unroll
-                                for (int k = 0; k < 32; ++k) {
-                                    const float s = __uint_as_float(v[ch][k]);
-                                    const int col = ch * 32 + k;
-                                    float z = cap > 0.f ? capped(s, c1, cap) : s * c1;
-                                    if (past)
-                                        z += __fmaf_rn(slope2, (float)col, b0);
-                                    else
-                                        z -= slope2 * (float)(abs(pos - k0 - col) - near);
-                                    v[ch][k] = __float_as_uint(z);
+                                    for (int k = 0; k < 32; ++k)
+                                        v[k] = __float_as_uint(__uint_as_float(v[k]) + __fmaf_rn(slope2, (float)k, bc));
+                                } else {
+                                    const int d = pos - k0 - ch * 32;
+#pragma unroll
+                                    for (int k = 0; k < 32; ++k)
+                                        v[k] = __float_as_uint(
+                                            __fmaf_rn(-slope2, (float)(abs(d - k) - near), __uint_as_float(v[k])));
                                 }
-                        }
-                        if (!all)
-#pragma unroll
-                            for (int ch = 0; ch < 4; ++ch)
+                            }
+                            if (!all && __any_sync(0xffffffffu, ~keep != 0u)) {
 #pragma unroll
                                 for (int k = 0; k < 32; ++k)
-                                    v[ch][k] = seen(ch * 32 + k) ? v[ch][k] : 0xff800000u;
-                        float mx1 = -INFINITY;
-#pragma unroll
-                        for (int ch = 0; ch < 4; ++ch)
+                                    v[k] = keep & (1u << k) ? v[k] : 0xff800000u;
+                            }
+                            if (MODE == kModeAny || !all)
+                                tmem_st32(scol + ch * 32, v);
 #pragma unroll
                             for (int k = 0; k < 32; k += 4) {
-                                mx = max3f(mx, __uint_as_float(v[ch][k]), __uint_as_float(v[ch][k + 1]));
-                                mx1 = max3f(mx1, __uint_as_float(v[ch][k + 2]), __uint_as_float(v[ch][k + 3]));
+                                mx = max3f(mx, __uint_as_float(v[k]), __uint_as_float(v[k + 1]));
+                                mx1 = max3f(mx1, __uint_as_float(v[k + 2]), __uint_as_float(v[k + 3]));
                             }
+                        });
                         mx = fmaxf(mx, mx1);
                         if (MODE == kModePlain)
                             mx *= c1;
@@ -661,14 +764,14 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                     }
                     const float base = m == -INFINITY ? 0.f : m;
                     const uint64_t nb = pack_f32x2(-base, -base);
-                    const uint64_t cc = MODE == kModePlain ? pack_f32x2(c1, c1) : pack_f32x2(1.f, 1.f);
+                    const uint64_t cc = pack_f32x2(c1, c1);
+                    tmem_wait_st();  // (what the first pass wrote back)
                     if (ok)
-#pragma unroll
-                        for (int ch = 0; ch < 4; ++ch) {
+                        for_chunks(scol, [&](uint32_t(&v)[32], int ch) {
                             uint32_t o[16];
 #pragma unroll
                             for (int k = 0; k < 32; k += 2) {
-                                const uint64_t s = pack_f32x2(__uint_as_float(v[ch][k]), __uint_as_float(v[ch][k + 1]));
+                                const uint64_t s = pack_f32x2(__uint_as_float(v[k]), __uint_as_float(v[k + 1]));
                                 const uint64_t z = MODE == kModePlain ? fma_f32x2(s, cc, nb) : add_f32x2(s, nb);
                                 float a, b;
                                 unpack_f32x2(z, a, b);
@@ -680,7 +783,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                                 o[k / 2] = pack_bf16x2(a, b);
                             }
                             tmem_st16(scol + ch * 16, o);
-                        }
+                        });
                 }
                 {
                     float a, b, d, e;
@@ -715,32 +818,67 @@ __global__ void __launch_bounds__(kTileThreads, 1)
             const int col0 = NT == 2 ? 0 : wg * COLS_W;  // of the group's columns
             const float inv = l == 0.f ? 0.f : 1.f / l;
             bool odd = lost || !(fabsf(l) < INFINITY);
-            float *rec = w.records + (2 * (int64_t)c + (x.g0 <= lo ? 0 : 1)) * w.record_floats +
+            float *rec = w.records + (2 * (int64_t)c + (x.g0 + kGroupSetup < lo ? 0 : 1)) * w.record_floats +
                          (NT == 2 ? wg : 0) * tile_record(C::kCols);
             const int64_t at = ((int64_t)x.m.qs + tok) * p.hq + head;
-            if (ok)
+            if (ok && !whole) {
 #pragma unroll 1
                 for (int ch = 0; ch < COLS_W; ch += 32) {
                     uint32_t o[32];
                     tmem_ld32(ocol + col0 + ch, o);
                     tmem_wait_ld();
-                    if (whole) {
+                    float4 *dst = reinterpret_cast<float4 *>(rec + 256) + (int64_t)(col0 + ch) / 4 * 128 + r;
 #pragma unroll
-                        for (int k = 0; k < 32; ++k) {
-                            const float f = __uint_as_float(o[k]) * inv;
-                            odd |= !(fabsf(f) < INFINITY);
-                            o[k] = __float_as_uint(f);
-                        }
-                        if (valid)
-                            store_out32(p.out + at * DH + part * C::kCols + col0 + ch, o);
-                    } else {
-                        float4 *dst = reinterpret_cast<float4 *>(rec + 256) + (int64_t)(col0 + ch) / 4 * 128 + r;
-#pragma unroll
-                        for (int k = 0; k < 8; ++k)
-                            dst[k * 128] = make_float4(__uint_as_float(o[4 * k]), __uint_as_float(o[4 * k + 1]),
-                                                       __uint_as_float(o[4 * k + 2]), __uint_as_float(o[4 * k + 3]));
-                    }
+                    for (int k = 0; k < 8; ++k)
+                        dst[k * 128] = make_float4(__uint_as_float(o[4 * k]), __uint_as_float(o[4 * k + 1]),
+                                                   __uint_as_float(o[4 * k + 2]), __uint_as_float(o[4 * k + 3]));
                 }
+            } else if (ok) {
+                uint8_t *stage = s_out + (warp - 4) * 4096;
+                const int64_t dst_row = valid ? at : -1;
+#pragma unroll 1
+                for (int ch = 0; ch < COLS_W; ch += 32) {
+                    uint32_t o[32];
+                    tmem_ld32(ocol + col0 + ch, o);
+                    tmem_wait_ld();
+                    // (a sum, not a test for each: NaN and infinities stay in it)
+                    float check = 0.f;
+#pragma unroll
+                    for (int k = 0; k < 32; ++k) {
+                        const float f = __uint_as_float(o[k]) * inv;
+                        check = __fmaf_rn(f, 0.f, check);
+                        o[k] = __float_as_uint(f);
+                    }
+                    odd |= check != 0.f;
+                    __nv_bfloat16 *out = p.out + part * C::kCols + col0 + ch;
+                    if (C::kOutBytes == 0) {
+                        if (valid)
+                            store_out32(out + at * DH, o);
+                        continue;
+                    }
+                    // 32 columns into their half of the rows' 128 bytes
+                    const int half = ch / 32 % 2;
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        *reinterpret_cast<uint4 *>(stage + lane * 128 + (((half * 4 + k) ^ (lane & 7)) << 4)) = make_uint4(
+                            pack_bf16x2(__uint_as_float(o[8 * k]), __uint_as_float(o[8 * k + 1])),
+                            pack_bf16x2(__uint_as_float(o[8 * k + 2]), __uint_as_float(o[8 * k + 3])),
+                            pack_bf16x2(__uint_as_float(o[8 * k + 4]), __uint_as_float(o[8 * k + 5])),
+                            pack_bf16x2(__uint_as_float(o[8 * k + 6]), __uint_as_float(o[8 * k + 7])));
+                    if (half == 0)
+                        continue;
+                    __syncwarp();
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) {
+                        const int sr = k * 4 + lane / 8, sc = lane % 8;
+                        const int64_t to = __shfl_sync(0xffffffffu, dst_row, sr);
+                        const uint4 v = *reinterpret_cast<const uint4 *>(stage + sr * 128 + ((sc ^ (sr & 7)) << 4));
+                        if (to >= 0)
+                            *reinterpret_cast<uint4 *>(out - 32 + to * DH + sc * 8) = v;
+                    }
+                    __syncwarp();
+                }
+            }
             if (NT == 2 || wg == 0) {
                 if (!whole) {
                     rec[r] = m;
@@ -756,10 +894,13 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                     scored_row<DH>(p, x.b, x.m, __shfl_sync(0xffffffffu, tok, from), __shfl_sync(0xffffffffu, head, from));
                 }
             }
-            item += n;
             m_base[0] += (uint32_t)(n + 1) / 2;
             m_base[1] += (uint32_t)n / 2;
             pv_base += (uint32_t)n;
+            ++seg;
+            tc_fence_before();
+            if (NT == 1)
+                named_sync(1, 256);  // the next group's products overwrite both groups' columns
         }
     }
     tc_fence_before();
@@ -783,7 +924,7 @@ __global__ void __launch_bounds__(128) scored_tile_fold_kernel(const ScoreParams
         return;
     const int64_t total = w.header[0];
     const int2 gr = w.groups[g], en = w.entries[g / heads];
-    const int64_t g0 = gr.x, g1 = g0 + gr.y;
+    const int64_t g0 = (int64_t)gr.x + kGroupSetup, g1 = (int64_t)gr.x + gr.y;  // its key tiles
     int c0 = 0, n = 0;
     if (gr.y > 0) {
         auto owner = [&](int64_t item) {
@@ -805,7 +946,7 @@ __global__ void __launch_bounds__(128) scored_tile_fold_kernel(const ScoreParams
     const bool valid = row < m.qn * p.group;
     const int tok = valid ? row / p.group : 0, head = kvh * p.group + (valid ? row - tok * p.group : 0);
     auto record = [&](int c) {
-        return w.records + (2 * (int64_t)c + (g0 <= range_lo(total, c, w.ctas) ? 0 : 1)) * w.record_floats +
+        return w.records + (2 * (int64_t)c + (g0 < range_lo(total, c, w.ctas) ? 0 : 1)) * w.record_floats +
                t * tile_record(C::kCols);
     };
     // (where there are more CTAs than items, some have none)
