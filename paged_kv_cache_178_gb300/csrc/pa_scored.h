@@ -11,6 +11,38 @@ constexpr int kScoredMaxTilesHost = 8192;    // requests times tiles of rows tha
 // Tensor maps of K and V: boxes of 64 columns by the 16 tokens of one page and head.
 bool scored_pool_maps(const ScoreParams &p, int32_t head_dim, CUtensorMap (&tm)[2]);
 
+// wait_bar for warps that wait beside warps at work: a try may sleep for up to a
+// millisecond, and the abort flag and the clock are read between tries.
+// (wait_bar's loop, which reads both at every try, was more than half of all
+// instructions that scored_tiles_kernel issued.)
+__device__ __forceinline__ bool wait_parked(uint32_t bar, uint32_t parity, volatile int *abort_flag, ErrState *err,
+                                            int where)
+{
+    constexpr uint32_t kSleepNs = 1000000;
+    uint64_t t0 = 0;
+    for (;;) {
+        uint32_t done;
+        asm volatile("{\n\t.reg .pred p;\n\t"
+                     "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+                     "selp.u32 %0, 1, 0, p;\n\t}"
+                     : "=r"(done)
+                     : "r"(bar), "r"(parity), "r"(kSleepNs)
+                     : "memory");
+        if (done)
+            return true;
+        if (*abort_flag)
+            return false;
+        const uint64_t now = global_timer_ns();
+        if (t0 == 0)
+            t0 = now;
+        if (now - t0 > kWaitLimitNs) {
+            *abort_flag = 1;
+            record_error(err, kErrTimeout, ((long long)blockIdx.x << 8) | where);
+            return false;
+        }
+    }
+}
+
 // Keys that a tile of rows sees: a prefix and one range (a hull: keys inside
 // it may be hidden from every row).
 struct TileView {

@@ -5,10 +5,10 @@
 
 namespace pa {
 
-extern template cudaError_t launch_tiles<128, 2>(const ScoreParams &, const CUtensorMap (&)[2], const TileWork &, int, cudaStream_t);
-extern template cudaError_t launch_tiles<128, 1>(const ScoreParams &, const CUtensorMap (&)[2], const TileWork &, int, cudaStream_t);
-extern template cudaError_t launch_tiles<256, 1>(const ScoreParams &, const CUtensorMap (&)[2], const TileWork &, int, cudaStream_t);
-extern template cudaError_t launch_tiles<512, 1>(const ScoreParams &, const CUtensorMap (&)[2], const TileWork &, int, cudaStream_t);
+extern template cudaError_t launch_tiles<128, 2>(const ScoreParams &, const CUtensorMap (&)[3], const TileWork &, int, cudaStream_t);
+extern template cudaError_t launch_tiles<128, 1>(const ScoreParams &, const CUtensorMap (&)[3], const TileWork &, int, cudaStream_t);
+extern template cudaError_t launch_tiles<256, 1>(const ScoreParams &, const CUtensorMap (&)[3], const TileWork &, int, cudaStream_t);
+extern template cudaError_t launch_tiles<512, 1>(const ScoreParams &, const CUtensorMap (&)[3], const TileWork &, int, cudaStream_t);
 extern template cudaError_t tiles_attributes<128, 2>();
 extern template cudaError_t tiles_attributes<128, 1>();
 extern template cudaError_t tiles_attributes<256, 1>();
@@ -74,9 +74,19 @@ size_t scored_tiles_bytes(int32_t num_seqs, int32_t hkv, int group, int32_t head
 cudaError_t launch_scored_tiles(const ScoreParams &p, int32_t head_dim, void *workspace, cudaStream_t stream, char *info,
                                 size_t info_len)
 {
-    CUtensorMap tm[2];
-    if (!scored_pool_maps(p, head_dim, tm))
+    CUtensorMap pool[2], tm[3] = {};
+    if (!scored_pool_maps(p, head_dim, pool))
         return cudaErrorInvalidValue;
+    tm[0] = pool[0], tm[1] = pool[1];
+    const bool q_boxes = 128 % p.group == 0;
+    if (q_boxes) {
+        const cuuint64_t dims[3] = {(cuuint64_t)head_dim, (cuuint64_t)p.hq, (cuuint64_t)p.num_q_tokens};
+        const cuuint64_t strides[2] = {(cuuint64_t)head_dim * 2, (cuuint64_t)p.q_tok_stride * 2};
+        const cuuint32_t box[3] = {64, (cuuint32_t)p.group, (cuuint32_t)(128 / p.group)};
+        if (encode_tiled(&tm[2], CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<__nv_bfloat16 *>(p.q), dims, strides, box,
+                         CU_TENSOR_MAP_SWIZZLE_128B) != CUDA_SUCCESS)
+            return cudaErrorInvalidValue;
+    }
     const TileSizes s = tile_sizes(scored_tiles_bound(p.num_seqs, p.group, head_dim, p.max_query_len, p.num_q_tokens), p.hkv,
                                    p.group, head_dim, p.max_query_len);
     TileWork w{};
@@ -86,6 +96,7 @@ cudaError_t launch_scored_tiles(const ScoreParams &p, int32_t head_dim, void *wo
     w.entries = reinterpret_cast<int2 *>(ws + s.entries);
     w.records = reinterpret_cast<float *>(ws + s.records);
     w.record_floats = s.record_floats;
+    w.q_boxes = q_boxes;
     const int64_t items = s.tiles * p.hkv * s.parts * (((int64_t)p.max_seq_len + kTileKeys - 1) / kTileKeys + 1 + kGroupSetup);
     w.ctas = (int32_t)(items < kScoredSms ? items : kScoredSms);
     w.max_tiles = (int32_t)s.tiles;

@@ -19,12 +19,24 @@
 //   warp 0      copies units of 128 keys by 128 columns (32 KB, a TMA box for each
 //               page and 64 columns) into a ring, in the order of their use
 //   warp 1      issues the products (one thread)
-//   warps 2, 3  Q of a group, once the products of the group before have read theirs
+//   warps 2, 3  Q of a group, once the products of the group before have read theirs:
+//               TMA boxes where a row tile is whole tokens (G divides 128), else
+//               row by row (63.4 us instead of 61.2 at the prompt below)
 //   warps 4-7, 8-11   softmax of one score buffer each, a row to a thread, and
 //               the output at a group's end
 // Head dim 512: the output's halves are two groups, each with all of the scores
 // (tensor memory holds 256 columns of output beside the scores): three halves of
 // the products of a whole one instead of two, and no exchange.
+//
+// Measured: a prompt of 4096 tokens, 8 query and 2 KV heads of 128, capped: 61.2
+// us, 0.56 PFLOP/s of the products that causality leaves; a prompt of 8192 tokens
+// of five documents behind a prefix, 16 and 2 heads of 256, a bias by distance:
+// 299 us, 0.50 PFLOP/s of those that the documents leave.  What bounds it is the
+// chain of a step (scores, softmax, products), not the tensor pipe: a pair of
+// 128-key tiles takes 4.9 k cycles at head dim 128, its products 2.1 k, a tile's
+// softmax 2.0 to 2.4 k.  Starting a CTA and its first scores take 15 k more, 12
+// percent of the prompt's time.  Slower when tried: two issuing threads (69 us),
+// 16 softmax warps (74), tiles of 64 keys (79).
 #pragma once
 #include "pa_scan.cuh"
 #include "pa_scored.h"
@@ -67,6 +79,7 @@ struct TileWork {
     float *records;    // [2 * ctas] of record_floats
     int64_t record_floats;
     int32_t ctas, max_tiles;
+    int32_t q_boxes;   // a tile's rows are whole tokens: Q by TMA boxes
 };
 
 // Floats of one row tile's record: m[128], l[128], then the output as [columns / 4][128 rows][4].
@@ -182,25 +195,19 @@ __device__ __forceinline__ int stale_row(const TileGroup &x, int k0)
     return x.m.L % 16 && page >= k0 && page < k0 + kTileKeys && page_seen(x.v, page) ? x.m.L - k0 : kTileKeys;
 }
 
-// f(values of 32 columns, chunk) for the four chunks of a score tile, the next
-// chunk's load in flight meanwhile.  (Two copies of f, not four: a CTA lives for
-// some 15 tiles, so what the instruction cache has to fetch shows.)
+// f(values of 32 columns, chunk) for the four chunks of a score tile.  One copy
+// of f: a CTA lives for some 15 tiles, so what the instruction cache has to fetch
+// shows.  (With the next chunk's load in flight, in two copies of f: 65.6 and
+// 342 us at the sizes above, against 63.4 and 302 before Q came by TMA.)
 template <typename F>
 __device__ __forceinline__ void for_chunks(uint32_t scol, F f)
 {
-    uint32_t a[32], b[32];
-    tmem_ld32(scol, a);
-    tmem_wait_ld();
 #pragma unroll 1
-    for (int h = 0; h < 2; ++h) {
-        tmem_ld32(scol + h * 64 + 32, b);
-        f(a, 2 * h);
+    for (int ch = 0; ch < 4; ++ch) {
+        uint32_t a[32];
+        tmem_ld32(scol + ch * 32, a);
         tmem_wait_ld();
-        if (h == 0)
-            tmem_ld32(scol + 64, a);
-        f(b, 2 * h + 1);
-        if (h == 0)
-            tmem_wait_ld();
+        f(a, ch);
     }
 }
 
@@ -210,7 +217,8 @@ __device__ __forceinline__ uint32_t bits_below(int n) { return n <= 0 ? 0u : (n 
 template <int DH, int NT, int MODE>
 __global__ void __launch_bounds__(kTileThreads, 1)
     scored_tiles_kernel(const __grid_constant__ ScoreParams p, const __grid_constant__ CUtensorMap tm_k,
-                        const __grid_constant__ CUtensorMap tm_v, const TileWork w)
+                        const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_q,
+                        const TileWork w)
 {
     using C = TileCfg<DH, NT>;
     constexpr int RT = NT * 128, NS = C::kStages, UK = C::kUnitsK, UV = C::kUnitsV;
@@ -232,7 +240,9 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     volatile int *abort_flag = s_flags;
     const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
     auto bar = [&](int i) { return smem_addr(&bars[i]); };
-    auto wait = [&](int i, uint32_t parity) { return wait_bar(bar(i), parity & 1u, abort_flag, p.err, i); };
+    auto wait = [&](int i, uint32_t parity) { return wait_parked(bar(i), parity & 1u, abort_flag, p.err, i); };
+    // (the warp that issues the products spins: it must not wake late)
+    auto wait_spin = [&](int i, uint32_t parity) { return wait_bar(bar(i), parity & 1u, abort_flag, p.err, i); };
     if (tid == 0) {
         for (int i = 0; i < 2 * NS; ++i)
             mbar_init(bar(i), 1);
@@ -445,7 +455,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                 const int t = NT == 2 ? i % 2 : 0, j = i / NT;
                 for (int u = 0; ok && u < UK; ++u) {
                     const uint32_t at = base + pos_k(j) + u, stage = at % NS;
-                    ok = wait(B_FULL + stage, at / NS);
+                    ok = wait_spin(B_FULL + stage, at / NS);
                     if (!ok)
                         return;
                     const uint64_t qd = sdesc_sw128(smem_addr(s_q + t * 128 * DH * 2 + u * 32768), 16, 1024);
@@ -468,13 +478,13 @@ __global__ void __launch_bounds__(kTileThreads, 1)
             };
             auto pv = [&](int i) {
                 const int t = NT == 2 ? i % 2 : 0, j = i / NT;
-                ok = wait(B_P + i % 2, p_seen[i % 2]);
+                ok = wait_spin(B_P + i % 2, p_seen[i % 2]);
                 ++p_seen[i % 2];
                 for (int u = 0; ok && u < UV; ++u) {
                     const uint32_t at = base + pos_v(j, n) + u, stage = at % NS;
-                    ok = wait(B_FULL + stage, at / NS);
+                    ok = wait_spin(B_FULL + stage, at / NS);
                     if (ok && zero && j == n - 1 && t == 0) {
-                        ok = wait(B_Z + stage, zeroed >> stage);
+                        ok = wait_spin(B_Z + stage, zeroed >> stage);
                         zeroed ^= 1u << stage;
                     }
                     if (!ok)
@@ -496,7 +506,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                     mma_commit(bar(B_PV));
             };
             if (lane == 0) {
-                ok = wait(B_Q, seg);
+                ok = wait_spin(B_Q, seg);
                 for (int i = 0; ok && i < min(2, ni); ++i)
                     qk(i);
                 for (int i = 0; ok && i < ni; ++i) {
@@ -523,6 +533,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         // A group's rows as soon as the products of the group before have read
         // theirs: a thread keeps its column, so that all copies are in flight.
         constexpr int CH = DH / 8, STEP = 64 / CH;  // 16-byte vectors of a row; rows apart
+        uint32_t boxes = 0;  // segments that came by TMA
         const int qt = tid - 64, ch = qt % CH;
         const int step_tok = STEP / p.group, step_head = STEP - step_tok * p.group;
         for (int64_t item = lo; ok && item < hi; item < hi ? next_group<DH, NT>(p, x, heads) : (void)0) {
@@ -536,6 +547,23 @@ __global__ void __launch_bounds__(kTileThreads, 1)
             if (!ok)
                 break;
             const int kvh = x.hv / C::kSplit, rows = min(RT, x.m.qn * p.group - x.tile * RT);
+            if (w.q_boxes) {
+                // whole tokens to a row tile: a TMA box for each tile and 64 columns.
+                // (Rows past the request's are other tokens', or zeros: their
+                // results go nowhere.)
+                if (lane == 0) {
+                    if (warp == 2)
+                        mbar_arrive_expect_tx(bar(B_Q), C::kQBytes);
+                    else
+                        mbar_arrive(bar(B_Q));
+                }
+                __syncwarp();
+                if (warp == 2 && lane < NT * (DH / 64))
+                    tma_load_3d(smem_addr(s_q) + lane * 16384, &tm_q, bar(B_Q), lane % (DH / 64) * 64, kvh * p.group,
+                                x.m.qs + (x.tile * NT + lane / (DH / 64)) * (128 / p.group));
+                boxes = seg;
+                continue;
+            }
             const int first = x.tile * RT + qt / CH;
             int tok = first / p.group, head = first - tok * p.group;
             const __nv_bfloat16 *src = p.q + (int64_t)x.m.qs * p.q_tok_stride + (int64_t)kvh * p.group * DH + ch * 8;
@@ -561,6 +589,8 @@ __global__ void __launch_bounds__(kTileThreads, 1)
             if (lane == 0)
                 mbar_arrive(bar(B_Q));
         }
+        if (!ok && boxes && lane == 0)
+            wait_bar_drain(bar(B_Q), (boxes - 1) & 1u);
     } else {
         // --------------------------------------------------------- softmax --
         const int wg = (warp - 4) / 4, r = (warp % 4) * 32 + lane;
@@ -1004,7 +1034,7 @@ __global__ void __launch_bounds__(128) scored_tile_fold_kernel(const ScoreParams
 
 // --------------------------------------------------------------------- host --
 template <int DH, int NT>
-cudaError_t launch_tiles(const ScoreParams &p, const CUtensorMap (&tm)[2], const TileWork &w, int mode, cudaStream_t stream)
+cudaError_t launch_tiles(const ScoreParams &p, const CUtensorMap (&tm)[3], const TileWork &w, int mode, cudaStream_t stream)
 {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)w.ctas);
@@ -1019,7 +1049,7 @@ cudaError_t launch_tiles(const ScoreParams &p, const CUtensorMap (&tm)[2], const
     auto kern = mode == kModePlain    ? scored_tiles_kernel<DH, NT, kModePlain>
                 : mode == kModeCapped ? scored_tiles_kernel<DH, NT, kModeCapped>
                                       : scored_tiles_kernel<DH, NT, kModeAny>;
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, p, tm[0], tm[1], w);
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, p, tm[0], tm[1], tm[2], w);
     if (e != cudaSuccess)
         return e;
     using C = TileCfg<DH, NT>;

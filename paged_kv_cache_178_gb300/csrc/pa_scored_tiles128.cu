@@ -3,9 +3,9 @@
 
 namespace pa {
 
-template cudaError_t launch_tiles<128, 2>(const ScoreParams &, const CUtensorMap (&)[2], const TileWork &, int, cudaStream_t);
+template cudaError_t launch_tiles<128, 2>(const ScoreParams &, const CUtensorMap (&)[3], const TileWork &, int, cudaStream_t);
 template cudaError_t tiles_attributes<128, 2>();
-template cudaError_t launch_tiles<128, 1>(const ScoreParams &, const CUtensorMap (&)[2], const TileWork &, int, cudaStream_t);
+template cudaError_t launch_tiles<128, 1>(const ScoreParams &, const CUtensorMap (&)[3], const TileWork &, int, cudaStream_t);
 template cudaError_t tiles_attributes<128, 1>();
 
 }  // namespace pa

@@ -3,7 +3,7 @@
 
 namespace pa {
 
-template cudaError_t launch_tiles<512, 1>(const ScoreParams &, const CUtensorMap (&)[2], const TileWork &, int, cudaStream_t);
+template cudaError_t launch_tiles<512, 1>(const ScoreParams &, const CUtensorMap (&)[3], const TileWork &, int, cudaStream_t);
 template cudaError_t tiles_attributes<512, 1>();
 
 }  // namespace pa
