@@ -746,8 +746,15 @@ PA_API size_t pa_paged_attention_scored_workspace_size(int32_t num_seqs, int32_t
  *     another.
  *   - out, lse and the workspace may not share bytes with an input or with one
  *     another (PA_ERR_INVALID_ARG).
- * num_seqs <= 8192; num_seqs * max_query_len * Hkv <= INT32_MAX; max_seq_len <=
- * INT32_MAX - 4096 (PA_ERR_UNSUPPORTED).
+ *   - A query_start_loc that decreases may leave rows unwritten: its requests
+ *     may form more row tiles than the bounds below allow for.
+ * Limits (PA_ERR_UNSUPPORTED), with G = Hq / Hkv <= 128 and head dims of 128, 256
+ * and 512: num_seqs <= 8192; num_seqs * max_query_len * Hq <= INT32_MAX;
+ * max_seq_len <= INT32_MAX - 4096; where max_query_len * G > 32, with
+ *   tiles = min(num_seqs * ceil(max_query_len * G / R), num_q_tokens * G / R + num_seqs),
+ *   R = 256 at head dim 128 if max_query_len * G > 128, else 128,
+ * num_seqs + tiles <= 23998 and tiles * Hkv * (max_seq_len / 128 + 4) <= 2^30, and
+ * where it is not, num_seqs * Hkv * (max_seq_len / 32 + 2) <= 2^31.
  */
 PA_API pa_status pa_paged_attention_scored(const void *q, int64_t num_q_tokens, int64_t q_tok_stride,
                                            int32_t num_q_heads, const pa_kv_cache *cache,
