@@ -95,8 +95,24 @@ __device__ __forceinline__ TileBlocks tile_blocks(const TileView &v, int keys)
     return t;
 }
 
-// First item of CTA c's range.
-__device__ __forceinline__ int64_t range_lo(int64_t total, int c, int ctas) { return total * c / ctas; }
+// First item of CTA c's range: floor(total * c / ctas), in 32 bits (total is at
+// most INT32_MAX, ctas a few hundred).
+__device__ __forceinline__ int64_t range_lo(int64_t total, int c, int ctas)
+{
+    const uint32_t each = (uint32_t)total / (uint32_t)ctas, rest = (uint32_t)total - each * (uint32_t)ctas;
+    return (int64_t)(each * (uint32_t)c + rest * (uint32_t)c / (uint32_t)ctas);
+}
+
+// The CTA whose range has an item.
+__device__ __forceinline__ int range_owner(int64_t total, int64_t item, int ctas)
+{
+    int c = min((int)((float)item * (float)ctas / (float)total), ctas - 1);
+    while (range_lo(total, c + 1, ctas) <= item)
+        ++c;
+    while (range_lo(total, c, ctas) > item)
+        --c;
+    return c;
+}
 
 bool scored_rows_fits(int32_t num_seqs, int32_t hkv, int group, int32_t head_dim, int32_t max_query_len,
                       int32_t max_seq_len);

@@ -460,14 +460,15 @@ __global__ void __launch_bounds__(kFoldThreads) scored_fold_kernel(const ScorePa
     constexpr int E = DH / 128;  // 16-byte vectors of a lane
     __shared__ float s_part[kFoldWarps][DH];
     __shared__ float s_ml[2][kFoldWarps];
-    griddep_wait();
-    griddep_launch_dependents();
     const int g = blockIdx.x / w.rows, r = blockIdx.x - g * w.rows;
     const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
     const int st = g / p.hkv, kvh = g - st * p.hkv, b = st / w.qtiles, tile = st - b * w.qtiles;
+    // (the caller's inputs were there before the first kernel read them)
+    const ReqMeta m = score_meta(p, b);
+    griddep_wait();
+    griddep_launch_dependents();
     const int2 gr = w.groups[g];
     const int64_t total = *w.total;
-    const ReqMeta m = score_meta(p, b);
     if (!m.ok) {
         // every row of the request, whatever its number: the grid goes by the bounds
         if (m.sane && tile == 0 && kvh == 0 && r == 0) {
@@ -487,16 +488,8 @@ __global__ void __launch_bounds__(kFoldThreads) scored_fold_kernel(const ScorePa
     const int64_t g0 = gr.x, g1 = g0 + gr.y;
     int c0 = 0, n = 0;
     if (gr.y > 0) {
-        auto owner = [&](int64_t item) {
-            int c = (int)(item * w.ctas / total);
-            while (range_lo(total, c + 1, w.ctas) <= item)
-                ++c;
-            while (range_lo(total, c, w.ctas) > item)
-                --c;
-            return c;
-        };
-        c0 = owner(g0);
-        n = owner(g1 - 1) - c0 + 1;
+        c0 = range_owner(total, g0, w.ctas);
+        n = range_owner(total, g1 - 1, w.ctas) - c0 + 1;
     }
     // a warp takes every eighth part
     float mx = -INFINITY, l = 0.f;

@@ -957,16 +957,8 @@ __global__ void __launch_bounds__(128) scored_tile_fold_kernel(const ScoreParams
     const int64_t g0 = (int64_t)gr.x + kGroupSetup, g1 = (int64_t)gr.x + gr.y;  // its key tiles
     int c0 = 0, n = 0;
     if (gr.y > 0) {
-        auto owner = [&](int64_t item) {
-            int c = (int)(item * w.ctas / total);
-            while (range_lo(total, c + 1, w.ctas) <= item)
-                ++c;
-            while (range_lo(total, c, w.ctas) > item)
-                --c;
-            return c;
-        };
-        c0 = owner(g0);
-        n = owner(g1 - 1) - c0 + 1;
+        c0 = range_owner(total, g0, w.ctas);
+        n = range_owner(total, g1 - 1, w.ctas) - c0 + 1;
         if (n == 1)
             return;  // written by the CTA that had all of it
     }
