@@ -20,29 +20,30 @@ constexpr int kScanMaxSeqs = 8192;
 // the total) by all NTH threads of the CTA.  The returned total is exact in
 // 64 bits; off[] holds the low 32 bits, so callers check the total against
 // their own (32-bit) limit before they use it.  `warp_sums` is scratch for
-// NTH/32 values.  Ends with a CTA barrier.
-template <int NTH, typename Count>
-__device__ __forceinline__ long long block_exclusive_sums(int n, int32_t *off, long long *warp_sums, Count count)
+// NTH/32 values; of type int where the sums are known to fit.  Ends with a CTA
+// barrier.
+template <int NTH, typename Sum, typename Count>
+__device__ __forceinline__ Sum block_exclusive_sums(int n, int32_t *off, Sum *warp_sums, Count count)
 {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    long long base = 0;
+    Sum base = 0;
     for (int b0 = 0; b0 < n; b0 += NTH) {
         const int b = b0 + tid;
-        const long long c = b < n ? (long long)count(b) : 0;
-        long long incl = c;
+        const Sum c = b < n ? (Sum)count(b) : 0;
+        Sum incl = c;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
-            const long long x = __shfl_up_sync(0xffffffffu, incl, o);
+            const Sum x = __shfl_up_sync(0xffffffffu, incl, o);
             if (lane >= o)
                 incl += x;
         }
         if (lane == 31)
             warp_sums[warp] = incl;
         __syncthreads();
-        long long before = base, total = base;
+        Sum before = base, total = base;
 #pragma unroll
         for (int w = 0; w < NTH / 32; ++w) {
-            const long long s = warp_sums[w];
+            const Sum s = warp_sums[w];
             before += w < warp ? s : 0;
             total += s;
         }

@@ -103,7 +103,7 @@ __device__ __forceinline__ int64_t range_lo(int64_t total, int c, int ctas)
     return (int64_t)(each * (uint32_t)c + rest * (uint32_t)c / (uint32_t)ctas);
 }
 
-// The CTA whose range has an item.
+// The CTA whose range has an item (total >= ctas: every range has some).
 __device__ __forceinline__ int range_owner(int64_t total, int64_t item, int ctas)
 {
     int c = min((int)((float)item * (float)ctas / (float)total), ctas - 1);

@@ -71,21 +71,31 @@ __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], 
                  : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-// Workspace: the items before each group and its own, then the records.
+// Workspace: where each group's parts are, then the records.
 struct RowsWork {
-    int2 *groups;      // [num_groups] (first item, items)
-    int64_t *total;    // items of all groups
+    int2 *groups;      // [num_groups] (first CTA * 4 + its record (record_slot), CTAs that have a part)
     float *records;    // [2 * ctas + num_groups] of record_floats
     int64_t record_floats;
     int32_t ctas, qtiles, rows;  // rows of a tile that any request can fill
 };
 
-// Record of the part that CTA c (items [clo, chi)) has of a group (items [g0, g1))
-__device__ __forceinline__ int64_t record_slot(int g, int64_t g0, int64_t g1, int c, int64_t clo, int64_t chi, int ctas)
+// Record of the part that a CTA (items [clo, chi)) has of a group (items [g0, g1)):
+// the group's own (2) where that is all of it, else the CTA's first (0) or second.
+__device__ __forceinline__ int record_slot(int g0, int g1, int clo, int chi)
 {
-    if (g0 >= clo && g1 <= chi)
-        return 2 * (int64_t)ctas + g;
-    return 2 * (int64_t)c + (g0 <= clo ? 0 : 1);
+    return g0 >= clo && g1 <= chi ? 2 : (g0 <= clo ? 0 : 1);
+}
+__device__ __forceinline__ int64_t record_index(int slot, int g, int c, int max_ctas)
+{
+    return 2 * (int64_t)(slot == 2 ? max_ctas : c) + (slot == 2 ? g : slot);
+}
+
+// Entry of RowsWork::groups for items [g0, g1) of all.
+__device__ __forceinline__ int2 group_parts(int total, int g0, int g1, int ctas)
+{
+    const int c = range_owner(total, g0, ctas), last = range_owner(total, g1 - 1, ctas);
+    return make_int2(c * 4 + record_slot(g0, g1, (int)range_lo(total, c, ctas), (int)range_lo(total, c + 1, ctas)),
+                     last - c + 1);
 }
 
 template <int DH, int MT>
@@ -117,9 +127,9 @@ __global__ void __launch_bounds__(kRowsThreads, RowsCfg<DH>::kCtas)
 
     // ----------------------------------------------- items before each tile --
     const int ntiles = p.num_seqs * w.qtiles;
-    long long *scratch = reinterpret_cast<long long *>(s_max);
-    static_assert(2 * kRowsWarps * 16 * 4 >= (kRowsWarps + 1) * 8, "scan scratch");
-    const long long per_head = block_exclusive_sums<kRowsThreads>(ntiles, s_off, scratch, [&](int st) {
+    int *scratch = reinterpret_cast<int *>(s_max);  // (all sums fit: at most INT32_MAX items)
+    static_assert(2 * kRowsWarps * 16 >= kRowsWarps + 1, "scan scratch");
+    const int per_head = block_exclusive_sums<kRowsThreads>(ntiles, s_off, scratch, [&](int st) {
         const int b = st / w.qtiles, tile = st - b * w.qtiles;
         const ReqMeta m = score_meta(p, b);
         if (!m.ok) {
@@ -130,17 +140,21 @@ __global__ void __launch_bounds__(kRowsThreads, RowsCfg<DH>::kCtas)
         const int rows = m.qn * p.group;
         return tile_blocks(tile_view(p, b, m, min(tile * R, rows), min(tile * R + R, rows)), KB).count;
     });
-    const int64_t total = per_head * p.hkv;
-    const int ctas = w.ctas, c = blockIdx.x;
-    for (int g = c * kRowsThreads + tid; g < ntiles * p.hkv; g += ctas * kRowsThreads) {
-        const int st = g / p.hkv, n = s_off[st + 1] - s_off[st];
-        w.groups[g] = make_int2(s_off[st] * p.hkv + (g - st * p.hkv) * n, n);
-    }
-    if (c == 0 && tid == 0)
-        *w.total = total;
-    const int64_t lo = range_lo(total, c, ctas), hi = range_lo(total, c + 1, ctas);
-    if (lo >= hi)
+    const int total = per_head * p.hkv, ctas = min(w.ctas, total), c = blockIdx.x;
+    // where the fold finds a group's parts
+    auto write_groups = [&](int at, int step) {
+        for (int g = at; g < ntiles * p.hkv; g += step) {
+            const int st = g / p.hkv, n = s_off[st + 1] - s_off[st];
+            const int first = s_off[st] * p.hkv + (g - st * p.hkv) * n;
+            w.groups[g] = n ? group_parts(total, first, first + n, ctas) : make_int2(0, 0);
+        }
+    };
+    if (c >= ctas) {
+        if (warp == kRowsWarps)
+            write_groups(c * 32 + lane, w.ctas * 32);
         return;
+    }
+    const int lo = (int)range_lo(total, c, ctas), hi = (int)range_lo(total, c + 1, ctas);
     if (tid == 0) {
         for (int s = 0; s < NS; ++s) {
             mbar_init(full(s), 1);
@@ -154,20 +168,20 @@ __global__ void __launch_bounds__(kRowsThreads, RowsCfg<DH>::kCtas)
     // the group of an item, as both sides walk through the range
     struct Group {
         int st, b, tile, kvh, g;
-        int64_t g0, g1;
+        int g0, g1;
         ReqMeta m;
         TileView v;
         TileBlocks t;
     };
-    auto group_of = [&](int64_t item) {
+    auto group_of = [&](int item) {
         Group x;
-        const int ph = (int)div_floor(item, p.hkv);  // no tile's items before ph / hkv are past the item
+        const int ph = item / p.hkv;  // no tile's items before ph / hkv are past the item
         x.st = owner_of(s_off, ntiles, ph);
         const int n = s_off[x.st + 1] - s_off[x.st];
-        const int64_t first = (int64_t)s_off[x.st] * p.hkv;
-        x.kvh = (int)div_floor(item - first, n);
+        const int first = s_off[x.st] * p.hkv;
+        x.kvh = (item - first) / n;
         x.g = x.st * p.hkv + x.kvh;
-        x.g0 = first + (int64_t)x.kvh * n;
+        x.g0 = first + x.kvh * n;
         x.g1 = x.g0 + n;
         x.b = x.st / w.qtiles;
         x.tile = x.st - x.b * w.qtiles;
@@ -187,12 +201,12 @@ __global__ void __launch_bounds__(kRowsThreads, RowsCfg<DH>::kCtas)
         const uint64_t policy = l2_policy_evict_first();
         int stage = 0, round = 0, issued = 0;
         bool ok = true;
-        for (int64_t item = lo; ok && item < hi;) {
+        for (int item = lo; ok && item < hi;) {
             const Group x = group_of(item);
             const int32_t *bt = p.block_tables + (int64_t)x.b * p.max_blocks;
-            const int64_t end = min(hi, x.g1);
+            const int end = min(hi, x.g1);
             for (; item < end; ++item) {
-                const int k0 = block_key(x, (int)(item - x.g0)) + pg * 16;
+                const int k0 = block_key(x, item - x.g0) + pg * 16;
                 // pages that hold no key which the tile sees are not read
                 const bool need = k0 < x.v.prefix || (k0 < x.v.hi && k0 + 16 > x.v.lo);
                 int id = need ? __ldg(bt + k0 / 16) : -1;
@@ -227,6 +241,7 @@ __global__ void __launch_bounds__(kRowsThreads, RowsCfg<DH>::kCtas)
         if (!ok && lane == 0)
             for (int i = max(0, issued - NS); i < issued; ++i)
                 wait_bar_drain(full(i % NS), (i / NS) & 1);
+        write_groups(c * 32 + lane, w.ctas * 32);
         return;
     }
 
@@ -234,9 +249,9 @@ __global__ void __launch_bounds__(kRowsThreads, RowsCfg<DH>::kCtas)
     const int g8 = lane / 4, t4 = lane % 4;
     int stage = 0, parity = 0;
     bool ok = true;
-    for (int64_t item = lo; item < hi;) {
+    for (int item = lo; item < hi;) {
         const Group x = group_of(item);
-        const int64_t end = min(hi, x.g1);
+        const int end = min(hi, x.g1);
         const int rows = min(R, x.m.qn * p.group - x.tile * R);
         named_sync(1, kRowsWarps * 32);  // Q and the sums of the group before have been read
         // Q into shared memory; rows past the tile's are zero
@@ -285,7 +300,7 @@ __global__ void __launch_bounds__(kRowsThreads, RowsCfg<DH>::kCtas)
                 o[i][j][0] = o[i][j][1] = o[i][j][2] = o[i][j][3] = 0.f;
         named_sync(1, kRowsWarps * 32);
         for (; item < end; ++item) {
-            const int k0 = block_key(x, (int)(item - x.g0));
+            const int k0 = block_key(x, item - x.g0);
             if (ok)
                 ok = wait_bar(full(stage), parity, s_abort, p.err, stage);
             const uint32_t kb = smem_addr(s_kv + stage * 2 * C::kView), vb = kb + C::kView;
@@ -424,7 +439,7 @@ __global__ void __launch_bounds__(kRowsThreads, RowsCfg<DH>::kCtas)
                 s_sum[warp * R + 8 * i + g8] = ok ? l[i] : __int_as_float(0x7FC00000);
         }
         named_sync(1, kRowsWarps * 32);
-        float *rec = w.records + record_slot(x.g, x.g0, x.g1, c, lo, hi, ctas) * w.record_floats;
+        float *rec = w.records + record_index(record_slot(x.g0, x.g1, lo, hi), x.g, c, w.ctas) * w.record_floats;
         if (warp == 0 && t4 == 0)
 #pragma unroll
             for (int i = 0; i < 2 * MT; ++i) {
@@ -467,8 +482,7 @@ __global__ void __launch_bounds__(kFoldThreads) scored_fold_kernel(const ScorePa
     const ReqMeta m = score_meta(p, b);
     griddep_wait();
     griddep_launch_dependents();
-    const int2 gr = w.groups[g];
-    const int64_t total = *w.total;
+    const int2 parts = w.groups[g];
     if (!m.ok) {
         // every row of the request, whatever its number: the grid goes by the bounds
         if (m.sane && tile == 0 && kvh == 0 && r == 0) {
@@ -484,13 +498,6 @@ __global__ void __launch_bounds__(kFoldThreads) scored_fold_kernel(const ScorePa
     const int row = tile * tile_rows + r, tok = row / p.group, h = kvh * p.group + row - tok * p.group;
     if (tok >= m.qn)
         return;
-    // CTAs that have a part of the group
-    const int64_t g0 = gr.x, g1 = g0 + gr.y;
-    int c0 = 0, n = 0;
-    if (gr.y > 0) {
-        c0 = range_owner(total, g0, w.ctas);
-        n = range_owner(total, g1 - 1, w.ctas) - c0 + 1;
-    }
     // a warp takes every eighth part
     float mx = -INFINITY, l = 0.f;
     float4 o[E];
@@ -498,12 +505,8 @@ __global__ void __launch_bounds__(kFoldThreads) scored_fold_kernel(const ScorePa
     for (int e = 0; e < E; ++e)
         o[e] = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
-    for (int i = warp; i < n; i += kFoldWarps) {
-        const int c = c0 + i;
-        const int64_t clo = range_lo(total, c, w.ctas), chi = range_lo(total, c + 1, w.ctas);
-        if (clo >= chi)
-            continue;  // (more CTAs than items)
-        const float *rec = w.records + record_slot(g, g0, g1, c, clo, chi, w.ctas) * w.record_floats;
+    for (int i = warp; i < parts.y; i += kFoldWarps) {
+        const float *rec = w.records + record_index(i == 0 ? parts.x & 3 : 0, g, (parts.x >> 2) + i, w.ctas) * w.record_floats;
         const float mr = __ldcg(rec + r), lr = __ldcg(rec + tile_rows + r);
         const float top = fmaxf(mx, mr);
         const float a = mx == top ? 1.f : ex2(mx - top), k = mr == top ? 1.f : ex2(mr - top);
@@ -593,7 +596,7 @@ size_t scored_rows_bytes(int32_t num_seqs, int32_t hkv, int group, int32_t head_
 {
     const int64_t groups = num_seqs * rows_tiles(max_query_len, group) * hkv;
     const int r = rows_of(max_query_len, group);
-    return 256 + align256((size_t)groups * 8) +
+    return align256((size_t)groups * 8) +
            (size_t)(2 * rows_ctas(groups, head_dim, max_seq_len) + groups) * r * (head_dim + 2) * 4;
 }
 
@@ -633,9 +636,8 @@ cudaError_t launch_scored_rows(const ScoreParams &p, int32_t head_dim, void *wor
     w.ctas = rows_ctas(groups, head_dim, p.max_seq_len);
     w.rows = (int32_t)((int64_t)p.max_query_len * p.group < r ? p.max_query_len * p.group : r);
     uint8_t *ws = static_cast<uint8_t *>(workspace);
-    w.total = reinterpret_cast<int64_t *>(ws);
-    w.groups = reinterpret_cast<int2 *>(ws + 256);
-    w.records = reinterpret_cast<float *>(ws + 256 + align256((size_t)groups * 8));
+    w.groups = reinterpret_cast<int2 *>(ws);
+    w.records = reinterpret_cast<float *>(ws + align256((size_t)groups * 8));
     w.record_floats = (int64_t)r * (head_dim + 2);
     snprintf(info, info_len, "scored attention dh=%d kernel=rows-r%d grid=%d tiles=%d", head_dim, r, w.ctas, w.qtiles);
     const bool two = r == 32;

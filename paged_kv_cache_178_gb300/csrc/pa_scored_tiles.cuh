@@ -267,11 +267,11 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     // --------------------------------------- items before each row tile ----
     // (in the ring, which is not in use yet; the roles then walk on from the
     // range's first group by themselves)
-    const int heads = p.hkv * C::kSplit, ctas = w.ctas, c = blockIdx.x;
+    const int heads = p.hkv * C::kSplit, c = blockIdx.x;
     int32_t *s_first = reinterpret_cast<int32_t *>(s_ring);  // [num_seqs + 1] first row tile of a request
     int32_t *s_off = s_first + p.num_seqs + 1;               // [row tiles + 1] first item of a row tile (of one head)
-    long long *scratch = reinterpret_cast<long long *>(small + 512);
-    const long long tiles = block_exclusive_sums<kTileThreads>(p.num_seqs, s_first, scratch, [&](int b) {
+    int *scratch = reinterpret_cast<int *>(small + 512);  // (all sums fit: at most INT32_MAX items)
+    const int tiles = block_exclusive_sums<kTileThreads>(p.num_seqs, s_first, scratch, [&](int b) {
         const ReqMeta m = score_meta(p, b);
         if (!m.ok && c == 0)
             record_error(p.err, kErrBadMetadata, b);
@@ -279,20 +279,20 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     });
     // (the host's bound holds for requests that do not overlap; a query_start_loc
     // that decreases may give more: those rows are left out, its request is named)
-    const int ntiles = (int)(tiles < w.max_tiles ? tiles : w.max_tiles);
-    const long long per_head = block_exclusive_sums<kTileThreads>(ntiles, s_off, scratch, [&](int e) {
+    const int ntiles = min(tiles, w.max_tiles);
+    const int per_head = block_exclusive_sums<kTileThreads>(ntiles, s_off, scratch, [&](int e) {
         const int b = owner_of(s_first, p.num_seqs, e), tile = e - s_first[b];
         const ReqMeta m = score_meta(p, b);
         const int rows = m.qn * p.group;
         const int n = tile_blocks(tile_view(p, b, m, min(tile * RT, rows), min(tile * RT + RT, rows)), kTileKeys).count;
         return n ? n + kGroupSetup : 0;
     });
-    const int64_t total = per_head * heads;
-    for (int g = c * kTileThreads + tid; g < ntiles * heads; g += ctas * kTileThreads) {
+    const int total = per_head * heads, ctas = min(w.ctas, total);
+    for (int g = c * kTileThreads + tid; g < ntiles * heads; g += w.ctas * kTileThreads) {
         const int e = g / heads, n = s_off[e + 1] - s_off[e];
         w.groups[g] = make_int2(s_off[e] * heads + (g - e * heads) * n, n);
     }
-    for (int e = c * kTileThreads + tid; e < ntiles; e += ctas * kTileThreads) {
+    for (int e = c * kTileThreads + tid; e < ntiles; e += w.ctas * kTileThreads) {
         const int b = owner_of(s_first, p.num_seqs, e);
         w.entries[e] = make_int2(b, e - s_first[b]);
     }
@@ -300,7 +300,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         w.header[0] = total;
         w.header[1] = ntiles;
     }
-    for (int b = c; b < p.num_seqs; b += ctas) {
+    for (int b = c; b < p.num_seqs; b += w.ctas) {
         const ReqMeta m = score_meta(p, b);
         if (!m.ok && m.sane) {
             const int64_t first = (int64_t)m.qs * p.hq, n = (int64_t)m.qn * p.hq;
@@ -311,11 +311,11 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                     p.lse[first + i] = __int_as_float(0x7FC00000);
         }
     }
-    const int64_t lo = range_lo(total, c, ctas), hi = range_lo(total, c + 1, ctas);
-    if (lo >= hi)
+    if (c >= ctas)
         return;
+    const int64_t lo = range_lo(total, c, ctas), hi = range_lo(total, c + 1, ctas);
     if (tid == 0) {
-        const int e = owner_of(s_off, ntiles, (int)div_floor(lo, heads));
+        const int e = owner_of(s_off, ntiles, (int)lo / heads);
         const int b = owner_of(s_first, p.num_seqs, e);
         s_flags[4] = b;
         s_flags[5] = e - s_first[b];
@@ -952,13 +952,13 @@ __global__ void __launch_bounds__(128) scored_tile_fold_kernel(const ScoreParams
     const int unit = blockIdx.x / CB, cb = blockIdx.x % CB, g = unit / NT, t = unit % NT;
     if (g >= w.header[1] * heads)
         return;
-    const int64_t total = w.header[0];
+    const int total = (int)w.header[0], ctas = min(w.ctas, total);
     const int2 gr = w.groups[g], en = w.entries[g / heads];
     const int64_t g0 = (int64_t)gr.x + kGroupSetup, g1 = (int64_t)gr.x + gr.y;  // its key tiles
     int c0 = 0, n = 0;
     if (gr.y > 0) {
-        c0 = range_owner(total, g0, w.ctas);
-        n = range_owner(total, g1 - 1, w.ctas) - c0 + 1;
+        c0 = range_owner(total, g0, ctas);
+        n = range_owner(total, g1 - 1, ctas) - c0 + 1;
         if (n == 1)
             return;  // written by the CTA that had all of it
     }
@@ -968,23 +968,18 @@ __global__ void __launch_bounds__(128) scored_tile_fold_kernel(const ScoreParams
     const bool valid = row < m.qn * p.group;
     const int tok = valid ? row / p.group : 0, head = kvh * p.group + (valid ? row - tok * p.group : 0);
     auto record = [&](int c) {
-        return w.records + (2 * (int64_t)c + (g0 < range_lo(total, c, w.ctas) ? 0 : 1)) * w.record_floats +
-               t * tile_record(C::kCols);
+        // (the group began in c0's range, and goes on in the others)
+        return w.records + (2 * (int64_t)c + (c == c0 ? 1 : 0)) * w.record_floats + t * tile_record(C::kCols);
     };
-    // (where there are more CTAs than items, some have none)
-    auto has_part = [&](int c) { return range_lo(total, c, w.ctas) < range_lo(total, c + 1, w.ctas); };
     float top = -INFINITY;
     for (int i = 0; i < n; ++i)
-        if (has_part(c0 + i))
-            top = fmaxf(top, __ldcg(record(c0 + i) + r));
+        top = fmaxf(top, __ldcg(record(c0 + i) + r));
     float sum = 0.f, o[32];
 #pragma unroll
     for (int k = 0; k < 32; ++k)
         o[k] = 0.f;
 #pragma unroll 2
     for (int i = 0; i < n; ++i) {
-        if (!has_part(c0 + i))
-            continue;
         const float *rec = record(c0 + i);
         const float mi = __ldcg(rec + r), f = mi == top ? 1.f : ex2(mi - top);
         sum += __ldcg(rec + 128 + r) * f;
