@@ -13,7 +13,8 @@
 namespace pa {
 
 // ------------------------------------------------------------ page copies --
-// Bytes in, bytes out: bound by the memory.  A warp takes 4 KB of one view
+// Bytes in, bytes out: bound by the memory (2000 pages of 8 heads of 128 in two
+// layers: 78.9 us, 6.64 TB/s; 16 pages in four layers: 2.8 us).  A warp takes 4 KB of one view
 // (K or V) of one page at a time, eight 16-byte vectors a lane, all loaded
 // before the first is stored.
 constexpr int kCopyThreads = 256;
@@ -91,9 +92,11 @@ cudaError_t launch_copy_pages(const CopyArgs &a, ErrState *err, cudaStream_t str
 // advance in place.  The sums over the requests are repeated by every CTA.
 // A CTA to 1024 pages or so, up to 16: the large calls are bound by what an SM
 // does with scattered words (an atomic takes it 3 cycles, a load 1.5).  16
-// instead of 8: 192 forks of 36 k pages 14.4 -> 11.0 us, a release of 35 k
-// references 27.4 -> 21.6, a pool of 300000 pages 34.0 -> 24.3; calls for few
-// pages (a CTA to four) take 6 to 11 us, half of it the sums of the requests.
+// instead of 8 took 192 forks of 36 k pages from 14.4 to 11.0 us, a release of 35
+// k references from 27.4 to 21.6 and a pool of 300000 pages from 34.0 to 24.3.
+// Measured: those calls 9.3, 20.6 and 19.3 us; 4 forks of a prompt 4.5 us, the
+// drafts of 64 requests 9.9, a pool of 2048 pages 7.8: chains of loads, sums and
+// barriers, of some 2 us for a launch.
 constexpr int kPageThreads = 1024;
 constexpr int kPageWarps = kPageThreads / 32;
 constexpr int kPageClusterMax = 16;
@@ -150,7 +153,7 @@ __global__ void __launch_bounds__(kPageThreads, 1) fork_requests_kernel(const Pa
     griddep_wait();
     griddep_launch_dependents();
     extern __shared__ int32_t s_fork[];
-    __shared__ longlong2 s_sums[kPageWarps];
+    __shared__ int2 s_sums[kPageWarps];
     const int n = a.num_forks, tid = threadIdx.x;
     int32_t *s_page = s_fork;         // [n + 1] first page of a fork's child among all
     int32_t *s_tail = s_page + n + 1; // [n + 1] forks before it with a partial page
@@ -168,7 +171,7 @@ __global__ void __launch_bounds__(kPageThreads, 1) fork_requests_kernel(const Pa
     }
     copy_shares(a);
     __syncthreads();
-    longlong2 total;
+    int2 total;  // (num_seqs * max_blocks is below 2^31)
     block_exclusive_sums2<kPageThreads>(n, s_page, s_tail, s_sums, total, [&](int i, int &pages, int &tails) {
         const int p = a.parents[i], c = a.children[i];
         int len = -1;
@@ -185,11 +188,10 @@ __global__ void __launch_bounds__(kPageThreads, 1) fork_requests_kernel(const Pa
             record_error(err, kErrBadMetadata, i);
         }
     });
-    const long long pages = total.x, tails = total.y;
+    const int pages = total.x, tails = total.y;
     const bool bad_cursor = cursor < 0 || cursor > a.num_free;
-    const bool short_pages = !bad_cursor && tails > (long long)a.num_free - cursor;
-    const bool too_many = pages > INT32_MAX;
-    const bool empty = bad_cursor || short_pages || too_many;
+    const bool short_pages = !bad_cursor && tails > a.num_free - cursor;
+    const bool empty = bad_cursor || short_pages;
     cluster_sync_all();  // every CTA has read what advances in place; shares_out is complete
     const int gtid = blockIdx.x * kPageThreads + tid, gsize = gridDim.x * kPageThreads;
     if (gtid == 0) {
@@ -197,7 +199,7 @@ __global__ void __launch_bounds__(kPageThreads, 1) fork_requests_kernel(const Pa
             record_error(err, kErrBudget, tails);
         else if (empty)
             record_error(err, kErrBadMetadata, n);
-        *a.cursor_out = empty ? cursor : cursor + (int)tails;
+        *a.cursor_out = empty ? cursor : cursor + tails;
     }
     for (int b = gtid; b < a.num_seqs; b += gsize) {
         const int i = s_owner[b], len = !empty && i != INT32_MAX ? s_len[i] : -1;
@@ -253,14 +255,14 @@ __global__ void __launch_bounds__(kPageThreads, 1) release_pages_kernel(const Pa
     griddep_wait();
     griddep_launch_dependents();
     extern __shared__ int32_t s_rel[];
-    __shared__ long long s_sums[kPageWarps];
+    __shared__ int s_sums[kPageWarps];
     __shared__ int32_t s_freed[kPageWarps];  // pages that a warp frees
     const int n = a.num_seqs, tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
     int32_t *s_off = s_rel;          // [n + 1] first dropped page of a request among all
     int32_t *s_keep = s_off + n + 1; // [n] tokens that stay
     const int64_t limit = (int64_t)a.max_blocks * 16;
     const int cursor = *a.cursor_in;
-    const long long total = block_exclusive_sums<kPageThreads>(n, s_off, s_sums, [&](int b) {
+    const int total = block_exclusive_sums<kPageThreads>(n, s_off, s_sums, [&](int b) {
         const int c = a.context_lens[b], k = a.keep_lens[b];
         int keep = c;
         bool ok = c >= 0 && (int64_t)c <= limit && k <= c;
@@ -283,7 +285,7 @@ __global__ void __launch_bounds__(kPageThreads, 1) release_pages_kernel(const Pa
     cluster_sync_all();
     const int gtid = blockIdx.x * kPageThreads + tid, gsize = gridDim.x * kPageThreads;
     // a warp takes 32 neighbouring references at a time of a range of its own
-    const int items = empty ? 0 : (int)total;
+    const int items = empty ? 0 : total;
     const int warps = gridDim.x * kPageWarps, per = ((items + warps - 1) / warps + 31) / 32 * 32;
     const int64_t lo = (int64_t)(blockIdx.x * kPageWarps + warp) * per;
     const int64_t hi = lo + per < items ? lo + per : items;
@@ -412,7 +414,7 @@ __global__ void __launch_bounds__(kPageThreads, 1) compact_pages_kernel(const Pa
     griddep_wait();
     griddep_launch_dependents();
     extern __shared__ int32_t s_comp[];
-    __shared__ long long s_sums[kPageWarps];
+    __shared__ int s_sums[kPageWarps];
     const int n = a.num_seqs, tid = threadIdx.x, blocks = (int)a.num_blocks;
     const int words = (blocks + 31) / 32, pairs = (words + 1) / 2;
     uint32_t *s_bits = reinterpret_cast<uint32_t *>(s_comp);             // [2 * pairs]
@@ -423,7 +425,7 @@ __global__ void __launch_bounds__(kPageThreads, 1) compact_pages_kernel(const Pa
     const int cursor = *a.cursor_in;
     for (int w = gtid; w < words; w += gsize)
         a.bitmap[w] = 0;
-    const long long total = block_exclusive_sums<kPageThreads>(n, s_off, s_sums, [&](int b) {
+    const int total = block_exclusive_sums<kPageThreads>(n, s_off, s_sums, [&](int b) {
         const int c = a.context_lens[b];
         if (c >= 0 && (int64_t)c <= limit)
             return pages_of(c);
@@ -448,7 +450,7 @@ __global__ void __launch_bounds__(kPageThreads, 1) compact_pages_kernel(const Pa
     for (int w = tid; w < 2 * pairs; w += kPageThreads)
         s_bits[w] = w < words ? __ldcg(a.bitmap + w) : 0u;
     __syncthreads();
-    const int live = (int)block_exclusive_sums<kPageThreads>(
+    const int live = block_exclusive_sums<kPageThreads>(
         pairs, s_count, s_sums, [&](int i) { return __popc(s_bits[2 * i]) + __popc(s_bits[2 * i + 1]); });
     auto is_live = [&](int id) { return (s_bits[id >> 5] >> (id & 31)) & 1u; };
     // pages in use below id

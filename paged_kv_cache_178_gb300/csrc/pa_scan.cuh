@@ -16,6 +16,28 @@ __device__ __forceinline__ int64_t div_floor(int64_t a, int64_t b)
 // Largest batch those kernels take: their offsets sit in shared memory.
 constexpr int kScanMaxSeqs = 8192;
 
+// Adds up what the warps of a CTA left in warp_sums: `before` gets the sums of
+// the warps before this one, `all` those of all NTH / 32.  (In 32 bits a lane
+// reads one and the warp reduces: with 32 warps that read all 32, the reads took a
+// thousand cycles.)
+template <int NTH, typename Sum>
+__device__ __forceinline__ void add_warp_sums(const Sum *warp_sums, int stride, Sum &before, Sum &all)
+{
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    if constexpr (sizeof(Sum) == 4) {
+        const Sum s = lane < NTH / 32 ? warp_sums[lane * stride] : 0;
+        before += __reduce_add_sync(0xffffffffu, lane < warp ? s : 0);
+        all += __reduce_add_sync(0xffffffffu, s);
+    } else {
+#pragma unroll
+        for (int w = 0; w < NTH / 32; ++w) {
+            const Sum s = warp_sums[w * stride];
+            before += w < warp ? s : 0;
+            all += s;
+        }
+    }
+}
+
 // Exclusive prefix sums of count(b), b in [0, n), into off[0..n] (off[n] =
 // the total) by all NTH threads of the CTA.  The returned total is exact in
 // 64 bits; off[] holds the low 32 bits, so callers check the total against
@@ -41,12 +63,7 @@ __device__ __forceinline__ Sum block_exclusive_sums(int n, int32_t *off, Sum *wa
             warp_sums[warp] = incl;
         __syncthreads();
         Sum before = base, total = base;
-#pragma unroll
-        for (int w = 0; w < NTH / 32; ++w) {
-            const Sum s = warp_sums[w];
-            before += w < warp ? s : 0;
-            total += s;
-        }
+        add_warp_sums<NTH>(warp_sums, 1, before, total);
         if (b < n)
             off[b] = (int32_t)(before + incl - c);
         base = total;
@@ -85,14 +102,8 @@ __device__ __forceinline__ void block_exclusive_sums2(int n, int32_t *off0, int3
             warp_sums[warp] = Pair{i0, i1};
         __syncthreads();
         Pair before = base;
-#pragma unroll
-        for (int w = 0; w < NTH / 32; ++w) {
-            const Pair s = warp_sums[w];
-            before.x += w < warp ? s.x : 0;
-            before.y += w < warp ? s.y : 0;
-            base.x += s.x;
-            base.y += s.y;
-        }
+        add_warp_sums<NTH>(&warp_sums->x, 2, before.x, base.x);
+        add_warp_sums<NTH>(&warp_sums->y, 2, before.y, base.y);
         if (b < n) {
             off0[b] = (int32_t)(before.x + i0 - c0);
             off1[b] = (int32_t)(before.y + i1 - c1);

@@ -28,13 +28,13 @@
 // (tensor memory holds 256 columns of output beside the scores): three halves of
 // the products of a whole one instead of two, and no exchange.
 //
-// Measured: a prompt of 4096 tokens, 8 query and 2 KV heads of 128, capped: 61.2
+// Measured: a prompt of 4096 tokens, 8 query and 2 KV heads of 128, capped: 61
 // us, 0.56 PFLOP/s of the products that causality leaves; a prompt of 8192 tokens
 // of five documents behind a prefix, 16 and 2 heads of 256, a bias by distance:
-// 299 us, 0.50 PFLOP/s of those that the documents leave.  What bounds it is the
+// 289 us, 0.52 PFLOP/s of those that the documents leave.  What bounds it is the
 // chain of a step (scores, softmax, products), not the tensor pipe: a pair of
 // 128-key tiles takes 4.9 k cycles at head dim 128, its products 2.1 k, a tile's
-// softmax 2.0 to 2.4 k.  Starting a CTA and its first scores take 15 k more, 12
+// softmax 2.0 to 2.4 k (of them 1.4 k issue slots where it is capped).  Starting a CTA and its first scores take 15 k more, 12
 // percent of the prompt's time.  Slower when tried: two issuing threads (69 us),
 // 16 softmax warps (74), tiles of 64 keys (79).
 #pragma once
@@ -136,7 +136,7 @@ __device__ __forceinline__ TileView warp_tile_view(const ScoreParams &p, int b, 
 // One group's part in a CTA's range, as every role walks through it.
 struct TileGroup {
     int b, tile, hv;    // request, row tile, (KV head, part of the columns)
-    int64_t g0;         // first item
+    int g0;             // first item
     int n, w;           // key tiles, items (kGroupSetup more, or none)
     ReqMeta m;
     TileView v;
@@ -313,9 +313,9 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     }
     if (c >= ctas)
         return;
-    const int64_t lo = range_lo(total, c, ctas), hi = range_lo(total, c + 1, ctas);
+    const int lo = (int)range_lo(total, c, ctas), hi = (int)range_lo(total, c + 1, ctas);
     if (tid == 0) {
-        const int e = owner_of(s_off, ntiles, (int)lo / heads);
+        const int e = owner_of(s_off, ntiles, lo / heads);
         const int b = owner_of(s_first, p.num_seqs, e);
         s_flags[4] = b;
         s_flags[5] = e - s_first[b];
@@ -336,20 +336,19 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     x.m = score_meta(p, x.b);
     load_group<DH, NT>(p, x);
     {
-        const int64_t first = (int64_t)s_flags[6] * heads;
-        x.hv = (int)((lo - first) / x.w);
-        x.g0 = first + (int64_t)x.hv * x.w;
+        const int first = s_flags[6] * heads;
+        x.hv = (lo - first) / x.w;
+        x.g0 = first + x.hv * x.w;
     }
     // this CTA's key tiles [j0, j0 + n) of the group, and the items after them
     struct Part {
-        int j0, n;
-        int64_t next;
+        int j0, n, next;
     };
-    auto part_of = [&](int64_t item) {
+    auto part_of = [&](int item) {
         Part s;
         s.next = min(hi, x.g0 + x.w);
-        s.j0 = max((int)(item - x.g0) - kGroupSetup, 0);
-        s.n = max((int)(s.next - x.g0) - kGroupSetup, 0) - s.j0;
+        s.j0 = max(item - x.g0 - kGroupSetup, 0);
+        s.n = max(s.next - x.g0 - kGroupSetup, 0) - s.j0;
         return s;
     };
     // position in the ring, within a segment of n tiles, of K or V of tile j
@@ -383,7 +382,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                                 col0 + u * 128 + cb * 64, x.hv / C::kSplit, 0, id);
             }
         };
-        for (int64_t item = lo; ok && item < hi; item < hi ? next_group<DH, NT>(p, x, heads) : (void)0) {
+        for (int item = lo; ok && item < hi; item < hi ? next_group<DH, NT>(p, x, heads) : (void)0) {
             const Part s = part_of(item);
             const int j0 = s.j0, n = s.n;
             item = s.next;
@@ -444,7 +443,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         uint32_t base = 0;               // units before the segment
         uint32_t p_seen[2] = {0, 0};     // probabilities consumed of each buffer
         uint32_t zeroed = 0;             // a bit per stage: the phase of its B_Z
-        for (int64_t item = lo; ok && item < hi; item < hi ? next_group<DH, NT>(p, x, heads) : (void)0) {
+        for (int item = lo; ok && item < hi; item < hi ? next_group<DH, NT>(p, x, heads) : (void)0) {
             const Part s = part_of(item);
             const int j0 = s.j0, n = s.n, ni = n * NT;
             item = s.next;
@@ -536,7 +535,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         uint32_t boxes = 0;  // segments that came by TMA
         const int qt = tid - 64, ch = qt % CH;
         const int step_tok = STEP / p.group, step_head = STEP - step_tok * p.group;
-        for (int64_t item = lo; ok && item < hi; item < hi ? next_group<DH, NT>(p, x, heads) : (void)0) {
+        for (int item = lo; ok && item < hi; item < hi ? next_group<DH, NT>(p, x, heads) : (void)0) {
             const Part s = part_of(item);
             item = s.next;
             if (s.n == 0)
@@ -608,7 +607,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         const uint64_t t2 = pack_f32x2(cap * 0.13145145773887634f, cap * 0.13145145773887634f);
         const uint64_t t3 = pack_f32x2(cap * -0.04337248206138611f, cap * -0.04337248206138611f);
         const uint64_t yy1 = pack_f32x2(y1, y1);
-        for (int64_t item = lo; item < hi; item < hi ? next_group<DH, NT>(p, x, heads) : (void)0) {
+        for (int item = lo; item < hi; item < hi ? next_group<DH, NT>(p, x, heads) : (void)0) {
             const Part s = part_of(item);
             const int j0 = s.j0, n = s.n;
             item = s.next;
