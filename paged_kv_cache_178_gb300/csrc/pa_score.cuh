@@ -72,6 +72,27 @@ __device__ __forceinline__ float rcp_approx(float x)
     return y;
 }
 
+// ln(l 2^m) - off, for a maximum m in log2 units and a sum l relative to it.  The
+// power of two in l goes to m with the rounding of that sum kept, so that the
+// error is the result's own half unit and what l brings (one logarithm of the
+// whole sum was off by up to four units).
+__device__ __forceinline__ float score_lse(float m, float l, float off)
+{
+    constexpr float kLn2Low = (float)(0.69314718055994530942 - (double)kLn2);
+    if (l == 0.f)
+        return -INFINITY;
+    if (!(l < INFINITY))
+        return l;
+    int e = (__float_as_int(l) >> 23) - 127;
+    float f = __int_as_float((__float_as_int(l) & 0x7fffff) | 0x3f800000);
+    if (f > 1.41421356f) {
+        f *= 0.5f;
+        ++e;
+    }
+    const float x = (float)e, hi = m + x, y = hi - m, low = (m - (hi - y)) + (x - y);
+    return __fmaf_rn(hi, kLn2, __fmaf_rn(hi, kLn2Low, __fmaf_rn(low, kLn2, logf(f)))) - off;
+}
+
 // cap * tanh(s / cap) in log2 units from the raw product q.k, as
 // cap (1 - 2 / (1 + exp(2 s / cap))): exact limits at both ends, an absolute
 // error of about 2^-22 cap (a share of it around 0, where the result is small,
@@ -143,7 +164,7 @@ __device__ __noinline__ void scored_row(const ScoreParams &p, int b, const ReqMe
         dst[e * 32 + lane] = __float2bfloat16_rn(o[e] * inv);
     if (lane == 0 && p.lse)
         p.lse[t * p.hq + h] = bad ? __int_as_float(0x7FC00000)
-                                  : (l == 0.f ? -INFINITY : (mx + __log2f(l)) * kLn2 - slope * (float)near);
+                                  : score_lse(mx, l, slope * (float)near);
     if (bad && lane == 0)
         record_error(p.err, kErrBadMetadata, b);
 }

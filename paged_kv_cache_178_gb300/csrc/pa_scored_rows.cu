@@ -562,7 +562,7 @@ __global__ void __launch_bounds__(kFoldThreads) scored_fold_kernel(const ScorePa
         const int pos = m.L - m.qn + tok;
         const int near = score_nearest(score_low(p, (int64_t)m.qs + tok, pos), pos, score_prefix(p, b, m.L));
         const float slope = p.slopes ? __ldg(p.slopes + h) : 0.f;
-        p.lse[at] = sum == 0.f ? -INFINITY : (top + __log2f(sum)) * kLn2 - slope * (float)near;
+        p.lse[at] = score_lse(top, sum, slope * (float)near);
     }
     if (__syncthreads_or(odd) && warp == 0)
         scored_row<DH>(p, b, m, tok, h);
