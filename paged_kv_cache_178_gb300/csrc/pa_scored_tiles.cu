@@ -37,7 +37,8 @@ bool scored_tiles_fits(int32_t num_seqs, int32_t hkv, int group, int32_t head_di
     if (num_q_tokens < 0)
         return true;  // (a workspace's size: the call itself is refused)
     const int64_t tiles = scored_tiles_bound(num_seqs, group, head_dim, max_query_len, num_q_tokens);
-    return num_seqs + tiles + 2 <= kScoredMaxEntriesHost &&
+    // (the fold's grid: at most 16 CTAs to a row tile and KV head)
+    return num_seqs + tiles + 2 <= kScoredMaxEntriesHost && tiles * hkv * 16 <= INT32_MAX &&
            tiles * hkv * 2 * (((int64_t)max_seq_len + kTileKeys - 1) / kTileKeys + 1 + kGroupSetup) <= INT32_MAX;
 }
 

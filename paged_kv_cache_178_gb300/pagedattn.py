@@ -1112,7 +1112,7 @@ def prepare_compact_pages(context_lens: torch.Tensor, block_tables: torch.Tensor
                     tables_out=tables_out, copy_src=copy_src, copy_dst=copy_dst, counts=counts)
     if tables_out.shape != block_tables.shape or copy_src.numel() != copy_dst.numel() or counts.numel() != 2:
         raise ValueError("metadata shapes disagree")
-    _require_same_device(workspace)
+    _require_same_device(context_lens, workspace)
     if not workspace.is_cuda or not workspace.is_contiguous():
         raise ValueError("workspace must be a contiguous CUDA tensor")
     args = (context_lens.data_ptr(), n, block_tables.data_ptr(), tables_out.data_ptr(), block_tables.shape[1],

@@ -55,7 +55,7 @@ def release(ctx, keep, tables, shares, free, cursor, num_blocks):
     """Returns (shares, free, seq_lens, cursor, bad); bad is None, ("request", b),
     ("pages", freed) or ("call",)."""
     start, shares, free = shares, shares.copy(), free.copy()
-    out, bad, gone, freed = np.array(ctx, np.int32), None, [], []
+    out, bad, gone, freed = np.array(ctx, np.int32), None, [], {}  # (freed: in order)
     for b, (c, k) in enumerate(zip(ctx, keep)):
         ok = 0 <= c <= tables.shape[1] * 16 and k <= c
         if ok and 0 <= k < c:
@@ -76,11 +76,12 @@ def release(ctx, keep, tables, shares, free, cursor, num_blocks):
             if p in freed:
                 bad = bad or ("request", b)
             else:
-                freed.append(p)
+                freed[p] = True
     if not 0 <= cursor <= len(free) or len(freed) > cursor:
         if bad is None:
             bad = ("pages", len(freed)) if 0 <= cursor <= len(free) else ("call",)
         return start.copy(), free, np.array(ctx, np.int32), cursor, bad
+    freed = list(freed)
     shares[freed] = 0
     cursor -= len(freed)
     free[cursor:cursor + len(freed)] = freed

@@ -331,6 +331,16 @@ def test_releases_that_do_not_fit(in_place):
         assert _release(s, [0, 0, 0], in_place) == (3, ("call",))
 
 
+@pytest.mark.parametrize("in_place", [False, True])
+def test_release_of_more_references_than_registers_hold(in_place):
+    """180000 references, some to pages that two of the requests share."""
+    s = State([360000] * 8, groups=2, common=1500, cols=22501)
+    keep = [0, 0, 16 * 1499 + 16, 0, -1, 0, 100000, 0]
+    _release(s, keep, in_place)
+    s = State([360000] * 8, groups=2, common=1500, cols=22501, seed=1)
+    _release(s, [0] * 8, in_place)
+
+
 # --------------------------------------------------------------- compaction --
 
 def _compact(s, max_moves, in_place, free_more=0):

@@ -203,6 +203,14 @@ def test_group_sizes(hq, hkv):
         _check(a, _rules("all", lens, new, hq))
 
 
+@pytest.mark.parametrize("hq,hkv,dh", [(3, 1, 512), (5, 1, 256), (12, 4, 512)])
+def test_groups_that_do_not_divide_a_tile(hq, hkv, dh):
+    lens, new = [300, 90, 43], [300, 1, 43]
+    a = _batch(lens, new, hq, hkv, dh, seed=14)
+    for rule in ("cap", "all"):
+        _check(a, _rules(rule, lens, new, hq))
+
+
 def test_pages_shared_and_held_twice():
     """Requests that share pages, and a table that names one page twice."""
     for new in (1, 40):
