@@ -753,9 +753,9 @@ PA_API size_t pa_paged_attention_scored_workspace_size(int32_t num_seqs, int32_t
  * max_seq_len <= INT32_MAX - 4096; where max_query_len * G > 32, with
  *   tiles = min(num_seqs * ceil(max_query_len * G / R), num_q_tokens * G / R + num_seqs),
  *   R = 256 at head dim 128 if max_query_len * G > 128, else 128,
- * num_seqs + tiles <= 23998, tiles * Hkv < 2^27 and tiles * Hkv * (max_seq_len /
- * 128 + 4) < 2^30, and where it is not, num_seqs * Hkv < 2^26 and num_seqs * Hkv *
- * (max_seq_len / 32 + 2) < 2^31.
+ * num_seqs + tiles <= 23998 and tiles * Hkv * (max_seq_len / 128 + 4) < 2^30, and
+ * where it is not, num_seqs * Hkv < 2^26 and num_seqs * Hkv * (max_seq_len / 32 + 2)
+ * < 2^31.
  */
 PA_API pa_status pa_paged_attention_scored(const void *q, int64_t num_q_tokens, int64_t q_tok_stride,
                                            int32_t num_q_heads, const pa_kv_cache *cache,

@@ -39,7 +39,7 @@ size_t scored_workspace_bytes(int32_t num_seqs, int32_t hq, int32_t hkv, int32_t
     const int group = hq / hkv;
     return few_rows(num_seqs, hkv, group, head_dim, max_query_len, max_seq_len)
                ? scored_rows_bytes(num_seqs, hkv, group, head_dim, max_query_len, max_seq_len)
-               : scored_tiles_bytes(num_seqs, hkv, group, head_dim, max_query_len);
+               : scored_tiles_bytes(group, head_dim, max_query_len);
 }
 
 static ScoreParams score_params(const AttnArgs &a, const ScoreRules &r, ErrState *err)

@@ -128,7 +128,7 @@ constexpr int kScoredMaxEntriesHost = 24000;  // requests and row tiles that a C
 int64_t scored_tiles_bound(int32_t num_seqs, int group, int32_t head_dim, int32_t max_query_len, int64_t num_q_tokens);
 bool scored_tiles_fits(int32_t num_seqs, int32_t hkv, int group, int32_t head_dim, int32_t max_query_len,
                        int32_t max_seq_len, int64_t num_q_tokens);
-size_t scored_tiles_bytes(int32_t num_seqs, int32_t hkv, int group, int32_t head_dim, int32_t max_query_len);
+size_t scored_tiles_bytes(int group, int32_t head_dim, int32_t max_query_len);
 cudaError_t launch_scored_tiles(const ScoreParams &p, int32_t head_dim, void *workspace, cudaStream_t stream, char *info,
                                 size_t info_len);
 cudaError_t init_scored_tiles_attributes();

@@ -37,39 +37,31 @@ bool scored_tiles_fits(int32_t num_seqs, int32_t hkv, int group, int32_t head_di
     if (num_q_tokens < 0)
         return true;  // (a workspace's size: the call itself is refused)
     const int64_t tiles = scored_tiles_bound(num_seqs, group, head_dim, max_query_len, num_q_tokens);
-    // (the fold's grid: at most 16 CTAs to a row tile and KV head)
-    return num_seqs + tiles + 2 <= kScoredMaxEntriesHost && tiles * hkv * 16 <= INT32_MAX &&
+    return num_seqs + tiles + 2 <= kScoredMaxEntriesHost &&
            tiles * hkv * 2 * (((int64_t)max_seq_len + kTileKeys - 1) / kTileKeys + 1 + kGroupSetup) <= INT32_MAX;
 }
 
 static size_t align256(size_t n) { return (n + 255) / 256 * 256; }
 
 struct TileSizes {
-    int nt, parts;
-    int64_t tiles, record_floats;
-    size_t groups, entries, records, bytes;  // offsets, and the whole
+    int nt;
+    int64_t record_floats;
+    size_t records, bytes;  // offset, and the whole
 };
 
-static TileSizes tile_sizes(int64_t tiles, int32_t hkv, int group, int32_t head_dim, int32_t max_query_len)
+static TileSizes tile_sizes(int group, int32_t head_dim, int32_t max_query_len)
 {
     TileSizes s{};
     s.nt = row_tiles(group, head_dim, max_query_len);
-    s.parts = head_dim == 512 ? 2 : 1;
-    s.tiles = tiles;
-    s.record_floats = s.nt * tile_record(head_dim / s.parts);
-    s.groups = 256;
-    s.entries = s.groups + align256((size_t)tiles * hkv * s.parts * 8);
-    s.records = s.entries + align256((size_t)tiles * 8);
+    s.record_floats = s.nt * tile_record(head_dim == 512 ? 256 : head_dim);
+    s.records = align256((size_t)kScoredSms * sizeof(int4));
     s.bytes = s.records + (size_t)2 * kScoredSms * s.record_floats * 4;
     return s;
 }
 
-size_t scored_tiles_bytes(int32_t num_seqs, int32_t hkv, int group, int32_t head_dim, int32_t max_query_len)
+size_t scored_tiles_bytes(int group, int32_t head_dim, int32_t max_query_len)
 {
-    int64_t tiles = scored_tiles_bound(num_seqs, group, head_dim, max_query_len, -1);
-    if (tiles > kScoredMaxEntriesHost)
-        tiles = kScoredMaxEntriesHost;
-    return tile_sizes(tiles, hkv, group, head_dim, max_query_len).bytes;
+    return tile_sizes(group, head_dim, max_query_len).bytes;
 }
 
 cudaError_t launch_scored_tiles(const ScoreParams &p, int32_t head_dim, void *workspace, cudaStream_t stream, char *info,
@@ -88,19 +80,17 @@ cudaError_t launch_scored_tiles(const ScoreParams &p, int32_t head_dim, void *wo
                          CU_TENSOR_MAP_SWIZZLE_128B) != CUDA_SUCCESS)
             return cudaErrorInvalidValue;
     }
-    const TileSizes s = tile_sizes(scored_tiles_bound(p.num_seqs, p.group, head_dim, p.max_query_len, p.num_q_tokens), p.hkv,
-                                   p.group, head_dim, p.max_query_len);
+    const TileSizes s = tile_sizes(p.group, head_dim, p.max_query_len);
+    const int64_t tiles = scored_tiles_bound(p.num_seqs, p.group, head_dim, p.max_query_len, p.num_q_tokens);
     TileWork w{};
     uint8_t *ws = static_cast<uint8_t *>(workspace);
-    w.header = reinterpret_cast<int64_t *>(ws);
-    w.groups = reinterpret_cast<int2 *>(ws + s.groups);
-    w.entries = reinterpret_cast<int2 *>(ws + s.entries);
+    w.tails = reinterpret_cast<int4 *>(ws);
     w.records = reinterpret_cast<float *>(ws + s.records);
     w.record_floats = s.record_floats;
     w.q_boxes = q_boxes;
-    const int64_t items = s.tiles * p.hkv * s.parts * (((int64_t)p.max_seq_len + kTileKeys - 1) / kTileKeys + 1 + kGroupSetup);
+    const int64_t items = tiles * p.hkv * (head_dim == 512 ? 2 : 1) * (((int64_t)p.max_seq_len + kTileKeys - 1) / kTileKeys + 1 + kGroupSetup);
     w.ctas = (int32_t)(items < kScoredSms ? items : kScoredSms);
-    w.max_tiles = (int32_t)s.tiles;
+    w.max_tiles = (int32_t)tiles;
     // Without a maximum the exponents stay within the cap: 2^80 times any number
     // of keys and values up to 2^20 is far from overflow (and a row that overflows
     // all the same is computed again key by key).
@@ -108,7 +98,7 @@ cudaError_t launch_scored_tiles(const ScoreParams &p, int32_t head_dim, void *wo
                      : p.cap_log2 > 0.f                    ? (p.cap_log2 <= 80.f ? kModeCapped : kModeAny)
                                                            : kModePlain;
     snprintf(info, info_len, "scored attention dh=%d kernel=tiles-m%d mode=%d grid=%d tiles=%lld", head_dim, 128 * s.nt, mode,
-             w.ctas, (long long)s.tiles);
+             w.ctas, (long long)tiles);
     switch (head_dim) {
     case 128: return s.nt == 2 ? launch_tiles<128, 2>(p, tm, w, mode, stream) : launch_tiles<128, 1>(p, tm, w, mode, stream);
     case 256: return launch_tiles<256, 1>(p, tm, w, mode, stream);

@@ -73,9 +73,8 @@ struct TileCfg {
 };
 
 struct TileWork {
-    int64_t *header;   // items of all groups; row tiles of all requests
-    int2 *groups;      // [row tiles * heads * parts] (first item, items)
-    int2 *entries;     // [row tiles] (request, row tile of it)
+    int4 *tails;       // [ctas] the group that goes on past a CTA's range and began in it:
+                       // request, row tile, (KV head, part of the columns), CTAs that have a part; 0: none
     float *records;    // [2 * ctas] of record_floats
     int64_t record_floats;
     int32_t ctas, max_tiles;
@@ -288,17 +287,21 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         return n ? n + kGroupSetup : 0;
     });
     const int total = per_head * heads, ctas = min(w.ctas, total);
-    for (int g = c * kTileThreads + tid; g < ntiles * heads; g += w.ctas * kTileThreads) {
-        const int e = g / heads, n = s_off[e + 1] - s_off[e];
-        w.groups[g] = make_int2(s_off[e] * heads + (g - e * heads) * n, n);
-    }
-    for (int e = c * kTileThreads + tid; e < ntiles; e += w.ctas * kTileThreads) {
-        const int b = owner_of(s_first, p.num_seqs, e);
-        w.entries[e] = make_int2(b, e - s_first[b]);
-    }
-    if (c == 0 && tid == 0) {
-        w.header[0] = total;
-        w.header[1] = ntiles;
+    // row tiles that see nothing
+    for (int e = c; e < ntiles; e += w.ctas) {
+        if (s_off[e + 1] > s_off[e])
+            continue;
+        const int b = owner_of(s_first, p.num_seqs, e), r0 = (e - s_first[b]) * RT;
+        const ReqMeta m = score_meta(p, b);
+        const int rows = min(RT, m.qn * p.group - r0);
+        for (int i = tid; i < rows * p.hkv; i += kTileThreads) {
+            const int row = r0 + i / p.hkv, tok = row / p.group;
+            const int64_t at = ((int64_t)m.qs + tok) * p.hq + i % p.hkv * p.group + row - tok * p.group;
+            for (int k = 0; k < DH / 8; ++k)
+                reinterpret_cast<uint4 *>(p.out + at * DH)[k] = make_uint4(0u, 0u, 0u, 0u);
+            if (p.lse)
+                p.lse[at] = -INFINITY;
+        }
     }
     for (int b = c; b < p.num_seqs; b += w.ctas) {
         const ReqMeta m = score_meta(p, b);
@@ -311,8 +314,11 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                     p.lse[first + i] = __int_as_float(0x7FC00000);
         }
     }
-    if (c >= ctas)
+    if (c >= ctas) {
+        if (tid == 0)
+            w.tails[c] = make_int4(0, 0, 0, 0);
         return;
+    }
     const int lo = (int)range_lo(total, c, ctas), hi = (int)range_lo(total, c + 1, ctas);
     if (tid == 0) {
         const int e = owner_of(s_off, ntiles, lo / heads);
@@ -320,6 +326,13 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         s_flags[4] = b;
         s_flags[5] = e - s_first[b];
         s_flags[6] = s_off[e];
+    }
+    if (tid == 64) {
+        const int e = owner_of(s_off, ntiles, (hi - 1) / heads), b = owner_of(s_first, p.num_seqs, e);
+        const int n = s_off[e + 1] - s_off[e], hv = (hi - 1 - s_off[e] * heads) / n;
+        const int g0 = s_off[e] * heads + hv * n, keys = g0 + kGroupSetup;  // first item; first key tile
+        w.tails[c] = make_int4(b, e - s_first[b], hv,
+                               g0 + n > hi && keys >= lo && keys < hi ? range_owner(total, g0 + n - 1, ctas) - c + 1 : 0);
     }
     if (warp == 1) {
         tmem_alloc(smem_addr(const_cast<int *>(&s_flags[1])), 512);
@@ -940,32 +953,28 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         tmem_dealloc(tmem, 512);
 }
 
-// Folds the records of the groups that several CTAs have a part of: a thread per
-// row, 32 columns of the output a CTA.
+// Folds the records of the groups that several CTAs have a part of, each at the
+// place of the CTA that it begins in: two threads
+// per row, each with every second part, and 32 columns of the output a CTA.  (A
+// few rows over many keys are a part to a CTA: one thread per row, part by
+// part, took 27 of 42 us for 64 rows over 4096 keys.)
+constexpr int kTileFoldThreads = 256;
+
 template <int DH, int NT>
-__global__ void __launch_bounds__(128) scored_tile_fold_kernel(const ScoreParams p, const TileWork w)
+__global__ void __launch_bounds__(kTileFoldThreads) scored_tile_fold_kernel(const ScoreParams p, const TileWork w)
 {
     using C = TileCfg<DH, NT>;
     griddep_wait();
     griddep_launch_dependents();
     constexpr int CB = C::kCols / 32;
-    const int heads = p.hkv * C::kSplit;
-    const int unit = blockIdx.x / CB, cb = blockIdx.x % CB, g = unit / NT, t = unit % NT;
-    if (g >= w.header[1] * heads)
+    __shared__ float s_top[2][128], s_o[33][128];  // the second threads' sums and columns
+    const int unit = blockIdx.x / CB, cb = blockIdx.x % CB, c0 = unit / NT, t = unit % NT;
+    const int4 tail = w.tails[c0];
+    const int b = tail.x, hv = tail.z, kvh = hv / C::kSplit, part = hv % C::kSplit, n = tail.w;
+    if (n == 0)
         return;
-    const int total = (int)w.header[0], ctas = min(w.ctas, total);
-    const int2 gr = w.groups[g], en = w.entries[g / heads];
-    const int64_t g0 = (int64_t)gr.x + kGroupSetup, g1 = (int64_t)gr.x + gr.y;  // its key tiles
-    int c0 = 0, n = 0;
-    if (gr.y > 0) {
-        c0 = range_owner(total, g0, ctas);
-        n = range_owner(total, g1 - 1, ctas) - c0 + 1;
-        if (n == 1)
-            return;  // written by the CTA that had all of it
-    }
-    const int b = en.x, hv = g % heads, kvh = hv / C::kSplit, part = hv % C::kSplit;
     const ReqMeta m = score_meta(p, b);
-    const int r = threadIdx.x, row = en.y * (NT * 128) + t * 128 + r;
+    const int r = threadIdx.x % 128, half = threadIdx.x / 128, row = tail.y * (NT * 128) + t * 128 + r;
     const bool valid = row < m.qn * p.group;
     const int tok = valid ? row / p.group : 0, head = kvh * p.group + (valid ? row - tok * p.group : 0);
     auto record = [&](int c) {
@@ -973,14 +982,18 @@ __global__ void __launch_bounds__(128) scored_tile_fold_kernel(const ScoreParams
         return w.records + (2 * (int64_t)c + (c == c0 ? 1 : 0)) * w.record_floats + t * tile_record(C::kCols);
     };
     float top = -INFINITY;
-    for (int i = 0; i < n; ++i)
+#pragma unroll 8
+    for (int i = half; i < n; i += 2)
         top = fmaxf(top, __ldcg(record(c0 + i) + r));
+    s_top[half][r] = top;
+    __syncthreads();
+    top = fmaxf(top, s_top[half ^ 1][r]);
     float sum = 0.f, o[32];
 #pragma unroll
     for (int k = 0; k < 32; ++k)
         o[k] = 0.f;
 #pragma unroll 2
-    for (int i = 0; i < n; ++i) {
+    for (int i = half; i < n; i += 2) {
         const float *rec = record(c0 + i);
         const float mi = __ldcg(rec + r), f = mi == top ? 1.f : ex2(mi - top);
         sum += __ldcg(rec + 128 + r) * f;
@@ -994,6 +1007,19 @@ __global__ void __launch_bounds__(128) scored_tile_fold_kernel(const ScoreParams
             o[4 * k + 3] += v.w * f;
         }
     }
+    if (half) {
+#pragma unroll
+        for (int k = 0; k < 32; ++k)
+            s_o[k][r] = o[k];
+        s_o[32][r] = sum;
+    }
+    __syncthreads();
+    if (half)
+        return;
+#pragma unroll
+    for (int k = 0; k < 32; ++k)
+        o[k] += s_o[k][r];
+    sum += s_o[32][r];
     const float inv = sum == 0.f ? 0.f : 1.f / sum;
     bool odd = !(fabsf(sum) < INFINITY);
     uint32_t q[32];
@@ -1041,8 +1067,8 @@ cudaError_t launch_tiles(const ScoreParams &p, const CUtensorMap (&tm)[3], const
     if (e != cudaSuccess)
         return e;
     using C = TileCfg<DH, NT>;
-    cfg.gridDim = dim3((unsigned)((int64_t)w.max_tiles * p.hkv * C::kSplit * NT * (C::kCols / 32)));
-    cfg.blockDim = dim3(128);
+    cfg.gridDim = dim3((unsigned)(w.ctas * NT * (C::kCols / 32)));
+    cfg.blockDim = dim3(kTileFoldThreads);
     cfg.dynamicSmemBytes = 0;
     return cudaLaunchKernelEx(&cfg, scored_tile_fold_kernel<DH, NT>, p, w);
 }

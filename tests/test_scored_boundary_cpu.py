@@ -113,10 +113,10 @@ def test_empty_batches(lib):
     assert _call(lib, seqs=0, rules=dict(window=-1)) == INVALID
 
 
-def test_more_heads_than_a_grid_counts(lib):
+def test_more_heads_than_items_count(lib):
     for dh in (128, 256, 512):
         cache = dict(num_kv_heads=20000, head_dim=dh, token_stride=20000 * dh, head_stride=dh, block_stride=16 * 20000 * dh)
-        assert _call(lib, cache=cache, hq=20000, seqs=8192, t=8192, mq=1, ms=16) == UNSUPPORTED
+        assert _call(lib, cache=cache, hq=20000, seqs=8192, t=8192, mq=1, ms=1024) == UNSUPPORTED
 
 
 @needs_no_gpu
