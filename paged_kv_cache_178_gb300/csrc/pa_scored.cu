@@ -18,7 +18,17 @@ bool scored_pool_maps(const ScoreParams &p, int32_t head_dim, CUtensorMap (&tm)[
 }
 
 // Few rows a request go to the kernel whose work follows the bytes, others to
-// the one that fills tensor-memory tiles.
+// the one that fills tensor-memory tiles.  Measured, us, few rows / tiles, for 4 and 32
+// requests of 4096 keys and 8 of 512, two KV heads (one at head dim 512), capped:
+//   16 rows   Dh 128  10.5 / 23.8   30.1 / 40.9    8.7 / 15.8
+//             Dh 256  14.5 / 27.4   50.4 / 69.4   10.4 / 18.3
+//             Dh 512  16.3 / 33.7   56.0 / 97.9   11.5 / 20.2
+//   32 rows   Dh 128  14.5 / 23.2   42.8 / 40.8   11.1 / 15.7
+//             Dh 256  19.9 / 27.0   73.8 / 69.8   13.5 / 18.1
+//             Dh 512  22.4 / 30.8   79.6 / 97.6   15.7 / 20.2
+//   64 rows   Dh 128  17.7 / 22.8   71.7 / 41.0   13.2 / 15.9
+//             Dh 512  28.0 / 31.1  137.2 / 98.5   19.4 / 20.5
+// From 33 on a few-rows call reads its keys twice, which only idle SMs hide.
 static bool few_rows(int32_t num_seqs, int32_t hkv, int group, int32_t head_dim, int32_t max_query_len, int32_t max_seq_len)
 {
     return (int64_t)max_query_len * group <= 32 &&

@@ -32,10 +32,12 @@ namespace pa {
 constexpr int kRowsWarps = 4;  // computing warps
 constexpr int kRowsThreads = (kRowsWarps + 1) * 32;
 
-template <int DH>
+template <int DH, int MT>
 struct RowsCfg {
     static constexpr int kKeys = DH == 128 ? 64 : 32;  // of a block: two or four pages
-    static constexpr int kStages = DH == 512 ? 2 : 3;
+    // (with three stages of head dim 256 and 32 rows an SM holds one CTA: 115 us
+    // instead of 74 for 32 requests of 4096 keys)
+    static constexpr int kStages = DH == 512 || (DH == 256 && MT == 2) ? 2 : 3;
     static constexpr int kCtas = DH == 512 ? 1 : 2;  // per SM
     static constexpr int kView = kKeys * DH * 2;     // bytes of K (or V) of a block
 };
@@ -43,10 +45,11 @@ struct RowsCfg {
 template <int DH, int MT>
 constexpr size_t rows_smem(int seq_tiles)
 {
-    using C = RowsCfg<DH>;
+    using C = RowsCfg<DH, MT>;
     return 1024 + (size_t)C::kStages * 2 * C::kView + 16 * MT * DH * 2 + 16 * MT * (C::kKeys * 2 + 16) +
            2 * kRowsWarps * 16 * MT * 4 + 256 + (size_t)(seq_tiles + 1) * 4;
 }
+static_assert(2 * (rows_smem<256, 2>(64) + 1024) <= kMaxSmemPerBlock + 1024, "two CTAs to an SM");
 static_assert(rows_smem<512, 2>(kScoredMaxTilesHost) <= kMaxSmemPerBlock, "shared-memory layout");
 static_assert(rows_smem<256, 2>(kScoredMaxTilesHost) <= kMaxSmemPerBlock, "shared-memory layout");
 static_assert(rows_smem<128, 2>(kScoredMaxTilesHost) <= kMaxSmemPerBlock, "shared-memory layout");
@@ -105,11 +108,11 @@ __device__ __forceinline__ int2 group_parts(int total, int g0, int g1, int ctas)
 }
 
 template <int DH, int MT>
-__global__ void __launch_bounds__(kRowsThreads, RowsCfg<DH>::kCtas)
+__global__ void __launch_bounds__(kRowsThreads, RowsCfg<DH, MT>::kCtas)
     scored_rows_kernel(const __grid_constant__ ScoreParams p, const __grid_constant__ CUtensorMap tm_k,
                        const __grid_constant__ CUtensorMap tm_v, const RowsWork w)
 {
-    using C = RowsCfg<DH>;
+    using C = RowsCfg<DH, MT>;
     constexpr int KB = C::kKeys, R = 16 * MT, NS = C::kStages;
     constexpr int KW = KB / kRowsWarps, NT = KW / 8;  // keys of a warp's scores, in n-tiles
     constexpr int DW = DH / kRowsWarps, OT = DW / 8;  // output columns of a warp, in n-tiles
