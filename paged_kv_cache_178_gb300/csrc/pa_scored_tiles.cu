@@ -38,7 +38,7 @@ bool scored_tiles_fits(int32_t num_seqs, int32_t hkv, int group, int32_t head_di
         return true;  // (a workspace's size: the call itself is refused)
     const int64_t tiles = scored_tiles_bound(num_seqs, group, head_dim, max_query_len, num_q_tokens);
     return num_seqs + tiles + 2 <= kScoredMaxEntriesHost &&
-           tiles * hkv * 2 * (((int64_t)max_seq_len + kTileKeys - 1) / kTileKeys + 1 + kGroupSetup) <= INT32_MAX;
+           tiles * hkv * 2 * (((int64_t)max_seq_len + kTileKeys - 1) / kTileKeys + 1 + kGroupSetup<2>) <= INT32_MAX;
 }
 
 static size_t align256(size_t n) { return (n + 255) / 256 * 256; }
@@ -88,7 +88,7 @@ cudaError_t launch_scored_tiles(const ScoreParams &p, int32_t head_dim, void *wo
     w.records = reinterpret_cast<float *>(ws + s.records);
     w.record_floats = s.record_floats;
     w.q_boxes = q_boxes;
-    const int64_t items = tiles * p.hkv * (head_dim == 512 ? 2 : 1) * (((int64_t)p.max_seq_len + kTileKeys - 1) / kTileKeys + 1 + kGroupSetup);
+    const int64_t items = tiles * p.hkv * (head_dim == 512 ? 2 : 1) * (((int64_t)p.max_seq_len + kTileKeys - 1) / kTileKeys + 1 + kGroupSetup<2>);
     w.ctas = (int32_t)(items < kScoredSms ? items : kScoredSms);
     w.max_tiles = (int32_t)tiles;
     // Without a maximum the exponents stay within the cap: 2^80 times any number

@@ -28,15 +28,17 @@
 // (tensor memory holds 256 columns of output beside the scores): three halves of
 // the products of a whole one instead of two, and no exchange.
 //
-// Measured: a prompt of 4096 tokens, 8 query and 2 KV heads of 128, capped: 61
-// us, 0.56 PFLOP/s of the products that causality leaves; a prompt of 8192 tokens
+// Measured: a prompt of 4096 tokens, 8 query and 2 KV heads of 128, capped: 60
+// us, 0.57 PFLOP/s of the products that causality leaves; a prompt of 8192 tokens
 // of five documents behind a prefix, 16 and 2 heads of 256, a bias by distance:
-// 289 us, 0.52 PFLOP/s of those that the documents leave.  What bounds it is the
+// 274 us, 0.55 PFLOP/s of those that the documents leave.  What bounds it is the
 // chain of a step (scores, softmax, products), not the tensor pipe: a pair of
 // 128-key tiles takes 4.9 k cycles at head dim 128, its products 2.1 k, a tile's
 // softmax 2.0 to 2.4 k (of them 1.4 k issue slots where it is capped).  Starting a CTA and its first scores take 15 k more, 12
 // percent of the prompt's time.  Slower when tried: two issuing threads (69 us),
-// 16 softmax warps (74), tiles of 64 keys (79).
+// 16 softmax warps (74), tiles of 64 keys (79), probabilities in shared memory so
+// that the next scores need not wait for the products (69: each product then
+// reads both operands there, 950 cycles instead of 800).
 #pragma once
 #include "pa_scan.cuh"
 #include "pa_scored.h"
@@ -47,8 +49,11 @@ constexpr int kTileThreads = 384;
 constexpr int kTileKeys = 128;
 constexpr int kUnitBytes = kTileKeys * 256;  // 128 keys by 128 columns
 // What a group costs beside its items, in items: it is dealt out with them, at
-// the group's start.
-constexpr int kGroupSetup = 2;
+// the group's start.  (With two row tiles 1, 2, 3 and 4 took 61.4, 60.1, 62.3 and
+// 64.7 us for the prompt above; with one 274.9, 281.3, 293.8 and 305.6 for the
+// documents.)
+template <int NT>
+constexpr int kGroupSetup = NT == 2 ? 2 : 1;
 
 // How a score becomes an exponent.
 enum ScoreMode : int {
@@ -151,7 +156,7 @@ __device__ __forceinline__ void load_group(const ScoreParams &p, TileGroup &x)
     x.v = warp_tile_view(p, x.b, x.m, min(x.tile * RT, rows), min(x.tile * RT + RT, rows));
     x.t = tile_blocks(x.v, kTileKeys);
     x.n = x.t.count;
-    x.w = x.n ? x.n + kGroupSetup : 0;
+    x.w = x.n ? x.n + kGroupSetup<NT> : 0;
 }
 
 // The next group with items (there is one: the range goes on).
@@ -284,7 +289,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         const ReqMeta m = score_meta(p, b);
         const int rows = m.qn * p.group;
         const int n = tile_blocks(tile_view(p, b, m, min(tile * RT, rows), min(tile * RT + RT, rows)), kTileKeys).count;
-        return n ? n + kGroupSetup : 0;
+        return n ? n + kGroupSetup<NT> : 0;
     });
     const int total = per_head * heads, ctas = min(w.ctas, total);
     // row tiles that see nothing
@@ -330,7 +335,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     if (tid == 64) {
         const int e = owner_of(s_off, ntiles, (hi - 1) / heads), b = owner_of(s_first, p.num_seqs, e);
         const int n = s_off[e + 1] - s_off[e], hv = (hi - 1 - s_off[e] * heads) / n;
-        const int g0 = s_off[e] * heads + hv * n, keys = g0 + kGroupSetup;  // first item; first key tile
+        const int g0 = s_off[e] * heads + hv * n, keys = g0 + kGroupSetup<NT>;  // first item; first key tile
         w.tails[c] = make_int4(b, e - s_first[b], hv,
                                g0 + n > hi && keys >= lo && keys < hi ? range_owner(total, g0 + n - 1, ctas) - c + 1 : 0);
     }
@@ -360,8 +365,8 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     auto part_of = [&](int item) {
         Part s;
         s.next = min(hi, x.g0 + x.w);
-        s.j0 = max(item - x.g0 - kGroupSetup, 0);
-        s.n = max(s.next - x.g0 - kGroupSetup, 0) - s.j0;
+        s.j0 = max(item - x.g0 - kGroupSetup<NT>, 0);
+        s.n = max(s.next - x.g0 - kGroupSetup<NT>, 0) - s.j0;
         return s;
     };
     // position in the ring, within a segment of n tiles, of K or V of tile j
@@ -862,7 +867,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
             const int col0 = NT == 2 ? 0 : wg * COLS_W;  // of the group's columns
             const float inv = l == 0.f ? 0.f : 1.f / l;
             bool odd = lost || !(fabsf(l) < INFINITY);
-            float *rec = w.records + (2 * (int64_t)c + (x.g0 + kGroupSetup < lo ? 0 : 1)) * w.record_floats +
+            float *rec = w.records + (2 * (int64_t)c + (x.g0 + kGroupSetup<NT> < lo ? 0 : 1)) * w.record_floats +
                          (NT == 2 ? wg : 0) * tile_record(C::kCols);
             const int64_t at = ((int64_t)x.m.qs + tok) * p.hq + head;
             if (ok && !whole) {
