@@ -34,7 +34,9 @@
 // 274 us, 0.55 PFLOP/s of those that the documents leave.  What bounds it is the
 // chain of a step (scores, softmax, products), not the tensor pipe: a pair of
 // 128-key tiles takes 4.9 k cycles at head dim 128, its products 2.1 k, a tile's
-// softmax 2.0 to 2.4 k (of them 1.4 k issue slots where it is capped).  Starting a CTA and its first scores take 15 k more, 12
+// softmax 2.0 to 2.4 k (of them 1.4 k issue slots where it is capped); at head dim
+// 256 a tile takes 6.4 k, of which the issuing thread waits 2.3 k for K and V (128
+// KB from L2, 6 TB/s over the GPU) and its products take 3.1 k.  Starting a CTA and its first scores take 15 k more, 12
 // percent of the prompt's time.  Slower when tried: two issuing threads (69 us),
 // 16 softmax warps (74), tiles of 64 keys (79), probabilities in shared memory so
 // that the next scores need not wait for the products (69: each product then
