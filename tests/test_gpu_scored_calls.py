@@ -211,6 +211,43 @@ def test_groups_that_do_not_divide_a_tile(hq, hkv, dh):
         _check(a, _rules(rule, lens, new, hq))
 
 
+@pytest.mark.parametrize("hq,hkv,dh", [(8, 2, 128), (6, 2, 256), (4, 1, 512)])
+@pytest.mark.parametrize("new", [1, 20, 300])
+def test_nothing_to_see(hq, hkv, dh, new):
+    """Tokens whose documents begin behind them, beside some that see keys, and alone."""
+    lens, n = [300, 310, 1000], [new, new, min(new, 3)]
+    a = _batch(lens, n, hq, hkv, dh, seed=15)
+    pos = [L - x + i for L, x in zip(lens, n) for i in range(x)]
+    first = [p + 1 for p in pos]
+    out, lse = _check(a, dict(first_keys=i32(first)))
+    assert not out.any() and bool((lse == -math.inf).all())
+    first[new:2 * new] = [0] * new
+    _check(a, dict(first_keys=i32(first), soft_cap=30.0))
+    _check(a, dict(first_keys=i32([2**31 - 1] * len(pos)), prefix_lens=i32([0, 0, 7])))
+
+
+@pytest.mark.parametrize("bound", [4, 300])
+def test_tokens_of_no_request(bound):
+    a = _batch([300, 40], [3, 1], 8, 2, 128, seed=16)
+    a.update(query_start_loc=i32([0, 0, 0]), max_query_len=bound)
+    out, lse = torch.full((4, 8, 128), 7.0, dtype=torch.bfloat16, device="cuda"), torch.full((4, 8), 7.0, device="cuda")
+    pa.paged_attention_scored(**a, out=out, lse=lse)
+    assert pa.check_errors() == (0, -1) and bool((out == 7).all()) and bool((lse == 7).all())
+
+
+@pytest.mark.parametrize("new", [4, 300])
+def test_decreasing_query_starts_touch_nothing_else(new):
+    """Requests that claim the same rows, and ones that end before they begin."""
+    a = _batch([400] * 5, [new, 0, 0, 0, 0], 8, 2, 128, seed=17)
+    a["query_start_loc"] = i32([0, new, 0, new, 0, new])
+    out = torch.full((new + 2, 8, 128), 7.0, dtype=torch.bfloat16, device="cuda")
+    lse = torch.full((new + 2, 8), 7.0, device="cuda")
+    pa.paged_attention_scored(**a, out=out[1:-1], lse=lse[1:-1])
+    assert pa.check_errors()[0] == pa.PA_ERR_BAD_METADATA
+    for t in (out, lse):
+        assert bool((t[0] == 7).all()) and bool((t[-1] == 7).all())
+
+
 def test_pages_shared_and_held_twice():
     """Requests that share pages, and a table that names one page twice."""
     for new in (1, 40):
