@@ -241,7 +241,10 @@ cudaError_t launch_fork_requests(const PageArgs &a, ErrState *err, cudaStream_t 
 }
 
 // The reference that takes a page's last owner is the one that frees it.  In
-// order: every dropped reference takes one off its page's count; then the
+// order: every dropped reference takes one off its page's count, and those that
+// find it 0 are counted: as many pages are freed, and where the stack has no room
+// for them the references give back what they took (before anything else has
+// become of the counts, so they end as they began); then the
 // references of pages whose count went below 0 meet in an atomic minimum of
 // -(2^30 + index), which the last of them wins; the winners' order among all
 // dropped references gives each page its place on the free stack.  So the
@@ -257,6 +260,7 @@ __global__ void __launch_bounds__(kPageThreads, 1) release_pages_kernel(const Pa
     extern __shared__ int32_t s_rel[];
     __shared__ int s_sums[kPageWarps];
     __shared__ int32_t s_freed[kPageWarps];  // pages that a warp frees
+    __shared__ int32_t s_ctas[kPageClusterMax];
     const int n = a.num_seqs, tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
     int32_t *s_off = s_rel;          // [n + 1] first dropped page of a request among all
     int32_t *s_keep = s_off + n + 1; // [n] tokens that stay
@@ -315,17 +319,58 @@ __global__ void __launch_bounds__(kPageThreads, 1) release_pages_kernel(const Pa
         for (int k = 0; k < kPageBatch; ++k)
             v[k] = ids[k] >= 0 ? __ldcg(a.shares_out + ids[k]) : 0;
     };
+    // the pages freed by all (s_freed of every warp), and before this warp's: a warp
+    // adds up one CTA's counts
+    auto sum_freed = [&](int &before) {
+        if (warp < (int)gridDim.x) {
+            int x;
+            asm volatile("ld.shared::cluster.s32 %0, [%1];"
+                         : "=r"(x)
+                         : "r"(mapa_shared(smem_addr(s_freed + lane), (uint32_t)warp))
+                         : "memory");
+            x = __reduce_add_sync(0xffffffffu, x);
+            if (lane == 0)
+                s_ctas[warp] = x;
+        }
+        __syncthreads();
+        const int x = lane < (int)gridDim.x ? s_ctas[lane] : 0;
+        before = __reduce_add_sync(0xffffffffu, (lane < (int)blockIdx.x ? x : 0) + (lane < warp ? s_freed[lane] : 0));
+        return __reduce_add_sync(0xffffffffu, x);
+    };
+    int last = 0, before;
     for_batches([&](int64_t x0, const int(&ids)[kPageBatch]) {
         int v[kPageBatch];
 #pragma unroll
         for (int k = 0; k < kPageBatch; ++k)
             v[k] = ids[k] >= 0 ? atomicSub(a.shares_out + ids[k], 1) : -1;
 #pragma unroll
-        for (int k = 0; k < kPageBatch; ++k)
+        for (int k = 0; k < kPageBatch; ++k) {
+            last += v[k] == 0;
             if (v[k] < 0 && x0 + 32 * k < hi)
                 record_error(err, kErrBadMetadata, owner_of(s_off, n, (int)(x0 + 32 * k)));
+        }
     });
+    last = __reduce_add_sync(0xffffffffu, last);
+    if (lane == 0)
+        s_freed[warp] = last;
     cluster_sync_all();
+    const int wanted = sum_freed(before);
+    if (!empty && wanted > cursor) {
+        // nothing is released: give every reference back
+        for_batches([&](int64_t, const int(&ids)[kPageBatch]) {
+            for (int k = 0; k < kPageBatch; ++k)
+                if (ids[k] >= 0)
+                    atomicAdd(a.shares_out + ids[k], 1);
+        });
+        for (int b = gtid; b < n; b += gsize)
+            a.seq_lens[b] = a.context_lens[b];
+        if (gtid == 0) {
+            record_error(err, kErrBudget, wanted);
+            *a.cursor_out = cursor;
+        }
+        cluster_sync_all();  // (the sums in shared memory have been read too)
+        return;
+    }
     for_batches([&](int64_t x0, const int(&ids)[kPageBatch]) {
         int v[kPageBatch];
         counts_of(ids, v);
@@ -346,53 +391,34 @@ __global__ void __launch_bounds__(kPageThreads, 1) release_pages_kernel(const Pa
     if (lane == 0)
         s_freed[warp] = freed;
     cluster_sync_all();
-    // pages freed before this warp's, and by all
-    int before = 0, all = 0;
-    for (int r = 0; r < (int)gridDim.x; ++r) {
-        const uint32_t at = mapa_shared(smem_addr(s_freed + lane), (uint32_t)r);
-        int x;
-        asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(x) : "r"(at) : "memory");
-        const bool earlier = r < (int)blockIdx.x || (r == (int)blockIdx.x && lane < warp);
-        before += earlier ? x : 0;
-        all += x;
-    }
-    before = __reduce_add_sync(0xffffffffu, before);
-    all = __reduce_add_sync(0xffffffffu, all);
-    const bool no_room = !empty && all > cursor;
+    // (as many as were counted, but for counts below 0 at the call's start: a page
+    // of such a count that does not fit is not kept)
+    const int all = sum_freed(before);
     for_batches([&](int64_t x0, const int(&ids)[kPageBatch]) {
         int v[kPageBatch];
         counts_of(ids, v);
 #pragma unroll
         for (int k = 0; k < kPageBatch; ++k) {
-            // (a page's other references read its mark, 0 or -1: none is theirs)
+            // (a page's other references read its mark or 0: neither is theirs)
             const bool mine = v[k] == -kReleaseMark - (int)(x0 + 32 * k);
             const uint32_t who = __ballot_sync(0xffffffffu, mine);
             if (mine) {
-                if (!no_room)
-                    a.free_pages[cursor - all + before + __popc(who & ((1u << lane) - 1u))] = ids[k];
-                a.shares_out[ids[k]] = no_room ? -1 : 0;
+                const int at = cursor - all + before + __popc(who & ((1u << lane) - 1u));
+                if (at >= 0)
+                    a.free_pages[at] = ids[k];
+                a.shares_out[ids[k]] = 0;
             }
             before += __popc(who);
         }
     });
-    cluster_sync_all();  // (the counts in shared memory have been read too)
-    if (no_room) {
-        // nothing is released: give every reference back
-        for_batches([&](int64_t, const int(&ids)[kPageBatch]) {
-            for (int k = 0; k < kPageBatch; ++k)
-                if (ids[k] >= 0)
-                    atomicAdd(a.shares_out + ids[k], 1);
-        });
-    }
     for (int b = gtid; b < n; b += gsize)
-        a.seq_lens[b] = empty || no_room ? a.context_lens[b] : s_keep[b];
+        a.seq_lens[b] = empty ? a.context_lens[b] : s_keep[b];
     if (gtid == 0) {
-        if (no_room)
-            record_error(err, kErrBudget, all);
-        else if (empty)
+        if (empty)
             record_error(err, kErrBadMetadata, n);
-        *a.cursor_out = empty || no_room ? cursor : cursor - all;
+        *a.cursor_out = empty ? cursor : max(cursor - all, 0);
     }
+    cluster_sync_all();  // (the counts in shared memory have been read too)
 }
 
 static size_t release_smem(int num_seqs) { return ((size_t)2 * num_seqs + 1) * 4; }
