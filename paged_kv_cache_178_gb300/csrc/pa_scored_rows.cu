@@ -343,6 +343,21 @@ __global__ void __launch_bounds__(kRowsThreads, RowsCfg<DH, MT>::kCtas)
                 }
             }
             // scores in log2 units, what is hidden at -inf; their row maxima
+            auto each_score = [&](auto f) {
+#pragma unroll
+                for (int i = 0; i < MT; ++i)
+#pragma unroll
+                    for (int j = 0; j < NT; ++j)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            s[i][j][e] = f(s[i][j][e]);
+            };
+            if (p.cap_log2 > kCapNarrow)
+                each_score([&](float z) { return capped_wide(z, p.scale_log2, p.cap_log2); });
+            else if (p.cap_log2 > 0.f)
+                each_score([&](float z) { return capped(z, p.scale_log2, p.cap_log2); });
+            else
+                each_score([&](float z) { return z * p.scale_log2; });
             const bool all = (k0 >= lo_max && k0 + KB - 1 <= pos_min) || k0 + KB <= x.v.prefix;
             float mx[2 * MT];
 #pragma unroll
@@ -354,7 +369,6 @@ __global__ void __launch_bounds__(kRowsThreads, RowsCfg<DH, MT>::kCtas)
                     for (int e = 0; e < 2; ++e) {
                         float &z = s[i / 2][j][(i % 2) * 2 + e];
                         const int key = k0 + warp * KW + j * 8 + t4 * 2 + e;
-                        z = p.cap_log2 > 0.f ? capped(z, p.scale_log2, p.cap_log2) : z * p.scale_log2;
                         if (p.slopes)
                             z -= slope[i] * (float)(abs(r_pos[i] - key) - r_near[i]);
                         if (bad_pages && (bad_pages >> ((key - k0) / 16) & 1u))

@@ -95,7 +95,7 @@ cudaError_t launch_scored_tiles(const ScoreParams &p, int32_t head_dim, void *wo
     // of keys and values up to 2^20 is far from overflow (and a row that overflows
     // all the same is computed again key by key).
     const int mode = p.slopes                              ? kModeAny
-                     : p.cap_log2 > 0.f                    ? (p.cap_log2 <= 80.f ? kModeCapped : kModeAny)
+                     : p.cap_log2 > 0.f                    ? (p.cap_log2 <= kCapNarrow ? kModeCapped : kModeAny)
                                                            : kModePlain;
     snprintf(info, info_len, "scored attention dh=%d kernel=tiles-m%d mode=%d grid=%d tiles=%lld", head_dim, 128 * s.nt, mode,
              w.ctas, (long long)tiles);

@@ -618,16 +618,12 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         const uint32_t ocol = tmem + lane_off + C::kOCol + (NT == 2 ? (uint32_t)wg * 128u : 0u);
         uint32_t s_seen = 0, m_base[2] = {0, 0}, pv_base = 0;
         const float c1 = p.scale_log2, cap = p.cap_log2;
-        // tanh(y) / y as a polynomial in y^2 for |y| <= 3/8 (least squares with
-        // weights moved to the largest errors: off by 5.8e-08 of itself at most), times cap.
-        // (For |y| <= 1/2 it is 2.3e-6 of itself, which lse showed, and another term
-        // took 4 percent of the time.)
         const float y1 = c1 * (0.5f * kLn2);  // raw score to y: c1 = 2 scale log2 e / soft_cap
-        const float limit = 0.375f / y1;
-        const uint64_t t0 = pack_f32x2(cap * 0.9999999418615936f, cap * 0.9999999418615936f);
-        const uint64_t t1 = pack_f32x2(cap * -0.33331991737634636f, cap * -0.33331991737634636f);
-        const uint64_t t2 = pack_f32x2(cap * 0.13284822465485238f, cap * 0.13284822465485238f);
-        const uint64_t t3 = pack_f32x2(cap * -0.04828743407056177f, cap * -0.04828743407056177f);
+        const float limit = kTanhReach / y1;
+        const uint64_t t0 = pack_f32x2(cap * kTanh0, cap * kTanh0);
+        const uint64_t t1 = pack_f32x2(cap * kTanh1, cap * kTanh1);
+        const uint64_t t2 = pack_f32x2(cap * kTanh2, cap * kTanh2);
+        const uint64_t t3 = pack_f32x2(cap * kTanh3, cap * kTanh3);
         const uint64_t yy1 = pack_f32x2(y1, y1);
         for (int item = lo; item < hi; item < hi ? next_group<DH, NT>(p, x, heads) : (void)0) {
             const Part s = part_of(item);
@@ -731,7 +727,11 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                             const uint32_t keep = all ? ~0u : seen(ch);
                             const bool some = all || __any_sync(0xffffffffu, keep != 0u);
                             if (MODE == kModeAny && some) {
-                                if (cap > 0.f)
+                                if (cap > kCapNarrow)
+#pragma unroll
+                                    for (int k = 0; k < 32; ++k)
+                                        v[k] = __float_as_uint(capped_wide(__uint_as_float(v[k]), c1, cap));
+                                else if (cap > 0.f)
 #pragma unroll
                                     for (int k = 0; k < 32; ++k)
                                         v[k] = __float_as_uint(capped(__uint_as_float(v[k]), c1, cap));

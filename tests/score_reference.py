@@ -21,7 +21,7 @@ def seen_keys(n, new, window=0, prefix=0, first=None, device="cpu"):
 
 
 def attention(q, k_cache, v_cache, tables, lens, starts, scale, soft_cap=0.0, slopes=None, window=0, prefix_lens=None,
-              first_keys=None):
+              first_keys=None, small_cap_error=False):
     """out [T, Hq, Dh], lse [T, Hq] and the bounds of a 32-bit computation's
     error, all float64.  Hidden keys take no part, whatever they hold.
 
@@ -31,7 +31,10 @@ def attention(q, k_cache, v_cache, tables, lens, starts, scale, soft_cap=0.0, sl
     the largest magnitude among them: together `delta`, an error of the exponent.
     Probabilities are rounded to BF16 (2^-8 of each), the result too:
       out: 2^-8 |out| + (2^-8 + 2 delta) sum_j p_j |v_j|, twice delta for the sum;
-      lse: delta + n 2^-24 (a chain of n additions) + 2^-22 |lse|."""
+      lse: delta + n 2^-24 (a chain of n additions) + 2^-22 |lse|.
+    With small_cap_error a cap above 56 adds 2^-19 of the capped score instead:
+    0.358 of the cap and more (|z| > 3/8 of it) are good to 2.3 units of 2^-22 of the
+    cap, less to a dozen roundings of themselves."""
     T, hq, dh = q.shape
     group = hq // k_cache.shape[2]
     dev = q.device
@@ -62,12 +65,13 @@ def attention(q, k_cache, v_cache, tables, lens, starts, scale, soft_cap=0.0, sl
             reach = x.abs() @ kk.abs().T * scale
             if soft_cap:
                 z = soft_cap * torch.tanh(z / soft_cap)
-            size = z.abs()
+            size = z_cap = z.abs()
             if slopes is not None:
                 bias = slopes[h].double() * dist
                 size = torch.maximum(size, (bias - slopes[h].double() * near).abs())
                 z = z - bias
-            delta = reach * dh * 2.0**-23 + soft_cap * 2.0**-21 + size * 2.0**-22 + 2.0**-21
+            of_cap = soft_cap * 2.0**-21 if soft_cap <= 56 or not small_cap_error else z_cap * 2.0**-19
+            delta = reach * dh * 2.0**-23 + of_cap + size * 2.0**-22 + 2.0**-21
             z = torch.where(see, z, torch.full_like(z, -math.inf))
             lse[s0:s1, h] = torch.logsumexp(z, 1)
             w = torch.where(see, torch.exp(z - lse[s0:s1, h, None]), torch.zeros_like(z))
