@@ -43,21 +43,24 @@ __device__ __forceinline__ bool wait_parked(uint32_t bar, uint32_t parity, volat
     }
 }
 
-// Keys that a tile of rows sees: a prefix and one range (a hull: keys inside
-// it may be hidden from every row).
+// Keys that a tile of rows sees: a prefix and one range.  Tokens that see something
+// see their own position, so the range is a hull with keys that no row sees only
+// where tokens that see nothing lie between tokens that do.
 struct TileView {
     int prefix, lo, hi;  // [0, prefix) and [lo, hi); hi <= lo: no range
+    bool gaps;           // some keys of the range may be hidden from every row
 };
 
 // rows [r0, r1) of a request (row = token * group + head)
 __device__ __forceinline__ TileView tile_view(const ScoreParams &p, int b, const ReqMeta &m, int r0, int r1)
 {
-    TileView v{0, 0, 0};
+    TileView v{0, 0, 0, false};
     if (r0 >= r1)
         return v;
     v.prefix = score_prefix(p, b, m.L);
     const int t0 = r0 / p.group, t1 = (r1 - 1) / p.group;
     const int base = m.L - m.qn;
+    int seeing = 0, from = 0;
     v.lo = INT32_MAX;
     v.hi = 0;
     if (!p.first_keys) {
@@ -69,10 +72,37 @@ __device__ __forceinline__ TileView tile_view(const ScoreParams &p, int b, const
             if (lo <= pos) {
                 v.lo = min(v.lo, lo);
                 v.hi = pos + 1;
+                from = seeing++ ? from : pos;
             }
         }
+        v.gaps = seeing < v.hi - from;
     }
     return v;
+}
+
+// Whether one of n tokens (the first of them token t0 of all, at position pos0)
+// sees a key of the page at k0 in its range.
+static __device__ __noinline__ bool page_in_ranges(const ScoreParams &p, int64_t t0, int pos0, int n, int k0)
+{
+    for (int i = max(k0 - pos0, 0); i < n; ++i) {
+        const int lo = score_low(p, t0 + i, pos0 + i);
+        if (lo <= pos0 + i && lo < k0 + 16)
+            return true;
+    }
+    return false;
+}
+
+// Whether rows [r0, r1) of a request see a key of the page at k0 (v: their view).
+__device__ __forceinline__ bool page_needed(const ScoreParams &p, const ReqMeta &m, const TileView &v, int r0, int r1, int k0)
+{
+    if (k0 < v.prefix)
+        return true;
+    if (k0 >= v.hi || k0 + 16 <= v.lo)
+        return false;
+    if (!v.gaps)
+        return true;
+    const int t0 = r0 / p.group;
+    return page_in_ranges(p, (int64_t)m.qs + t0, m.L - m.qn + t0, (r1 - 1) / p.group - t0 + 1, k0);
 }
 
 // Blocks of `keys` keys that hold what a tile sees: the prefix's np first ones,

@@ -217,7 +217,8 @@ __global__ void __launch_bounds__(kRowsThreads, RowsCfg<DH, MT>::kCtas)
             for (; item < end; ++item) {
                 const int k0 = block_key(x, item - x.g0) + pg * 16;
                 // pages that hold no key which the tile sees are not read
-                const bool need = k0 < x.v.prefix || (k0 < x.v.hi && k0 + 16 > x.v.lo);
+                const int rows = x.m.qn * p.group;
+                const bool need = page_needed(p, x.m, x.v, x.tile * R, min(x.tile * R + R, rows), k0);
                 int id = need ? __ldg(bt + k0 / 16) : -1;
                 const bool bad = need && (id < 0 || (int64_t)id >= p.num_blocks);
                 if (bad)

@@ -116,7 +116,7 @@ __device__ __forceinline__ int group_tiles(const ScoreParams &p, const ReqMeta &
 // tile_view of rows [r0, r1) by a whole warp.
 __device__ __forceinline__ TileView warp_tile_view(const ScoreParams &p, int b, const ReqMeta &m, int r0, int r1)
 {
-    TileView v{0, 0, 0};
+    TileView v{0, 0, 0, false};
     if (r0 >= r1)
         return v;
     v.prefix = score_prefix(p, b, m.L);
@@ -126,16 +126,19 @@ __device__ __forceinline__ TileView warp_tile_view(const ScoreParams &p, int b, 
         v.hi = base + t1 + 1;
         return v;
     }
-    int lo = INT32_MAX, hi = 0;
+    int lo = INT32_MAX, hi = 0, from = INT32_MAX, seeing = 0;
     for (int t = t0 + (int)(threadIdx.x % 32); t <= t1; t += 32) {
         const int pos = base + t, l = score_low(p, (int64_t)m.qs + t, pos);
         if (l <= pos) {
             lo = min(lo, l);
             hi = pos + 1;
+            from = min(from, pos);
+            ++seeing;
         }
     }
     v.lo = __reduce_min_sync(0xffffffffu, lo);
     v.hi = __reduce_max_sync(0xffffffffu, hi);
+    v.gaps = (int)__reduce_add_sync(0xffffffffu, seeing) < v.hi - __reduce_min_sync(0xffffffffu, from);
     return v;
 }
 
@@ -182,7 +185,7 @@ __device__ __forceinline__ void next_group(const ScoreParams &p, TileGroup &x, i
     } while (x.n == 0);
 }
 
-// Whether a tile of 16 keys at k0 holds one that the group sees.
+// Whether the page at k0 holds a key of the group's prefix or range.
 __device__ __forceinline__ bool page_seen(const TileView &v, int k0)
 {
     return k0 < v.prefix || (k0 < v.hi && k0 + 16 > v.lo);
@@ -382,9 +385,15 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         // -------------------------------------------------------- producer --
         uint32_t pos = 0;  // units so far
         const int pg = lane % 8, cb = (lane / 8) % 2;
-        auto ids_of = [&](int j) {
-            const int k0 = tile_key(x.t, j) + pg * 16;
-            return page_seen(x.v, k0) ? __ldg(p.block_tables + (int64_t)x.b * p.max_blocks + k0 / 16) : -1;
+        struct Page {
+            int id;
+            bool needed;
+        };
+        // (pages that hold no key which the group sees are not read)
+        auto page_of = [&](int j) {
+            const int k0 = tile_key(x.t, j) + pg * 16, rows = x.m.qn * p.group;
+            const bool needed = page_needed(p, x.m, x.v, x.tile * RT, min(x.tile * RT + RT, rows), k0);
+            return Page{needed ? __ldg(p.block_tables + (int64_t)x.b * p.max_blocks + k0 / 16) : -1, needed};
         };
         auto load = [&](const CUtensorMap *map, int units, int col0, int id) {
             for (int u = 0; ok && u < units; ++u, ++pos) {
@@ -409,8 +418,8 @@ __global__ void __launch_bounds__(kTileThreads, 1)
             if (n == 0)
                 continue;
             const int v_col = x.hv % C::kSplit * C::kCols;
-            auto check = [&](int raw, int j) {
-                const bool bad = page_seen(x.v, tile_key(x.t, j) + pg * 16) && (raw < 0 || (int64_t)raw >= p.num_blocks);
+            auto check = [&](const Page &page) {
+                const bool bad = page.needed && (page.id < 0 || (int64_t)page.id >= p.num_blocks);
                 if (__any_sync(0xffffffffu, bad)) {
                     if (lane == 0) {
                         record_error(p.err, kErrBadMetadata, x.b);
@@ -418,15 +427,16 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                     }
                     __syncwarp();
                 }
-                return bad ? -1 : raw;
+                return bad ? -1 : page.id;
             };
-            int cur = check(ids_of(j0), j0), ahead = n > 1 ? ids_of(j0 + 1) : -1;
+            int cur = check(page_of(j0));
+            Page ahead = n > 1 ? page_of(j0 + 1) : Page{-1, false};
             load(&tm_k, UK, 0, cur);
             for (int j = 0; ok && j < n; ++j) {
                 const int id = cur;
                 if (j + 1 < n) {
-                    cur = check(ahead, j0 + j + 1);
-                    ahead = j + 2 < n ? ids_of(j0 + j + 2) : -1;
+                    cur = check(ahead);
+                    ahead = j + 2 < n ? page_of(j0 + j + 2) : Page{-1, false};
                 }
                 if (NT == 2)
                     load(&tm_v, UV, v_col, id);
