@@ -243,7 +243,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     uint8_t *s_out = s_ring + NS * kUnitBytes; // [8 warps][32 rows][128 bytes]
     uint8_t *small = s_out + C::kOutBytes;
     uint64_t *bars = reinterpret_cast<uint64_t *>(small);
-    volatile int *s_flags = reinterpret_cast<volatile int *>(small + 256);  // [0] abort [1] tmem [2] bad [4..8) start
+    volatile int *s_flags = reinterpret_cast<volatile int *>(small + 256);  // [0] abort [1] tmem [4..7) start [8..16) bad pages in a segment
     float *s_m = reinterpret_cast<float *>(small + 512);                    // [128] the shared running maximum
     float *s_l = s_m + 128;                                                 // [2][128] the two halves' sums
     volatile int *abort_flag = s_flags;
@@ -267,7 +267,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         mbar_init(bar(B_DONE), 1);
         for (int i = 0; i < NS; ++i)
             mbar_init(bar(B_Z + i), 1);
-        s_flags[0] = s_flags[2] = 0;
+        s_flags[0] = 0;
         fence_barrier_init();
     }
     griddep_wait();
@@ -418,12 +418,18 @@ __global__ void __launch_bounds__(kTileThreads, 1)
             if (n == 0)
                 continue;
             const int v_col = x.hv % C::kSplit * C::kCols;
+            // (Read when the segment's products are done.  The copies of a segment need
+            // at least two stages, and the products of the next one wait for this one's
+            // softmax, so the producer is less than eight segments ahead of a reader.)
+            static_assert(NS <= 8, "flags of bad pages");
+            if (lane == 0)
+                s_flags[8 + seg % 8] = 0;
             auto check = [&](const Page &page) {
                 const bool bad = page.needed && (page.id < 0 || (int64_t)page.id >= p.num_blocks);
                 if (__any_sync(0xffffffffu, bad)) {
                     if (lane == 0) {
                         record_error(p.err, kErrBadMetadata, x.b);
-                        s_flags[2] = 1;  // every row is then computed key by key
+                        s_flags[8 + seg % 8] = 1;
                     }
                     __syncwarp();
                 }
@@ -445,6 +451,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                 if (NT == 1)
                     load(&tm_v, UV, v_col, id);
             }
+            ++seg;
             // V rows past the request's length (in its last tile) become zeros
             const int k_last = tile_key(x.t, j0 + n - 1), row0 = stale_row(x, k_last);
             if (ok && row0 < kTileKeys) {
@@ -545,7 +552,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                 }
                 if (ok) {
                     mma_commit(bar(B_O));
-                    mbar_arrive(bar(B_O));  // (and what this thread has seen of the producer's flag)
+                    mbar_arrive(bar(B_O));  // (and what this thread has seen of the producer's flags)
                 }
             }
             ok = __shfl_sync(0xffffffffu, ok, 0);
@@ -875,7 +882,19 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                 named_sync(1, 256);
                 l = s_l[r] + s_l[128 + r];
             }
-            const bool lost = !ok || s_flags[2];
+            // rows that see a key of a bad page (its keys and values came as zeros) are NaN
+            if (ok && s_flags[8 + seg % 8]) {
+                bool bad = false;
+                for (int i = 0; valid && i < n * (kTileKeys / 16); ++i) {
+                    const int page = tile_key(x.t, j0 + i / (kTileKeys / 16)) + i % (kTileKeys / 16) * 16;
+                    if (page < prefix || (page <= pos && page + 16 > r_lo && r_len > 0)) {
+                        const int id = __ldg(p.block_tables + (int64_t)x.b * p.max_blocks + page / 16);
+                        bad |= id < 0 || (int64_t)id >= p.num_blocks;
+                    }
+                }
+                l = bad ? __int_as_float(0x7FC00000) : l;
+            }
+            const bool lost = !ok;
             const int col0 = NT == 2 ? 0 : wg * COLS_W;  // of the group's columns
             const float inv = l == 0.f ? 0.f : 1.f / l;
             bool odd = lost || !(fabsf(l) < INFINITY);
