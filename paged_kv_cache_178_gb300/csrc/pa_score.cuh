@@ -124,9 +124,12 @@ __device__ __forceinline__ float capped_wide(float raw, float scale_log2, float 
 
 // One (token, head) row by one warp, key by key, over exactly the keys that it
 // sees: what no row sees is not read, so nothing there (NaN, infinities, a
-// page of another request) can matter.
+// page of another request) can matter.  Who finds its part of a row not finite
+// has that part written, columns [c0, c0 + cols) (multiples of 32) and, with_lse,
+// the row's lse: others may be storing theirs.
 template <int DH>
-__device__ __noinline__ void scored_row(const ScoreParams &p, int b, const ReqMeta &m, int i, int h)
+__device__ __noinline__ void scored_row(const ScoreParams &p, int b, const ReqMeta &m, int i, int h, int c0, int cols,
+                                        bool with_lse)
 {
     constexpr int E = DH / 32;  // elements of a lane
     const int lane = threadIdx.x % 32, kvh = h / p.group;
@@ -174,7 +177,8 @@ __device__ __noinline__ void scored_row(const ScoreParams &p, int b, const ReqMe
             l = l * keep + w;
 #pragma unroll
             for (int e = 0; e < E; ++e)
-                o[e] = o[e] * keep + w * __bfloat162float(p.v[at + e * 32 + lane]);
+                if (e * 32 >= c0 && e * 32 < c0 + cols)
+                    o[e] = o[e] * keep + w * __bfloat162float(p.v[at + e * 32 + lane]);
             mx = m_new;
         }
     }
@@ -182,8 +186,9 @@ __device__ __noinline__ void scored_row(const ScoreParams &p, int b, const ReqMe
     __nv_bfloat16 *dst = p.out + (t * p.hq + h) * DH;
 #pragma unroll
     for (int e = 0; e < E; ++e)
-        dst[e * 32 + lane] = __float2bfloat16_rn(o[e] * inv);
-    if (lane == 0 && p.lse)
+        if (e * 32 >= c0 && e * 32 < c0 + cols)
+            dst[e * 32 + lane] = __float2bfloat16_rn(o[e] * inv);
+    if (lane == 0 && with_lse && p.lse)
         p.lse[t * p.hq + h] = bad ? __int_as_float(0x7FC00000)
                                   : score_lse(mx, l, slope * (float)near);
     if (bad && lane == 0)

@@ -583,7 +583,7 @@ __global__ void __launch_bounds__(kFoldThreads) scored_fold_kernel(const ScorePa
         p.lse[at] = score_lse(top, sum, slope * (float)near);
     }
     if (__syncthreads_or(odd) && warp == 0)
-        scored_row<DH>(p, b, m, tok, h);
+        scored_row<DH>(p, b, m, tok, h, 0, DH, !(fabsf(sum) < INFINITY));
 }
 
 // --------------------------------------------------------------------- host --

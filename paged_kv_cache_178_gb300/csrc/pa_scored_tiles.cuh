@@ -971,7 +971,9 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                 __syncwarp();
                 for (uint32_t todo = __ballot_sync(0xffffffffu, odd && valid); todo; todo &= todo - 1) {
                     const int from = __ffs(todo) - 1;
-                    scored_row<DH>(p, x.b, x.m, __shfl_sync(0xffffffffu, tok, from), __shfl_sync(0xffffffffu, head, from));
+                    const bool sum_odd = __shfl_sync(0xffffffffu, lost || !(fabsf(l) < INFINITY), from);
+                    scored_row<DH>(p, x.b, x.m, __shfl_sync(0xffffffffu, tok, from), __shfl_sync(0xffffffffu, head, from),
+                                   part * C::kCols + col0, COLS_W, sum_odd && part == 0 && col0 == 0);
                 }
             }
             m_base[0] += (uint32_t)(n + 1) / 2;
@@ -1078,7 +1080,9 @@ __global__ void __launch_bounds__(kTileFoldThreads) scored_tile_fold_kernel(cons
     __syncwarp();
     for (uint32_t todo = __ballot_sync(0xffffffffu, odd && valid); todo; todo &= todo - 1) {
         const int from = __ffs(todo) - 1;
-        scored_row<DH>(p, b, m, __shfl_sync(0xffffffffu, tok, from), __shfl_sync(0xffffffffu, head, from));
+        scored_row<DH>(p, b, m, __shfl_sync(0xffffffffu, tok, from), __shfl_sync(0xffffffffu, head, from),
+                       part * C::kCols + cb * 32, 32,
+                       __shfl_sync(0xffffffffu, !(fabsf(sum) < INFINITY), from) && part == 0 && cb == 0);
     }
 }
 

@@ -1,0 +1,72 @@
+"""Rows whose result is not finite beside rows whose is, in pa_paged_attention_scored:
+the same bits every time, and nothing changes for who does not see the cause."""
+import math
+
+import pytest
+import torch
+
+from paged_kv_cache_178_gb300 import pagedattn as pa
+from tests.test_gpu_scored_attention import _batch, _slopes
+
+pytestmark = pytest.mark.gpu
+
+RULES = {"plain": {}, "cap": dict(soft_cap=20.0), "bias": dict(slopes=True)}
+
+
+def _run(a, rules):
+    rules = {k: _slopes(a["q"].shape[1]) if v is True else v for k, v in rules.items()}
+    out, lse = pa.paged_attention_scored(**a, **rules)
+    return out, lse, pa.check_errors()
+
+
+# one group to many CTAs, many groups to a CTA, both; one row tile and two
+BATCHES = [([1500], [40]), ([1500], [600]), ([90] * 200, [90] * 200), ([700, 300, 1200], [700, 20, 33])]
+
+
+@pytest.mark.parametrize("heads", [(8, 2, 128), (4, 1, 256), (16, 1, 256), (4, 1, 512)])
+@pytest.mark.parametrize("batch", range(len(BATCHES)))
+@pytest.mark.parametrize("rule", list(RULES))
+def test_one_bad_column_and_the_same_bits_every_time(rule, batch, heads):
+    """An infinity in one column of a value: every repeat gives the same bits, lse is
+    what it is without it (it does not depend on values), and rows that do not see
+    the key keep their results within the rounding of the probabilities."""
+    lens, new = BATCHES[batch]
+    a = _batch(lens, new, *heads, seed=1)
+    rules = dict(RULES[rule], window=64)
+    clean = _run(a, rules)
+    for b, n in enumerate(lens):
+        j = n - new[b] // 2 - 1
+        a["v_cache"][int(a["block_tables"][b, j // 16]), j % 16, :, (7 * b + 40) % heads[2]] = math.inf
+    first = _run(a, rules)
+    assert first[2] == (0, -1) and torch.equal(first[1], clean[1])
+    for _ in range(8):
+        again = _run(a, rules)
+        assert torch.equal(first[0].view(torch.int16), again[0].view(torch.int16)) and torch.equal(first[1], again[1])
+    starts = a["query_start_loc"].tolist()
+    for b, n in enumerate(lens):
+        j, d = n - new[b] // 2 - 1, (7 * b + 40) % heads[2]
+        pos = torch.arange(n - new[b], n, device="cuda")
+        sees = (pos >= j) & (pos - j < 64)
+        rows = slice(starts[b], starts[b + 1])
+        got, want = first[0][rows], clean[0][rows]
+        assert bool((got[sees][..., d] == math.inf).all()), b
+        finite = got.isfinite()
+        finite[..., d] |= sees[:, None]
+        assert bool(finite.all()), b
+        # (both are within 2^-8 of the value and 2^-8 of the values' size, here below 4)
+        err = torch.where(got.isfinite(), (got.double() - want.double()).abs(), torch.zeros((), dtype=torch.float64, device="cuda"))
+        assert bool((err <= 2.0**-6 * (want.double().abs() + 4)).all()), b
+
+
+@pytest.mark.parametrize("heads", [(8, 2, 128), (4, 1, 512)])
+def test_columns_of_other_owners_keep_their_bits(heads):
+    """Head dim 512: the halves of the columns are computed apart; a part of a group:
+    32 columns at a time.  Who owns sound columns stores what it stores without the
+    bad one."""
+    a = _batch([1500], [40 if heads[2] == 128 else 100], *heads, seed=2)
+    clean = _run(a, {})
+    a["v_cache"][int(a["block_tables"][0, 3]), 1, :, 1] = math.inf
+    out, lse, _ = _run(a, {})
+    assert bool((out[..., 1] == math.inf).all()) and torch.equal(lse, clean[1])
+    from_ = 32 if heads[2] == 128 else 256
+    assert torch.equal(out[..., from_:], clean[0][..., from_:])
