@@ -223,6 +223,47 @@ __device__ __forceinline__ void for_chunks(uint32_t scol, F f)
 // Bits below n.
 __device__ __forceinline__ uint32_t bits_below(int n) { return n <= 0 ? 0u : (n >= 32 ? ~0u : (1u << n) - 1u); }
 
+// The rows of the groups that lie wholly in a CTA's range [lo, hi), which begins in
+// row tile `tile` of request b (`first` items of one head before it), whose result is
+// not finite though their sum is: computed again key by key, over exactly their own
+// keys (one that only other rows of the tile see may have met a zero probability
+// with an infinity or a NaN).  By all warps once the CTA's other work is done: a row
+// takes 0.3 us and more for each key, and no wait of another warp may last so long.
+template <int DH, int NT>
+__device__ __noinline__ void repair_groups(const ScoreParams &p, int b, int tile, int first, int lo, int hi)
+{
+    using C = TileCfg<DH, NT>;
+    constexpr int RT = NT * 128;
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, heads = p.hkv * C::kSplit;
+    TileGroup x;
+    x.b = b;
+    x.tile = tile;
+    x.m = score_meta(p, x.b);
+    load_group<DH, NT>(p, x);
+    x.hv = (lo - first * heads) / x.w;
+    x.g0 = first * heads + x.hv * x.w;
+    for (int item = lo; item < hi; item < hi ? next_group<DH, NT>(p, x, heads) : (void)0) {
+        item = min(hi, x.g0 + x.w);
+        if (x.g0 + kGroupSetup<NT> < lo || x.g0 + x.w > hi)
+            continue;  // others have a part
+        const int rows = min(RT, x.m.qn * p.group - x.tile * RT), part = x.hv % C::kSplit;
+        for (int r = warp; r < rows; r += kTileThreads / 32) {
+            const int row = x.tile * RT + r, tok = row / p.group, head = x.hv / C::kSplit * p.group + row - tok * p.group;
+            const int64_t at = ((int64_t)x.m.qs + tok) * p.hq + head;
+            const uint32_t *out = reinterpret_cast<const uint32_t *>(p.out + at * DH + part * C::kCols);
+            bool odd = false;
+            for (int k = lane; k < C::kCols / 2; k += 32) {
+                const uint32_t v = __ldcg(out + k);
+                odd |= (v & 0x7F80u) == 0x7F80u || (v & 0x7F800000u) == 0x7F800000u;
+            }
+            if (__any_sync(0xffffffffu, odd)) {
+                const float lse = part == 0 && p.lse ? __ldcg(p.lse + at) : 0.f;
+                scored_row<DH>(p, x.b, x.m, tok, head, part * C::kCols, C::kCols, lse != lse);
+            }
+        }
+    }
+}
+
 template <int DH, int NT, int MODE>
 __global__ void __launch_bounds__(kTileThreads, 1)
     scored_tiles_kernel(const __grid_constant__ ScoreParams p, const __grid_constant__ CUtensorMap tm_k,
@@ -243,7 +284,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     uint8_t *s_out = s_ring + NS * kUnitBytes; // [8 warps][32 rows][128 bytes]
     uint8_t *small = s_out + C::kOutBytes;
     uint64_t *bars = reinterpret_cast<uint64_t *>(small);
-    volatile int *s_flags = reinterpret_cast<volatile int *>(small + 256);  // [0] abort [1] tmem [4..7) start [8..16) bad pages in a segment
+    volatile int *s_flags = reinterpret_cast<volatile int *>(small + 256);  // [0] abort [1] tmem [2] odd rows [4..7) start [8..16) bad pages in a segment
     float *s_m = reinterpret_cast<float *>(small + 512);                    // [128] the shared running maximum
     float *s_l = s_m + 128;                                                 // [2][128] the two halves' sums
     volatile int *abort_flag = s_flags;
@@ -267,7 +308,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         mbar_init(bar(B_DONE), 1);
         for (int i = 0; i < NS; ++i)
             mbar_init(bar(B_Z + i), 1);
-        s_flags[0] = 0;
+        s_flags[0] = s_flags[2] = 0;
         fence_barrier_init();
     }
     griddep_wait();
@@ -894,10 +935,12 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                 }
                 l = bad ? __int_as_float(0x7FC00000) : l;
             }
-            const bool lost = !ok;
+            // (after a wait that ran out a part's sum is NaN, and so are whole rows)
+            if (!ok)
+                l = __int_as_float(0x7FC00000);
             const int col0 = NT == 2 ? 0 : wg * COLS_W;  // of the group's columns
             const float inv = l == 0.f ? 0.f : 1.f / l;
-            bool odd = lost || !(fabsf(l) < INFINITY);
+            bool odd = !ok;
             float *rec = w.records + (2 * (int64_t)c + (x.g0 + kGroupSetup<NT> < lo ? 0 : 1)) * w.record_floats +
                          (NT == 2 ? wg : 0) * tile_record(C::kCols);
             const int64_t at = ((int64_t)x.m.qs + tok) * p.hq + head;
@@ -929,7 +972,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                         check = __fmaf_rn(f, 0.f, check);
                         o[k] = __float_as_uint(f);
                     }
-                    odd |= check != 0.f;
+                    odd |= check != 0.f && fabsf(l) < INFINITY;
                     __nv_bfloat16 *out = p.out + part * C::kCols + col0 + ch;
                     if (C::kOutBytes == 0) {
                         if (valid)
@@ -959,23 +1002,20 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                     __syncwarp();
                 }
             }
+            if (!ok && whole && valid)
+                for (int k = 0; k < COLS_W / 8; ++k)
+                    reinterpret_cast<uint4 *>(p.out + at * DH + part * C::kCols + col0)[k] =
+                        make_uint4(0x7FC07FC0u, 0x7FC07FC0u, 0x7FC07FC0u, 0x7FC07FC0u);
             if (NT == 2 || wg == 0) {
                 if (!whole) {
                     rec[r] = m;
-                    rec[128 + r] = lost ? __int_as_float(0x7FC00000) : l;
+                    rec[128 + r] = l;
                 } else if (valid && part == 0 && p.lse) {
                     p.lse[at] = score_lse(m, l, slope * (float)near);
                 }
             }
-            if (whole) {
-                __syncwarp();
-                for (uint32_t todo = __ballot_sync(0xffffffffu, odd && valid); todo; todo &= todo - 1) {
-                    const int from = __ffs(todo) - 1;
-                    const bool sum_odd = __shfl_sync(0xffffffffu, lost || !(fabsf(l) < INFINITY), from);
-                    scored_row<DH>(p, x.b, x.m, __shfl_sync(0xffffffffu, tok, from), __shfl_sync(0xffffffffu, head, from),
-                                   part * C::kCols + col0, COLS_W, sum_odd && part == 0 && col0 == 0);
-                }
-            }
+            if (whole && odd && valid)
+                s_flags[2] = 1;
             m_base[0] += (uint32_t)(n + 1) / 2;
             m_base[1] += (uint32_t)n / 2;
             pv_base += (uint32_t)n;
@@ -989,11 +1029,12 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     __syncthreads();
     if (warp == 1)
         tmem_dealloc(tmem, 512);
+    if (s_flags[2])
+        repair_groups<DH, NT>(p, s_flags[4], s_flags[5], s_flags[6], lo, hi);
 }
 
 // Folds the records of the groups that several CTAs have a part of, each at the
-// place of the CTA that it begins in: two threads
-// per row, each with every second part, and 32 columns of the output a CTA.  (A
+// place of the CTA that it begins in: two threads per row, each with every second part, and 32 columns of the output a CTA.  (A
 // few rows over many keys are a part to a CTA: one thread per row, part by
 // part, took 27 of 42 us for 64 rows over 4096 keys.)
 constexpr int kTileFoldThreads = 256;

@@ -70,3 +70,36 @@ def test_columns_of_other_owners_keep_their_bits(heads):
     assert bool((out[..., 1] == math.inf).all()) and torch.equal(lse, clean[1])
     from_ = 32 if heads[2] == 128 else 256
     assert torch.equal(out[..., from_:], clean[0][..., from_:])
+
+
+def test_rows_that_take_seconds_latch_nothing():
+    """Two groups of 256 rows over 262144 keys to a CTA; an infinity that all rows of
+    the first see: they are computed again key by key, which takes longer than any
+    wait between warps may last."""
+    n, new, hq, dh, count = 262144, 32, 8, 128, 304
+    pages = n // 16
+    g = torch.Generator(device="cuda").manual_seed(3)
+    pool = torch.randn(pages + 1, 2, 16, 1, dh, generator=g, device="cuda").to(torch.bfloat16)
+    pool[pages] = pool[0]
+    pool[pages, 1, 5, 0, 9] = math.inf
+    tables = torch.arange(pages, dtype=torch.int32, device="cuda").repeat(count, 1)
+    tables[::2, 0] = pages
+    q = torch.randn(new, hq, dh, generator=g, device="cuda").to(torch.bfloat16).repeat(count, 1, 1)
+    a = dict(q=q, k_cache=pool[:, 0], v_cache=pool[:, 1], block_tables=tables,
+             seq_lens=torch.full((count,), n, dtype=torch.int32, device="cuda"),
+             query_start_loc=torch.arange(0, count * new + 1, new, dtype=torch.int32, device="cuda"), scale=dh**-0.5,
+             max_query_len=new, max_seq_len=n)
+    out, lse, st = _run(a, {})
+    assert st == (0, -1)
+    out, lse = out.unflatten(0, (count, new)), lse.unflatten(0, (count, new))
+    assert bool((out[::2, ..., 9] == math.inf).all()) and bool(out[1::2].isfinite().all())
+    assert torch.equal(lse, lse[:1].expand_as(lse))
+    clean = out[1].double()
+    for b in range(count):
+        if b % 2:
+            assert torch.equal(out[b], out[1])
+            continue
+        # (both are within 2^-8 of the value and of sum p |v|, which is below 1)
+        err = (out[b].double() - clean).abs()
+        err[..., 9] = 0
+        assert bool((err <= 2.0**-6).all())
