@@ -736,6 +736,16 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                             tmem_st16(scol + ch * 16, o);
                             return;
                         }
+                        // (hidden scores take no part in the choice of a form either: what a row
+                        // does not see changes no bit of its result)
+                        const bool some = !all && __any_sync(0xffffffffu, ~keep != 0u);
+                        auto hide = [&]() {
+#pragma unroll
+                            for (int k = 0; k < 32; ++k)
+                                v[k] = keep & (1u << k) ? v[k] : 0u;
+                        };
+                        if (some)
+                            hide();
                         float top = 0.f, top1 = 0.f;
 #pragma unroll
                         for (int k = 0; k < 32; k += 4) {
@@ -743,7 +753,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                             top1 = max3f(top1, fabsf(__uint_as_float(v[k + 2])), fabsf(__uint_as_float(v[k + 3])));
                         }
                         // (a NaN passes the test unseen and stays one in both ways)
-                        if (__all_sync(0xffffffffu, fmaxf(top, top1) <= limit)) {
+                        if (__all_sync(0xffffffffu, fmaxf(top, top1) <= limit || !valid)) {
 #pragma unroll
                             for (int k = 0; k < 32; k += 2) {
                                 const uint64_t y = mul_f32x2(pack_f32x2(__uint_as_float(v[k]), __uint_as_float(v[k + 1])), yy1);
@@ -759,11 +769,8 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                             for (int k = 0; k < 32; ++k)
                                 v[k] = __float_as_uint(ex2(capped(__uint_as_float(v[k]), c1, cap)));
                         }
-                        if (!all && __any_sync(0xffffffffu, ~keep != 0u)) {
-#pragma unroll
-                            for (int k = 0; k < 32; ++k)
-                                v[k] = keep & (1u << k) ? v[k] : 0u;
-                        }
+                        if (some)
+                            hide();
                         uint32_t o[16];
 #pragma unroll
                         for (int k = 0; k < 32; k += 4) {
