@@ -26,13 +26,12 @@ bool scored_pool_maps(const ScoreParams &p, int32_t head_dim, CUtensorMap (&tm)[
 //   32 rows   Dh 128  14.5 / 23.2   42.8 / 40.8   11.1 / 15.7
 //             Dh 256  19.9 / 27.0   73.8 / 69.8   13.5 / 18.1
 //             Dh 512  22.4 / 30.8   79.6 / 97.6   15.7 / 20.2
-//   64 rows   Dh 128  17.7 / 22.8   71.7 / 41.0   13.2 / 15.9
-//             Dh 512  28.0 / 31.1  137.2 / 98.5   19.4 / 20.5
-// From 33 on a few-rows call reads its keys twice, which only idle SMs hide.
+// (The few-rows kernel takes the rows of a request and KV head in one tile of at most
+// 32: a second tile would read the keys again.)
 static bool few_rows(int32_t num_seqs, int32_t hkv, int group, int32_t head_dim, int32_t max_query_len, int32_t max_seq_len)
 {
     return (int64_t)max_query_len * group <= 32 &&
-           scored_rows_fits(num_seqs, hkv, group, head_dim, max_query_len, max_seq_len);
+           scored_rows_fits(num_seqs, hkv, head_dim, max_seq_len);
 }
 
 bool scored_supported(int32_t num_seqs, int32_t hq, int32_t hkv, int32_t head_dim, int32_t max_query_len,

@@ -6,7 +6,6 @@
 namespace pa {
 
 constexpr int kScoredSms = 152;              // CTAs of a wave are counted by it, on the host alone
-constexpr int kScoredMaxTilesHost = 8192;    // requests times tiles of rows that a CTA sums over
 
 // Tensor maps of K and V: boxes of 64 columns by the 16 tokens of one page and head.
 bool scored_pool_maps(const ScoreParams &p, int32_t head_dim, CUtensorMap (&tm)[2]);
@@ -144,16 +143,15 @@ __device__ __forceinline__ int range_owner(int64_t total, int64_t item, int ctas
     return c;
 }
 
-bool scored_rows_fits(int32_t num_seqs, int32_t hkv, int group, int32_t head_dim, int32_t max_query_len,
-                      int32_t max_seq_len);
+bool scored_rows_fits(int32_t num_seqs, int32_t hkv, int32_t head_dim, int32_t max_seq_len);
 size_t scored_rows_bytes(int32_t num_seqs, int32_t hkv, int group, int32_t head_dim, int32_t max_query_len,
                          int32_t max_seq_len);
 cudaError_t launch_scored_rows(const ScoreParams &p, int32_t head_dim, void *workspace, cudaStream_t stream, char *info,
                                size_t info_len);
 cudaError_t init_scored_rows_attributes();
 
-// Row tiles that the batch can form (num_q_tokens < 0: by the other bounds
-// alone), and whether the kernels take that many.
+// Row tiles that the batch can form, and whether the kernels take that many
+// (num_q_tokens < 0, for a workspace's size: left to the call itself).
 constexpr int kScoredMaxEntriesHost = 24000;  // requests and row tiles that a CTA sums over
 int64_t scored_tiles_bound(int32_t num_seqs, int group, int32_t head_dim, int32_t max_query_len, int64_t num_q_tokens);
 bool scored_tiles_fits(int32_t num_seqs, int32_t hkv, int group, int32_t head_dim, int32_t max_query_len,

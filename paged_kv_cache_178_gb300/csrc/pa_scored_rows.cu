@@ -4,8 +4,8 @@
 // 16 or 32 rows do not fill an M = 128 tensor-memory tile, so the products run
 // on mma.m16n8k16, whose rate is many times what the bytes ask for.
 //
-// Work: a group is one (request, KV head, tile of rows), its items the blocks of
-// kKeys keys that some row of the tile sees.  The items of all groups are dealt
+// Work: a group is one (request, KV head), at most 32 rows, its items the blocks of
+// kKeys keys that some row sees.  The items of all groups are dealt
 // out as one wave of equal contiguous ranges, one to a CTA.  What a CTA has of a
 // group becomes a record (maximum, sum, unnormalised output) in the workspace; a
 // second kernel folds a group's records, in order.
@@ -43,16 +43,16 @@ struct RowsCfg {
 };
 
 template <int DH, int MT>
-constexpr size_t rows_smem(int seq_tiles)
+constexpr size_t rows_smem(int num_seqs)
 {
     using C = RowsCfg<DH, MT>;
     return 1024 + (size_t)C::kStages * 2 * C::kView + 16 * MT * DH * 2 + 16 * MT * (C::kKeys * 2 + 16) +
-           2 * kRowsWarps * 16 * MT * 4 + 256 + (size_t)(seq_tiles + 1) * 4;
+           2 * kRowsWarps * 16 * MT * 4 + 256 + (size_t)(num_seqs + 1) * 4;
 }
 static_assert(2 * (rows_smem<256, 2>(64) + 1024) <= kMaxSmemPerBlock + 1024, "two CTAs to an SM");
-static_assert(rows_smem<512, 2>(kScoredMaxTilesHost) <= kMaxSmemPerBlock, "shared-memory layout");
-static_assert(rows_smem<256, 2>(kScoredMaxTilesHost) <= kMaxSmemPerBlock, "shared-memory layout");
-static_assert(rows_smem<128, 2>(kScoredMaxTilesHost) <= kMaxSmemPerBlock, "shared-memory layout");
+static_assert(rows_smem<512, 2>(kScanMaxSeqs) <= kMaxSmemPerBlock, "shared-memory layout");
+static_assert(rows_smem<256, 2>(kScanMaxSeqs) <= kMaxSmemPerBlock, "shared-memory layout");
+static_assert(rows_smem<128, 2>(kScanMaxSeqs) <= kMaxSmemPerBlock, "shared-memory layout");
 
 __device__ __forceinline__ void ldsm4(uint32_t addr, uint32_t (&r)[4])
 {
@@ -85,7 +85,7 @@ struct RowsWork {
     int2 *groups;      // [num_groups] (first CTA * 4 + its record (record_slot), CTAs that have a part)
     float *records;    // [2 * ctas + num_groups] of record_floats
     int64_t record_floats;
-    int32_t ctas, qtiles, rows;  // rows of a tile that any request can fill
+    int32_t ctas, rows;  // rows that any request can fill
 };
 
 // Record of the part that a CTA (items [clo, chi)) has of a group (items [g0, g1)):
@@ -129,32 +129,29 @@ __global__ void __launch_bounds__(kRowsThreads, RowsCfg<DH, MT>::kCtas)
     uint64_t *bars = reinterpret_cast<uint64_t *>(s_sum + kRowsWarps * R);  // full[NS], empty[NS]
     volatile int *s_abort = reinterpret_cast<volatile int *>(bars + 2 * NS);
     uint32_t *s_bad = reinterpret_cast<uint32_t *>(bars + 2 * NS + 1);      // [NS] bad pages of a stage
-    int32_t *s_off = reinterpret_cast<int32_t *>(reinterpret_cast<uint8_t *>(bars) + 256);  // [seq tiles + 1]
+    int32_t *s_off = reinterpret_cast<int32_t *>(reinterpret_cast<uint8_t *>(bars) + 256);  // [num_seqs + 1]
     const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
     auto full = [&](int s) { return smem_addr(bars + s); };
     auto empty = [&](int s) { return smem_addr(bars + NS + s); };
 
-    // ----------------------------------------------- items before each tile --
-    const int ntiles = p.num_seqs * w.qtiles;
+    // -------------------------------------------- items before each request --
     int *scratch = reinterpret_cast<int *>(s_max);  // (all sums fit: at most INT32_MAX items)
     static_assert(2 * kRowsWarps * 16 >= kRowsWarps + 1, "scan scratch");
-    const int per_head = block_exclusive_sums<kRowsThreads>(ntiles, s_off, scratch, [&](int st) {
-        const int b = st / w.qtiles, tile = st - b * w.qtiles;
+    const int per_head = block_exclusive_sums<kRowsThreads>(p.num_seqs, s_off, scratch, [&](int b) {
         const ReqMeta m = score_meta(p, b);
         if (!m.ok) {
-            if (blockIdx.x == 0 && tile == 0)
+            if (blockIdx.x == 0)
                 record_error(p.err, kErrBadMetadata, b);
             return 0;
         }
-        const int rows = m.qn * p.group;
-        return tile_blocks(tile_view(p, b, m, min(tile * R, rows), min(tile * R + R, rows)), KB).count;
+        return tile_blocks(tile_view(p, b, m, 0, m.qn * p.group), KB).count;
     });
     const int total = per_head * p.hkv, ctas = min(w.ctas, total), c = blockIdx.x;
     // where the fold finds a group's parts
     auto write_groups = [&](int at, int step) {
-        for (int g = at; g < ntiles * p.hkv; g += step) {
-            const int st = g / p.hkv, n = s_off[st + 1] - s_off[st];
-            const int first = s_off[st] * p.hkv + (g - st * p.hkv) * n;
+        for (int g = at; g < p.num_seqs * p.hkv; g += step) {
+            const int b = g / p.hkv, n = s_off[b + 1] - s_off[b];
+            const int first = s_off[b] * p.hkv + (g - b * p.hkv) * n;
             w.groups[g] = n ? group_parts(total, first, first + n, ctas) : make_int2(0, 0);
         }
     };
@@ -176,7 +173,7 @@ __global__ void __launch_bounds__(kRowsThreads, RowsCfg<DH, MT>::kCtas)
 
     // the group of an item, as both sides walk through the range
     struct Group {
-        int st, b, tile, kvh, g;
+        int b, kvh, g, rows;
         int g0, g1;
         ReqMeta m;
         TileView v;
@@ -184,19 +181,15 @@ __global__ void __launch_bounds__(kRowsThreads, RowsCfg<DH, MT>::kCtas)
     };
     auto group_of = [&](int item) {
         Group x;
-        const int ph = item / p.hkv;  // no tile's items before ph / hkv are past the item
-        x.st = owner_of(s_off, ntiles, ph);
-        const int n = s_off[x.st + 1] - s_off[x.st];
-        const int first = s_off[x.st] * p.hkv;
+        x.b = owner_of(s_off, p.num_seqs, item / p.hkv);  // no request's items before that are past the item
+        const int n = s_off[x.b + 1] - s_off[x.b], first = s_off[x.b] * p.hkv;
         x.kvh = (item - first) / n;
-        x.g = x.st * p.hkv + x.kvh;
+        x.g = x.b * p.hkv + x.kvh;
         x.g0 = first + x.kvh * n;
         x.g1 = x.g0 + n;
-        x.b = x.st / w.qtiles;
-        x.tile = x.st - x.b * w.qtiles;
         x.m = score_meta(p, x.b);
-        const int rows = x.m.qn * p.group;
-        x.v = tile_view(p, x.b, x.m, min(x.tile * R, rows), min(x.tile * R + R, rows));
+        x.rows = x.m.qn * p.group;
+        x.v = tile_view(p, x.b, x.m, 0, x.rows);
         x.t = tile_blocks(x.v, KB);
         return x;
     };
@@ -216,9 +209,8 @@ __global__ void __launch_bounds__(kRowsThreads, RowsCfg<DH, MT>::kCtas)
             const int end = min(hi, x.g1);
             for (; item < end; ++item) {
                 const int k0 = block_key(x, item - x.g0) + pg * 16;
-                // pages that hold no key which the tile sees are not read
-                const int rows = x.m.qn * p.group;
-                const bool need = page_needed(p, x.m, x.v, x.tile * R, min(x.tile * R + R, rows), k0);
+                // pages that hold no key which some row sees are not read
+                const bool need = page_needed(p, x.m, x.v, 0, x.rows, k0);
                 int id = need ? __ldg(bt + k0 / 16) : -1;
                 const bool bad = need && (id < 0 || (int64_t)id >= p.num_blocks);
                 if (bad)
@@ -262,14 +254,14 @@ __global__ void __launch_bounds__(kRowsThreads, RowsCfg<DH, MT>::kCtas)
     for (int item = lo; item < hi;) {
         const Group x = group_of(item);
         const int end = min(hi, x.g1);
-        const int rows = min(R, x.m.qn * p.group - x.tile * R);
+        const int rows = x.rows;
         named_sync(1, kRowsWarps * 32);  // Q and the sums of the group before have been read
-        // Q into shared memory; rows past the tile's are zero
+        // Q into shared memory; rows past the request's are zero
         for (int i = tid; i < R * (DH / 8); i += kRowsWarps * 32) {
             const int r = i / (DH / 8), ch = i % (DH / 8);
             uint4 v = make_uint4(0u, 0u, 0u, 0u);
             if (r < rows) {
-                const int row = x.tile * R + r, tok = row / p.group, h = x.kvh * p.group + row - tok * p.group;
+                const int tok = r / p.group, h = x.kvh * p.group + r - tok * p.group;
                 v = __ldg(reinterpret_cast<const uint4 *>(p.q + ((int64_t)x.m.qs + tok) * p.q_tok_stride + (int64_t)h * DH) + ch);
             }
             *reinterpret_cast<uint4 *>(s_q + r * DH * 2 + (ch ^ (r & 7)) * 16) = v;
@@ -280,17 +272,17 @@ __global__ void __launch_bounds__(kRowsThreads, RowsCfg<DH, MT>::kCtas)
         int lo_max = 0, pos_min = INT32_MAX;
 #pragma unroll
         for (int i = 0; i < 2 * MT; ++i) {
-            const int r = 8 * i + g8, row = x.tile * R + r;
+            const int r = 8 * i + g8;
             r_lo[i] = r_len[i] = r_near[i] = r_pos[i] = 0;
             slope[i] = 0.f;
             if (r < rows) {
-                const int tok = row / p.group, pos = x.m.L - x.m.qn + tok;
+                const int tok = r / p.group, pos = x.m.L - x.m.qn + tok;
                 r_pos[i] = pos;
                 r_lo[i] = score_low(p, (int64_t)x.m.qs + tok, pos);
                 r_len[i] = pos - r_lo[i] + 1;
                 r_near[i] = score_nearest(r_lo[i], pos, x.v.prefix);
                 if (p.slopes)
-                    slope[i] = __ldg(p.slopes + x.kvh * p.group + row - tok * p.group) * kLog2e;
+                    slope[i] = __ldg(p.slopes + x.kvh * p.group + r - tok * p.group) * kLog2e;
                 lo_max = max(lo_max, r_lo[i]);
                 pos_min = min(pos_min, pos);
             }
@@ -417,7 +409,7 @@ __global__ void __launch_bounds__(kRowsThreads, RowsCfg<DH, MT>::kCtas)
                             o[i][j][e] *= alpha[2 * i + e / 2];
             }
             named_sync(1, kRowsWarps * 32);
-            // output: V rows that no row of the tile sees become zeros (they may
+            // output: V rows that no row sees become zeros (they may
             // hold anything, and 0 * NaN is NaN)
             const bool whole = (k0 >= x.v.lo && k0 + KB <= x.v.hi) || k0 + KB <= x.v.prefix;
 #pragma unroll
@@ -488,7 +480,7 @@ __global__ void __launch_bounds__(kRowsThreads, RowsCfg<DH, MT>::kCtas)
 }
 
 // Folds a row's records: a CTA per (group, row).  A row whose result is not
-// finite is computed again key by key: a key that only other rows of its tile
+// finite is computed again key by key: a key that only other rows of the request
 // see may have met a zero probability with an infinity or a NaN.
 constexpr int kFoldThreads = 256;
 constexpr int kFoldWarps = kFoldThreads / 32;
@@ -501,7 +493,7 @@ __global__ void __launch_bounds__(kFoldThreads) scored_fold_kernel(const ScorePa
     __shared__ float s_ml[2][kFoldWarps];
     const int g = blockIdx.x / w.rows, r = blockIdx.x - g * w.rows;
     const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
-    const int st = g / p.hkv, kvh = g - st * p.hkv, b = st / w.qtiles, tile = st - b * w.qtiles;
+    const int b = g / p.hkv, kvh = g - b * p.hkv;
     // (the caller's inputs were there before the first kernel read them)
     const ReqMeta m = score_meta(p, b);
     griddep_wait();
@@ -509,7 +501,7 @@ __global__ void __launch_bounds__(kFoldThreads) scored_fold_kernel(const ScorePa
     const int2 parts = w.groups[g];
     if (!m.ok) {
         // every row of the request, whatever its number: the grid goes by the bounds
-        if (m.sane && tile == 0 && kvh == 0 && r == 0) {
+        if (m.sane && kvh == 0 && r == 0) {
             const int64_t first = (int64_t)m.qs * p.hq, n = (int64_t)m.qn * p.hq;
             for (int64_t i = tid; i < n * DH; i += kFoldThreads)
                 p.out[first * DH + i] = __ushort_as_bfloat16(0x7FC0);
@@ -519,7 +511,7 @@ __global__ void __launch_bounds__(kFoldThreads) scored_fold_kernel(const ScorePa
         }
         return;
     }
-    const int row = tile * tile_rows + r, tok = row / p.group, h = kvh * p.group + row - tok * p.group;
+    const int tok = r / p.group, h = kvh * p.group + r - tok * p.group;
     if (tok >= m.qn)
         return;
     // a warp takes every eighth part
@@ -589,20 +581,13 @@ __global__ void __launch_bounds__(kFoldThreads) scored_fold_kernel(const ScorePa
 // --------------------------------------------------------------------- host --
 static int rows_of(int32_t max_query_len, int group) { return max_query_len * group <= 16 ? 16 : 32; }
 
-static int64_t rows_tiles(int32_t max_query_len, int group)
-{
-    const int r = rows_of(max_query_len, group);
-    return ((int64_t)max_query_len * group + r - 1) / r;
-}
-
 static int rows_keys(int dh) { return dh == 128 ? 64 : 32; }
 
-bool scored_rows_fits(int32_t num_seqs, int32_t hkv, int group, int32_t head_dim, int32_t max_query_len,
-                      int32_t max_seq_len)
+bool scored_rows_fits(int32_t num_seqs, int32_t hkv, int32_t head_dim, int32_t max_seq_len)
 {
-    const int64_t tiles = (int64_t)num_seqs * rows_tiles(max_query_len, group);
-    return tiles <= kScoredMaxTilesHost && tiles * hkv * 32 <= INT32_MAX &&
-           tiles * hkv * (((int64_t)max_seq_len + rows_keys(head_dim) - 1) / rows_keys(head_dim) + 1) <= INT32_MAX;
+    const int64_t groups = (int64_t)num_seqs * hkv;
+    return groups * 32 <= INT32_MAX &&
+           groups * (((int64_t)max_seq_len + rows_keys(head_dim) - 1) / rows_keys(head_dim) + 1) <= INT32_MAX;
 }
 
 static size_t align256(size_t n) { return (n + 255) / 256 * 256; }
@@ -618,7 +603,7 @@ static int rows_ctas(int64_t groups, int head_dim, int32_t max_seq_len)
 size_t scored_rows_bytes(int32_t num_seqs, int32_t hkv, int group, int32_t head_dim, int32_t max_query_len,
                          int32_t max_seq_len)
 {
-    const int64_t groups = num_seqs * rows_tiles(max_query_len, group) * hkv;
+    const int64_t groups = (int64_t)num_seqs * hkv;
     const int r = rows_of(max_query_len, group);
     return align256((size_t)groups * 8) +
            (size_t)(2 * rows_ctas(groups, head_dim, max_seq_len) + groups) * r * (head_dim + 2) * 4;
@@ -631,7 +616,7 @@ static cudaError_t launch_rows(const ScoreParams &p, const CUtensorMap &k, const
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)w.ctas);
     cfg.blockDim = dim3(kRowsThreads);
-    cfg.dynamicSmemBytes = rows_smem<DH, MT>(p.num_seqs * w.qtiles);
+    cfg.dynamicSmemBytes = rows_smem<DH, MT>(p.num_seqs);
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -655,15 +640,14 @@ cudaError_t launch_scored_rows(const ScoreParams &p, int32_t head_dim, void *wor
         return cudaErrorInvalidValue;
     RowsWork w{};
     const int r = rows_of(p.max_query_len, p.group);
-    w.qtiles = (int32_t)rows_tiles(p.max_query_len, p.group);
-    const int64_t groups = (int64_t)p.num_seqs * w.qtiles * p.hkv;
+    const int64_t groups = (int64_t)p.num_seqs * p.hkv;
     w.ctas = rows_ctas(groups, head_dim, p.max_seq_len);
-    w.rows = (int32_t)((int64_t)p.max_query_len * p.group < r ? p.max_query_len * p.group : r);
+    w.rows = p.max_query_len * p.group;
     uint8_t *ws = static_cast<uint8_t *>(workspace);
     w.groups = reinterpret_cast<int2 *>(ws);
     w.records = reinterpret_cast<float *>(ws + align256((size_t)groups * 8));
     w.record_floats = (int64_t)r * (head_dim + 2);
-    snprintf(info, info_len, "scored attention dh=%d kernel=rows-r%d grid=%d tiles=%d", head_dim, r, w.ctas, w.qtiles);
+    snprintf(info, info_len, "scored attention dh=%d kernel=rows-r%d grid=%d", head_dim, r, w.ctas);
     const bool two = r == 32;
     switch (head_dim) {
     case 128: return two ? launch_rows<128, 2>(p, tm[0], tm[1], w, groups, stream) : launch_rows<128, 1>(p, tm[0], tm[1], w, groups, stream);
@@ -676,7 +660,7 @@ template <int DH, int MT>
 static cudaError_t rows_attribute()
 {
     return cudaFuncSetAttribute(scored_rows_kernel<DH, MT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                (int)rows_smem<DH, MT>(kScoredMaxTilesHost));
+                                (int)rows_smem<DH, MT>(kScanMaxSeqs));
 }
 
 cudaError_t init_scored_rows_attributes()

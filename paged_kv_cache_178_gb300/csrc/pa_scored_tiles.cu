@@ -25,8 +25,6 @@ int64_t scored_tiles_bound(int32_t num_seqs, int group, int32_t head_dim, int32_
 {
     const int rows = 128 * row_tiles(group, head_dim, max_query_len);
     const int64_t by_len = num_seqs * (((int64_t)max_query_len * group + rows - 1) / rows);
-    if (num_q_tokens < 0)
-        return by_len;
     const int64_t by_tokens = num_q_tokens * group / rows + num_seqs;
     return by_len < by_tokens ? by_len : by_tokens;
 }
