@@ -79,18 +79,6 @@ __device__ __forceinline__ TileView tile_view(const ScoreParams &p, int b, const
     return v;
 }
 
-// Whether one of n tokens (the first of them token t0 of all, at position pos0)
-// sees a key of the page at k0 in its range.
-static __device__ __noinline__ bool page_in_ranges(const ScoreParams &p, int64_t t0, int pos0, int n, int k0)
-{
-    for (int i = max(k0 - pos0, 0); i < n; ++i) {
-        const int lo = score_low(p, t0 + i, pos0 + i);
-        if (lo <= pos0 + i && lo < k0 + 16)
-            return true;
-    }
-    return false;
-}
-
 // Whether rows [r0, r1) of a request see a key of the page at k0 (v: their view).
 __device__ __forceinline__ bool page_needed(const ScoreParams &p, const ReqMeta &m, const TileView &v, int r0, int r1, int k0)
 {
@@ -100,8 +88,14 @@ __device__ __forceinline__ bool page_needed(const ScoreParams &p, const ReqMeta 
         return false;
     if (!v.gaps)
         return true;
-    const int t0 = r0 / p.group;
-    return page_in_ranges(p, (int64_t)m.qs + t0, m.L - m.qn + t0, (r1 - 1) / p.group - t0 + 1, k0);
+    const int base = m.L - m.qn, t1 = (r1 - 1) / p.group;
+    bool seen = false;
+#pragma unroll 1
+    for (int t = max(r0 / p.group, k0 - base); t <= t1 && !seen; ++t) {
+        const int lo = score_low(p, (int64_t)m.qs + t, base + t);
+        seen = lo <= base + t && lo < k0 + 16;
+    }
+    return seen;
 }
 
 // Blocks of `keys` keys that hold what a tile sees: the prefix's np first ones,

@@ -113,7 +113,9 @@ __device__ __forceinline__ int group_tiles(const ScoreParams &p, const ReqMeta &
     return m.ok ? (int)(((int64_t)m.qn * p.group + rows - 1) / rows) : 0;
 }
 
-// tile_view of rows [r0, r1) by a whole warp.
+// tile_view of rows [r0, r1) by a whole warp (without `gaps`: where the range has some,
+// pages in them are copied if their ids are good, and hidden like any other key; with
+// their pages left out the copying warp's longer loop took the prompts one percent).
 __device__ __forceinline__ TileView warp_tile_view(const ScoreParams &p, int b, const ReqMeta &m, int r0, int r1)
 {
     TileView v{0, 0, 0, false};
@@ -126,19 +128,16 @@ __device__ __forceinline__ TileView warp_tile_view(const ScoreParams &p, int b, 
         v.hi = base + t1 + 1;
         return v;
     }
-    int lo = INT32_MAX, hi = 0, from = INT32_MAX, seeing = 0;
+    int lo = INT32_MAX, hi = 0;
     for (int t = t0 + (int)(threadIdx.x % 32); t <= t1; t += 32) {
         const int pos = base + t, l = score_low(p, (int64_t)m.qs + t, pos);
         if (l <= pos) {
             lo = min(lo, l);
             hi = pos + 1;
-            from = min(from, pos);
-            ++seeing;
         }
     }
     v.lo = __reduce_min_sync(0xffffffffu, lo);
     v.hi = __reduce_max_sync(0xffffffffu, hi);
-    v.gaps = (int)__reduce_add_sync(0xffffffffu, seeing) < v.hi - __reduce_min_sync(0xffffffffu, from);
     return v;
 }
 
@@ -228,7 +227,8 @@ __device__ __forceinline__ uint32_t bits_below(int n) { return n <= 0 ? 0u : (n 
 // not finite though their sum is: computed again key by key, over exactly their own
 // keys (one that only other rows of the tile see may have met a zero probability
 // with an infinity or a NaN).  By all warps once the CTA's other work is done: a row
-// takes 0.3 us and more for each key, and no wait of another warp may last so long.
+// takes 0.6 to 1 us for each key, and no wait of another warp may last so long. (One
+// infinite value that all 4096 tokens of a prompt see makes its 60 us 110 ms.)
 template <int DH, int NT>
 __device__ __noinline__ void repair_groups(const ScoreParams &p, int b, int tile, int first, int lo, int hi)
 {
@@ -426,15 +426,9 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         // -------------------------------------------------------- producer --
         uint32_t pos = 0;  // units so far
         const int pg = lane % 8, cb = (lane / 8) % 2;
-        struct Page {
-            int id;
-            bool needed;
-        };
-        // (pages that hold no key which the group sees are not read)
-        auto page_of = [&](int j) {
-            const int k0 = tile_key(x.t, j) + pg * 16, rows = x.m.qn * p.group;
-            const bool needed = page_needed(p, x.m, x.v, x.tile * RT, min(x.tile * RT + RT, rows), k0);
-            return Page{needed ? __ldg(p.block_tables + (int64_t)x.b * p.max_blocks + k0 / 16) : -1, needed};
+        auto ids_of = [&](int j) {
+            const int k0 = tile_key(x.t, j) + pg * 16;
+            return page_seen(x.v, k0) ? __ldg(p.block_tables + (int64_t)x.b * p.max_blocks + k0 / 16) : -1;
         };
         auto load = [&](const CUtensorMap *map, int units, int col0, int id) {
             for (int u = 0; ok && u < units; ++u, ++pos) {
@@ -465,25 +459,23 @@ __global__ void __launch_bounds__(kTileThreads, 1)
             static_assert(NS <= 8, "flags of bad pages");
             if (lane == 0)
                 s_flags[8 + seg % 8] = 0;
-            auto check = [&](const Page &page) {
-                const bool bad = page.needed && (page.id < 0 || (int64_t)page.id >= p.num_blocks);
+            auto check = [&](int raw, int j) {
+                // (whether some row sees a key of the page is looked up at the segment's end)
+                const bool bad = page_seen(x.v, tile_key(x.t, j) + pg * 16) && (raw < 0 || (int64_t)raw >= p.num_blocks);
                 if (__any_sync(0xffffffffu, bad)) {
-                    if (lane == 0) {
-                        record_error(p.err, kErrBadMetadata, x.b);
+                    if (lane == 0)
                         s_flags[8 + seg % 8] = 1;
-                    }
                     __syncwarp();
                 }
-                return bad ? -1 : page.id;
+                return bad ? -1 : raw;
             };
-            int cur = check(page_of(j0));
-            Page ahead = n > 1 ? page_of(j0 + 1) : Page{-1, false};
+            int cur = check(ids_of(j0), j0), ahead = n > 1 ? ids_of(j0 + 1) : -1;
             load(&tm_k, UK, 0, cur);
             for (int j = 0; ok && j < n; ++j) {
                 const int id = cur;
                 if (j + 1 < n) {
-                    cur = check(ahead);
-                    ahead = j + 2 < n ? page_of(j0 + j + 2) : Page{-1, false};
+                    cur = check(ahead, j0 + j + 1);
+                    ahead = j + 2 < n ? ids_of(j0 + j + 2) : -1;
                 }
                 if (NT == 2)
                     load(&tm_v, UV, v_col, id);
@@ -930,7 +922,8 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                 named_sync(1, 256);
                 l = s_l[r] + s_l[128 + r];
             }
-            // rows that see a key of a bad page (its keys and values came as zeros) are NaN
+            // rows that see a key of a bad page (its keys and values came as zeros) are NaN;
+            // a bad id whose keys no row sees does not matter
             if (ok && s_flags[8 + seg % 8]) {
                 bool bad = false;
                 for (int i = 0; valid && i < n * (kTileKeys / 16); ++i) {
@@ -940,7 +933,10 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                         bad |= id < 0 || (int64_t)id >= p.num_blocks;
                     }
                 }
-                l = bad ? __int_as_float(0x7FC00000) : l;
+                if (bad) {
+                    record_error(p.err, kErrBadMetadata, x.b);
+                    l = __int_as_float(0x7FC00000);
+                }
             }
             // (after a wait that ran out a part's sum is NaN, and so are whole rows)
             if (!ok)
