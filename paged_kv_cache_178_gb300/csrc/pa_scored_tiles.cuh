@@ -921,6 +921,8 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                 s_l[wg * 128 + r] = l;
                 named_sync(1, 256);
                 l = s_l[r] + s_l[128 + r];
+                // (a wait that ran out in the other group leaves the row without its tiles)
+                ok = __all_sync(0xffffffffu, ok && !*abort_flag);
             }
             // rows that see a key of a bad page (its keys and values came as zeros) are NaN;
             // a bad id whose keys no row sees does not matter
