@@ -249,6 +249,9 @@ __global__ void __launch_bounds__(kRowsThreads, RowsCfg<DH, MT>::kCtas)
 
     // ------------------------------------------------------------- compute --
     const int g8 = lane / 4, t4 = lane % 4;
+    // (a wide cap has a pass of its own, and leaves nothing to do here)
+    const bool wide = p.cap_log2 > kCapNarrow;
+    const float c1 = wide ? 1.f : p.scale_log2, cap = wide ? 0.f : p.cap_log2;
     int stage = 0, parity = 0;
     bool ok = true;
     for (int item = lo; item < hi;) {
@@ -336,21 +339,15 @@ __global__ void __launch_bounds__(kRowsThreads, RowsCfg<DH, MT>::kCtas)
                 }
             }
             // scores in log2 units, what is hidden at -inf; their row maxima
-            auto each_score = [&](auto f) {
+            if (wide) {
 #pragma unroll
                 for (int i = 0; i < MT; ++i)
 #pragma unroll
                     for (int j = 0; j < NT; ++j)
 #pragma unroll
                         for (int e = 0; e < 4; ++e)
-                            s[i][j][e] = f(s[i][j][e]);
-            };
-            if (p.cap_log2 > kCapNarrow)
-                each_score([&](float z) { return capped_wide(z, p.scale_log2, p.cap_log2); });
-            else if (p.cap_log2 > 0.f)
-                each_score([&](float z) { return capped(z, p.scale_log2, p.cap_log2); });
-            else
-                each_score([&](float z) { return z * p.scale_log2; });
+                            s[i][j][e] = capped_wide(s[i][j][e], p.scale_log2, p.cap_log2);
+            }
             const bool all = (k0 >= lo_max && k0 + KB - 1 <= pos_min) || k0 + KB <= x.v.prefix;
             float mx[2 * MT];
 #pragma unroll
@@ -362,6 +359,7 @@ __global__ void __launch_bounds__(kRowsThreads, RowsCfg<DH, MT>::kCtas)
                     for (int e = 0; e < 2; ++e) {
                         float &z = s[i / 2][j][(i % 2) * 2 + e];
                         const int key = k0 + warp * KW + j * 8 + t4 * 2 + e;
+                        z = cap > 0.f ? capped(z, c1, cap) : z * c1;
                         if (p.slopes)
                             z -= slope[i] * (float)(abs(r_pos[i] - key) - r_near[i]);
                         if (bad_pages && (bad_pages >> ((key - k0) / 16) & 1u))

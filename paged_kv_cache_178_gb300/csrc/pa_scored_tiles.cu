@@ -92,9 +92,10 @@ cudaError_t launch_scored_tiles(const ScoreParams &p, int32_t head_dim, void *wo
     // Without a maximum the exponents stay within the cap: 2^80 times any number
     // of keys and values up to 2^20 is far from overflow (and a row that overflows
     // all the same is computed again key by key).
-    const int mode = p.slopes                              ? kModeAny
-                     : p.cap_log2 > 0.f                    ? (p.cap_log2 <= kCapNarrow ? kModeCapped : kModeAny)
-                                                           : kModePlain;
+    const int mode = p.cap_log2 > kCapNarrow          ? kModeWide
+                     : p.slopes                       ? kModeAny
+                     : p.cap_log2 > 0.f               ? kModeCapped
+                                                      : kModePlain;
     snprintf(info, info_len, "scored attention dh=%d kernel=tiles-m%d mode=%d grid=%d tiles=%lld", head_dim, 128 * s.nt, mode,
              w.ctas, (long long)tiles);
     switch (head_dim) {

@@ -61,7 +61,8 @@ constexpr int kGroupSetup = NT == 2 ? 2 : 1;
 enum ScoreMode : int {
     kModePlain = 0,   // scaled
     kModeCapped = 1,  // capped, and the cap small enough to need no running maximum
-    kModeAny = 2,     // capped or not, with a bias
+    kModeAny = 2,     // with a bias, capped or not; the cap at most kCapNarrow
+    kModeWide = 3,    // with or without a bias; the cap above that
 };
 
 template <int DH, int NT>
@@ -783,8 +784,8 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                         for_chunks(scol, [&](uint32_t(&v)[32], int ch) {
                             const uint32_t keep = all ? ~0u : seen(ch);
                             const bool some = all || __any_sync(0xffffffffu, keep != 0u);
-                            if (MODE == kModeAny && some) {
-                                if (cap > kCapNarrow)
+                            if (MODE != kModePlain && some) {
+                                if constexpr (MODE == kModeWide)
 #pragma unroll
                                     for (int k = 0; k < 32; ++k)
                                         v[k] = __float_as_uint(capped_wide(__uint_as_float(v[k]), c1, cap));
@@ -814,7 +815,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                                 for (int k = 0; k < 32; ++k)
                                     v[k] = keep & (1u << k) ? v[k] : 0xff800000u;
                             }
-                            if (MODE == kModeAny || !all)
+                            if (MODE != kModePlain || !all)
                                 tmem_st32(scol + ch * 32, v);
 #pragma unroll
                             for (int k = 0; k < 32; k += 4) {
@@ -1148,7 +1149,8 @@ cudaError_t launch_tiles(const ScoreParams &p, const CUtensorMap (&tm)[3], const
     cfg.numAttrs = 1;
     auto kern = mode == kModePlain    ? scored_tiles_kernel<DH, NT, kModePlain>
                 : mode == kModeCapped ? scored_tiles_kernel<DH, NT, kModeCapped>
-                                      : scored_tiles_kernel<DH, NT, kModeAny>;
+                : mode == kModeAny    ? scored_tiles_kernel<DH, NT, kModeAny>
+                                      : scored_tiles_kernel<DH, NT, kModeWide>;
     const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, p, tm[0], tm[1], tm[2], w);
     if (e != cudaSuccess)
         return e;
@@ -1168,6 +1170,8 @@ cudaError_t tiles_attributes()
         e = cudaFuncSetAttribute(scored_tiles_kernel<DH, NT, kModeCapped>, attr, (int)tiles_smem<DH, NT>());
     if (e == cudaSuccess)
         e = cudaFuncSetAttribute(scored_tiles_kernel<DH, NT, kModeAny>, attr, (int)tiles_smem<DH, NT>());
+    if (e == cudaSuccess)
+        e = cudaFuncSetAttribute(scored_tiles_kernel<DH, NT, kModeWide>, attr, (int)tiles_smem<DH, NT>());
     return e;
 }
 
