@@ -734,13 +734,21 @@ PA_API size_t pa_paged_attention_scored_workspace_size(int32_t num_seqs, int32_t
  * Arguments, ownership and errors as for pa_paged_attention; kv_tile is
  * ignored.  Differences:
  *   - Keys that a token does not see never matter to it, whatever their bytes
- *     (NaN included); a page that no token of the request sees a key of is
- *     never read, and its table entry may be anything (pages that a window has
- *     left behind may be released).  A bad id of another page makes the rows that
+ *     (NaN included), and the table entry of a page that no token of the request
+ *     sees a key of may be anything.  A bad id of another page makes the rows that
  *     see a key of it NaN and latches PA_ERR_BAD_METADATA (index = the request).
+ *   - Pages that a window has left behind are needed by this call no more.  The
+ *     calls above know nothing of it: pa_release_pages gives up a request's last
+ *     pages only, and a fork, a release or a compaction takes every entry up to the
+ *     request's length for a page that the request owns.
  *   - Sums, maxima and lse are fp32, the probabilities BF16.  A call's results
  *     are bitwise reproducible; other bounds, or the token in another call, may
  *     round differently (the fixed schedule of pa_paged_attention is not kept).
+ *     The cap costs a score about 2^-21 of the cap, above a cap of 55 2^-19 of the score.
+ *   - Where a value (V) of a key that rows compute together is infinite or NaN, the
+ *     rows whose result that makes not finite are computed again, each over its own
+ *     keys: right, but slow (0.6 to 1 us for each key of a row) and rounded
+ *     differently.
  *   - workspace: pa_paged_attention_scored_workspace_size(...) bytes, 256-byte
  *     aligned, any contents; calls with different bounds may share it one after
  *     another.

@@ -14,7 +14,9 @@ namespace pa {
 
 // ------------------------------------------------------------ page copies --
 // Bytes in, bytes out: bound by the memory (2000 pages of 8 heads of 128 in two
-// layers: 78.9 us, 6.64 TB/s; 16 pages in four layers: 2.8 us).  A warp takes 4 KB of one view
+// layers: 78.9 us, 6.65 TB/s; 16 pages in four layers: 2.8 us; in 4 bits 2000 pages
+// of 8 heads in two layers 24.0 us, 6.1 TB/s, 8000 of one head in four 28.7: a
+// view's page is then 72 vectors, of which a warp could take 256).  A warp takes 4 KB of one view
 // (K or V) of one page at a time, eight 16-byte vectors a lane, all loaded
 // before the first is stored.
 constexpr int kCopyThreads = 256;
@@ -94,8 +96,8 @@ cudaError_t launch_copy_pages(const CopyArgs &a, ErrState *err, cudaStream_t str
 // does with scattered words (an atomic takes it 3 cycles, a load 1.5).  16
 // instead of 8 took 192 forks of 36 k pages from 14.4 to 11.0 us, a release of 35
 // k references from 27.4 to 21.6 and a pool of 300000 pages from 34.0 to 24.3.
-// Measured: those calls 9.3, 20.6 and 19.3 us; 4 forks of a prompt 4.5 us, the
-// drafts of 64 requests 9.9, a pool of 2048 pages 7.8: chains of loads, sums and
+// Measured: those calls 9.2, 17.6 and 19.7 us; 4 forks of a prompt 4.3 us, the
+// drafts of 64 requests 9.4, a pool of 2048 pages 7.5: chains of loads, sums and
 // barriers, of some 2 us for a launch.
 constexpr int kPageThreads = 1024;
 constexpr int kPageWarps = kPageThreads / 32;
@@ -250,7 +252,7 @@ cudaError_t launch_fork_requests(const PageArgs &a, ErrState *err, cudaStream_t 
 // dropped references gives each page its place on the free stack.  So the
 // result is the one of a loop over requests and columns, without one.  A lane
 // takes kPageBatch references through each phase at a time (their atomics return
-// values: 30.1 -> 21.6 us for 35 k references).
+// values: 30.1 -> 21.6 us for 35 k references; a warp to sum one CTA's counts, 18.8).
 constexpr int kReleaseMark = 1 << 30;
 
 __global__ void __launch_bounds__(kPageThreads, 1) release_pages_kernel(const PageArgs a, ErrState *err)

@@ -17,10 +17,12 @@
 // maxima and probabilities cross through shared memory (two barriers a block).
 //
 // Measured, heads of 8 and 2 by 128: a token of each of 64 requests, 312 MB of K
-// and V, capped: 54 us, 5.8 TB/s (a plain copy: 6.8); of 4 requests behind a
+// and V, capped: 56 us, 5.6 TB/s (a plain copy: 6.8); 4 and 8 tokens of each (16 and
+// 32 rows) 61 and 84 us: two m16 tiles a block and three special-function operations a
+// score are then more than the bytes; of 4 requests behind a
 // window of 1024, 3.7 MB: 8.7 us, two launches and the chain of lengths, table,
-// copy, products and fold.  With 64-bit divisions in the ranges of items these took
-// 59 and 15.9 us.
+// copy, products and fold.  With 64-bit divisions in the ranges of items the first
+// and last took 59 and 15.9 us.
 #include <cstdio>
 
 #include "pa_scan.cuh"

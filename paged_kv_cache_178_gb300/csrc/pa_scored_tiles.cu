@@ -91,7 +91,8 @@ cudaError_t launch_scored_tiles(const ScoreParams &p, int32_t head_dim, void *wo
     w.max_tiles = (int32_t)tiles;
     // Without a maximum the exponents stay within the cap: 2^80 times any number
     // of keys and values up to 2^20 is far from overflow (and a row that overflows
-    // all the same is computed again key by key).
+    // all the same is computed again key by key).  Where all scores lie at the negative
+    // cap, values below 2^-46 lose bits: their products pass fp32's smallest normal.
     const int mode = p.cap_log2 > kCapNarrow          ? kModeWide
                      : p.slopes                       ? kModeAny
                      : p.cap_log2 > 0.f               ? kModeCapped

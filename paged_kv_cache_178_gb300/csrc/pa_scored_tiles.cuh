@@ -28,16 +28,21 @@
 // (tensor memory holds 256 columns of output beside the scores): three halves of
 // the products of a whole one instead of two, and no exchange.
 //
-// Measured: a prompt of 4096 tokens, 8 query and 2 KV heads of 128, capped: 60
-// us, 0.57 PFLOP/s of the products that causality leaves; a prompt of 8192 tokens
+// Measured: a prompt of 4096 tokens, 8 query and 2 KV heads of 128, capped: 62.5
+// us, 0.55 PFLOP/s of the products that causality leaves (plain 56, with a window of
+// 1024 40, with a bias 74, with both cap and bias 95; 80 with scores that are mostly
+// above 3/8 of the cap, which then cost two exponentials and a reciprocal instead of
+// one exponential: spread 4 under a cap of 30 instead of 50); at head dim 256 and 512
+// (one KV head) 110 and 279; a prompt of 8192 tokens
 // of five documents behind a prefix, 16 and 2 heads of 256, a bias by distance:
 // 274 us, 0.55 PFLOP/s of those that the documents leave.  What bounds it is the
 // chain of a step (scores, softmax, products), not the tensor pipe: a pair of
 // 128-key tiles takes 4.9 k cycles at head dim 128, its products 2.1 k, a tile's
 // softmax 2.0 to 2.4 k (of them 1.4 k issue slots where it is capped); at head dim
 // 256 a tile takes 6.4 k, of which the issuing thread waits 2.3 k for K and V (128
-// KB from L2, 6 TB/s over the GPU) and its products take 3.1 k.  Starting a CTA and its first scores take 15 k more, 12
-// percent of the prompt's time.  Slower when tried: two issuing threads (69 us),
+// KB from L2, 6 TB/s over the GPU) and its products take 3.1 k.  Starting a CTA and
+// its first scores take 15 k more, 12 percent of the prompt's time.  Slower when
+// tried, against 61 us for the capped prompt then: two issuing threads (69 us),
 // 16 softmax warps (74), tiles of 64 keys (79), probabilities in shared memory so
 // that the next scores need not wait for the products (69: each product then
 // reads both operands there, 950 cycles instead of 800).
