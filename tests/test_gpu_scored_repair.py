@@ -103,3 +103,56 @@ def test_rows_that_take_seconds_latch_nothing():
         err = (out[b].double() - clean).abs()
         err[..., 9] = 0
         assert bool((err <= 2.0**-6).all())
+
+
+SHAPES = {"few": ([700, 33, 1, 260], [1, 1, 1, 1], 8, 2, 128), "many": ([300, 513, 40], [300, 200, 40], 8, 2, 128),
+          "wide": ([600, 70], [600, 3], 4, 1, 512), "one_tile": ([400] * 40, [9] * 40, 6, 1, 256)}
+
+
+@pytest.mark.parametrize("pinned", [False, True])
+@pytest.mark.parametrize("shape", list(SHAPES))
+def test_a_captured_call_with_and_without_the_cause(shape, pinned):
+    """Replays see an infinity, a bad page, nothing, in turn: each gives what a call by
+    itself gives, and nothing of the one before stays."""
+    lens, new, *heads = SHAPES[shape]
+    a = _batch(lens, new, *heads, seed=4)
+    T, hq, dh = a["q"].shape
+    out, lse = torch.empty(T, hq, dh, dtype=torch.bfloat16), torch.empty(T, hq)
+    out, lse = (t.pin_memory() if pinned else t.cuda() for t in (out, lse))
+    ws = pa.new_scored_workspace(len(lens), hq, heads[1], dh, a["max_query_len"], a["max_seq_len"])
+    pa.init()
+    st = torch.cuda.Stream()
+    st.wait_stream(torch.cuda.current_stream())
+    call = pa.prepare_paged_attention_scored(**a, out=out, lse=lse, workspace=ws, soft_cap=20.0, window=100, stream=st)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, stream=st):
+        call()
+    j = lens[0] - new[0] // 2 - 1
+    value, entry = a["v_cache"][int(a["block_tables"][0, j // 16]), j % 16], a["block_tables"][0, j // 16]
+    sound, page = value.clone(), entry.clone()
+    for cause in ("none", "value", "page", "none", "page", "value"):
+        value.copy_(sound)
+        entry.copy_(page)
+        if cause == "value":
+            value[..., 3] = math.inf
+        if cause == "page":
+            entry.fill_(-5)
+        g.replay()
+        torch.cuda.synchronize()
+        status = pa.check_errors()
+        want = pa.paged_attention_scored(**a, soft_cap=20.0, window=100)
+        assert status == pa.check_errors() == ((pa.PA_ERR_BAD_METADATA, 0) if cause == "page" else (0, -1))
+        assert torch.equal(out.cuda().view(torch.int16), want[0].view(torch.int16))
+        assert torch.equal(lse.cuda().view(torch.int32), want[1].view(torch.int32))
+        assert bool(want[0].isfinite().all()) == (cause == "none")
+
+
+@pytest.mark.parametrize("shape", list(SHAPES))
+def test_without_lse(shape):
+    lens, new, *heads = SHAPES[shape]
+    a = _batch(lens, new, *heads, seed=5)
+    j = lens[0] - new[0] // 2 - 1
+    a["v_cache"][int(a["block_tables"][0, j // 16]), j % 16, :, 3] = math.inf
+    want, _ = pa.paged_attention_scored(**a)
+    out, lse = pa.paged_attention_scored(**a, want_lse=False)
+    assert lse is None and torch.equal(out, want) and not bool(out.isfinite().all())
