@@ -80,7 +80,8 @@ __device__ __forceinline__ TileView tile_view(const ScoreParams &p, int b, const
 }
 
 // Whether rows [r0, r1) of a request see a key of the page at k0 (v: their view).
-__device__ __forceinline__ bool page_needed(const ScoreParams &p, const ReqMeta &m, const TileView &v, int r0, int r1, int k0)
+__device__ __forceinline__ bool page_needed(const ScoreParams &p, const ReqMeta &m, const TileView &v, int r0, int r1,
+                                            int k0)
 {
     if (k0 < v.prefix)
         return true;

@@ -290,7 +290,8 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     uint8_t *s_out = s_ring + NS * kUnitBytes; // [8 warps][32 rows][128 bytes]
     uint8_t *small = s_out + C::kOutBytes;
     uint64_t *bars = reinterpret_cast<uint64_t *>(small);
-    volatile int *s_flags = reinterpret_cast<volatile int *>(small + 256);  // [0] abort [1] tmem [2] odd rows [4..7) start [8..16) bad pages in a segment
+    // [0] abort [1] tmem [2] odd rows [4..7) start [8..16) bad pages in a segment
+    volatile int *s_flags = reinterpret_cast<volatile int *>(small + 256);
     float *s_m = reinterpret_cast<float *>(small + 512);                    // [128] the shared running maximum
     float *s_l = s_m + 128;                                                 // [2][128] the two halves' sums
     volatile int *abort_flag = s_flags;
@@ -1045,9 +1046,9 @@ __global__ void __launch_bounds__(kTileThreads, 1)
 }
 
 // Folds the records of the groups that several CTAs have a part of, each at the
-// place of the CTA that it begins in: two threads per row, each with every second part, and 32 columns of the output a CTA.  (A
-// few rows over many keys are a part to a CTA: one thread per row, part by
-// part, took 27 of 42 us for 64 rows over 4096 keys.)
+// place of the CTA that it begins in: two threads per row, each with every second
+// part, and 32 columns of the output a CTA.  (A few rows over many keys are a part to
+// a CTA: one thread per row, part by part, took 27 of 42 us for 64 rows over 4096 keys.)
 constexpr int kTileFoldThreads = 256;
 
 template <int DH, int NT>
