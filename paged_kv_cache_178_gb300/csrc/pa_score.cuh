@@ -144,6 +144,9 @@ __device__ __noinline__ void scored_row(const ScoreParams &p, int b, const ReqMe
         q[e] = __bfloat162float(qr[e * 32 + lane]);
         o[e] = 0.f;
     }
+    // Sums of 2^-32 of the values: up to 2^31 of the largest stay below infinity, and
+    // what that costs those below 2^-94 is less than 2^-116.
+    constexpr float kDown = 0x1p-32f, kUp = 0x1p32f;
     float mx = -INFINITY, l = 0.f;
     bool bad = false;
     const int32_t *bt = p.block_tables + (int64_t)b * p.max_blocks;
@@ -178,7 +181,7 @@ __device__ __noinline__ void scored_row(const ScoreParams &p, int b, const ReqMe
 #pragma unroll
             for (int e = 0; e < E; ++e)
                 if (e * 32 >= c0 && e * 32 < c0 + cols)
-                    o[e] = o[e] * keep + w * __bfloat162float(p.v[at + e * 32 + lane]);
+                    o[e] = o[e] * keep + w * (__bfloat162float(p.v[at + e * 32 + lane]) * kDown);
             mx = m_new;
         }
     }
@@ -187,7 +190,7 @@ __device__ __noinline__ void scored_row(const ScoreParams &p, int b, const ReqMe
 #pragma unroll
     for (int e = 0; e < E; ++e)
         if (e * 32 >= c0 && e * 32 < c0 + cols)
-            dst[e * 32 + lane] = __float2bfloat16_rn(o[e] * inv);
+            dst[e * 32 + lane] = __float2bfloat16_rn(o[e] * inv * kUp);
     if (lane == 0 && with_lse && p.lse)
         p.lse[t * p.hq + h] = bad ? __int_as_float(0x7FC00000)
                                   : score_lse(mx, l, slope * (float)near);

@@ -791,18 +791,19 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                             const uint32_t keep = all ? ~0u : seen(ch);
                             const bool some = all || __any_sync(0xffffffffu, keep != 0u);
                             if (MODE != kModePlain && some) {
-                                if constexpr (MODE == kModeWide)
+                                if constexpr (MODE == kModeWide) {
 #pragma unroll
                                     for (int k = 0; k < 32; ++k)
                                         v[k] = __float_as_uint(capped_wide(__uint_as_float(v[k]), c1, cap));
-                                else if (cap > 0.f)
+                                } else if (cap > 0.f) {
 #pragma unroll
                                     for (int k = 0; k < 32; ++k)
                                         v[k] = __float_as_uint(capped(__uint_as_float(v[k]), c1, cap));
-                                else
+                                } else {
 #pragma unroll
                                     for (int k = 0; k < 32; ++k)
                                         v[k] = __float_as_uint(__uint_as_float(v[k]) * c1);
+                                }
                                 if (past) {
                                     const float bc = __fmaf_rn(slope2, (float)(ch * 32), b0);
 #pragma unroll

@@ -156,3 +156,52 @@ def test_without_lse(shape):
     want, _ = pa.paged_attention_scored(**a)
     out, lse = pa.paged_attention_scored(**a, want_lse=False)
     assert lse is None and torch.equal(out, want) and not bool(out.isfinite().all())
+
+
+CAUSES = {"up": (math.inf,), "down": (-math.inf,), "nan": (math.nan,), "both": (math.inf, -math.inf), "up_nan": (math.inf, math.nan)}
+
+
+@pytest.mark.parametrize("cause", list(CAUSES))
+@pytest.mark.parametrize("shape", list(SHAPES))
+def test_who_sees_values_that_are_not_finite(shape, cause):
+    """They have them in that column, who sees none of them has a number there; other
+    columns are as good as without them, and lse keeps its bits."""
+    lens, new, *heads = SHAPES[shape]
+    a = _batch(lens, new, *heads, seed=6)
+    out, lse = pa.paged_attention_scored(**a, window=60)
+    clean = out.clone(), lse.clone()
+    base = lens[0] - new[0]
+    keys = [max(base - 20, 0), max(base - 20, 0) + 7][:len(CAUSES[cause])]
+    for j, value in zip(keys, CAUSES[cause]):
+        a["v_cache"][int(a["block_tables"][0, j // 16]), j % 16, :, 17] = value
+    got = pa.paged_attention_scored(**a, window=60)
+    assert pa.check_errors() == (0, -1)
+    others = [d for d in range(heads[2]) if d != 17]
+    assert torch.equal(got[1], clean[1])
+    # (both are within 2^-8 of the value and 2^-8 of the values' size, here below 4)
+    x, y = got[0][..., others].double(), clean[0][..., others].double()
+    assert bool(((x - y).abs() <= 2.0**-6 * (y.abs() + 4)).all())
+    column, was = got[0][..., 17], clean[0][..., 17]
+    for t in range(out.shape[0]):
+        pos = base + t
+        seen = [v for j, v in zip(keys, CAUSES[cause]) if t < new[0] and j <= pos and pos - j < 60]
+        if not seen:
+            assert bool(((column[t].double() - was[t].double()).abs() <= 2.0**-6 * (was[t].double().abs() + 4)).all()), t
+        elif len(set(seen)) == 1 and not math.isnan(seen[0]):
+            assert bool((column[t] == seen[0]).all()), t
+        else:
+            assert bool(column[t].isnan().all()), t
+
+
+def test_a_sum_that_overflows_before_its_division():
+    """Values near the largest: the sum of weight times value passes 32 bits, the
+    result does not."""
+    for heads, new in (((8, 2, 128), 300), ((4, 1, 256), 300), ((4, 1, 512), 40), ((8, 2, 128), 1)):
+        a = _batch([600], [new], *heads, seed=8)
+        for page in a["block_tables"][0, :38].tolist():
+            v = a["v_cache"][page]
+            v[..., 5] = torch.where(v[..., 5].isnan(), v[..., 5], torch.full_like(v[..., 5], 3e38))
+        out, lse = pa.paged_attention_scored(**a)
+        assert pa.check_errors() == (0, -1) and bool(out.isfinite().all())
+        # (2^-8 of the result, 2^-8 of the sum's probabilities, all of one sign)
+        assert bool(((out[..., 5].double() / 3e38 - 1).abs() <= 2.0**-6).all())
