@@ -145,7 +145,9 @@ __device__ __noinline__ void scored_row(const ScoreParams &p, int b, const ReqMe
         o[e] = 0.f;
     }
     // Sums of 2^-32 of the values: up to 2^31 of the largest stay below infinity, and
-    // what that costs those below 2^-94 is less than 2^-116.
+    // what that costs those below 2^-94 is less than 2^-116.  Every weight is
+    // positive, also one below the smallest of 32 bits: an infinite value or a NaN
+    // counts as it is.
     constexpr float kDown = 0x1p-32f, kUp = 0x1p32f;
     float mx = -INFINITY, l = 0.f;
     bool bad = false;
@@ -180,8 +182,10 @@ __device__ __noinline__ void scored_row(const ScoreParams &p, int b, const ReqMe
             l = l * keep + w;
 #pragma unroll
             for (int e = 0; e < E; ++e)
-                if (e * 32 >= c0 && e * 32 < c0 + cols)
-                    o[e] = o[e] * keep + w * (__bfloat162float(p.v[at + e * 32 + lane]) * kDown);
+                if (e * 32 >= c0 && e * 32 < c0 + cols) {
+                    const float v = __bfloat162float(p.v[at + e * 32 + lane]);
+                    o[e] = o[e] * (fabsf(o[e]) < INFINITY ? keep : 1.f) + (fabsf(v) < INFINITY ? w * (v * kDown) : v);
+                }
             mx = m_new;
         }
     }

@@ -193,6 +193,19 @@ def test_who_sees_values_that_are_not_finite(shape, cause):
             assert bool(column[t].isnan().all()), t
 
 
+@pytest.mark.parametrize("key,slope", [(35, 1.0), (299, -1.0)])
+@pytest.mark.parametrize("new", [1, 100])
+@pytest.mark.parametrize("heads", [(4, 2, 128), (2, 1, 256), (2, 1, 512)])
+def test_an_infinity_of_little_weight(heads, new, key, slope):
+    """A weight below the smallest of 32 bits (of keys behind it, or before it, that
+    weigh more) is not zero: the column is infinite."""
+    a = _batch([400], [new], *heads, seed=7)
+    a["v_cache"][int(a["block_tables"][0, key // 16]), key % 16, :, 70] = -math.inf
+    out, lse = pa.paged_attention_scored(**a, slopes=torch.full((heads[0],), slope, device="cuda"))
+    assert pa.check_errors() == (0, -1) and bool(lse.isfinite().all())
+    assert bool((out[..., 70] == -math.inf).all()) and bool(out[..., :70].isfinite().all())
+
+
 def test_a_sum_that_overflows_before_its_division():
     """Values near the largest: the sum of weight times value passes 32 bits, the
     result does not."""
