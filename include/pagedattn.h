@@ -745,10 +745,10 @@ PA_API size_t pa_paged_attention_scored_workspace_size(int32_t num_seqs, int32_t
  *     are bitwise reproducible; other bounds, or the token in another call, may
  *     round differently (the fixed schedule of pa_paged_attention is not kept).
  *     The cap costs a score about 2^-21 of the cap, above a cap of 55 2^-19 of the score.
- *   - Where a value (V) of a key that rows compute together is infinite or NaN, the
- *     rows whose result that makes not finite are computed again, each over its own
- *     keys: right, but slow (0.6 to 1 us for each key of a row) and rounded
- *     differently.
+ *   - Where a value (V) of a key that rows compute together is infinite or NaN, or so
+ *     large that a sum overflows before its division, the rows whose result that makes
+ *     not finite are computed again, each over its own keys: right, but slow (0.6 to 1
+ *     us for each key of a row) and rounded differently.
  *   - workspace: pa_paged_attention_scored_workspace_size(...) bytes, 256-byte
  *     aligned, any contents; calls with different bounds may share it one after
  *     another.

@@ -96,7 +96,7 @@ cudaError_t launch_copy_pages(const CopyArgs &a, ErrState *err, cudaStream_t str
 // does with scattered words (an atomic takes it 3 cycles, a load 1.5).  16
 // instead of 8 took 192 forks of 36 k pages from 14.4 to 11.0 us, a release of 35
 // k references from 27.4 to 21.6 and a pool of 300000 pages from 34.0 to 24.3.
-// Measured: those calls 9.2, 17.6 and 19.7 us; 4 forks of a prompt 4.3 us, the
+// Measured: those calls 9.2, 18.8 and 19.5 us; 4 forks of a prompt 4.3 us, the
 // drafts of 64 requests 9.4, a pool of 2048 pages 7.5: chains of loads, sums and
 // barriers, of some 2 us for a launch.
 constexpr int kPageThreads = 1024;
